@@ -1,0 +1,159 @@
+/*
+ * scape_layers.h -- C ABI of the training-layer operators on one GB300 (sm_103a).
+ *
+ * A sharded optimizer step reads W workers' gradients; these operators produce
+ * them on the same GPU: the residual RMS norm, activation checkpoints in
+ * 8 bits, and the linear layer with its gradients.  What the backward pass
+ * keeps of a layer is 8 bits a value, because the workers' residuals
+ * (scape_bind()) take most of the device's memory; weight gradients are written
+ * where the caller wants them, e.g. into the flat vector scape_step() reads.
+ *
+ * Conventions for every entry point
+ *   - Return value: SCAPE_OK or a negative scape_status (scape.h).  Nothing
+ *     throws across the ABI.  scape_layer_last_error() gives the message of the
+ *     calling thread's last failure.
+ *   - Pointers are device pointers; the caller owns every buffer.  Nothing is
+ *     allocated.  Where an entry point takes a workspace, its *_workspace
+ *     function gives the bytes (0: NULL will do); the workspace is 256-byte
+ *     aligned, is free for other use once the call's work is done, and holds
+ *     nothing between calls.
+ *   - `stream` is a cudaStream_t passed as void*; all work is enqueued on it.
+ *     Calls can be captured into a CUDA graph.
+ *   - Matrices are row-major with unit column stride and a row stride (ld*,
+ *     in elements, at least the number of columns).  Any alignment and any
+ *     stride is accepted; outputs must not overlap inputs unless said.
+ *     Rows or columns of zero length are valid and do nothing (a weight
+ *     gradient of no rows is zero).
+ *   - dtype arguments are scape_dtype (SCAPE_F32, SCAPE_BF16).  Sums, norms and
+ *     products are held in 32 bits and rounded once, when they are stored.
+ *   - Results do not depend on timing: equal calls give equal bits.
+ *
+ * 8-bit format.  Each row is cut into blocks of 32 consecutive columns (the
+ * last may be shorter).  A block holds one scale byte `code`, meaning
+ * 2^(code - 127), and e4m3 values q (4 exponent bits, 3 fraction bits, largest
+ * 448), x ~ q 2^(code - 127): code is the smallest value >= 1 for which the
+ * block's largest finite magnitude is at most 448 2^(code - 127); q is rounded
+ * to nearest even.  Infinities and NaN become NaN and do not affect the rest of
+ * their block.  A power-of-two scale makes every q 2^(code - 127) exact in
+ * bfloat16.  Scales are uint8, ceil(cols / 32) contiguous bytes a row.
+ */
+#ifndef SCAPE_LAYERS_H
+#define SCAPE_LAYERS_H
+
+#include "scape.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+#define SCAPE_PACK_BLOCK 32
+
+/* Activations: identity; max(z, 0); 0.5 z (1 + tanh(sqrt(2/pi) (z + 0.044715
+ * z^3))); z / (1 + exp(-z)).  The slope of relu at 0 is 0. */
+enum scape_activation {
+    SCAPE_ACT_NONE = 0,
+    SCAPE_ACT_RELU = 1,
+    SCAPE_ACT_GELU = 2,
+    SCAPE_ACT_SILU = 3
+};
+
+/* Message of the calling thread's last failed scape_layer_* call ("" if none). */
+const char *scape_layer_last_error(void);
+
+/*
+ * Reads and clears the device's record of kernels that gave up a wait (every
+ * wait inside the matrix-product kernels ends after a time limit; a kernel
+ * that gave up leaves its output incomplete).  0 = none.  Synchronises
+ * `stream`.
+ */
+int scape_layer_status(int *host_status, void *stream);
+
+/* x[rows, cols] -> q[rows, cols], scale[rows, ceil(cols / 32)]. */
+int scape_layer_pack8(const void *x, int64_t ldx, int dtype, int64_t rows, int64_t cols,
+                      uint8_t *q, int64_t ldq, uint8_t *scale, void *stream);
+
+/* y = act(values of (q, scale)), in dtype. */
+int scape_layer_unpack8(const uint8_t *q, int64_t ldq, const uint8_t *scale, int64_t rows,
+                        int64_t cols, int activation, void *y, int64_t ldy, int dtype,
+                        void *stream);
+
+/* dz = dy * act'(values of (q, scale)): the gradient through an activation
+ * whose input was kept in 8 bits.  dz may be dy. */
+int scape_layer_act_grad(const void *dy, int64_t lddy, const uint8_t *q, int64_t ldq,
+                         const uint8_t *scale, int64_t rows, int64_t cols, int activation,
+                         void *dz, int64_t lddz, int dtype, void *stream);
+
+/*
+ * h = x + residual (h = x when residual is NULL);  rstd = (mean h^2 + eps)^-1/2
+ * y = h * rstd * weight.  x, residual, h and y are of dtype; weight (cols) is of
+ * weight_dtype; rstd is float32, one a row.  h, rstd, and the 8-bit form of y
+ * (q, scale; rounded from the 32-bit y) may be NULL; h may be x or residual.
+ */
+int scape_layer_add_rmsnorm(const void *x, int64_t ldx, const void *residual, int64_t ldres,
+                            const void *weight, int weight_dtype, int64_t rows, int64_t cols,
+                            float eps, int dtype, void *y, int64_t ldy, void *h, int64_t ldh,
+                            float *rstd, uint8_t *q, int64_t ldq, uint8_t *scale, void *stream);
+
+/*
+ * Its gradient, from h and rstd: n = h * rstd, d = dy * weight,
+ *   dx = rstd * (d - n * mean(d * n)) + dh,   dweight = sum over rows of dy * n.
+ * dh is the gradient that reaches h from elsewhere (NULL: none); dx is the
+ * gradient of x and of residual alike.  dweight (cols, of dweight_dtype) may be
+ * NULL.  dx may be dy or dh.
+ */
+int scape_layer_add_rmsnorm_bwd_workspace(int64_t rows, int64_t cols, size_t *bytes);
+int scape_layer_add_rmsnorm_bwd(const void *dy, int64_t lddy, const void *h, int64_t ldh,
+                                const void *weight, int weight_dtype, const float *rstd,
+                                const void *dh, int64_t lddh, int64_t rows, int64_t cols,
+                                int dtype, void *dx, int64_t lddx, void *dweight,
+                                int dweight_dtype, void *workspace, size_t ws_bytes,
+                                void *stream);
+
+/*
+ * z = x weight^T + bias;  y = act(z) + residual;  all bfloat16.
+ * x[rows, k], weight[n, k], bias[n] or NULL, residual[rows, n] or NULL,
+ * y[rows, n]; q, scale (the 8-bit form of z, rounded from 32 bits) may be NULL.
+ * y may be residual.  k >= 1.
+ */
+int scape_layer_linear_workspace(const void *x, int64_t ldx, const void *weight, int64_t ldw,
+                                 int64_t rows, int64_t k, int64_t n, size_t *bytes);
+int scape_layer_linear(const void *x, int64_t ldx, const void *weight, int64_t ldw,
+                       const void *bias, const void *residual, int64_t ldres, int64_t rows,
+                       int64_t k, int64_t n, int activation, void *y, int64_t ldy, uint8_t *q,
+                       int64_t ldq, uint8_t *scale, void *workspace, size_t ws_bytes,
+                       void *stream);
+
+/*
+ * dx = (dy weight) * act'(values of (q, scale)): the gradient of a linear
+ * layer's input, taken on through the activation that made that input, whose
+ * own input was kept in 8 bits (activation SCAPE_ACT_NONE: q, scale unused).
+ * dy[rows, n], weight[n, k], q[rows, k], dx[rows, k]; bfloat16.  n >= 1.
+ */
+int scape_layer_linear_bwd_input_workspace(const void *dy, int64_t lddy, const void *weight,
+                                           int64_t ldw, int64_t rows, int64_t k, int64_t n,
+                                           size_t *bytes);
+int scape_layer_linear_bwd_input(const void *dy, int64_t lddy, const void *weight, int64_t ldw,
+                                 const uint8_t *q, int64_t ldq, const uint8_t *scale,
+                                 int activation, int64_t rows, int64_t k, int64_t n, void *dx,
+                                 int64_t lddx, void *workspace, size_t ws_bytes, void *stream);
+
+/*
+ * dweight = dy^T a, dbias = sum over rows of dy, for the layer input
+ * a[rows, k]: either x (bfloat16; q NULL), or act(values of (q, scale)) (x
+ * NULL).  a is rounded to bfloat16, as the forward pass used it.
+ * dweight[n, k] and dbias[n] (or NULL) are of grad_dtype.
+ */
+int scape_layer_linear_bwd_weight_workspace(const void *dy, int64_t lddy, const void *x,
+                                            int64_t ldx, int64_t rows, int64_t k, int64_t n,
+                                            size_t *bytes);
+int scape_layer_linear_bwd_weight(const void *dy, int64_t lddy, const void *x, int64_t ldx,
+                                  const uint8_t *q, int64_t ldq, const uint8_t *scale,
+                                  int activation, int64_t rows, int64_t k, int64_t n,
+                                  void *dweight, int64_t lddw, void *dbias, int grad_dtype,
+                                  void *workspace, size_t ws_bytes, void *stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* SCAPE_LAYERS_H */

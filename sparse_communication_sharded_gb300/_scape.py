@@ -11,6 +11,7 @@ import ctypes
 import os
 
 from . import build as _build
+from ._layers import PROTOS as _LAYER_PROTOS
 
 SCAPE_OK = 0
 SCAPE_EINVAL = -1
@@ -86,6 +87,7 @@ _PROTOS = {
     "scape_xc_get_state": (_i32, [_vp, _vp, _vp, _vp]),
     "scape_xc_set_state": (_i32, [_vp, _i64, _vp, _vp]),
     "scape_xc_launch_count": (_i64, [_vp]),
+    **_LAYER_PROTOS,
 }
 
 

@@ -1,0 +1,446 @@
+// layer_api.cu -- host side of the training-layer operators (include/scape_layers.h):
+// checks of the arguments, workspaces and launches.
+#include <algorithm>
+#include <atomic>
+#include <cmath>
+#include <cstdio>
+
+#include "layer_gemm.cuh"
+
+namespace scapek {
+namespace layer {
+namespace {
+
+__device__ unsigned int g_status;  // set by a kernel that gave up a wait
+
+constexpr int kMaxDevices = 64;
+std::atomic<unsigned int*> g_status_word[kMaxDevices];
+
+thread_local char g_error[256];
+
+int fail(int code, const char* what) {
+  std::snprintf(g_error, sizeof g_error, "%s", what);
+  return code;
+}
+int cuda_result(cudaError_t e, const char* what) {
+  if (e == cudaSuccess) return SCAPE_OK;
+  std::snprintf(g_error, sizeof g_error, "%s: %s", what, cudaGetErrorString(e));
+  return SCAPE_ECUDA;
+}
+
+// Sizes stay below this so that column numbers and tile coordinates fit an int.
+constexpr int64_t kMaxSize = (int64_t{1} << 31) - 1024;
+
+bool size_ok(int64_t n) { return n >= 0 && n <= kMaxSize; }
+bool dtype_ok(int d) { return d == SCAPE_F32 || d == SCAPE_BF16; }
+bool act_ok(int a) { return a >= SCAPE_ACT_NONE && a <= SCAPE_ACT_SILU; }
+bool elem_ok(const void* p, int dtype) { return p && aligned(p, dtype == SCAPE_BF16 ? 2 : 4); }
+
+// Rows `from` of src (any alignment) copied to 16-byte aligned rows.  A thread
+// writes eight values; its reads, two bytes each, fall on lines that its
+// neighbours read as well.
+__global__ __launch_bounds__(256) void align_rows_kernel(const bf16* src, int64_t ld, int64_t rows,
+                                                         int64_t cols, bf16* dst, int64_t ldd) {
+  const int64_t per_row = ldd / 8;
+  for (int64_t row = blockIdx.y; row < rows; row += gridDim.y) {
+    const int64_t c = ((int64_t)blockIdx.x * 256 + threadIdx.x);
+    if (c >= per_row) continue;
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      v[i] = c * 8 + i < cols ? __bfloat162float(src[row * ld + c * 8 + i]) : 0.0f;
+    store_vec<8>(dst + row * ldd + c * 8, v);
+  }
+}
+cudaError_t launch_align_rows(const bf16* src, int64_t ld, int64_t rows, int64_t cols, bf16* dst,
+                              int64_t ldd, cudaStream_t st) {
+  const unsigned x = (unsigned)ceil_div(ldd / 8, 256);
+  align_rows_kernel<<<dim3(x, (unsigned)std::min<int64_t>(rows, 32768)), 256, 0, st>>>(
+      src, ld, rows, cols, dst, ldd);
+  return cudaGetLastError();
+}
+
+int64_t round8(int64_t n) { return (n + 7) / 8 * 8; }
+size_t round256(size_t n) { return (n + 255) / 256 * 256; }
+size_t copy_bytes(int64_t rows, int64_t cols) { return round256((size_t)rows * round8(cols) * 2); }
+
+// TMA reads rows that start on 16-byte boundaries; other operands are first
+// copied to such rows in the workspace.
+bool tma_rows(const void* p, int64_t ld) { return rows16(p, ld, 2); }
+size_t operand_bytes(const void* p, int64_t ld, int64_t rows, int64_t cols) {
+  return tma_rows(p, ld) ? 0 : copy_bytes(rows, cols);
+}
+cudaError_t operand(const void* p, int64_t ld, int64_t rows, int64_t cols, uint8_t*& ws,
+                    GemmOperand* out, cudaStream_t st) {
+  if (tma_rows(p, ld)) {
+    *out = {static_cast<const bf16*>(p), ld};
+    return cudaSuccess;
+  }
+  bf16* dst = reinterpret_cast<bf16*>(ws);
+  ws += copy_bytes(rows, cols);
+  *out = {dst, round8(cols)};
+  return launch_align_rows(static_cast<const bf16*>(p), ld, rows, cols, dst, round8(cols), st);
+}
+
+int check_workspace(const void* ws, size_t have, size_t need) {
+  if (need == 0) return SCAPE_OK;
+  if (!ws || !aligned(ws, 256)) return fail(SCAPE_EINVAL, "workspace is NULL or not 256-byte aligned");
+  if (have < need) return fail(SCAPE_EINVAL, "workspace is too small");
+  return SCAPE_OK;
+}
+
+int check_packed(const uint8_t* q, int64_t ldq, const uint8_t* scale, int64_t cols) {
+  if (!q || !scale) return fail(SCAPE_EINVAL, "q and scale must both be given");
+  if (ldq < cols) return fail(SCAPE_EINVAL, "row stride of q is below its columns");
+  return SCAPE_OK;
+}
+int check_matrix(const void* p, int64_t ld, int64_t cols, int dtype, const char* what) {
+  if (!elem_ok(p, dtype)) return fail(SCAPE_EINVAL, what);
+  if (ld < cols) return fail(SCAPE_EINVAL, "a row stride is below the number of columns");
+  return SCAPE_OK;
+}
+
+}  // namespace
+
+cudaError_t gemm_status_word(unsigned int** word) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  unsigned int* p = g_status_word[dev].load(std::memory_order_acquire);
+  if (!p) {
+    void* v = nullptr;
+    e = cudaGetSymbolAddress(&v, g_status);
+    if (e != cudaSuccess) return e;
+    p = static_cast<unsigned int*>(v);
+    g_status_word[dev].store(p, std::memory_order_release);
+  }
+  *word = p;
+  return cudaSuccess;
+}
+
+cudaError_t gemm_tensor_map(CUtensorMap* map, const bf16* p, int64_t rows, int64_t cols,
+                            int64_t ld, int box_rows) {
+  using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                              const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                              const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+  static std::atomic<Encode> encode{nullptr};
+  Encode f = encode.load(std::memory_order_acquire);
+  if (!f) {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000,
+                                                           cudaEnableDefault, &found);
+    if (e != cudaSuccess) return e;
+    if (found != cudaDriverEntryPointSuccess || !fn) return cudaErrorNotSupported;
+    f = reinterpret_cast<Encode>(fn);
+    encode.store(f, std::memory_order_release);
+  }
+  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
+  const cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
+  const cuuint32_t ones[2] = {1, 1};
+  const CUresult r = f(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<bf16*>(p), dims,
+                       strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                       CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+}  // namespace layer
+}  // namespace scapek
+
+using namespace scapek::layer;
+
+extern "C" const char* scape_layer_last_error(void) { return g_error; }
+
+extern "C" int scape_layer_status(int* host_status, void* stream) {
+  if (!host_status) return fail(SCAPE_EINVAL, "host_status is NULL");
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  unsigned int* word = nullptr;
+  unsigned int v = 0;
+  cudaError_t e = gemm_status_word(&word);
+  if (e == cudaSuccess) e = cudaMemcpyAsync(&v, word, sizeof v, cudaMemcpyDeviceToHost, st);
+  if (e == cudaSuccess) e = cudaMemsetAsync(word, 0, sizeof v, st);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+  *host_status = (int)v;
+  return cuda_result(e, "scape_layer_status");
+}
+
+extern "C" int scape_layer_pack8(const void* x, int64_t ldx, int dtype, int64_t rows, int64_t cols,
+                                 uint8_t* q, int64_t ldq, uint8_t* scale, void* stream) {
+  if (!dtype_ok(dtype)) return fail(SCAPE_EINVAL, "unknown dtype");
+  if (!size_ok(rows) || !size_ok(cols)) return fail(SCAPE_EINVAL, "rows or cols out of range");
+  if (rows == 0 || cols == 0) return SCAPE_OK;
+  int rc = check_matrix(x, ldx, cols, dtype, "x is NULL or misaligned");
+  if (!rc) rc = check_packed(q, ldq, scale, cols);
+  if (rc) return rc;
+  return cuda_result(launch_pack8(x, ldx, dtype, rows, cols, q, ldq, scale,
+                                  static_cast<cudaStream_t>(stream)),
+                     "scape_layer_pack8");
+}
+
+extern "C" int scape_layer_unpack8(const uint8_t* q, int64_t ldq, const uint8_t* scale,
+                                   int64_t rows, int64_t cols, int activation, void* y,
+                                   int64_t ldy, int dtype, void* stream) {
+  if (!dtype_ok(dtype)) return fail(SCAPE_EINVAL, "unknown dtype");
+  if (!act_ok(activation)) return fail(SCAPE_EINVAL, "unknown activation");
+  if (!size_ok(rows) || !size_ok(cols)) return fail(SCAPE_EINVAL, "rows or cols out of range");
+  if (rows == 0 || cols == 0) return SCAPE_OK;
+  int rc = check_packed(q, ldq, scale, cols);
+  if (!rc) rc = check_matrix(y, ldy, cols, dtype, "y is NULL or misaligned");
+  if (rc) return rc;
+  return cuda_result(launch_unpack8(q, ldq, scale, rows, cols, activation, y, ldy, dtype,
+                                    static_cast<cudaStream_t>(stream)),
+                     "scape_layer_unpack8");
+}
+
+extern "C" int scape_layer_act_grad(const void* dy, int64_t lddy, const uint8_t* q, int64_t ldq,
+                                    const uint8_t* scale, int64_t rows, int64_t cols,
+                                    int activation, void* dz, int64_t lddz, int dtype,
+                                    void* stream) {
+  if (!dtype_ok(dtype)) return fail(SCAPE_EINVAL, "unknown dtype");
+  if (!act_ok(activation)) return fail(SCAPE_EINVAL, "unknown activation");
+  if (!size_ok(rows) || !size_ok(cols)) return fail(SCAPE_EINVAL, "rows or cols out of range");
+  if (rows == 0 || cols == 0) return SCAPE_OK;
+  int rc = check_matrix(dy, lddy, cols, dtype, "dy is NULL or misaligned");
+  if (!rc) rc = check_packed(q, ldq, scale, cols);
+  if (!rc) rc = check_matrix(dz, lddz, cols, dtype, "dz is NULL or misaligned");
+  if (rc) return rc;
+  return cuda_result(launch_act_grad(dy, lddy, q, ldq, scale, rows, cols, activation, dz, lddz,
+                                     dtype, static_cast<cudaStream_t>(stream)),
+                     "scape_layer_act_grad");
+}
+
+extern "C" int scape_layer_add_rmsnorm(const void* x, int64_t ldx, const void* residual,
+                                       int64_t ldres, const void* weight, int weight_dtype,
+                                       int64_t rows, int64_t cols, float eps, int dtype, void* y,
+                                       int64_t ldy, void* h, int64_t ldh, float* rstd, uint8_t* q,
+                                       int64_t ldq, uint8_t* scale, void* stream) {
+  if (!dtype_ok(dtype) || !dtype_ok(weight_dtype)) return fail(SCAPE_EINVAL, "unknown dtype");
+  if (!size_ok(rows) || !size_ok(cols)) return fail(SCAPE_EINVAL, "rows or cols out of range");
+  if (!(eps >= 0.0f) || !std::isfinite(eps)) return fail(SCAPE_EINVAL, "eps must be finite and >= 0");
+  if (rows == 0 || cols == 0) return SCAPE_OK;
+  int rc = check_matrix(x, ldx, cols, dtype, "x is NULL or misaligned");
+  if (!rc && residual) rc = check_matrix(residual, ldres, cols, dtype, "residual is misaligned");
+  if (!rc) rc = check_matrix(y, ldy, cols, dtype, "y is NULL or misaligned");
+  if (!rc && h) rc = check_matrix(h, ldh, cols, dtype, "h is misaligned");
+  if (!rc && !elem_ok(weight, weight_dtype)) rc = fail(SCAPE_EINVAL, "weight is NULL or misaligned");
+  if (!rc && rstd && !aligned(rstd, 4)) rc = fail(SCAPE_EINVAL, "rstd is misaligned");
+  if (!rc && (q || scale)) rc = check_packed(q, ldq, scale, cols);
+  if (rc) return rc;
+  NormFwd a;
+  a.x = x, a.res = residual, a.w = weight;
+  a.ldx = ldx, a.ldres = ldres, a.ldy = ldy, a.ldh = ldh, a.ldq = ldq;
+  a.w_bf16 = weight_dtype == SCAPE_BF16;
+  a.rows = rows, a.cols = (int)cols, a.eps = eps;
+  a.y = y, a.h = h, a.rstd = rstd, a.q = q, a.scale = scale;
+  return cuda_result(launch_norm_fwd(a, dtype, static_cast<cudaStream_t>(stream)),
+                     "scape_layer_add_rmsnorm");
+}
+
+extern "C" int scape_layer_add_rmsnorm_bwd_workspace(int64_t rows, int64_t cols, size_t* bytes) {
+  if (!bytes) return fail(SCAPE_EINVAL, "bytes is NULL");
+  if (!size_ok(rows) || !size_ok(cols)) return fail(SCAPE_EINVAL, "rows or cols out of range");
+  *bytes = rows && cols ? round256((size_t)norm_bwd_partials(rows, cols) * cols * 4) : 0;
+  return SCAPE_OK;
+}
+
+extern "C" int scape_layer_add_rmsnorm_bwd(const void* dy, int64_t lddy, const void* h,
+                                           int64_t ldh, const void* weight, int weight_dtype,
+                                           const float* rstd, const void* dh, int64_t lddh,
+                                           int64_t rows, int64_t cols, int dtype, void* dx,
+                                           int64_t lddx, void* dweight, int dweight_dtype,
+                                           void* workspace, size_t ws_bytes, void* stream) {
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (!dtype_ok(dtype) || !dtype_ok(weight_dtype) || !dtype_ok(dweight_dtype))
+    return fail(SCAPE_EINVAL, "unknown dtype");
+  if (!size_ok(rows) || !size_ok(cols)) return fail(SCAPE_EINVAL, "rows or cols out of range");
+  if (cols == 0) return SCAPE_OK;
+  if (dweight && !elem_ok(dweight, dweight_dtype)) return fail(SCAPE_EINVAL, "dweight is misaligned");
+  if (rows == 0) {
+    if (!dweight) return SCAPE_OK;
+    return cuda_result(cudaMemsetAsync(dweight, 0, cols * (dweight_dtype == SCAPE_BF16 ? 2 : 4), st),
+                       "scape_layer_add_rmsnorm_bwd");
+  }
+  int rc = check_matrix(dy, lddy, cols, dtype, "dy is NULL or misaligned");
+  if (!rc) rc = check_matrix(h, ldh, cols, dtype, "h is NULL or misaligned");
+  if (!rc && dh) rc = check_matrix(dh, lddh, cols, dtype, "dh is misaligned");
+  if (!rc) rc = check_matrix(dx, lddx, cols, dtype, "dx is NULL or misaligned");
+  if (!rc && !elem_ok(weight, weight_dtype)) rc = fail(SCAPE_EINVAL, "weight is NULL or misaligned");
+  if (!rc && (!rstd || !aligned(rstd, 4))) rc = fail(SCAPE_EINVAL, "rstd is NULL or misaligned");
+  size_t need = 0;
+  if (!rc && dweight) rc = scape_layer_add_rmsnorm_bwd_workspace(rows, cols, &need);
+  if (!rc) rc = check_workspace(workspace, ws_bytes, need);
+  if (rc) return rc;
+  NormBwd a;
+  a.dy = dy, a.h = h, a.w = weight, a.dh = dh;
+  a.lddy = lddy, a.ldh = ldh, a.lddh = lddh, a.lddx = lddx;
+  a.rstd = rstd, a.w_bf16 = weight_dtype == SCAPE_BF16, a.dw_bf16 = dweight_dtype == SCAPE_BF16;
+  a.rows = rows, a.cols = (int)cols, a.dx = dx, a.dw = dweight;
+  a.partial = static_cast<float*>(workspace);
+  return cuda_result(launch_norm_bwd(a, dtype, st), "scape_layer_add_rmsnorm_bwd");
+}
+
+// ---------------------------------------------------------------------- linear
+extern "C" int scape_layer_linear_workspace(const void* x, int64_t ldx, const void* weight,
+                                            int64_t ldw, int64_t rows, int64_t k, int64_t n,
+                                            size_t* bytes) {
+  if (!bytes) return fail(SCAPE_EINVAL, "bytes is NULL");
+  if (!size_ok(rows) || !size_ok(k) || !size_ok(n)) return fail(SCAPE_EINVAL, "a size is out of range");
+  *bytes = rows && n ? operand_bytes(x, ldx, rows, k) + operand_bytes(weight, ldw, n, k) : 0;
+  return SCAPE_OK;
+}
+
+extern "C" int scape_layer_linear(const void* x, int64_t ldx, const void* weight, int64_t ldw,
+                                  const void* bias, const void* residual, int64_t ldres,
+                                  int64_t rows, int64_t k, int64_t n, int activation, void* y,
+                                  int64_t ldy, uint8_t* q, int64_t ldq, uint8_t* scale,
+                                  void* workspace, size_t ws_bytes, void* stream) {
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (!act_ok(activation)) return fail(SCAPE_EINVAL, "unknown activation");
+  if (!size_ok(rows) || !size_ok(k) || !size_ok(n)) return fail(SCAPE_EINVAL, "a size is out of range");
+  if (k == 0) return fail(SCAPE_EINVAL, "k must be at least 1");
+  if (rows == 0 || n == 0) return SCAPE_OK;
+  int rc = check_matrix(x, ldx, k, SCAPE_BF16, "x is NULL or misaligned");
+  if (!rc) rc = check_matrix(weight, ldw, k, SCAPE_BF16, "weight is NULL or misaligned");
+  if (!rc && bias && !aligned(bias, 2)) rc = fail(SCAPE_EINVAL, "bias is misaligned");
+  if (!rc && residual) rc = check_matrix(residual, ldres, n, SCAPE_BF16, "residual is misaligned");
+  if (!rc) rc = check_matrix(y, ldy, n, SCAPE_BF16, "y is NULL or misaligned");
+  if (!rc && (q || scale)) rc = check_packed(q, ldq, scale, n);
+  size_t need = 0;
+  if (!rc) rc = scape_layer_linear_workspace(x, ldx, weight, ldw, rows, k, n, &need);
+  if (!rc) rc = check_workspace(workspace, ws_bytes, need);
+  if (rc) return rc;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  GemmCall c = {};
+  cudaError_t e = operand(x, ldx, rows, k, ws, &c.a, st);
+  if (e == cudaSuccess) e = operand(weight, ldw, n, k, ws, &c.b, st);
+  c.m = rows, c.n = n, c.k = k;
+  c.e.act = activation;
+  c.e.bias = static_cast<const bf16*>(bias);
+  c.e.bias_vec = aligned(bias, 16);
+  c.e.res = static_cast<const bf16*>(residual);
+  c.e.ldres = ldres;
+  c.e.res_vec = rows16(residual, ldres, 2);
+  c.e.q = q, c.e.ldq = ldq, c.e.scale = scale;
+  c.e.q_vec = rows16(q, ldq, 1);
+  c.e.blocks_per_row = ceil_div(n, kBlock);
+  c.e.out = y, c.e.ldo = ldy;
+  c.e.out_vec = rows16(y, ldy, 2);
+  if (e == cudaSuccess) e = gemm_forward(c, st);
+  return cuda_result(e, "scape_layer_linear");
+}
+
+extern "C" int scape_layer_linear_bwd_input_workspace(const void* dy, int64_t lddy,
+                                                      const void* weight, int64_t ldw,
+                                                      int64_t rows, int64_t k, int64_t n,
+                                                      size_t* bytes) {
+  if (!bytes) return fail(SCAPE_EINVAL, "bytes is NULL");
+  if (!size_ok(rows) || !size_ok(k) || !size_ok(n)) return fail(SCAPE_EINVAL, "a size is out of range");
+  *bytes = rows && k ? operand_bytes(dy, lddy, rows, n) + operand_bytes(weight, ldw, n, k) : 0;
+  return SCAPE_OK;
+}
+
+extern "C" int scape_layer_linear_bwd_input(const void* dy, int64_t lddy, const void* weight,
+                                            int64_t ldw, const uint8_t* q, int64_t ldq,
+                                            const uint8_t* scale, int activation, int64_t rows,
+                                            int64_t k, int64_t n, void* dx, int64_t lddx,
+                                            void* workspace, size_t ws_bytes, void* stream) {
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (!act_ok(activation)) return fail(SCAPE_EINVAL, "unknown activation");
+  if (!size_ok(rows) || !size_ok(k) || !size_ok(n)) return fail(SCAPE_EINVAL, "a size is out of range");
+  if (n == 0) return fail(SCAPE_EINVAL, "n must be at least 1");
+  if (rows == 0 || k == 0) return SCAPE_OK;
+  int rc = check_matrix(dy, lddy, n, SCAPE_BF16, "dy is NULL or misaligned");
+  if (!rc) rc = check_matrix(weight, ldw, k, SCAPE_BF16, "weight is NULL or misaligned");
+  if (!rc) rc = check_matrix(dx, lddx, k, SCAPE_BF16, "dx is NULL or misaligned");
+  if (!rc && activation != SCAPE_ACT_NONE) rc = check_packed(q, ldq, scale, k);
+  size_t need = 0;
+  if (!rc) rc = scape_layer_linear_bwd_input_workspace(dy, lddy, weight, ldw, rows, k, n, &need);
+  if (!rc) rc = check_workspace(workspace, ws_bytes, need);
+  if (rc) return rc;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  GemmCall c = {};
+  cudaError_t e = operand(dy, lddy, rows, n, ws, &c.a, st);
+  if (e == cudaSuccess) e = operand(weight, ldw, n, k, ws, &c.b, st);
+  c.m = rows, c.n = k, c.k = n;
+  c.e.act = activation;
+  c.e.pre_q = q, c.e.ldpre = ldq, c.e.pre_scale = scale;
+  c.e.pre_vec = rows8(q, ldq);
+  c.e.blocks_per_row = ceil_div(k, kBlock);
+  c.e.out = dx, c.e.ldo = lddx;
+  c.e.out_vec = rows16(dx, lddx, 2);
+  if (e == cudaSuccess) e = gemm_input_grad(c, st);
+  return cuda_result(e, "scape_layer_linear_bwd_input");
+}
+
+extern "C" int scape_layer_linear_bwd_weight_workspace(const void* dy, int64_t lddy, const void* x,
+                                                       int64_t ldx, int64_t rows, int64_t k,
+                                                       int64_t n, size_t* bytes) {
+  if (!bytes) return fail(SCAPE_EINVAL, "bytes is NULL");
+  if (!size_ok(rows) || !size_ok(k) || !size_ok(n)) return fail(SCAPE_EINVAL, "a size is out of range");
+  *bytes = 0;
+  if (rows == 0 || n == 0) return SCAPE_OK;
+  *bytes = operand_bytes(dy, lddy, rows, n) +
+           (x ? operand_bytes(x, ldx, rows, k) : copy_bytes(rows, k)) +
+           round256((size_t)colsum_partials(rows, n) * n * 4);
+  return SCAPE_OK;
+}
+
+extern "C" int scape_layer_linear_bwd_weight(const void* dy, int64_t lddy, const void* x,
+                                             int64_t ldx, const uint8_t* q, int64_t ldq,
+                                             const uint8_t* scale, int activation, int64_t rows,
+                                             int64_t k, int64_t n, void* dweight, int64_t lddw,
+                                             void* dbias, int grad_dtype, void* workspace,
+                                             size_t ws_bytes, void* stream) {
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const char* const who = "scape_layer_linear_bwd_weight";
+  if (!act_ok(activation)) return fail(SCAPE_EINVAL, "unknown activation");
+  if (!dtype_ok(grad_dtype)) return fail(SCAPE_EINVAL, "unknown dtype");
+  if (!size_ok(rows) || !size_ok(k) || !size_ok(n)) return fail(SCAPE_EINVAL, "a size is out of range");
+  if (x && q) return fail(SCAPE_EINVAL, "x and q are both given");
+  if (x && activation != SCAPE_ACT_NONE)
+    return fail(SCAPE_EINVAL, "an activation is applied to an 8-bit input only");
+  if (n == 0) return SCAPE_OK;
+  const size_t ge = grad_dtype == SCAPE_BF16 ? 2 : 4;
+  if (dbias && !elem_ok(dbias, grad_dtype)) return fail(SCAPE_EINVAL, "dbias is misaligned");
+  int rc = SCAPE_OK;
+  if (k) rc = check_matrix(dweight, lddw, k, grad_dtype, "dweight is NULL or misaligned");
+  if (rc) return rc;
+  if (rows == 0) {
+    cudaError_t e = cudaSuccess;
+    if (k) e = cudaMemset2DAsync(dweight, lddw * ge, 0, k * ge, n, st);
+    if (e == cudaSuccess && dbias) e = cudaMemsetAsync(dbias, 0, n * ge, st);
+    return cuda_result(e, who);
+  }
+  rc = check_matrix(dy, lddy, n, SCAPE_BF16, "dy is NULL or misaligned");
+  if (!rc && k) rc = x ? check_matrix(x, ldx, k, SCAPE_BF16, "x is misaligned") : check_packed(q, ldq, scale, k);
+  size_t need = 0;
+  if (!rc) rc = scape_layer_linear_bwd_weight_workspace(dy, lddy, x, ldx, rows, k, n, &need);
+  if (!rc) rc = check_workspace(workspace, ws_bytes, need);
+  if (rc) return rc;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  cudaError_t e = cudaSuccess;
+  if (k) {
+    GemmCall c = {};
+    e = operand(dy, lddy, rows, n, ws, &c.a, st);
+    if (e == cudaSuccess && x) {
+      e = operand(x, ldx, rows, k, ws, &c.b, st);
+    } else if (e == cudaSuccess) {
+      bf16* a = reinterpret_cast<bf16*>(ws);
+      ws += copy_bytes(rows, k);
+      c.b = {a, round8(k)};
+      e = launch_unpack8(q, ldq, scale, rows, k, activation, a, round8(k), SCAPE_BF16, st);
+    }
+    c.m = n, c.n = k, c.k = rows;
+    c.e.out = dweight, c.e.ldo = lddw, c.e.out_f32 = grad_dtype == SCAPE_F32;
+    c.e.out_vec = rows16(dweight, lddw, ge);
+    if (e == cudaSuccess) e = gemm_weight_grad(c, st);
+  }
+  if (e == cudaSuccess && dbias)
+    e = launch_colsum(static_cast<const bf16*>(dy), lddy, rows, n, reinterpret_cast<float*>(ws),
+                      dbias, grad_dtype == SCAPE_BF16, st);
+  return cuda_result(e, who);
+}

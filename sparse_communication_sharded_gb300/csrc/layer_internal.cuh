@@ -1,0 +1,342 @@
+// layer_internal.cuh -- device helpers shared by the training-layer operators
+// (include/scape_layers.h): vector loads and stores, the 8-bit block format and
+// the activations.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "scape_layers.h"
+
+namespace scapek {
+
+int sm_count();
+
+namespace layer {
+
+using bf16 = __nv_bfloat16;
+constexpr int kBlock = SCAPE_PACK_BLOCK;
+
+inline bool aligned(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
+inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+// A row-major matrix whose every row starts on a 16-byte boundary.
+inline bool rows16(const void* p, int64_t ld, size_t elem) {
+  return p == nullptr || (aligned(p, 16) && (ld * (int64_t)elem) % 16 == 0);
+}
+// The same for the 8-byte rows that one thread's eight 8-bit values take.
+inline bool rows8(const void* p, int64_t ld) {
+  return p == nullptr || (aligned(p, 8) && ld % 8 == 0);
+}
+
+// ------------------------------------------------------------------ loads and stores
+// VEC consecutive elements as floats.  VEC 8 needs 16-byte alignment (one load
+// of bfloat16, two of float32); VEC 1 any.
+template <int VEC>
+__device__ __forceinline__ void load_vec(const bf16* p, float (&v)[VEC]) {
+  if constexpr (VEC == 8) {
+    const uint4 u = *reinterpret_cast<const uint4*>(p);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) v[i] = __bfloat162float(p[i]);
+  }
+}
+template <int VEC>
+__device__ __forceinline__ void load_vec(const float* p, float (&v)[VEC]) {
+  if constexpr (VEC == 8) {
+    const float4 a = reinterpret_cast<const float4*>(p)[0];
+    const float4 b = reinterpret_cast<const float4*>(p)[1];
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+    v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  } else {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) v[i] = p[i];
+  }
+}
+
+__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
+  const __nv_bfloat162 r = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+template <int VEC>
+__device__ __forceinline__ void store_vec(bf16* p, const float (&v)[VEC]) {
+  if constexpr (VEC == 8) {
+    uint4 u;
+    u.x = bf16_pair(v[0], v[1]), u.y = bf16_pair(v[2], v[3]);
+    u.z = bf16_pair(v[4], v[5]), u.w = bf16_pair(v[6], v[7]);
+    *reinterpret_cast<uint4*>(p) = u;
+  } else {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) p[i] = __float2bfloat16_rn(v[i]);
+  }
+}
+template <int VEC>
+__device__ __forceinline__ void store_vec(float* p, const float (&v)[VEC]) {
+  if constexpr (VEC == 8) {
+    reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) p[i] = v[i];
+  }
+}
+
+// The first n (0..VEC) elements of a vector at a row's end; the rest read as 0.
+template <int VEC, typename T>
+__device__ __forceinline__ void load_part(const T* p, int n, float (&v)[VEC]) {
+  if (n >= VEC) {
+    load_vec<VEC>(p, v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) v[i] = i < n ? (float)p[i] : 0.0f;
+  }
+}
+template <int VEC, typename T>
+__device__ __forceinline__ void store_part(T* p, int n, const float (&v)[VEC]) {
+  if (n >= VEC) {
+    store_vec<VEC>(p, v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i)
+      if (i < n) p[i] = (T)v[i];
+  }
+}
+// A weight vector of either type (the type is the same for the whole grid).
+template <int VEC>
+__device__ __forceinline__ void load_weight(const void* w, int is_bf16, bool vec_ok, int64_t c,
+                                            int n, float (&v)[VEC]) {
+  if (is_bf16) {
+    const bf16* p = static_cast<const bf16*>(w) + c;
+    if (VEC == 1 || vec_ok) {
+      load_part<VEC>(p, n, v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) v[i] = i < n ? __bfloat162float(p[i]) : 0.0f;
+    }
+  } else {
+    const float* p = static_cast<const float*>(w) + c;
+    if (VEC == 1 || vec_ok) {
+      load_part<VEC>(p, n, v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) v[i] = i < n ? p[i] : 0.0f;
+    }
+  }
+}
+
+// ------------------------------------------------------------------ the 8-bit block format
+__device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
+constexpr uint32_t kInfBits = 0x7F800000u;
+
+// Scale code of a block whose largest finite magnitude has these bits.  A
+// magnitude 1.f 2^(E-127) is at most 448 2^c = 1.75 2^(c+8) for c = E-127-8
+// when 1.f <= 1.75, and for one more otherwise; code = c + 127, at least 1 so
+// that the scale and its reciprocal are normal numbers.
+__device__ __forceinline__ uint32_t scale_code(uint32_t top) {
+  const int c = (int)(top >> 23) - 8 + ((top & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+  return (uint32_t)max(c, 1);
+}
+__device__ __forceinline__ float scale_value(uint32_t code) { return __uint_as_float(code << 23); }
+__device__ __forceinline__ float scale_inverse(uint32_t code) {
+  return __uint_as_float((254u - code) << 23);
+}
+__device__ __forceinline__ uint32_t e4m3_pair(float a, float b) {
+  return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+}
+// Infinities become NaN (the conversion would clamp them).
+__device__ __forceinline__ float nan_unless_finite(float x) {
+  return abs_bits(x) >= kInfBits ? __uint_as_float(0x7FC00000u) : x;
+}
+// Scaling by a power of two is exact down to the subnormals, where e4m3 is 0.
+__device__ __forceinline__ uint32_t e4m3_byte(float x, float inv) {
+  return e4m3_pair(nan_unless_finite(x * inv), 0.0f) & 0xFFu;
+}
+
+// N values of one block (or an N-long part of it) that one thread holds; `top`
+// is the block's largest magnitude's bits over all values, infinities and NaN
+// included, `finite` gives the largest finite one when those are present.
+template <int N>
+__device__ __forceinline__ uint32_t part_top(const float (&v)[N]) {
+  uint32_t t = 0;
+#pragma unroll
+  for (int i = 0; i < N; ++i) t = max(t, abs_bits(v[i]));
+  return t;
+}
+template <int N>
+__device__ __forceinline__ uint32_t part_top_finite(const float (&v)[N]) {
+  uint32_t t = 0;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const uint32_t b = abs_bits(v[i]);
+    if (b < kInfBits) t = max(t, b);
+  }
+  return t;
+}
+// e4m3 words of N values (N a multiple of 4) at a scale.
+template <int N>
+__device__ __forceinline__ void to_e4m3(const float (&v)[N], float inv, bool all_finite,
+                                        uint32_t (&w)[N / 4]) {
+#pragma unroll
+  for (int i = 0; i < N / 4; ++i) {
+    float a = v[4 * i] * inv, b = v[4 * i + 1] * inv, c = v[4 * i + 2] * inv,
+          d = v[4 * i + 3] * inv;
+    if (!all_finite) {
+      a = nan_unless_finite(a), b = nan_unless_finite(b);
+      c = nan_unless_finite(c), d = nan_unless_finite(d);
+    }
+    w[i] = e4m3_pair(a, b) | (e4m3_pair(c, d) << 16);
+  }
+}
+// Four e4m3 values as floats (exact).
+__device__ __forceinline__ void from_e4m3(uint32_t w, float scale, float* v) {
+  const __half2_raw lo = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w & 0xFFFFu), __NV_E4M3);
+  const __half2_raw hi = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> 16), __NV_E4M3);
+  const float2 a = __half22float2(__half2(lo)), b = __half22float2(__half2(hi));
+  v[0] = a.x * scale, v[1] = a.y * scale, v[2] = b.x * scale, v[3] = b.y * scale;
+}
+__device__ __forceinline__ float from_e4m3_byte(uint32_t b, float scale) {
+  const __half_raw h = __nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)b, __NV_E4M3);
+  return __half2float(__half(h)) * scale;
+}
+
+// One warp's 32 lanes pack VEC values each; with VEC 8 four neighbouring lanes
+// hold a block, with VEC 1 the whole warp does.  n values of the thread are
+// real (the others are 0).  All 32 lanes call it together.
+template <int VEC>
+__device__ __forceinline__ void warp_pack(const float (&v)[VEC], int n, uint8_t* q, uint8_t* scale,
+                                          bool writes_scale) {
+  uint32_t top = part_top<VEC>(v);
+  bool all_finite = true;
+  if constexpr (VEC == 1) {
+    top = __reduce_max_sync(0xFFFFFFFFu, top);
+    if (top >= kInfBits) {
+      top = __reduce_max_sync(0xFFFFFFFFu, part_top_finite<VEC>(v));
+      all_finite = false;
+    }
+  } else {
+    top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+    top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+    if (__any_sync(0xFFFFFFFFu, top >= kInfBits)) {
+      top = part_top_finite<VEC>(v);
+      top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+      top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+      all_finite = false;
+    }
+  }
+  const uint32_t code = scale_code(top);
+  const float inv = scale_inverse(code);
+  if constexpr (VEC == 1) {
+    if (n > 0) *q = (uint8_t)e4m3_byte(v[0], inv);
+  } else {
+    uint32_t w[2];
+    to_e4m3<8>(v, inv, all_finite, w);
+    if (n >= 8) {
+      *reinterpret_cast<uint2*>(q) = make_uint2(w[0], w[1]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i < n) q[i] = (uint8_t)(w[i / 4] >> (8 * (i % 4)));
+    }
+  }
+  if (writes_scale) *scale = (uint8_t)code;
+}
+
+// ------------------------------------------------------------------ activations
+// gelu's 0.5 (1 + tanh u) is the logistic function of 2u, so gelu and silu are
+// both z * logistic(a): one exponential and one reciprocal a value, and a
+// relative (not absolute) error where the result is small.
+constexpr float kGelu2C = 1.5957691216057308f;  // 2 sqrt(2 / pi)
+constexpr float kGeluA = 0.044715f;
+
+__device__ __forceinline__ float logistic(float a) { return __fdividef(1.0f, 1.0f + __expf(-a)); }
+
+template <int ACT>
+__device__ __forceinline__ float act_value(float z) {
+  if constexpr (ACT == SCAPE_ACT_RELU) return z > 0.0f ? z : (z != z ? z : 0.0f);
+  if constexpr (ACT == SCAPE_ACT_GELU)
+    return z * logistic(kGelu2C * z * (1.0f + kGeluA * z * z));
+  if constexpr (ACT == SCAPE_ACT_SILU) return z * logistic(z);
+  return z;
+}
+// Past |z| = 20 the logistic is 0 or 1 to the last bit and its slope term is 0;
+// the clamp keeps 0 times an overflowed z^3 out.  A NaN comes back through p.
+template <int ACT>
+__device__ __forceinline__ float act_slope(float z) {
+  if constexpr (ACT == SCAPE_ACT_RELU) return z > 0.0f ? 1.0f : (z != z ? z : 0.0f);
+  if constexpr (ACT == SCAPE_ACT_GELU) {
+    const float p = logistic(kGelu2C * z * (1.0f + kGeluA * z * z));
+    const float c = fminf(fmaxf(z, -20.0f), 20.0f);
+    const float du = kGelu2C * (1.0f + 3.0f * kGeluA * c * c);
+    return p + c * du * p * (1.0f - p);
+  }
+  if constexpr (ACT == SCAPE_ACT_SILU) {
+    const float p = logistic(z);
+    const float c = fminf(fmaxf(z, -100.0f), 100.0f);
+    return p + c * p * (1.0f - p);
+  }
+  return 1.0f;
+}
+
+// Runs f.template operator()<ACT>() for an activation known at run time.
+#define SCAPE_ACT_SWITCH(act, CALL)                              \
+  switch (act) {                                                 \
+    case SCAPE_ACT_RELU: { constexpr int ACT = SCAPE_ACT_RELU; CALL; break; } \
+    case SCAPE_ACT_GELU: { constexpr int ACT = SCAPE_ACT_GELU; CALL; break; } \
+    case SCAPE_ACT_SILU: { constexpr int ACT = SCAPE_ACT_SILU; CALL; break; } \
+    default: { constexpr int ACT = SCAPE_ACT_NONE; CALL; break; }             \
+  }
+
+// ------------------------------------------------------------------ launchers
+cudaError_t launch_pack8(const void* x, int64_t ldx, int dtype, int64_t rows, int64_t cols,
+                         uint8_t* q, int64_t ldq, uint8_t* scale, cudaStream_t st);
+cudaError_t launch_unpack8(const uint8_t* q, int64_t ldq, const uint8_t* scale, int64_t rows,
+                           int64_t cols, int act, void* y, int64_t ldy, int dtype,
+                           cudaStream_t st);
+cudaError_t launch_act_grad(const void* dy, int64_t lddy, const uint8_t* q, int64_t ldq,
+                            const uint8_t* scale, int64_t rows, int64_t cols, int act, void* dz,
+                            int64_t lddz, int dtype, cudaStream_t st);
+
+struct NormFwd {
+  const void *x, *res, *w;
+  int64_t ldx, ldres, ldy, ldh, ldq;
+  int w_bf16;
+  int64_t rows;
+  int cols;
+  float eps;
+  void *y, *h;
+  float* rstd;
+  uint8_t *q, *scale;
+};
+cudaError_t launch_norm_fwd(const NormFwd& a, int dtype, cudaStream_t st);
+
+struct NormBwd {
+  const void *dy, *h, *w, *dh;
+  int64_t lddy, ldh, lddh, lddx;
+  const float* rstd;
+  int w_bf16, dw_bf16;
+  int64_t rows;
+  int cols;
+  void *dx, *dw;
+  float* partial;  // rows of partial weight gradients, one a block
+};
+int64_t norm_bwd_partials(int64_t rows, int64_t cols);
+cudaError_t launch_norm_bwd(const NormBwd& a, int dtype, cudaStream_t st);
+
+// Column sums of m[rows, cols] (bfloat16) in 32 bits.
+int64_t colsum_partials(int64_t rows, int64_t cols);
+cudaError_t launch_colsum(const bf16* m, int64_t ld, int64_t rows, int64_t cols, float* partial,
+                          void* out, int out_bf16, cudaStream_t st);
+// Sum of `parts` rows of partial[parts, cols].
+cudaError_t launch_sum_partials(const float* partial, int64_t parts, int64_t cols, void* out,
+                                int out_bf16, cudaStream_t st);
+
+}  // namespace layer
+}  // namespace scapek
