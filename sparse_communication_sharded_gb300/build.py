@@ -1,8 +1,9 @@
-"""Build the SCAPE CUDA library (libscape.so) in-tree for sm_103a.
+"""Build the SCAPE CUDA library (libscape.so) in-tree for sm_103a, and the torch
+binding of its training-layer operators (_layers_torch.so).
 
-Each translation unit under csrc/ is compiled by nvcc in parallel, then linked
-into sparse_communication_sharded_gb300/_build/libscape.so.  No CMake; one
--gencode (compute_103a -> sm_103a).
+Each translation unit under csrc/ is compiled in parallel (.cu by nvcc, the
+binding by g++), then linked into sparse_communication_sharded_gb300/_build/.
+No CMake; one -gencode (compute_103a -> sm_103a).
 """
 from __future__ import annotations
 
@@ -11,6 +12,7 @@ import glob
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -18,6 +20,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libscape.so")
+BINDING_SRC = os.path.join(CSRC, "layers_torch.cpp")
+BINDING = os.path.join(BUILD, "_layers_torch.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2",
@@ -35,15 +39,47 @@ def _sources():
 
 
 def _deps():
-    return (_sources() + glob.glob(os.path.join(CSRC, "*.cuh"))
+    return (_sources() + [BINDING_SRC] + glob.glob(os.path.join(CSRC, "*.cuh"))
             + glob.glob(os.path.join(INCLUDE, "*.h")))
 
 
 def is_stale() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BINDING):
         return True
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     return any(os.path.getmtime(p) > t for p in _deps())
+
+
+def _torch_dir():
+    import torch
+    return os.path.dirname(torch.__file__), int(torch._C._GLIBCXX_USE_CXX11_ABI)
+
+
+def _compile_binding():
+    torch_dir, abi = _torch_dir()
+    cuda = os.path.dirname(os.path.dirname(_nvcc())) or "/usr/local/cuda"
+    obj = os.path.join(BUILD, "layers_torch.o")
+    inc = [INCLUDE, os.path.join(torch_dir, "include"),
+           os.path.join(torch_dir, "include/torch/csrc/api/include"),
+           os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={abi}",
+           *[f"-I{d}" for d in inc], "-c", BINDING_SRC, "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {BINDING_SRC}:\n{r.stderr}")
+    return obj
+
+
+def _link_binding(obj):
+    lib = os.path.join(_torch_dir()[0], "lib")
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = ["g++", "-shared", "-o", tmp, obj, f"-L{BUILD}", "-lscape", f"-L{lib}", "-ltorch_python",
+           "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN",
+           f"-Wl,-rpath,{lib}"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{r.stderr}")
+    os.replace(tmp, BINDING)
 
 
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
@@ -61,8 +97,10 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
             raise RuntimeError(f"nvcc failed on {src}:\n{r.stderr}")
         return obj, r.stderr
 
-    with cf.ThreadPoolExecutor(max_workers=4) as ex:
+    with cf.ThreadPoolExecutor(max_workers=8) as ex:
+        binding = ex.submit(_compile_binding)
         results = list(ex.map(compile_one, _sources()))
+        binding_obj = binding.result()
     if verbose_ptxas:
         for _, log in results:
             sys.stderr.write(log)
@@ -73,6 +111,7 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, LIB)
+    _link_binding(binding_obj)
     return LIB
 
 
