@@ -64,6 +64,10 @@ int64_t round8(int64_t n) { return (n + 7) / 8 * 8; }
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 size_t copy_bytes(int64_t rows, int64_t cols) { return round256((size_t)rows * round8(cols) * 2); }
 
+bool rows32(const void* p, int64_t ld, size_t elem) {
+  return aligned(p, 32) && (ld * (int64_t)elem) % 32 == 0;
+}
+
 // TMA reads rows that start on 16-byte boundaries; other operands are first
 // copied to such rows in the workspace.
 bool tma_rows(const void* p, int64_t ld) { return rows16(p, ld, 2); }
@@ -119,8 +123,29 @@ cudaError_t gemm_status_word(unsigned int** word) {
   return cudaSuccess;
 }
 
-cudaError_t gemm_tensor_map(CUtensorMap* map, const bf16* p, int64_t rows, int64_t cols,
-                            int64_t ld, int box_rows) {
+cudaError_t gemm_allow_smem(const void* kernel, int bytes) {
+  // per device, the kernels already told
+  struct Told {
+    std::atomic<const void*> kernel[32];
+  };
+  static Told told[kMaxDevices];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  for (auto& k : told[dev].kernel) {
+    const void* have = k.load(std::memory_order_acquire);
+    if (have == kernel) return cudaSuccess;
+    if (have) continue;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) k.compare_exchange_strong(have, kernel, std::memory_order_acq_rel);
+    return e;
+  }
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
+cudaError_t gemm_tensor_map(CUtensorMap* map, const void* p, int64_t rows, int64_t cols,
+                            int64_t ld, int box_rows, int box_cols) {
   using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
                               const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
                               const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
@@ -139,12 +164,12 @@ cudaError_t gemm_tensor_map(CUtensorMap* map, const bf16* p, int64_t rows, int64
   }
   const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
   const cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
-  const cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
+  const cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
   const cuuint32_t ones[2] = {1, 1};
-  const CUresult r = f(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<bf16*>(p), dims,
+  const CUresult r = f(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(p), dims,
                        strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                       CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                       box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                       CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
@@ -320,12 +345,11 @@ extern "C" int scape_layer_linear(const void* x, int64_t ldx, const void* weight
   c.m = rows, c.n = n, c.k = k;
   c.e.act = activation;
   c.e.bias = static_cast<const bf16*>(bias);
-  c.e.bias_vec = aligned(bias, 16);
   c.e.res = static_cast<const bf16*>(residual);
   c.e.ldres = ldres;
-  c.e.res_vec = rows16(residual, ldres, 2);
+  c.e.res_vec = rows16(residual, ldres, 2) + rows32(residual, ldres, 2);
   c.e.q = q, c.e.ldq = ldq, c.e.scale = scale;
-  c.e.q_vec = rows16(q, ldq, 1);
+  c.e.q_vec = rows16(q, ldq, 1) + rows32(q, ldq, 1);
   c.e.blocks_per_row = ceil_div(n, kBlock);
   c.e.out = y, c.e.ldo = ldy;
   c.e.out_vec = rows16(y, ldy, 2);
@@ -368,7 +392,7 @@ extern "C" int scape_layer_linear_bwd_input(const void* dy, int64_t lddy, const 
   c.m = rows, c.n = k, c.k = n;
   c.e.act = activation;
   c.e.pre_q = q, c.e.ldpre = ldq, c.e.pre_scale = scale;
-  c.e.pre_vec = rows8(q, ldq);
+  c.e.pre_vec = rows8(q, ldq) + rows32(q, ldq, 1);
   c.e.blocks_per_row = ceil_div(k, kBlock);
   c.e.out = dx, c.e.ldo = lddx;
   c.e.out_vec = rows16(dx, lddx, 2);

@@ -126,8 +126,7 @@ __global__ __launch_bounds__(kThreads) void unpack8_kernel(const uint8_t* q, int
   for (int i = 0; i < kUnroll; ++i) {
     float v[VEC];
     values_of<VEC>(p[i], v);
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) v[j] = act_value<ACT>(v[j]);
+    act_values<ACT, sizeof(T) == 4>(v);
     store_part<VEC>(y + un[i].row * ldy + un[i].col, un[i].n, v);
   }
 }
@@ -150,8 +149,9 @@ __global__ __launch_bounds__(kThreads) void act_grad_kernel(
   for (int i = 0; i < kUnroll; ++i) {
     float v[VEC];
     values_of<VEC>(p[i], v);
+    act_slopes<ACT>(v);
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) v[j] = g[i][j] * act_slope<ACT>(v[j]);
+    for (int j = 0; j < VEC; ++j) v[j] *= g[i][j];
     store_part<VEC>(dz + un[i].row * lddz + un[i].col, un[i].n, v);
   }
 }

@@ -36,7 +36,8 @@ struct Epilogue {
   void* out;
   int64_t ldo;
   int out_f32;
-  int out_vec, res_vec, q_vec, pre_vec, bias_vec;  // rows (or the vector) aligned for 16 bytes
+  // rows aligned for 16 bytes (1; pre: 8 bytes) or for 32 (2)
+  int out_vec, res_vec, q_vec, pre_vec;
 };
 
 struct GemmOperand {
@@ -57,12 +58,16 @@ cudaError_t gemm_forward(const GemmCall& c, cudaStream_t st);
 cudaError_t gemm_input_grad(const GemmCall& c, cudaStream_t st);
 cudaError_t gemm_weight_grad(const GemmCall& c, cudaStream_t st);
 
+// Lets a kernel use this much dynamic shared memory (asked of CUDA once).
+cudaError_t gemm_allow_smem(const void* kernel, int bytes);
+
 // Where kernels record that they gave up a wait (one word a device).
 cudaError_t gemm_status_word(unsigned int** word);
 
-// 2-D tensor map of 64-column, `box_rows`-row boxes with 128-byte swizzle.
-cudaError_t gemm_tensor_map(CUtensorMap* map, const bf16* p, int64_t rows, int64_t cols,
-                            int64_t ld, int box_rows);
+// 2-D tensor map of box_rows x box_cols boxes, their rows (64 or 128 bytes)
+// swizzled over that width.
+cudaError_t gemm_tensor_map(CUtensorMap* map, const void* p, int64_t rows, int64_t cols,
+                            int64_t ld, int box_rows, int box_cols);
 
 #ifdef __CUDACC__
 
@@ -91,18 +96,60 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
+// The same with the visibility of writes made elsewhere in the cluster.
+__device__ __forceinline__ bool mbar_try_cluster(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 __device__ __forceinline__ uint64_t now_ns() {
   uint64_t t;
   asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
   return t;
 }
+// PAIR: the copy signals a barrier of the pair's first block (bar is that one's
+// address in the cluster).
+template <bool PAIR>
 __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int x, int y,
                                          uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-      "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
-      "l"(map), "r"(x), "r"(y), "r"(bar)
-      : "memory");
+  if constexpr (PAIR) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile"
+        ".mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+  } else {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+  }
+}
+__device__ __forceinline__ void tma_store(const CUtensorMap* map, int x, int y, uint32_t src) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                   map),
+               "r"(x), "r"(y), "r"(src)
+               : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+// At most N of this thread's stores still read shared memory.
+template <int N>
+__device__ __forceinline__ void tma_store_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void tma_store_wait_all() {
+  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+}
+// This thread's shared memory writes, before a bulk copy reads them.
+__device__ __forceinline__ void fence_for_bulk() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 __device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t (&r)[32]) {
   asm volatile(
@@ -125,52 +172,121 @@ __device__ __forceinline__ void tc_fence_before() {
 __device__ __forceinline__ void tc_fence_after() {
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
+// Arrives on bar when the matrix instructions issued so far are done; PAIR: on
+// the barrier at that address in both blocks.
+template <bool PAIR>
 __device__ __forceinline__ void tc_commit(uint32_t bar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
-      : "memory");
+  if constexpr (PAIR) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+        "[%0], %1;" ::"r"(bar),
+        "h"((uint16_t)3)
+        : "memory");
+  } else {
+    asm volatile(
+        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+        : "memory");
+  }
 }
+template <bool PAIR>
 __device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
                                        bool accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
-      : "memory");
+  if constexpr (PAIR) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
+        : "memory");
+  } else {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
+        : "memory");
+  }
+}
+template <bool PAIR>
+__device__ __forceinline__ void tmem_alloc(uint32_t* where, int columns) {
+  if constexpr (PAIR) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_addr(where)),
+                 "r"(columns)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+  } else {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_addr(where)),
+                 "r"(columns)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+}
+template <bool PAIR>
+__device__ __forceinline__ void tmem_free(uint32_t tmem, int columns) {
+  if constexpr (PAIR)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(columns));
+  else
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(columns));
 }
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
                    : "memory");
 }
-__device__ __forceinline__ float cluster_load(uint32_t addr, uint32_t rank) {
+__device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, uint32_t rank) {
   uint32_t remote;
-  float v;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(addr), "r"(rank));
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(remote) : "memory");
+  return remote;
+}
+__device__ __forceinline__ void cluster_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ float cluster_load(uint32_t addr, uint32_t rank) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr(addr, rank)) : "memory");
   return v;
 }
 
 // ------------------------------------------------------------------ tiles
-constexpr int kBM = 128;   // rows of a tile: the tensor core's 128 accumulator lanes
-constexpr int kBK = 64;    // contraction a stage: one 128-byte swizzled row of bfloat16
-constexpr int kChunk = 8192;  // bytes of 64 staged rows of 128 bytes
-constexpr int kGemmThreads = 384;       // TMA, MMA, TMEM, one idle warp; 8 epilogue warps
+constexpr int kBM = 128;  // rows of a block's tile: the tensor core's 128 accumulator lanes
+constexpr int kBK = 64;   // contraction a stage: one 128-byte swizzled row of bfloat16
+constexpr int kChunk = 8192;       // bytes of 64 staged rows of 128 bytes
+constexpr int kGemmThreads = 384;  // TMA, MMA, TMEM, one idle warp; 8 epilogue warps
 constexpr int kEpilogueWarps = 8;
+constexpr int kBoxBytes = 2048;    // 32 x 32 bfloat16 on their way out
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 
-template <int BN>
+// How a product is laid over the blocks.
+enum GemmMode {
+  // One tile a cluster of 1 to 8 blocks, the contraction cut over them.
+  kModeSplit = 0,
+  // Persistent pairs of blocks on neighbouring SMs: the pair's 256 x BN tile is
+  // one tensor-core instruction stream, each block holding half of either
+  // operand, so a byte read feeds twice the work it does in a single block.
+  kModePair = 1
+};
+
+template <int BN, int MODE>
 struct Tile {
+  static constexpr bool kPair = MODE == kModePair;
+  static constexpr int kBRows = kPair ? BN / 2 : BN;  // operand B rows a block stages
   static constexpr int kABytes = kBM * kBK * 2;
-  static constexpr int kBBytes = BN * kBK * 2;
+  static constexpr int kBBytes = kBRows * kBK * 2;
   static constexpr int kStageBytes = kABytes + kBBytes;
-  static constexpr int kStages = BN == 256 ? 4 : BN == 128 ? 6 : 8;
+  // as many stages as fit beside the output boxes and the bias
+  static constexpr int kStages = kStageBytes > 24576 ? 5 : kStageBytes > 16384 ? 6 : 8;
   static constexpr int kColumns = 2 * BN;  // two accumulators
+  static constexpr int kWarpCols = BN / 2;  // columns an epilogue warp handles
+  static constexpr int kBoxAt = kStages * kStageBytes;
+  static constexpr int kBiasAt = kBoxAt + kEpilogueWarps * 2 * kBoxBytes;
+  static constexpr int kSmem = kBiasAt + kEpilogueWarps * kWarpCols * 4 + 1024;
   // column stride of the partial tile that split products exchange: odd, and 8
   // columns apart fall 8 banks apart
   static constexpr int kPartialLd = kBM + 1;
-  static constexpr int kSmem = kStages * kStageBytes + 1024;
-  static_assert(kPartialLd * BN * 4 <= kStages * kStageBytes, "partial tile fits the stages");
+  static_assert(kPair || kPartialLd * BN * 4 <= kStages * kStageBytes, "partial tile fits");
+  static_assert(kSmem <= 232448, "shared memory of a block");
+  static_assert(kBRows % 64 == 0, "transposed operands are staged 64 rows at a time");
 };
 
 // Matrix descriptor of a 128-byte swizzled operand.  Contraction-major: 8-row
@@ -184,13 +300,13 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, bool transposed) {
   d |= (uint64_t)2 << 61;  // 128-byte swizzle
   return d;
 }
-template <int BN, bool TA, bool TB>
+template <int ROWS, int BN, bool TA, bool TB>
 __device__ __forceinline__ constexpr uint32_t instr_desc() {
   return (1u << 4)            // 32-bit float accumulator
          | (1u << 7)          // A bfloat16
          | (1u << 10)         // B bfloat16
          | ((TA ? 1u : 0u) << 15) | ((TB ? 1u : 0u) << 16) | ((uint32_t)(BN >> 3) << 17) |
-         ((uint32_t)(kBM >> 4) << 24);
+         ((uint32_t)(ROWS >> 4) << 24);
 }
 
 // ------------------------------------------------------------------ epilogue
@@ -206,40 +322,47 @@ __device__ __forceinline__ uint32_t block_top(uint32_t t) {
   return t;
 }
 
-template <int N>
-__device__ __forceinline__ void load_bf16_row(const bf16* p, int left, bool vec, float (&v)[N]) {
-  if (vec && left >= N) {
-#pragma unroll
-    for (int i = 0; i < N / 8; ++i) {
-      float t[8];
-      load_vec<8>(p + 8 * i, t);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[8 * i + j] = t[j];
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = i < left ? __bfloat162float(p[i]) : 0.0f;
-  }
+__device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]),
+               "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+__device__ __forceinline__ void load32(const void* p, uint32_t* w) {
+  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]),
+                 "=r"(w[6]), "=r"(w[7])
+               : "l"(p)
+               : "memory");
 }
 
 template <int N>
-__device__ __forceinline__ void pack_row(float (&v)[N], int left, bool live, const Epilogue& e,
-                                         int64_t row, int c0) {
+__device__ __forceinline__ void pack_row(const float (&v)[N], int left, bool live,
+                                         const Epilogue& e, int64_t row, int c0) {
   float z[N];
+  if (left >= N) {
 #pragma unroll
-  for (int i = 0; i < N; ++i) z[i] = i < left ? v[i] : 0.0f;
+    for (int i = 0; i < N; ++i) z[i] = v[i];
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) z[i] = i < left ? v[i] : 0.0f;
+  }
   uint32_t top = block_top<N>(part_top<N>(z));
-  const bool odd = top >= kInfBits;
-  const uint32_t finite = block_top<N>(part_top_finite<N>(z));
-  if (odd) top = finite;
+  bool no_inf = true;
+  if (__any_sync(0xFFFFFFFFu, top >= kInfBits)) {
+    const uint32_t finite = block_top<N>(part_top_finite<N>(z));
+    if (top >= kInfBits) top = finite;
+    no_inf = false;
+  }
   const uint32_t code = scale_code(top);
   uint32_t w[N / 4];
-  to_e4m3<N>(z, scale_inverse(code), !odd, w);
+  to_e4m3<N>(z, scale_inverse(code), no_inf, w);
   if (!live || left <= 0) return;
   uint8_t* q = e.q + row * e.ldq + c0;
-  if (e.q_vec && left >= N) {
+  if (left >= N && e.q_vec) {
     if constexpr (N == 8) {
       *reinterpret_cast<uint2*>(q) = make_uint2(w[0], w[1]);
+    } else if (e.q_vec == 2) {
+      store32(q, w);
     } else {
 #pragma unroll
       for (int i = 0; i < N / 16; ++i)
@@ -253,46 +376,95 @@ __device__ __forceinline__ void pack_row(float (&v)[N], int left, bool live, con
   if (c0 % kBlock == 0) e.scale[row * e.blocks_per_row + c0 / kBlock] = (uint8_t)code;
 }
 
+// What the epilogue reads of its row from memory: N bfloat16 of the residual,
+// or N 8-bit values and their scale.
 template <int KIND, int N>
-__device__ __forceinline__ void epilogue_row(float (&v)[N], bool live, int64_t row, int c0,
-                                             int left, const Epilogue& e) {
+struct Beside {
+  uint32_t w[KIND == kGemmForward ? N / 2 : KIND == kGemmInputGrad ? N / 4 : 1];
+  uint32_t code;
+};
+template <int KIND, int N>
+__device__ __forceinline__ void load_beside(Beside<KIND, N>& b, bool live, int64_t row, int c0,
+                                            int left, const Epilogue& e) {
   if constexpr (KIND == kGemmForward) {
-    if (e.bias) {
-      float b[N];
-      load_bf16_row<N>(e.bias + c0, left, e.bias_vec, b);
-#pragma unroll
-      for (int i = 0; i < N; ++i) v[i] += b[i];
-    }
-    if (e.q) pack_row<N>(v, left, live, e, row, c0);
-    SCAPE_ACT_SWITCH(e.act, _Pragma("unroll") for (int i = 0; i < N; ++i) v[i] = act_value<ACT>(v[i]));
-    if (!live) return;
-    if (e.res) {
-      float r[N];
-      load_bf16_row<N>(e.res + row * e.ldres + c0, left, e.res_vec, r);
-#pragma unroll
-      for (int i = 0; i < N; ++i) v[i] += r[i];
-    }
-  }
-  if (!live || left <= 0) return;
-  if constexpr (KIND == kGemmInputGrad) {
-    if (e.act != SCAPE_ACT_NONE) {
-      const uint8_t* p = e.pre_q + row * e.ldpre + c0;
-      const float s = scale_value(e.pre_scale[row * e.blocks_per_row + c0 / kBlock]);
-      float z[N];
-      if (e.pre_vec && left >= N) {
-#pragma unroll
-        for (int i = 0; i < N / 8; ++i) {
-          const uint2 w = reinterpret_cast<const uint2*>(p)[i];
-          from_e4m3(w.x, s, z + 8 * i);
-          from_e4m3(w.y, s, z + 8 * i + 4);
-        }
+    if (!e.res || !live || left <= 0) return;
+    const bf16* p = e.res + row * e.ldres + c0;
+    if (left >= N && e.res_vec) {
+      if (N == 32 && e.res_vec == 2) {
+        load32(p, b.w);
+        load32(p + 16, b.w + 8 % (N / 2));
       } else {
 #pragma unroll
-        for (int i = 0; i < N; ++i) z[i] = i < left ? from_e4m3_byte(p[i], s) : 0.0f;
+        for (int i = 0; i < N / 8; ++i) {
+          const uint4 u = reinterpret_cast<const uint4*>(p)[i];
+          b.w[4 * i] = u.x, b.w[4 * i + 1] = u.y, b.w[4 * i + 2] = u.z, b.w[4 * i + 3] = u.w;
+        }
       }
-      SCAPE_ACT_SWITCH(e.act, _Pragma("unroll") for (int i = 0; i < N; ++i) v[i] *= act_slope<ACT>(z[i]));
+    } else {
+      const uint16_t* s = reinterpret_cast<const uint16_t*>(p);
+#pragma unroll
+      for (int i = 0; i < N / 2; ++i)
+        b.w[i] = (2 * i < left ? s[2 * i] : 0u) |
+                 ((uint32_t)(2 * i + 1 < left ? s[2 * i + 1] : 0u) << 16);
+    }
+  } else if constexpr (KIND == kGemmInputGrad) {
+    if (e.act == SCAPE_ACT_NONE || !live || left <= 0) return;
+    const uint8_t* p = e.pre_q + row * e.ldpre + c0;
+    b.code = e.pre_scale[row * e.blocks_per_row + c0 / kBlock];
+    if (left >= N && e.pre_vec) {
+      if (N == 32 && e.pre_vec == 2) {
+        load32(p, b.w);
+      } else {
+#pragma unroll
+        for (int i = 0; i < N / 8; ++i) {
+          const uint2 u = reinterpret_cast<const uint2*>(p)[i];
+          b.w[2 * i] = u.x, b.w[2 * i + 1] = u.y;
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < N / 4; ++i) {
+        b.w[i] = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (4 * i + j < left) b.w[i] |= (uint32_t)p[4 * i + j] << (8 * j);
+      }
     }
   }
+}
+
+// The accumulators become the values to store; the 8-bit form is stored here.
+// All 32 lanes call it.
+template <int KIND, int N>
+__device__ __forceinline__ void epilogue_math(float (&v)[N], const Beside<KIND, N>& b, bool live,
+                                              int64_t row, int c0, int left, const Epilogue& e) {
+  if constexpr (KIND == kGemmForward) {
+    if (e.q) pack_row<N>(v, left, live, e, row, c0);
+    SCAPE_ACT_SWITCH(e.act, act_values<ACT>(v));
+    if (e.res && live && left > 0) {
+#pragma unroll
+      for (int i = 0; i < N / 2; ++i) {
+        v[2 * i] += __uint_as_float(b.w[i] << 16);
+        v[2 * i + 1] += __uint_as_float(b.w[i] & 0xFFFF0000u);
+      }
+    }
+  } else if constexpr (KIND == kGemmInputGrad) {
+    if (e.act != SCAPE_ACT_NONE && live && left > 0) {
+      const float s = scale_value(b.code);
+      float z[N];
+#pragma unroll
+      for (int i = 0; i < N / 4; ++i) from_e4m3(b.w[i], s, z + 4 * i);
+      SCAPE_ACT_SWITCH(e.act, act_slopes<ACT>(z));
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] *= z[i];
+    }
+  }
+}
+
+// Stores N values of a row straight from registers.
+template <int KIND, int N>
+__device__ __forceinline__ void store_row(const float (&v)[N], int64_t row, int c0, int left,
+                                          const Epilogue& e) {
   if (KIND == kGemmWeightGrad && e.out_f32) {
     float* o = static_cast<float*>(e.out) + row * e.ldo + c0;
     if (e.out_vec && left >= N) {
@@ -320,6 +492,40 @@ __device__ __forceinline__ void epilogue_row(float (&v)[N], bool live, int64_t r
   }
 }
 
+// A warp's 32 x 32 values, one row a lane, through shared memory: 64-byte rows
+// whose 16-byte quarters are swizzled as the output's tensor map has them, so
+// neither side meets a bank twice.  Aligned outputs leave as one bulk copy
+// (which cuts what is past the matrix), others row by row, a lane a column.
+__device__ __forceinline__ void store_box(const float (&v)[32], uint32_t box, int lane,
+                                          const CUtensorMap* map, int64_t row0, int c0, int rows,
+                                          int left, const Epilogue& e) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    asm volatile("st.shared::cta.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                     box + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)),
+                 "r"(bf16_pair(v[8 * j], v[8 * j + 1])), "r"(bf16_pair(v[8 * j + 2], v[8 * j + 3])),
+                 "r"(bf16_pair(v[8 * j + 4], v[8 * j + 5])), "r"(bf16_pair(v[8 * j + 6], v[8 * j + 7]))
+                 : "memory");
+  if (e.out_vec) {
+    fence_for_bulk();
+    __syncwarp();
+    if (lane == 0) tma_store(map, c0, (int)row0, box);
+  } else {
+    __syncwarp();
+    uint16_t* o = static_cast<uint16_t*>(e.out) + row0 * e.ldo + c0 + lane;
+    const uint32_t from = box + (lane & 7) * 2;
+#pragma unroll 8
+    for (int r = 0; r < 32; ++r) {
+      uint16_t x;
+      asm volatile("ld.shared::cta.u16 %0, [%1];"
+                   : "=h"(x)
+                   : "r"(from + r * 64 + (((lane >> 3) ^ ((r >> 1) & 3)) << 4))
+                   : "memory");
+      if (r < rows && lane < left) o[r * e.ldo] = x;
+    }
+  }
+}
+
 // ------------------------------------------------------------------ the kernel
 struct GemmShape {
   int m, n;
@@ -327,13 +533,16 @@ struct GemmShape {
   unsigned int* status;
 };
 
-template <int KIND, int BN, bool SPLIT>
+template <int KIND, int BN, int MODE>
 __global__ __launch_bounds__(kGemmThreads, 1) void gemm_kernel(
     const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-    const GemmShape s, const __grid_constant__ Epilogue e) {
-  using TL = Tile<BN>;
+    const __grid_constant__ CUtensorMap map_out, const GemmShape s,
+    const __grid_constant__ Epilogue e) {
+  using TL = Tile<BN, MODE>;
+  constexpr bool PAIR = MODE == kModePair;
   constexpr bool TA = KIND == kGemmWeightGrad;
   constexpr bool TB = KIND != kGemmForward;
+  constexpr int kTileRows = PAIR ? 2 * kBM : kBM;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t bars[2 * TL::kStages + 5];
   __shared__ uint32_t tmem_base;
@@ -348,34 +557,34 @@ __global__ __launch_bounds__(kGemmThreads, 1) void gemm_kernel(
   auto acc_empty = [&](int i) { return bar0 + 8 * (2 * TL::kStages + 2 + i); };
   const uint32_t drain = bar0 + 8 * (2 * TL::kStages + 4);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint32_t rank, ranks;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(ranks));
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < TL::kStages; ++i) mbar_init(full(i), 1), mbar_init(empty(i), 1);
-    for (int i = 0; i < 2; ++i) mbar_init(acc_full(i), 1), mbar_init(acc_empty(i), kEpilogueWarps);
+    for (int i = 0; i < 2; ++i)
+      mbar_init(acc_full(i), 1), mbar_init(acc_empty(i), kEpilogueWarps * (PAIR ? 2 : 1));
     mbar_init(drain, 1);
     gave_up = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 2) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                     smem_addr(&tmem_base)),
-                 "n"(TL::kColumns)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
-  }
+  if (warp == 2) tmem_alloc<PAIR>(&tmem_base, TL::kColumns);
   tc_fence_before();
   __syncthreads();
+  if constexpr (PAIR) cluster_sync();
   tc_fence_after();
   const uint32_t tmem = tmem_base;
 
   // Every wait ends: after the limit the kernel records it and all its roles
   // stop (they look at gave_up while they wait).
   auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
-    if (mbar_try(bar, parity)) return true;
+    auto once = [&] { return PAIR ? mbar_try_cluster(bar, parity) : mbar_try(bar, parity); };
+    if (once()) return true;
     const uint64_t t0 = now_ns();
     for (;;) {
       for (int i = 0; i < 16; ++i)
-        if (mbar_try(bar, parity)) return true;
+        if (once()) return true;
       if (gave_up) return false;
       if (now_ns() - t0 > kWaitLimitNs) {
         gave_up = 1;
@@ -385,17 +594,11 @@ __global__ __launch_bounds__(kGemmThreads, 1) void gemm_kernel(
     }
   };
 
-  // SPLIT: one tile a cluster, its contraction cut over the cluster's blocks.
-  uint32_t rank = 0, ranks = 1;
-  if constexpr (SPLIT) {
-    asm("mov.u32 %0, %cluster_ctarank;" : "=r"(rank));
-    asm("mov.u32 %0, %cluster_nctarank;" : "=r"(ranks));
-  }
   const int tiles = s.tiles_m * s.tiles_n;
-  const int first = SPLIT ? blockIdx.x / ranks : blockIdx.x;
-  const int step = SPLIT ? tiles : gridDim.x;
-  const int k0 = SPLIT ? (int)((int64_t)s.ksteps * rank / ranks) : 0;
-  const int k1 = SPLIT ? (int)((int64_t)s.ksteps * (rank + 1) / ranks) : s.ksteps;
+  const int first = blockIdx.x / ranks;
+  const int step = PAIR ? gridDim.x / 2 : tiles;
+  const int k0 = PAIR ? 0 : (int)((int64_t)s.ksteps * rank / ranks);
+  const int k1 = PAIR ? s.ksteps : (int)((int64_t)s.ksteps * (rank + 1) / ranks);
   // Tiles are taken down strips of 8 tile rows, so that the blocks at work at one
   // time share operand rows in L2.
   auto tile_at = [&](int t, int& tm, int& tn) {
@@ -408,31 +611,36 @@ __global__ __launch_bounds__(kGemmThreads, 1) void gemm_kernel(
   };
 
   if (warp == 0 && lane == 0) {
-    // ---------------- producer
+    // ---------------- producer: this block's rows of A and of B.  In a pair both
+    // blocks' copies count on the first block's barrier, which expects them all.
+    const uint32_t lead = PAIR ? cluster_addr(bar0, 0) - bar0 : 0;
     int stage = 0, phase = 0;
     int64_t issued = 0;
     bool ok = true;
     for (int t = first; ok && t < tiles; t += step) {
       int tm, tn;
       tile_at(t, tm, tn);
+      const int row_a = tm * kTileRows + (PAIR ? rank * kBM : 0);
+      const int row_b = tn * BN + (PAIR ? rank * TL::kBRows : 0);
       for (int k = k0; k < k1; ++k) {
         ok = wait(empty(stage), phase ^ 1);
         if (!ok) break;
         const uint32_t a = smem + stage * TL::kStageBytes, b = a + TL::kABytes;
-        mbar_expect_tx(full(stage), TL::kStageBytes);
+        const uint32_t bar = full(stage) + lead;
+        if (!PAIR || rank == 0) mbar_expect_tx(full(stage), TL::kStageBytes * (PAIR ? 2 : 1));
         if constexpr (TA) {
 #pragma unroll
           for (int i = 0; i < kBM / 64; ++i)
-            tma_load(a + i * kChunk, &map_a, tm * kBM + i * 64, k * kBK, full(stage));
+            tma_load<PAIR>(a + i * kChunk, &map_a, row_a + i * 64, k * kBK, bar);
         } else {
-          tma_load(a, &map_a, k * kBK, tm * kBM, full(stage));
+          tma_load<PAIR>(a, &map_a, k * kBK, row_a, bar);
         }
         if constexpr (TB) {
 #pragma unroll
-          for (int i = 0; i < BN / 64; ++i)
-            tma_load(b + i * kChunk, &map_b, tn * BN + i * 64, k * kBK, full(stage));
+          for (int i = 0; i < TL::kBRows / 64; ++i)
+            tma_load<PAIR>(b + i * kChunk, &map_b, row_b + i * 64, k * kBK, bar);
         } else {
-          tma_load(b, &map_b, k * kBK, tn * BN, full(stage));
+          tma_load<PAIR>(b, &map_b, k * kBK, row_b, bar);
         }
         ++issued;
         if (++stage == TL::kStages) stage = 0, phase ^= 1;
@@ -440,16 +648,21 @@ __global__ __launch_bounds__(kGemmThreads, 1) void gemm_kernel(
     }
     if (!ok) {
       // let the copies in flight land before the block's memory is given back
-      const int64_t from = issued > TL::kStages ? issued - TL::kStages : 0;
-      for (int64_t i = from; i < issued; ++i) {
-        const uint64_t t0 = now_ns();
-        while (!mbar_try(full((int)(i % TL::kStages)), (uint32_t)((i / TL::kStages) & 1)))
-          if (now_ns() - t0 > kWaitLimitNs) break;
+      const uint64_t t0 = now_ns();
+      if (!PAIR) {
+        const int64_t from = issued > TL::kStages ? issued - TL::kStages : 0;
+        for (int64_t i = from; i < issued; ++i)
+          while (!mbar_try(full((int)(i % TL::kStages)), (uint32_t)((i / TL::kStages) & 1)))
+            if (now_ns() - t0 > kWaitLimitNs) break;
+      } else {
+        // the barrier that counts them may be the other block's: wait a time
+        // that is long for a copy instead
+        while (now_ns() - t0 < kWaitLimitNs / 100) __nanosleep(1000);
       }
     }
-  } else if (warp == 1 && lane == 0) {
+  } else if (warp == 1 && lane == 0 && (!PAIR || rank == 0)) {
     // ---------------- tensor core
-    constexpr uint32_t idesc = instr_desc<BN, TA, TB>();
+    constexpr uint32_t idesc = instr_desc<kTileRows, BN, TA, TB>();
     int stage = 0, phase = 0, acc = 0, acc_phase = 0;
     bool ok = true;
     for (int t = first; ok && t < tiles; t += step) {
@@ -467,17 +680,17 @@ __global__ __launch_bounds__(kGemmThreads, 1) void gemm_kernel(
           // 16 of the contraction: 32 bytes along a row, or 16 rows
           const uint64_t da = smem_desc(a + i * (TA ? 2048 : 32), TA);
           const uint64_t db = smem_desc(b + i * (TB ? 2048 : 32), TB);
-          tc_mma(d, da, db, idesc, k > k0 || i > 0);
+          tc_mma<PAIR>(d, da, db, idesc, k > k0 || i > 0);
         }
-        tc_commit(empty(stage));
+        tc_commit<PAIR>(empty(stage));
         if (++stage == TL::kStages) stage = 0, phase ^= 1;
       }
       if (!ok) break;
-      tc_commit(acc_full(acc));
+      tc_commit<PAIR>(acc_full(acc));
       if (++acc == 2) acc = 0, acc_phase ^= 1;
     }
     if (!ok) {
-      tc_commit(drain);
+      tc_commit<PAIR>(drain);
       const uint64_t t0 = now_ns();
       while (!mbar_try(drain, 0))
         if (now_ns() - t0 > kWaitLimitNs) break;
@@ -486,45 +699,108 @@ __global__ __launch_bounds__(kGemmThreads, 1) void gemm_kernel(
     // ---------------- epilogue: warp w reads the accumulator lanes of its quarter,
     // the two warps of a quarter take half of the columns each
     const int quarter = warp & 3, half = (warp - 4) >> 2;
-    int acc = 0, acc_phase = 0;
+    const uint32_t box = smem + TL::kBoxAt + (warp - 4) * 2 * kBoxBytes;
+    const uint32_t bias_at = smem + TL::kBiasAt + (warp - 4) * TL::kWarpCols * 4;
+    const bool through_box = KIND != kGemmWeightGrad || !e.out_f32;
+    int acc = 0, acc_phase = 0, boxes = 0, bias_tile = -1;
     for (int t = first; t < tiles; t += step) {
       int tm, tn;
       tile_at(t, tm, tn);
+      const int64_t row0 = (int64_t)tm * kTileRows + (PAIR ? rank * kBM : 0) + quarter * 32;
+      const int64_t row = row0 + lane;
+      const bool live = row < s.m;
+      const int col0 = tn * BN + half * TL::kWarpCols;
+      Beside<KIND, 32> next;
+      if constexpr (PAIR) {
+        // before the accumulator is ready: this tile's bias, the first chunk's
+        // residual or 8-bit values
+        if (KIND == kGemmForward && e.bias && bias_tile != tn) {
+          bias_tile = tn;
+          __syncwarp();
+#pragma unroll
+          for (int i = lane; i < TL::kWarpCols; i += 32)
+            asm volatile("st.shared::cta.f32 [%0], %1;" ::"r"(bias_at + 4 * i),
+                         "f"(col0 + i < s.n ? __bfloat162float(e.bias[col0 + i]) : 0.0f)
+                         : "memory");
+          __syncwarp();
+        }
+        load_beside<KIND, 32>(next, live, row, col0, s.n - col0, e);
+      }
       if (!__all_sync(0xFFFFFFFFu, wait(acc_full(acc), acc_phase))) break;
       tc_fence_after();
-      const uint32_t lanes = tmem + acc * BN + ((uint32_t)(quarter * 32) << 16);
-      const int64_t row = (int64_t)tm * kBM + quarter * 32 + lane;
+      const uint32_t lanes = tmem + acc * BN + ((uint32_t)(quarter * 32) << 16) + half * TL::kWarpCols;
 #pragma unroll 1
-      for (int c = half * (BN / 2); c < (half + 1) * (BN / 2); c += 32) {
+      for (int c = 0; c < TL::kWarpCols; c += 32) {
         uint32_t r[32];
         tmem_ld32(lanes + c, r);
-        tmem_ld_wait();
-        if constexpr (SPLIT) {
+        if constexpr (!PAIR) {
+          tmem_ld_wait();
           const uint32_t p = smem + 4 * (quarter * 32 + lane);
 #pragma unroll
           for (int i = 0; i < 32; ++i)
-            asm volatile("st.shared::cta.b32 [%0], %1;" ::"r"(p + 4 * TL::kPartialLd * (c + i)),
+            asm volatile("st.shared::cta.b32 [%0], %1;" ::"r"(
+                             p + 4 * TL::kPartialLd * (half * TL::kWarpCols + c + i)),
                          "r"(r[i])
                          : "memory");
         } else {
-          const int c0 = tn * BN + c;
-          if (c0 < s.n) {
+          const int c0 = col0 + c, left = s.n - c0;
+          const Beside<KIND, 32> beside = next;
+          if (c + 32 < TL::kWarpCols) load_beside<KIND, 32>(next, live, row, c0 + 32, left - 32, e);
+          tmem_ld_wait();
+          if (left > 0) {
             float v[32];
+            if (KIND == kGemmForward && e.bias) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-            epilogue_row<KIND, 32>(v, row < s.m, row, c0, s.n - c0, e);
+              for (int i = 0; i < 8; ++i) {
+                float b0, b1, b2, b3;
+                asm volatile("ld.shared::cta.v4.f32 {%0, %1, %2, %3}, [%4];"
+                             : "=f"(b0), "=f"(b1), "=f"(b2), "=f"(b3)
+                             : "r"(bias_at + 4 * c + 16 * i)
+                             : "memory");
+                unpair(add2(pair(__uint_as_float(r[4 * i]), __uint_as_float(r[4 * i + 1])), pair(b0, b1)),
+                       v[4 * i], v[4 * i + 1]);
+                unpair(add2(pair(__uint_as_float(r[4 * i + 2]), __uint_as_float(r[4 * i + 3])), pair(b2, b3)),
+                       v[4 * i + 2], v[4 * i + 3]);
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+            }
+            epilogue_math<KIND, 32>(v, beside, live, row, c0, left, e);
+            if (through_box) {
+              if (e.out_vec) {
+                // the box two chunks ago has been read
+                if (lane == 0) tma_store_wait_read<1>();
+              }
+              __syncwarp();
+              if (row0 < s.m) {
+                store_box(v, box + (boxes & 1) * kBoxBytes, lane, &map_out, row0, c0,
+                          (int)min((int64_t)32, s.m - row0), left, e);
+                ++boxes;  // counts stores: two in a row never use one box
+              }
+            } else if (live) {
+              store_row<KIND, 32>(v, row, c0, left, e);
+            }
           }
         }
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(acc_empty(acc));
+      if (lane == 0) {
+        if constexpr (PAIR)
+          cluster_arrive(cluster_addr(acc_empty(acc), 0));
+        else
+          mbar_arrive(acc_empty(acc));
+      }
       if (++acc == 2) acc = 0, acc_phase ^= 1;
     }
+    if (lane == 0) tma_store_wait_all();
   }
 
   __syncwarp();
-  if constexpr (SPLIT) {
+  if constexpr (PAIR) {
+    cluster_sync();
+  } else {
     // Each block adds up its share of the tile's rows over the cluster's partial
     // tiles, in rank order.
     cluster_sync();
@@ -536,16 +812,26 @@ __global__ __launch_bounds__(kGemmThreads, 1) void gemm_kernel(
       for (int g = warp - 4; g < groups; g += kEpilogueWarps) {
         const int r = rank * rows + g % (rows / 8) * 8 + (lane & 7);
         const int c = g / (rows / 8) * 32 + (lane >> 3) * 8;
+        const int64_t row = (int64_t)tm * kBM + r;
+        const int c0 = tn * BN + c, left = s.n - c0;
+        const bool live = row < s.m;
+        Beside<KIND, 8> beside;
+        load_beside<KIND, 8>(beside, live, row, c0, left, e);
         float v[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+        for (int i = 0; i < 8; ++i)
+          v[i] = KIND == kGemmForward && e.bias && i < left ? __bfloat162float(e.bias[c0 + i]) : 0.0f;
+        float sum[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum[i] = 0.0f;
         for (uint32_t q = 0; q < ranks; ++q)
 #pragma unroll
           for (int i = 0; i < 8; ++i)
-            v[i] += cluster_load(smem + 4 * (TL::kPartialLd * (c + i) + r), q);
-        const int64_t row = (int64_t)tm * kBM + r;
-        const int c0 = tn * BN + c;
-        epilogue_row<KIND, 8>(v, row < s.m, row, c0, s.n - c0, e);
+            sum[i] += cluster_load(smem + 4 * (TL::kPartialLd * (c + i) + r), q);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] += sum[i];
+        epilogue_math<KIND, 8>(v, beside, live, row, c0, left, e);
+        if (live && left > 0) store_row<KIND, 8>(v, row, c0, left, e);
       }
     }
     __syncwarp();
@@ -555,76 +841,71 @@ __global__ __launch_bounds__(kGemmThreads, 1) void gemm_kernel(
   __syncthreads();
   if (warp == 2) {
     tc_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
-                 "n"(TL::kColumns));
+    tmem_free<PAIR>(tmem, TL::kColumns);
   }
 }
 
 // ------------------------------------------------------------------ launch
-template <int KIND, int BN, bool SPLIT>
+template <int KIND, int BN, int MODE>
 cudaError_t gemm_launch(const GemmCall& c, int split, cudaStream_t st) {
-  using TL = Tile<BN>;
+  using TL = Tile<BN, MODE>;
+  constexpr bool PAIR = MODE == kModePair;
   constexpr bool TA = KIND == kGemmWeightGrad;
   constexpr bool TB = KIND != kGemmForward;
-  CUtensorMap ma, mb;
-  cudaError_t err = TA ? gemm_tensor_map(&ma, c.a.p, c.k, c.m, c.a.ld, kBK)
-                       : gemm_tensor_map(&ma, c.a.p, c.m, c.k, c.a.ld, kBM);
+  CUtensorMap ma, mb, mo;
+  cudaError_t err = TA ? gemm_tensor_map(&ma, c.a.p, c.k, c.m, c.a.ld, kBK, kBK)
+                       : gemm_tensor_map(&ma, c.a.p, c.m, c.k, c.a.ld, kBM, kBK);
   if (err == cudaSuccess)
-    err = TB ? gemm_tensor_map(&mb, c.b.p, c.k, c.n, c.b.ld, kBK)
-             : gemm_tensor_map(&mb, c.b.p, c.n, c.k, c.b.ld, BN);
+    err = TB ? gemm_tensor_map(&mb, c.b.p, c.k, c.n, c.b.ld, kBK, kBK)
+             : gemm_tensor_map(&mb, c.b.p, c.n, c.k, c.b.ld, TL::kBRows, kBK);
+  if (PAIR && c.e.out_vec && !c.e.out_f32) {
+    if (err == cudaSuccess) err = gemm_tensor_map(&mo, c.e.out, c.m, c.n, c.e.ldo, 32, 32);
+  } else {
+    mo = ma;  // not used
+  }
   GemmShape s;
   s.m = (int)c.m;
   s.n = (int)c.n;
-  s.tiles_m = (int)ceil_div(c.m, kBM);
+  s.tiles_m = (int)ceil_div(c.m, PAIR ? 2 * kBM : kBM);
   s.tiles_n = (int)ceil_div(c.n, BN);
   s.ksteps = (int)ceil_div(c.k, kBK);
   if (err == cudaSuccess) err = gemm_status_word(&s.status);
-  auto kernel = gemm_kernel<KIND, BN, SPLIT>;
-  if (err == cudaSuccess)
-    err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, TL::kSmem);
+  auto kernel = gemm_kernel<KIND, BN, MODE>;
+  if (err == cudaSuccess) err = gemm_allow_smem((const void*)kernel, TL::kSmem);
   if (err != cudaSuccess) return err;
   const int64_t tiles = (int64_t)s.tiles_m * s.tiles_n;
+  const int cluster = PAIR ? 2 : split;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(SPLIT ? tiles * split : std::min<int64_t>(tiles, sm_count())));
+  cfg.gridDim = dim3((unsigned)(PAIR ? 2 * std::min<int64_t>(tiles, sm_count() / 2) : tiles * split));
   cfg.blockDim = dim3(kGemmThreads);
   cfg.dynamicSmemBytes = TL::kSmem;
   cfg.stream = st;
   cudaLaunchAttribute at[1];
-  if (SPLIT) {
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = (unsigned)split;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-  }
-  return cudaLaunchKernelEx(&cfg, kernel, ma, mb, s, c.e);
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = (unsigned)cluster;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, ma, mb, mo, s, c.e);
 }
 
-// Tile width and split.  A wide tile reads the fewest bytes a product; a narrow
-// one, or a contraction cut over a cluster of blocks, puts more of the SMs to
-// work.  So: the widest tile that fills the SMs, else the narrowest, and of the
-// contraction as many cuts (a power of two up to the portable cluster of 8) as
-// the SMs have room for with four stages or more left in each.
+// Tile and mode.  Pairs with wide tiles do the most work a byte read and keep
+// the tensor cores busy through the epilogue; they want tiles for most of the
+// SMs.  Below that, narrow tiles, each cut over a cluster as far as there are
+// SMs and at least four stages of the contraction for every block.
 template <int KIND>
 cudaError_t gemm_run(const GemmCall& c, cudaStream_t st) {
   const int64_t sms = sm_count();
+  const int64_t tp = ceil_div(c.m, 2 * kBM);
+  if (tp * ceil_div(c.n, 256) * 2 * 5 >= sms * 4) return gemm_launch<KIND, 256, kModePair>(c, 2, st);
+  if (tp * ceil_div(c.n, 128) * 2 * 5 >= sms * 4) return gemm_launch<KIND, 128, kModePair>(c, 2, st);
   const int64_t tm = ceil_div(c.m, kBM), ksteps = ceil_div(c.k, kBK);
-  int bn = 64;
-  if (tm * ceil_div(c.n, 256) * 5 >= sms * 4)
-    bn = 256;
-  else if (tm * ceil_div(c.n, 128) * 5 >= sms * 4)
-    bn = 128;
+  const int bn = tm * ceil_div(c.n, 64) <= sms ? 64 : 128;
   const int64_t tiles = tm * ceil_div(c.n, bn);
   int split = 1;
   while (split < 8 && tiles * split * 2 <= sms && ksteps / (split * 2) >= 4) split *= 2;
-  if (split > 1) {
-    if (bn == 64) return gemm_launch<KIND, 64, true>(c, split, st);
-    if (bn == 128) return gemm_launch<KIND, 128, true>(c, split, st);
-    return gemm_launch<KIND, 256, true>(c, split, st);
-  }
-  if (bn == 64) return gemm_launch<KIND, 64, false>(c, 1, st);
-  if (bn == 128) return gemm_launch<KIND, 128, false>(c, 1, st);
-  return gemm_launch<KIND, 256, false>(c, 1, st);
+  return bn == 64 ? gemm_launch<KIND, 64, kModeSplit>(c, split, st)
+                  : gemm_launch<KIND, 128, kModeSplit>(c, split, st);
 }
 
 #endif  // __CUDACC__

@@ -151,24 +151,19 @@ __device__ __forceinline__ float scale_inverse(uint32_t code) {
 __device__ __forceinline__ uint32_t e4m3_pair(float a, float b) {
   return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
 }
-// Infinities become NaN (the conversion would clamp them).
+// Infinities become NaN (the conversion would clamp them); a NaN stays one.
 __device__ __forceinline__ float nan_unless_finite(float x) {
   return abs_bits(x) >= kInfBits ? __uint_as_float(0x7FC00000u) : x;
 }
-// Scaling by a power of two is exact down to the subnormals, where e4m3 is 0.
-__device__ __forceinline__ uint32_t e4m3_byte(float x, float inv) {
-  return e4m3_pair(nan_unless_finite(x * inv), 0.0f) & 0xFFu;
-}
 
-// N values of one block (or an N-long part of it) that one thread holds; `top`
-// is the block's largest magnitude's bits over all values, infinities and NaN
-// included, `finite` gives the largest finite one when those are present.
+// Bits of the largest magnitude among N values (not counting NaN), and among
+// the finite ones.
 template <int N>
 __device__ __forceinline__ uint32_t part_top(const float (&v)[N]) {
-  uint32_t t = 0;
+  float t = 0.0f;
 #pragma unroll
-  for (int i = 0; i < N; ++i) t = max(t, abs_bits(v[i]));
-  return t;
+  for (int i = 0; i < N; ++i) t = fmaxf(t, fabsf(v[i]));
+  return __float_as_uint(t);
 }
 template <int N>
 __device__ __forceinline__ uint32_t part_top_finite(const float (&v)[N]) {
@@ -180,15 +175,16 @@ __device__ __forceinline__ uint32_t part_top_finite(const float (&v)[N]) {
   }
   return t;
 }
-// e4m3 words of N values (N a multiple of 4) at a scale.
+// e4m3 words of N values (N a multiple of 4) at a scale.  Scaling by a power of
+// two is exact down to the subnormals, where e4m3 is 0.
 template <int N>
-__device__ __forceinline__ void to_e4m3(const float (&v)[N], float inv, bool all_finite,
+__device__ __forceinline__ void to_e4m3(const float (&v)[N], float inv, bool no_inf,
                                         uint32_t (&w)[N / 4]) {
 #pragma unroll
   for (int i = 0; i < N / 4; ++i) {
     float a = v[4 * i] * inv, b = v[4 * i + 1] * inv, c = v[4 * i + 2] * inv,
           d = v[4 * i + 3] * inv;
-    if (!all_finite) {
+    if (!no_inf) {
       a = nan_unless_finite(a), b = nan_unless_finite(b);
       c = nan_unless_finite(c), d = nan_unless_finite(d);
     }
@@ -214,12 +210,12 @@ template <int VEC>
 __device__ __forceinline__ void warp_pack(const float (&v)[VEC], int n, uint8_t* q, uint8_t* scale,
                                           bool writes_scale) {
   uint32_t top = part_top<VEC>(v);
-  bool all_finite = true;
+  bool no_inf = true;
   if constexpr (VEC == 1) {
     top = __reduce_max_sync(0xFFFFFFFFu, top);
     if (top >= kInfBits) {
       top = __reduce_max_sync(0xFFFFFFFFu, part_top_finite<VEC>(v));
-      all_finite = false;
+      no_inf = false;
     }
   } else {
     top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
@@ -228,16 +224,17 @@ __device__ __forceinline__ void warp_pack(const float (&v)[VEC], int n, uint8_t*
       top = part_top_finite<VEC>(v);
       top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
       top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-      all_finite = false;
+      no_inf = false;
     }
   }
   const uint32_t code = scale_code(top);
   const float inv = scale_inverse(code);
   if constexpr (VEC == 1) {
-    if (n > 0) *q = (uint8_t)e4m3_byte(v[0], inv);
+    const float x = v[0] * inv;
+    if (n > 0) *q = (uint8_t)e4m3_pair(no_inf ? x : nan_unless_finite(x), 0.0f);
   } else {
     uint32_t w[2];
-    to_e4m3<8>(v, inv, all_finite, w);
+    to_e4m3<8>(v, inv, no_inf, w);
     if (n >= 8) {
       *reinterpret_cast<uint2*>(q) = make_uint2(w[0], w[1]);
     } else {
@@ -252,40 +249,150 @@ __device__ __forceinline__ void warp_pack(const float (&v)[VEC], int n, uint8_t*
 // ------------------------------------------------------------------ activations
 // gelu's 0.5 (1 + tanh u) is the logistic function of 2u, so gelu and silu are
 // both z * logistic(a): one exponential and one reciprocal a value, and a
-// relative (not absolute) error where the result is small.
-constexpr float kGelu2C = 1.5957691216057308f;  // 2 sqrt(2 / pi)
-constexpr float kGeluA = 0.044715f;
-
-__device__ __forceinline__ float logistic(float a) { return __fdividef(1.0f, 1.0f + __expf(-a)); }
-
-template <int ACT>
-__device__ __forceinline__ float act_value(float z) {
-  if constexpr (ACT == SCAPE_ACT_RELU) return z > 0.0f ? z : (z != z ? z : 0.0f);
-  if constexpr (ACT == SCAPE_ACT_GELU)
-    return z * logistic(kGelu2C * z * (1.0f + kGeluA * z * z));
-  if constexpr (ACT == SCAPE_ACT_SILU) return z * logistic(z);
-  return z;
+// relative (not absolute) error where the result is small.  Two values at a
+// time: the multiplications and additions are packed 32-bit pairs, which halves
+// their issue slots; the exponential and the reciprocal (16 a clock an SM) are
+// then what bounds the arithmetic.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
 }
-// Past |z| = 20 the logistic is 0 or 1 to the last bit and its slope term is 0;
-// the clamp keeps 0 times an overflowed z^3 out.  A NaN comes back through p.
-template <int ACT>
-__device__ __forceinline__ float act_slope(float z) {
-  if constexpr (ACT == SCAPE_ACT_RELU) return z > 0.0f ? 1.0f : (z != z ? z : 0.0f);
+__device__ __forceinline__ void unpair(uint64_t r, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(r));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t both(float a) { return pair(a, a); }
+__device__ __forceinline__ float exp2_fast(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float reciprocal_fast(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// Limits that keep a NaN.
+__device__ __forceinline__ float at_least(float x, float lo) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float at_most(float x, float hi) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(hi));
+  return r;
+}
+
+constexpr double kLog2e = 1.4426950408889634074;
+constexpr double kGelu2C = 1.5957691216057307117;  // 2 sqrt(2 / pi)
+constexpr double kGeluA = 0.044715;
+__host__ __device__ constexpr float high(double x) { return (float)x; }
+__host__ __device__ constexpr float low(double x) { return (float)(x - (double)(float)x); }
+
+// The logistic function of silu's and gelu's argument a at z, by 2^e with
+// e = -a log2(e).  An error d in e is a relative error 0.69 d of the result where
+// that is small: at e = 100 the roundings of e alone are 2^-18 or so.  A bfloat16
+// result cannot show that; DEEP, for 32-bit results, carries e's roundings and
+// its constants' low parts along as d and corrects 2^e by 1 + d ln 2.
+template <int ACT, bool DEEP>
+__device__ __forceinline__ uint64_t logistic2(uint64_t z) {
+  constexpr double k0 = ACT == SCAPE_ACT_GELU ? -kGelu2C * kLog2e : -kLog2e;
+  constexpr double k1 = -kGelu2C * kGeluA * kLog2e;
+  uint64_t t = both(high(k0)), z2 = 0;
   if constexpr (ACT == SCAPE_ACT_GELU) {
-    const float p = logistic(kGelu2C * z * (1.0f + kGeluA * z * z));
-    const float c = fminf(fmaxf(z, -20.0f), 20.0f);
-    const float du = kGelu2C * (1.0f + 3.0f * kGeluA * c * c);
-    return p + c * du * p * (1.0f - p);
+    z2 = mul2(z, z);
+    t = fma2(z2, both(high(k1)), both(high(k0)));
   }
-  if constexpr (ACT == SCAPE_ACT_SILU) {
-    const float p = logistic(z);
-    const float c = fminf(fmaxf(z, -100.0f), 100.0f);
-    return p + c * p * (1.0f - p);
+  const uint64_t e = mul2(z, t);
+  float a, b;
+  unpair(e, a, b);
+  uint64_t x = pair(exp2_fast(a), exp2_fast(b));
+  if constexpr (DEEP) {
+    const uint64_t minus = both(-1.0f);
+    uint64_t t_low = both(low(k0));
+    if constexpr (ACT == SCAPE_ACT_GELU)
+      t_low = fma2(z2, both(low(k1)), add2(both(low(k0)), fma2(z2, both(high(k1)), fma2(t, minus, both(high(k0))))));
+    const uint64_t d = fma2(z, t_low, fma2(z, t, mul2(e, minus)));
+    float da, db;
+    unpair(mul2(d, both(0.69314718f)), da, db);
+    unpair(x, a, b);
+    // where e or z^2 has overflowed d says nothing, and 2^e is 0 or infinite
+    x = pair(a > 1e-37f && a < 1e37f ? fmaf(a, da, a) : a,
+             b > 1e-37f && b < 1e37f ? fmaf(b, db, b) : b);
   }
-  return 1.0f;
+  unpair(add2(x, both(1.0f)), a, b);
+  return pair(reciprocal_fast(a), reciprocal_fast(b));
 }
 
-// Runs f.template operator()<ACT>() for an activation known at run time.
+template <int ACT, bool DEEP = false>
+__device__ __forceinline__ void act_pair(float& x, float& y) {
+  if constexpr (ACT == SCAPE_ACT_RELU) {
+    x = at_least(x, 0.0f);
+    y = at_least(y, 0.0f);
+  } else if constexpr (ACT == SCAPE_ACT_GELU || ACT == SCAPE_ACT_SILU) {
+    const uint64_t z = pair(x, y);
+    unpair(mul2(z, logistic2<ACT, DEEP>(z)), x, y);
+  }
+}
+// x, y become the activation's slopes there.  Past |z| = 20 (gelu) and 100 (silu)
+// the logistic is 0 or 1 to the last bit and so is the slope; the limit keeps 0
+// times an overflowed z^2 out.
+template <int ACT>
+__device__ __forceinline__ void slope_pair(float& x, float& y) {
+  if constexpr (ACT == SCAPE_ACT_RELU) {
+    x = x > 0.0f ? 1.0f : (x != x ? x : 0.0f);
+    y = y > 0.0f ? 1.0f : (y != y ? y : 0.0f);
+  } else if constexpr (ACT == SCAPE_ACT_GELU || ACT == SCAPE_ACT_SILU) {
+    constexpr float kLim = ACT == SCAPE_ACT_GELU ? 20.0f : 100.0f;
+    const uint64_t z = pair(at_most(at_least(x, -kLim), kLim), at_most(at_least(y, -kLim), kLim));
+    const uint64_t p = logistic2<ACT, false>(z);
+    uint64_t m = z;  // z da/dz
+    if constexpr (ACT == SCAPE_ACT_GELU)
+      m = mul2(z, fma2(mul2(z, z), both(high(3.0 * kGelu2C * kGeluA)), both(high(kGelu2C))));
+    const uint64_t pq = fma2(mul2(p, both(-1.0f)), p, p);  // p (1 - p)
+    unpair(fma2(m, pq, p), x, y);
+  } else {
+    x = y = 1.0f;
+  }
+}
+template <int ACT, bool DEEP = false, int N>
+__device__ __forceinline__ void act_values(float (&v)[N]) {
+  if constexpr (N == 1) {
+    float other = 0.0f;
+    act_pair<ACT, DEEP>(v[0], other);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) act_pair<ACT, DEEP>(v[2 * i], v[2 * i + 1]);
+  }
+}
+template <int ACT, int N>
+__device__ __forceinline__ void act_slopes(float (&v)[N]) {
+  if constexpr (N == 1) {
+    float other = 0.0f;
+    slope_pair<ACT>(v[0], other);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) slope_pair<ACT>(v[2 * i], v[2 * i + 1]);
+  }
+}
+
+// CALL with ACT a constant, for an activation known at run time.
 #define SCAPE_ACT_SWITCH(act, CALL)                              \
   switch (act) {                                                 \
     case SCAPE_ACT_RELU: { constexpr int ACT = SCAPE_ACT_RELU; CALL; break; } \
