@@ -56,16 +56,18 @@ __global__ __launch_bounds__(kThreads) void pack8_kernel(const T* x, int64_t ldx
                                                          int64_t blocks_per_row) {
   const uint32_t first = blockIdx.x * (kThreads * kUnroll) + threadIdx.x;
   Unit un[kUnroll];
-  float v[kUnroll][VEC];
+  Raw<T, VEC> raw[kUnroll];
 #pragma unroll
   for (int i = 0; i < kUnroll; ++i) {
     un[i] = unit_at<VEC>(first + i * kThreads, units, per_row, cols);
-    load_part<VEC>(x + un[i].row * ldx + un[i].col, un[i].n, v[i]);
+    raw[i] = load_raw<VEC>(x + un[i].row * ldx + un[i].col, un[i].n);
   }
 #pragma unroll
   for (int i = 0; i < kUnroll; ++i) {
     const Unit& u = un[i];
-    warp_pack<VEC>(v[i], u.n, q + u.row * ldq + u.col,
+    float v[VEC];
+    to_floats(raw[i], v);
+    warp_pack<VEC>(v, u.n, q + u.row * ldq + u.col,
                    scale + u.row * blocks_per_row + u.col / kBlock,
                    u.n > 0 && u.col % kBlock == 0);
   }
@@ -138,20 +140,21 @@ __global__ __launch_bounds__(kThreads) void act_grad_kernel(
   const uint32_t first = blockIdx.x * (kThreads * kUnroll) + threadIdx.x;
   Unit un[kUnroll];
   Packed<VEC> p[kUnroll];
-  float g[kUnroll][VEC];
+  Raw<T, VEC> raw[kUnroll];
 #pragma unroll
   for (int i = 0; i < kUnroll; ++i) {
     un[i] = unit_at<VEC>(first + i * kThreads, units, per_row, cols);
     p[i] = load_packed<VEC>(q, ldq, scale, blocks_per_row, un[i]);
-    load_part<VEC>(dy + un[i].row * lddy + un[i].col, un[i].n, g[i]);
+    raw[i] = load_raw<VEC>(dy + un[i].row * lddy + un[i].col, un[i].n);
   }
 #pragma unroll
   for (int i = 0; i < kUnroll; ++i) {
-    float v[VEC];
+    float v[VEC], g[VEC];
     values_of<VEC>(p[i], v);
     act_slopes<ACT>(v);
+    to_floats(raw[i], g);
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) v[j] *= g[i][j];
+    for (int j = 0; j < VEC; ++j) v[j] *= g[j];
     store_part<VEC>(dz + un[i].row * lddz + un[i].col, un[i].n, v);
   }
 }

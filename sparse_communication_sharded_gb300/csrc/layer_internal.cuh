@@ -32,33 +32,55 @@ inline bool rows8(const void* p, int64_t ld) {
 }
 
 // ------------------------------------------------------------------ loads and stores
-// VEC consecutive elements as floats.  VEC 8 needs 16-byte alignment (one load
-// of bfloat16, two of float32); VEC 1 any.
-template <int VEC>
-__device__ __forceinline__ void load_vec(const bf16* p, float (&v)[VEC]) {
-  if constexpr (VEC == 8) {
-    const uint4 u = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+// VEC consecutive elements as they lie in memory.  Loads fill these and nothing
+// else, so that a thread has all its loads in flight before it converts the
+// first: a conversion between two loads would wait for the one before it.
+// VEC 8 needs 16-byte alignment, VEC 1 none.
+template <typename T, int VEC>
+struct Raw {
+  static constexpr int kWords = VEC * sizeof(T) >= 4 ? VEC * sizeof(T) / 4 : 1;
+  uint32_t w[kWords];
+};
+template <int VEC, typename T>
+__device__ __forceinline__ Raw<T, VEC> load_raw(const T* p, int n) {
+  Raw<T, VEC> r;
+  if (n >= VEC) {
+    if constexpr (VEC == 8) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = __uint_as_float(w[i] << 16);
-      v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+      for (int i = 0; i < Raw<T, VEC>::kWords / 4; ++i) {
+        const uint4 u = reinterpret_cast<const uint4*>(p)[i];
+        r.w[4 * i] = u.x, r.w[4 * i + 1] = u.y, r.w[4 * i + 2] = u.z, r.w[4 * i + 3] = u.w;
+      }
+    } else if constexpr (sizeof(T) == 2) {
+      r.w[0] = *reinterpret_cast<const uint16_t*>(p);
+    } else {
+      r.w[0] = *reinterpret_cast<const uint32_t*>(p);
     }
   } else {
+    // a row's end: the first n elements, zeros after
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) v[i] = __bfloat162float(p[i]);
+    for (int i = 0; i < Raw<T, VEC>::kWords; ++i) r.w[i] = 0;
+    if (VEC > 1 && n > 0) {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i)
+        if (i < n) {
+          if constexpr (sizeof(T) == 2)
+            r.w[i / 2] |= (uint32_t) reinterpret_cast<const uint16_t*>(p)[i] << (16 * (i % 2));
+          else
+            r.w[i] = reinterpret_cast<const uint32_t*>(p)[i];
+        }
+    }
   }
+  return r;
 }
-template <int VEC>
-__device__ __forceinline__ void load_vec(const float* p, float (&v)[VEC]) {
-  if constexpr (VEC == 8) {
-    const float4 a = reinterpret_cast<const float4*>(p)[0];
-    const float4 b = reinterpret_cast<const float4*>(p)[1];
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-    v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-  } else {
+template <typename T, int VEC>
+__device__ __forceinline__ void to_floats(const Raw<T, VEC>& r, float (&v)[VEC]) {
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) v[i] = p[i];
+  for (int i = 0; i < VEC; ++i) {
+    if constexpr (sizeof(T) == 2)
+      v[i] = __uint_as_float(i % 2 ? r.w[i / 2] & 0xFFFF0000u : r.w[i / 2] << 16);
+    else
+      v[i] = __uint_as_float(r.w[i]);
   }
 }
 
@@ -89,16 +111,7 @@ __device__ __forceinline__ void store_vec(float* p, const float (&v)[VEC]) {
   }
 }
 
-// The first n (0..VEC) elements of a vector at a row's end; the rest read as 0.
-template <int VEC, typename T>
-__device__ __forceinline__ void load_part(const T* p, int n, float (&v)[VEC]) {
-  if (n >= VEC) {
-    load_vec<VEC>(p, v);
-  } else {
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) v[i] = i < n ? (float)p[i] : 0.0f;
-  }
-}
+// The first n (0..VEC) elements of a vector at a row's end.
 template <int VEC, typename T>
 __device__ __forceinline__ void store_part(T* p, int n, const float (&v)[VEC]) {
   if (n >= VEC) {
@@ -109,22 +122,23 @@ __device__ __forceinline__ void store_part(T* p, int n, const float (&v)[VEC]) {
       if (i < n) p[i] = (T)v[i];
   }
 }
-// A weight vector of either type (the type is the same for the whole grid).
+// Part of a weight vector of either type (the same for the whole grid), which
+// may lie at any element of a flat parameter vector (aligned: on 16 bytes).
 template <int VEC>
-__device__ __forceinline__ void load_weight(const void* w, int is_bf16, bool vec_ok, int64_t c,
+__device__ __forceinline__ void load_weight(const void* w, int is_bf16, bool aligned, int64_t c,
                                             int n, float (&v)[VEC]) {
   if (is_bf16) {
     const bf16* p = static_cast<const bf16*>(w) + c;
-    if (VEC == 1 || vec_ok) {
-      load_part<VEC>(p, n, v);
+    if (VEC == 1 || aligned) {
+      to_floats<bf16, VEC>(load_raw<VEC>(p, n), v);
     } else {
 #pragma unroll
       for (int i = 0; i < VEC; ++i) v[i] = i < n ? __bfloat162float(p[i]) : 0.0f;
     }
   } else {
     const float* p = static_cast<const float*>(w) + c;
-    if (VEC == 1 || vec_ok) {
-      load_part<VEC>(p, n, v);
+    if (VEC == 1 || aligned) {
+      to_floats<float, VEC>(load_raw<VEC>(p, n), v);
     } else {
 #pragma unroll
       for (int i = 0; i < VEC; ++i) v[i] = i < n ? p[i] : 0.0f;

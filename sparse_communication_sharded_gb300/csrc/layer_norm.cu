@@ -56,20 +56,22 @@ __global__ __launch_bounds__(WARP ? 32 * kWarpRows : 512) void norm_fwd_kernel(N
   }
   int flip = 0;
   for (int64_t row = first; row < a.rows; row += step) {
-    float v[NV][VEC];
+    Raw<T, VEC> rx[NV], rr[NV];
     const T* x = static_cast<const T*>(a.x) + row * a.ldx;
+    const T* res = static_cast<const T*>(a.res) + row * a.ldres;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = vec_col<VEC>(i, t, width);
-      load_part<VEC>(x + c, a.cols - c, v[i]);
+      rx[i] = load_raw<VEC>(x + c, a.cols - c);
+      rr[i] = load_raw<VEC>(res + c, a.res ? a.cols - c : 0);
     }
-    if (a.res) {
-      const T* res = static_cast<const T*>(a.res) + row * a.ldres;
+    float v[NV][VEC];
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int c = vec_col<VEC>(i, t, width);
+    for (int i = 0; i < NV; ++i) {
+      to_floats(rx[i], v[i]);
+      if (a.res) {
         float r[VEC];
-        load_part<VEC>(res + c, a.cols - c, r);
+        to_floats(rr[i], r);
 #pragma unroll
         for (int j = 0; j < VEC; ++j) v[i][j] += r[j];
       }
@@ -150,20 +152,25 @@ __global__ __launch_bounds__(WARP ? 32 * kWarpRows : 512) void norm_bwd_kernel(N
     for (int j = 0; j < VEC; ++j) acc[i][j] = 0.0f;
   int flip = 0;
   for (int64_t row = first; row < a.rows; row += step) {
-    float g[NV][VEC], n[NV][VEC];
     const float rstd = a.rstd[row];
     const T* dy = static_cast<const T*>(a.dy) + row * a.lddy;
     const T* h = static_cast<const T*>(a.h) + row * a.ldh;
+    const T* dh = static_cast<const T*>(a.dh) + row * a.lddh;
+    Raw<T, VEC> rg[NV], rn[NV], rd[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = vec_col<VEC>(i, t, width);
-      load_part<VEC>(dy + c, a.cols - c, g[i]);
-      load_part<VEC>(h + c, a.cols - c, n[i]);
+      rg[i] = load_raw<VEC>(dy + c, a.cols - c);
+      rn[i] = load_raw<VEC>(h + c, a.cols - c);
+      rd[i] = load_raw<VEC>(dh + c, a.dh ? a.cols - c : 0);
     }
+    float g[NV][VEC], n[NV][VEC];
     float s = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = vec_col<VEC>(i, t, width);
+      to_floats(rg[i], g[i]);
+      to_floats(rn[i], n[i]);
       float w[VEC];
       load_weight<VEC>(a.w, a.w_bf16, w_vec, c, min(max(a.cols - c, 0), VEC), w);
 #pragma unroll
@@ -184,7 +191,7 @@ __global__ __launch_bounds__(WARP ? 32 * kWarpRows : 512) void norm_bwd_kernel(N
       for (int j = 0; j < VEC; ++j) g[i][j] = rstd * (g[i][j] - n[i][j] * mean);
       if (a.dh) {
         float d[VEC];
-        load_part<VEC>(static_cast<const T*>(a.dh) + row * a.lddh + c, a.cols - c, d);
+        to_floats(rd[i], d);
 #pragma unroll
         for (int j = 0; j < VEC; ++j) g[i][j] += d[j];
       }
