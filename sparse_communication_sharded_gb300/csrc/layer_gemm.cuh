@@ -242,9 +242,11 @@ __device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, uint32_t rank) {
 __device__ __forceinline__ void cluster_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-__device__ __forceinline__ float cluster_load(uint32_t addr, uint32_t rank) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr(addr, rank)) : "memory");
+__device__ __forceinline__ float4 cluster_load(uint32_t addr, uint32_t rank) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(cluster_addr(addr, rank)));
   return v;
 }
 
@@ -252,39 +254,47 @@ __device__ __forceinline__ float cluster_load(uint32_t addr, uint32_t rank) {
 constexpr int kBM = 128;  // rows of a block's tile: the tensor core's 128 accumulator lanes
 constexpr int kBK = 64;   // contraction a stage: one 128-byte swizzled row of bfloat16
 constexpr int kChunk = 8192;       // bytes of 64 staged rows of 128 bytes
-constexpr int kGemmThreads = 384;  // TMA, MMA, TMEM, one idle warp; 8 epilogue warps
-constexpr int kEpilogueWarps = 8;
 constexpr int kBoxBytes = 2048;    // 32 x 32 bfloat16 on their way out
+constexpr int kTileCost = 16;      // what a tile costs besides its columns, in columns
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 
 // How a product is laid over the blocks.
 enum GemmMode {
   // One tile a cluster of 1 to 8 blocks, the contraction cut over them.
   kModeSplit = 0,
-  // Persistent pairs of blocks on neighbouring SMs: the pair's 256 x BN tile is
+  // Persistent pairs of blocks on neighbouring SMs: the pair's 256-row tile is
   // one tensor-core instruction stream, each block holding half of either
   // operand, so a byte read feeds twice the work it does in a single block.
+  // The tile's width is chosen at run time (a multiple of 32 up to BN = 256).
   kModePair = 1
 };
 
-template <int BN, int MODE>
+template <int KIND, int BN, int MODE>
 struct Tile {
   static constexpr bool kPair = MODE == kModePair;
-  static constexpr int kBRows = kPair ? BN / 2 : BN;  // operand B rows a block stages
+  // The epilogue of a pair has a tile's multiplication time (8192 clocks for a
+  // contraction of 1024) to turn 128 x 256 accumulators into output.  With
+  // activations to compute, 8 warps (2 a scheduler) kept 30% of the issue slots
+  // busy and took twice that; 16 warps overlap their latencies.
+  static constexpr int kEpilogueWarps = kPair && KIND != kGemmWeightGrad ? 16 : 8;
+  static constexpr int kThreads = 128 + 32 * kEpilogueWarps;  // + TMA, MMA, TMEM, an idle warp
+  static constexpr int kGroups = kEpilogueWarps / 4;  // warps that share a quarter of the rows
+  static constexpr int kWarpChunks = BN / 32 / kGroups;       // 32-column chunks a warp, at most
+  static constexpr int kBRows = kPair ? BN / 2 : BN;  // operand B rows a block stages, at most
   static constexpr int kABytes = kBM * kBK * 2;
   static constexpr int kBBytes = kBRows * kBK * 2;
   static constexpr int kStageBytes = kABytes + kBBytes;
   // as many stages as fit beside the output boxes and the bias
-  static constexpr int kStages = kStageBytes > 24576 ? 5 : kStageBytes > 16384 ? 6 : 8;
+  static constexpr int kStages = kStageBytes > 24576 ? (kEpilogueWarps == 16 ? 4 : 5) : 6;
   static constexpr int kColumns = 2 * BN;  // two accumulators
-  static constexpr int kWarpCols = BN / 2;  // columns an epilogue warp handles
   static constexpr int kBoxAt = kStages * kStageBytes;
-  static constexpr int kBiasAt = kBoxAt + kEpilogueWarps * 2 * kBoxBytes;
-  static constexpr int kSmem = kBiasAt + kEpilogueWarps * kWarpCols * 4 + 1024;
-  // column stride of the partial tile that split products exchange: odd, and 8
-  // columns apart fall 8 banks apart
-  static constexpr int kPartialLd = kBM + 1;
-  static_assert(kPair || kPartialLd * BN * 4 <= kStages * kStageBytes, "partial tile fits");
+  static constexpr int kBiasAt = kBoxAt + (kPair ? kEpilogueWarps * 2 * kBoxBytes : 0);
+  static constexpr int kSmem =
+      kBiasAt + (kPair ? kEpilogueWarps * kWarpChunks * 128 : 0) + 1024;
+  // row stride of the partial tile that split products exchange: 16-byte
+  // accesses of 8 neighbouring rows fall on different banks
+  static constexpr int kPartialLd = BN + 4;
+  static_assert(kPair || kPartialLd * kBM * 4 <= kStages * kStageBytes, "partial tile fits");
   static_assert(kSmem <= 232448, "shared memory of a block");
   static_assert(kBRows % 64 == 0, "transposed operands are staged 64 rows at a time");
 };
@@ -300,12 +310,12 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, bool transposed) {
   d |= (uint64_t)2 << 61;  // 128-byte swizzle
   return d;
 }
-template <int ROWS, int BN, bool TA, bool TB>
-__device__ __forceinline__ constexpr uint32_t instr_desc() {
+template <int ROWS, bool TA, bool TB>
+__device__ __forceinline__ uint32_t instr_desc(int bn) {
   return (1u << 4)            // 32-bit float accumulator
          | (1u << 7)          // A bfloat16
          | (1u << 10)         // B bfloat16
-         | ((TA ? 1u : 0u) << 15) | ((TB ? 1u : 0u) << 16) | ((uint32_t)(BN >> 3) << 17) |
+         | ((TA ? 1u : 0u) << 15) | ((TB ? 1u : 0u) << 16) | ((uint32_t)(bn >> 3) << 17) |
          ((uint32_t)(ROWS >> 4) << 24);
 }
 
@@ -433,6 +443,19 @@ __device__ __forceinline__ void load_beside(Beside<KIND, N>& b, bool live, int64
   }
 }
 
+// v *= act'(z), four z at a time from their 8-bit words.
+template <int ACT, int N, int W>
+__device__ __forceinline__ void times_slopes(float (&v)[N], const uint32_t (&w)[W], float scale) {
+#pragma unroll
+  for (int i = 0; i < N / 4; ++i) {
+    float z[4];
+    from_e4m3(w[i], scale, z);
+    act_slopes<ACT>(z);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[4 * i + j] *= z[j];
+  }
+}
+
 // The accumulators become the values to store; the 8-bit form is stored here.
 // All 32 lanes call it.
 template <int KIND, int N>
@@ -450,13 +473,7 @@ __device__ __forceinline__ void epilogue_math(float (&v)[N], const Beside<KIND, 
     }
   } else if constexpr (KIND == kGemmInputGrad) {
     if (e.act != SCAPE_ACT_NONE && live && left > 0) {
-      const float s = scale_value(b.code);
-      float z[N];
-#pragma unroll
-      for (int i = 0; i < N / 4; ++i) from_e4m3(b.w[i], s, z + 4 * i);
-      SCAPE_ACT_SWITCH(e.act, act_slopes<ACT>(z));
-#pragma unroll
-      for (int i = 0; i < N; ++i) v[i] *= z[i];
+      SCAPE_ACT_SWITCH(e.act, times_slopes<ACT>(v, b.w, scale_value(b.code)));
     }
   }
 }
@@ -529,16 +546,17 @@ __device__ __forceinline__ void store_box(const float (&v)[32], uint32_t box, in
 // ------------------------------------------------------------------ the kernel
 struct GemmShape {
   int m, n;
+  int bn;  // columns of a tile
   int tiles_m, tiles_n, ksteps;
   unsigned int* status;
 };
 
 template <int KIND, int BN, int MODE>
-__global__ __launch_bounds__(kGemmThreads, 1) void gemm_kernel(
+__global__ __launch_bounds__(Tile<KIND, BN, MODE>::kThreads, 1) void gemm_kernel(
     const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
     const __grid_constant__ CUtensorMap map_out, const GemmShape s,
     const __grid_constant__ Epilogue e) {
-  using TL = Tile<BN, MODE>;
+  using TL = Tile<KIND, BN, MODE>;
   constexpr bool PAIR = MODE == kModePair;
   constexpr bool TA = KIND == kGemmWeightGrad;
   constexpr bool TB = KIND != kGemmForward;
@@ -564,7 +582,7 @@ __global__ __launch_bounds__(kGemmThreads, 1) void gemm_kernel(
   if (threadIdx.x == 0) {
     for (int i = 0; i < TL::kStages; ++i) mbar_init(full(i), 1), mbar_init(empty(i), 1);
     for (int i = 0; i < 2; ++i)
-      mbar_init(acc_full(i), 1), mbar_init(acc_empty(i), kEpilogueWarps * (PAIR ? 2 : 1));
+      mbar_init(acc_full(i), 1), mbar_init(acc_empty(i), TL::kEpilogueWarps * (PAIR ? 2 : 1));
     mbar_init(drain, 1);
     gave_up = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -594,6 +612,8 @@ __global__ __launch_bounds__(kGemmThreads, 1) void gemm_kernel(
     }
   };
 
+  const int bn = PAIR ? s.bn : BN;
+  const int b_rows = PAIR ? bn / 2 : BN;  // operand B rows this block stages
   const int tiles = s.tiles_m * s.tiles_n;
   const int first = blockIdx.x / ranks;
   const int step = PAIR ? gridDim.x / 2 : tiles;
@@ -613,6 +633,8 @@ __global__ __launch_bounds__(kGemmThreads, 1) void gemm_kernel(
   if (warp == 0 && lane == 0) {
     // ---------------- producer: this block's rows of A and of B.  In a pair both
     // blocks' copies count on the first block's barrier, which expects them all.
+    const int b_boxes = TB ? (b_rows + 63) / 64 : 1;
+    const uint32_t bytes = TL::kABytes + (TB ? b_boxes * kChunk : b_rows * kBK * 2);
     const uint32_t lead = PAIR ? cluster_addr(bar0, 0) - bar0 : 0;
     int stage = 0, phase = 0;
     int64_t issued = 0;
@@ -621,13 +643,13 @@ __global__ __launch_bounds__(kGemmThreads, 1) void gemm_kernel(
       int tm, tn;
       tile_at(t, tm, tn);
       const int row_a = tm * kTileRows + (PAIR ? rank * kBM : 0);
-      const int row_b = tn * BN + (PAIR ? rank * TL::kBRows : 0);
+      const int row_b = tn * bn + (PAIR ? rank * b_rows : 0);
       for (int k = k0; k < k1; ++k) {
         ok = wait(empty(stage), phase ^ 1);
         if (!ok) break;
         const uint32_t a = smem + stage * TL::kStageBytes, b = a + TL::kABytes;
         const uint32_t bar = full(stage) + lead;
-        if (!PAIR || rank == 0) mbar_expect_tx(full(stage), TL::kStageBytes * (PAIR ? 2 : 1));
+        if (!PAIR || rank == 0) mbar_expect_tx(full(stage), bytes * (PAIR ? 2 : 1));
         if constexpr (TA) {
 #pragma unroll
           for (int i = 0; i < kBM / 64; ++i)
@@ -636,8 +658,7 @@ __global__ __launch_bounds__(kGemmThreads, 1) void gemm_kernel(
           tma_load<PAIR>(a, &map_a, k * kBK, row_a, bar);
         }
         if constexpr (TB) {
-#pragma unroll
-          for (int i = 0; i < TL::kBRows / 64; ++i)
+          for (int i = 0; i < b_boxes; ++i)
             tma_load<PAIR>(b + i * kChunk, &map_b, row_b + i * 64, k * kBK, bar);
         } else {
           tma_load<PAIR>(b, &map_b, k * kBK, row_b, bar);
@@ -662,7 +683,7 @@ __global__ __launch_bounds__(kGemmThreads, 1) void gemm_kernel(
     }
   } else if (warp == 1 && lane == 0 && (!PAIR || rank == 0)) {
     // ---------------- tensor core
-    constexpr uint32_t idesc = instr_desc<kTileRows, BN, TA, TB>();
+    const uint32_t idesc = instr_desc<kTileRows, TA, TB>(bn);
     int stage = 0, phase = 0, acc = 0, acc_phase = 0;
     bool ok = true;
     for (int t = first; ok && t < tiles; t += step) {
@@ -696,11 +717,11 @@ __global__ __launch_bounds__(kGemmThreads, 1) void gemm_kernel(
         if (now_ns() - t0 > kWaitLimitNs) break;
     }
   } else if (warp >= 4) {
-    // ---------------- epilogue: warp w reads the accumulator lanes of its quarter,
-    // the two warps of a quarter take half of the columns each
-    const int quarter = warp & 3, half = (warp - 4) >> 2;
+    // ---------------- epilogue: warp w reads the accumulator lanes of its quarter;
+    // the warps of a quarter take 32-column chunks in turn
+    const int quarter = warp & 3, group = (warp - 4) >> 2;
     const uint32_t box = smem + TL::kBoxAt + (warp - 4) * 2 * kBoxBytes;
-    const uint32_t bias_at = smem + TL::kBiasAt + (warp - 4) * TL::kWarpCols * 4;
+    const uint32_t bias_at = smem + TL::kBiasAt + (warp - 4) * TL::kWarpChunks * 128;
     const bool through_box = KIND != kGemmWeightGrad || !e.out_f32;
     int acc = 0, acc_phase = 0, boxes = 0, bias_tile = -1;
     for (int t = first; t < tiles; t += step) {
@@ -709,7 +730,7 @@ __global__ __launch_bounds__(kGemmThreads, 1) void gemm_kernel(
       const int64_t row0 = (int64_t)tm * kTileRows + (PAIR ? rank * kBM : 0) + quarter * 32;
       const int64_t row = row0 + lane;
       const bool live = row < s.m;
-      const int col0 = tn * BN + half * TL::kWarpCols;
+      const int col0 = tn * bn + group * 32;
       Beside<KIND, 32> next;
       if constexpr (PAIR) {
         // before the accumulator is ready: this tile's bias, the first chunk's
@@ -718,34 +739,39 @@ __global__ __launch_bounds__(kGemmThreads, 1) void gemm_kernel(
           bias_tile = tn;
           __syncwarp();
 #pragma unroll
-          for (int i = lane; i < TL::kWarpCols; i += 32)
-            asm volatile("st.shared::cta.f32 [%0], %1;" ::"r"(bias_at + 4 * i),
-                         "f"(col0 + i < s.n ? __bfloat162float(e.bias[col0 + i]) : 0.0f)
+          for (int j = 0; j < TL::kWarpChunks; ++j) {
+            const int c = col0 + j * TL::kGroups * 32 + lane;
+            asm volatile("st.shared::cta.f32 [%0], %1;" ::"r"(bias_at + j * 128 + lane * 4),
+                         "f"(c < s.n ? __bfloat162float(e.bias[c]) : 0.0f)
                          : "memory");
+          }
           __syncwarp();
         }
-        load_beside<KIND, 32>(next, live, row, col0, s.n - col0, e);
+        load_beside<KIND, 32>(next, live, row, col0, group * 32 < bn ? s.n - col0 : 0, e);
       }
       if (!__all_sync(0xFFFFFFFFu, wait(acc_full(acc), acc_phase))) break;
       tc_fence_after();
-      const uint32_t lanes = tmem + acc * BN + ((uint32_t)(quarter * 32) << 16) + half * TL::kWarpCols;
+      const uint32_t lanes = tmem + acc * BN + ((uint32_t)(quarter * 32) << 16) + group * 32;
 #pragma unroll 1
-      for (int c = 0; c < TL::kWarpCols; c += 32) {
+      for (int j = 0; j < TL::kWarpChunks; ++j) {
+        const int c = j * TL::kGroups * 32;  // from this warp's first column
+        if (group * 32 + c >= bn) break;
         uint32_t r[32];
         tmem_ld32(lanes + c, r);
         if constexpr (!PAIR) {
           tmem_ld_wait();
-          const uint32_t p = smem + 4 * (quarter * 32 + lane);
+          const uint32_t p = smem + 4 * (TL::kPartialLd * (quarter * 32 + lane) + group * 32 + c);
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            asm volatile("st.shared::cta.b32 [%0], %1;" ::"r"(
-                             p + 4 * TL::kPartialLd * (half * TL::kWarpCols + c + i)),
-                         "r"(r[i])
+          for (int i = 0; i < 8; ++i)
+            asm volatile("st.shared::cta.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(p + 16 * i),
+                         "r"(r[4 * i]), "r"(r[4 * i + 1]), "r"(r[4 * i + 2]), "r"(r[4 * i + 3])
                          : "memory");
         } else {
           const int c0 = col0 + c, left = s.n - c0;
           const Beside<KIND, 32> beside = next;
-          if (c + 32 < TL::kWarpCols) load_beside<KIND, 32>(next, live, row, c0 + 32, left - 32, e);
+          if (j + 1 < TL::kWarpChunks && group * 32 + c + TL::kGroups * 32 < bn)
+            load_beside<KIND, 32>(next, live, row, c0 + TL::kGroups * 32,
+                                  left - TL::kGroups * 32, e);
           tmem_ld_wait();
           if (left > 0) {
             float v[32];
@@ -755,7 +781,7 @@ __global__ __launch_bounds__(kGemmThreads, 1) void gemm_kernel(
                 float b0, b1, b2, b3;
                 asm volatile("ld.shared::cta.v4.f32 {%0, %1, %2, %3}, [%4];"
                              : "=f"(b0), "=f"(b1), "=f"(b2), "=f"(b3)
-                             : "r"(bias_at + 4 * c + 16 * i)
+                             : "r"(bias_at + j * 128 + 16 * i)
                              : "memory");
                 unpair(add2(pair(__uint_as_float(r[4 * i]), __uint_as_float(r[4 * i + 1])), pair(b0, b1)),
                        v[4 * i], v[4 * i + 1]);
@@ -769,7 +795,7 @@ __global__ __launch_bounds__(kGemmThreads, 1) void gemm_kernel(
             epilogue_math<KIND, 32>(v, beside, live, row, c0, left, e);
             if (through_box) {
               if (e.out_vec) {
-                // the box two chunks ago has been read
+                // the box two stores ago has been read
                 if (lane == 0) tma_store_wait_read<1>();
               }
               __syncwarp();
@@ -809,7 +835,7 @@ __global__ __launch_bounds__(kGemmThreads, 1) void gemm_kernel(
       tile_at(first, tm, tn);
       const int rows = kBM / ranks;
       const int groups = rows / 8 * (BN / 32);
-      for (int g = warp - 4; g < groups; g += kEpilogueWarps) {
+      for (int g = warp - 4; g < groups; g += TL::kEpilogueWarps) {
         const int r = rank * rows + g % (rows / 8) * 8 + (lane & 7);
         const int c = g / (rows / 8) * 32 + (lane >> 3) * 8;
         const int64_t row = (int64_t)tm * kBM + r;
@@ -824,10 +850,24 @@ __global__ __launch_bounds__(kGemmThreads, 1) void gemm_kernel(
         float sum[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) sum[i] = 0.0f;
-        for (uint32_t q = 0; q < ranks; ++q)
+        const uint32_t at = smem + 4 * (TL::kPartialLd * r + c);
+        // four blocks' parts at a time in flight
+        for (uint32_t q = 0; q < ranks; q += 4) {
+          float4 part[4][2];
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            sum[i] += cluster_load(smem + 4 * (TL::kPartialLd * (c + i) + r), q);
+          for (uint32_t i = 0; i < 4; ++i)
+            if (q + i < ranks) {
+              part[i][0] = cluster_load(at, q + i);
+              part[i][1] = cluster_load(at + 16, q + i);
+            }
+#pragma unroll
+          for (uint32_t i = 0; i < 4; ++i)
+            if (q + i < ranks) {
+              sum[0] += part[i][0].x, sum[1] += part[i][0].y, sum[2] += part[i][0].z;
+              sum[3] += part[i][0].w, sum[4] += part[i][1].x, sum[5] += part[i][1].y;
+              sum[6] += part[i][1].z, sum[7] += part[i][1].w;
+            }
+        }
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] += sum[i];
         epilogue_math<KIND, 8>(v, beside, live, row, c0, left, e);
@@ -847,8 +887,8 @@ __global__ __launch_bounds__(kGemmThreads, 1) void gemm_kernel(
 
 // ------------------------------------------------------------------ launch
 template <int KIND, int BN, int MODE>
-cudaError_t gemm_launch(const GemmCall& c, int split, cudaStream_t st) {
-  using TL = Tile<BN, MODE>;
+cudaError_t gemm_launch(const GemmCall& c, int bn, int split, cudaStream_t st) {
+  using TL = Tile<KIND, BN, MODE>;
   constexpr bool PAIR = MODE == kModePair;
   constexpr bool TA = KIND == kGemmWeightGrad;
   constexpr bool TB = KIND != kGemmForward;
@@ -857,7 +897,7 @@ cudaError_t gemm_launch(const GemmCall& c, int split, cudaStream_t st) {
                        : gemm_tensor_map(&ma, c.a.p, c.m, c.k, c.a.ld, kBM, kBK);
   if (err == cudaSuccess)
     err = TB ? gemm_tensor_map(&mb, c.b.p, c.k, c.n, c.b.ld, kBK, kBK)
-             : gemm_tensor_map(&mb, c.b.p, c.n, c.k, c.b.ld, TL::kBRows, kBK);
+             : gemm_tensor_map(&mb, c.b.p, c.n, c.k, c.b.ld, PAIR ? bn / 2 : bn, kBK);
   if (PAIR && c.e.out_vec && !c.e.out_f32) {
     if (err == cudaSuccess) err = gemm_tensor_map(&mo, c.e.out, c.m, c.n, c.e.ldo, 32, 32);
   } else {
@@ -866,8 +906,9 @@ cudaError_t gemm_launch(const GemmCall& c, int split, cudaStream_t st) {
   GemmShape s;
   s.m = (int)c.m;
   s.n = (int)c.n;
+  s.bn = bn;
   s.tiles_m = (int)ceil_div(c.m, PAIR ? 2 * kBM : kBM);
-  s.tiles_n = (int)ceil_div(c.n, BN);
+  s.tiles_n = (int)ceil_div(c.n, bn);
   s.ksteps = (int)ceil_div(c.k, kBK);
   if (err == cudaSuccess) err = gemm_status_word(&s.status);
   auto kernel = gemm_kernel<KIND, BN, MODE>;
@@ -877,7 +918,7 @@ cudaError_t gemm_launch(const GemmCall& c, int split, cudaStream_t st) {
   const int cluster = PAIR ? 2 : split;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(PAIR ? 2 * std::min<int64_t>(tiles, sm_count() / 2) : tiles * split));
-  cfg.blockDim = dim3(kGemmThreads);
+  cfg.blockDim = dim3(TL::kThreads);
   cfg.dynamicSmemBytes = TL::kSmem;
   cfg.stream = st;
   cudaLaunchAttribute at[1];
@@ -889,23 +930,32 @@ cudaError_t gemm_launch(const GemmCall& c, int split, cudaStream_t st) {
   return cudaLaunchKernelEx(&cfg, kernel, ma, mb, mo, s, c.e);
 }
 
-// Tile and mode.  Pairs with wide tiles do the most work a byte read and keep
-// the tensor cores busy through the epilogue; they want tiles for most of the
-// SMs.  Below that, narrow tiles, each cut over a cluster as far as there are
-// SMs and at least four stages of the contraction for every block.
+// Tile and mode.  Pairs do the most work a byte read and keep the tensor cores
+// busy through the epilogue; they take whole tiles, so their time goes by the
+// number of tiles the busiest pair gets times a tile's width (plus what a tile
+// costs whatever its width), and the width is the one that makes it least.  They
+// want at least 3/4 of the SMs at work.  Below that, narrow tiles, each cut
+// over a cluster as far as there are SMs and at least four stages of the
+// contraction for every block.
 template <int KIND>
 cudaError_t gemm_run(const GemmCall& c, cudaStream_t st) {
-  const int64_t sms = sm_count();
+  const int64_t sms = sm_count(), pairs = sms / 2;
   const int64_t tp = ceil_div(c.m, 2 * kBM);
-  if (tp * ceil_div(c.n, 256) * 2 * 5 >= sms * 4) return gemm_launch<KIND, 256, kModePair>(c, 2, st);
-  if (tp * ceil_div(c.n, 128) * 2 * 5 >= sms * 4) return gemm_launch<KIND, 128, kModePair>(c, 2, st);
+  int best = 0;
+  int64_t least = 0;
+  for (int bn = 256; bn >= 128; bn -= 32) {
+    const int64_t tiles = tp * ceil_div(c.n, bn);
+    const int64_t cost = ceil_div(tiles, pairs) * (bn + kTileCost);
+    if (tiles * 4 >= pairs * 3 && (best == 0 || cost < least)) best = bn, least = cost;
+  }
+  if (best) return gemm_launch<KIND, 256, kModePair>(c, best, 2, st);
   const int64_t tm = ceil_div(c.m, kBM), ksteps = ceil_div(c.k, kBK);
   const int bn = tm * ceil_div(c.n, 64) <= sms ? 64 : 128;
   const int64_t tiles = tm * ceil_div(c.n, bn);
   int split = 1;
   while (split < 8 && tiles * split * 2 <= sms && ksteps / (split * 2) >= 4) split *= 2;
-  return bn == 64 ? gemm_launch<KIND, 64, kModeSplit>(c, split, st)
-                  : gemm_launch<KIND, 128, kModeSplit>(c, split, st);
+  return bn == 64 ? gemm_launch<KIND, 64, kModeSplit>(c, 64, split, st)
+                  : gemm_launch<KIND, 128, kModeSplit>(c, 128, split, st);
 }
 
 #endif  // __CUDACC__

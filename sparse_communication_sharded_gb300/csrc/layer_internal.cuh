@@ -174,10 +174,12 @@ __device__ __forceinline__ float nan_unless_finite(float x) {
 // the finite ones.
 template <int N>
 __device__ __forceinline__ uint32_t part_top(const float (&v)[N]) {
-  float t = 0.0f;
+  constexpr int kLanes = N >= 16 ? 4 : 1;  // chains that do not wait for each other
+  float t[kLanes] = {};
 #pragma unroll
-  for (int i = 0; i < N; ++i) t = fmaxf(t, fabsf(v[i]));
-  return __float_as_uint(t);
+  for (int i = 0; i < N; ++i) t[i % kLanes] = fmaxf(t[i % kLanes], fabsf(v[i]));
+  if constexpr (kLanes == 4) t[0] = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
+  return __float_as_uint(t[0]);
 }
 template <int N>
 __device__ __forceinline__ uint32_t part_top_finite(const float (&v)[N]) {
