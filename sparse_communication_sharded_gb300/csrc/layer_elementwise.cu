@@ -2,7 +2,7 @@
 // activation) and the gradient through an activation kept in 8 bits.
 //
 // Each is one streaming pass over rows x cols values: bound by memory.  A row is
-// cut into units of VEC columns, a thread takes kUnroll units that lie a block's
+// cut into units of VEC columns, a thread takes unroll() units that lie a block's
 // width apart, so that their loads are all in flight before the first is used.
 #include <algorithm>
 
@@ -13,7 +13,11 @@ namespace layer {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kUnroll = 4;
+// Units a thread: 32 columns, or 8 of single columns.
+template <int VEC>
+__host__ __device__ constexpr int unroll() {
+  return VEC == 16 ? 2 : VEC == 8 ? 4 : 8;
+}
 
 // n / d for n < 2^31 by a multiplication (Granlund and Montgomery, "Division by
 // invariant integers using multiplication", 1994).
@@ -54,16 +58,17 @@ __global__ __launch_bounds__(kThreads) void pack8_kernel(const T* x, int64_t ldx
                                                          FastDiv per_row, int64_t cols, uint8_t* q,
                                                          int64_t ldq, uint8_t* scale,
                                                          int64_t blocks_per_row) {
-  const uint32_t first = blockIdx.x * (kThreads * kUnroll) + threadIdx.x;
-  Unit un[kUnroll];
-  Raw<T, VEC> raw[kUnroll];
+  constexpr int U = unroll<VEC>();
+  const uint32_t first = blockIdx.x * (kThreads * U) + threadIdx.x;
+  Unit un[U];
+  Raw<T, VEC> raw[U];
 #pragma unroll
-  for (int i = 0; i < kUnroll; ++i) {
+  for (int i = 0; i < U; ++i) {
     un[i] = unit_at<VEC>(first + i * kThreads, units, per_row, cols);
     raw[i] = load_raw<VEC>(x + un[i].row * ldx + un[i].col, un[i].n);
   }
 #pragma unroll
-  for (int i = 0; i < kUnroll; ++i) {
+  for (int i = 0; i < U; ++i) {
     const Unit& u = un[i];
     float v[VEC];
     to_floats(raw[i], v);
@@ -76,7 +81,7 @@ __global__ __launch_bounds__(kThreads) void pack8_kernel(const T* x, int64_t ldx
 // The 8-bit values of a unit and their scale.
 template <int VEC>
 struct Packed {
-  uint32_t w[VEC == 8 ? 2 : 1];
+  uint32_t w[VEC >= 4 ? VEC / 4 : 1];
   uint32_t code;
 };
 template <int VEC>
@@ -86,28 +91,21 @@ __device__ __forceinline__ Packed<VEC> load_packed(const uint8_t* q, int64_t ldq
   Packed<VEC> p = {};
   if (u.n > 0) {
     const uint8_t* s = q + u.row * ldq + u.col;
-    if (VEC == 8 && u.n == 8) {
+    p.code = scale[u.row * blocks_per_row + u.col / kBlock];
+    if (VEC == 16 && u.n == 16) {
+      const uint4 a = *reinterpret_cast<const uint4*>(s);
+      p.w[0] = a.x, p.w[VEC == 16 ? 1 : 0] = a.y;
+      p.w[VEC == 16 ? 2 : 0] = a.z, p.w[VEC == 16 ? 3 : 0] = a.w;
+    } else if (VEC == 8 && u.n == 8) {
       const uint2 a = *reinterpret_cast<const uint2*>(s);
-      p.w[0] = a.x;
-      p.w[VEC == 8 ? 1 : 0] = a.y;
+      p.w[0] = a.x, p.w[VEC >= 8 ? 1 : 0] = a.y;
     } else {
 #pragma unroll
       for (int i = 0; i < VEC; ++i)
         if (i < u.n) p.w[i / 4] |= (uint32_t)s[i] << (8 * (i % 4));
     }
-    p.code = scale[u.row * blocks_per_row + u.col / kBlock];
   }
   return p;
-}
-template <int VEC>
-__device__ __forceinline__ void values_of(const Packed<VEC>& p, float (&v)[VEC]) {
-  const float s = scale_value(p.code);
-  if constexpr (VEC == 8) {
-    from_e4m3(p.w[0], s, v);
-    from_e4m3(p.w[1], s, v + 4);
-  } else {
-    v[0] = from_e4m3_byte(p.w[0], s);
-  }
 }
 
 template <typename T, int VEC, int ACT>
@@ -116,20 +114,35 @@ __global__ __launch_bounds__(kThreads) void unpack8_kernel(const uint8_t* q, int
                                                            int64_t blocks_per_row, uint32_t units,
                                                            FastDiv per_row, int64_t cols, T* y,
                                                            int64_t ldy) {
-  const uint32_t first = blockIdx.x * (kThreads * kUnroll) + threadIdx.x;
-  Unit un[kUnroll];
-  Packed<VEC> p[kUnroll];
+  constexpr int U = unroll<VEC>();
+  const uint32_t first = blockIdx.x * (kThreads * U) + threadIdx.x;
+  Unit un[U];
+  Packed<VEC> p[U];
 #pragma unroll
-  for (int i = 0; i < kUnroll; ++i) {
+  for (int i = 0; i < U; ++i) {
     un[i] = unit_at<VEC>(first + i * kThreads, units, per_row, cols);
     p[i] = load_packed<VEC>(q, ldq, scale, blocks_per_row, un[i]);
   }
 #pragma unroll
-  for (int i = 0; i < kUnroll; ++i) {
-    float v[VEC];
-    values_of<VEC>(p[i], v);
-    act_values<ACT, sizeof(T) == 4>(v);
-    store_part<VEC>(y + un[i].row * ldy + un[i].col, un[i].n, v);
+  for (int i = 0; i < U; ++i) {
+    const Activation<ACT> f(scale_value(p[i].code));
+    const Activation<SCAPE_ACT_NONE> scaled(scale_value(p[i].code));
+    float v[VEC < 4 ? 4 : VEC];
+#pragma unroll
+    for (int j = 0; j < (VEC < 4 ? 1 : VEC / 4); ++j) {
+      uint64_t lo, hi;
+      e4m3_pairs(p[i].w[j], lo, hi);
+      if constexpr (sizeof(T) == 4) {
+        unpair(scaled.value(lo), v[4 * j], v[4 * j + 1]);
+        unpair(scaled.value(hi), v[4 * j + 2], v[4 * j + 3]);
+#pragma unroll
+        for (int l = 0; l < (VEC < 4 ? VEC : 4); ++l) v[4 * j + l] = act_exact<ACT>(v[4 * j + l]);
+      } else {
+        unpair(f.value(lo), v[4 * j], v[4 * j + 1]);
+        unpair(f.value(hi), v[4 * j + 2], v[4 * j + 3]);
+      }
+    }
+    store_part<VEC>(y + un[i].row * ldy + un[i].col, un[i].n, reinterpret_cast<float (&)[VEC]>(v));
   }
 }
 
@@ -137,38 +150,50 @@ template <typename T, int VEC, int ACT>
 __global__ __launch_bounds__(kThreads) void act_grad_kernel(
     const T* dy, int64_t lddy, const uint8_t* q, int64_t ldq, const uint8_t* scale,
     int64_t blocks_per_row, uint32_t units, FastDiv per_row, int64_t cols, T* dz, int64_t lddz) {
-  const uint32_t first = blockIdx.x * (kThreads * kUnroll) + threadIdx.x;
-  Unit un[kUnroll];
-  Packed<VEC> p[kUnroll];
-  Raw<T, VEC> raw[kUnroll];
+  constexpr int U = unroll<VEC>();
+  const uint32_t first = blockIdx.x * (kThreads * U) + threadIdx.x;
+  Unit un[U];
+  Packed<VEC> p[U];
+  Raw<T, VEC> raw[U];
 #pragma unroll
-  for (int i = 0; i < kUnroll; ++i) {
+  for (int i = 0; i < U; ++i) {
     un[i] = unit_at<VEC>(first + i * kThreads, units, per_row, cols);
     p[i] = load_packed<VEC>(q, ldq, scale, blocks_per_row, un[i]);
     raw[i] = load_raw<VEC>(dy + un[i].row * lddy + un[i].col, un[i].n);
   }
 #pragma unroll
-  for (int i = 0; i < kUnroll; ++i) {
-    float v[VEC], g[VEC];
-    values_of<VEC>(p[i], v);
-    act_slopes<ACT>(v);
+  for (int i = 0; i < U; ++i) {
+    const Slope<ACT> f(scale_value(p[i].code));
+    float g[VEC];
     to_floats(raw[i], g);
+    if constexpr (VEC == 1) {
+      uint64_t lo, hi;
+      e4m3_pairs(p[i].w[0], lo, hi);
+      float other;
+      unpair(mul2(f.slope(lo), pair(g[0], 0.0f)), g[0], other);
+    } else {
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) v[j] *= g[j];
-    store_part<VEC>(dz + un[i].row * lddz + un[i].col, un[i].n, v);
+      for (int j = 0; j < VEC / 4; ++j) {
+        uint64_t lo, hi;
+        e4m3_pairs(p[i].w[j], lo, hi);
+        unpair(mul2(f.slope(lo), pair(g[4 * j], g[4 * j + 1])), g[4 * j], g[4 * j + 1]);
+        unpair(mul2(f.slope(hi), pair(g[4 * j + 2], g[4 * j + 3])), g[4 * j + 2], g[4 * j + 3]);
+      }
+    }
+    store_part<VEC>(dz + un[i].row * lddz + un[i].col, un[i].n, g);
   }
 }
 
 // Calls launch(row0, units, per_row, grid) for row ranges of fewer than 2^30
 // units each, so that unit numbers stay within the 31 bits of FastDiv.
-template <typename F>
-cudaError_t for_row_ranges(int64_t rows, int64_t cols, int vec, F&& launch) {
-  const int64_t per_row = ceil_div(cols, kBlock) * (kBlock / vec);
+template <int VEC, typename F>
+cudaError_t for_row_ranges(int64_t rows, int64_t cols, F&& launch) {
+  const int64_t per_row = ceil_div(cols, kBlock) * (kBlock / VEC);
   const int64_t step = std::max<int64_t>(1, (int64_t{1} << 30) / per_row);
   for (int64_t r = 0; r < rows; r += step) {
     const int64_t units = std::min(step, rows - r) * per_row;
     launch(r, (uint32_t)units, FastDiv((uint32_t)per_row),
-           (unsigned)ceil_div(units, kThreads * kUnroll));
+           (unsigned)ceil_div(units, kThreads * unroll<VEC>()));
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
@@ -179,7 +204,7 @@ template <typename T, int VEC>
 cudaError_t run_pack8(const T* x, int64_t ldx, int64_t rows, int64_t cols, uint8_t* q, int64_t ldq,
                       uint8_t* scale, cudaStream_t st) {
   const int64_t bpr = ceil_div(cols, kBlock);
-  return for_row_ranges(rows, cols, VEC, [&](int64_t r, uint32_t units, FastDiv d, unsigned grid) {
+  return for_row_ranges<VEC>(rows, cols, [&](int64_t r, uint32_t units, FastDiv d, unsigned grid) {
     pack8_kernel<T, VEC><<<grid, kThreads, 0, st>>>(x + r * ldx, ldx, units, d, cols, q + r * ldq,
                                                     ldq, scale + r * bpr, bpr);
   });
@@ -188,7 +213,7 @@ template <typename T, int VEC>
 cudaError_t run_unpack8(const uint8_t* q, int64_t ldq, const uint8_t* scale, int64_t rows,
                         int64_t cols, int act, T* y, int64_t ldy, cudaStream_t st) {
   const int64_t bpr = ceil_div(cols, kBlock);
-  return for_row_ranges(rows, cols, VEC, [&](int64_t r, uint32_t units, FastDiv d, unsigned grid) {
+  return for_row_ranges<VEC>(rows, cols, [&](int64_t r, uint32_t units, FastDiv d, unsigned grid) {
     SCAPE_ACT_SWITCH(act, (unpack8_kernel<T, VEC, ACT><<<grid, kThreads, 0, st>>>(
                               q + r * ldq, ldq, scale + r * bpr, bpr, units, d, cols, y + r * ldy,
                               ldy)));
@@ -199,61 +224,69 @@ cudaError_t run_act_grad(const T* dy, int64_t lddy, const uint8_t* q, int64_t ld
                          const uint8_t* scale, int64_t rows, int64_t cols, int act, T* dz,
                          int64_t lddz, cudaStream_t st) {
   const int64_t bpr = ceil_div(cols, kBlock);
-  return for_row_ranges(rows, cols, VEC, [&](int64_t r, uint32_t units, FastDiv d, unsigned grid) {
+  return for_row_ranges<VEC>(rows, cols, [&](int64_t r, uint32_t units, FastDiv d, unsigned grid) {
     SCAPE_ACT_SWITCH(act, (act_grad_kernel<T, VEC, ACT><<<grid, kThreads, 0, st>>>(
                               dy + r * lddy, lddy, q + r * ldq, ldq, scale + r * bpr, bpr, units,
                               d, cols, dz + r * lddz, lddz)));
   });
 }
 
-}  // namespace
 
-// Eight columns a thread (16-byte loads) where every row is aligned for them,
-// else one: a warp then reads 32 neighbouring columns, a whole block, at a time.
-cudaError_t launch_pack8(const void* x, int64_t ldx, int dtype, int64_t rows, int64_t cols,
-                         uint8_t* q, int64_t ldq, uint8_t* scale, cudaStream_t st) {
-  const size_t e = dtype == SCAPE_BF16 ? 2 : 4;
-  const bool vec = rows16(x, ldx, e) && rows8(q, ldq);
-  if (dtype == SCAPE_BF16) {
-    const bf16* p = static_cast<const bf16*>(x);
-    return vec ? run_pack8<bf16, 8>(p, ldx, rows, cols, q, ldq, scale, st)
-               : run_pack8<bf16, 1>(p, ldx, rows, cols, q, ldq, scale, st);
-  }
-  const float* p = static_cast<const float*>(x);
-  return vec ? run_pack8<float, 8>(p, ldx, rows, cols, q, ldq, scale, st)
-             : run_pack8<float, 1>(p, ldx, rows, cols, q, ldq, scale, st);
+// Columns a thread, as the rows' alignment allows: 16 (one 16-byte word of 8-bit
+// values), 8, or 1: a warp then reads 32 neighbouring columns, a whole block, at
+// a time.  16 against 8: unpack8 of 8192 x 5632 to bfloat16 took 23.2 against
+// 26.5 us, the fewer addresses for the same bytes.
+#define SCAPE_VEC_SWITCH(v16, v8, CALL)              \
+  if (v16) { constexpr int VEC = 16; return CALL; }  \
+  if (v8) { constexpr int VEC = 8; return CALL; }    \
+  { constexpr int VEC = 1; return CALL; }
+
+template <typename T>
+cudaError_t pack8_of(const T* x, int64_t ldx, int64_t rows, int64_t cols, uint8_t* q, int64_t ldq,
+                     uint8_t* scale, cudaStream_t st) {
+  const bool ok = rows16(x, ldx, sizeof(T));
+  SCAPE_VEC_SWITCH(ok && rows16(q, ldq, 1), ok && rows8(q, ldq),
+                   (run_pack8<T, VEC>(x, ldx, rows, cols, q, ldq, scale, st)));
+}
+template <typename T>
+cudaError_t unpack8_of(const uint8_t* q, int64_t ldq, const uint8_t* scale, int64_t rows,
+                       int64_t cols, int act, T* y, int64_t ldy, cudaStream_t st) {
+  const bool ok = rows16(y, ldy, sizeof(T));
+  SCAPE_VEC_SWITCH(ok && rows16(q, ldq, 1), ok && rows8(q, ldq),
+                   (run_unpack8<T, VEC>(q, ldq, scale, rows, cols, act, y, ldy, st)));
+}
+template <typename T>
+cudaError_t act_grad_of(const T* dy, int64_t lddy, const uint8_t* q, int64_t ldq,
+                        const uint8_t* scale, int64_t rows, int64_t cols, int act, T* dz,
+                        int64_t lddz, cudaStream_t st) {
+  const bool ok = rows16(dy, lddy, sizeof(T)) && rows16(dz, lddz, sizeof(T));
+  SCAPE_VEC_SWITCH(ok && rows16(q, ldq, 1), ok && rows8(q, ldq),
+                   (run_act_grad<T, VEC>(dy, lddy, q, ldq, scale, rows, cols, act, dz, lddz, st)));
 }
 
+}  // namespace
+
+cudaError_t launch_pack8(const void* x, int64_t ldx, int dtype, int64_t rows, int64_t cols,
+                         uint8_t* q, int64_t ldq, uint8_t* scale, cudaStream_t st) {
+  return dtype == SCAPE_BF16
+             ? pack8_of(static_cast<const bf16*>(x), ldx, rows, cols, q, ldq, scale, st)
+             : pack8_of(static_cast<const float*>(x), ldx, rows, cols, q, ldq, scale, st);
+}
 cudaError_t launch_unpack8(const uint8_t* q, int64_t ldq, const uint8_t* scale, int64_t rows,
                            int64_t cols, int act, void* y, int64_t ldy, int dtype,
                            cudaStream_t st) {
-  const size_t e = dtype == SCAPE_BF16 ? 2 : 4;
-  const bool vec = rows16(y, ldy, e) && rows8(q, ldq);
-  if (dtype == SCAPE_BF16) {
-    bf16* p = static_cast<bf16*>(y);
-    return vec ? run_unpack8<bf16, 8>(q, ldq, scale, rows, cols, act, p, ldy, st)
-               : run_unpack8<bf16, 1>(q, ldq, scale, rows, cols, act, p, ldy, st);
-  }
-  float* p = static_cast<float*>(y);
-  return vec ? run_unpack8<float, 8>(q, ldq, scale, rows, cols, act, p, ldy, st)
-             : run_unpack8<float, 1>(q, ldq, scale, rows, cols, act, p, ldy, st);
+  return dtype == SCAPE_BF16
+             ? unpack8_of(q, ldq, scale, rows, cols, act, static_cast<bf16*>(y), ldy, st)
+             : unpack8_of(q, ldq, scale, rows, cols, act, static_cast<float*>(y), ldy, st);
 }
-
 cudaError_t launch_act_grad(const void* dy, int64_t lddy, const uint8_t* q, int64_t ldq,
                             const uint8_t* scale, int64_t rows, int64_t cols, int act, void* dz,
                             int64_t lddz, int dtype, cudaStream_t st) {
-  const size_t e = dtype == SCAPE_BF16 ? 2 : 4;
-  const bool vec = rows16(dy, lddy, e) && rows16(dz, lddz, e) && rows8(q, ldq);
-  if (dtype == SCAPE_BF16) {
-    const bf16* p = static_cast<const bf16*>(dy);
-    bf16* o = static_cast<bf16*>(dz);
-    return vec ? run_act_grad<bf16, 8>(p, lddy, q, ldq, scale, rows, cols, act, o, lddz, st)
-               : run_act_grad<bf16, 1>(p, lddy, q, ldq, scale, rows, cols, act, o, lddz, st);
-  }
-  const float* p = static_cast<const float*>(dy);
-  float* o = static_cast<float*>(dz);
-  return vec ? run_act_grad<float, 8>(p, lddy, q, ldq, scale, rows, cols, act, o, lddz, st)
-             : run_act_grad<float, 1>(p, lddy, q, ldq, scale, rows, cols, act, o, lddz, st);
+  return dtype == SCAPE_BF16
+             ? act_grad_of(static_cast<const bf16*>(dy), lddy, q, ldq, scale, rows, cols, act,
+                           static_cast<bf16*>(dz), lddz, st)
+             : act_grad_of(static_cast<const float*>(dy), lddy, q, ldq, scale, rows, cols, act,
+                           static_cast<float*>(dz), lddz, st);
 }
 
 }  // namespace layer

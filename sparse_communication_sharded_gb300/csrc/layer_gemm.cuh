@@ -446,13 +446,13 @@ __device__ __forceinline__ void load_beside(Beside<KIND, N>& b, bool live, int64
 // v *= act'(z), four z at a time from their 8-bit words.
 template <int ACT, int N, int W>
 __device__ __forceinline__ void times_slopes(float (&v)[N], const uint32_t (&w)[W], float scale) {
+  const Slope<ACT> f(scale);
 #pragma unroll
   for (int i = 0; i < N / 4; ++i) {
-    float z[4];
-    from_e4m3(w[i], scale, z);
-    act_slopes<ACT>(z);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) v[4 * i + j] *= z[j];
+    uint64_t lo, hi;
+    e4m3_pairs(w[i], lo, hi);
+    unpair(mul2(f.slope(lo), pair(v[4 * i], v[4 * i + 1])), v[4 * i], v[4 * i + 1]);
+    unpair(mul2(f.slope(hi), pair(v[4 * i + 2], v[4 * i + 3])), v[4 * i + 2], v[4 * i + 3]);
   }
 }
 

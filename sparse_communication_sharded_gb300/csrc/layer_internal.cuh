@@ -35,7 +35,7 @@ inline bool rows8(const void* p, int64_t ld) {
 // VEC consecutive elements as they lie in memory.  Loads fill these and nothing
 // else, so that a thread has all its loads in flight before it converts the
 // first: a conversion between two loads would wait for the one before it.
-// VEC 8 needs 16-byte alignment, VEC 1 none.
+// VEC 8 and 16 need 16-byte alignment, VEC 1 none.
 template <typename T, int VEC>
 struct Raw {
   static constexpr int kWords = VEC * sizeof(T) >= 4 ? VEC * sizeof(T) / 4 : 1;
@@ -45,7 +45,7 @@ template <int VEC, typename T>
 __device__ __forceinline__ Raw<T, VEC> load_raw(const T* p, int n) {
   Raw<T, VEC> r;
   if (n >= VEC) {
-    if constexpr (VEC == 8) {
+    if constexpr (VEC >= 8) {
 #pragma unroll
       for (int i = 0; i < Raw<T, VEC>::kWords / 4; ++i) {
         const uint4 u = reinterpret_cast<const uint4*>(p)[i];
@@ -90,11 +90,12 @@ __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
 }
 template <int VEC>
 __device__ __forceinline__ void store_vec(bf16* p, const float (&v)[VEC]) {
-  if constexpr (VEC == 8) {
-    uint4 u;
-    u.x = bf16_pair(v[0], v[1]), u.y = bf16_pair(v[2], v[3]);
-    u.z = bf16_pair(v[4], v[5]), u.w = bf16_pair(v[6], v[7]);
-    *reinterpret_cast<uint4*>(p) = u;
+  if constexpr (VEC >= 8) {
+#pragma unroll
+    for (int i = 0; i < VEC / 8; ++i)
+      reinterpret_cast<uint4*>(p)[i] =
+          make_uint4(bf16_pair(v[8 * i], v[8 * i + 1]), bf16_pair(v[8 * i + 2], v[8 * i + 3]),
+                     bf16_pair(v[8 * i + 4], v[8 * i + 5]), bf16_pair(v[8 * i + 6], v[8 * i + 7]));
   } else {
 #pragma unroll
     for (int i = 0; i < VEC; ++i) p[i] = __float2bfloat16_rn(v[i]);
@@ -102,9 +103,10 @@ __device__ __forceinline__ void store_vec(bf16* p, const float (&v)[VEC]) {
 }
 template <int VEC>
 __device__ __forceinline__ void store_vec(float* p, const float (&v)[VEC]) {
-  if constexpr (VEC == 8) {
-    reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+  if constexpr (VEC >= 8) {
+#pragma unroll
+    for (int i = 0; i < VEC / 4; ++i)
+      reinterpret_cast<float4*>(p)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
   } else {
 #pragma unroll
     for (int i = 0; i < VEC; ++i) p[i] = v[i];
@@ -144,6 +146,32 @@ __device__ __forceinline__ void load_weight(const void* w, int is_bf16, bool ali
       for (int i = 0; i < VEC; ++i) v[i] = i < n ? p[i] : 0.0f;
     }
   }
+}
+
+// ------------------------------------------------------------------ packed pairs of floats
+// One instruction for two values: half the issue slots.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t r, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(r));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
 }
 
 // ------------------------------------------------------------------ the 8-bit block format
@@ -196,10 +224,12 @@ __device__ __forceinline__ uint32_t part_top_finite(const float (&v)[N]) {
 template <int N>
 __device__ __forceinline__ void to_e4m3(const float (&v)[N], float inv, bool no_inf,
                                         uint32_t (&w)[N / 4]) {
+  const uint64_t inv2 = pair(inv, inv);
 #pragma unroll
   for (int i = 0; i < N / 4; ++i) {
-    float a = v[4 * i] * inv, b = v[4 * i + 1] * inv, c = v[4 * i + 2] * inv,
-          d = v[4 * i + 3] * inv;
+    float a, b, c, d;
+    unpair(mul2(pair(v[4 * i], v[4 * i + 1]), inv2), a, b);
+    unpair(mul2(pair(v[4 * i + 2], v[4 * i + 3]), inv2), c, d);
     if (!no_inf) {
       a = nan_unless_finite(a), b = nan_unless_finite(b);
       c = nan_unless_finite(c), d = nan_unless_finite(d);
@@ -207,20 +237,16 @@ __device__ __forceinline__ void to_e4m3(const float (&v)[N], float inv, bool no_
     w[i] = e4m3_pair(a, b) | (e4m3_pair(c, d) << 16);
   }
 }
-// Four e4m3 values as floats (exact).
-__device__ __forceinline__ void from_e4m3(uint32_t w, float scale, float* v) {
-  const __half2_raw lo = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w & 0xFFFFu), __NV_E4M3);
-  const __half2_raw hi = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> 16), __NV_E4M3);
-  const float2 a = __half22float2(__half2(lo)), b = __half22float2(__half2(hi));
-  v[0] = a.x * scale, v[1] = a.y * scale, v[2] = b.x * scale, v[3] = b.y * scale;
+// Four e4m3 values as two pairs of floats, before their scale (exact).
+__device__ __forceinline__ void e4m3_pairs(uint32_t w, uint64_t& lo, uint64_t& hi) {
+  const __half2_raw l = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w & 0xFFFFu), __NV_E4M3);
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> 16), __NV_E4M3);
+  const float2 a = __half22float2(__half2(l)), b = __half22float2(__half2(h));
+  lo = pair(a.x, a.y);
+  hi = pair(b.x, b.y);
 }
-__device__ __forceinline__ float from_e4m3_byte(uint32_t b, float scale) {
-  const __half_raw h = __nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)b, __NV_E4M3);
-  return __half2float(__half(h)) * scale;
-}
-
-// One warp's 32 lanes pack VEC values each; with VEC 8 four neighbouring lanes
-// hold a block, with VEC 1 the whole warp does.  n values of the thread are
+// One warp's 32 lanes pack VEC values each; with VEC 16 two neighbouring lanes
+// hold a block, with VEC 8 four, with VEC 1 the whole warp.  n values of the thread are
 // real (the others are 0).  All 32 lanes call it together.
 template <int VEC>
 __device__ __forceinline__ void warp_pack(const float (&v)[VEC], int n, uint8_t* q, uint8_t* scale,
@@ -234,12 +260,14 @@ __device__ __forceinline__ void warp_pack(const float (&v)[VEC], int n, uint8_t*
       no_inf = false;
     }
   } else {
-    top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-    top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+    auto over_lanes = [](uint32_t t) {
+      t = max(t, __shfl_xor_sync(0xFFFFFFFFu, t, 1));
+      if (VEC == 8) t = max(t, __shfl_xor_sync(0xFFFFFFFFu, t, 2));
+      return t;
+    };
+    top = over_lanes(top);
     if (__any_sync(0xFFFFFFFFu, top >= kInfBits)) {
-      top = part_top_finite<VEC>(v);
-      top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-      top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+      top = over_lanes(part_top_finite<VEC>(v));
       no_inf = false;
     }
   }
@@ -249,13 +277,16 @@ __device__ __forceinline__ void warp_pack(const float (&v)[VEC], int n, uint8_t*
     const float x = v[0] * inv;
     if (n > 0) *q = (uint8_t)e4m3_pair(no_inf ? x : nan_unless_finite(x), 0.0f);
   } else {
-    uint32_t w[2];
-    to_e4m3<8>(v, inv, no_inf, w);
-    if (n >= 8) {
-      *reinterpret_cast<uint2*>(q) = make_uint2(w[0], w[1]);
+    uint32_t w[VEC / 4];
+    to_e4m3<VEC>(v, inv, no_inf, w);
+    if (n >= VEC) {
+      if constexpr (VEC == 16)
+        *reinterpret_cast<uint4*>(q) = make_uint4(w[0], w[1], w[2], w[3]);
+      else
+        *reinterpret_cast<uint2*>(q) = make_uint2(w[0], w[1]);
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
+      for (int i = 0; i < VEC; ++i)
         if (i < n) q[i] = (uint8_t)(w[i / 4] >> (8 * (i % 4)));
     }
   }
@@ -265,34 +296,7 @@ __device__ __forceinline__ void warp_pack(const float (&v)[VEC], int n, uint8_t*
 // ------------------------------------------------------------------ activations
 // gelu's 0.5 (1 + tanh u) is the logistic function of 2u, so gelu and silu are
 // both z * logistic(a): one exponential and one reciprocal a value, and a
-// relative (not absolute) error where the result is small.  Two values at a
-// time: the multiplications and additions are packed 32-bit pairs, which halves
-// their issue slots; the exponential and the reciprocal (16 a clock an SM) are
-// then what bounds the arithmetic.
-__device__ __forceinline__ uint64_t pair(float a, float b) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ void unpair(uint64_t r, float& a, float& b) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(r));
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t both(float a) { return pair(a, a); }
+// relative (not absolute) error where the result is small.
 __device__ __forceinline__ float exp2_fast(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -303,109 +307,148 @@ __device__ __forceinline__ float reciprocal_fast(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
-// Limits that keep a NaN.
-__device__ __forceinline__ float at_least(float x, float lo) {
+// x if it is above 0 (or not a number), else 0.
+__device__ __forceinline__ float above_zero(float x) {
   float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(lo));
+  asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(r) : "f"(x));
   return r;
 }
-__device__ __forceinline__ float at_most(float x, float hi) {
-  float r;
-  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(hi));
+// A constant in both halves of a register pair, which the compiler takes for a
+// value it cannot make again: without this it made the constants anew for every
+// use, two moves each, half as many instructions again as the arithmetic.
+__device__ __forceinline__ uint64_t held(float a) {
+  uint64_t r;
+  asm volatile("mov.b64 %0, {%1, %1};" : "=l"(r) : "f"(a));
   return r;
 }
 
 constexpr double kLog2e = 1.4426950408889634074;
 constexpr double kGelu2C = 1.5957691216057307117;  // 2 sqrt(2 / pi)
 constexpr double kGeluA = 0.044715;
+constexpr double kGeluK0 = -kGelu2C * kLog2e;  // 2^(z (K0 + K1 z^2)) = exp(-2u)
+constexpr double kGeluK1 = -kGelu2C * kGeluA * kLog2e;
 __host__ __device__ constexpr float high(double x) { return (float)x; }
 __host__ __device__ constexpr float low(double x) { return (float)(x - (double)(float)x); }
 
-// The logistic function of silu's and gelu's argument a at z, by 2^e with
-// e = -a log2(e).  An error d in e is a relative error 0.69 d of the result where
-// that is small: at e = 100 the roundings of e alone are 2^-18 or so.  A bfloat16
-// result cannot show that; DEEP, for 32-bit results, carries e's roundings and
-// its constants' low parts along as d and corrects 2^e by 1 + d ln 2.
-template <int ACT, bool DEEP>
-__device__ __forceinline__ uint64_t logistic2(uint64_t z) {
-  constexpr double k0 = ACT == SCAPE_ACT_GELU ? -kGelu2C * kLog2e : -kLog2e;
-  constexpr double k1 = -kGelu2C * kGeluA * kLog2e;
-  uint64_t t = both(high(k0)), z2 = 0;
-  if constexpr (ACT == SCAPE_ACT_GELU) {
-    z2 = mul2(z, z);
-    t = fma2(z2, both(high(k1)), both(high(k0)));
+// An activation on pairs of values z = q s with a common scale s, which goes into
+// the coefficients.  2^e with e = q (a + b q^2) gives the logistic function
+// p = 1 / (1 + 2^e).  Where s is over 2^20 the exponent takes 2^20 for it: any q
+// but 0 is then at least 2^-9, so |z| is over 2^11 either way and p is 0 or 1.
+template <int ACT>
+struct Activation {
+  static constexpr bool kLogistic = ACT == SCAPE_ACT_GELU || ACT == SCAPE_ACT_SILU;
+  uint64_t s, a, b, one;
+
+  __device__ __forceinline__ explicit Activation(float scale) {
+    s = held(scale);
+    if constexpr (kLogistic) {
+      const float l = fminf(scale, 1048576.0f);
+      one = held(1.0f);
+      if constexpr (ACT == SCAPE_ACT_GELU) {
+        a = held(high(kGeluK0) * l);
+        b = held(high(kGeluK1) * l * l * l);
+      } else {
+        a = held(high(-kLog2e) * l);
+      }
+    }
   }
-  const uint64_t e = mul2(z, t);
-  float a, b;
-  unpair(e, a, b);
-  uint64_t x = pair(exp2_fast(a), exp2_fast(b));
-  if constexpr (DEEP) {
-    const uint64_t minus = both(-1.0f);
-    uint64_t t_low = both(low(k0));
-    if constexpr (ACT == SCAPE_ACT_GELU)
-      t_low = fma2(z2, both(low(k1)), add2(both(low(k0)), fma2(z2, both(high(k1)), fma2(t, minus, both(high(k0))))));
-    const uint64_t d = fma2(z, t_low, fma2(z, t, mul2(e, minus)));
-    float da, db;
-    unpair(mul2(d, both(0.69314718f)), da, db);
-    unpair(x, a, b);
-    // where e or z^2 has overflowed d says nothing, and 2^e is 0 or infinite
-    x = pair(a > 1e-37f && a < 1e37f ? fmaf(a, da, a) : a,
-             b > 1e-37f && b < 1e37f ? fmaf(b, db, b) : b);
+  __device__ __forceinline__ uint64_t logistic(uint64_t q) const {
+    uint64_t t = a;
+    if constexpr (ACT == SCAPE_ACT_GELU) t = fma2(mul2(q, q), b, a);
+    float x, y;
+    unpair(mul2(q, t), x, y);
+    unpair(add2(pair(exp2_fast(x), exp2_fast(y)), one), x, y);
+    return pair(reciprocal_fast(x), reciprocal_fast(y));
   }
-  unpair(add2(x, both(1.0f)), a, b);
-  return pair(reciprocal_fast(a), reciprocal_fast(b));
+  // act(q s)
+  __device__ __forceinline__ uint64_t value(uint64_t q) const {
+    if constexpr (kLogistic) return mul2(mul2(q, s), logistic(q));
+    if constexpr (ACT == SCAPE_ACT_RELU) {
+      float x, y;
+      unpair(mul2(q, s), x, y);
+      return pair(above_zero(x), above_zero(y));
+    }
+    return mul2(q, s);
+  }
+};
+
+// act(z) for z without a scale.
+template <int ACT, int N>
+__device__ __forceinline__ void act_values(float (&v)[N]) {
+  if constexpr (ACT == SCAPE_ACT_RELU) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = above_zero(v[i]);
+  } else if constexpr (ACT != SCAPE_ACT_NONE) {
+    const Activation<ACT> f(1.0f);
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+      const uint64_t z = pair(v[i], N == 1 ? 0.0f : v[(i + 1) % N]);
+      float other;
+      unpair(mul2(z, f.logistic(z)), v[i], N == 1 ? other : v[(i + 1) % N]);
+    }
+  }
 }
 
-template <int ACT, bool DEEP = false>
-__device__ __forceinline__ void act_pair(float& x, float& y) {
-  if constexpr (ACT == SCAPE_ACT_RELU) {
-    x = at_least(x, 0.0f);
-    y = at_least(y, 0.0f);
-  } else if constexpr (ACT == SCAPE_ACT_GELU || ACT == SCAPE_ACT_SILU) {
-    const uint64_t z = pair(x, y);
-    unpair(mul2(z, logistic2<ACT, DEEP>(z)), x, y);
-  }
-}
-// x, y become the activation's slopes there.  Past |z| = 20 (gelu) and 100 (silu)
-// the logistic is 0 or 1 to the last bit and so is the slope; the limit keeps 0
-// times an overflowed z^2 out.
+// act'(q s): p + z a'(z) p (1 - p), whose second term is q (c + d q^2) p (1 - p)
+// with c = s, d = 0 for silu.  With the exponent's limit on s nothing overflows:
+// |z| stays below 2^29.
 template <int ACT>
-__device__ __forceinline__ void slope_pair(float& x, float& y) {
-  if constexpr (ACT == SCAPE_ACT_RELU) {
-    x = x > 0.0f ? 1.0f : (x != x ? x : 0.0f);
-    y = y > 0.0f ? 1.0f : (y != y ? y : 0.0f);
-  } else if constexpr (ACT == SCAPE_ACT_GELU || ACT == SCAPE_ACT_SILU) {
-    constexpr float kLim = ACT == SCAPE_ACT_GELU ? 20.0f : 100.0f;
-    const uint64_t z = pair(at_most(at_least(x, -kLim), kLim), at_most(at_least(y, -kLim), kLim));
-    const uint64_t p = logistic2<ACT, false>(z);
-    uint64_t m = z;  // z da/dz
-    if constexpr (ACT == SCAPE_ACT_GELU)
-      m = mul2(z, fma2(mul2(z, z), both(high(3.0 * kGelu2C * kGeluA)), both(high(kGelu2C))));
-    const uint64_t pq = fma2(mul2(p, both(-1.0f)), p, p);  // p (1 - p)
-    unpair(fma2(m, pq, p), x, y);
-  } else {
-    x = y = 1.0f;
+struct Slope : Activation<ACT> {
+  uint64_t c, d, minus;
+  __device__ __forceinline__ explicit Slope(float scale) : Activation<ACT>(scale) {
+    if constexpr (Activation<ACT>::kLogistic) {
+      const float l = fminf(scale, 1048576.0f);
+      minus = held(-1.0f);
+      if constexpr (ACT == SCAPE_ACT_GELU) {
+        c = held(high(kGelu2C) * l);
+        d = held(high(3.0 * kGelu2C * kGeluA) * l * l * l);
+      } else {
+        c = held(l);
+      }
+    }
   }
-}
-template <int ACT, bool DEEP = false, int N>
-__device__ __forceinline__ void act_values(float (&v)[N]) {
-  if constexpr (N == 1) {
-    float other = 0.0f;
-    act_pair<ACT, DEEP>(v[0], other);
-  } else {
-#pragma unroll
-    for (int i = 0; i < N / 2; ++i) act_pair<ACT, DEEP>(v[2 * i], v[2 * i + 1]);
+  __device__ __forceinline__ uint64_t slope(uint64_t q) const {
+    if constexpr (Activation<ACT>::kLogistic) {
+      const uint64_t p = this->logistic(q);
+      uint64_t t = c;
+      if constexpr (ACT == SCAPE_ACT_GELU) t = fma2(mul2(q, q), d, c);
+      return fma2(mul2(q, t), fma2(mul2(p, minus), p, p), p);
+    }
+    float x, y;
+    unpair(q, x, y);
+    if constexpr (ACT == SCAPE_ACT_RELU) {
+      x = x > 0.0f ? 1.0f : (x != x ? x : 0.0f);
+      y = y > 0.0f ? 1.0f : (y != y ? y : 0.0f);
+    } else {
+      x = y = 1.0f;
+    }
+    return pair(x, y);
   }
-}
-template <int ACT, int N>
-__device__ __forceinline__ void act_slopes(float (&v)[N]) {
-  if constexpr (N == 1) {
-    float other = 0.0f;
-    slope_pair<ACT>(v[0], other);
-  } else {
-#pragma unroll
-    for (int i = 0; i < N / 2; ++i) slope_pair<ACT>(v[2 * i], v[2 * i + 1]);
+};
+
+// 32-bit results.  An error d in e is a relative error 0.69 d of 2^e, and at
+// e = 100, far out in the tail, the roundings of e alone are 2^-18 or so: no
+// bfloat16 result shows it, a 32-bit one does.  So e's roundings and its
+// constants' low parts are carried along as d, and 2^e corrected by 1 + d ln 2.
+template <int ACT>
+__device__ __forceinline__ float act_exact(float z) {
+  if constexpr (ACT == SCAPE_ACT_RELU) return above_zero(z);
+  if constexpr (ACT == SCAPE_ACT_GELU || ACT == SCAPE_ACT_SILU) {
+    constexpr double k0 = ACT == SCAPE_ACT_GELU ? kGeluK0 : -kLog2e;
+    float t = high(k0), t_low = low(k0);
+    if constexpr (ACT == SCAPE_ACT_GELU) {
+      const float z2 = z * z;
+      t = fmaf(z2, high(kGeluK1), high(k0));
+      t_low = fmaf(z2, low(kGeluK1), low(k0) + fmaf(z2, high(kGeluK1), high(k0) - t));
+    }
+    const float e = z * t;
+    const float d = fmaf(z, t_low, fmaf(z, t, -e));
+    float x = exp2_fast(e);
+    // where e or z^2 has overflowed d says nothing, and 2^e is 0 or infinite
+    if (x > 1e-37f && x < 1e37f) x = fmaf(x, d * 0.69314718f, x);
+    return z * reciprocal_fast(1.0f + x);
   }
+  return z;
 }
 
 // CALL with ACT a constant, for an activation known at run time.
