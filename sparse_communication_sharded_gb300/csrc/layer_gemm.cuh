@@ -85,26 +85,17 @@ __device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+// One try; the hardware may suspend the thread for up to the hinted millisecond.
+// Without the hint the waiting warps' polls took enough of the SM to slow the
+// products by 2 to 10% (8192^3: 562 against 550 us).
 __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-// The same with the visibility of writes made elsewhere in the cluster.
-__device__ __forceinline__ bool mbar_try_cluster(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
+      : "r"(bar), "r"(parity), "r"(1000000u)
       : "memory");
   return ok != 0;
 }
@@ -255,7 +246,7 @@ constexpr int kBM = 128;  // rows of a block's tile: the tensor core's 128 accum
 constexpr int kBK = 64;   // contraction a stage: one 128-byte swizzled row of bfloat16
 constexpr int kChunk = 8192;       // bytes of 64 staged rows of 128 bytes
 constexpr int kBoxBytes = 2048;    // 32 x 32 bfloat16 on their way out
-constexpr int kTileCost = 16;      // what a tile costs besides its columns, in columns
+constexpr int kTileCost = 500;     // clocks a tile costs besides its stages
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 
 // How a product is laid over the blocks.
@@ -272,11 +263,11 @@ enum GemmMode {
 template <int KIND, int BN, int MODE>
 struct Tile {
   static constexpr bool kPair = MODE == kModePair;
-  // The epilogue of a pair has a tile's multiplication time (8192 clocks for a
-  // contraction of 1024) to turn 128 x 256 accumulators into output.  With
-  // activations to compute, 8 warps (2 a scheduler) kept 30% of the issue slots
-  // busy and took twice that; 16 warps overlap their latencies.
-  static constexpr int kEpilogueWarps = kPair && KIND != kGemmWeightGrad ? 16 : 8;
+  // 8 warps, 2 a scheduler.  16 made a gelu epilogue shorter (input gradient of
+  // 8192 x 4096, contraction 1024: 49 against 53 us) but the others longer
+  // (forward without an activation: 53 against 41 us): they crowd the one thread
+  // that issues the matrix instructions, and their output boxes take a stage.
+  static constexpr int kEpilogueWarps = 8;
   static constexpr int kThreads = 128 + 32 * kEpilogueWarps;  // + TMA, MMA, TMEM, an idle warp
   static constexpr int kGroups = kEpilogueWarps / 4;  // warps that share a quarter of the rows
   static constexpr int kWarpChunks = BN / 32 / kGroups;       // 32-column chunks a warp, at most
@@ -285,7 +276,7 @@ struct Tile {
   static constexpr int kBBytes = kBRows * kBK * 2;
   static constexpr int kStageBytes = kABytes + kBBytes;
   // as many stages as fit beside the output boxes and the bias
-  static constexpr int kStages = kStageBytes > 24576 ? (kEpilogueWarps == 16 ? 4 : 5) : 6;
+  static constexpr int kStages = kStageBytes > 24576 ? 5 : 6;
   static constexpr int kColumns = 2 * BN;  // two accumulators
   static constexpr int kBoxAt = kStages * kStageBytes;
   static constexpr int kBiasAt = kBoxAt + (kPair ? kEpilogueWarps * 2 * kBoxBytes : 0);
@@ -597,12 +588,11 @@ __global__ __launch_bounds__(Tile<KIND, BN, MODE>::kThreads, 1) void gemm_kernel
   // Every wait ends: after the limit the kernel records it and all its roles
   // stop (they look at gave_up while they wait).
   auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
-    auto once = [&] { return PAIR ? mbar_try_cluster(bar, parity) : mbar_try(bar, parity); };
-    if (once()) return true;
+    if (mbar_try(bar, parity)) return true;
     const uint64_t t0 = now_ns();
     for (;;) {
       for (int i = 0; i < 16; ++i)
-        if (once()) return true;
+        if (mbar_try(bar, parity)) return true;
       if (gave_up) return false;
       if (now_ns() - t0 > kWaitLimitNs) {
         gave_up = 1;
@@ -684,6 +674,7 @@ __global__ __launch_bounds__(Tile<KIND, BN, MODE>::kThreads, 1) void gemm_kernel
   } else if (warp == 1 && lane == 0 && (!PAIR || rank == 0)) {
     // ---------------- tensor core
     const uint32_t idesc = instr_desc<kTileRows, TA, TB>(bn);
+    const uint64_t desc_a = smem_desc(smem, TA), desc_b = smem_desc(smem + TL::kABytes, TB);
     int stage = 0, phase = 0, acc = 0, acc_phase = 0;
     bool ok = true;
     for (int t = first; ok && t < tiles; t += step) {
@@ -695,14 +686,13 @@ __global__ __launch_bounds__(Tile<KIND, BN, MODE>::kThreads, 1) void gemm_kernel
         ok = wait(full(stage), phase);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t a = smem + stage * TL::kStageBytes, b = a + TL::kABytes;
+        // 16 of the contraction: 32 bytes along a row, or 16 rows (addresses count
+        // 16 bytes; a block's shared memory ends below where they would carry)
+        const uint64_t da = desc_a + ((stage * TL::kStageBytes) >> 4);
+        const uint64_t db = desc_b + ((stage * TL::kStageBytes) >> 4);
 #pragma unroll
-        for (int i = 0; i < kBK / 16; ++i) {
-          // 16 of the contraction: 32 bytes along a row, or 16 rows
-          const uint64_t da = smem_desc(a + i * (TA ? 2048 : 32), TA);
-          const uint64_t db = smem_desc(b + i * (TB ? 2048 : 32), TB);
-          tc_mma<PAIR>(d, da, db, idesc, k > k0 || i > 0);
-        }
+        for (int i = 0; i < kBK / 16; ++i)
+          tc_mma<PAIR>(d, da + i * (TA ? 128 : 2), db + i * (TB ? 128 : 2), idesc, k > k0 || i > 0);
         tc_commit<PAIR>(empty(stage));
         if (++stage == TL::kStages) stage = 0, phase ^= 1;
       }
@@ -932,24 +922,27 @@ cudaError_t gemm_launch(const GemmCall& c, int bn, int split, cudaStream_t st) {
 
 // Tile and mode.  Pairs do the most work a byte read and keep the tensor cores
 // busy through the epilogue; they take whole tiles, so their time goes by the
-// number of tiles the busiest pair gets times a tile's width (plus what a tile
-// costs whatever its width), and the width is the one that makes it least.  They
-// want at least 3/4 of the SMs at work.  Below that, narrow tiles, each cut
-// over a cluster as far as there are SMs and at least four stages of the
-// contraction for every block.
+// number of tiles the busiest pair gets times a tile's.  A stage of a tile takes
+// 2 clocks a column on the tensor cores, or 18 a kilobyte that comes into the SM
+// (measured: 590 clocks for 32 KB, whatever the width), whichever is more.  The
+// width with the least time is taken.  Pairs want at least 3/4 of the SMs at
+// work.  Below that, narrow tiles, each cut over a cluster as far as there are
+// SMs and at least four stages of the contraction for every block.
 template <int KIND>
 cudaError_t gemm_run(const GemmCall& c, cudaStream_t st) {
   const int64_t sms = sm_count(), pairs = sms / 2;
-  const int64_t tp = ceil_div(c.m, 2 * kBM);
+  const int64_t tp = ceil_div(c.m, 2 * kBM), ksteps = ceil_div(c.k, kBK);
   int best = 0;
   int64_t least = 0;
   for (int bn = 256; bn >= 128; bn -= 32) {
     const int64_t tiles = tp * ceil_div(c.n, bn);
-    const int64_t cost = ceil_div(tiles, pairs) * (bn + kTileCost);
+    const int64_t kb = 16 + (KIND == kGemmForward ? bn / 16 : ceil_div(bn, 128) * 8);
+    const int64_t tile = ksteps * std::max<int64_t>(2 * bn, 18 * kb) + kTileCost;
+    const int64_t cost = ceil_div(tiles, pairs) * tile;
     if (tiles * 4 >= pairs * 3 && (best == 0 || cost < least)) best = bn, least = cost;
   }
   if (best) return gemm_launch<KIND, 256, kModePair>(c, best, 2, st);
-  const int64_t tm = ceil_div(c.m, kBM), ksteps = ceil_div(c.k, kBK);
+  const int64_t tm = ceil_div(c.m, kBM);
   const int bn = tm * ceil_div(c.n, 64) <= sms ? 64 : 128;
   const int64_t tiles = tm * ceil_div(c.n, bn);
   int split = 1;
