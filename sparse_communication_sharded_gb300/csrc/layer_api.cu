@@ -408,8 +408,7 @@ extern "C" int scape_layer_linear_bwd_weight_workspace(const void* dy, int64_t l
   *bytes = 0;
   if (rows == 0 || n == 0) return SCAPE_OK;
   *bytes = operand_bytes(dy, lddy, rows, n) +
-           (x ? operand_bytes(x, ldx, rows, k) : copy_bytes(rows, k)) +
-           round256((size_t)colsum_partials(rows, n) * n * 4);
+           (x ? operand_bytes(x, ldx, rows, k) : copy_bytes(rows, k));
   return SCAPE_OK;
 }
 
@@ -464,7 +463,7 @@ extern "C" int scape_layer_linear_bwd_weight(const void* dy, int64_t lddy, const
     if (e == cudaSuccess) e = gemm_weight_grad(c, st);
   }
   if (e == cudaSuccess && dbias)
-    e = launch_colsum(static_cast<const bf16*>(dy), lddy, rows, n, reinterpret_cast<float*>(ws),
-                      dbias, grad_dtype == SCAPE_BF16, st);
+    e = launch_colsum(static_cast<const bf16*>(dy), lddy, rows, n, dbias, grad_dtype == SCAPE_BF16,
+                      st);
   return cuda_result(e, who);
 }

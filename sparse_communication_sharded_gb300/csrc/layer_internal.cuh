@@ -497,9 +497,8 @@ int64_t norm_bwd_partials(int64_t rows, int64_t cols);
 cudaError_t launch_norm_bwd(const NormBwd& a, int dtype, cudaStream_t st);
 
 // Column sums of m[rows, cols] (bfloat16) in 32 bits.
-int64_t colsum_partials(int64_t rows, int64_t cols);
-cudaError_t launch_colsum(const bf16* m, int64_t ld, int64_t rows, int64_t cols, float* partial,
-                          void* out, int out_bf16, cudaStream_t st);
+cudaError_t launch_colsum(const bf16* m, int64_t ld, int64_t rows, int64_t cols, void* out,
+                          int out_bf16, cudaStream_t st);
 // Sum of `parts` rows of partial[parts, cols].
 cudaError_t launch_sum_partials(const float* partial, int64_t parts, int64_t cols, void* out,
                                 int out_bf16, cudaStream_t st);

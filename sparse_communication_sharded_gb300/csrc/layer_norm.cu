@@ -4,7 +4,7 @@
 // squares (or of gradient products) is taken over the warps that hold the row,
 // and the outputs are written from the same registers.
 //
-// A row of up to kWarpCols columns belongs to one warp (no block barrier), a
+// A row of up to 1024 columns (backward 512) belongs to one warp (no block barrier), a
 // wider one to a block that is as wide as the row needs; rows over kBlockCols
 // are read twice by the *_wide kernels.
 #include <algorithm>
@@ -15,7 +15,8 @@ namespace scapek {
 namespace layer {
 namespace {
 
-constexpr int kWarpCols = 1024;
+constexpr int kWarpCols = 1024;   // forward
+constexpr int kWarpColsBwd = 512;  // backward, which holds twice as much a column
 constexpr int kBlockCols = 8192;
 constexpr int kWarpRows = 4;  // rows (warps) a block, for the narrow rows
 
@@ -35,37 +36,46 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
   return warp_sum(s);
 }
 
-// Where a thread's vectors lie: vector i of thread t of `width` covers columns
-// (i * width + t) * VEC and on.
-template <int VEC>
-__device__ __forceinline__ int vec_col(int i, int t, int width) { return (i * width + t) * VEC; }
+// Vector i of thread t of `width` covers columns (i * width + t) * VEC and on.
 
-template <typename T, int VEC, int NV, bool WARP>
-__global__ __launch_bounds__(WARP ? 32 * kWarpRows : 512) void norm_fwd_kernel(NormFwd a, bool w_vec) {
+// WIDTH threads own a row: 32 (a warp) or a block of that many; 0: the block's
+// size, known at launch only.
+template <int WIDTH>
+struct Team {
+  static constexpr bool kWarp = WIDTH == 32;
+  static constexpr int kThreads = kWarp ? 32 * kWarpRows : WIDTH ? WIDTH : 512;
+  __device__ static int lane() { return kWarp ? threadIdx.x & 31 : threadIdx.x; }
+  __device__ static int width() { return WIDTH ? WIDTH : blockDim.x; }
+  __device__ static int64_t first() {
+    return kWarp ? (int64_t)blockIdx.x * kWarpRows + (threadIdx.x >> 5) : blockIdx.x;
+  }
+  __device__ static int64_t step() { return kWarp ? (int64_t)gridDim.x * kWarpRows : gridDim.x; }
+};
+
+template <typename T, int VEC, int NV, int WIDTH>
+__global__ __launch_bounds__(Team<WIDTH>::kThreads) void norm_fwd_kernel(
+    const __grid_constant__ NormFwd a, bool w_vec) {
+  using TM = Team<WIDTH>;
   __shared__ float red[2][32];
-  const int t = WARP ? threadIdx.x & 31 : threadIdx.x;
-  const int width = WARP ? 32 : blockDim.x;
-  const int64_t first = WARP ? (int64_t)blockIdx.x * kWarpRows + (threadIdx.x >> 5) : blockIdx.x;
-  const int64_t step = WARP ? (int64_t)gridDim.x * kWarpRows : gridDim.x;
+  const int t = TM::lane(), width = TM::width();
   const int blocks_per_row = (a.cols + kBlock - 1) / kBlock;
+  const int mine = a.cols - t * VEC;  // columns from this thread's first on
   float w[NV][VEC];
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = vec_col<VEC>(i, t, width);
-    load_weight<VEC>(a.w, a.w_bf16, w_vec, c, min(max(a.cols - c, 0), VEC), w[i]);
-  }
+  for (int i = 0; i < NV; ++i)
+    load_weight<VEC>(a.w, a.w_bf16, w_vec, (i * width + t) * VEC, mine - i * width * VEC, w[i]);
   int flip = 0;
-  for (int64_t row = first; row < a.rows; row += step) {
+  for (int64_t row = TM::first(); row < a.rows; row += TM::step()) {
     Raw<T, VEC> rx[NV], rr[NV];
-    const T* x = static_cast<const T*>(a.x) + row * a.ldx;
-    const T* res = static_cast<const T*>(a.res) + row * a.ldres;
+    const T* x = static_cast<const T*>(a.x) + row * a.ldx + t * VEC;
+    const T* res = static_cast<const T*>(a.res) + row * a.ldres + t * VEC;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = vec_col<VEC>(i, t, width);
-      rx[i] = load_raw<VEC>(x + c, a.cols - c);
-      rr[i] = load_raw<VEC>(res + c, a.res ? a.cols - c : 0);
+      rx[i] = load_raw<VEC>(x + i * width * VEC, mine - i * width * VEC);
+      rr[i] = load_raw<VEC>(res + i * width * VEC, a.res ? mine - i * width * VEC : 0);
     }
     float v[NV][VEC];
+    float ss = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       to_floats(rx[i], v[i]);
@@ -75,27 +85,34 @@ __global__ __launch_bounds__(WARP ? 32 * kWarpRows : 512) void norm_fwd_kernel(N
 #pragma unroll
         for (int j = 0; j < VEC; ++j) v[i][j] += r[j];
       }
-    }
-    float ss = 0.0f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
 #pragma unroll
       for (int j = 0; j < VEC; ++j) ss += v[i][j] * v[i][j];
-    ss = WARP ? warp_sum(ss) : block_sum(ss, red[flip]);
+    }
+    ss = TM::kWarp ? warp_sum(ss) : block_sum(ss, red[flip]);
     flip ^= 1;
     const float rstd = 1.0f / sqrtf(ss / (float)a.cols + a.eps);
     if (a.rstd && t == 0) a.rstd[row] = rstd;
+    if (a.h) {
+      T* h = static_cast<T*>(a.h) + row * a.ldh + t * VEC;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) store_part<VEC>(h + i * width * VEC, mine - i * width * VEC, v[i]);
+    }
+    T* y = static_cast<T*>(a.y) + row * a.ldy + t * VEC;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = vec_col<VEC>(i, t, width);
-      const int n = a.cols - c;
-      if (a.h) store_part<VEC>(static_cast<T*>(a.h) + row * a.ldh + c, n, v[i]);
 #pragma unroll
       for (int j = 0; j < VEC; ++j) v[i][j] = v[i][j] * rstd * w[i][j];
-      store_part<VEC>(static_cast<T*>(a.y) + row * a.ldy + c, n, v[i]);
-      if (a.q)
-        warp_pack<VEC>(v[i], n, a.q + row * a.ldq + c,
-                       a.scale + row * blocks_per_row + c / kBlock, n > 0 && c % kBlock == 0);
+      store_part<VEC>(y + i * width * VEC, mine - i * width * VEC, v[i]);
+    }
+    if (a.q) {
+      uint8_t* q = a.q + row * a.ldq + t * VEC;
+      uint8_t* scale = a.scale + row * blocks_per_row + t * VEC / kBlock;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int n = mine - i * width * VEC;
+        warp_pack<VEC>(v[i], n, q + i * width * VEC, scale + i * width * VEC / kBlock,
+                       n > 0 && t * VEC % kBlock == 0);
+      }
     }
   }
 }
@@ -137,90 +154,105 @@ __global__ __launch_bounds__(512) void norm_fwd_wide_kernel(NormFwd a) {
 
 // A thread keeps its columns' weight gradients in registers over all its rows;
 // one row of partial sums a block goes to a.partial, added up by sum_partials.
-template <typename T, int VEC, int NV, bool WARP>
-__global__ __launch_bounds__(WARP ? 32 * kWarpRows : 512) void norm_bwd_kernel(NormBwd a, bool w_vec) {
+// The next row's loads are in flight while this one is summed over the block.
+template <typename T, int VEC, int NV, int WIDTH>
+__global__ __launch_bounds__(Team<WIDTH>::kThreads) void norm_bwd_kernel(
+    const __grid_constant__ NormBwd a, bool w_vec) {
+  using TM = Team<WIDTH>;
   __shared__ float red[2][32];
-  __shared__ float cross[WARP ? kWarpRows * kWarpCols : 1];
-  const int t = WARP ? threadIdx.x & 31 : threadIdx.x;
-  const int width = WARP ? 32 : blockDim.x;
-  const int64_t first = WARP ? (int64_t)blockIdx.x * kWarpRows + (threadIdx.x >> 5) : blockIdx.x;
-  const int64_t step = WARP ? (int64_t)gridDim.x * kWarpRows : gridDim.x;
-  float acc[NV][VEC];
+  __shared__ float cross[TM::kWarp ? kWarpRows * kWarpColsBwd : 1];
+  const int t = TM::lane(), width = TM::width();
+  const int mine = a.cols - t * VEC;
+  // eight columns' weights stay in registers, more are read again every row
+  constexpr bool kHoldWeight = NV * VEC <= 8;
+  float acc[NV][VEC], held[kHoldWeight ? NV : 1][VEC];
 #pragma unroll
-  for (int i = 0; i < NV; ++i)
+  for (int i = 0; i < NV; ++i) {
+    if (kHoldWeight)
+      load_weight<VEC>(a.w, a.w_bf16, w_vec, (i * width + t) * VEC, mine - i * width * VEC, held[i % (kHoldWeight ? NV : 1)]);
 #pragma unroll
     for (int j = 0; j < VEC; ++j) acc[i][j] = 0.0f;
-  int flip = 0;
-  for (int64_t row = first; row < a.rows; row += step) {
-    const float rstd = a.rstd[row];
-    const T* dy = static_cast<const T*>(a.dy) + row * a.lddy;
-    const T* h = static_cast<const T*>(a.h) + row * a.ldh;
-    const T* dh = static_cast<const T*>(a.dh) + row * a.lddh;
-    Raw<T, VEC> rg[NV], rn[NV], rd[NV];
+  }
+  Raw<T, VEC> rg[NV], rn[NV], rd[NV];
+  float rstd = 0.0f;
+  auto load_row = [&](int64_t row) {
+    const T* dy = static_cast<const T*>(a.dy) + row * a.lddy + t * VEC;
+    const T* h = static_cast<const T*>(a.h) + row * a.ldh + t * VEC;
+    const T* dh = static_cast<const T*>(a.dh) + row * a.lddh + t * VEC;
+    rstd = a.rstd[row];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = vec_col<VEC>(i, t, width);
-      rg[i] = load_raw<VEC>(dy + c, a.cols - c);
-      rn[i] = load_raw<VEC>(h + c, a.cols - c);
-      rd[i] = load_raw<VEC>(dh + c, a.dh ? a.cols - c : 0);
+      const int n = mine - i * width * VEC;
+      rg[i] = load_raw<VEC>(dy + i * width * VEC, n);
+      rn[i] = load_raw<VEC>(h + i * width * VEC, n);
+      rd[i] = load_raw<VEC>(dh + i * width * VEC, a.dh ? n : 0);
     }
+  };
+  int flip = 0;
+  int64_t row = TM::first();
+  if (row < a.rows) load_row(row);
+  while (row < a.rows) {
+    const float r = rstd;
     float g[NV][VEC], n[NV][VEC];
+    Raw<T, VEC> d[NV];
     float s = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = vec_col<VEC>(i, t, width);
       to_floats(rg[i], g[i]);
       to_floats(rn[i], n[i]);
+      d[i] = rd[i];
+    }
+    const int64_t next = row + TM::step();
+    if (next < a.rows) load_row(next);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
       float w[VEC];
-      load_weight<VEC>(a.w, a.w_bf16, w_vec, c, min(max(a.cols - c, 0), VEC), w);
+      if (!kHoldWeight)
+        load_weight<VEC>(a.w, a.w_bf16, w_vec, (i * width + t) * VEC, mine - i * width * VEC, w);
 #pragma unroll
       for (int j = 0; j < VEC; ++j) {
-        n[i][j] *= rstd;
+        n[i][j] *= r;
         acc[i][j] += g[i][j] * n[i][j];
-        g[i][j] *= w[j];
+        g[i][j] *= kHoldWeight ? held[i % (kHoldWeight ? NV : 1)][j] : w[j];
         s += g[i][j] * n[i][j];
       }
     }
-    s = WARP ? warp_sum(s) : block_sum(s, red[flip]);
+    s = TM::kWarp ? warp_sum(s) : block_sum(s, red[flip]);
     flip ^= 1;
     const float mean = s / (float)a.cols;
+    T* dx = static_cast<T*>(a.dx) + row * a.lddx + t * VEC;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = vec_col<VEC>(i, t, width);
+      float add[VEC];
+      to_floats(d[i], add);
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) g[i][j] = rstd * (g[i][j] - n[i][j] * mean);
-      if (a.dh) {
-        float d[VEC];
-        to_floats(rd[i], d);
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) g[i][j] += d[j];
-      }
-      store_part<VEC>(static_cast<T*>(a.dx) + row * a.lddx + c, a.cols - c, g[i]);
+      for (int j = 0; j < VEC; ++j) g[i][j] = r * (g[i][j] - n[i][j] * mean) + (a.dh ? add[j] : 0.0f);
+      store_part<VEC>(dx + i * width * VEC, mine - i * width * VEC, g[i]);
     }
+    row = next;
   }
   if (!a.dw) return;
   float* out = a.partial + (int64_t)blockIdx.x * a.cols;
-  if constexpr (WARP) {
+  if constexpr (TM::kWarp) {
     // the block's warps hold the same columns: add them up in warp order
-    float* mine = cross + (threadIdx.x >> 5) * kWarpCols;
+    float* own = cross + (threadIdx.x >> 5) * kWarpColsBwd;
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) mine[vec_col<VEC>(i, t, 32) + j] = acc[i][j];
+      for (int j = 0; j < VEC; ++j) own[(i * 32 + t) * VEC + j] = acc[i][j];
     __syncthreads();
     for (int c = threadIdx.x; c < a.cols; c += blockDim.x) {
       float s = 0.0f;
 #pragma unroll
-      for (int k = 0; k < kWarpRows; ++k) s += cross[k * kWarpCols + c];
+      for (int k = 0; k < kWarpRows; ++k) s += cross[k * kWarpColsBwd + c];
       out[c] = s;
     }
   } else {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = vec_col<VEC>(i, t, width);
 #pragma unroll
       for (int j = 0; j < VEC; ++j)
-        if (c + j < a.cols) out[c + j] = acc[i][j];
+        if (i * width * VEC + j < mine) out[(i * width + t) * VEC + j] = acc[i][j];
     }
   }
 }
@@ -264,87 +296,162 @@ __global__ __launch_bounds__(256) void norm_dw_wide_kernel(NormBwd a) {
   a.partial[(int64_t)blockIdx.y * a.cols + c] = s;
 }
 
-// Column sums: a block takes 64 columns (two a thread) and every gridDim.y-th
-// group of 8 rows.
+// Column sums in one launch: a cluster of kSumBlocks blocks shares kSumCols
+// columns, each block taking its share of the rows; the parts meet in the first
+// block's shared memory, in block order.
 constexpr int kSumCols = 64;
-__global__ __launch_bounds__(256) void colsum_kernel(const bf16* m, int64_t ld, int64_t rows,
-                                                     int64_t cols, float* partial) {
-  __shared__ float part[8][kSumCols];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t c = (int64_t)blockIdx.x * kSumCols + lane;
-  float s0 = 0.0f, s1 = 0.0f;
-  for (int64_t r = (int64_t)blockIdx.y * 8 + warp; r < rows; r += (int64_t)gridDim.y * 8) {
-    if (c < cols) s0 += __bfloat162float(m[r * ld + c]);
-    if (c + 32 < cols) s1 += __bfloat162float(m[r * ld + c + 32]);
-  }
-  part[warp][lane] = s0;
-  part[warp][lane + 32] = s1;
-  __syncthreads();
-  if (threadIdx.x < kSumCols) {
-    const int64_t o = (int64_t)blockIdx.x * kSumCols + threadIdx.x;
-    float s = 0.0f;
+constexpr int kSumBlocks = 8;
+constexpr int kSumThreads = 512;
+
+template <int VEC>
+__global__ __launch_bounds__(kSumThreads) __cluster_dims__(kSumBlocks, 1, 1) void colsum_kernel(
+    const bf16* m, int64_t ld, int64_t rows, int64_t cols, void* out, int out_bf16) {
+  // VEC 8: eight threads a row, VEC 1: 64
+  constexpr int kPerRow = kSumCols / VEC, kRows = kSumThreads / kPerRow;
+  __shared__ float part[kRows][kSumCols + 4];
+  __shared__ float sums[kSumBlocks][kSumCols];
+  uint32_t rank;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+  const int at = threadIdx.x % kPerRow, r0 = threadIdx.x / kPerRow;
+  const int64_t c = (int64_t)(blockIdx.x / kSumBlocks) * kSumCols + at * VEC;
+  const int n = (int)min((int64_t)VEC, cols - c);
+  const int64_t begin = rows * rank / kSumBlocks, end = rows * (rank + 1) / kSumBlocks;
+  float s[VEC];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) s += part[k][threadIdx.x];
-    if (o < cols) partial[(int64_t)blockIdx.y * cols + o] = s;
+  for (int j = 0; j < VEC; ++j) s[j] = 0.0f;
+  constexpr int kUnroll = 4;
+  for (int64_t r = begin + r0; r < end; r += kRows * kUnroll) {
+    Raw<bf16, VEC> v[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u)
+      v[u] = load_raw<VEC>(m + (r + u * kRows) * ld + c, r + u * kRows < end ? n : 0);
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      float f[VEC];
+      to_floats(v[u], f);
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) s[j] += f[j];
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < VEC; ++j) part[r0][at * VEC + j] = s[j];
+  __syncthreads();
+  // to the first block: kSumCols sums of this one
+  if (threadIdx.x < kSumCols) {
+    float t = 0.0f;
+#pragma unroll 8
+    for (int k = 0; k < kRows; ++k) t += part[k][threadIdx.x];
+    uint32_t to = (uint32_t)__cvta_generic_to_shared(&sums[rank][threadIdx.x]);
+    asm volatile("mapa.shared::cluster.u32 %0, %0, %1;" : "+r"(to) : "r"(0));
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to), "f"(t) : "memory");
+  }
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                   : "memory");
+  if (rank == 0 && threadIdx.x < kSumCols) {
+    const int64_t o = (int64_t)(blockIdx.x / kSumBlocks) * kSumCols + threadIdx.x;
+    float t = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kSumBlocks; ++k) t += sums[k][threadIdx.x];
+    if (o < cols) {
+      if (out_bf16)
+        static_cast<bf16*>(out)[o] = __float2bfloat16_rn(t);
+      else
+        static_cast<float*>(out)[o] = t;
+    }
   }
 }
 
-// 32 columns a block, 8 warps over the rows of partial sums.
-__global__ __launch_bounds__(256) void sum_partials_kernel(const float* partial, int64_t parts,
-                                                           int64_t cols, void* out, int out_bf16) {
-  __shared__ float part[8][32];
+// 32 columns a block, 32 warps over the rows of partial sums.
+__global__ __launch_bounds__(1024) void sum_partials_kernel(const float* partial, int64_t parts,
+                                                            int64_t cols, void* out, int out_bf16) {
+  __shared__ float part[32][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t c = (int64_t)blockIdx.x * 32 + lane;
   float s = 0.0f;
-  if (c < cols)
-    for (int64_t p = warp; p < parts; p += 8) s += partial[p * cols + c];
+  if (c < cols) {
+    constexpr int kUnroll = 8;
+    for (int64_t p = warp; p < parts; p += 32 * kUnroll) {
+      float v[kUnroll];
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) v[u] = p + u * 32 < parts ? partial[(p + u * 32) * cols + c] : 0.0f;
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) s += v[u];
+    }
+  }
   part[warp][lane] = s;
   __syncthreads();
-  if (warp == 0 && c < cols) {
-    float r = 0.0f;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) r += part[k][lane];
+  // warp w sums the 32 parts of column w
+  const float r = warp_sum(part[lane][warp]);
+  const int64_t o = (int64_t)blockIdx.x * 32 + warp;
+  if (lane == 0 && o < cols) {
     if (out_bf16)
-      static_cast<bf16*>(out)[c] = __float2bfloat16_rn(r);
+      static_cast<bf16*>(out)[o] = __float2bfloat16_rn(r);
     else
-      static_cast<float*>(out)[c] = r;
+      static_cast<float*>(out)[o] = r;
   }
 }
 
 // Launch shape of a row kernel: warps own rows up to kWarpCols, blocks above.
+// Eight columns a thread need a block as wide as the row; single columns (rows
+// of any alignment) need a width known to the compiler, so that a thread's
+// addresses are one register and constants (777 x 1283 float32 with the 8-bit
+// output: 10.8 us with the width in a register).
 struct Shape {
-  bool warp;
-  int nv;  // vectors of 8 a thread
+  int nv;     // vectors of 8 (or their 8 single columns) a thread
+  int width;  // threads a row
   int threads;
   unsigned grid;
 };
-Shape shape_of(int64_t rows, int64_t cols, int blocks_per_sm) {
+Shape shape_of(int64_t rows, int64_t cols, bool vec, int warp_cols, int blocks_per_sm) {
   Shape s;
-  s.warp = cols <= kWarpCols;
-  if (s.warp) {
+  const int64_t most = (int64_t)sm_count() * blocks_per_sm;
+  if (cols <= warp_cols) {
     s.nv = cols <= 256 ? 1 : cols <= 512 ? 2 : 4;
+    s.width = 32;
     s.threads = 32 * kWarpRows;
-    s.grid = (unsigned)std::min<int64_t>(ceil_div(rows, kWarpRows), (int64_t)sm_count() * blocks_per_sm);
+    s.grid = (unsigned)std::min(ceil_div(rows, kWarpRows), most);
   } else {
-    s.nv = cols <= 2048 ? 1 : 2;
-    s.threads = (int)(ceil_div(ceil_div(cols, 8 * s.nv), 32) * 32);
-    s.grid = (unsigned)std::min<int64_t>(rows, (int64_t)sm_count() * blocks_per_sm);
+    s.nv = cols <= (vec ? 2048 : 4096) ? 1 : 2;
+    s.threads = vec ? (int)(ceil_div(ceil_div(cols, 8 * s.nv), 32) * 32) : cols <= 1024 ? 128 : cols <= 2048 ? 256 : 512;
+    s.width = vec ? 0 : s.threads;
+    s.grid = (unsigned)std::min(rows, most);
   }
   return s;
 }
 
-// Runs CALL with NV and WARP as constants for a shape (NV counts vectors of
-// 8 values, so a VEC 1 kernel has 8 NV of them).
-#define SCAPE_SHAPE_SWITCH(s, CALL)                                        \
-  if (s.warp) {                                                            \
-    constexpr bool WARP = true;                                            \
-    if (s.nv == 1) { constexpr int NV = 1; CALL; }                         \
-    else if (s.nv == 2) { constexpr int NV = 2; CALL; }                    \
-    else { constexpr int NV = 4; CALL; }                                   \
-  } else {                                                                 \
-    constexpr bool WARP = false;                                           \
-    if (s.nv == 1) { constexpr int NV = 1; CALL; }                         \
-    else { constexpr int NV = 2; CALL; }                                   \
+// Runs CALL with VEC, NV and WIDTH as constants for a shape (rows of up to
+// WARP_COLS columns belong to a warp).
+#define SCAPE_SHAPE_SWITCH(vec, s, WARP_COLS, CALL)                                         \
+  if (vec) {                                                                                \
+    constexpr int VEC = 8;                                                                  \
+    if (s.width == 32) {                                                                    \
+      constexpr int WIDTH = 32;                                                             \
+      if (s.nv == 1) { constexpr int NV = 1; CALL; }                                        \
+      else if (s.nv == 2) { constexpr int NV = 2; CALL; }                                   \
+      else { constexpr int NV = WARP_COLS / 256; CALL; }                                    \
+    } else {                                                                                \
+      constexpr int WIDTH = 0;                                                              \
+      if (s.nv == 1) { constexpr int NV = 1; CALL; }                                        \
+      else { constexpr int NV = 2; CALL; }                                                  \
+    }                                                                                       \
+  } else {                                                                                  \
+    constexpr int VEC = 1;                                                                  \
+    if (s.width == 32) {                                                                    \
+      constexpr int WIDTH = 32;                                                             \
+      if (s.nv == 1) { constexpr int NV = 8; CALL; }                                        \
+      else if (s.nv == 2) { constexpr int NV = 16; CALL; }                                  \
+      else { constexpr int NV = WARP_COLS / 32; CALL; }                                     \
+    } else if (s.width == 128) {                                                            \
+      constexpr int WIDTH = 128, NV = 8;                                                    \
+      CALL;                                                                                 \
+    } else if (s.width == 256) {                                                            \
+      constexpr int WIDTH = 256, NV = 8;                                                    \
+      CALL;                                                                                 \
+    } else {                                                                                \
+      constexpr int WIDTH = 512;                                                            \
+      if (s.nv == 1) { constexpr int NV = 8; CALL; }                                        \
+      else { constexpr int NV = 16; CALL; }                                                 \
+    }                                                                                       \
   }
 
 constexpr int kFwdBlocksPerSm = 8;
@@ -356,16 +463,12 @@ cudaError_t run_norm_fwd(const NormFwd& a, cudaStream_t st) {
     norm_fwd_wide_kernel<T><<<(unsigned)std::min<int64_t>(a.rows, (int64_t)sm_count() * 4), 512, 0, st>>>(a);
     return cudaGetLastError();
   }
-  const Shape s = shape_of(a.rows, a.cols, kFwdBlocksPerSm);
   const size_t e = sizeof(T);
   const bool vec = rows16(a.x, a.ldx, e) && rows16(a.res, a.ldres, e) && rows16(a.y, a.ldy, e) &&
                    rows16(a.h, a.ldh, e) && rows8(a.q, a.ldq);
   const bool wv = aligned(a.w, 16);
-  if (vec) {
-    SCAPE_SHAPE_SWITCH(s, (norm_fwd_kernel<T, 8, NV, WARP><<<s.grid, s.threads, 0, st>>>(a, wv)));
-  } else {
-    SCAPE_SHAPE_SWITCH(s, (norm_fwd_kernel<T, 1, NV * 8, WARP><<<s.grid, s.threads, 0, st>>>(a, wv)));
-  }
+  const Shape s = shape_of(a.rows, a.cols, vec, kWarpCols, kFwdBlocksPerSm);
+  SCAPE_SHAPE_SWITCH(vec, s, kWarpCols, (norm_fwd_kernel<T, VEC, NV, WIDTH><<<s.grid, s.threads, 0, st>>>(a, wv)));
   return cudaGetLastError();
 }
 
@@ -380,16 +483,12 @@ cudaError_t run_norm_bwd(const NormBwd& a, cudaStream_t st) {
     }
     norm_bwd_wide_kernel<T><<<(unsigned)std::min<int64_t>(a.rows, (int64_t)sm_count() * 4), 512, 0, st>>>(a);
   } else {
-    const Shape s = shape_of(a.rows, a.cols, kBwdBlocksPerSm);
     const size_t e = sizeof(T);
     const bool vec = rows16(a.dy, a.lddy, e) && rows16(a.h, a.ldh, e) &&
                      rows16(a.dh, a.lddh, e) && rows16(a.dx, a.lddx, e);
     const bool wv = aligned(a.w, 16);
-    if (vec) {
-      SCAPE_SHAPE_SWITCH(s, (norm_bwd_kernel<T, 8, NV, WARP><<<s.grid, s.threads, 0, st>>>(a, wv)));
-    } else {
-      SCAPE_SHAPE_SWITCH(s, (norm_bwd_kernel<T, 1, NV * 8, WARP><<<s.grid, s.threads, 0, st>>>(a, wv)));
-    }
+    const Shape s = shape_of(a.rows, a.cols, vec, kWarpColsBwd, kBwdBlocksPerSm);
+    SCAPE_SHAPE_SWITCH(vec, s, kWarpColsBwd, (norm_bwd_kernel<T, VEC, NV, WIDTH><<<s.grid, s.threads, 0, st>>>(a, wv)));
   }
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !a.dw) return e;
@@ -403,29 +502,24 @@ cudaError_t launch_norm_fwd(const NormFwd& a, int dtype, cudaStream_t st) {
 }
 int64_t norm_bwd_partials(int64_t rows, int64_t cols) {
   if (cols > kBlockCols) return std::min<int64_t>(ceil_div(rows, 8), 64);
-  return shape_of(rows, cols, kBwdBlocksPerSm).grid;
+  return shape_of(rows, cols, true, kWarpColsBwd, kBwdBlocksPerSm).grid;  // the grid does not go by `vec`
 }
 cudaError_t launch_norm_bwd(const NormBwd& a, int dtype, cudaStream_t st) {
   return dtype == SCAPE_BF16 ? run_norm_bwd<bf16>(a, st) : run_norm_bwd<float>(a, st);
 }
 
-int64_t colsum_partials(int64_t rows, int64_t cols) {
-  const int64_t across = ceil_div(cols, kSumCols);
-  const int64_t want = std::max<int64_t>(1, (int64_t)sm_count() * 8 / across);
-  return std::max<int64_t>(1, std::min(want, ceil_div(rows, 32)));
-}
-cudaError_t launch_colsum(const bf16* m, int64_t ld, int64_t rows, int64_t cols, float* partial,
-                          void* out, int out_bf16, cudaStream_t st) {
-  const int64_t parts = colsum_partials(rows, cols);
-  colsum_kernel<<<dim3((unsigned)ceil_div(cols, kSumCols), (unsigned)parts), 256, 0, st>>>(
-      m, ld, rows, cols, partial);
-  const cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  return launch_sum_partials(partial, parts, cols, out, out_bf16, st);
+cudaError_t launch_colsum(const bf16* m, int64_t ld, int64_t rows, int64_t cols, void* out,
+                          int out_bf16, cudaStream_t st) {
+  const unsigned grid = (unsigned)ceil_div(cols, kSumCols) * kSumBlocks;
+  if (rows16(m, ld, 2))
+    colsum_kernel<8><<<grid, kSumThreads, 0, st>>>(m, ld, rows, cols, out, out_bf16);
+  else
+    colsum_kernel<1><<<grid, kSumThreads, 0, st>>>(m, ld, rows, cols, out, out_bf16);
+  return cudaGetLastError();
 }
 cudaError_t launch_sum_partials(const float* partial, int64_t parts, int64_t cols, void* out,
                                 int out_bf16, cudaStream_t st) {
-  sum_partials_kernel<<<(unsigned)ceil_div(cols, 32), 256, 0, st>>>(partial, parts, cols, out, out_bf16);
+  sum_partials_kernel<<<(unsigned)ceil_div(cols, 32), 1024, 0, st>>>(partial, parts, cols, out, out_bf16);
   return cudaGetLastError();
 }
 
