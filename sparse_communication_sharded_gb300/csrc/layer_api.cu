@@ -260,7 +260,7 @@ extern "C" int scape_layer_add_rmsnorm(const void* x, int64_t ldx, const void* r
   a.ldx = ldx, a.ldres = ldres, a.ldy = ldy, a.ldh = ldh, a.ldq = ldq;
   a.w_bf16 = weight_dtype == SCAPE_BF16;
   a.rows = rows, a.cols = (int)cols, a.eps = eps;
-  a.y = y, a.h = h, a.rstd = rstd, a.q = q, a.scale = scale;
+  a.y = y, a.h = h, a.rstd = rstd, a.q = q, a.scale = scale, a.q16 = false;
   return cuda_result(launch_norm_fwd(a, dtype, static_cast<cudaStream_t>(stream)),
                      "scape_layer_add_rmsnorm");
 }

@@ -74,7 +74,7 @@ __global__ __launch_bounds__(kThreads) void pack8_kernel(const T* x, int64_t ldx
     to_floats(raw[i], v);
     warp_pack<VEC>(v, u.n, q + u.row * ldq + u.col,
                    scale + u.row * blocks_per_row + u.col / kBlock,
-                   u.n > 0 && u.col % kBlock == 0);
+                   u.n > 0 && u.col % kBlock == 0, VEC == 16);
   }
 }
 

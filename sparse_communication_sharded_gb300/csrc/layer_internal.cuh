@@ -247,10 +247,11 @@ __device__ __forceinline__ void e4m3_pairs(uint32_t w, uint64_t& lo, uint64_t& h
 }
 // One warp's 32 lanes pack VEC values each; with VEC 16 two neighbouring lanes
 // hold a block, with VEC 8 four, with VEC 1 the whole warp.  n values of the thread are
-// real (the others are 0).  All 32 lanes call it together.
+// real (the others are 0).  q is on 8 bytes, or 16 where q16 says so (VEC 1: any).
+// All 32 lanes call it together.
 template <int VEC>
 __device__ __forceinline__ void warp_pack(const float (&v)[VEC], int n, uint8_t* q, uint8_t* scale,
-                                          bool writes_scale) {
+                                          bool writes_scale, bool q16) {
   uint32_t top = part_top<VEC>(v);
   bool no_inf = true;
   if constexpr (VEC == 1) {
@@ -280,10 +281,16 @@ __device__ __forceinline__ void warp_pack(const float (&v)[VEC], int n, uint8_t*
     uint32_t w[VEC / 4];
     to_e4m3<VEC>(v, inv, no_inf, w);
     if (n >= VEC) {
-      if constexpr (VEC == 16)
-        *reinterpret_cast<uint4*>(q) = make_uint4(w[0], w[1], w[2], w[3]);
-      else
+      if constexpr (VEC == 16) {
+        if (q16) {
+          *reinterpret_cast<uint4*>(q) = make_uint4(w[0], w[1], w[2], w[3]);
+        } else {
+          reinterpret_cast<uint2*>(q)[0] = make_uint2(w[0], w[1]);
+          reinterpret_cast<uint2*>(q)[1] = make_uint2(w[2], w[3]);
+        }
+      } else {
         *reinterpret_cast<uint2*>(q) = make_uint2(w[0], w[1]);
+      }
     } else {
 #pragma unroll
       for (int i = 0; i < VEC; ++i)
@@ -480,6 +487,7 @@ struct NormFwd {
   void *y, *h;
   float* rstd;
   uint8_t *q, *scale;
+  bool q16;  // rows of q on 16 bytes
 };
 cudaError_t launch_norm_fwd(const NormFwd& a, int dtype, cudaStream_t st);
 

@@ -2,11 +2,15 @@
 //
 // Bound by memory: a row's inputs are read once into registers, the sum of
 // squares (or of gradient products) is taken over the warps that hold the row,
-// and the outputs are written from the same registers.
+// and the outputs are written from the same registers.  What stands between that
+// and the copy rate is the work a row costs each thread whatever its width (the
+// sum over the block, addresses), so a thread takes 16 columns and works on pairs
+// (8 columns and single floats: 33 instructions a value, 13.4 us for 4096 x 1280
+// with all outputs).
 //
-// A row of up to 1024 columns (backward 512) belongs to one warp (no block barrier), a
-// wider one to a block that is as wide as the row needs; rows over kBlockCols
-// are read twice by the *_wide kernels.
+// A row of up to 1024 columns (backward 512) belongs to one warp (no block
+// barrier), a wider one to a block that is as wide as the row needs; rows over
+// kBlockCols are read twice by the *_wide kernels.
 #include <algorithm>
 
 #include "layer_internal.cuh"
@@ -25,15 +29,67 @@ __device__ __forceinline__ float warp_sum(float v) {
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
   return v;
 }
-// Sum over the block, the same bits in every thread.  `red` holds 32 floats of
+// Sum over the block, the same bits in every thread.  `red` holds 16 floats of
 // this call's own: the next call uses another one, so one barrier will do.
 __device__ __forceinline__ float block_sum(float v, float* red) {
   v = warp_sum(v);
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
   __syncthreads();
   const int warps = blockDim.x >> 5;
-  float s = (int)(threadIdx.x & 31) < warps ? red[threadIdx.x & 31] : 0.0f;
-  return warp_sum(s);
+  float s = 0.0f;
+  for (int i = 0; i < warps; i += 4) {  // unused places hold 0
+    const float4 r = *reinterpret_cast<const float4*>(red + i);
+    s += (r.x + r.y) + (r.z + r.w);
+  }
+  return s;
+}
+__device__ __forceinline__ void clear_sums(float (*red)[16]) {
+  if (threadIdx.x < 32) red[threadIdx.x >> 4][threadIdx.x & 15] = 0.0f;
+  __syncthreads();
+}
+// 1 / sqrt(x): the hardware's estimate and one Newton step.
+__device__ __forceinline__ float inverse_root(float x) {
+  const float r = rsqrtf(x);
+  return isinf(r) || r == 0.0f ? r : r * fmaf(-0.5f * x * r, r, 1.5f);
+}
+
+// A thread's NV vectors as pairs of floats: pair k holds its values 2k, 2k + 1.
+template <typename T, int VEC, int NV>
+__device__ __forceinline__ uint64_t raw_pair(const Raw<T, VEC> (&r)[NV], int k) {
+  if constexpr (VEC == 1) {
+    float a[1], b[1];
+    to_floats(r[2 * k], a);
+    to_floats(r[2 * k + 1], b);
+    return pair(a[0], b[0]);
+  } else if constexpr (sizeof(T) == 2) {
+    const uint32_t w = r[2 * k / VEC].w[k % (VEC / 2)];
+    return pair(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+  } else {
+    const uint32_t* w = &r[2 * k / VEC].w[2 * k % VEC];
+    return pair(__uint_as_float(w[0]), __uint_as_float(w[1]));
+  }
+}
+template <int VEC, int NV>
+__device__ __forceinline__ void load_weights(uint64_t (&w)[NV * VEC / 2], const void* p, int is_bf16,
+                                             bool aligned, int t, int width, int mine) {
+  float f[NV][VEC];
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+    load_weight<VEC>(p, is_bf16, aligned, (i * width + t) * VEC, mine - i * width * VEC, f[i]);
+#pragma unroll
+  for (int k = 0; k < NV * VEC / 2; ++k)
+    w[k] = pair(f[2 * k / VEC][2 * k % VEC], f[(2 * k + 1) / VEC][(2 * k + 1) % VEC]);
+}
+template <int VEC, int NV>
+__device__ __forceinline__ void split_pairs(const uint64_t (&p)[NV * VEC / 2], float (&v)[NV][VEC]) {
+#pragma unroll
+  for (int k = 0; k < NV * VEC / 2; ++k)
+    unpair(p[k], v[2 * k / VEC][2 * k % VEC], v[(2 * k + 1) / VEC][(2 * k + 1) % VEC]);
+}
+__device__ __forceinline__ float pair_sum(uint64_t p) {
+  float a, b;
+  unpair(p, a, b);
+  return a + b;
 }
 
 // Vector i of thread t of `width` covers columns (i * width + t) * VEC and on.
@@ -54,16 +110,16 @@ struct Team {
 
 template <typename T, int VEC, int NV, int WIDTH>
 __global__ __launch_bounds__(Team<WIDTH>::kThreads) void norm_fwd_kernel(
-    const __grid_constant__ NormFwd a, bool w_vec) {
+    const __grid_constant__ NormFwd a, bool w_vec, float inv_cols) {
   using TM = Team<WIDTH>;
-  __shared__ float red[2][32];
+  constexpr int P = NV * VEC / 2;
+  __shared__ __align__(16) float red[2][16];
+  if (!TM::kWarp) clear_sums(red);
   const int t = TM::lane(), width = TM::width();
   const int blocks_per_row = (a.cols + kBlock - 1) / kBlock;
   const int mine = a.cols - t * VEC;  // columns from this thread's first on
-  float w[NV][VEC];
-#pragma unroll
-  for (int i = 0; i < NV; ++i)
-    load_weight<VEC>(a.w, a.w_bf16, w_vec, (i * width + t) * VEC, mine - i * width * VEC, w[i]);
+  uint64_t w[P];
+  load_weights<VEC, NV>(w, a.w, a.w_bf16, w_vec, t, width, mine);
   int flip = 0;
   for (int64_t row = TM::first(); row < a.rows; row += TM::step()) {
     Raw<T, VEC> rx[NV], rr[NV];
@@ -72,46 +128,41 @@ __global__ __launch_bounds__(Team<WIDTH>::kThreads) void norm_fwd_kernel(
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       rx[i] = load_raw<VEC>(x + i * width * VEC, mine - i * width * VEC);
-      rr[i] = load_raw<VEC>(res + i * width * VEC, a.res ? mine - i * width * VEC : 0);
+      if (a.res) rr[i] = load_raw<VEC>(res + i * width * VEC, mine - i * width * VEC);
     }
-    float v[NV][VEC];
-    float ss = 0.0f;
+    uint64_t v[P], sum = pair(0.0f, 0.0f);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      to_floats(rx[i], v[i]);
-      if (a.res) {
-        float r[VEC];
-        to_floats(rr[i], r);
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) v[i][j] += r[j];
-      }
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) ss += v[i][j] * v[i][j];
+    for (int k = 0; k < P; ++k) {
+      v[k] = raw_pair(rx, k);
+      if (a.res) v[k] = add2(v[k], raw_pair(rr, k));
+      sum = fma2(v[k], v[k], sum);
     }
+    float ss = pair_sum(sum);
     ss = TM::kWarp ? warp_sum(ss) : block_sum(ss, red[flip]);
     flip ^= 1;
-    const float rstd = 1.0f / sqrtf(ss / (float)a.cols + a.eps);
+    const float rstd = inverse_root(fmaf(ss, inv_cols, a.eps));
     if (a.rstd && t == 0) a.rstd[row] = rstd;
+    float f[NV][VEC];
     if (a.h) {
       T* h = static_cast<T*>(a.h) + row * a.ldh + t * VEC;
+      split_pairs<VEC, NV>(v, f);
 #pragma unroll
-      for (int i = 0; i < NV; ++i) store_part<VEC>(h + i * width * VEC, mine - i * width * VEC, v[i]);
+      for (int i = 0; i < NV; ++i) store_part<VEC>(h + i * width * VEC, mine - i * width * VEC, f[i]);
     }
+#pragma unroll
+    for (int k = 0; k < P; ++k) v[k] = mul2(mul2(v[k], pair(rstd, rstd)), w[k]);
+    split_pairs<VEC, NV>(v, f);
     T* y = static_cast<T*>(a.y) + row * a.ldy + t * VEC;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) v[i][j] = v[i][j] * rstd * w[i][j];
-      store_part<VEC>(y + i * width * VEC, mine - i * width * VEC, v[i]);
-    }
+    for (int i = 0; i < NV; ++i) store_part<VEC>(y + i * width * VEC, mine - i * width * VEC, f[i]);
     if (a.q) {
       uint8_t* q = a.q + row * a.ldq + t * VEC;
       uint8_t* scale = a.scale + row * blocks_per_row + t * VEC / kBlock;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int n = mine - i * width * VEC;
-        warp_pack<VEC>(v[i], n, q + i * width * VEC, scale + i * width * VEC / kBlock,
-                       n > 0 && t * VEC % kBlock == 0);
+        warp_pack<VEC>(f[i], n, q + i * width * VEC, scale + i * width * VEC / kBlock,
+                       n > 0 && t * VEC % kBlock == 0, a.q16);
       }
     }
   }
@@ -120,7 +171,8 @@ __global__ __launch_bounds__(Team<WIDTH>::kThreads) void norm_fwd_kernel(
 // Any width: the row is read a second time (from the caches) for the outputs.
 template <typename T>
 __global__ __launch_bounds__(512) void norm_fwd_wide_kernel(NormFwd a) {
-  __shared__ float red[2][32];
+  __shared__ __align__(16) float red[2][16];
+  clear_sums(red);
   const int64_t blocks_per_row = (a.cols + kBlock - 1) / kBlock;
   int flip = 0;
   for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
@@ -133,7 +185,7 @@ __global__ __launch_bounds__(512) void norm_fwd_wide_kernel(NormFwd a) {
     }
     ss = block_sum(ss, red[flip]);
     flip ^= 1;
-    const float rstd = 1.0f / sqrtf(ss / (float)a.cols + a.eps);
+    const float rstd = inverse_root(ss / (float)a.cols + a.eps);
     if (a.rstd && threadIdx.x == 0) a.rstd[row] = rstd;
     for (int c0 = 0; c0 < a.cols; c0 += blockDim.x) {
       const int c = c0 + threadIdx.x, n = a.cols - c;
@@ -147,7 +199,7 @@ __global__ __launch_bounds__(512) void norm_fwd_wide_kernel(NormFwd a) {
       }
       if (a.q)
         warp_pack<1>(v, n, a.q + row * a.ldq + c, a.scale + row * blocks_per_row + c / kBlock,
-                     n > 0 && c % kBlock == 0);
+                     n > 0 && c % kBlock == 0, false);
     }
   }
 }
@@ -156,23 +208,19 @@ __global__ __launch_bounds__(512) void norm_fwd_wide_kernel(NormFwd a) {
 // one row of partial sums a block goes to a.partial, added up by sum_partials.
 // The next row's loads are in flight while this one is summed over the block.
 template <typename T, int VEC, int NV, int WIDTH>
-__global__ __launch_bounds__(Team<WIDTH>::kThreads) void norm_bwd_kernel(
-    const __grid_constant__ NormBwd a, bool w_vec) {
+__global__ __launch_bounds__(Team<WIDTH>::kThreads, (VEC == 8 && sizeof(T) == 2 && NV == 1 ? 1024 : 512) / Team<WIDTH>::kThreads) void norm_bwd_kernel(
+    const __grid_constant__ NormBwd a, bool w_vec, float inv_cols) {
   using TM = Team<WIDTH>;
-  __shared__ float red[2][32];
+  constexpr int P = NV * VEC / 2;
+  __shared__ __align__(16) float red[2][16];
   __shared__ float cross[TM::kWarp ? kWarpRows * kWarpColsBwd : 1];
+  if (!TM::kWarp) clear_sums(red);
   const int t = TM::lane(), width = TM::width();
   const int mine = a.cols - t * VEC;
-  // eight columns' weights stay in registers, more are read again every row
-  constexpr bool kHoldWeight = NV * VEC <= 8;
-  float acc[NV][VEC], held[kHoldWeight ? NV : 1][VEC];
+  uint64_t acc[P], w[P];
+  load_weights<VEC, NV>(w, a.w, a.w_bf16, w_vec, t, width, mine);
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    if (kHoldWeight)
-      load_weight<VEC>(a.w, a.w_bf16, w_vec, (i * width + t) * VEC, mine - i * width * VEC, held[i % (kHoldWeight ? NV : 1)]);
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) acc[i][j] = 0.0f;
-  }
+  for (int k = 0; k < P; ++k) acc[k] = pair(0.0f, 0.0f);
   Raw<T, VEC> rg[NV], rn[NV], rd[NV];
   float rstd = 0.0f;
   auto load_row = [&](int64_t row) {
@@ -185,53 +233,50 @@ __global__ __launch_bounds__(Team<WIDTH>::kThreads) void norm_bwd_kernel(
       const int n = mine - i * width * VEC;
       rg[i] = load_raw<VEC>(dy + i * width * VEC, n);
       rn[i] = load_raw<VEC>(h + i * width * VEC, n);
-      rd[i] = load_raw<VEC>(dh + i * width * VEC, a.dh ? n : 0);
+      if (a.dh) rd[i] = load_raw<VEC>(dh + i * width * VEC, n);
     }
   };
   int flip = 0;
   int64_t row = TM::first();
   if (row < a.rows) load_row(row);
   while (row < a.rows) {
-    const float r = rstd;
-    float g[NV][VEC], n[NV][VEC];
+    const uint64_t r2 = pair(rstd, rstd);
+    uint64_t g[P], n[P], sum = pair(0.0f, 0.0f);
     Raw<T, VEC> d[NV];
-    float s = 0.0f;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      to_floats(rg[i], g[i]);
-      to_floats(rn[i], n[i]);
-      d[i] = rd[i];
+    for (int k = 0; k < P; ++k) {
+      g[k] = raw_pair(rg, k);
+      n[k] = mul2(raw_pair(rn, k), r2);
     }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) d[i] = rd[i];
     const int64_t next = row + TM::step();
     if (next < a.rows) load_row(next);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      float w[VEC];
-      if (!kHoldWeight)
-        load_weight<VEC>(a.w, a.w_bf16, w_vec, (i * width + t) * VEC, mine - i * width * VEC, w);
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        n[i][j] *= r;
-        acc[i][j] += g[i][j] * n[i][j];
-        g[i][j] *= kHoldWeight ? held[i % (kHoldWeight ? NV : 1)][j] : w[j];
-        s += g[i][j] * n[i][j];
-      }
+    for (int k = 0; k < P; ++k) {
+      acc[k] = fma2(g[k], n[k], acc[k]);
+      g[k] = mul2(g[k], w[k]);
+      sum = fma2(g[k], n[k], sum);
     }
+    float s = pair_sum(sum);
     s = TM::kWarp ? warp_sum(s) : block_sum(s, red[flip]);
     flip ^= 1;
-    const float mean = s / (float)a.cols;
+    const uint64_t mean = pair(-s * inv_cols, -s * inv_cols);
+#pragma unroll
+    for (int k = 0; k < P; ++k) {
+      g[k] = fma2(n[k], mean, g[k]);
+      g[k] = a.dh ? fma2(g[k], r2, raw_pair(d, k)) : mul2(g[k], r2);
+    }
+    float f[NV][VEC];
+    split_pairs<VEC, NV>(g, f);
     T* dx = static_cast<T*>(a.dx) + row * a.lddx + t * VEC;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      float add[VEC];
-      to_floats(d[i], add);
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) g[i][j] = r * (g[i][j] - n[i][j] * mean) + (a.dh ? add[j] : 0.0f);
-      store_part<VEC>(dx + i * width * VEC, mine - i * width * VEC, g[i]);
-    }
+    for (int i = 0; i < NV; ++i) store_part<VEC>(dx + i * width * VEC, mine - i * width * VEC, f[i]);
     row = next;
   }
   if (!a.dw) return;
+  float f[NV][VEC];
+  split_pairs<VEC, NV>(acc, f);
   float* out = a.partial + (int64_t)blockIdx.x * a.cols;
   if constexpr (TM::kWarp) {
     // the block's warps hold the same columns: add them up in warp order
@@ -239,7 +284,7 @@ __global__ __launch_bounds__(Team<WIDTH>::kThreads) void norm_bwd_kernel(
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) own[(i * 32 + t) * VEC + j] = acc[i][j];
+      for (int j = 0; j < VEC; ++j) own[(i * 32 + t) * VEC + j] = f[i][j];
     __syncthreads();
     for (int c = threadIdx.x; c < a.cols; c += blockDim.x) {
       float s = 0.0f;
@@ -252,14 +297,15 @@ __global__ __launch_bounds__(Team<WIDTH>::kThreads) void norm_bwd_kernel(
     for (int i = 0; i < NV; ++i) {
 #pragma unroll
       for (int j = 0; j < VEC; ++j)
-        if (i * width * VEC + j < mine) out[(i * width + t) * VEC + j] = acc[i][j];
+        if (i * width * VEC + j < mine) out[(i * width + t) * VEC + j] = f[i][j];
     }
   }
 }
 
 template <typename T>
 __global__ __launch_bounds__(512) void norm_bwd_wide_kernel(NormBwd a) {
-  __shared__ float red[2][32];
+  __shared__ __align__(16) float red[2][16];
+  clear_sums(red);
   int flip = 0;
   for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
     const float rstd = a.rstd[row];
@@ -361,104 +407,113 @@ __global__ __launch_bounds__(kSumThreads) __cluster_dims__(kSumBlocks, 1, 1) voi
   }
 }
 
-// 32 columns a block, 32 warps over the rows of partial sums.
-__global__ __launch_bounds__(1024) void sum_partials_kernel(const float* partial, int64_t parts,
-                                                            int64_t cols, void* out, int out_bf16) {
-  __shared__ float part[32][33];
+// Sums of partial[parts, cols]: 32 columns a cluster, each of its blocks' warps
+// taking every 128th row; the blocks' parts meet in the first one's shared
+// memory.  (One block of 1024 threads for 32 columns took 9 us for 1216 rows of
+// 256 columns: the rows of one block come through one SM.)
+constexpr int kPartBlocks = 8;
+constexpr int kPartWarps = 16;
+__global__ __launch_bounds__(32 * kPartWarps) __cluster_dims__(kPartBlocks, 1, 1) void sum_partials_kernel(
+    const float* partial, int64_t parts, int64_t cols, void* out, int out_bf16) {
+  __shared__ float part[kPartWarps][33];
+  __shared__ float sums[kPartBlocks][32];
+  uint32_t rank;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t c = (int64_t)blockIdx.x * 32 + lane;
+  const int64_t c = (int64_t)(blockIdx.x / kPartBlocks) * 32 + lane;
   float s = 0.0f;
   if (c < cols) {
-    constexpr int kUnroll = 8;
-    for (int64_t p = warp; p < parts; p += 32 * kUnroll) {
+    constexpr int kUnroll = 8, kStep = kPartBlocks * kPartWarps;
+    for (int64_t p = rank * kPartWarps + warp; p < parts; p += kStep * kUnroll) {
       float v[kUnroll];
 #pragma unroll
-      for (int u = 0; u < kUnroll; ++u) v[u] = p + u * 32 < parts ? partial[(p + u * 32) * cols + c] : 0.0f;
+      for (int u = 0; u < kUnroll; ++u)
+        v[u] = p + u * kStep < parts ? partial[(p + u * kStep) * cols + c] : 0.0f;
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) s += v[u];
     }
   }
   part[warp][lane] = s;
   __syncthreads();
-  // warp w sums the 32 parts of column w
-  const float r = warp_sum(part[lane][warp]);
-  const int64_t o = (int64_t)blockIdx.x * 32 + warp;
-  if (lane == 0 && o < cols) {
+  if (warp == 0) {
+    float t = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kPartWarps; ++k) t += part[k][lane];
+    uint32_t to = (uint32_t)__cvta_generic_to_shared(&sums[rank][lane]);
+    asm volatile("mapa.shared::cluster.u32 %0, %0, %1;" : "+r"(to) : "r"(0));
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to), "f"(t) : "memory");
+  }
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                   : "memory");
+  if (rank == 0 && warp == 0 && c < cols) {
+    float t = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kPartBlocks; ++k) t += sums[k][lane];
     if (out_bf16)
-      static_cast<bf16*>(out)[o] = __float2bfloat16_rn(r);
+      static_cast<bf16*>(out)[c] = __float2bfloat16_rn(t);
     else
-      static_cast<float*>(out)[o] = r;
+      static_cast<float*>(out)[c] = t;
   }
 }
 
-// Launch shape of a row kernel: warps own rows up to kWarpCols, blocks above.
-// Eight columns a thread need a block as wide as the row; single columns (rows
-// of any alignment) need a width known to the compiler, so that a thread's
+// Launch shape of a row kernel: warps own rows up to warp_cols, blocks above, as
+// wide as the row at 8 columns a thread (16 past 4096).  Single columns (rows of
+// any alignment) need a width known to the compiler, so that a thread's
 // addresses are one register and constants (777 x 1283 float32 with the 8-bit
-// output: 10.8 us with the width in a register).
+// output: 10.8 us with the width in a register, 6.0 without).
 struct Shape {
-  int nv;     // vectors of 8 (or their 8 single columns) a thread
-  int width;  // threads a row
+  int per;    // columns a thread
+  int width;  // threads a row; 0: the block's
   int threads;
   unsigned grid;
 };
-Shape shape_of(int64_t rows, int64_t cols, bool vec, int warp_cols, int blocks_per_sm) {
+Shape shape_of(int64_t rows, int64_t cols, bool vec, int warp_cols, int threads_per_sm) {
   Shape s;
-  const int64_t most = (int64_t)sm_count() * blocks_per_sm;
   if (cols <= warp_cols) {
-    s.nv = cols <= 256 ? 1 : cols <= 512 ? 2 : 4;
+    s.per = cols <= 256 ? 8 : cols <= 512 ? 16 : 32;
     s.width = 32;
     s.threads = 32 * kWarpRows;
-    s.grid = (unsigned)std::min(ceil_div(rows, kWarpRows), most);
   } else {
-    s.nv = cols <= (vec ? 2048 : 4096) ? 1 : 2;
-    s.threads = vec ? (int)(ceil_div(ceil_div(cols, 8 * s.nv), 32) * 32) : cols <= 1024 ? 128 : cols <= 2048 ? 256 : 512;
+    s.per = !vec || cols > 4096 ? 16 : 8;
+    s.threads = vec ? (int)(ceil_div(ceil_div(cols, s.per), 32) * 32)
+                    : cols <= 1024 ? 64 : cols <= 2048 ? 128 : cols <= 4096 ? 256 : 512;
     s.width = vec ? 0 : s.threads;
-    s.grid = (unsigned)std::min(rows, most);
   }
+  const int64_t rows_per_block = s.width == 32 ? kWarpRows : 1;
+  s.grid = (unsigned)std::min(ceil_div(rows, rows_per_block),
+                              (int64_t)sm_count() * std::max(1, threads_per_sm / s.threads));
   return s;
 }
 
 // Runs CALL with VEC, NV and WIDTH as constants for a shape (rows of up to
 // WARP_COLS columns belong to a warp).
-#define SCAPE_SHAPE_SWITCH(vec, s, WARP_COLS, CALL)                                         \
-  if (vec) {                                                                                \
-    constexpr int VEC = 8;                                                                  \
-    if (s.width == 32) {                                                                    \
-      constexpr int WIDTH = 32;                                                             \
-      if (s.nv == 1) { constexpr int NV = 1; CALL; }                                        \
-      else if (s.nv == 2) { constexpr int NV = 2; CALL; }                                   \
-      else { constexpr int NV = WARP_COLS / 256; CALL; }                                    \
-    } else {                                                                                \
-      constexpr int WIDTH = 0;                                                              \
-      if (s.nv == 1) { constexpr int NV = 1; CALL; }                                        \
-      else { constexpr int NV = 2; CALL; }                                                  \
-    }                                                                                       \
-  } else {                                                                                  \
-    constexpr int VEC = 1;                                                                  \
-    if (s.width == 32) {                                                                    \
-      constexpr int WIDTH = 32;                                                             \
-      if (s.nv == 1) { constexpr int NV = 8; CALL; }                                        \
-      else if (s.nv == 2) { constexpr int NV = 16; CALL; }                                  \
-      else { constexpr int NV = WARP_COLS / 32; CALL; }                                     \
-    } else if (s.width == 128) {                                                            \
-      constexpr int WIDTH = 128, NV = 8;                                                    \
-      CALL;                                                                                 \
-    } else if (s.width == 256) {                                                            \
-      constexpr int WIDTH = 256, NV = 8;                                                    \
-      CALL;                                                                                 \
-    } else {                                                                                \
-      constexpr int WIDTH = 512;                                                            \
-      if (s.nv == 1) { constexpr int NV = 8; CALL; }                                        \
-      else { constexpr int NV = 16; CALL; }                                                 \
-    }                                                                                       \
+#define SCAPE_SHAPE_SWITCH(vec, s, WARP_COLS, CALL)                                      \
+  if (vec) {                                                                             \
+    if (s.width == 0 && s.per == 8) { constexpr int VEC = 8, WIDTH = 0, NV = 1; CALL; }  \
+    else if (s.width == 0) { constexpr int VEC = 16, WIDTH = 0, NV = 1; CALL; }          \
+    else if (s.per == 8) { constexpr int VEC = 8, WIDTH = 32, NV = 1; CALL; }            \
+    else if (s.per == 16) { constexpr int VEC = 8, WIDTH = 32, NV = 2; CALL; }           \
+    else { constexpr int VEC = 8, WIDTH = 32, NV = WARP_COLS / 256; CALL; }              \
+  } else {                                                                               \
+    constexpr int VEC = 1;                                                               \
+    if (s.width == 32 && s.per == 8) { constexpr int WIDTH = 32, NV = 8; CALL; }         \
+    else if (s.width == 32 && s.per == 16) { constexpr int WIDTH = 32, NV = 16; CALL; }  \
+    else if (s.width == 32) { constexpr int WIDTH = 32, NV = WARP_COLS / 32; CALL; }     \
+    else if (s.width == 64) { constexpr int WIDTH = 64, NV = 16; CALL; }                 \
+    else if (s.width == 128) { constexpr int WIDTH = 128, NV = 16; CALL; }               \
+    else if (s.width == 256) { constexpr int WIDTH = 256, NV = 16; CALL; }               \
+    else { constexpr int WIDTH = 512, NV = 16; CALL; }                                   \
   }
 
-constexpr int kFwdBlocksPerSm = 8;
-constexpr int kBwdBlocksPerSm = 4;
+// Threads an SM that the grids are made for.  Backward: all that fit at once, as
+// blocks keep their weight gradients to the end.  Forward: several rounds, so
+// that blocks that end early make room.
+constexpr int kFwdThreads = 16384;
+template <typename T>
+constexpr int bwd_threads() { return sizeof(T) == 2 ? 1024 : 512; }
 
 template <typename T>
-cudaError_t run_norm_fwd(const NormFwd& a, cudaStream_t st) {
+cudaError_t run_norm_fwd(NormFwd a, cudaStream_t st) {
   if (a.cols > kBlockCols) {
     norm_fwd_wide_kernel<T><<<(unsigned)std::min<int64_t>(a.rows, (int64_t)sm_count() * 4), 512, 0, st>>>(a);
     return cudaGetLastError();
@@ -466,15 +521,17 @@ cudaError_t run_norm_fwd(const NormFwd& a, cudaStream_t st) {
   const size_t e = sizeof(T);
   const bool vec = rows16(a.x, a.ldx, e) && rows16(a.res, a.ldres, e) && rows16(a.y, a.ldy, e) &&
                    rows16(a.h, a.ldh, e) && rows8(a.q, a.ldq);
+  a.q16 = rows16(a.q, a.ldq, 1);
   const bool wv = aligned(a.w, 16);
-  const Shape s = shape_of(a.rows, a.cols, vec, kWarpCols, kFwdBlocksPerSm);
-  SCAPE_SHAPE_SWITCH(vec, s, kWarpCols, (norm_fwd_kernel<T, VEC, NV, WIDTH><<<s.grid, s.threads, 0, st>>>(a, wv)));
+  const float inv = (float)(1.0 / a.cols);
+  const Shape s = shape_of(a.rows, a.cols, vec, kWarpCols, kFwdThreads);
+  SCAPE_SHAPE_SWITCH(vec, s, kWarpCols, (norm_fwd_kernel<T, VEC, NV, WIDTH><<<s.grid, s.threads, 0, st>>>(a, wv, inv)));
   return cudaGetLastError();
 }
 
 template <typename T>
 cudaError_t run_norm_bwd(const NormBwd& a, cudaStream_t st) {
-  const int64_t parts = norm_bwd_partials(a.rows, a.cols);
+  int64_t parts = norm_bwd_partials(a.rows, a.cols);
   if (a.cols > kBlockCols) {
     if (a.dw) {
       norm_dw_wide_kernel<T><<<dim3((unsigned)ceil_div(a.cols, 256), (unsigned)parts), 256, 0, st>>>(a);
@@ -487,8 +544,10 @@ cudaError_t run_norm_bwd(const NormBwd& a, cudaStream_t st) {
     const bool vec = rows16(a.dy, a.lddy, e) && rows16(a.h, a.ldh, e) &&
                      rows16(a.dh, a.lddh, e) && rows16(a.dx, a.lddx, e);
     const bool wv = aligned(a.w, 16);
-    const Shape s = shape_of(a.rows, a.cols, vec, kWarpColsBwd, kBwdBlocksPerSm);
-    SCAPE_SHAPE_SWITCH(vec, s, kWarpColsBwd, (norm_bwd_kernel<T, VEC, NV, WIDTH><<<s.grid, s.threads, 0, st>>>(a, wv)));
+    const float inv = (float)(1.0 / a.cols);
+    const Shape s = shape_of(a.rows, a.cols, vec, kWarpColsBwd, vec && a.cols <= 4096 ? bwd_threads<T>() : 512);
+    SCAPE_SHAPE_SWITCH(vec, s, kWarpColsBwd, (norm_bwd_kernel<T, VEC, NV, WIDTH><<<s.grid, s.threads, 0, st>>>(a, wv, inv)));
+    parts = s.grid;
   }
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !a.dw) return e;
@@ -502,7 +561,8 @@ cudaError_t launch_norm_fwd(const NormFwd& a, int dtype, cudaStream_t st) {
 }
 int64_t norm_bwd_partials(int64_t rows, int64_t cols) {
   if (cols > kBlockCols) return std::min<int64_t>(ceil_div(rows, 8), 64);
-  return shape_of(rows, cols, true, kWarpColsBwd, kBwdBlocksPerSm).grid;  // the grid does not go by `vec`
+  return std::max(shape_of(rows, cols, true, kWarpColsBwd, 1024).grid,
+                  shape_of(rows, cols, false, kWarpColsBwd, 512).grid);
 }
 cudaError_t launch_norm_bwd(const NormBwd& a, int dtype, cudaStream_t st) {
   return dtype == SCAPE_BF16 ? run_norm_bwd<bf16>(a, st) : run_norm_bwd<float>(a, st);
@@ -519,7 +579,7 @@ cudaError_t launch_colsum(const bf16* m, int64_t ld, int64_t rows, int64_t cols,
 }
 cudaError_t launch_sum_partials(const float* partial, int64_t parts, int64_t cols, void* out,
                                 int out_bf16, cudaStream_t st) {
-  sum_partials_kernel<<<(unsigned)ceil_div(cols, 32), 1024, 0, st>>>(partial, parts, cols, out, out_bf16);
+  sum_partials_kernel<<<(unsigned)ceil_div(cols, 32) * kPartBlocks, 32 * kPartWarps, 0, st>>>(partial, parts, cols, out, out_bf16);
   return cudaGetLastError();
 }
 
