@@ -36,28 +36,38 @@ bool dtype_ok(int d) { return d == SCAPE_F32 || d == SCAPE_BF16; }
 bool act_ok(int a) { return a >= SCAPE_ACT_NONE && a <= SCAPE_ACT_SILU; }
 bool elem_ok(const void* p, int dtype) { return p && aligned(p, dtype == SCAPE_BF16 ? 2 : 4); }
 
-// Rows `from` of src (any alignment) copied to 16-byte aligned rows.  A thread
-// writes eight values; its reads, two bytes each, fall on lines that its
-// neighbours read as well.
-__global__ __launch_bounds__(256) void align_rows_kernel(const bf16* src, int64_t ld, int64_t rows,
-                                                         int64_t cols, bf16* dst, int64_t ldd) {
-  const int64_t per_row = ldd / 8;
-  for (int64_t row = blockIdx.y; row < rows; row += gridDim.y) {
-    const int64_t c = ((int64_t)blockIdx.x * 256 + threadIdx.x);
-    if (c >= per_row) continue;
-    float v[8];
+struct Matrix {
+  const void* p;
+  int64_t ld, rows, cols;
+};
+
+// Up to two matrices (blockIdx.z) of any alignment copied to 16-byte aligned
+// rows.  A thread writes eight values; its reads, two bytes each, fall on lines
+// that its neighbours read as well.
+struct AlignCopy {
+  const bf16* src;
+  int64_t ld, rows, cols;
+  bf16* dst;
+  int64_t ldd;
+};
+struct AlignCopies {
+  AlignCopy m[2];
+};
+__global__ __launch_bounds__(256) void align_rows_kernel(const __grid_constant__ AlignCopies a) {
+  const AlignCopy& m = a.m[blockIdx.z];
+  // a block covers 8 rows of 32 vectors, or what of them there is
+  const int64_t c = ((int64_t)blockIdx.x * 32 + (threadIdx.x & 31)) * 8;
+  if (c >= m.ldd) return;
+  for (int64_t row = (int64_t)blockIdx.y * 8 + (threadIdx.x >> 5); row < m.rows; row += (int64_t)gridDim.y * 8) {
+    const uint16_t* s = reinterpret_cast<const uint16_t*>(m.src) + row * m.ld + c;
+    uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      v[i] = c * 8 + i < cols ? __bfloat162float(src[row * ld + c * 8 + i]) : 0.0f;
-    store_vec<8>(dst + row * ldd + c * 8, v);
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t lo = c + 2 * i < m.cols ? s[2 * i] : 0, hi = c + 2 * i + 1 < m.cols ? s[2 * i + 1] : 0;
+      w[i] = lo | hi << 16;
+    }
+    *reinterpret_cast<uint4*>(m.dst + row * m.ldd + c) = make_uint4(w[0], w[1], w[2], w[3]);
   }
-}
-cudaError_t launch_align_rows(const bf16* src, int64_t ld, int64_t rows, int64_t cols, bf16* dst,
-                              int64_t ldd, cudaStream_t st) {
-  const unsigned x = (unsigned)ceil_div(ldd / 8, 256);
-  align_rows_kernel<<<dim3(x, (unsigned)std::min<int64_t>(rows, 32768)), 256, 0, st>>>(
-      src, ld, rows, cols, dst, ldd);
-  return cudaGetLastError();
 }
 
 int64_t round8(int64_t n) { return (n + 7) / 8 * 8; }
@@ -74,16 +84,29 @@ bool tma_rows(const void* p, int64_t ld) { return rows16(p, ld, 2); }
 size_t operand_bytes(const void* p, int64_t ld, int64_t rows, int64_t cols) {
   return tma_rows(p, ld) ? 0 : copy_bytes(rows, cols);
 }
-cudaError_t operand(const void* p, int64_t ld, int64_t rows, int64_t cols, uint8_t*& ws,
-                    GemmOperand* out, cudaStream_t st) {
-  if (tma_rows(p, ld)) {
-    *out = {static_cast<const bf16*>(p), ld};
-    return cudaSuccess;
+cudaError_t operands(const Matrix& a, const Matrix& b, bool any_rows, uint8_t* ws, GemmCall* call,
+                     cudaStream_t st) {
+  const Matrix* in[2] = {&a, &b};
+  GemmOperand* out[2] = {&call->a, &call->b};
+  AlignCopies copies = {};
+  int n = 0;
+  int64_t x = 1, y = 1;
+  for (int i = 0; i < 2; ++i) {
+    const Matrix& m = *in[i];
+    if (any_rows || tma_rows(m.p, m.ld)) {
+      *out[i] = {static_cast<const bf16*>(m.p), m.ld};
+      continue;
+    }
+    AlignCopy& c = copies.m[n++];
+    c = {static_cast<const bf16*>(m.p), m.ld, m.rows, m.cols, reinterpret_cast<bf16*>(ws), round8(m.cols)};
+    ws += copy_bytes(m.rows, m.cols);
+    *out[i] = {c.dst, c.ldd};
+    x = std::max(x, ceil_div(c.ldd, 256));
+    y = std::max(y, ceil_div(c.rows, 8));
   }
-  bf16* dst = reinterpret_cast<bf16*>(ws);
-  ws += copy_bytes(rows, cols);
-  *out = {dst, round8(cols)};
-  return launch_align_rows(static_cast<const bf16*>(p), ld, rows, cols, dst, round8(cols), st);
+  if (n == 0) return cudaSuccess;
+  align_rows_kernel<<<dim3((unsigned)x, (unsigned)std::min<int64_t>(y, 32768), (unsigned)n), 256, 0, st>>>(copies);
+  return cudaGetLastError();
 }
 
 int check_workspace(const void* ws, size_t have, size_t need) {
@@ -314,7 +337,7 @@ extern "C" int scape_layer_linear_workspace(const void* x, int64_t ldx, const vo
                                             size_t* bytes) {
   if (!bytes) return fail(SCAPE_EINVAL, "bytes is NULL");
   if (!size_ok(rows) || !size_ok(k) || !size_ok(n)) return fail(SCAPE_EINVAL, "a size is out of range");
-  *bytes = rows && n ? operand_bytes(x, ldx, rows, k) + operand_bytes(weight, ldw, n, k) : 0;
+  *bytes = rows > kSkinnyRows && n ? operand_bytes(x, ldx, rows, k) + operand_bytes(weight, ldw, n, k) : 0;
   return SCAPE_OK;
 }
 
@@ -340,8 +363,8 @@ extern "C" int scape_layer_linear(const void* x, int64_t ldx, const void* weight
   if (rc) return rc;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   GemmCall c = {};
-  cudaError_t e = operand(x, ldx, rows, k, ws, &c.a, st);
-  if (e == cudaSuccess) e = operand(weight, ldw, n, k, ws, &c.b, st);
+  const bool skinny = rows <= kSkinnyRows;
+  cudaError_t e = operands({x, ldx, rows, k}, {weight, ldw, n, k}, skinny, ws, &c, st);
   c.m = rows, c.n = n, c.k = k;
   c.e.act = activation;
   c.e.bias = static_cast<const bf16*>(bias);
@@ -353,7 +376,7 @@ extern "C" int scape_layer_linear(const void* x, int64_t ldx, const void* weight
   c.e.blocks_per_row = ceil_div(n, kBlock);
   c.e.out = y, c.e.ldo = ldy;
   c.e.out_vec = rows16(y, ldy, 2);
-  if (e == cudaSuccess) e = gemm_forward(c, st);
+  if (e == cudaSuccess) e = skinny ? skinny_forward(c, st) : gemm_forward(c, st);
   return cuda_result(e, "scape_layer_linear");
 }
 
@@ -363,7 +386,7 @@ extern "C" int scape_layer_linear_bwd_input_workspace(const void* dy, int64_t ld
                                                       size_t* bytes) {
   if (!bytes) return fail(SCAPE_EINVAL, "bytes is NULL");
   if (!size_ok(rows) || !size_ok(k) || !size_ok(n)) return fail(SCAPE_EINVAL, "a size is out of range");
-  *bytes = rows && k ? operand_bytes(dy, lddy, rows, n) + operand_bytes(weight, ldw, n, k) : 0;
+  *bytes = rows > kSkinnyRows && k ? operand_bytes(dy, lddy, rows, n) + operand_bytes(weight, ldw, n, k) : 0;
   return SCAPE_OK;
 }
 
@@ -387,8 +410,8 @@ extern "C" int scape_layer_linear_bwd_input(const void* dy, int64_t lddy, const 
   if (rc) return rc;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   GemmCall c = {};
-  cudaError_t e = operand(dy, lddy, rows, n, ws, &c.a, st);
-  if (e == cudaSuccess) e = operand(weight, ldw, n, k, ws, &c.b, st);
+  const bool skinny = rows <= kSkinnyRows;
+  cudaError_t e = operands({dy, lddy, rows, n}, {weight, ldw, n, k}, skinny, ws, &c, st);
   c.m = rows, c.n = k, c.k = n;
   c.e.act = activation;
   c.e.pre_q = q, c.e.ldpre = ldq, c.e.pre_scale = scale;
@@ -396,7 +419,7 @@ extern "C" int scape_layer_linear_bwd_input(const void* dy, int64_t lddy, const 
   c.e.blocks_per_row = ceil_div(k, kBlock);
   c.e.out = dx, c.e.ldo = lddx;
   c.e.out_vec = rows16(dx, lddx, 2);
-  if (e == cudaSuccess) e = gemm_input_grad(c, st);
+  if (e == cudaSuccess) e = skinny ? skinny_input_grad(c, st) : gemm_input_grad(c, st);
   return cuda_result(e, "scape_layer_linear_bwd_input");
 }
 
@@ -406,7 +429,7 @@ extern "C" int scape_layer_linear_bwd_weight_workspace(const void* dy, int64_t l
   if (!bytes) return fail(SCAPE_EINVAL, "bytes is NULL");
   if (!size_ok(rows) || !size_ok(k) || !size_ok(n)) return fail(SCAPE_EINVAL, "a size is out of range");
   *bytes = 0;
-  if (rows == 0 || n == 0) return SCAPE_OK;
+  if (rows <= kSkinnyRows || n == 0) return SCAPE_OK;
   *bytes = operand_bytes(dy, lddy, rows, n) +
            (x ? operand_bytes(x, ldx, rows, k) : copy_bytes(rows, k));
   return SCAPE_OK;
@@ -446,16 +469,23 @@ extern "C" int scape_layer_linear_bwd_weight(const void* dy, int64_t lddy, const
   if (rc) return rc;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   cudaError_t e = cudaSuccess;
+  if (k && rows <= kSkinnyRows) {
+    SkinnyWeightGrad a;
+    a.dy = static_cast<const bf16*>(dy), a.x = static_cast<const bf16*>(x);
+    a.lddy = lddy, a.ldx = ldx, a.q = q, a.scale = scale, a.ldq = ldq, a.act = activation;
+    a.rows = rows, a.k = k, a.n = n;
+    a.dw = dweight, a.db = dbias, a.lddw = lddw, a.out_f32 = grad_dtype == SCAPE_F32;
+    return cuda_result(skinny_weight_grad(a, st), who);
+  }
   if (k) {
     GemmCall c = {};
-    e = operand(dy, lddy, rows, n, ws, &c.a, st);
-    if (e == cudaSuccess && x) {
-      e = operand(x, ldx, rows, k, ws, &c.b, st);
-    } else if (e == cudaSuccess) {
+    if (x) {
+      e = operands({dy, lddy, rows, n}, {x, ldx, rows, k}, false, ws, &c, st);
+    } else {
       bf16* a = reinterpret_cast<bf16*>(ws);
       ws += copy_bytes(rows, k);
-      c.b = {a, round8(k)};
       e = launch_unpack8(q, ldq, scale, rows, k, activation, a, round8(k), SCAPE_BF16, st);
+      if (e == cudaSuccess) e = operands({dy, lddy, rows, n}, {a, round8(k), rows, k}, false, ws, &c, st);
     }
     c.m = n, c.n = k, c.k = rows;
     c.e.out = dweight, c.e.ldo = lddw, c.e.out_f32 = grad_dtype == SCAPE_F32;

@@ -41,7 +41,7 @@ struct Epilogue {
 };
 
 struct GemmOperand {
-  const bf16* p;  // 16-byte aligned, ld a multiple of 8
+  const bf16* p;  // 16-byte aligned, ld a multiple of 8 (skinny products: any)
   int64_t ld;
 };
 
@@ -57,6 +57,24 @@ struct GemmCall {
 cudaError_t gemm_forward(const GemmCall& c, cudaStream_t st);
 cudaError_t gemm_input_grad(const GemmCall& c, cudaStream_t st);
 cudaError_t gemm_weight_grad(const GemmCall& c, cudaStream_t st);
+
+// The same products for up to kSkinnyRows rows, of operands of any alignment
+// (layer_skinny.cu); m is the rows.
+constexpr int kSkinnyRows = 8;
+cudaError_t skinny_forward(const GemmCall& c, cudaStream_t st);
+cudaError_t skinny_input_grad(const GemmCall& c, cudaStream_t st);
+struct SkinnyWeightGrad {
+  const bf16 *dy, *x;
+  int64_t lddy, ldx;
+  const uint8_t *q, *scale;
+  int64_t ldq;
+  int act;
+  int64_t rows, k, n;
+  void *dw, *db;
+  int64_t lddw;
+  int out_f32;
+};
+cudaError_t skinny_weight_grad(const SkinnyWeightGrad& a, cudaStream_t st);
 
 // Lets a kernel use this much dynamic shared memory (asked of CUDA once).
 cudaError_t gemm_allow_smem(const void* kernel, int bytes);
@@ -537,7 +555,8 @@ __device__ __forceinline__ void store_box(const float (&v)[32], uint32_t box, in
 // ------------------------------------------------------------------ the kernel
 struct GemmShape {
   int m, n;
-  int bn;  // columns of a tile
+  int bn;       // columns of a tile
+  int a_bytes;  // of operand A a block copies for a stage
   int tiles_m, tiles_n, ksteps;
   unsigned int* status;
 };
@@ -624,7 +643,7 @@ __global__ __launch_bounds__(Tile<KIND, BN, MODE>::kThreads, 1) void gemm_kernel
     // ---------------- producer: this block's rows of A and of B.  In a pair both
     // blocks' copies count on the first block's barrier, which expects them all.
     const int b_boxes = TB ? (b_rows + 63) / 64 : 1;
-    const uint32_t bytes = TL::kABytes + (TB ? b_boxes * kChunk : b_rows * kBK * 2);
+    const uint32_t bytes = s.a_bytes + (TB ? b_boxes * kChunk : b_rows * kBK * 2);
     const uint32_t lead = PAIR ? cluster_addr(bar0, 0) - bar0 : 0;
     int stage = 0, phase = 0;
     int64_t issued = 0;
@@ -883,8 +902,11 @@ cudaError_t gemm_launch(const GemmCall& c, int bn, int split, cudaStream_t st) {
   constexpr bool TA = KIND == kGemmWeightGrad;
   constexpr bool TB = KIND != kGemmForward;
   CUtensorMap ma, mb, mo;
+  // fewer rows than a tile's: copy those only (what lies in the others' place
+  // reaches accumulator rows that nobody reads)
+  const int a_rows = (int)std::min<int64_t>(kBM, (c.m + 7) / 8 * 8);
   cudaError_t err = TA ? gemm_tensor_map(&ma, c.a.p, c.k, c.m, c.a.ld, kBK, kBK)
-                       : gemm_tensor_map(&ma, c.a.p, c.m, c.k, c.a.ld, kBM, kBK);
+                       : gemm_tensor_map(&ma, c.a.p, c.m, c.k, c.a.ld, a_rows, kBK);
   if (err == cudaSuccess)
     err = TB ? gemm_tensor_map(&mb, c.b.p, c.k, c.n, c.b.ld, kBK, kBK)
              : gemm_tensor_map(&mb, c.b.p, c.n, c.k, c.b.ld, PAIR ? bn / 2 : bn, kBK);
@@ -897,6 +919,7 @@ cudaError_t gemm_launch(const GemmCall& c, int bn, int split, cudaStream_t st) {
   s.m = (int)c.m;
   s.n = (int)c.n;
   s.bn = bn;
+  s.a_bytes = TA ? TL::kABytes : a_rows * kBK * 2;
   s.tiles_m = (int)ceil_div(c.m, PAIR ? 2 * kBM : kBM);
   s.tiles_n = (int)ceil_div(c.n, bn);
   s.ksteps = (int)ceil_div(c.k, kBK);

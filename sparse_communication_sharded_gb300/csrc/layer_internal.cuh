@@ -467,6 +467,39 @@ __device__ __forceinline__ float act_exact(float z) {
     default: { constexpr int ACT = SCAPE_ACT_NONE; CALL; break; }             \
   }
 
+// ------------------------------------------------------------------ clusters
+// Blocks of a cluster that give sums to the first one: cluster_begin() at the
+// start, cluster_ready() before the first to_first() (all blocks have begun by
+// then), cluster_done() before the first block reads.  All threads call each.
+__device__ __forceinline__ uint32_t block_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_blocks() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_begin() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_ready() {
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_done() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                   : "memory");
+}
+// Stores to the same place of the cluster's first block.
+__device__ __forceinline__ void to_first(float* p, float v) {
+  uint32_t a = (uint32_t)__cvta_generic_to_shared(p);
+  asm volatile("mapa.shared::cluster.u32 %0, %0, %1;" : "+r"(a) : "r"(0));
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory");
+}
+
 // ------------------------------------------------------------------ launchers
 cudaError_t launch_pack8(const void* x, int64_t ldx, int dtype, int64_t rows, int64_t cols,
                          uint8_t* q, int64_t ldq, uint8_t* scale, cudaStream_t st);

@@ -350,18 +350,18 @@ constexpr int kSumBlocks = 8;
 constexpr int kSumThreads = 512;
 
 template <int VEC>
-__global__ __launch_bounds__(kSumThreads) __cluster_dims__(kSumBlocks, 1, 1) void colsum_kernel(
+__global__ __launch_bounds__(kSumThreads) void colsum_kernel(
     const bf16* m, int64_t ld, int64_t rows, int64_t cols, void* out, int out_bf16) {
   // VEC 8: eight threads a row, VEC 1: 64
   constexpr int kPerRow = kSumCols / VEC, kRows = kSumThreads / kPerRow;
   __shared__ float part[kRows][kSumCols + 4];
   __shared__ float sums[kSumBlocks][kSumCols];
-  uint32_t rank;
-  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+  const uint32_t rank = block_rank(), ranks = cluster_blocks();
+  cluster_begin();
   const int at = threadIdx.x % kPerRow, r0 = threadIdx.x / kPerRow;
-  const int64_t c = (int64_t)(blockIdx.x / kSumBlocks) * kSumCols + at * VEC;
+  const int64_t c = (int64_t)(blockIdx.x / ranks) * kSumCols + at * VEC;
   const int n = (int)min((int64_t)VEC, cols - c);
-  const int64_t begin = rows * rank / kSumBlocks, end = rows * (rank + 1) / kSumBlocks;
+  const int64_t begin = rows * rank / ranks, end = rows * (rank + 1) / ranks;
   float s[VEC];
 #pragma unroll
   for (int j = 0; j < VEC; ++j) s[j] = 0.0f;
@@ -382,22 +382,21 @@ __global__ __launch_bounds__(kSumThreads) __cluster_dims__(kSumBlocks, 1, 1) voi
 #pragma unroll
   for (int j = 0; j < VEC; ++j) part[r0][at * VEC + j] = s[j];
   __syncthreads();
+  cluster_ready();
   // to the first block: kSumCols sums of this one
   if (threadIdx.x < kSumCols) {
     float t = 0.0f;
 #pragma unroll 8
     for (int k = 0; k < kRows; ++k) t += part[k][threadIdx.x];
-    uint32_t to = (uint32_t)__cvta_generic_to_shared(&sums[rank][threadIdx.x]);
-    asm volatile("mapa.shared::cluster.u32 %0, %0, %1;" : "+r"(to) : "r"(0));
-    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to), "f"(t) : "memory");
+    to_first(&sums[rank][threadIdx.x], t);
   }
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
-                   : "memory");
+  cluster_done();
   if (rank == 0 && threadIdx.x < kSumCols) {
-    const int64_t o = (int64_t)(blockIdx.x / kSumBlocks) * kSumCols + threadIdx.x;
+    const int64_t o = (int64_t)(blockIdx.x / ranks) * kSumCols + threadIdx.x;
     float t = 0.0f;
 #pragma unroll
-    for (int k = 0; k < kSumBlocks; ++k) t += sums[k][threadIdx.x];
+    for (uint32_t k = 0; k < kSumBlocks; ++k)
+      if (k < ranks) t += sums[k][threadIdx.x];
     if (o < cols) {
       if (out_bf16)
         static_cast<bf16*>(out)[o] = __float2bfloat16_rn(t);
@@ -408,22 +407,23 @@ __global__ __launch_bounds__(kSumThreads) __cluster_dims__(kSumBlocks, 1, 1) voi
 }
 
 // Sums of partial[parts, cols]: 32 columns a cluster, each of its blocks' warps
-// taking every 128th row; the blocks' parts meet in the first one's shared
+// taking every 16th of its rows; the blocks' parts meet in the first one's shared
 // memory.  (One block of 1024 threads for 32 columns took 9 us for 1216 rows of
 // 256 columns: the rows of one block come through one SM.)
 constexpr int kPartBlocks = 8;
 constexpr int kPartWarps = 16;
-__global__ __launch_bounds__(32 * kPartWarps) __cluster_dims__(kPartBlocks, 1, 1) void sum_partials_kernel(
+__global__ __launch_bounds__(32 * kPartWarps) void sum_partials_kernel(
     const float* partial, int64_t parts, int64_t cols, void* out, int out_bf16) {
   __shared__ float part[kPartWarps][33];
   __shared__ float sums[kPartBlocks][32];
-  uint32_t rank;
-  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+  const uint32_t rank = block_rank(), ranks = cluster_blocks();
+  cluster_begin();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t c = (int64_t)(blockIdx.x / kPartBlocks) * 32 + lane;
+  const int64_t c = (int64_t)(blockIdx.x / ranks) * 32 + lane;
   float s = 0.0f;
   if (c < cols) {
-    constexpr int kUnroll = 8, kStep = kPartBlocks * kPartWarps;
+    constexpr int kUnroll = 8;
+    const int kStep = ranks * kPartWarps;
     for (int64_t p = rank * kPartWarps + warp; p < parts; p += kStep * kUnroll) {
       float v[kUnroll];
 #pragma unroll
@@ -435,20 +435,19 @@ __global__ __launch_bounds__(32 * kPartWarps) __cluster_dims__(kPartBlocks, 1, 1
   }
   part[warp][lane] = s;
   __syncthreads();
+  cluster_ready();
   if (warp == 0) {
     float t = 0.0f;
 #pragma unroll
     for (int k = 0; k < kPartWarps; ++k) t += part[k][lane];
-    uint32_t to = (uint32_t)__cvta_generic_to_shared(&sums[rank][lane]);
-    asm volatile("mapa.shared::cluster.u32 %0, %0, %1;" : "+r"(to) : "r"(0));
-    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to), "f"(t) : "memory");
+    to_first(&sums[rank][lane], t);
   }
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
-                   : "memory");
+  cluster_done();
   if (rank == 0 && warp == 0 && c < cols) {
     float t = 0.0f;
 #pragma unroll
-    for (int k = 0; k < kPartBlocks; ++k) t += sums[k][lane];
+    for (uint32_t k = 0; k < kPartBlocks; ++k)
+      if (k < ranks) t += sums[k][lane];
     if (out_bf16)
       static_cast<bf16*>(out)[c] = __float2bfloat16_rn(t);
     else
@@ -568,19 +567,32 @@ cudaError_t launch_norm_bwd(const NormBwd& a, int dtype, cudaStream_t st) {
   return dtype == SCAPE_BF16 ? run_norm_bwd<bf16>(a, st) : run_norm_bwd<float>(a, st);
 }
 
+// Launches a kernel over `clusters` clusters: of one block where there is little
+// to add up, which starts sooner.
+template <typename... P, typename... A>
+static cudaError_t launch_clusters(void (*kernel)(P...), int64_t clusters, int blocks, int threads,
+                                   cudaStream_t st, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(clusters * blocks));
+  cfg.blockDim = dim3(threads);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = (unsigned)blocks;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
 cudaError_t launch_colsum(const bf16* m, int64_t ld, int64_t rows, int64_t cols, void* out,
                           int out_bf16, cudaStream_t st) {
-  const unsigned grid = (unsigned)ceil_div(cols, kSumCols) * kSumBlocks;
-  if (rows16(m, ld, 2))
-    colsum_kernel<8><<<grid, kSumThreads, 0, st>>>(m, ld, rows, cols, out, out_bf16);
-  else
-    colsum_kernel<1><<<grid, kSumThreads, 0, st>>>(m, ld, rows, cols, out, out_bf16);
-  return cudaGetLastError();
+  return launch_clusters(rows16(m, ld, 2) ? colsum_kernel<8> : colsum_kernel<1>, ceil_div(cols, kSumCols),
+                         rows <= 256 ? 1 : kSumBlocks, kSumThreads, st, m, ld, rows, cols, out, out_bf16);
 }
 cudaError_t launch_sum_partials(const float* partial, int64_t parts, int64_t cols, void* out,
                                 int out_bf16, cudaStream_t st) {
-  sum_partials_kernel<<<(unsigned)ceil_div(cols, 32) * kPartBlocks, 32 * kPartWarps, 0, st>>>(partial, parts, cols, out, out_bf16);
-  return cudaGetLastError();
+  return launch_clusters(sum_partials_kernel, ceil_div(cols, 32), parts <= 128 ? 1 : kPartBlocks,
+                         32 * kPartWarps, st, partial, parts, cols, out, out_bf16);
 }
 
 }  // namespace layer

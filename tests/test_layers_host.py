@@ -71,10 +71,12 @@ def test_linear_refusals(lib):
     n = ctypes.c_size_t(9)
     assert lib.scape_layer_linear_workspace(A, 64, A, 64, 8, 64, 32, ctypes.byref(n)) == C.SCAPE_OK
     assert n.value == 0  # aligned operands need none
+    assert lib.scape_layer_linear_workspace(A, 65, A, 64, 16, 64, 32, ctypes.byref(n)) == C.SCAPE_OK
+    assert n.value >= 16 * 64 * 2
     assert lib.scape_layer_linear_workspace(A, 65, A, 64, 8, 64, 32, ctypes.byref(n)) == C.SCAPE_OK
-    assert n.value >= 8 * 64 * 2
+    assert n.value == 0  # few rows are read in place whatever their alignment
 
-    def f(x=A, ldx=64, rows=8, k=64, act=0, y=A, ws=None, nbytes=0):
+    def f(x=A, ldx=64, rows=16, k=64, act=0, y=A, ws=None, nbytes=0):
         return lib.scape_layer_linear(x, ldx, A, 64, None, None, 0, rows, k, 32, act, y, 32, None, 0,
                                       None, ws, nbytes, None)
     refused(lib, f(x=None), "x")
