@@ -146,6 +146,23 @@ cudaError_t gemm_status_word(unsigned int** word) {
   return cudaSuccess;
 }
 
+int64_t gemm_clusters(int blocks) {
+  static std::atomic<int> known[kMaxDevices][4];  // 1, 2, 4, 8 blocks
+  const int i = blocks == 1 ? 0 : blocks == 2 ? 1 : blocks == 4 ? 2 : 3;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 0;
+  int n = known[dev][i].load(std::memory_order_relaxed);
+  if (n == 0) {
+    // an answer that is not to be had counts as no cluster, i.e. no cut
+    if (gemm_probe_clusters(blocks, &n) != cudaSuccess || n <= 0) {
+      (void)cudaGetLastError();
+      n = -1;
+    }
+    known[dev][i].store(n, std::memory_order_relaxed);
+  }
+  return n < 0 ? 0 : n;
+}
+
 cudaError_t gemm_allow_smem(const void* kernel, int bytes) {
   // per device, the kernels already told
   struct Told {
@@ -429,7 +446,7 @@ extern "C" int scape_layer_linear_bwd_weight_workspace(const void* dy, int64_t l
   if (!bytes) return fail(SCAPE_EINVAL, "bytes is NULL");
   if (!size_ok(rows) || !size_ok(k) || !size_ok(n)) return fail(SCAPE_EINVAL, "a size is out of range");
   *bytes = 0;
-  if (rows <= kSkinnyRows || n == 0) return SCAPE_OK;
+  if (rows <= kSkinnyWeightRows || n == 0) return SCAPE_OK;
   *bytes = operand_bytes(dy, lddy, rows, n) +
            (x ? operand_bytes(x, ldx, rows, k) : copy_bytes(rows, k));
   return SCAPE_OK;
@@ -469,7 +486,7 @@ extern "C" int scape_layer_linear_bwd_weight(const void* dy, int64_t lddy, const
   if (rc) return rc;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   cudaError_t e = cudaSuccess;
-  if (k && rows <= kSkinnyRows) {
+  if (k && rows <= kSkinnyWeightRows) {
     SkinnyWeightGrad a;
     a.dy = static_cast<const bf16*>(dy), a.x = static_cast<const bf16*>(x);
     a.lddy = lddy, a.ldx = ldx, a.q = q, a.scale = scale, a.ldq = ldq, a.act = activation;

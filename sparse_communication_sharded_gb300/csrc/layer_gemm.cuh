@@ -58,9 +58,10 @@ cudaError_t gemm_forward(const GemmCall& c, cudaStream_t st);
 cudaError_t gemm_input_grad(const GemmCall& c, cudaStream_t st);
 cudaError_t gemm_weight_grad(const GemmCall& c, cudaStream_t st);
 
-// The same products for up to kSkinnyRows rows, of operands of any alignment
-// (layer_skinny.cu); m is the rows.
-constexpr int kSkinnyRows = 8;
+// The same products for up to kSkinnyRows rows (weight gradient:
+// kSkinnyWeightRows), of operands of any alignment (layer_skinny.cu); m is the rows.
+constexpr int kSkinnyRows = 4;
+constexpr int kSkinnyWeightRows = 8;
 cudaError_t skinny_forward(const GemmCall& c, cudaStream_t st);
 cudaError_t skinny_input_grad(const GemmCall& c, cudaStream_t st);
 struct SkinnyWeightGrad {
@@ -78,6 +79,13 @@ cudaError_t skinny_weight_grad(const SkinnyWeightGrad& a, cudaStream_t st);
 
 // Lets a kernel use this much dynamic shared memory (asked of CUDA once).
 cudaError_t gemm_allow_smem(const void* kernel, int bytes);
+
+// Clusters of so many blocks, one block an SM, that are at work at one time (asked
+// of CUDA once; clusters do not cross the GPU's processing clusters, so there are
+// fewer than SMs / blocks: 15 of 8 blocks on 152 SMs, and a 16th waits for a whole
+// one to end).
+int64_t gemm_clusters(int blocks);
+cudaError_t gemm_probe_clusters(int blocks, int* n);
 
 // Where kernels record that they gave up a wait (one word a device).
 cudaError_t gemm_status_word(unsigned int** word);
@@ -140,6 +148,9 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, i
         "l"(map), "r"(x), "r"(y), "r"(bar)
         : "memory");
   }
+}
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
 __device__ __forceinline__ void tma_store(const CUtensorMap* map, int x, int y, uint32_t src) {
   asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
@@ -597,6 +608,11 @@ __global__ __launch_bounds__(Tile<KIND, BN, MODE>::kThreads, 1) void gemm_kernel
     gave_up = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  if (threadIdx.x == 96) {
+    prefetch_map(&map_a);
+    prefetch_map(&map_b);
+    if constexpr (PAIR) prefetch_map(&map_out);
+  }
   if (warp == 2) tmem_alloc<PAIR>(&tmem_base, TL::kColumns);
   tc_fence_before();
   __syncthreads();
@@ -969,7 +985,7 @@ cudaError_t gemm_run(const GemmCall& c, cudaStream_t st) {
   const int bn = tm * ceil_div(c.n, 64) <= sms ? 64 : 128;
   const int64_t tiles = tm * ceil_div(c.n, bn);
   int split = 1;
-  while (split < 8 && tiles * split * 2 <= sms && ksteps / (split * 2) >= 4) split *= 2;
+  while (split < 8 && tiles <= gemm_clusters(split * 2) && ksteps / (split * 2) >= 4) split *= 2;
   return bn == 64 ? gemm_launch<KIND, 64, kModeSplit>(c, 64, split, st)
                   : gemm_launch<KIND, 128, kModeSplit>(c, 128, split, st);
 }

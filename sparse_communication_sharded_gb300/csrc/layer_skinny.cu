@@ -1,10 +1,12 @@
-// layer_skinny.cu -- the linear layer and its gradients for a few rows (up to
-// kSkinnyRows), where the matrix is read (or the gradient written) once and
+// layer_skinny.cu -- the linear layer and its gradients for a few rows, where the matrix is read (or the gradient written) once and
 // nothing else is in the way: bound by memory and, at these sizes, by latency.
 //
 // The tensor cores would multiply a tile of 128 rows for them and cost a launch's
 // set-up (tensor maps, barriers, tensor memory); here a thread multiplies what it
-// loads.  One row through 4096 x 1024: 9.4 us on the tensor cores, 3.4 here.
+// loads.  4096 x 1024, forward / input gradient / weight and bias gradient, in us:
+// 1 row 4.1 / 4.6 / 2.9, 4 rows 5.7 / 6.9 / 3.8, 8 rows 8.5 / 11.2 / 5.1; on the
+// tensor cores 7.6 / 9.5 / 10.5 for up to 64 rows.  Hence up to 4 rows (weight
+// gradient 8) here.
 // Any alignment is read in place: 8 columns a thread where rows allow it, single
 // ones (32 neighbours a warp) where not.
 #include <algorithm>
@@ -34,6 +36,8 @@ template <int R, int VEC>
 __global__ __launch_bounds__(kThreads) void skinny_forward_kernel(
     const bf16* x, int64_t ldx, const bf16* w, int64_t ldw, int rows, int64_t k, int64_t n,
     const __grid_constant__ Epilogue e) {
+  constexpr int kRun = 1024;
+  __shared__ __align__(16) float xs[R][kRun];
   __shared__ float sums[8][R][kCols];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint32_t rank = block_rank(), ranks = cluster_blocks();
@@ -49,30 +53,38 @@ __global__ __launch_bounds__(kThreads) void skinny_forward_kernel(
 #pragma unroll
     for (int j = 0; j < kColsPerWarp; ++j) acc[r][j] = 0.0f;
   const int64_t col = c0 + warp * kColsPerWarp;
-  // several steps' loads in flight
-  constexpr int kUnroll = R <= 2 ? 4 : 2;
-  for (int64_t at = k0 + lane * VEC; at < k1; at += kStep * kUnroll) {
-    Raw<bf16, VEC> rw[kUnroll][kColsPerWarp];
+  // several steps' loads in flight; x comes from shared memory, a run at a time
+  constexpr int kUnroll = VEC == 1 ? 8 : R == 1 ? 4 : 2;
+  for (int64_t from = k0; from < k1; from += kRun) {
+    const int run = (int)min((int64_t)kRun, k1 - from);
+    __syncthreads();
+    for (int i = threadIdx.x; i < R * kRun; i += kThreads) {
+      const int r = i / kRun, j = i % kRun;
+      xs[r][j] = r < rows && j < run ? __bfloat162float(x[r * ldx + from + j]) : 0.0f;
+    }
+    __syncthreads();
+    for (int at = lane * VEC; at < run; at += kStep * kUnroll) {
+      Raw<bf16, VEC> rw[kUnroll][kColsPerWarp];
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u)
-#pragma unroll
-      for (int j = 0; j < kColsPerWarp; ++j)
-        rw[u][j] = load_raw<VEC>(w + (col + j) * ldw + at + u * kStep,
-                                 col + j < n ? (int)min((int64_t)VEC, k1 - at - u * kStep) : 0);
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      float fw[kColsPerWarp][VEC];
-#pragma unroll
-      for (int j = 0; j < kColsPerWarp; ++j) to_floats(rw[u][j], fw[j]);
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        float fx[VEC];
-        to_floats(load_raw<VEC>(x + r * ldx + at + u * kStep,
-                                r < rows ? (int)min((int64_t)VEC, k1 - at - u * kStep) : 0), fx);
+      for (int u = 0; u < kUnroll; ++u)
 #pragma unroll
         for (int j = 0; j < kColsPerWarp; ++j)
+          rw[u][j] = load_raw<VEC>(w + (col + j) * ldw + from + at + u * kStep,
+                                   col + j < n ? run - at - u * kStep : 0);
 #pragma unroll
-          for (int i = 0; i < VEC; ++i) acc[r][j] = fmaf(fx[i], fw[j][i], acc[r][j]);
+      for (int u = 0; u < kUnroll; ++u) {
+        if (at + u * kStep >= run) break;
+        float fw[kColsPerWarp][VEC];
+#pragma unroll
+        for (int j = 0; j < kColsPerWarp; ++j) to_floats(rw[u][j], fw[j]);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const float* fx = &xs[r][at + u * kStep];
+#pragma unroll
+          for (int j = 0; j < kColsPerWarp; ++j)
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) acc[r][j] = fmaf(fx[i], fw[j][i], acc[r][j]);
+        }
       }
     }
   }
@@ -117,7 +129,12 @@ __global__ __launch_bounds__(kThreads) void skinny_input_grad_kernel(
   constexpr int kPerRow = kGradCols / VEC;     // threads across the columns
   constexpr int kLanes = kThreads / kPerRow;   // weight rows at a time
   constexpr int kParts = VEC == 8 ? kWarps : kLanes;
-  __shared__ float part[kParts][R][kGradCols];
+  // values of dy for a run of weight rows; later the threads' partial sums
+  constexpr int kRun = 512;
+  __shared__ __align__(16) union {
+    float g[kRun][R];
+    float part[kParts][R][kGradCols];
+  } sh;
   __shared__ float sums[8][R][kGradCols];
   const uint32_t rank = block_rank(), ranks = cluster_blocks();
   cluster_begin();
@@ -132,27 +149,34 @@ __global__ __launch_bounds__(kThreads) void skinny_input_grad_kernel(
 #pragma unroll
     for (int i = 0; i < VEC; ++i) acc[r][i] = 0.0f;
   constexpr int kUnroll = 4;
-  for (int64_t i = n0 + first; i < n1; i += kLanes * kUnroll) {
-    Raw<bf16, VEC> rw[kUnroll];
-    float g[kUnroll][R];
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int64_t row = i + u * kLanes;
-      rw[u] = load_raw<VEC>(w + row * ldw + c, row < n1 ? have : 0);
-#pragma unroll
-      for (int r = 0; r < R; ++r)
-        g[u][r] = row < n1 && r < rows ? __bfloat162float(dy[r * lddy + row]) : 0.0f;
+  for (int64_t from = n0; from < n1; from += kRun) {
+    const int run = (int)min((int64_t)kRun, n1 - from);
+    __syncthreads();
+    for (int i = threadIdx.x; i < kRun * R; i += kThreads) {
+      const int r = i / kRun, j = i % kRun;
+      sh.g[j][r] = j < run && r < rows ? __bfloat162float(dy[r * lddy + from + j]) : 0.0f;
     }
+    __syncthreads();
+    for (int i = first; i < run; i += kLanes * kUnroll) {
+      Raw<bf16, VEC> rw[kUnroll];
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      float f[VEC];
-      to_floats(rw[u], f);
+      for (int u = 0; u < kUnroll; ++u)
+        rw[u] = load_raw<VEC>(w + (from + i + u * kLanes) * ldw + c, i + u * kLanes < run ? have : 0);
 #pragma unroll
-      for (int r = 0; r < R; ++r)
+      for (int u = 0; u < kUnroll; ++u) {
+        if (i + u * kLanes >= run) break;
+        float f[VEC];
+        to_floats(rw[u], f);
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) acc[r][j] = fmaf(g[u][r], f[j], acc[r][j]);
+        for (int r = 0; r < R; ++r) {
+          const float g = sh.g[i + u * kLanes][r];
+#pragma unroll
+          for (int j = 0; j < VEC; ++j) acc[r][j] = fmaf(g, f[j], acc[r][j]);
+        }
+      }
     }
   }
+  __syncthreads();
   if constexpr (VEC == 8) {
     // a warp holds 4 weight rows of the same 64 columns
 #pragma unroll
@@ -161,13 +185,13 @@ __global__ __launch_bounds__(kThreads) void skinny_input_grad_kernel(
       for (int j = 0; j < VEC; ++j) {
         acc[r][j] += __shfl_xor_sync(0xFFFFFFFFu, acc[r][j], 8);
         acc[r][j] += __shfl_xor_sync(0xFFFFFFFFu, acc[r][j], 16);
-        if ((threadIdx.x & 31) < 8) part[threadIdx.x >> 5][r][at * VEC + j] = acc[r][j];
+        if ((threadIdx.x & 31) < 8) sh.part[threadIdx.x >> 5][r][at * VEC + j] = acc[r][j];
       }
   } else {
 #pragma unroll
     for (int r = 0; r < R; ++r)
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) part[first % kParts][r][at * VEC + j] = acc[r][j];
+      for (int j = 0; j < VEC; ++j) sh.part[first % kParts][r][at * VEC + j] = acc[r][j];
   }
   __syncthreads();
   cluster_ready();
@@ -175,7 +199,7 @@ __global__ __launch_bounds__(kThreads) void skinny_input_grad_kernel(
     const int r = i / kGradCols, j = i % kGradCols;
     float s = 0.0f;
 #pragma unroll
-    for (int p = 0; p < kParts; ++p) s += part[p][r][j];
+    for (int p = 0; p < kParts; ++p) s += sh.part[p][r][j];
     to_first(&sums[rank][r][j], s);
   }
   cluster_done();
@@ -208,33 +232,80 @@ constexpr int kPerWarp = 8;
 template <int R, int VEC, typename T>
 __global__ __launch_bounds__(kThreads) void skinny_weight_grad_kernel(
     const bf16* dy, int64_t lddy, const bf16* x, int64_t ldx, const uint8_t* q, int64_t ldq,
-    const uint8_t* scale, int act, int rows, int64_t k, int64_t n, T* dw, int64_t lddw, T* db) {
+    const uint8_t* scale, bool x16, bool q8, int act, int rows, int64_t k, int64_t n, T* dw,
+    int64_t lddw, T* db) {
   // a lane's columns: VEC 8 neighbours, or 8 singles that lie 32 apart
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t across = (k + 255) / 256, down = blockIdx.x / across;
   const int64_t base = (blockIdx.x - down * across) * 256;
   auto column = [&](int i) { return VEC == 8 ? base + lane * 8 + i : base + i * 32 + lane; };
   const int64_t blocks_per_row = (k + kBlock - 1) / kBlock;
+  const int have = VEC == 8 ? (int)min((int64_t)8, k - column(0)) : 0;
   float a[R][8];
+  if (VEC == 8 && q && q8) {
+    // 8 neighbours of one block: a word pair and a scale
+    uint2 w[R];
+    uint32_t code[R];
 #pragma unroll
-  for (int r = 0; r < R; ++r)
+    for (int r = 0; r < R; ++r) {
+      w[r] = make_uint2(0, 0), code[r] = 1;
+      if (r >= rows || have <= 0) continue;
+      const uint8_t* p = q + r * ldq + column(0);
+      code[r] = scale[r * blocks_per_row + column(0) / kBlock];
+      if (have == 8) {
+        w[r] = *reinterpret_cast<const uint2*>(p);
+      } else {
+        for (int i = 0; i < have; ++i) (i < 4 ? w[r].x : w[r].y) |= (uint32_t)p[i] << (8 * (i & 3));
+      }
+    }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int64_t c = column(i);
-      float v = 0.0f;
-      if (r < rows && c < k) {
-        if (x) {
-          v = __bfloat162float(x[r * ldx + c]);
-        } else {
-          uint64_t lo, hi;
-          e4m3_pairs(q[r * ldq + c], lo, hi);
-          const float s = scale_value(scale[r * blocks_per_row + c / kBlock]);
-          float other;
-          unpair(mul2(lo, pair(s, s)), v, other);
+    for (int r = 0; r < R; ++r) {
+      const uint64_t s = pair(scale_value(code[r]), scale_value(code[r]));
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint64_t lo, hi;
+        e4m3_pairs(h ? w[r].y : w[r].x, lo, hi);
+        unpair(mul2(lo, s), a[r][4 * h], a[r][4 * h + 1]);
+        unpair(mul2(hi, s), a[r][4 * h + 2], a[r][4 * h + 3]);
+      }
+    }
+  } else if (VEC == 8 && x && x16) {
+    Raw<bf16, 8> raw[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) raw[r] = load_raw<8>(x + r * ldx + column(0), r < rows ? have : 0);
+#pragma unroll
+    for (int r = 0; r < R; ++r) to_floats(raw[r], a[r]);
+  } else {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      // a row's loads first, then what they mean
+      uint32_t w[8], code[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int64_t c = column(i);
+        w[i] = 0, code[i] = 1;
+        if (r < rows && c < k) {
+          if (x) {
+            w[i] = reinterpret_cast<const uint16_t*>(x)[r * ldx + c];
+          } else {
+            w[i] = q[r * ldq + c];
+            code[i] = scale[r * blocks_per_row + c / kBlock];
+          }
         }
       }
-      a[r][i] = v;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (x) {
+          a[r][i] = __uint_as_float(w[i] << 16);
+        } else {
+          uint64_t lo, hi;
+          e4m3_pairs(w[i], lo, hi);
+          float other;
+          unpair(mul2(lo, pair(scale_value(code[i]), scale_value(code[i]))), a[r][i], other);
+        }
+      }
     }
+  }
   if (act != SCAPE_ACT_NONE) {
 #pragma unroll
     for (int r = 0; r < R; ++r) {
@@ -301,17 +372,17 @@ cudaError_t launch(K kernel, int64_t clusters, int cluster, cudaStream_t st, A..
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-#define SCAPE_ROWS_SWITCH(rows, vec, CALL)                                        \
-  if (vec) {                                                                      \
-    constexpr int VEC = 8;                                                        \
-    if (rows == 1) { constexpr int R = 1; CALL; }                                 \
-    else if (rows <= 4) { constexpr int R = 4; CALL; }                            \
-    else { constexpr int R = 8; CALL; }                                           \
-  } else {                                                                        \
-    constexpr int VEC = 1;                                                        \
-    if (rows == 1) { constexpr int R = 1; CALL; }                                 \
-    else if (rows <= 4) { constexpr int R = 4; CALL; }                            \
-    else { constexpr int R = 8; CALL; }                                           \
+#define SCAPE_ROWS_SWITCH(rows, vec, MOST, CALL)        \
+  if (vec) {                                            \
+    constexpr int VEC = 8;                              \
+    if (rows == 1) { constexpr int R = 1; CALL; }       \
+    else if (rows <= 4) { constexpr int R = 4; CALL; }  \
+    else { constexpr int R = MOST; CALL; }              \
+  } else {                                              \
+    constexpr int VEC = 1;                              \
+    if (rows == 1) { constexpr int R = 1; CALL; }       \
+    else if (rows <= 4) { constexpr int R = 4; CALL; }  \
+    else { constexpr int R = MOST; CALL; }              \
   }
 
 }  // namespace
@@ -322,7 +393,7 @@ cudaError_t skinny_forward(const GemmCall& c, cudaStream_t st) {
   const int64_t clusters = ceil_div(c.n, kCols);
   const int s = cuts(clusters, c.k, 512);
   cudaError_t e = cudaSuccess;
-  SCAPE_ROWS_SWITCH(rows, vec, e = (launch(skinny_forward_kernel<R, VEC>, clusters, s, st, c.a.p, c.a.ld,
+  SCAPE_ROWS_SWITCH(rows, vec, kSkinnyRows, e = (launch(skinny_forward_kernel<R, VEC>, clusters, s, st, c.a.p, c.a.ld,
                                            c.b.p, c.b.ld, rows, c.k, c.n, c.e)));
   return e;
 }
@@ -332,22 +403,22 @@ cudaError_t skinny_input_grad(const GemmCall& c, cudaStream_t st) {
   const int64_t clusters = ceil_div(c.n, kGradCols);
   const int s = cuts(clusters, c.k, 128);
   cudaError_t e = cudaSuccess;
-  SCAPE_ROWS_SWITCH(rows, vec, e = (launch(skinny_input_grad_kernel<R, VEC>, clusters, s, st, c.a.p,
+  SCAPE_ROWS_SWITCH(rows, vec, kSkinnyRows, e = (launch(skinny_input_grad_kernel<R, VEC>, clusters, s, st, c.a.p,
                                            c.a.ld, c.b.p, c.b.ld, rows, c.n, c.k, c.e)));
   return e;
 }
 cudaError_t skinny_weight_grad(const SkinnyWeightGrad& a, cudaStream_t st) {
   const size_t ge = a.out_f32 ? 4 : 2;
-  const bool vec = rows16(a.dw, a.lddw, ge);
+  const bool vec = rows16(a.dw, a.lddw, ge), x16 = rows16(a.x, a.ldx, 2), q8 = rows8(a.q, a.ldq);
   const int rows = (int)a.rows;
   const unsigned grid = (unsigned)(ceil_div(a.k, 256) * ceil_div(a.n, kWarps * kPerWarp));
   if (a.out_f32) {
-    SCAPE_ROWS_SWITCH(rows, vec, (skinny_weight_grad_kernel<R, VEC, float><<<grid, kThreads, 0, st>>>(
-                                     a.dy, a.lddy, a.x, a.ldx, a.q, a.ldq, a.scale, a.act, rows, a.k, a.n,
+    SCAPE_ROWS_SWITCH(rows, vec, kSkinnyWeightRows, (skinny_weight_grad_kernel<R, VEC, float><<<grid, kThreads, 0, st>>>(
+                                     a.dy, a.lddy, a.x, a.ldx, a.q, a.ldq, a.scale, x16, q8, a.act, rows, a.k, a.n,
                                      static_cast<float*>(a.dw), a.lddw, static_cast<float*>(a.db))));
   } else {
-    SCAPE_ROWS_SWITCH(rows, vec, (skinny_weight_grad_kernel<R, VEC, bf16><<<grid, kThreads, 0, st>>>(
-                                     a.dy, a.lddy, a.x, a.ldx, a.q, a.ldq, a.scale, a.act, rows, a.k, a.n,
+    SCAPE_ROWS_SWITCH(rows, vec, kSkinnyWeightRows, (skinny_weight_grad_kernel<R, VEC, bf16><<<grid, kThreads, 0, st>>>(
+                                     a.dy, a.lddy, a.x, a.ldx, a.q, a.ldq, a.scale, x16, q8, a.act, rows, a.k, a.n,
                                      static_cast<bf16*>(a.dw), a.lddw, static_cast<bf16*>(a.db))));
   }
   return cudaGetLastError();

@@ -73,7 +73,7 @@ def test_linear_refusals(lib):
     assert n.value == 0  # aligned operands need none
     assert lib.scape_layer_linear_workspace(A, 65, A, 64, 16, 64, 32, ctypes.byref(n)) == C.SCAPE_OK
     assert n.value >= 16 * 64 * 2
-    assert lib.scape_layer_linear_workspace(A, 65, A, 64, 8, 64, 32, ctypes.byref(n)) == C.SCAPE_OK
+    assert lib.scape_layer_linear_workspace(A, 65, A, 64, 4, 64, 32, ctypes.byref(n)) == C.SCAPE_OK
     assert n.value == 0  # few rows are read in place whatever their alignment
 
     def f(x=A, ldx=64, rows=16, k=64, act=0, y=A, ws=None, nbytes=0):
