@@ -276,6 +276,9 @@ constexpr int kBK = 64;   // contraction a stage: one 128-byte swizzled row of b
 constexpr int kChunk = 8192;       // bytes of 64 staged rows of 128 bytes
 constexpr int kBoxBytes = 2048;    // 32 x 32 bfloat16 on their way out
 constexpr int kTileCost = 500;     // clocks a tile costs besides its stages
+// A second, split launch: clocks a stage of a 128 x 128 tile, and besides.
+constexpr int kSmallStage = 600;
+constexpr int kSmallLaunch = 9000;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 
 // How a product is laid over the blocks.
@@ -377,15 +380,14 @@ __device__ __forceinline__ void pack_row(const float (&v)[N], int left, bool liv
     for (int i = 0; i < N; ++i) z[i] = i < left ? v[i] : 0.0f;
   }
   uint32_t top = block_top<N>(part_top<N>(z));
-  bool no_inf = true;
   if (__any_sync(0xFFFFFFFFu, top >= kInfBits)) {
-    const uint32_t finite = block_top<N>(part_top_finite<N>(z));
-    if (top >= kInfBits) top = finite;
-    no_inf = false;
+    top = block_top<N>(part_top_finite<N>(z));
+#pragma unroll
+    for (int i = 0; i < N; ++i) z[i] = nan_unless_finite(z[i]);
   }
   const uint32_t code = scale_code(top);
   uint32_t w[N / 4];
-  to_e4m3<N>(z, scale_inverse(code), no_inf, w);
+  to_e4m3<N>(z, scale_inverse(code), w);
   if (!live || left <= 0) return;
   uint8_t* q = e.q + row * e.ldq + c0;
   if (left >= N && e.q_vec) {
@@ -569,6 +571,10 @@ struct GemmShape {
   int bn;       // columns of a tile
   int a_bytes;  // of operand A a block copies for a stage
   int tiles_m, tiles_n, ksteps;
+  int tiles;  // this launch's
+  // a split launch for the tiles that pairs left over: pair tiles from tile_base
+  // on, each cut into 2 x sub_n of this launch's (sub_n 0: tiles of its own)
+  int tile_base, sub_n;
   unsigned int* status;
 };
 
@@ -639,7 +645,7 @@ __global__ __launch_bounds__(Tile<KIND, BN, MODE>::kThreads, 1) void gemm_kernel
 
   const int bn = PAIR ? s.bn : BN;
   const int b_rows = PAIR ? bn / 2 : BN;  // operand B rows this block stages
-  const int tiles = s.tiles_m * s.tiles_n;
+  const int tiles = s.tiles;
   const int first = blockIdx.x / ranks;
   const int step = PAIR ? gridDim.x / 2 : tiles;
   const int k0 = PAIR ? 0 : (int)((int64_t)s.ksteps * rank / ranks);
@@ -647,12 +653,21 @@ __global__ __launch_bounds__(Tile<KIND, BN, MODE>::kThreads, 1) void gemm_kernel
   // Tiles are taken down strips of 8 tile rows, so that the blocks at work at one
   // time share operand rows in L2.
   auto tile_at = [&](int t, int& tm, int& tn) {
+    int part = 0;
+    if (!PAIR && s.sub_n) {
+      part = t % (2 * s.sub_n);
+      t = s.tile_base + t / (2 * s.sub_n);
+    }
     const int strip = t / (8 * s.tiles_n);
     const int base = strip * 8;
     const int high = min(8, s.tiles_m - base);
     const int r = t - strip * 8 * s.tiles_n;
     tm = base + r % high;
     tn = r / high;
+    if (!PAIR && s.sub_n) {
+      tm = 2 * tm + part / s.sub_n;
+      tn = tn * s.sub_n + part % s.sub_n;
+    }
   };
 
   if (warp == 0 && lane == 0) {
@@ -911,8 +926,16 @@ __global__ __launch_bounds__(Tile<KIND, BN, MODE>::kThreads, 1) void gemm_kernel
 }
 
 // ------------------------------------------------------------------ launch
+// The tiles of a launch, where they are not all there are: pairs take the first
+// `count`; a split launch takes what is left of a grid of pair tiles of `of_bn`
+// columns, from `base` on.
+struct TileRange {
+  int64_t count = 0, base = 0;
+  int of_bn = 0;
+};
+
 template <int KIND, int BN, int MODE>
-cudaError_t gemm_launch(const GemmCall& c, int bn, int split, cudaStream_t st) {
+cudaError_t gemm_launch(const GemmCall& c, int bn, int split, cudaStream_t st, TileRange range = {}) {
   using TL = Tile<KIND, BN, MODE>;
   constexpr bool PAIR = MODE == kModePair;
   constexpr bool TA = KIND == kGemmWeightGrad;
@@ -936,14 +959,19 @@ cudaError_t gemm_launch(const GemmCall& c, int bn, int split, cudaStream_t st) {
   s.n = (int)c.n;
   s.bn = bn;
   s.a_bytes = TA ? TL::kABytes : a_rows * kBK * 2;
-  s.tiles_m = (int)ceil_div(c.m, PAIR ? 2 * kBM : kBM);
-  s.tiles_n = (int)ceil_div(c.n, bn);
+  const bool rest = range.of_bn != 0;
+  s.tiles_m = (int)ceil_div(c.m, PAIR || rest ? 2 * kBM : kBM);
+  s.tiles_n = (int)ceil_div(c.n, rest ? range.of_bn : bn);
+  s.sub_n = rest ? range.of_bn / bn : 0;
+  s.tile_base = (int)range.base;
+  s.tiles = rest ? (int)((s.tiles_m * (int64_t)s.tiles_n - range.base) * 2 * s.sub_n)
+                 : range.count ? (int)range.count : s.tiles_m * s.tiles_n;
   s.ksteps = (int)ceil_div(c.k, kBK);
   if (err == cudaSuccess) err = gemm_status_word(&s.status);
   auto kernel = gemm_kernel<KIND, BN, MODE>;
   if (err == cudaSuccess) err = gemm_allow_smem((const void*)kernel, TL::kSmem);
   if (err != cudaSuccess) return err;
-  const int64_t tiles = (int64_t)s.tiles_m * s.tiles_n;
+  const int64_t tiles = s.tiles;
   const int cluster = PAIR ? 2 : split;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(PAIR ? 2 * std::min<int64_t>(tiles, sm_count() / 2) : tiles * split));
@@ -964,21 +992,40 @@ cudaError_t gemm_launch(const GemmCall& c, int bn, int split, cudaStream_t st) {
 // number of tiles the busiest pair gets times a tile's.  A stage of a tile takes
 // 2 clocks a column on the tensor cores, or 18 a kilobyte that comes into the SM
 // (measured: 590 clocks for 32 KB, whatever the width), whichever is more.  The
-// width with the least time is taken.  Pairs want at least 3/4 of the SMs at
+// width with the least time is taken, or whole rounds of pairs with a second
+// launch for the tiles left over (4096 x 1280, contraction 3584: 80 tiles for 76
+// pairs, 42 us in two rounds, 30 us so).  Pairs want at least 3/4 of the SMs at
 // work.  Below that, narrow tiles, each cut over a cluster as far as there are
 // SMs and at least four stages of the contraction for every block.
 template <int KIND>
 cudaError_t gemm_run(const GemmCall& c, cudaStream_t st) {
   const int64_t sms = sm_count(), pairs = sms / 2;
   const int64_t tp = ceil_div(c.m, 2 * kBM), ksteps = ceil_div(c.k, kBK);
-  int best = 0;
+  int best = 0, best_split = 0;
   int64_t least = 0;
   for (int bn = 256; bn >= 128; bn -= 32) {
     const int64_t tiles = tp * ceil_div(c.n, bn);
     const int64_t kb = 16 + (KIND == kGemmForward ? bn / 16 : ceil_div(bn, 128) * 8);
     const int64_t tile = ksteps * std::max<int64_t>(2 * bn, 18 * kb) + kTileCost;
     const int64_t cost = ceil_div(tiles, pairs) * tile;
-    if (tiles * 4 >= pairs * 3 && (best == 0 || cost < least)) best = bn, least = cost;
+    if (tiles * 4 >= pairs * 3 && (best == 0 || cost < least)) best = bn, best_split = 0, least = cost;
+    // whole rounds of pairs, and the tiles left over as 128 x 128 ones cut over
+    // clusters, all at one time
+    const int64_t rest = tiles % pairs;
+    if (bn % 128 != 0 || tiles < pairs || rest == 0) continue;
+    const int64_t small = rest * 2 * (bn / 128);
+    int split = 1;
+    while (split < 8 && small <= gemm_clusters(split * 2) && ksteps / (split * 2) >= 4) split *= 2;
+    const int64_t both_cost = tiles / pairs * tile + ceil_div(ksteps, split) * kSmallStage + kSmallLaunch;
+    if (small <= gemm_clusters(split) && both_cost < least) best = bn, best_split = split, least = both_cost;
+  }
+  if (best && best_split) {
+    const int64_t whole = tp * ceil_div(c.n, best) / pairs * pairs;
+    TileRange first, rest;
+    first.count = rest.base = whole;
+    rest.of_bn = best;
+    const cudaError_t e = gemm_launch<KIND, 256, kModePair>(c, best, 2, st, first);
+    return e != cudaSuccess ? e : gemm_launch<KIND, 128, kModeSplit>(c, 128, best_split, st, rest);
   }
   if (best) return gemm_launch<KIND, 256, kModePair>(c, best, 2, st);
   const int64_t tm = ceil_div(c.m, kBM);

@@ -222,18 +222,13 @@ __device__ __forceinline__ uint32_t part_top_finite(const float (&v)[N]) {
 // e4m3 words of N values (N a multiple of 4) at a scale.  Scaling by a power of
 // two is exact down to the subnormals, where e4m3 is 0.
 template <int N>
-__device__ __forceinline__ void to_e4m3(const float (&v)[N], float inv, bool no_inf,
-                                        uint32_t (&w)[N / 4]) {
+__device__ __forceinline__ void to_e4m3(const float (&v)[N], float inv, uint32_t (&w)[N / 4]) {
   const uint64_t inv2 = pair(inv, inv);
 #pragma unroll
   for (int i = 0; i < N / 4; ++i) {
     float a, b, c, d;
     unpair(mul2(pair(v[4 * i], v[4 * i + 1]), inv2), a, b);
     unpair(mul2(pair(v[4 * i + 2], v[4 * i + 3]), inv2), c, d);
-    if (!no_inf) {
-      a = nan_unless_finite(a), b = nan_unless_finite(b);
-      c = nan_unless_finite(c), d = nan_unless_finite(d);
-    }
     w[i] = e4m3_pair(a, b) | (e4m3_pair(c, d) << 16);
   }
 }
@@ -250,15 +245,17 @@ __device__ __forceinline__ void e4m3_pairs(uint32_t w, uint64_t& lo, uint64_t& h
 // real (the others are 0).  q is on 8 bytes, or 16 where q16 says so (VEC 1: any).
 // All 32 lanes call it together.
 template <int VEC>
-__device__ __forceinline__ void warp_pack(const float (&v)[VEC], int n, uint8_t* q, uint8_t* scale,
-                                          bool writes_scale, bool q16) {
+__device__ __forceinline__ void warp_pack(const float (&values)[VEC], int n, uint8_t* q,
+                                          uint8_t* scale, bool writes_scale, bool q16) {
+  float v[VEC];
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) v[i] = values[i];
   uint32_t top = part_top<VEC>(v);
-  bool no_inf = true;
   if constexpr (VEC == 1) {
     top = __reduce_max_sync(0xFFFFFFFFu, top);
     if (top >= kInfBits) {
       top = __reduce_max_sync(0xFFFFFFFFu, part_top_finite<VEC>(v));
-      no_inf = false;
+      v[0] = nan_unless_finite(v[0]);
     }
   } else {
     auto over_lanes = [](uint32_t t) {
@@ -269,17 +266,17 @@ __device__ __forceinline__ void warp_pack(const float (&v)[VEC], int n, uint8_t*
     top = over_lanes(top);
     if (__any_sync(0xFFFFFFFFu, top >= kInfBits)) {
       top = over_lanes(part_top_finite<VEC>(v));
-      no_inf = false;
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) v[i] = nan_unless_finite(v[i]);
     }
   }
   const uint32_t code = scale_code(top);
   const float inv = scale_inverse(code);
   if constexpr (VEC == 1) {
-    const float x = v[0] * inv;
-    if (n > 0) *q = (uint8_t)e4m3_pair(no_inf ? x : nan_unless_finite(x), 0.0f);
+    if (n > 0) *q = (uint8_t)e4m3_pair(v[0] * inv, 0.0f);
   } else {
     uint32_t w[VEC / 4];
-    to_e4m3<VEC>(v, inv, no_inf, w);
+    to_e4m3<VEC>(v, inv, w);
     if (n >= VEC) {
       if constexpr (VEC == 16) {
         if (q16) {

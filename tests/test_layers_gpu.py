@@ -327,6 +327,31 @@ def test_linear_large_tiles_every_layout(cuda_device):
     assert L.status() == 0
 
 
+@pytest.mark.parametrize("m,n,k", [(4100, 1276, 3592), (4096, 1280, 3584)])
+def test_linear_tiles_left_over(cuda_device, m, n, k):
+    """A few more tiles than the GPU takes at one time and a long contraction: the
+    last ones go out in a launch of their own.  m x n outputs, contraction k."""
+    act, pre = "silu", L.pack8(rand(9, m, n, scale=2.0))
+    x, w, b, res = rand(1, m, k), rand(2, n, k, scale=0.03), rand(3, n), rand(4, m, n)
+    z, e = x.double() @ w.double().t() + b.double(), product_error(x, w.t(), k)
+    a = R.act(z, act)
+    y, z8 = L.linear(x, w, bias=b, residual=res, activation=act, keep_pre=True)
+    want = a + res.double()
+    near(y, want, want.abs() * R.U_BF16 + 1.2 * e + z.abs() * 2.0 ** -23 + a.abs() * R.ACT_REL
+         + res.double().abs() * 2.0 ** -23, "y")
+    near(L.unpack8(z8, dtype=F32), z, R.pack_error(z) + 1.1 * e + z.abs() * 2.0 ** -23
+         + R.blocks(e).amax(-1).repeat_interleave(32, dim=1)[:, :n] * 2.0 ** -17, "z8")
+    w2 = rand(5, k, n, scale=0.03)
+    want, e, s = x.double() @ w2.double(), product_error(x, w2, k), R.slope(vals(pre), act)
+    near(L.linear_backward_input(x, w2, pre=pre, activation=act), want * s,
+         (want * s).abs() * R.U_BF16 + e * 1.2 + want.abs() * 3 * R.ACT_REL, "dx")
+    dy, x2 = rand(6, k, m, scale=0.01), rand(7, k, n)
+    want, e = dy.double().t() @ x2.double(), product_error(dy.t(), x2, k)
+    near(L.linear_backward_weight(dy, x2), want, want.abs() * R.U_BF16 + e, "dw")
+    near(L.linear_backward_weight(dy, x2, grad_dtype=F32), want, want.abs() * R.U_F32 + e, "dw32")
+    assert L.status() == 0
+
+
 def test_linear_gradients_against_differences(cuda_device):
     """d/dt of sum(c * act-linear(x)) with the input made by gelu from z: the
     64-bit formula's central differences along random directions of z and w."""
