@@ -54,6 +54,7 @@ struct AlignCopies {
   AlignCopy m[2];
 };
 __global__ __launch_bounds__(256) void align_rows_kernel(const __grid_constant__ AlignCopies a) {
+  start();
   const AlignCopy& m = a.m[blockIdx.z];
   // a block covers 8 rows of 32 vectors, or what of them there is
   const int64_t c = ((int64_t)blockIdx.x * 32 + (threadIdx.x & 31)) * 8;
@@ -105,8 +106,8 @@ cudaError_t operands(const Matrix& a, const Matrix& b, bool any_rows, uint8_t* w
     y = std::max(y, ceil_div(c.rows, 8));
   }
   if (n == 0) return cudaSuccess;
-  align_rows_kernel<<<dim3((unsigned)x, (unsigned)std::min<int64_t>(y, 32768), (unsigned)n), 256, 0, st>>>(copies);
-  return cudaGetLastError();
+  return launch_kernel(align_rows_kernel, dim3((unsigned)x, (unsigned)std::min<int64_t>(y, 32768), (unsigned)n),
+                       256, 0, 0, st, copies);
 }
 
 int check_workspace(const void* ws, size_t have, size_t need) {

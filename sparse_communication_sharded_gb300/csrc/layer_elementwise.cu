@@ -58,6 +58,7 @@ __global__ __launch_bounds__(kThreads) void pack8_kernel(const T* x, int64_t ldx
                                                          FastDiv per_row, int64_t cols, uint8_t* q,
                                                          int64_t ldq, uint8_t* scale,
                                                          int64_t blocks_per_row) {
+  start();
   constexpr int U = unroll<VEC>();
   const uint32_t first = blockIdx.x * (kThreads * U) + threadIdx.x;
   Unit un[U];
@@ -114,6 +115,7 @@ __global__ __launch_bounds__(kThreads) void unpack8_kernel(const uint8_t* q, int
                                                            int64_t blocks_per_row, uint32_t units,
                                                            FastDiv per_row, int64_t cols, T* y,
                                                            int64_t ldy) {
+  start();
   constexpr int U = unroll<VEC>();
   const uint32_t first = blockIdx.x * (kThreads * U) + threadIdx.x;
   Unit un[U];
@@ -150,6 +152,7 @@ template <typename T, int VEC, int ACT>
 __global__ __launch_bounds__(kThreads) void act_grad_kernel(
     const T* dy, int64_t lddy, const uint8_t* q, int64_t ldq, const uint8_t* scale,
     int64_t blocks_per_row, uint32_t units, FastDiv per_row, int64_t cols, T* dz, int64_t lddz) {
+  start();
   constexpr int U = unroll<VEC>();
   const uint32_t first = blockIdx.x * (kThreads * U) + threadIdx.x;
   Unit un[U];
@@ -192,9 +195,8 @@ cudaError_t for_row_ranges(int64_t rows, int64_t cols, F&& launch) {
   const int64_t step = std::max<int64_t>(1, (int64_t{1} << 30) / per_row);
   for (int64_t r = 0; r < rows; r += step) {
     const int64_t units = std::min(step, rows - r) * per_row;
-    launch(r, (uint32_t)units, FastDiv((uint32_t)per_row),
-           (unsigned)ceil_div(units, kThreads * unroll<VEC>()));
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e = launch(r, (uint32_t)units, FastDiv((uint32_t)per_row),
+                                 (unsigned)ceil_div(units, kThreads * unroll<VEC>()));
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
@@ -205,8 +207,8 @@ cudaError_t run_pack8(const T* x, int64_t ldx, int64_t rows, int64_t cols, uint8
                       uint8_t* scale, cudaStream_t st) {
   const int64_t bpr = ceil_div(cols, kBlock);
   return for_row_ranges<VEC>(rows, cols, [&](int64_t r, uint32_t units, FastDiv d, unsigned grid) {
-    pack8_kernel<T, VEC><<<grid, kThreads, 0, st>>>(x + r * ldx, ldx, units, d, cols, q + r * ldq,
-                                                    ldq, scale + r * bpr, bpr);
+    return launch_kernel(pack8_kernel<T, VEC>, grid, kThreads, 0, 0, st, x + r * ldx, ldx, units, d, cols,
+                         q + r * ldq, ldq, scale + r * bpr, bpr);
   });
 }
 template <typename T, int VEC>
@@ -214,9 +216,10 @@ cudaError_t run_unpack8(const uint8_t* q, int64_t ldq, const uint8_t* scale, int
                         int64_t cols, int act, T* y, int64_t ldy, cudaStream_t st) {
   const int64_t bpr = ceil_div(cols, kBlock);
   return for_row_ranges<VEC>(rows, cols, [&](int64_t r, uint32_t units, FastDiv d, unsigned grid) {
-    SCAPE_ACT_SWITCH(act, (unpack8_kernel<T, VEC, ACT><<<grid, kThreads, 0, st>>>(
-                              q + r * ldq, ldq, scale + r * bpr, bpr, units, d, cols, y + r * ldy,
-                              ldy)));
+    cudaError_t e = cudaSuccess;
+    SCAPE_ACT_SWITCH(act, e = (launch_kernel(unpack8_kernel<T, VEC, ACT>, grid, kThreads, 0, 0, st, q + r * ldq,
+                                             ldq, scale + r * bpr, bpr, units, d, cols, y + r * ldy, ldy)));
+    return e;
   });
 }
 template <typename T, int VEC>
@@ -225,12 +228,13 @@ cudaError_t run_act_grad(const T* dy, int64_t lddy, const uint8_t* q, int64_t ld
                          int64_t lddz, cudaStream_t st) {
   const int64_t bpr = ceil_div(cols, kBlock);
   return for_row_ranges<VEC>(rows, cols, [&](int64_t r, uint32_t units, FastDiv d, unsigned grid) {
-    SCAPE_ACT_SWITCH(act, (act_grad_kernel<T, VEC, ACT><<<grid, kThreads, 0, st>>>(
-                              dy + r * lddy, lddy, q + r * ldq, ldq, scale + r * bpr, bpr, units,
-                              d, cols, dz + r * lddz, lddz)));
+    cudaError_t e = cudaSuccess;
+    SCAPE_ACT_SWITCH(act, e = (launch_kernel(act_grad_kernel<T, VEC, ACT>, grid, kThreads, 0, 0, st,
+                                             dy + r * lddy, lddy, q + r * ldq, ldq, scale + r * bpr, bpr,
+                                             units, d, cols, dz + r * lddz, lddz)));
+    return e;
   });
 }
-
 
 // Columns a thread, as the rows' alignment allows: 16 (one 16-byte word of 8-bit
 // values), 8, or 1: a warp then reads 32 neighbouring columns, a whole block, at

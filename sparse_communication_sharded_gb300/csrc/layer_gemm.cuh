@@ -588,6 +588,7 @@ __global__ __launch_bounds__(Tile<KIND, BN, MODE>::kThreads, 1) void gemm_kernel
   constexpr bool TA = KIND == kGemmWeightGrad;
   constexpr bool TB = KIND != kGemmForward;
   constexpr int kTileRows = PAIR ? 2 * kBM : kBM;
+  let_next_start();
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t bars[2 * TL::kStages + 5];
   __shared__ uint32_t tmem_base;
@@ -625,6 +626,7 @@ __global__ __launch_bounds__(Tile<KIND, BN, MODE>::kThreads, 1) void gemm_kernel
   if constexpr (PAIR) cluster_sync();
   tc_fence_after();
   const uint32_t tmem = tmem_base;
+  wait_for_earlier();  // all of the above is this kernel's own
 
   // Every wait ends: after the limit the kernel records it and all its roles
   // stop (they look at gave_up while they wait).
@@ -973,18 +975,8 @@ cudaError_t gemm_launch(const GemmCall& c, int bn, int split, cudaStream_t st, T
   if (err != cudaSuccess) return err;
   const int64_t tiles = s.tiles;
   const int cluster = PAIR ? 2 : split;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(PAIR ? 2 * std::min<int64_t>(tiles, sm_count() / 2) : tiles * split));
-  cfg.blockDim = dim3(TL::kThreads);
-  cfg.dynamicSmemBytes = TL::kSmem;
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = (unsigned)cluster;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, ma, mb, mo, s, c.e);
+  const int64_t grid = PAIR ? 2 * std::min<int64_t>(tiles, sm_count() / 2) : tiles * split;
+  return launch_kernel(kernel, (unsigned)grid, TL::kThreads, TL::kSmem, cluster, st, ma, mb, mo, s, c.e);
 }
 
 // Tile and mode.  Pairs do the most work a byte read and keep the tensor cores

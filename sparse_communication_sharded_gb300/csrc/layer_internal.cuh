@@ -464,6 +464,41 @@ __device__ __forceinline__ float act_exact(float z) {
     default: { constexpr int ACT = SCAPE_ACT_NONE; CALL; break; }             \
   }
 
+// ------------------------------------------------------------------ launches
+// Every kernel here is launched so that it may start while the one before it on
+// the stream ends: start() lets the next one do the same, and waits until all
+// earlier work is complete and visible.  Nothing is read or written before it.
+// What overlaps is the launch and the set-up (64 x 256 through 256 x 256, one
+// after the other: 8.2 us a call without, 5.2 with).
+__device__ __forceinline__ void let_next_start() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void wait_for_earlier() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+__device__ __forceinline__ void start() {
+  let_next_start();
+  wait_for_earlier();
+}
+template <typename... P, typename... A>
+cudaError_t launch_kernel(void (*kernel)(P...), dim3 grid, int threads, size_t smem, int cluster,
+                          cudaStream_t st, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = (unsigned)cluster;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = cluster ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
 // ------------------------------------------------------------------ clusters
 // Blocks of a cluster that give sums to the first one: cluster_begin() at the
 // start, cluster_ready() before the first to_first() (all blocks have begun by

@@ -43,9 +43,10 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
   }
   return s;
 }
+// The places of warps that the block does not have; block_sum's own barrier makes
+// them visible.
 __device__ __forceinline__ void clear_sums(float (*red)[16]) {
-  if (threadIdx.x < 32) red[threadIdx.x >> 4][threadIdx.x & 15] = 0.0f;
-  __syncthreads();
+  if (threadIdx.x < 32 && (threadIdx.x & 15) >= blockDim.x >> 5) red[threadIdx.x >> 4][threadIdx.x & 15] = 0.0f;
 }
 // 1 / sqrt(x): the hardware's estimate and one Newton step.
 __device__ __forceinline__ float inverse_root(float x) {
@@ -113,6 +114,7 @@ __global__ __launch_bounds__(Team<WIDTH>::kThreads) void norm_fwd_kernel(
     const __grid_constant__ NormFwd a, bool w_vec, float inv_cols) {
   using TM = Team<WIDTH>;
   constexpr int P = NV * VEC / 2;
+  start();
   __shared__ __align__(16) float red[2][16];
   if (!TM::kWarp) clear_sums(red);
   const int t = TM::lane(), width = TM::width();
@@ -171,6 +173,7 @@ __global__ __launch_bounds__(Team<WIDTH>::kThreads) void norm_fwd_kernel(
 // Any width: the row is read a second time (from the caches) for the outputs.
 template <typename T>
 __global__ __launch_bounds__(512) void norm_fwd_wide_kernel(NormFwd a) {
+  start();
   __shared__ __align__(16) float red[2][16];
   clear_sums(red);
   const int64_t blocks_per_row = (a.cols + kBlock - 1) / kBlock;
@@ -212,6 +215,7 @@ __global__ __launch_bounds__(Team<WIDTH>::kThreads, (VEC == 8 && sizeof(T) == 2 
     const __grid_constant__ NormBwd a, bool w_vec, float inv_cols) {
   using TM = Team<WIDTH>;
   constexpr int P = NV * VEC / 2;
+  start();
   __shared__ __align__(16) float red[2][16];
   __shared__ float cross[TM::kWarp ? kWarpRows * kWarpColsBwd : 1];
   if (!TM::kWarp) clear_sums(red);
@@ -304,6 +308,7 @@ __global__ __launch_bounds__(Team<WIDTH>::kThreads, (VEC == 8 && sizeof(T) == 2 
 
 template <typename T>
 __global__ __launch_bounds__(512) void norm_bwd_wide_kernel(NormBwd a) {
+  start();
   __shared__ __align__(16) float red[2][16];
   clear_sums(red);
   int flip = 0;
@@ -333,6 +338,7 @@ __global__ __launch_bounds__(512) void norm_bwd_wide_kernel(NormBwd a) {
 // (x, y) sums rows y, y + gridDim.y, ... of its 256 columns.
 template <typename T>
 __global__ __launch_bounds__(256) void norm_dw_wide_kernel(NormBwd a) {
+  start();
   const int c = blockIdx.x * 256 + threadIdx.x;
   if (c >= a.cols) return;
   float s = 0.0f;
@@ -358,6 +364,7 @@ __global__ __launch_bounds__(kSumThreads) void colsum_kernel(
   __shared__ float sums[kSumBlocks][kSumCols];
   const uint32_t rank = block_rank(), ranks = cluster_blocks();
   cluster_begin();
+  start();
   const int at = threadIdx.x % kPerRow, r0 = threadIdx.x / kPerRow;
   const int64_t c = (int64_t)(blockIdx.x / ranks) * kSumCols + at * VEC;
   const int n = (int)min((int64_t)VEC, cols - c);
@@ -418,6 +425,7 @@ __global__ __launch_bounds__(32 * kPartWarps) void sum_partials_kernel(
   __shared__ float sums[kPartBlocks][32];
   const uint32_t rank = block_rank(), ranks = cluster_blocks();
   cluster_begin();
+  start();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t c = (int64_t)(blockIdx.x / ranks) * 32 + lane;
   float s = 0.0f;
@@ -515,8 +523,8 @@ constexpr int bwd_threads() { return sizeof(T) == 2 ? 1024 : 512; }
 template <typename T>
 cudaError_t run_norm_fwd(NormFwd a, cudaStream_t st) {
   if (a.cols > kBlockCols) {
-    norm_fwd_wide_kernel<T><<<(unsigned)std::min<int64_t>(a.rows, (int64_t)sm_count() * 4), 512, 0, st>>>(a);
-    return cudaGetLastError();
+    return launch_kernel(norm_fwd_wide_kernel<T>, (unsigned)std::min<int64_t>(a.rows, (int64_t)sm_count() * 4),
+                         512, 0, 0, st, a);
   }
   const size_t e = sizeof(T);
   const bool vec = rows16(a.x, a.ldx, e) && rows16(a.res, a.ldres, e) && rows16(a.y, a.ldy, e) &&
@@ -525,20 +533,23 @@ cudaError_t run_norm_fwd(NormFwd a, cudaStream_t st) {
   const bool wv = aligned(a.w, 16);
   const float inv = (float)(1.0 / a.cols);
   const Shape s = shape_of(a.rows, a.cols, vec, kWarpCols, kFwdThreads);
-  SCAPE_SHAPE_SWITCH(vec, s, kWarpCols, (norm_fwd_kernel<T, VEC, NV, WIDTH><<<s.grid, s.threads, 0, st>>>(a, wv, inv)));
-  return cudaGetLastError();
+  cudaError_t err = cudaSuccess;
+  SCAPE_SHAPE_SWITCH(vec, s, kWarpCols, err = (launch_kernel(norm_fwd_kernel<T, VEC, NV, WIDTH>, s.grid, s.threads,
+                                                             0, 0, st, a, wv, inv)));
+  return err;
 }
 
 template <typename T>
 cudaError_t run_norm_bwd(const NormBwd& a, cudaStream_t st) {
   int64_t parts = norm_bwd_partials(a.rows, a.cols);
+  cudaError_t err = cudaSuccess;
   if (a.cols > kBlockCols) {
-    if (a.dw) {
-      norm_dw_wide_kernel<T><<<dim3((unsigned)ceil_div(a.cols, 256), (unsigned)parts), 256, 0, st>>>(a);
-      const cudaError_t e = cudaGetLastError();
-      if (e != cudaSuccess) return e;
-    }
-    norm_bwd_wide_kernel<T><<<(unsigned)std::min<int64_t>(a.rows, (int64_t)sm_count() * 4), 512, 0, st>>>(a);
+    if (a.dw)
+      err = launch_kernel(norm_dw_wide_kernel<T>, dim3((unsigned)ceil_div(a.cols, 256), (unsigned)parts), 256, 0,
+                          0, st, a);
+    if (err == cudaSuccess)
+      err = launch_kernel(norm_bwd_wide_kernel<T>, (unsigned)std::min<int64_t>(a.rows, (int64_t)sm_count() * 4),
+                          512, 0, 0, st, a);
   } else {
     const size_t e = sizeof(T);
     const bool vec = rows16(a.dy, a.lddy, e) && rows16(a.h, a.ldh, e) &&
@@ -546,11 +557,11 @@ cudaError_t run_norm_bwd(const NormBwd& a, cudaStream_t st) {
     const bool wv = aligned(a.w, 16);
     const float inv = (float)(1.0 / a.cols);
     const Shape s = shape_of(a.rows, a.cols, vec, kWarpColsBwd, vec && a.cols <= 4096 ? bwd_threads<T>() : 512);
-    SCAPE_SHAPE_SWITCH(vec, s, kWarpColsBwd, (norm_bwd_kernel<T, VEC, NV, WIDTH><<<s.grid, s.threads, 0, st>>>(a, wv, inv)));
+    SCAPE_SHAPE_SWITCH(vec, s, kWarpColsBwd, err = (launch_kernel(norm_bwd_kernel<T, VEC, NV, WIDTH>, s.grid,
+                                                                  s.threads, 0, 0, st, a, wv, inv)));
     parts = s.grid;
   }
-  const cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess || !a.dw) return e;
+  if (err != cudaSuccess || !a.dw) return err;
   return launch_sum_partials(a.partial, parts, a.cols, a.dw, a.dw_bf16, st);
 }
 
@@ -568,32 +579,19 @@ cudaError_t launch_norm_bwd(const NormBwd& a, int dtype, cudaStream_t st) {
   return dtype == SCAPE_BF16 ? run_norm_bwd<bf16>(a, st) : run_norm_bwd<float>(a, st);
 }
 
-// Launches a kernel over `clusters` clusters: of one block where there is little
-// to add up, which starts sooner.
-template <typename... P, typename... A>
-static cudaError_t launch_clusters(void (*kernel)(P...), int64_t clusters, int blocks, int threads,
-                                   cudaStream_t st, A... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(clusters * blocks));
-  cfg.blockDim = dim3(threads);
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = (unsigned)blocks;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
+// In clusters of one block where there is little to add up: they start sooner.
 cudaError_t launch_colsum(const bf16* m, int64_t ld, int64_t rows, int64_t cols, void* out,
                           int out_bf16, cudaStream_t st) {
-  return launch_clusters(rows16(m, ld, 2) ? colsum_kernel<8> : colsum_kernel<1>, ceil_div(cols, kSumCols),
-                         rows <= 256 ? 1 : kSumBlocks, kSumThreads, st, m, ld, rows, cols, out, out_bf16);
+  const int blocks = rows <= 256 ? 1 : kSumBlocks;
+  return launch_kernel(rows16(m, ld, 2) ? colsum_kernel<8> : colsum_kernel<1>,
+                       (unsigned)(ceil_div(cols, kSumCols) * blocks), kSumThreads, 0, blocks, st, m, ld, rows,
+                       cols, out, out_bf16);
 }
 cudaError_t launch_sum_partials(const float* partial, int64_t parts, int64_t cols, void* out,
                                 int out_bf16, cudaStream_t st) {
-  return launch_clusters(sum_partials_kernel, ceil_div(cols, 32), parts <= 128 ? 1 : kPartBlocks,
-                         32 * kPartWarps, st, partial, parts, cols, out, out_bf16);
+  const int blocks = parts <= 128 ? 1 : kPartBlocks;
+  return launch_kernel(sum_partials_kernel, (unsigned)(ceil_div(cols, 32) * blocks), 32 * kPartWarps, 0, blocks,
+                       st, partial, parts, cols, out, out_bf16);
 }
 
 }  // namespace layer

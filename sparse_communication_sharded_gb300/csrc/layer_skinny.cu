@@ -42,6 +42,7 @@ __global__ __launch_bounds__(kThreads) void skinny_forward_kernel(
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint32_t rank = block_rank(), ranks = cluster_blocks();
   cluster_begin();
+  start();
   const int64_t c0 = (int64_t)(blockIdx.x / ranks) * kCols;
   // this block's part of the contraction, in whole warp steps
   constexpr int kStep = 32 * VEC;
@@ -138,6 +139,7 @@ __global__ __launch_bounds__(kThreads) void skinny_input_grad_kernel(
   __shared__ float sums[8][R][kGradCols];
   const uint32_t rank = block_rank(), ranks = cluster_blocks();
   cluster_begin();
+  start();
   const int64_t c0 = (int64_t)(blockIdx.x / ranks) * kGradCols;
   const int at = threadIdx.x % kPerRow, first = threadIdx.x / kPerRow;
   const int64_t c = c0 + at * VEC;
@@ -234,6 +236,7 @@ __global__ __launch_bounds__(kThreads) void skinny_weight_grad_kernel(
     const bf16* dy, int64_t lddy, const bf16* x, int64_t ldx, const uint8_t* q, int64_t ldq,
     const uint8_t* scale, bool x16, bool q8, int act, int rows, int64_t k, int64_t n, T* dw,
     int64_t lddw, T* db) {
+  start();
   // a lane's columns: VEC 8 neighbours, or 8 singles that lie 32 apart
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t across = (k + 255) / 256, down = blockIdx.x / across;
@@ -357,21 +360,6 @@ int cuts(int64_t clusters, int64_t contraction, int64_t least) {
   while (s < 8 && clusters * s * 2 <= 2 * sm_count() && contraction / (s * 2) >= least) s *= 2;
   return s;
 }
-template <typename K, typename... A>
-cudaError_t launch(K kernel, int64_t clusters, int cluster, cudaStream_t st, A... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(clusters * cluster));
-  cfg.blockDim = dim3(kThreads);
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = (unsigned)cluster;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 #define SCAPE_ROWS_SWITCH(rows, vec, MOST, CALL)        \
   if (vec) {                                            \
     constexpr int VEC = 8;                              \
@@ -393,7 +381,7 @@ cudaError_t skinny_forward(const GemmCall& c, cudaStream_t st) {
   const int64_t clusters = ceil_div(c.n, kCols);
   const int s = cuts(clusters, c.k, 512);
   cudaError_t e = cudaSuccess;
-  SCAPE_ROWS_SWITCH(rows, vec, kSkinnyRows, e = (launch(skinny_forward_kernel<R, VEC>, clusters, s, st, c.a.p, c.a.ld,
+  SCAPE_ROWS_SWITCH(rows, vec, kSkinnyRows, e = (launch_kernel(skinny_forward_kernel<R, VEC>, (unsigned)(clusters * s), kThreads, 0, s, st, c.a.p, c.a.ld,
                                            c.b.p, c.b.ld, rows, c.k, c.n, c.e)));
   return e;
 }
@@ -403,7 +391,7 @@ cudaError_t skinny_input_grad(const GemmCall& c, cudaStream_t st) {
   const int64_t clusters = ceil_div(c.n, kGradCols);
   const int s = cuts(clusters, c.k, 128);
   cudaError_t e = cudaSuccess;
-  SCAPE_ROWS_SWITCH(rows, vec, kSkinnyRows, e = (launch(skinny_input_grad_kernel<R, VEC>, clusters, s, st, c.a.p,
+  SCAPE_ROWS_SWITCH(rows, vec, kSkinnyRows, e = (launch_kernel(skinny_input_grad_kernel<R, VEC>, (unsigned)(clusters * s), kThreads, 0, s, st, c.a.p,
                                            c.a.ld, c.b.p, c.b.ld, rows, c.n, c.k, c.e)));
   return e;
 }
@@ -412,16 +400,17 @@ cudaError_t skinny_weight_grad(const SkinnyWeightGrad& a, cudaStream_t st) {
   const bool vec = rows16(a.dw, a.lddw, ge), x16 = rows16(a.x, a.ldx, 2), q8 = rows8(a.q, a.ldq);
   const int rows = (int)a.rows;
   const unsigned grid = (unsigned)(ceil_div(a.k, 256) * ceil_div(a.n, kWarps * kPerWarp));
+  cudaError_t e = cudaSuccess;
   if (a.out_f32) {
-    SCAPE_ROWS_SWITCH(rows, vec, kSkinnyWeightRows, (skinny_weight_grad_kernel<R, VEC, float><<<grid, kThreads, 0, st>>>(
+    SCAPE_ROWS_SWITCH(rows, vec, kSkinnyWeightRows, e = (launch_kernel(skinny_weight_grad_kernel<R, VEC, float>, grid, kThreads, 0, 0, st,
                                      a.dy, a.lddy, a.x, a.ldx, a.q, a.ldq, a.scale, x16, q8, a.act, rows, a.k, a.n,
                                      static_cast<float*>(a.dw), a.lddw, static_cast<float*>(a.db))));
   } else {
-    SCAPE_ROWS_SWITCH(rows, vec, kSkinnyWeightRows, (skinny_weight_grad_kernel<R, VEC, bf16><<<grid, kThreads, 0, st>>>(
+    SCAPE_ROWS_SWITCH(rows, vec, kSkinnyWeightRows, e = (launch_kernel(skinny_weight_grad_kernel<R, VEC, bf16>, grid, kThreads, 0, 0, st,
                                      a.dy, a.lddy, a.x, a.ldx, a.q, a.ldq, a.scale, x16, q8, a.act, rows, a.k, a.n,
                                      static_cast<bf16*>(a.dw), a.lddw, static_cast<bf16*>(a.db))));
   }
-  return cudaGetLastError();
+  return e;
 }
 
 }  // namespace layer
