@@ -292,17 +292,20 @@ enum GemmMode {
   kModePair = 1
 };
 
-template <int KIND, int BN, int MODE>
+// FULL: an epilogue with an activation or an 8-bit output; without, a bias and a
+// residual at most.
+template <int KIND, int BN, int MODE, bool FULL>
 struct Tile {
   static constexpr bool kPair = MODE == kModePair;
-  // 8 warps, 2 a scheduler.  16 made a gelu epilogue shorter (input gradient of
-  // 8192 x 4096, contraction 1024: 49 against 53 us) but the others longer
-  // (forward without an activation: 53 against 41 us): they crowd the one thread
-  // that issues the matrix instructions, and their output boxes take a stage.
-  static constexpr int kEpilogueWarps = 8;
+  // 8 warps, 2 a scheduler; with an activation to compute 12, whose latencies
+  // overlap more.  8192 x 4096, contraction 1024, in us with 8 / 12 / 16 warps:
+  // forward 40.0 / 41.3 / 53, with gelu 46.5 / 44.9 / 54, input gradient through
+  // gelu 51.9 / 47.5 / 48.3.  More warps crowd the one thread that issues the
+  // matrix instructions; at 16 their output boxes take a stage as well.
+  static constexpr int kEpilogueWarps = kPair && FULL ? 12 : 8;
   static constexpr int kThreads = 128 + 32 * kEpilogueWarps;  // + TMA, MMA, TMEM, an idle warp
   static constexpr int kGroups = kEpilogueWarps / 4;  // warps that share a quarter of the rows
-  static constexpr int kWarpChunks = BN / 32 / kGroups;       // 32-column chunks a warp, at most
+  static constexpr int kWarpChunks = (BN / 32 + kGroups - 1) / kGroups;  // 32-column chunks a warp, at most
   static constexpr int kBRows = kPair ? BN / 2 : BN;  // operand B rows a block stages, at most
   static constexpr int kABytes = kBM * kBK * 2;
   static constexpr int kBBytes = kBRows * kBK * 2;
@@ -415,7 +418,7 @@ struct Beside {
   uint32_t w[KIND == kGemmForward ? N / 2 : KIND == kGemmInputGrad ? N / 4 : 1];
   uint32_t code;
 };
-template <int KIND, int N>
+template <int KIND, bool FULL, int N>
 __device__ __forceinline__ void load_beside(Beside<KIND, N>& b, bool live, int64_t row, int c0,
                                             int left, const Epilogue& e) {
   if constexpr (KIND == kGemmForward) {
@@ -439,7 +442,7 @@ __device__ __forceinline__ void load_beside(Beside<KIND, N>& b, bool live, int64
         b.w[i] = (2 * i < left ? s[2 * i] : 0u) |
                  ((uint32_t)(2 * i + 1 < left ? s[2 * i + 1] : 0u) << 16);
     }
-  } else if constexpr (KIND == kGemmInputGrad) {
+  } else if constexpr (KIND == kGemmInputGrad && FULL) {
     if (e.act == SCAPE_ACT_NONE || !live || left <= 0) return;
     const uint8_t* p = e.pre_q + row * e.ldpre + c0;
     b.code = e.pre_scale[row * e.blocks_per_row + c0 / kBlock];
@@ -480,12 +483,14 @@ __device__ __forceinline__ void times_slopes(float (&v)[N], const uint32_t (&w)[
 
 // The accumulators become the values to store; the 8-bit form is stored here.
 // All 32 lanes call it.
-template <int KIND, int N>
+template <int KIND, bool FULL, int N>
 __device__ __forceinline__ void epilogue_math(float (&v)[N], const Beside<KIND, N>& b, bool live,
                                               int64_t row, int c0, int left, const Epilogue& e) {
   if constexpr (KIND == kGemmForward) {
-    if (e.q) pack_row<N>(v, left, live, e, row, c0);
-    SCAPE_ACT_SWITCH(e.act, act_values<ACT>(v));
+    if constexpr (FULL) {
+      if (e.q) pack_row<N>(v, left, live, e, row, c0);
+      SCAPE_ACT_SWITCH(e.act, act_values<ACT>(v));
+    }
     if (e.res && live && left > 0) {
 #pragma unroll
       for (int i = 0; i < N / 2; ++i) {
@@ -493,7 +498,7 @@ __device__ __forceinline__ void epilogue_math(float (&v)[N], const Beside<KIND, 
         v[2 * i + 1] += __uint_as_float(b.w[i] & 0xFFFF0000u);
       }
     }
-  } else if constexpr (KIND == kGemmInputGrad) {
+  } else if constexpr (KIND == kGemmInputGrad && FULL) {
     if (e.act != SCAPE_ACT_NONE && live && left > 0) {
       SCAPE_ACT_SWITCH(e.act, times_slopes<ACT>(v, b.w, scale_value(b.code)));
     }
@@ -578,12 +583,12 @@ struct GemmShape {
   unsigned int* status;
 };
 
-template <int KIND, int BN, int MODE>
-__global__ __launch_bounds__(Tile<KIND, BN, MODE>::kThreads, 1) void gemm_kernel(
+template <int KIND, int BN, int MODE, bool FULL>
+__global__ __launch_bounds__(Tile<KIND, BN, MODE, FULL>::kThreads, 1) void gemm_kernel(
     const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
     const __grid_constant__ CUtensorMap map_out, const GemmShape s,
     const __grid_constant__ Epilogue e) {
-  using TL = Tile<KIND, BN, MODE>;
+  using TL = Tile<KIND, BN, MODE, FULL>;
   constexpr bool PAIR = MODE == kModePair;
   constexpr bool TA = KIND == kGemmWeightGrad;
   constexpr bool TB = KIND != kGemmForward;
@@ -789,7 +794,7 @@ __global__ __launch_bounds__(Tile<KIND, BN, MODE>::kThreads, 1) void gemm_kernel
           }
           __syncwarp();
         }
-        load_beside<KIND, 32>(next, live, row, col0, group * 32 < bn ? s.n - col0 : 0, e);
+        load_beside<KIND, FULL, 32>(next, live, row, col0, group * 32 < bn ? s.n - col0 : 0, e);
       }
       if (!__all_sync(0xFFFFFFFFu, wait(acc_full(acc), acc_phase))) break;
       tc_fence_after();
@@ -812,7 +817,7 @@ __global__ __launch_bounds__(Tile<KIND, BN, MODE>::kThreads, 1) void gemm_kernel
           const int c0 = col0 + c, left = s.n - c0;
           const Beside<KIND, 32> beside = next;
           if (j + 1 < TL::kWarpChunks && group * 32 + c + TL::kGroups * 32 < bn)
-            load_beside<KIND, 32>(next, live, row, c0 + TL::kGroups * 32,
+            load_beside<KIND, FULL, 32>(next, live, row, c0 + TL::kGroups * 32,
                                   left - TL::kGroups * 32, e);
           tmem_ld_wait();
           if (left > 0) {
@@ -834,7 +839,7 @@ __global__ __launch_bounds__(Tile<KIND, BN, MODE>::kThreads, 1) void gemm_kernel
 #pragma unroll
               for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
             }
-            epilogue_math<KIND, 32>(v, beside, live, row, c0, left, e);
+            epilogue_math<KIND, FULL, 32>(v, beside, live, row, c0, left, e);
             if (through_box) {
               if (e.out_vec) {
                 // the box two stores ago has been read
@@ -884,7 +889,7 @@ __global__ __launch_bounds__(Tile<KIND, BN, MODE>::kThreads, 1) void gemm_kernel
         const int c0 = tn * BN + c, left = s.n - c0;
         const bool live = row < s.m;
         Beside<KIND, 8> beside;
-        load_beside<KIND, 8>(beside, live, row, c0, left, e);
+        load_beside<KIND, FULL, 8>(beside, live, row, c0, left, e);
         float v[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i)
@@ -912,7 +917,7 @@ __global__ __launch_bounds__(Tile<KIND, BN, MODE>::kThreads, 1) void gemm_kernel
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] += sum[i];
-        epilogue_math<KIND, 8>(v, beside, live, row, c0, left, e);
+        epilogue_math<KIND, FULL, 8>(v, beside, live, row, c0, left, e);
         if (live && left > 0) store_row<KIND, 8>(v, row, c0, left, e);
       }
     }
@@ -936,9 +941,9 @@ struct TileRange {
   int of_bn = 0;
 };
 
-template <int KIND, int BN, int MODE>
+template <int KIND, int BN, int MODE, bool FULL>
 cudaError_t gemm_launch(const GemmCall& c, int bn, int split, cudaStream_t st, TileRange range = {}) {
-  using TL = Tile<KIND, BN, MODE>;
+  using TL = Tile<KIND, BN, MODE, FULL>;
   constexpr bool PAIR = MODE == kModePair;
   constexpr bool TA = KIND == kGemmWeightGrad;
   constexpr bool TB = KIND != kGemmForward;
@@ -970,13 +975,21 @@ cudaError_t gemm_launch(const GemmCall& c, int bn, int split, cudaStream_t st, T
                  : range.count ? (int)range.count : s.tiles_m * s.tiles_n;
   s.ksteps = (int)ceil_div(c.k, kBK);
   if (err == cudaSuccess) err = gemm_status_word(&s.status);
-  auto kernel = gemm_kernel<KIND, BN, MODE>;
+  auto kernel = gemm_kernel<KIND, BN, MODE, FULL>;
   if (err == cudaSuccess) err = gemm_allow_smem((const void*)kernel, TL::kSmem);
   if (err != cudaSuccess) return err;
   const int64_t tiles = s.tiles;
   const int cluster = PAIR ? 2 : split;
   const int64_t grid = PAIR ? 2 * std::min<int64_t>(tiles, sm_count() / 2) : tiles * split;
   return launch_kernel(kernel, (unsigned)grid, TL::kThreads, TL::kSmem, cluster, st, ma, mb, mo, s, c.e);
+}
+
+template <int KIND>
+cudaError_t gemm_pairs(const GemmCall& c, int bn, cudaStream_t st, TileRange range) {
+  if constexpr (KIND != kGemmWeightGrad) {
+    if (c.e.act != SCAPE_ACT_NONE || c.e.q) return gemm_launch<KIND, 256, kModePair, true>(c, bn, 2, st, range);
+  }
+  return gemm_launch<KIND, 256, kModePair, false>(c, bn, 2, st, range);
 }
 
 // Tile and mode.  Pairs do the most work a byte read and keep the tensor cores
@@ -1016,17 +1029,17 @@ cudaError_t gemm_run(const GemmCall& c, cudaStream_t st) {
     TileRange first, rest;
     first.count = rest.base = whole;
     rest.of_bn = best;
-    const cudaError_t e = gemm_launch<KIND, 256, kModePair>(c, best, 2, st, first);
-    return e != cudaSuccess ? e : gemm_launch<KIND, 128, kModeSplit>(c, 128, best_split, st, rest);
+    const cudaError_t e = gemm_pairs<KIND>(c, best, st, first);
+    return e != cudaSuccess ? e : gemm_launch<KIND, 128, kModeSplit, true>(c, 128, best_split, st, rest);
   }
-  if (best) return gemm_launch<KIND, 256, kModePair>(c, best, 2, st);
+  if (best) return gemm_pairs<KIND>(c, best, st, {});
   const int64_t tm = ceil_div(c.m, kBM);
   const int bn = tm * ceil_div(c.n, 64) <= sms ? 64 : 128;
   const int64_t tiles = tm * ceil_div(c.n, bn);
   int split = 1;
   while (split < 8 && tiles <= gemm_clusters(split * 2) && ksteps / (split * 2) >= 4) split *= 2;
-  return bn == 64 ? gemm_launch<KIND, 64, kModeSplit>(c, 64, split, st)
-                  : gemm_launch<KIND, 128, kModeSplit>(c, 128, split, st);
+  return bn == 64 ? gemm_launch<KIND, 64, kModeSplit, true>(c, 64, split, st)
+                  : gemm_launch<KIND, 128, kModeSplit, true>(c, 128, split, st);
 }
 
 #endif  // __CUDACC__
