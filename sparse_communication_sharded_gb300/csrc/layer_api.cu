@@ -42,8 +42,8 @@ struct Matrix {
 };
 
 // Up to two matrices (blockIdx.z) of any alignment copied to 16-byte aligned
-// rows.  A thread writes eight values; its reads, two bytes each, fall on lines
-// that its neighbours read as well.
+// rows, eight values a thread.  (Eight 2-byte loads a thread took 42 us for two
+// passes over 10384 x 3114, bound by their instructions.)
 struct AlignCopy {
   const bf16* src;
   int64_t ld, rows, cols;
@@ -53,21 +53,26 @@ struct AlignCopy {
 struct AlignCopies {
   AlignCopy m[2];
 };
+constexpr int kCopyRows = 4;
 __global__ __launch_bounds__(256) void align_rows_kernel(const __grid_constant__ AlignCopies a) {
   start();
   const AlignCopy& m = a.m[blockIdx.z];
-  // a block covers 8 rows of 32 vectors, or what of them there is
+  // a block covers 8 rows of 32 vectors at a time, a thread kCopyRows of them
   const int64_t c = ((int64_t)blockIdx.x * 32 + (threadIdx.x & 31)) * 8;
   if (c >= m.ldd) return;
-  for (int64_t row = (int64_t)blockIdx.y * 8 + (threadIdx.x >> 5); row < m.rows; row += (int64_t)gridDim.y * 8) {
-    const uint16_t* s = reinterpret_cast<const uint16_t*>(m.src) + row * m.ld + c;
-    uint32_t w[4];
+  const bf16* end = m.src + (m.rows - 1) * m.ld + m.cols;
+  const int n = (int)min((int64_t)8, m.cols - c);
+  for (int64_t row = (int64_t)blockIdx.y * 8 * kCopyRows + (threadIdx.x >> 5); row < m.rows;
+       row += (int64_t)gridDim.y * 8 * kCopyRows) {
+    Raw<bf16, 8> v[kCopyRows];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t lo = c + 2 * i < m.cols ? s[2 * i] : 0, hi = c + 2 * i + 1 < m.cols ? s[2 * i + 1] : 0;
-      w[i] = lo | hi << 16;
-    }
-    *reinterpret_cast<uint4*>(m.dst + row * m.ldd + c) = make_uint4(w[0], w[1], w[2], w[3]);
+    for (int i = 0; i < kCopyRows; ++i)
+      v[i] = load_any<8>(m.src + (row + 8 * i) * m.ld + c, row + 8 * i < m.rows ? n : 0, m.src, end);
+#pragma unroll
+    for (int i = 0; i < kCopyRows; ++i)
+      if (row + 8 * i < m.rows)
+        *reinterpret_cast<uint4*>(m.dst + (row + 8 * i) * m.ldd + c) =
+            make_uint4(v[i].w[0], v[i].w[1], v[i].w[2], v[i].w[3]);
   }
 }
 
@@ -103,7 +108,7 @@ cudaError_t operands(const Matrix& a, const Matrix& b, bool any_rows, uint8_t* w
     ws += copy_bytes(m.rows, m.cols);
     *out[i] = {c.dst, c.ldd};
     x = std::max(x, ceil_div(c.ldd, 256));
-    y = std::max(y, ceil_div(c.rows, 8));
+    y = std::max(y, ceil_div(c.rows, 8 * kCopyRows));
   }
   if (n == 0) return cudaSuccess;
   return launch_kernel(align_rows_kernel, dim3((unsigned)x, (unsigned)std::min<int64_t>(y, 32768), (unsigned)n),
@@ -509,6 +514,8 @@ extern "C" int scape_layer_linear_bwd_weight(const void* dy, int64_t lddy, const
     c.e.out = dweight, c.e.ldo = lddw, c.e.out_f32 = grad_dtype == SCAPE_F32;
     c.e.out_vec = rows16(dweight, lddw, ge);
     if (e == cudaSuccess) e = gemm_weight_grad(c, st);
+    // from aligned rows, if they had to be made
+    dy = c.a.p, lddy = c.a.ld;
   }
   if (e == cudaSuccess && dbias)
     e = launch_colsum(static_cast<const bf16*>(dy), lddy, rows, n, dbias, grad_dtype == SCAPE_BF16,

@@ -53,10 +53,11 @@ __device__ __forceinline__ Unit unit_at(uint32_t u, uint32_t units, const FastDi
   return r;
 }
 
-template <typename T, int VEC>
-__global__ __launch_bounds__(kThreads) void pack8_kernel(const T* x, int64_t ldx, uint32_t units,
-                                                         FastDiv per_row, int64_t cols, uint8_t* q,
-                                                         int64_t ldq, uint8_t* scale,
+// ANY: rows of x of any alignment (lo, hi: where x begins and ends).
+template <typename T, int VEC, bool ANY>
+__global__ __launch_bounds__(kThreads) void pack8_kernel(const T* x, int64_t ldx, const T* lo, const T* hi,
+                                                         uint32_t units, FastDiv per_row, int64_t cols,
+                                                         uint8_t* q, int64_t ldq, uint8_t* scale,
                                                          int64_t blocks_per_row) {
   start();
   constexpr int U = unroll<VEC>();
@@ -66,7 +67,11 @@ __global__ __launch_bounds__(kThreads) void pack8_kernel(const T* x, int64_t ldx
 #pragma unroll
   for (int i = 0; i < U; ++i) {
     un[i] = unit_at<VEC>(first + i * kThreads, units, per_row, cols);
-    raw[i] = load_raw<VEC>(x + un[i].row * ldx + un[i].col, un[i].n);
+    const T* p = x + un[i].row * ldx + un[i].col;
+    if constexpr (ANY)
+      raw[i] = load_any<VEC>(p, un[i].n, lo, hi);
+    else
+      raw[i] = load_raw<VEC>(p, un[i].n);
   }
 #pragma unroll
   for (int i = 0; i < U; ++i) {
@@ -202,13 +207,14 @@ cudaError_t for_row_ranges(int64_t rows, int64_t cols, F&& launch) {
   return cudaSuccess;
 }
 
-template <typename T, int VEC>
+template <typename T, int VEC, bool ANY>
 cudaError_t run_pack8(const T* x, int64_t ldx, int64_t rows, int64_t cols, uint8_t* q, int64_t ldq,
                       uint8_t* scale, cudaStream_t st) {
   const int64_t bpr = ceil_div(cols, kBlock);
+  const T* end = x + (rows - 1) * ldx + cols;
   return for_row_ranges<VEC>(rows, cols, [&](int64_t r, uint32_t units, FastDiv d, unsigned grid) {
-    return launch_kernel(pack8_kernel<T, VEC>, grid, kThreads, 0, 0, st, x + r * ldx, ldx, units, d, cols,
-                         q + r * ldq, ldq, scale + r * bpr, bpr);
+    return launch_kernel(pack8_kernel<T, VEC, ANY>, grid, kThreads, 0, 0, st, x + r * ldx, ldx, x, end, units,
+                         d, cols, q + r * ldq, ldq, scale + r * bpr, bpr);
   });
 }
 template <typename T, int VEC>
@@ -240,17 +246,21 @@ cudaError_t run_act_grad(const T* dy, int64_t lddy, const uint8_t* q, int64_t ld
 // values), 8, or 1: a warp then reads 32 neighbouring columns, a whole block, at
 // a time.  16 against 8: unpack8 of 8192 x 5632 to bfloat16 took 23.2 against
 // 26.5 us, the fewer addresses for the same bytes.
-#define SCAPE_VEC_SWITCH(v16, v8, CALL)              \
-  if (v16) { constexpr int VEC = 16; return CALL; }  \
-  if (v8) { constexpr int VEC = 8; return CALL; }    \
-  { constexpr int VEC = 1; return CALL; }
+#define SCAPE_VEC_SWITCH(v16, v8, CALL)                \
+  do {                                                 \
+    if (v16) { constexpr int VEC = 16; return CALL; }  \
+    if (v8) { constexpr int VEC = 8; return CALL; }    \
+    { constexpr int VEC = 1; return CALL; }            \
+  } while (0)
 
 template <typename T>
 cudaError_t pack8_of(const T* x, int64_t ldx, int64_t rows, int64_t cols, uint8_t* q, int64_t ldq,
                      uint8_t* scale, cudaStream_t st) {
-  const bool ok = rows16(x, ldx, sizeof(T));
-  SCAPE_VEC_SWITCH(ok && rows16(q, ldq, 1), ok && rows8(q, ldq),
-                   (run_pack8<T, VEC>(x, ldx, rows, cols, q, ldq, scale, st)));
+  if (rows16(x, ldx, sizeof(T)))
+    SCAPE_VEC_SWITCH(rows16(q, ldq, 1), rows8(q, ldq),
+                     (run_pack8<T, VEC, false>(x, ldx, rows, cols, q, ldq, scale, st)));
+  SCAPE_VEC_SWITCH(false, rows8(q, ldq),
+                   (run_pack8<T, VEC, (VEC > 1)>(x, ldx, rows, cols, q, ldq, scale, st)));
 }
 template <typename T>
 cudaError_t unpack8_of(const uint8_t* q, int64_t ldq, const uint8_t* scale, int64_t rows,

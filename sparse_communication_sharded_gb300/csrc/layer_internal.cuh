@@ -73,6 +73,57 @@ __device__ __forceinline__ Raw<T, VEC> load_raw(const T* p, int n) {
   }
   return r;
 }
+// The same for rows of any alignment, VEC 8 or 16: a piece of 16 bytes is cut out of
+// the two aligned ones that hold it (the second is the neighbour's first, so it
+// comes from L1).  What lies between lo and hi is the matrix: pieces whose aligned
+// words do not lie there entirely are read element by element.
+template <int VEC, typename T>
+__device__ __forceinline__ Raw<T, VEC> load_any(const T* p, int n, const T* lo, const T* hi) {
+  constexpr int kPer = 16 / sizeof(T);
+  Raw<T, VEC> r;
+#pragma unroll
+  for (int i = 0; i < VEC / kPer; ++i) {
+    const T* q = p + i * kPer;
+    const int have = n - i * kPer;
+    const uint32_t off = (uint32_t)(reinterpret_cast<uintptr_t>(q) & 15u);
+    const char* a = reinterpret_cast<const char*>(q) - off;
+    uint32_t w[8];
+    if (have >= kPer && off == 0) {
+      const uint4 u = *reinterpret_cast<const uint4*>(a);
+      r.w[4 * i] = u.x, r.w[4 * i + 1] = u.y, r.w[4 * i + 2] = u.z, r.w[4 * i + 3] = u.w;
+    } else if (have >= kPer && a >= reinterpret_cast<const char*>(lo) &&
+               a + 32 <= reinterpret_cast<const char*>(hi)) {
+      const uint4 u = reinterpret_cast<const uint4*>(a)[0], v = reinterpret_cast<const uint4*>(a)[1];
+      w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w, w[4] = v.x, w[5] = v.y, w[6] = v.z, w[7] = v.w;
+      if (off & 8) {
+#pragma unroll
+        for (int j = 0; j < 6; ++j) w[j] = w[j + 2];
+      }
+      if (off & 4) {
+#pragma unroll
+        for (int j = 0; j < 5; ++j) w[j] = w[j + 1];
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        r.w[4 * i + j] = sizeof(T) == 4 ? w[j] : __funnelshift_r(w[j], w[j + 1], (off & 2) * 8);
+    } else {
+      Raw<T, kPer> part;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) part.w[j] = 0;
+#pragma unroll
+      for (int j = 0; j < kPer; ++j)
+        if (j < have) {
+          if constexpr (sizeof(T) == 2)
+            part.w[j / 2] |= (uint32_t) reinterpret_cast<const uint16_t*>(q)[j] << (16 * (j % 2));
+          else
+            part.w[j] = reinterpret_cast<const uint32_t*>(q)[j];
+        }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) r.w[4 * i + j] = part.w[j];
+    }
+  }
+  return r;
+}
 template <typename T, int VEC>
 __device__ __forceinline__ void to_floats(const Raw<T, VEC>& r, float (&v)[VEC]) {
 #pragma unroll

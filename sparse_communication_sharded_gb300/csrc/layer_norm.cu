@@ -109,7 +109,8 @@ struct Team {
   __device__ static int64_t step() { return kWarp ? (int64_t)gridDim.x * kWarpRows : gridDim.x; }
 };
 
-template <typename T, int VEC, int NV, int WIDTH>
+// ANY: rows of x and the residual of any alignment (the outputs' are aligned).
+template <typename T, int VEC, int NV, int WIDTH, bool ANY>
 __global__ __launch_bounds__(Team<WIDTH>::kThreads) void norm_fwd_kernel(
     const __grid_constant__ NormFwd a, bool w_vec, float inv_cols) {
   using TM = Team<WIDTH>;
@@ -129,8 +130,15 @@ __global__ __launch_bounds__(Team<WIDTH>::kThreads) void norm_fwd_kernel(
     const T* res = static_cast<const T*>(a.res) + row * a.ldres + t * VEC;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      rx[i] = load_raw<VEC>(x + i * width * VEC, mine - i * width * VEC);
-      if (a.res) rr[i] = load_raw<VEC>(res + i * width * VEC, mine - i * width * VEC);
+      const int n = mine - i * width * VEC;
+      if constexpr (ANY) {
+        const T *x0 = static_cast<const T*>(a.x), *r0 = static_cast<const T*>(a.res);
+        rx[i] = load_any<VEC>(x + i * width * VEC, n, x0, x0 + (a.rows - 1) * a.ldx + a.cols);
+        if (a.res) rr[i] = load_any<VEC>(res + i * width * VEC, n, r0, r0 + (a.rows - 1) * a.ldres + a.cols);
+      } else {
+        rx[i] = load_raw<VEC>(x + i * width * VEC, n);
+        if (a.res) rr[i] = load_raw<VEC>(res + i * width * VEC, n);
+      }
     }
     uint64_t v[P], sum = pair(0.0f, 0.0f);
 #pragma unroll
@@ -355,10 +363,12 @@ constexpr int kSumCols = 64;
 constexpr int kSumBlocks = 8;
 constexpr int kSumThreads = 512;
 
-template <int VEC>
+template <bool ANY>
 __global__ __launch_bounds__(kSumThreads) void colsum_kernel(
     const bf16* m, int64_t ld, int64_t rows, int64_t cols, void* out, int out_bf16) {
-  // VEC 8: eight threads a row, VEC 1: 64
+  // eight columns a thread, rows of any alignment with ANY
+  constexpr int VEC = 8;
+  const bf16* hi = m + (rows - 1) * ld + cols;
   constexpr int kPerRow = kSumCols / VEC, kRows = kSumThreads / kPerRow;
   __shared__ float part[kRows][kSumCols + 4];
   __shared__ float sums[kSumBlocks][kSumCols];
@@ -377,7 +387,10 @@ __global__ __launch_bounds__(kSumThreads) void colsum_kernel(
     Raw<bf16, VEC> v[kUnroll];
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u)
-      v[u] = load_raw<VEC>(m + (r + u * kRows) * ld + c, r + u * kRows < end ? n : 0);
+      if constexpr (ANY)
+        v[u] = load_any<VEC>(m + (r + u * kRows) * ld + c, r + u * kRows < end ? n : 0, m, hi);
+      else
+        v[u] = load_raw<VEC>(m + (r + u * kRows) * ld + c, r + u * kRows < end ? n : 0);
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       float f[VEC];
@@ -527,15 +540,20 @@ cudaError_t run_norm_fwd(NormFwd a, cudaStream_t st) {
                          512, 0, 0, st, a);
   }
   const size_t e = sizeof(T);
-  const bool vec = rows16(a.x, a.ldx, e) && rows16(a.res, a.ldres, e) && rows16(a.y, a.ldy, e) &&
-                   rows16(a.h, a.ldh, e) && rows8(a.q, a.ldq);
+  const bool vec = rows16(a.y, a.ldy, e) && rows16(a.h, a.ldh, e) && rows8(a.q, a.ldq);
+  const bool any = !rows16(a.x, a.ldx, e) || !rows16(a.res, a.ldres, e);
   a.q16 = rows16(a.q, a.ldq, 1);
   const bool wv = aligned(a.w, 16);
   const float inv = (float)(1.0 / a.cols);
   const Shape s = shape_of(a.rows, a.cols, vec, kWarpCols, kFwdThreads);
   cudaError_t err = cudaSuccess;
-  SCAPE_SHAPE_SWITCH(vec, s, kWarpCols, err = (launch_kernel(norm_fwd_kernel<T, VEC, NV, WIDTH>, s.grid, s.threads,
-                                                             0, 0, st, a, wv, inv)));
+  if (any) {
+    SCAPE_SHAPE_SWITCH(vec, s, kWarpCols, err = (launch_kernel(norm_fwd_kernel<T, VEC, NV, WIDTH, (VEC > 1)>, s.grid,
+                                                               s.threads, 0, 0, st, a, wv, inv)));
+  } else {
+    SCAPE_SHAPE_SWITCH(vec, s, kWarpCols, err = (launch_kernel(norm_fwd_kernel<T, VEC, NV, WIDTH, false>, s.grid,
+                                                               s.threads, 0, 0, st, a, wv, inv)));
+  }
   return err;
 }
 
@@ -583,7 +601,7 @@ cudaError_t launch_norm_bwd(const NormBwd& a, int dtype, cudaStream_t st) {
 cudaError_t launch_colsum(const bf16* m, int64_t ld, int64_t rows, int64_t cols, void* out,
                           int out_bf16, cudaStream_t st) {
   const int blocks = rows <= 256 ? 1 : kSumBlocks;
-  return launch_kernel(rows16(m, ld, 2) ? colsum_kernel<8> : colsum_kernel<1>,
+  return launch_kernel(rows16(m, ld, 2) ? colsum_kernel<false> : colsum_kernel<true>,
                        (unsigned)(ceil_div(cols, kSumCols) * blocks), kSumThreads, 0, blocks, st, m, ld, rows,
                        cols, out, out_bf16);
 }
