@@ -84,6 +84,12 @@ bool rows32(const void* p, int64_t ld, size_t elem) {
   return aligned(p, 32) && (ld * (int64_t)elem) % 32 == 0;
 }
 
+// Bytes (up to 8) that every row starts on a multiple of.
+int row_alignment(const void* p, int64_t pitch) {
+  const uint64_t all = reinterpret_cast<uintptr_t>(p) | (uint64_t)pitch;
+  return all % 8 == 0 ? 8 : all % 4 == 0 ? 4 : 2;
+}
+
 // TMA reads rows that start on 16-byte boundaries; other operands are first
 // copied to such rows in the workspace.
 bool tma_rows(const void* p, int64_t ld) { return rows16(p, ld, 2); }
@@ -399,6 +405,7 @@ extern "C" int scape_layer_linear(const void* x, int64_t ldx, const void* weight
   c.e.blocks_per_row = ceil_div(n, kBlock);
   c.e.out = y, c.e.ldo = ldy;
   c.e.out_vec = rows16(y, ldy, 2);
+  c.e.out_align = row_alignment(y, ldy * 2);
   if (e == cudaSuccess) e = skinny ? skinny_forward(c, st) : gemm_forward(c, st);
   return cuda_result(e, "scape_layer_linear");
 }
@@ -442,6 +449,7 @@ extern "C" int scape_layer_linear_bwd_input(const void* dy, int64_t lddy, const 
   c.e.blocks_per_row = ceil_div(k, kBlock);
   c.e.out = dx, c.e.ldo = lddx;
   c.e.out_vec = rows16(dx, lddx, 2);
+  c.e.out_align = row_alignment(dx, lddx * 2);
   if (e == cudaSuccess) e = skinny ? skinny_input_grad(c, st) : gemm_input_grad(c, st);
   return cuda_result(e, "scape_layer_linear_bwd_input");
 }
@@ -513,6 +521,7 @@ extern "C" int scape_layer_linear_bwd_weight(const void* dy, int64_t lddy, const
     c.m = n, c.n = k, c.k = rows;
     c.e.out = dweight, c.e.ldo = lddw, c.e.out_f32 = grad_dtype == SCAPE_F32;
     c.e.out_vec = rows16(dweight, lddw, ge);
+    c.e.out_align = row_alignment(dweight, lddw * ge);
     if (e == cudaSuccess) e = gemm_weight_grad(c, st);
     // from aligned rows, if they had to be made
     dy = c.a.p, lddy = c.a.ld;

@@ -90,10 +90,13 @@ struct Packed {
   uint32_t w[VEC >= 4 ? VEC / 4 : 1];
   uint32_t code;
 };
-template <int VEC>
+// ANY (VEC 8): 8 bytes at any address, cut out of the two aligned 8-byte words that
+// hold them where both lie between lo and hi, the matrix.
+template <int VEC, bool ANY = false>
 __device__ __forceinline__ Packed<VEC> load_packed(const uint8_t* q, int64_t ldq,
                                                    const uint8_t* scale, int64_t blocks_per_row,
-                                                   const Unit& u) {
+                                                   const Unit& u, const uint8_t* lo = nullptr,
+                                                   const uint8_t* hi = nullptr) {
   Packed<VEC> p = {};
   if (u.n > 0) {
     const uint8_t* s = q + u.row * ldq + u.col;
@@ -102,9 +105,16 @@ __device__ __forceinline__ Packed<VEC> load_packed(const uint8_t* q, int64_t ldq
       const uint4 a = *reinterpret_cast<const uint4*>(s);
       p.w[0] = a.x, p.w[VEC == 16 ? 1 : 0] = a.y;
       p.w[VEC == 16 ? 2 : 0] = a.z, p.w[VEC == 16 ? 3 : 0] = a.w;
-    } else if (VEC == 8 && u.n == 8) {
+    } else if (VEC == 8 && u.n == 8 && !ANY) {
       const uint2 a = *reinterpret_cast<const uint2*>(s);
       p.w[0] = a.x, p.w[VEC >= 8 ? 1 : 0] = a.y;
+    } else if (VEC == 8 && u.n == 8 && s - (reinterpret_cast<uintptr_t>(s) & 7) >= lo &&
+               s - (reinterpret_cast<uintptr_t>(s) & 7) + 16 <= hi) {
+      const uint32_t off = (uint32_t)(reinterpret_cast<uintptr_t>(s) & 7);
+      const uint2 a = reinterpret_cast<const uint2*>(s - off)[0], b = reinterpret_cast<const uint2*>(s - off)[1];
+      const uint32_t w0 = off & 4 ? a.y : a.x, w1 = off & 4 ? b.x : a.y, w2 = off & 4 ? b.y : b.x;
+      p.w[0] = __funnelshift_r(w0, w1, (off & 3) * 8);
+      p.w[VEC >= 8 ? 1 : 0] = __funnelshift_r(w1, w2, (off & 3) * 8);
     } else {
 #pragma unroll
       for (int i = 0; i < VEC; ++i)
@@ -114,9 +124,9 @@ __device__ __forceinline__ Packed<VEC> load_packed(const uint8_t* q, int64_t ldq
   return p;
 }
 
-template <typename T, int VEC, int ACT>
-__global__ __launch_bounds__(kThreads) void unpack8_kernel(const uint8_t* q, int64_t ldq,
-                                                           const uint8_t* scale,
+template <typename T, int VEC, int ACT, bool ANY>
+__global__ __launch_bounds__(kThreads) void unpack8_kernel(const uint8_t* q, int64_t ldq, const uint8_t* lo,
+                                                           const uint8_t* hi, const uint8_t* scale,
                                                            int64_t blocks_per_row, uint32_t units,
                                                            FastDiv per_row, int64_t cols, T* y,
                                                            int64_t ldy) {
@@ -128,7 +138,7 @@ __global__ __launch_bounds__(kThreads) void unpack8_kernel(const uint8_t* q, int
 #pragma unroll
   for (int i = 0; i < U; ++i) {
     un[i] = unit_at<VEC>(first + i * kThreads, units, per_row, cols);
-    p[i] = load_packed<VEC>(q, ldq, scale, blocks_per_row, un[i]);
+    p[i] = load_packed<VEC, ANY>(q, ldq, scale, blocks_per_row, un[i], lo, hi);
   }
 #pragma unroll
   for (int i = 0; i < U; ++i) {
@@ -217,14 +227,14 @@ cudaError_t run_pack8(const T* x, int64_t ldx, int64_t rows, int64_t cols, uint8
                          d, cols, q + r * ldq, ldq, scale + r * bpr, bpr);
   });
 }
-template <typename T, int VEC>
+template <typename T, int VEC, bool ANY>
 cudaError_t run_unpack8(const uint8_t* q, int64_t ldq, const uint8_t* scale, int64_t rows,
                         int64_t cols, int act, T* y, int64_t ldy, cudaStream_t st) {
   const int64_t bpr = ceil_div(cols, kBlock);
   return for_row_ranges<VEC>(rows, cols, [&](int64_t r, uint32_t units, FastDiv d, unsigned grid) {
     cudaError_t e = cudaSuccess;
-    SCAPE_ACT_SWITCH(act, e = (launch_kernel(unpack8_kernel<T, VEC, ACT>, grid, kThreads, 0, 0, st, q + r * ldq,
-                                             ldq, scale + r * bpr, bpr, units, d, cols, y + r * ldy, ldy)));
+    SCAPE_ACT_SWITCH(act, e = (launch_kernel(unpack8_kernel<T, VEC, ACT, ANY>, grid, kThreads, 0, 0, st,
+                                             q + r * ldq, ldq, q, q + (rows - 1) * ldq + cols, scale + r * bpr, bpr, units, d, cols, y + r * ldy, ldy)));
     return e;
   });
 }
@@ -266,8 +276,9 @@ template <typename T>
 cudaError_t unpack8_of(const uint8_t* q, int64_t ldq, const uint8_t* scale, int64_t rows,
                        int64_t cols, int act, T* y, int64_t ldy, cudaStream_t st) {
   const bool ok = rows16(y, ldy, sizeof(T));
-  SCAPE_VEC_SWITCH(ok && rows16(q, ldq, 1), ok && rows8(q, ldq),
-                   (run_unpack8<T, VEC>(q, ldq, scale, rows, cols, act, y, ldy, st)));
+  if (ok && !rows8(q, ldq)) return run_unpack8<T, 8, true>(q, ldq, scale, rows, cols, act, y, ldy, st);
+  SCAPE_VEC_SWITCH(ok && rows16(q, ldq, 1), ok,
+                   (run_unpack8<T, VEC, false>(q, ldq, scale, rows, cols, act, y, ldy, st)));
 }
 template <typename T>
 cudaError_t act_grad_of(const T* dy, int64_t lddy, const uint8_t* q, int64_t ldq,

@@ -38,6 +38,7 @@ struct Epilogue {
   int out_f32;
   // rows aligned for 16 bytes (1; pre: 8 bytes) or for 32 (2)
   int out_vec, res_vec, q_vec, pre_vec;
+  int out_align;  // bytes that rows of out are aligned for: 2, 4 or 8 (with out_vec: more)
 };
 
 struct GemmOperand {
@@ -536,10 +537,45 @@ __device__ __forceinline__ void store_row(const float (&v)[N], int64_t row, int 
   }
 }
 
+// Rows of a box in shared memory, written out G bytes a lane (the rows' alignment).
+template <int G>
+__device__ __forceinline__ void store_box_rows(uint32_t box, int lane, char* out, int64_t pitch, int rows,
+                                               int left) {
+  constexpr int kLanes = 64 / G, kRows = 32 / kLanes;  // lanes a row, rows at a time
+  const int at = lane % kLanes * G, r0 = lane / kLanes;
+#pragma unroll 8
+  for (int r = r0; r < 32; r += kRows) {
+    const uint32_t from = box + r * 64 + (((at >> 4) ^ ((r >> 1) & 3)) << 4) + (at & 15);
+    char* to = out + r * pitch + at;
+    if constexpr (G == 8) {
+      uint32_t x, y;
+      asm volatile("ld.shared::cta.v2.b32 {%0, %1}, [%2];" : "=r"(x), "=r"(y) : "r"(from) : "memory");
+      if (r < rows && at + 8 <= 2 * left) {
+        *reinterpret_cast<uint2*>(to) = make_uint2(x, y);
+      } else if (r < rows) {
+        if (at < 2 * left) reinterpret_cast<uint16_t*>(to)[0] = (uint16_t)x;
+        if (at + 2 < 2 * left) reinterpret_cast<uint16_t*>(to)[1] = (uint16_t)(x >> 16);
+        if (at + 4 < 2 * left) reinterpret_cast<uint16_t*>(to)[2] = (uint16_t)y;
+      }
+    } else if constexpr (G == 4) {
+      uint32_t x;
+      asm volatile("ld.shared::cta.b32 %0, [%1];" : "=r"(x) : "r"(from) : "memory");
+      if (r < rows && at + 4 <= 2 * left)
+        *reinterpret_cast<uint32_t*>(to) = x;
+      else if (r < rows && at < 2 * left)
+        *reinterpret_cast<uint16_t*>(to) = (uint16_t)x;
+    } else {
+      uint16_t x;
+      asm volatile("ld.shared::cta.u16 %0, [%1];" : "=h"(x) : "r"(from) : "memory");
+      if (r < rows && at < 2 * left) *reinterpret_cast<uint16_t*>(to) = x;
+    }
+  }
+}
+
 // A warp's 32 x 32 values, one row a lane, through shared memory: 64-byte rows
 // whose 16-byte quarters are swizzled as the output's tensor map has them, so
 // neither side meets a bank twice.  Aligned outputs leave as one bulk copy
-// (which cuts what is past the matrix), others row by row, a lane a column.
+// (which cuts what is past the matrix), others row by row.
 __device__ __forceinline__ void store_box(const float (&v)[32], uint32_t box, int lane,
                                           const CUtensorMap* map, int64_t row0, int c0, int rows,
                                           int left, const Epilogue& e) {
@@ -556,17 +592,13 @@ __device__ __forceinline__ void store_box(const float (&v)[32], uint32_t box, in
     if (lane == 0) tma_store(map, c0, (int)row0, box);
   } else {
     __syncwarp();
-    uint16_t* o = static_cast<uint16_t*>(e.out) + row0 * e.ldo + c0 + lane;
-    const uint32_t from = box + (lane & 7) * 2;
-#pragma unroll 8
-    for (int r = 0; r < 32; ++r) {
-      uint16_t x;
-      asm volatile("ld.shared::cta.u16 %0, [%1];"
-                   : "=h"(x)
-                   : "r"(from + r * 64 + (((lane >> 3) ^ ((r >> 1) & 3)) << 4))
-                   : "memory");
-      if (r < rows && lane < left) o[r * e.ldo] = x;
-    }
+    char* out = static_cast<char*>(e.out) + (row0 * e.ldo + c0) * 2;
+    if (e.out_align == 8)
+      store_box_rows<8>(box, lane, out, e.ldo * 2, rows, left);
+    else if (e.out_align == 4)
+      store_box_rows<4>(box, lane, out, e.ldo * 2, rows, left);
+    else
+      store_box_rows<2>(box, lane, out, e.ldo * 2, rows, left);
   }
 }
 

@@ -382,7 +382,7 @@ __global__ __launch_bounds__(kSumThreads) void colsum_kernel(
   float s[VEC];
 #pragma unroll
   for (int j = 0; j < VEC; ++j) s[j] = 0.0f;
-  constexpr int kUnroll = 4;
+  constexpr int kUnroll = 8;
   for (int64_t r = begin + r0; r < end; r += kRows * kUnroll) {
     Raw<bf16, VEC> v[kUnroll];
 #pragma unroll
