@@ -263,6 +263,13 @@ __device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, uint32_t rank) {
 __device__ __forceinline__ void cluster_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+__device__ __forceinline__ float4 block_load(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cta.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr));
+  return v;
+}
 __device__ __forceinline__ float4 cluster_load(uint32_t addr, uint32_t rank) {
   float4 v;
   asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
@@ -615,6 +622,74 @@ struct GemmShape {
   unsigned int* status;
 };
 
+// Split tiles: a warp's part of the sum over the cluster's partial tiles, in rank
+// order, and the epilogue: 8 rows of 32 columns at a time, two such groups
+// together.  A block does this once, so its time is latency: groups in flight
+// together, no division, and a block's own part from its own shared memory.
+template <int KIND, int BN, bool FULL>
+__device__ __forceinline__ void join_parts(const Epilogue& e, uint32_t smem, int tm, int tn, int m, int n,
+                                           uint32_t rank, uint32_t ranks) {
+  using TL = Tile<KIND, BN, kModeSplit, FULL>;
+  const int warp = (threadIdx.x >> 5) - 4, lane = threadIdx.x & 31;
+  const int log_rows8 = 4 - (__ffs(ranks) - 1);  // 16 / ranks groups of 8 rows
+  const int groups = (BN / 32) << log_rows8;
+#pragma unroll 1
+  for (int g0 = warp; g0 < groups; g0 += 2 * TL::kEpilogueWarps) {
+    float v[2][8];
+    Beside<KIND, 8> beside[2];
+    int r[2], c[2];
+    bool live[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int g = g0 + k * TL::kEpilogueWarps;
+      r[k] = ((rank << log_rows8) + (g & ((1 << log_rows8) - 1))) * 8 + (lane & 7);
+      c[k] = (g >> log_rows8) * 32 + (lane >> 3) * 8;
+      live[k] = g < groups && tm * kBM + r[k] < m;
+      if (g >= groups) r[k] = c[k] = 0;
+      load_beside<KIND, FULL, 8>(beside[k], live[k], (int64_t)tm * kBM + r[k], tn * BN + c[k],
+                                 n - tn * BN - c[k], e);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[k][i] = 0.0f;
+    }
+#pragma unroll 1
+    for (uint32_t q = 0; q < ranks; q += 2) {
+      float4 part[2][2][2];
+#pragma unroll
+      for (uint32_t i = 0; i < 2; ++i)
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          if (q + i < ranks) {
+            const uint32_t at = smem + 4 * (TL::kPartialLd * r[k] + c[k]);
+            if (q + i == rank) {
+              part[i][k][0] = block_load(at), part[i][k][1] = block_load(at + 16);
+            } else {
+              part[i][k][0] = cluster_load(at, q + i), part[i][k][1] = cluster_load(at + 16, q + i);
+            }
+          }
+#pragma unroll
+      for (uint32_t i = 0; i < 2; ++i)
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          if (q + i < ranks) {
+            const float4 a = part[i][k][0], b = part[i][k][1];
+            v[k][0] += a.x, v[k][1] += a.y, v[k][2] += a.z, v[k][3] += a.w;
+            v[k][4] += b.x, v[k][5] += b.y, v[k][6] += b.z, v[k][7] += b.w;
+          }
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int64_t row = (int64_t)tm * kBM + r[k];
+      const int c0 = tn * BN + c[k], left = n - c0;
+      if (KIND == kGemmForward && e.bias) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[k][i] += i < left ? __bfloat162float(e.bias[c0 + i]) : 0.0f;
+      }
+      epilogue_math<KIND, FULL, 8>(v[k], beside[k], live[k], row, c0, left, e);
+      if (live[k] && left > 0) store_row<KIND, 8>(v[k], row, c0, left, e);
+    }
+  }
+}
+
 template <int KIND, int BN, int MODE, bool FULL>
 __global__ __launch_bounds__(Tile<KIND, BN, MODE, FULL>::kThreads, 1) void gemm_kernel(
     const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
@@ -906,55 +981,20 @@ __global__ __launch_bounds__(Tile<KIND, BN, MODE, FULL>::kThreads, 1) void gemm_
   if constexpr (PAIR) {
     cluster_sync();
   } else {
-    // Each block adds up its share of the tile's rows over the cluster's partial
-    // tiles, in rank order.
-    cluster_sync();
+    auto sync_parts = [&] {
+      if (ranks > 1)
+        cluster_sync();
+      else
+        __syncthreads();
+    };
+    sync_parts();
     if (warp >= 4 && !gave_up) {
       int tm, tn;
       tile_at(first, tm, tn);
-      const int rows = kBM / ranks;
-      const int groups = rows / 8 * (BN / 32);
-      for (int g = warp - 4; g < groups; g += TL::kEpilogueWarps) {
-        const int r = rank * rows + g % (rows / 8) * 8 + (lane & 7);
-        const int c = g / (rows / 8) * 32 + (lane >> 3) * 8;
-        const int64_t row = (int64_t)tm * kBM + r;
-        const int c0 = tn * BN + c, left = s.n - c0;
-        const bool live = row < s.m;
-        Beside<KIND, 8> beside;
-        load_beside<KIND, FULL, 8>(beside, live, row, c0, left, e);
-        float v[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          v[i] = KIND == kGemmForward && e.bias && i < left ? __bfloat162float(e.bias[c0 + i]) : 0.0f;
-        float sum[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) sum[i] = 0.0f;
-        const uint32_t at = smem + 4 * (TL::kPartialLd * r + c);
-        // four blocks' parts at a time in flight
-        for (uint32_t q = 0; q < ranks; q += 4) {
-          float4 part[4][2];
-#pragma unroll
-          for (uint32_t i = 0; i < 4; ++i)
-            if (q + i < ranks) {
-              part[i][0] = cluster_load(at, q + i);
-              part[i][1] = cluster_load(at + 16, q + i);
-            }
-#pragma unroll
-          for (uint32_t i = 0; i < 4; ++i)
-            if (q + i < ranks) {
-              sum[0] += part[i][0].x, sum[1] += part[i][0].y, sum[2] += part[i][0].z;
-              sum[3] += part[i][0].w, sum[4] += part[i][1].x, sum[5] += part[i][1].y;
-              sum[6] += part[i][1].z, sum[7] += part[i][1].w;
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] += sum[i];
-        epilogue_math<KIND, FULL, 8>(v, beside, live, row, c0, left, e);
-        if (live && left > 0) store_row<KIND, 8>(v, row, c0, left, e);
-      }
+      join_parts<KIND, BN, FULL>(e, smem, tm, tn, s.m, s.n, rank, ranks);
     }
     __syncwarp();
-    cluster_sync();
+    if (ranks > 1) cluster_sync();  // the parts have been read
   }
   tc_fence_before();
   __syncthreads();
