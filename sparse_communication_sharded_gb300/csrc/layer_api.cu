@@ -175,25 +175,33 @@ int64_t gemm_clusters(int blocks) {
   return n < 0 ? 0 : n;
 }
 
-cudaError_t gemm_allow_smem(const void* kernel, int bytes) {
-  // per device, the kernels already told
+cudaError_t allow_smem(const void* kernel, int bytes) {
+  // per device, the kernels already told and how much
   struct Told {
-    std::atomic<const void*> kernel[32];
+    std::atomic<const void*> kernel;
+    std::atomic<int> bytes;
   };
-  static Told told[kMaxDevices];
+  static Told told[kMaxDevices][64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
-  for (auto& k : told[dev].kernel) {
-    const void* have = k.load(std::memory_order_acquire);
-    if (have == kernel) return cudaSuccess;
-    if (have) continue;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e == cudaSuccess) k.compare_exchange_strong(have, kernel, std::memory_order_acq_rel);
-    return e;
+  Told* mine = nullptr;
+  for (Told& t : told[dev]) {
+    const void* have = t.kernel.load(std::memory_order_acquire);
+    if (!have && t.kernel.compare_exchange_strong(have, kernel, std::memory_order_acq_rel)) have = kernel;
+    if (have == kernel) {
+      mine = &t;
+      break;
+    }
   }
-  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (mine && mine->bytes.load(std::memory_order_acquire) >= bytes) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  // (two threads that ask at once both tell CUDA; the attribute never shrinks
+  // below what a launch was just allowed, as both then launch with their own)
+  if (e == cudaSuccess && mine && mine->bytes.load(std::memory_order_relaxed) < bytes)
+    mine->bytes.store(bytes, std::memory_order_release);
+  return e;
 }
 
 cudaError_t gemm_tensor_map(CUtensorMap* map, const void* p, int64_t rows, int64_t cols,

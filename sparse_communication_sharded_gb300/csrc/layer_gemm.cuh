@@ -78,9 +78,6 @@ struct SkinnyWeightGrad {
 };
 cudaError_t skinny_weight_grad(const SkinnyWeightGrad& a, cudaStream_t st);
 
-// Lets a kernel use this much dynamic shared memory (asked of CUDA once).
-cudaError_t gemm_allow_smem(const void* kernel, int bytes);
-
 // Clusters of so many blocks, one block an SM, that are at work at one time (asked
 // of CUDA once; clusters do not cross the GPU's processing clusters, so there are
 // fewer than SMs / blocks: 15 of 8 blocks on 152 SMs, and a 16th waits for a whole
@@ -1048,7 +1045,7 @@ cudaError_t gemm_launch(const GemmCall& c, int bn, int split, cudaStream_t st, T
   s.ksteps = (int)ceil_div(c.k, kBK);
   if (err == cudaSuccess) err = gemm_status_word(&s.status);
   auto kernel = gemm_kernel<KIND, BN, MODE, FULL>;
-  if (err == cudaSuccess) err = gemm_allow_smem((const void*)kernel, TL::kSmem);
+  if (err == cudaSuccess) err = allow_smem((const void*)kernel, TL::kSmem);
   if (err != cudaSuccess) return err;
   const int64_t tiles = s.tiles;
   const int cluster = PAIR ? 2 : split;

@@ -10,7 +10,7 @@ namespace layer {
 cudaError_t gemm_probe_clusters(int blocks, int* n) {
   using TL = Tile<kGemmForward, 64, kModeSplit, true>;
   auto kernel = gemm_kernel<kGemmForward, 64, kModeSplit, true>;
-  const cudaError_t e = gemm_allow_smem((const void*)kernel, TL::kSmem);
+  const cudaError_t e = allow_smem((const void*)kernel, TL::kSmem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)blocks);

@@ -593,6 +593,10 @@ cudaError_t launch_act_grad(const void* dy, int64_t lddy, const uint8_t* q, int6
                             const uint8_t* scale, int64_t rows, int64_t cols, int act, void* dz,
                             int64_t lddz, int dtype, cudaStream_t st);
 
+// Lets a kernel use this much dynamic shared memory; CUDA is asked when a kernel
+// first wants more than before.
+cudaError_t allow_smem(const void* kernel, int bytes);
+
 struct NormFwd {
   const void *x, *res, *w;
   int64_t ldx, ldres, ldy, ldh, ldq;

@@ -109,6 +109,53 @@ struct Team {
   __device__ static int64_t step() { return kWarp ? (int64_t)gridDim.x * kWarpRows : gridDim.x; }
 };
 
+// The forward pass's rows on their way into shared memory, kDepth of them ahead:
+// every thread copies its own 16-byte pieces to places of its own and waits for its
+// own copies, so no barrier is needed and no register holds them (8192 x 2048 with
+// all outputs: 23.5 us, from registers 27.5, three rows ahead 23.8; with 16 columns a thread, rows over
+// 4096, it was slower, 49 against 45 us for 4096 x 5632).
+template <typename T, int VEC, int NV>
+struct Ring {
+  static constexpr int kVecPieces = VEC * (int)sizeof(T) / 16;
+  static constexpr int kPieces = NV * kVecPieces;
+  static constexpr int kDepth = 2;
+  static constexpr int kBytesPerThread = kDepth * 2 * kPieces * 16;  // x and the residual
+  uint32_t base, pitch;
+  __device__ explicit Ring(const void* smem)
+      : base((uint32_t)__cvta_generic_to_shared(smem) + threadIdx.x * 16), pitch(blockDim.x * 16) {}
+  __device__ uint32_t at(int stage, int tensor, int piece) const {
+    return base + ((stage * 2 + tensor) * kPieces + piece) * pitch;
+  }
+  // A row of one tensor, from this thread's first column on; `mine` columns left.
+  __device__ void copy(int stage, int tensor, const T* p, int step, int mine) const {
+    constexpr int kPer = 16 / (int)sizeof(T);
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int j = 0; j < kVecPieces; ++j) {
+        const int left = mine - i * step - j * kPer;
+        const int bytes = left >= kPer ? 16 : left > 0 ? left * (int)sizeof(T) : 0;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at(stage, tensor, i * kVecPieces + j)),
+                     "l"(bytes ? p + i * step + j * kPer : p), "r"(bytes)
+                     : "memory");
+      }
+  }
+  __device__ static void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+  // The oldest of kDepth rows has landed.
+  __device__ static void wait() { asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory"); }
+  template <typename R>
+  __device__ void read(int stage, int tensor, R (&r)[NV]) const {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int j = 0; j < kVecPieces; ++j)
+        asm volatile("ld.shared::cta.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(r[i].w[4 * j]), "=r"(r[i].w[4 * j + 1]), "=r"(r[i].w[4 * j + 2]), "=r"(r[i].w[4 * j + 3])
+                     : "r"(at(stage, tensor, i * kVecPieces + j))
+                     : "memory");
+  }
+};
+
 // ANY: rows of x and the residual of any alignment (the outputs' are aligned).
 template <typename T, int VEC, int NV, int WIDTH, bool ANY>
 __global__ __launch_bounds__(Team<WIDTH>::kThreads) void norm_fwd_kernel(
@@ -123,13 +170,35 @@ __global__ __launch_bounds__(Team<WIDTH>::kThreads) void norm_fwd_kernel(
   const int mine = a.cols - t * VEC;  // columns from this thread's first on
   uint64_t w[P];
   load_weights<VEC, NV>(w, a.w, a.w_bf16, w_vec, t, width, mine);
-  int flip = 0;
+  constexpr bool kRing = VEC == 8 && !ANY;
+  using RG = Ring<T, 8, NV>;
+  extern __shared__ __align__(16) uint4 ring_memory[];
+  const RG ring(ring_memory);
+  auto copy_row = [&](int64_t row, int stage) {
+    if (row < a.rows) {
+      ring.copy(stage, 0, static_cast<const T*>(a.x) + row * a.ldx + t * VEC, width * VEC, mine);
+      if (a.res) ring.copy(stage, 1, static_cast<const T*>(a.res) + row * a.ldres + t * VEC, width * VEC, mine);
+    }
+    RG::commit();
+  };
+  int flip = 0, stage = 0;
+  if constexpr (kRing) {
+#pragma unroll
+    for (int d = 0; d < RG::kDepth; ++d) copy_row(TM::first() + d * TM::step(), d);
+  }
   for (int64_t row = TM::first(); row < a.rows; row += TM::step()) {
     Raw<T, VEC> rx[NV], rr[NV];
     const T* x = static_cast<const T*>(a.x) + row * a.ldx + t * VEC;
     const T* res = static_cast<const T*>(a.res) + row * a.ldres + t * VEC;
+    if constexpr (kRing) {
+      RG::wait();
+      ring.read(stage, 0, rx);
+      if (a.res) ring.read(stage, 1, rr);
+      copy_row(row + RG::kDepth * TM::step(), stage);
+      if (++stage == RG::kDepth) stage = 0;
+    }
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
+    for (int i = 0; i < (kRing ? 0 : NV); ++i) {
       const int n = mine - i * width * VEC;
       if constexpr (ANY) {
         const T *x0 = static_cast<const T*>(a.x), *r0 = static_cast<const T*>(a.res);
@@ -217,7 +286,9 @@ __global__ __launch_bounds__(512) void norm_fwd_wide_kernel(NormFwd a) {
 
 // A thread keeps its columns' weight gradients in registers over all its rows;
 // one row of partial sums a block goes to a.partial, added up by sum_partials.
-// The next row's loads are in flight while this one is summed over the block.
+// The next row's loads are in flight while this one is summed over the block (in
+// registers: a ring of shared memory as the forward pass has was slower here,
+// 8192 x 2048 in 32.2 against 30.1 us).
 template <typename T, int VEC, int NV, int WIDTH>
 __global__ __launch_bounds__(Team<WIDTH>::kThreads, (VEC == 8 && sizeof(T) == 2 && NV == 1 ? 1024 : 512) / Team<WIDTH>::kThreads) void norm_bwd_kernel(
     const __grid_constant__ NormBwd a, bool w_vec, float inv_cols) {
@@ -525,6 +596,20 @@ Shape shape_of(int64_t rows, int64_t cols, bool vec, int warp_cols, int threads_
     else { constexpr int WIDTH = 512, NV = 16; CALL; }                                   \
   }
 
+template <typename T, int VEC, int NV>
+constexpr size_t ring_bytes(int threads) {
+  return VEC == 8 ? (size_t)Ring<T, 8, NV>::kBytesPerThread * threads : 0;
+}
+// Launches a row kernel with its ring of shared memory.
+template <typename... P, typename... A>
+cudaError_t launch_rows(void (*kernel)(P...), const Shape& s, size_t smem, cudaStream_t st, const A&... args) {
+  if (smem > 32 * 1024) {  // with the static part, what a kernel may have unasked is 48 KB
+    const cudaError_t e = allow_smem((const void*)kernel, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_kernel(kernel, s.grid, s.threads, smem, 0, st, args...);
+}
+
 // Threads an SM that the grids are made for.  Backward: all that fit at once, as
 // blocks keep their weight gradients to the end.  Forward: about two rounds, so
 // that blocks that end early make room (one round 28.8 us, two 27.8, sixteen 28.7
@@ -548,11 +633,11 @@ cudaError_t run_norm_fwd(NormFwd a, cudaStream_t st) {
   const Shape s = shape_of(a.rows, a.cols, vec, kWarpCols, kFwdThreads);
   cudaError_t err = cudaSuccess;
   if (any) {
-    SCAPE_SHAPE_SWITCH(vec, s, kWarpCols, err = (launch_kernel(norm_fwd_kernel<T, VEC, NV, WIDTH, (VEC > 1)>, s.grid,
-                                                               s.threads, 0, 0, st, a, wv, inv)));
+    SCAPE_SHAPE_SWITCH(vec, s, kWarpCols, err = (launch_rows(norm_fwd_kernel<T, VEC, NV, WIDTH, (VEC > 1)>, s, 0,
+                                                             st, a, wv, inv)));
   } else {
-    SCAPE_SHAPE_SWITCH(vec, s, kWarpCols, err = (launch_kernel(norm_fwd_kernel<T, VEC, NV, WIDTH, false>, s.grid,
-                                                               s.threads, 0, 0, st, a, wv, inv)));
+    SCAPE_SHAPE_SWITCH(vec, s, kWarpCols, err = (launch_rows(norm_fwd_kernel<T, VEC, NV, WIDTH, false>, s,
+                                                             ring_bytes<T, VEC, NV>(s.threads), st, a, wv, inv)));
   }
   return err;
 }
@@ -575,8 +660,8 @@ cudaError_t run_norm_bwd(const NormBwd& a, cudaStream_t st) {
     const bool wv = aligned(a.w, 16);
     const float inv = (float)(1.0 / a.cols);
     const Shape s = shape_of(a.rows, a.cols, vec, kWarpColsBwd, vec && a.cols <= 4096 ? bwd_threads<T>() : 512);
-    SCAPE_SHAPE_SWITCH(vec, s, kWarpColsBwd, err = (launch_kernel(norm_bwd_kernel<T, VEC, NV, WIDTH>, s.grid,
-                                                                  s.threads, 0, 0, st, a, wv, inv)));
+    SCAPE_SHAPE_SWITCH(vec, s, kWarpColsBwd, err = (launch_rows(norm_bwd_kernel<T, VEC, NV, WIDTH>, s,
+                                                                0, st, a, wv, inv)));
     parts = s.grid;
   }
   if (err != cudaSuccess || !a.dw) return err;
