@@ -254,8 +254,8 @@ cudaError_t run_act_grad(const T* dy, int64_t lddy, const uint8_t* q, int64_t ld
 
 // Columns a thread, as the rows' alignment allows: 16 (one 16-byte word of 8-bit
 // values), 8, or 1: a warp then reads 32 neighbouring columns, a whole block, at
-// a time.  16 against 8: unpack8 of 8192 x 5632 to bfloat16 took 23.2 against
-// 26.5 us, the fewer addresses for the same bytes.
+// a time.  16 against 8: unpack8 of 8192 x 5632 to bfloat16 took 25.4 against
+// 26.4 us, the fewer addresses for the same bytes.
 #define SCAPE_VEC_SWITCH(v16, v8, CALL)                \
   do {                                                 \
     if (v16) { constexpr int VEC = 16; return CALL; }  \

@@ -1068,7 +1068,7 @@ cudaError_t gemm_pairs(const GemmCall& c, int bn, cudaStream_t st, TileRange ran
 // (measured: 590 clocks for 32 KB, whatever the width), whichever is more.  The
 // width with the least time is taken, or whole rounds of pairs with a second
 // launch for the tiles left over (4096 x 1280, contraction 3584: 80 tiles for 76
-// pairs, 42 us in two rounds, 30 us so).  Pairs want at least 3/4 of the SMs at
+// pairs, 42 us in two rounds, 33 us so).  Pairs want at least 3/4 of the SMs at
 // work.  Below that, narrow tiles, each cut over a cluster as far as there are
 // SMs and at least four stages of the contraction for every block.
 template <int KIND>
