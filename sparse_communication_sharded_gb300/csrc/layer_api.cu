@@ -462,6 +462,16 @@ extern "C" int scape_layer_linear_bwd_input(const void* dy, int64_t lddy, const 
   return cuda_result(e, "scape_layer_linear_bwd_input");
 }
 
+// Whether the bias sums go into the launch that unpacks the input: both read
+// memory, and neither fills the GPU to its end (8192 x 4096 against 1024 columns
+// of dy: 69.3 us with the product, in a launch of their own 72.2; 4096 x 1280
+// against 3584: 36.1, 41.1; 64 x 256 against 256: 6.4, 8.2).  Where the sums are
+// the longer part, a launch of their own has more of them in flight (65536 x 256
+// against 1024: 105 us, 98 so; 32768 x 64 against 512: 35.1, 31.1).
+static bool sums_beside(const void* dy, int64_t lddy, int64_t rows, int64_t k, int64_t n) {
+  return rows16(dy, lddy, 2) && (rows <= 16384 || k >= n);
+}
+
 extern "C" int scape_layer_linear_bwd_weight_workspace(const void* dy, int64_t lddy, const void* x,
                                                        int64_t ldx, int64_t rows, int64_t k,
                                                        int64_t n, size_t* bytes) {
@@ -523,7 +533,13 @@ extern "C" int scape_layer_linear_bwd_weight(const void* dy, int64_t lddy, const
     } else {
       bf16* a = reinterpret_cast<bf16*>(ws);
       ws += copy_bytes(rows, k);
-      e = launch_unpack8(q, ldq, scale, rows, k, activation, a, round8(k), SCAPE_BF16, st);
+      if (dbias && sums_beside(dy, lddy, rows, k, n)) {
+        e = launch_unpack8_sums(q, ldq, scale, rows, k, activation, a, round8(k),
+                                {static_cast<const bf16*>(dy), lddy, rows, n, dbias, grad_dtype == SCAPE_BF16}, st);
+        dbias = nullptr;
+      } else {
+        e = launch_unpack8(q, ldq, scale, rows, k, activation, a, round8(k), SCAPE_BF16, st);
+      }
       if (e == cudaSuccess) e = operands({dy, lddy, rows, n}, {a, round8(k), rows, k}, false, ws, &c, st);
     }
     c.m = n, c.n = k, c.k = rows;
@@ -535,7 +551,6 @@ extern "C" int scape_layer_linear_bwd_weight(const void* dy, int64_t lddy, const
     dy = c.a.p, lddy = c.a.ld;
   }
   if (e == cudaSuccess && dbias)
-    e = launch_colsum(static_cast<const bf16*>(dy), lddy, rows, n, dbias, grad_dtype == SCAPE_BF16,
-                      st);
+    e = launch_colsum({static_cast<const bf16*>(dy), lddy, rows, n, dbias, grad_dtype == SCAPE_BF16}, st);
   return cuda_result(e, who);
 }

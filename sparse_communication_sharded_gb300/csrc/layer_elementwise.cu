@@ -124,15 +124,26 @@ __device__ __forceinline__ Packed<VEC> load_packed(const uint8_t* q, int64_t ldq
   return p;
 }
 
-template <typename T, int VEC, int ACT, bool ANY>
+// SUMS: the grid's first sum_blocks blocks take column sums of another matrix.
+template <typename T, int VEC, int ACT, bool ANY, bool SUMS>
 __global__ __launch_bounds__(kThreads) void unpack8_kernel(const uint8_t* q, int64_t ldq, const uint8_t* lo,
                                                            const uint8_t* hi, const uint8_t* scale,
                                                            int64_t blocks_per_row, uint32_t units,
                                                            FastDiv per_row, int64_t cols, T* y,
-                                                           int64_t ldy) {
+                                                           int64_t ldy, const __grid_constant__ ColumnSums sums,
+                                                           uint32_t sum_blocks) {
   start();
+  uint32_t block = blockIdx.x;
+  if constexpr (SUMS) {
+    if (block < sum_blocks) {
+      cluster_begin();
+      sum_columns<kThreads, false>(sums);
+      return;
+    }
+    block -= sum_blocks;
+  }
   constexpr int U = unroll<VEC>();
-  const uint32_t first = blockIdx.x * (kThreads * U) + threadIdx.x;
+  const uint32_t first = block * (kThreads * U) + threadIdx.x;
   Unit un[U];
   Packed<VEC> p[U];
 #pragma unroll
@@ -227,14 +238,20 @@ cudaError_t run_pack8(const T* x, int64_t ldx, int64_t rows, int64_t cols, uint8
                          d, cols, q + r * ldq, ldq, scale + r * bpr, bpr);
   });
 }
-template <typename T, int VEC, bool ANY>
+template <typename T, int VEC, bool ANY, bool SUMS = false>
 cudaError_t run_unpack8(const uint8_t* q, int64_t ldq, const uint8_t* scale, int64_t rows,
-                        int64_t cols, int act, T* y, int64_t ldy, cudaStream_t st) {
+                        int64_t cols, int act, T* y, int64_t ldy, cudaStream_t st,
+                        const ColumnSums& sums = {}) {
   const int64_t bpr = ceil_div(cols, kBlock);
+  const int cluster = SUMS ? sum_cluster(sums.rows) : 0;
+  unsigned sum_blocks = SUMS ? (unsigned)(ceil_div(sums.cols, kSumCols) * cluster) : 0;
   return for_row_ranges<VEC>(rows, cols, [&](int64_t r, uint32_t units, FastDiv d, unsigned grid) {
     cudaError_t e = cudaSuccess;
-    SCAPE_ACT_SWITCH(act, e = (launch_kernel(unpack8_kernel<T, VEC, ACT, ANY>, grid, kThreads, 0, 0, st,
-                                             q + r * ldq, ldq, q, q + (rows - 1) * ldq + cols, scale + r * bpr, bpr, units, d, cols, y + r * ldy, ldy)));
+    if (SUMS) grid = (unsigned)(ceil_div(grid, cluster) * cluster) + sum_blocks;
+    SCAPE_ACT_SWITCH(act, e = (launch_kernel(unpack8_kernel<T, VEC, ACT, ANY, SUMS>, grid, kThreads, 0, cluster, st, q + r * ldq, ldq, q, q + (rows - 1) * ldq + cols,
+                                             scale + r * bpr, bpr, units, d, cols, y + r * ldy, ldy, sums,
+                                             sum_blocks)));
+    sum_blocks = 0;  // once
     return e;
   });
 }
@@ -303,6 +320,12 @@ cudaError_t launch_unpack8(const uint8_t* q, int64_t ldq, const uint8_t* scale, 
   return dtype == SCAPE_BF16
              ? unpack8_of(q, ldq, scale, rows, cols, act, static_cast<bf16*>(y), ldy, st)
              : unpack8_of(q, ldq, scale, rows, cols, act, static_cast<float*>(y), ldy, st);
+}
+cudaError_t launch_unpack8_sums(const uint8_t* q, int64_t ldq, const uint8_t* scale, int64_t rows,
+                                int64_t cols, int act, bf16* y, int64_t ldy, const ColumnSums& sums,
+                                cudaStream_t st) {
+  if (rows16(q, ldq, 1)) return run_unpack8<bf16, 16, false, true>(q, ldq, scale, rows, cols, act, y, ldy, st, sums);
+  return run_unpack8<bf16, 8, true, true>(q, ldq, scale, rows, cols, act, y, ldy, st, sums);
 }
 cudaError_t launch_act_grad(const void* dy, int64_t lddy, const uint8_t* q, int64_t ldq,
                             const uint8_t* scale, int64_t rows, int64_t cols, int act, void* dz,

@@ -583,12 +583,93 @@ __device__ __forceinline__ void to_first(float* p, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory");
 }
 
+// ------------------------------------------------------------------ column sums
+// Of m[rows, cols] in 32 bits: a cluster of `cluster` blocks shares kSumCols
+// columns, each block taking its share of the rows; the parts meet in the first
+// block's shared memory, in block order.  The clusters are the grid's first.
+struct ColumnSums {
+  const bf16* m;
+  int64_t ld, rows, cols;
+  void* out;
+  int out_bf16;
+};
+constexpr int kSumCols = 64;
+constexpr int kSumBlocks = 8;
+// In clusters of one block where there is little to add up: they start sooner.
+inline int sum_cluster(int64_t rows) { return rows <= 256 ? 1 : kSumBlocks; }
+
+// After cluster_begin(); eight columns a thread, rows of any alignment with ANY.
+template <int THREADS, bool ANY>
+__device__ __forceinline__ void sum_columns(const ColumnSums& a) {
+  constexpr int VEC = 8, kPerRow = kSumCols / VEC, kRows = THREADS / kPerRow, kUnroll = 8;
+  __shared__ float part[kRows][kSumCols + 4];
+  __shared__ float sums[kSumBlocks][kSumCols];
+  const bf16* hi = a.m + (a.rows - 1) * a.ld + a.cols;
+  const uint32_t rank = block_rank(), ranks = cluster_blocks();
+  const int at = threadIdx.x % kPerRow, r0 = threadIdx.x / kPerRow;
+  const int64_t c = (int64_t)(blockIdx.x / ranks) * kSumCols + at * VEC;
+  const int n = (int)min((int64_t)VEC, a.cols - c);
+  const int64_t begin = a.rows * rank / ranks, end = a.rows * (rank + 1) / ranks;
+  float s[VEC];
+#pragma unroll
+  for (int j = 0; j < VEC; ++j) s[j] = 0.0f;
+  for (int64_t r = begin + r0; r < end; r += kRows * kUnroll) {
+    Raw<bf16, VEC> v[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const bf16* p = a.m + (r + u * kRows) * a.ld + c;
+      const int left = r + u * kRows < end ? n : 0;
+      if constexpr (ANY)
+        v[u] = load_any<VEC>(p, left, a.m, hi);
+      else
+        v[u] = load_raw<VEC>(p, left);
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      float f[VEC];
+      to_floats(v[u], f);
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) s[j] += f[j];
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < VEC; ++j) part[r0][at * VEC + j] = s[j];
+  __syncthreads();
+  cluster_ready();
+  // to the first block: kSumCols sums of this one
+  if (threadIdx.x < kSumCols) {
+    float t = 0.0f;
+#pragma unroll 8
+    for (int k = 0; k < kRows; ++k) t += part[k][threadIdx.x];
+    to_first(&sums[rank][threadIdx.x], t);
+  }
+  cluster_done();
+  if (rank == 0 && threadIdx.x < kSumCols) {
+    const int64_t o = (int64_t)(blockIdx.x / ranks) * kSumCols + threadIdx.x;
+    float t = 0.0f;
+#pragma unroll
+    for (uint32_t k = 0; k < kSumBlocks; ++k)
+      if (k < ranks) t += sums[k][threadIdx.x];
+    if (o < a.cols) {
+      if (a.out_bf16)
+        static_cast<bf16*>(a.out)[o] = __float2bfloat16_rn(t);
+      else
+        static_cast<float*>(a.out)[o] = t;
+    }
+  }
+}
+
 // ------------------------------------------------------------------ launchers
 cudaError_t launch_pack8(const void* x, int64_t ldx, int dtype, int64_t rows, int64_t cols,
                          uint8_t* q, int64_t ldq, uint8_t* scale, cudaStream_t st);
 cudaError_t launch_unpack8(const uint8_t* q, int64_t ldq, const uint8_t* scale, int64_t rows,
                            int64_t cols, int act, void* y, int64_t ldy, int dtype,
                            cudaStream_t st);
+// unpack8 to bfloat16 rows on 16 bytes, and column sums of another matrix beside
+// it in the same launch.
+cudaError_t launch_unpack8_sums(const uint8_t* q, int64_t ldq, const uint8_t* scale, int64_t rows,
+                                int64_t cols, int act, bf16* y, int64_t ldy, const ColumnSums& sums,
+                                cudaStream_t st);
 cudaError_t launch_act_grad(const void* dy, int64_t lddy, const uint8_t* q, int64_t ldq,
                             const uint8_t* scale, int64_t rows, int64_t cols, int act, void* dz,
                             int64_t lddz, int dtype, cudaStream_t st);
@@ -625,8 +706,7 @@ int64_t norm_bwd_partials(int64_t rows, int64_t cols);
 cudaError_t launch_norm_bwd(const NormBwd& a, int dtype, cudaStream_t st);
 
 // Column sums of m[rows, cols] (bfloat16) in 32 bits.
-cudaError_t launch_colsum(const bf16* m, int64_t ld, int64_t rows, int64_t cols, void* out,
-                          int out_bf16, cudaStream_t st);
+cudaError_t launch_colsum(const ColumnSums& a, cudaStream_t st);
 // Sum of `parts` rows of partial[parts, cols].
 cudaError_t launch_sum_partials(const float* partial, int64_t parts, int64_t cols, void* out,
                                 int out_bf16, cudaStream_t st);

@@ -427,74 +427,12 @@ __global__ __launch_bounds__(256) void norm_dw_wide_kernel(NormBwd a) {
   a.partial[(int64_t)blockIdx.y * a.cols + c] = s;
 }
 
-// Column sums in one launch: a cluster of kSumBlocks blocks shares kSumCols
-// columns, each block taking its share of the rows; the parts meet in the first
-// block's shared memory, in block order.
-constexpr int kSumCols = 64;
-constexpr int kSumBlocks = 8;
-constexpr int kSumThreads = 512;
-
+constexpr int kColsumThreads = 512;
 template <bool ANY>
-__global__ __launch_bounds__(kSumThreads) void colsum_kernel(
-    const bf16* m, int64_t ld, int64_t rows, int64_t cols, void* out, int out_bf16) {
-  // eight columns a thread, rows of any alignment with ANY
-  constexpr int VEC = 8;
-  const bf16* hi = m + (rows - 1) * ld + cols;
-  constexpr int kPerRow = kSumCols / VEC, kRows = kSumThreads / kPerRow;
-  __shared__ float part[kRows][kSumCols + 4];
-  __shared__ float sums[kSumBlocks][kSumCols];
-  const uint32_t rank = block_rank(), ranks = cluster_blocks();
+__global__ __launch_bounds__(kColsumThreads) void colsum_kernel(const __grid_constant__ ColumnSums a) {
   cluster_begin();
   start();
-  const int at = threadIdx.x % kPerRow, r0 = threadIdx.x / kPerRow;
-  const int64_t c = (int64_t)(blockIdx.x / ranks) * kSumCols + at * VEC;
-  const int n = (int)min((int64_t)VEC, cols - c);
-  const int64_t begin = rows * rank / ranks, end = rows * (rank + 1) / ranks;
-  float s[VEC];
-#pragma unroll
-  for (int j = 0; j < VEC; ++j) s[j] = 0.0f;
-  constexpr int kUnroll = 8;
-  for (int64_t r = begin + r0; r < end; r += kRows * kUnroll) {
-    Raw<bf16, VEC> v[kUnroll];
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u)
-      if constexpr (ANY)
-        v[u] = load_any<VEC>(m + (r + u * kRows) * ld + c, r + u * kRows < end ? n : 0, m, hi);
-      else
-        v[u] = load_raw<VEC>(m + (r + u * kRows) * ld + c, r + u * kRows < end ? n : 0);
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      float f[VEC];
-      to_floats(v[u], f);
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) s[j] += f[j];
-    }
-  }
-#pragma unroll
-  for (int j = 0; j < VEC; ++j) part[r0][at * VEC + j] = s[j];
-  __syncthreads();
-  cluster_ready();
-  // to the first block: kSumCols sums of this one
-  if (threadIdx.x < kSumCols) {
-    float t = 0.0f;
-#pragma unroll 8
-    for (int k = 0; k < kRows; ++k) t += part[k][threadIdx.x];
-    to_first(&sums[rank][threadIdx.x], t);
-  }
-  cluster_done();
-  if (rank == 0 && threadIdx.x < kSumCols) {
-    const int64_t o = (int64_t)(blockIdx.x / ranks) * kSumCols + threadIdx.x;
-    float t = 0.0f;
-#pragma unroll
-    for (uint32_t k = 0; k < kSumBlocks; ++k)
-      if (k < ranks) t += sums[k][threadIdx.x];
-    if (o < cols) {
-      if (out_bf16)
-        static_cast<bf16*>(out)[o] = __float2bfloat16_rn(t);
-      else
-        static_cast<float*>(out)[o] = t;
-    }
-  }
+  sum_columns<kColsumThreads, ANY>(a);
 }
 
 // Sums of partial[parts, cols]: 32 columns a cluster, each of its blocks' warps
@@ -682,14 +620,12 @@ cudaError_t launch_norm_bwd(const NormBwd& a, int dtype, cudaStream_t st) {
   return dtype == SCAPE_BF16 ? run_norm_bwd<bf16>(a, st) : run_norm_bwd<float>(a, st);
 }
 
-// In clusters of one block where there is little to add up: they start sooner.
-cudaError_t launch_colsum(const bf16* m, int64_t ld, int64_t rows, int64_t cols, void* out,
-                          int out_bf16, cudaStream_t st) {
-  const int blocks = rows <= 256 ? 1 : kSumBlocks;
-  return launch_kernel(rows16(m, ld, 2) ? colsum_kernel<false> : colsum_kernel<true>,
-                       (unsigned)(ceil_div(cols, kSumCols) * blocks), kSumThreads, 0, blocks, st, m, ld, rows,
-                       cols, out, out_bf16);
+cudaError_t launch_colsum(const ColumnSums& a, cudaStream_t st) {
+  const int blocks = sum_cluster(a.rows);
+  return launch_kernel(rows16(a.m, a.ld, 2) ? colsum_kernel<false> : colsum_kernel<true>,
+                       (unsigned)(ceil_div(a.cols, kSumCols) * blocks), kColsumThreads, 0, blocks, st, a);
 }
+// In clusters of one block where there is little to add up: they start sooner.
 cudaError_t launch_sum_partials(const float* partial, int64_t parts, int64_t cols, void* out,
                                 int out_bf16, cudaStream_t st) {
   const int blocks = parts <= 128 ? 1 : kPartBlocks;
