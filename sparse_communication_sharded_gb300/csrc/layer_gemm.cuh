@@ -281,6 +281,9 @@ constexpr int kBK = 64;   // contraction a stage: one 128-byte swizzled row of b
 constexpr int kChunk = 8192;       // bytes of 64 staged rows of 128 bytes
 constexpr int kBoxBytes = 2048;    // 32 x 32 bfloat16 on their way out
 constexpr int kTileCost = 500;     // clocks a tile costs besides its stages
+// Clocks that a tile wider than 256 columns is read out with nothing beside it,
+// without and with an 8-bit output.
+constexpr int kWideCost = 3000, kWidePackCost = 6000;
 // A second, split launch: clocks a stage of a 128 x 128 tile, and besides.
 constexpr int kSmallStage = 600;
 constexpr int kSmallLaunch = 9000;
@@ -293,7 +296,9 @@ enum GemmMode {
   // Persistent pairs of blocks on neighbouring SMs: the pair's 256-row tile is
   // one tensor-core instruction stream, each block holding half of either
   // operand, so a byte read feeds twice the work it does in a single block.
-  // The tile's width is chosen at run time (a multiple of 32 up to BN = 256).
+  // The tile's width is chosen at run time (a multiple of 32 up to BN).  BN = 256
+  // keeps two accumulators; BN = 384 has one, written by two instructions: the
+  // first 256 columns and the others.
   kModePair = 1
 };
 
@@ -316,8 +321,9 @@ struct Tile {
   static constexpr int kBBytes = kBRows * kBK * 2;
   static constexpr int kStageBytes = kABytes + kBBytes;
   // as many stages as fit beside the output boxes and the bias
-  static constexpr int kStages = kStageBytes > 24576 ? 5 : 6;
-  static constexpr int kColumns = 2 * BN;  // two accumulators
+  static constexpr int kStages = kStageBytes > 32768 ? 4 : kStageBytes > 24576 ? 5 : 6;
+  static constexpr bool kWide = BN > 256;
+  static constexpr int kColumns = kWide ? 512 : 2 * BN;  // two accumulators
   static constexpr int kBoxAt = kStages * kStageBytes;
   static constexpr int kBiasAt = kBoxAt + (kPair ? kEpilogueWarps * 2 * kBoxBytes : 0);
   static constexpr int kSmem =
@@ -697,6 +703,7 @@ __global__ __launch_bounds__(Tile<KIND, BN, MODE, FULL>::kThreads, 1) void gemm_
   constexpr bool TA = KIND == kGemmWeightGrad;
   constexpr bool TB = KIND != kGemmForward;
   constexpr int kTileRows = PAIR ? 2 * kBM : kBM;
+  constexpr bool WIDE = TL::kWide;
   let_next_start();
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t bars[2 * TL::kStages + 5];
@@ -755,7 +762,9 @@ __global__ __launch_bounds__(Tile<KIND, BN, MODE, FULL>::kThreads, 1) void gemm_
   };
 
   const int bn = PAIR ? s.bn : BN;
-  const int b_rows = PAIR ? bn / 2 : BN;  // operand B rows this block stages
+  const int b_rows = WIDE ? 128 : PAIR ? bn / 2 : BN;  // operand B rows this block stages
+  // WIDE: beside those of the first 256 columns, its half of the others
+  const int b_more = WIDE ? bn / 2 - 128 : 0;
   const int tiles = s.tiles;
   const int first = blockIdx.x / ranks;
   const int step = PAIR ? gridDim.x / 2 : tiles;
@@ -784,8 +793,8 @@ __global__ __launch_bounds__(Tile<KIND, BN, MODE, FULL>::kThreads, 1) void gemm_
   if (warp == 0 && lane == 0) {
     // ---------------- producer: this block's rows of A and of B.  In a pair both
     // blocks' copies count on the first block's barrier, which expects them all.
-    const int b_boxes = TB ? (b_rows + 63) / 64 : 1;
-    const uint32_t bytes = s.a_bytes + (TB ? b_boxes * kChunk : b_rows * kBK * 2);
+    const int b_boxes = TB || WIDE ? (b_rows + 63) / 64 + (b_more + 63) / 64 : 1;
+    const uint32_t bytes = s.a_bytes + (TB || WIDE ? b_boxes * kChunk : b_rows * kBK * 2);
     const uint32_t lead = PAIR ? cluster_addr(bar0, 0) - bar0 : 0;
     int stage = 0, phase = 0;
     int64_t issued = 0;
@@ -795,6 +804,7 @@ __global__ __launch_bounds__(Tile<KIND, BN, MODE, FULL>::kThreads, 1) void gemm_
       tile_at(t, tm, tn);
       const int row_a = tm * kTileRows + (PAIR ? rank * kBM : 0);
       const int row_b = tn * bn + (PAIR ? rank * b_rows : 0);
+      const int row_b2 = tn * bn + 256 + (int)rank * b_more;
       for (int k = k0; k < k1; ++k) {
         ok = wait(empty(stage), phase ^ 1);
         if (!ok) break;
@@ -808,9 +818,11 @@ __global__ __launch_bounds__(Tile<KIND, BN, MODE, FULL>::kThreads, 1) void gemm_
         } else {
           tma_load<PAIR>(a, &map_a, k * kBK, row_a, bar);
         }
-        if constexpr (TB) {
-          for (int i = 0; i < b_boxes; ++i)
-            tma_load<PAIR>(b + i * kChunk, &map_b, row_b + i * 64, k * kBK, bar);
+        if constexpr (TB || WIDE) {
+          for (int i = 0; i < b_boxes; ++i) {
+            const int r = WIDE && i == 2 ? row_b2 : row_b + i * 64;
+            tma_load<PAIR>(b + i * kChunk, &map_b, TB ? r : k * kBK, TB ? k * kBK : r, bar);
+          }
         } else {
           tma_load<PAIR>(b, &map_b, k * kBK, row_b, bar);
         }
@@ -834,7 +846,8 @@ __global__ __launch_bounds__(Tile<KIND, BN, MODE, FULL>::kThreads, 1) void gemm_
     }
   } else if (warp == 1 && lane == 0 && (!PAIR || rank == 0)) {
     // ---------------- tensor core
-    const uint32_t idesc = instr_desc<kTileRows, TA, TB>(bn);
+    const uint32_t idesc = instr_desc<kTileRows, TA, TB>(WIDE ? 256 : bn);
+    const uint32_t idesc2 = WIDE ? instr_desc<kTileRows, TA, TB>(bn - 256) : 0;
     const uint64_t desc_a = smem_desc(smem, TA), desc_b = smem_desc(smem + TL::kABytes, TB);
     int stage = 0, phase = 0, acc = 0, acc_phase = 0;
     bool ok = true;
@@ -854,12 +867,18 @@ __global__ __launch_bounds__(Tile<KIND, BN, MODE, FULL>::kThreads, 1) void gemm_
 #pragma unroll
         for (int i = 0; i < kBK / 16; ++i)
           tc_mma<PAIR>(d, da + i * (TA ? 128 : 2), db + i * (TB ? 128 : 2), idesc, k > k0 || i > 0);
+        if constexpr (WIDE) {
+#pragma unroll
+          for (int i = 0; i < kBK / 16; ++i)
+            tc_mma<PAIR>(d + 256, da + i * (TA ? 128 : 2), db + ((2 * kChunk) >> 4) + i * (TB ? 128 : 2), idesc2,
+                         k > k0 || i > 0);
+        }
         tc_commit<PAIR>(empty(stage));
         if (++stage == TL::kStages) stage = 0, phase ^= 1;
       }
       if (!ok) break;
       tc_commit<PAIR>(acc_full(acc));
-      if (++acc == 2) acc = 0, acc_phase ^= 1;
+      if (WIDE || ++acc == 2) acc = 0, acc_phase ^= 1;
     }
     if (!ok) {
       tc_commit<PAIR>(drain);
@@ -972,7 +991,7 @@ __global__ __launch_bounds__(Tile<KIND, BN, MODE, FULL>::kThreads, 1) void gemm_
         else
           mbar_arrive(acc_empty(acc));
       }
-      if (++acc == 2) acc = 0, acc_phase ^= 1;
+      if (WIDE || ++acc == 2) acc = 0, acc_phase ^= 1;
       turn = (turn + TL::kGroups * 8 - bn / 32) % TL::kGroups;
     }
     if (lane == 0) tma_store_wait_all();
@@ -1028,7 +1047,7 @@ cudaError_t gemm_launch(const GemmCall& c, int bn, int split, cudaStream_t st, T
                        : gemm_tensor_map(&ma, c.a.p, c.m, c.k, c.a.ld, a_rows, kBK);
   if (err == cudaSuccess)
     err = TB ? gemm_tensor_map(&mb, c.b.p, c.k, c.n, c.b.ld, kBK, kBK)
-             : gemm_tensor_map(&mb, c.b.p, c.n, c.k, c.b.ld, PAIR ? bn / 2 : bn, kBK);
+             : gemm_tensor_map(&mb, c.b.p, c.n, c.k, c.b.ld, TL::kWide ? 64 : PAIR ? bn / 2 : bn, kBK);
   if (PAIR && c.e.out_vec && !c.e.out_f32) {
     if (err == cudaSuccess) err = gemm_tensor_map(&mo, c.e.out, c.m, c.n, c.e.ldo, 32, 32);
   } else {
@@ -1060,8 +1079,11 @@ cudaError_t gemm_launch(const GemmCall& c, int bn, int split, cudaStream_t st, T
 template <int KIND>
 cudaError_t gemm_pairs(const GemmCall& c, int bn, cudaStream_t st, TileRange range) {
   if constexpr (KIND != kGemmWeightGrad) {
-    if (c.e.act != SCAPE_ACT_NONE || c.e.q) return gemm_launch<KIND, 256, kModePair, true>(c, bn, 2, st, range);
+    if (c.e.act != SCAPE_ACT_NONE || c.e.q)
+      return bn > 256 ? gemm_launch<KIND, 384, kModePair, true>(c, bn, 2, st, range)
+                      : gemm_launch<KIND, 256, kModePair, true>(c, bn, 2, st, range);
   }
+  if (bn > 256) return gemm_launch<KIND, 384, kModePair, false>(c, bn, 2, st, range);
   return gemm_launch<KIND, 256, kModePair, false>(c, bn, 2, st, range);
 }
 
@@ -1071,8 +1093,10 @@ cudaError_t gemm_pairs(const GemmCall& c, int bn, cudaStream_t st, TileRange ran
 // 2 clocks a column on the tensor cores, or 18 a kilobyte that comes into the SM
 // (measured: 590 clocks for 32 KB, whatever the width), whichever is more.  The
 // width with the least time is taken, or whole rounds of pairs with a second
-// launch for the tiles left over (4096 x 1280, contraction 3584: 80 tiles for 76
-// pairs, 42 us in two rounds, 33 us so).  Pairs want at least 3/4 of the SMs at
+// launch for the tiles left over, or one round of wider tiles (4096 x 1280,
+// contraction 3584: 80 tiles for 76 pairs, 42 us in two rounds, 34.5 with 4 left
+// over, 26.1 as 64 of 320 columns; contraction 1280: 23.0 left over, 13.3 wide;
+// 5120 x 1024, 4096: 37.4, 31.8).  Pairs want at least 3/4 of the SMs at
 // work.  Below that, narrow tiles, each cut over a cluster as far as there are
 // SMs and at least four stages of the contraction for every block.
 template <int KIND>
@@ -1096,6 +1120,15 @@ cudaError_t gemm_run(const GemmCall& c, cudaStream_t st) {
     while (split < 8 && small <= gemm_clusters(split * 2) && ksteps / (split * 2) >= 4) split *= 2;
     const int64_t both_cost = tiles / pairs * tile + ceil_div(ksteps, split) * kSmallStage + kSmallLaunch;
     if (small <= gemm_clusters(split) && both_cost < least) best = bn, best_split = split, least = both_cost;
+  }
+  // One round of tiles of 320 or 384 columns, where that is less.  They are read
+  // out after their products, not beside them, so further rounds would wait, and
+  // a short contraction is better off with two rounds of narrow ones (forward,
+  // 4096 x 1280: 9.9 against 8.9 us at 512).
+  for (int bn = 384; bn > 256; bn -= 64) {
+    const int64_t tiles = tp * ceil_div(c.n, bn);
+    const int64_t cost = ksteps * std::max<int64_t>(2 * bn, 18 * 40) + kTileCost + (c.e.q ? kWidePackCost : kWideCost);
+    if (tiles <= pairs && tiles * 4 >= pairs * 3 && best && cost < least) best = bn, best_split = 0, least = cost;
   }
   if (best && best_split) {
     const int64_t whole = tp * ceil_div(c.n, best) / pairs * pairs;

@@ -352,6 +352,36 @@ def test_linear_tiles_left_over(cuda_device, m, n, k):
     assert L.status() == 0
 
 
+@pytest.mark.parametrize("m,n,k,act", [
+    (4090, 1272, 72, None), (4090, 1272, 72, "gelu"), (4864, 1100, 40, "relu"), (4700, 1149, 300, "silu"),
+    (20224, 256, 1800, "gelu")])
+def test_linear_other_tilings(cuda_device, m, n, k, act):
+    """Products whose tiles go out in one round of wider ones, and (the last case)
+    with tiles left over where wider ones do not help."""
+    xf, wf, b = rand(1, m, k), rand(2, n, k, scale=0.03), rand(3, n)
+    z, e = xf.double() @ wf.double().t() + b.double(), product_error(xf, wf.t(), k)
+    if act:
+        y, z8 = L.linear(xf, wf, bias=b, activation=act, keep_pre=True)
+        near(L.unpack8(z8, dtype=F32), z, R.pack_error(z) + 1.1 * e + z.abs() * 2.0 ** -23
+             + R.blocks(e).amax(-1).repeat_interleave(32, dim=1)[:, :n] * 2.0 ** -17, "z8")
+    else:
+        y = L.linear(xf, wf, bias=b)
+    want = R.act(z, act) if act else z
+    near(y, want, want.abs() * R.U_BF16 + 1.2 * e + z.abs() * 2.0 ** -23 + want.abs() * R.ACT_REL, "y")
+    pre = L.pack8(rand(9, m, n, scale=2.0)) if act else None
+    x, w2 = rand(1, m, k), rand(5, k, n, scale=0.03)
+    want, e = x.double() @ w2.double(), product_error(x, w2, k)
+    if act:
+        e = e * 1.2 + want.abs() * 3 * R.ACT_REL
+        want = want * R.slope(vals(pre), act)
+    near(L.linear_backward_input(x, w2, pre=pre, activation=act), want, want.abs() * R.U_BF16 + e, "dx")
+    dy, x2 = rand(6, k, m, scale=0.01), rand(7, k, n)
+    want, e = dy.double().t() @ x2.double(), product_error(dy.t(), x2, k)
+    near(L.linear_backward_weight(dy, x2), want, want.abs() * R.U_BF16 + e, "dw")
+    near(L.linear_backward_weight(dy, x2, grad_dtype=F32), want, want.abs() * R.U_F32 + e, "dw32")
+    assert L.status() == 0
+
+
 def test_linear_gradients_against_differences(cuda_device):
     """d/dt of sum(c * act-linear(x)) with the input made by gelu from z: the
     64-bit formula's central differences along random directions of z and w."""
