@@ -6,6 +6,7 @@
 #include <cstdio>
 
 #include "layer_gemm.cuh"
+#include "layer_limits.h"
 
 namespace scapek {
 namespace layer {
@@ -13,7 +14,7 @@ namespace {
 
 __device__ unsigned int g_status;  // set by a kernel that gave up a wait
 
-constexpr int kMaxDevices = 64;
+constexpr int kMaxDevices = RaisedLimits::kDevices;
 std::atomic<unsigned int*> g_status_word[kMaxDevices];
 
 thread_local char g_error[256];
@@ -176,32 +177,14 @@ int64_t gemm_clusters(int blocks) {
 }
 
 cudaError_t allow_smem(const void* kernel, int bytes) {
-  // per device, the kernels already told and how much
-  struct Told {
-    std::atomic<const void*> kernel;
-    std::atomic<int> bytes;
-  };
-  static Told told[kMaxDevices][64];
+  static RaisedLimits limits;
   int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  const cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
-  Told* mine = nullptr;
-  for (Told& t : told[dev]) {
-    const void* have = t.kernel.load(std::memory_order_acquire);
-    if (!have && t.kernel.compare_exchange_strong(have, kernel, std::memory_order_acq_rel)) have = kernel;
-    if (have == kernel) {
-      mine = &t;
-      break;
-    }
-  }
-  if (mine && mine->bytes.load(std::memory_order_acquire) >= bytes) return cudaSuccess;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  // (two threads that ask at once both tell CUDA; the attribute never shrinks
-  // below what a launch was just allowed, as both then launch with their own)
-  if (e == cudaSuccess && mine && mine->bytes.load(std::memory_order_relaxed) < bytes)
-    mine->bytes.store(bytes, std::memory_order_release);
-  return e;
+  return limits.raise(dev, kernel, bytes, cudaErrorMemoryAllocation, [&](int b) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, b);
+  });
 }
 
 cudaError_t gemm_tensor_map(CUtensorMap* map, const void* p, int64_t rows, int64_t cols,

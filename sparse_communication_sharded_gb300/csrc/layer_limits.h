@@ -1,0 +1,55 @@
+// layer_limits.h -- what CUDA has been told a kernel may use, per device.  Host code
+// without CUDA's headers, so that a test can interleave its callers.
+#pragma once
+
+#include <atomic>
+#include <mutex>
+
+namespace scapek {
+namespace layer {
+
+// Each kernel's limit on each device, which only rises.  CUDA's call sets a limit
+// and does not raise it, so the comparison, the call and the record are one step
+// under a lock: with two callers between them, the smaller limit could be the one
+// that stays while the larger is on record, and the larger launch fails from then on.
+// A limit on record is read without the lock.
+class RaisedLimits {
+ public:
+  static constexpr int kDevices = 64, kKernels = 64;
+
+  // Calls set(bytes), which returns 0 or an error, unless the kernel has that much
+  // already.  Returns set's error, or `full` where there is no place left.
+  template <typename E, typename Set>
+  E raise(int device, const void* kernel, int bytes, E full, Set&& set) {
+    Place* const places = places_[device];
+    for (int i = 0; i < kKernels; ++i) {
+      const void* k = places[i].kernel.load(std::memory_order_acquire);
+      if (!k) break;
+      if (k == kernel && places[i].bytes.load(std::memory_order_acquire) >= bytes) return E(0);
+    }
+    std::lock_guard<std::mutex> hold(lock_);
+    for (int i = 0; i < kKernels; ++i) {
+      Place& p = places[i];
+      const void* k = p.kernel.load(std::memory_order_relaxed);
+      if (k && k != kernel) continue;
+      if (k && p.bytes.load(std::memory_order_relaxed) >= bytes) return E(0);
+      const E e = set(bytes);
+      if (e != E(0)) return e;
+      p.bytes.store(bytes, std::memory_order_release);
+      p.kernel.store(kernel, std::memory_order_release);
+      return E(0);
+    }
+    return full;
+  }
+
+ private:
+  struct Place {
+    std::atomic<const void*> kernel{nullptr};
+    std::atomic<int> bytes{0};
+  };
+  Place places_[kDevices][kKernels];
+  std::mutex lock_;
+};
+
+}  // namespace layer
+}  // namespace scapek

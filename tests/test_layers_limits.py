@@ -1,0 +1,95 @@
+"""The record of what CUDA was told a kernel may use, with two host threads in it
+at once (csrc/layer_limits.h, compiled here; CUDA's call is a fake)."""
+import os
+import subprocess
+
+import pytest
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
+                    "sparse_communication_sharded_gb300", "csrc")
+
+PROGRAM = r"""
+#include <chrono>
+#include <condition_variable>
+#include <cstdio>
+#include <cstdlib>
+#include <initializer_list>
+#include <thread>
+#include "layer_limits.h"
+
+using namespace std::chrono_literals;
+static std::mutex m;
+static std::condition_variable cv;
+static bool inside = false, second_done = false;
+static int attribute = 0, calls = 0;  // what "CUDA" holds
+
+static int set(int bytes, bool first, bool holds_after) {
+  std::unique_lock<std::mutex> l(m);
+  ++calls;
+  if (holds_after) attribute = bytes;
+  if (first) {
+    // lets the other thread do what it can, whole or not at all
+    inside = true;
+    cv.notify_all();
+    cv.wait_for(l, 500ms, [] { return second_done; });
+  }
+  if (!holds_after) attribute = bytes;
+  return 0;
+}
+
+int main(int argc, char** argv) {
+  const int first = atoi(argv[1]), second = atoi(argv[2]);
+  const bool holds_after = atoi(argv[3]);  // the first call takes effect before or after the second's
+  static scapek::layer::RaisedLimits limits;
+  const int kernel = 0;
+  std::thread a([&] { limits.raise(0, &kernel, first, -1, [&](int b) { return set(b, true, holds_after); }); });
+  std::thread b([&] {
+    {
+      std::unique_lock<std::mutex> l(m);
+      cv.wait(l, [] { return inside; });
+    }
+    limits.raise(0, &kernel, second, -1, [&](int x) { return set(x, false, true); });
+    std::unique_lock<std::mutex> l(m);
+    second_done = true;
+    cv.notify_all();
+  });
+  a.join();
+  b.join();
+  // every size that was asked for must launch now, from the record or by another call
+  for (int bytes : {first, second}) {
+    const int r = limits.raise(0, &kernel, bytes, -1, [&](int x) { return set(x, false, true); });
+    if (r != 0 || attribute < bytes) {
+      printf("%d bytes allowed, the attribute is %d\n", bytes, attribute);
+      return 1;
+    }
+  }
+  // errors are passed on and not recorded; another kernel and device are their own
+  const int other = 0;
+  if (limits.raise(0, &other, 64, -1, [](int) { return 7; }) != 7) return 2;
+  int told = 0;
+  if (limits.raise(0, &other, 64, -1, [&](int) { return ++told, 0; }) != 0 || told != 1) return 3;
+  if (limits.raise(1, &other, 64, -1, [&](int) { return ++told, 0; }) != 0 || told != 2) return 4;
+  if (limits.raise(1, &other, 32, -1, [&](int) { return ++told, 0; }) != 0 || told != 2) return 5;
+  // no place left: the call says so
+  static int many[80];
+  int full = 0;
+  for (int& k : many) full += limits.raise(2, &k, 1, -1, [](int) { return 0; }) == -1;
+  return full == 80 - scapek::layer::RaisedLimits::kKernels ? 0 : 6;
+}
+"""
+
+
+@pytest.fixture(scope="module")
+def program(tmp_path_factory):
+    d = tmp_path_factory.mktemp("limits")
+    src, exe = d / "limits.cpp", d / "limits"
+    src.write_text(PROGRAM)
+    subprocess.run(["g++", "-std=c++17", "-O1", "-pthread", f"-I{CSRC}", str(src), "-o", str(exe)], check=True)
+    return str(exe)
+
+
+@pytest.mark.parametrize("first,second", [(65536, 36864), (36864, 65536), (65536, 65536)])
+@pytest.mark.parametrize("early", [0, 1])
+def test_two_threads_raise_one_kernel(program, first, second, early):
+    r = subprocess.run([program, str(first), str(second), str(early)], capture_output=True, text=True, timeout=30)
+    assert r.returncode == 0, r.stdout
