@@ -22,6 +22,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libscape.so")
 BINDING_SRC = os.path.join(CSRC, "layers_torch.cpp")
 BINDING = os.path.join(BUILD, "_layers_torch.so")
+BINDING_FOR = os.path.join(BUILD, "_layers_torch.for")  # what the binding was built against
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2",
@@ -47,7 +48,25 @@ def is_stale() -> bool:
     if not os.path.exists(LIB) or not os.path.exists(BINDING):
         return True
     t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
-    return any(os.path.getmtime(p) > t for p in _deps())
+    return any(os.path.getmtime(p) > t for p in _deps()) or binding_mismatch() is not None
+
+
+def _here() -> str:
+    """The interpreter and torch that a binding built now would fit."""
+    import torch
+    return (f"python {sys.version_info.major}.{sys.version_info.minor}, torch {torch.__version__}, "
+            f"C++11 ABI {int(torch._C._GLIBCXX_USE_CXX11_ABI)}")
+
+
+def binding_mismatch() -> str | None:
+    """Why the built binding does not fit this process, or None: it uses torch's C++
+    classes, whose layout another torch may have changed without a missing symbol."""
+    try:
+        with open(BINDING_FOR) as f:
+            built = f.read()
+    except OSError:
+        built = "unknown"
+    return None if built == _here() else f"built for {built}; this is {_here()}"
 
 
 def _torch_dir():
@@ -79,7 +98,11 @@ def _link_binding(obj):
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr}")
+    if os.path.exists(BINDING_FOR):
+        os.remove(BINDING_FOR)  # no moment at which it stands for another binding
     os.replace(tmp, BINDING)
+    with open(BINDING_FOR, "w") as f:
+        f.write(_here())
 
 
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:

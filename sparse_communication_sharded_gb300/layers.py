@@ -30,11 +30,16 @@ _binding = None
 
 
 def _lib():
-    """The binding (csrc/layers_torch.cpp); raises if it has not been built."""
+    """The binding (csrc/layers_torch.cpp); raises if it has not been built, or for
+    another torch."""
     global _binding
     if _binding is None:
         if not os.path.exists(_build.BINDING):
             raise ImportError(f"{_build.BINDING} not found: build it with "
+                              "`python -m sparse_communication_sharded_gb300.build`")
+        why = _build.binding_mismatch()
+        if why:
+            raise ImportError(f"{_build.BINDING} was {why}: build it again with "
                               "`python -m sparse_communication_sharded_gb300.build`")
         name = "_layers_torch"
         loader = importlib.machinery.ExtensionFileLoader(name, _build.BINDING)
