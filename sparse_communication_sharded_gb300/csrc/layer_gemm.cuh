@@ -206,6 +206,16 @@ __device__ __forceinline__ void tc_commit(uint32_t bar) {
         : "memory");
   }
 }
+// The same on this block's own barrier only.
+template <bool PAIR>
+__device__ __forceinline__ void tc_commit_own(uint32_t bar) {
+  if constexpr (PAIR)
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+        : "memory");
+  else
+    tc_commit<false>(bar);
+}
 template <bool PAIR>
 __device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
                                        bool accumulate) {
@@ -830,6 +840,13 @@ __global__ __launch_bounds__(Tile<KIND, BN, MODE, FULL>::kThreads, 1) void gemm_
         if (++stage == TL::kStages) stage = 0, phase ^= 1;
       }
     }
+    // The products of every stage are done, so its copies have landed: the tensor
+    // core may give up after the last copy was issued, and then nothing else would
+    // know that copies are in flight.
+    for (int i = 0; ok && i < TL::kStages; ++i) {
+      ok = wait(empty(stage), phase ^ 1);
+      if (++stage == TL::kStages) stage = 0, phase ^= 1;
+    }
     if (!ok) {
       // let the copies in flight land before the block's memory is given back
       const uint64_t t0 = now_ns();
@@ -880,12 +897,13 @@ __global__ __launch_bounds__(Tile<KIND, BN, MODE, FULL>::kThreads, 1) void gemm_
       tc_commit<PAIR>(acc_full(acc));
       if (WIDE || ++acc == 2) acc = 0, acc_phase ^= 1;
     }
-    if (!ok) {
-      tc_commit<PAIR>(drain);
-      const uint64_t t0 = now_ns();
-      while (!mbar_try(drain, 0))
-        if (now_ns() - t0 > kWaitLimitNs) break;
-    }
+    // Tensor memory is given back when all matrix instructions are done, also where
+    // the epilogue gave up before they were.  (On this block's barrier alone: the
+    // pair's other block does not wait for it and may be gone when it is signalled.)
+    tc_commit_own<PAIR>(drain);
+    const uint64_t t0 = now_ns();
+    while (!mbar_try(drain, 0))
+      if (now_ns() - t0 > kWaitLimitNs) break;
   } else if (warp >= 4) {
     // ---------------- epilogue: warp w reads the accumulator lanes of its quarter;
     // the warps of a quarter take 32-column chunks in turn, and go on with it in the
