@@ -12,6 +12,7 @@
 #include <cuda.h>
 
 #include "layer_internal.cuh"
+#include "layer_limits.h"
 
 namespace scapek {
 namespace layer {
@@ -297,7 +298,6 @@ constexpr int kWideCost = 3000, kWidePackCost = 6000;
 // A second, split launch: clocks a stage of a 128 x 128 tile, and besides.
 constexpr int kSmallStage = 600;
 constexpr int kSmallLaunch = 9000;
-constexpr uint64_t kWaitLimitNs = 2000000000ull;
 
 // How a product is laid over the blocks.
 enum GemmMode {
@@ -632,6 +632,7 @@ struct GemmShape {
   // a split launch for the tiles that pairs left over: pair tiles from tile_base
   // on, each cut into 2 x sub_n of this launch's (sub_n 0: tiles of its own)
   int tile_base, sub_n;
+  uint64_t product_ns;  // limit of the wait for an accumulator
   unsigned int* status;
 };
 
@@ -756,14 +757,14 @@ __global__ __launch_bounds__(Tile<KIND, BN, MODE, FULL>::kThreads, 1) void gemm_
 
   // Every wait ends: after the limit the kernel records it and all its roles
   // stop (they look at gave_up while they wait).
-  auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
+  auto wait = [&](uint32_t bar, uint32_t parity, uint64_t limit = kWaitLimitNs) -> bool {
     if (mbar_try(bar, parity)) return true;
     const uint64_t t0 = now_ns();
     for (;;) {
       for (int i = 0; i < 16; ++i)
         if (mbar_try(bar, parity)) return true;
       if (gave_up) return false;
-      if (now_ns() - t0 > kWaitLimitNs) {
+      if (now_ns() - t0 > limit) {
         gave_up = 1;
         atomicExch(s.status, 1u);
         return false;
@@ -940,7 +941,7 @@ __global__ __launch_bounds__(Tile<KIND, BN, MODE, FULL>::kThreads, 1) void gemm_
         }
         load_beside<KIND, FULL, 32>(next, live, row, col0, turn * 32 < bn ? s.n - col0 : 0, e);
       }
-      if (!__all_sync(0xFFFFFFFFu, wait(acc_full(acc), acc_phase))) break;
+      if (!__all_sync(0xFFFFFFFFu, wait(acc_full(acc), acc_phase, s.product_ns))) break;
       tc_fence_after();
       const uint32_t lanes = tmem + acc * BN + ((uint32_t)(quarter * 32) << 16) + turn * 32;
 #pragma unroll 1
@@ -1084,6 +1085,7 @@ cudaError_t gemm_launch(const GemmCall& c, int bn, int split, cudaStream_t st, T
   s.tiles = rest ? (int)((s.tiles_m * (int64_t)s.tiles_n - range.base) * 2 * s.sub_n)
                  : range.count ? (int)range.count : s.tiles_m * s.tiles_n;
   s.ksteps = (int)ceil_div(c.k, kBK);
+  s.product_ns = product_wait_ns(ceil_div(s.ksteps, PAIR ? 1 : split));
   if (err == cudaSuccess) err = gemm_status_word(&s.status);
   auto kernel = gemm_kernel<KIND, BN, MODE, FULL>;
   if (err == cudaSuccess) err = allow_smem((const void*)kernel, TL::kSmem);

@@ -1,8 +1,10 @@
-// layer_limits.h -- what CUDA has been told a kernel may use, per device.  Host code
-// without CUDA's headers, so that a test can interleave its callers.
+// layer_limits.h -- what the host keeps about kernels between calls: what CUDA has
+// been told they may use, and how long their waits may last.  Host code without
+// CUDA's headers, so that a test can interleave its callers.
 #pragma once
 
 #include <atomic>
+#include <cstdint>
 #include <mutex>
 
 namespace scapek {
@@ -50,6 +52,14 @@ class RaisedLimits {
   Place places_[kDevices][kKernels];
   std::mutex lock_;
 };
+
+// Every wait of the product kernels ends: one for a copy, a stage or an accumulator
+// to be read after two seconds.  An accumulator is not ready before its whole
+// contraction is done, so the wait for it has 5 us a stage of that more (a stage
+// takes 0.3 us): 2^31 rows make a weight gradient of 4 million stages a block, which
+// can last longer than two seconds.
+constexpr uint64_t kWaitLimitNs = 2000000000ull;
+constexpr uint64_t product_wait_ns(int64_t stages) { return kWaitLimitNs + (uint64_t)stages * 5000u; }
 
 }  // namespace layer
 }  // namespace scapek

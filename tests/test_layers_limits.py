@@ -1,5 +1,6 @@
-"""The record of what CUDA was told a kernel may use, with two host threads in it
-at once (csrc/layer_limits.h, compiled here; CUDA's call is a fake)."""
+"""What the host keeps about kernels between calls (csrc/layer_limits.h, compiled
+here): the record of what CUDA was told they may use, with two host threads in it
+at once and a fake for CUDA's call, and the limits of their waits."""
 import os
 import subprocess
 
@@ -36,6 +37,12 @@ static int set(int bytes, bool first, bool holds_after) {
   if (!holds_after) attribute = bytes;
   return 0;
 }
+
+using scapek::layer::kWaitLimitNs;
+using scapek::layer::product_wait_ns;
+static_assert(product_wait_ns(1) < 2 * kWaitLimitNs, "a short contraction fails as soon as any wait");
+// the longest contraction a block can have, 2^31 rows of 64 a stage, at 1 us a stage
+static_assert(product_wait_ns((int64_t{1} << 31) / 64) > ((uint64_t{1} << 31) / 64) * 1000, "and a long one lasts");
 
 int main(int argc, char** argv) {
   const int first = atoi(argv[1]), second = atoi(argv[2]);
