@@ -61,12 +61,20 @@ enum scape_activation {
 const char *scape_layer_last_error(void);
 
 /*
- * Reads and clears the device's record of kernels that gave up a wait (every
- * wait inside the matrix-product kernels ends after a time limit; a kernel
- * that gave up leaves its output incomplete).  0 = none.  Synchronises
- * `stream`.
+ * Waits that kernels on the current device have given up since the last call, by
+ * any thread (every wait inside the matrix-product kernels ends after a time
+ * limit; a kernel that gave up leaves its output incomplete, and the call that
+ * launched it returned SCAPE_OK).  0 = none, for all work before it on `stream`,
+ * which it synchronises.
  */
 int scape_layer_status(int *host_status, void *stream);
+
+/*
+ * Launches a kernel that waits limit_ns (1 ns to 2 s) for something that does not
+ * come, then gives up as a product kernel does.  It writes nothing else.  For
+ * tests of a program's handling of scape_layer_status().
+ */
+int scape_layer_probe_wait(int64_t limit_ns, void *stream);
 
 /* x[rows, cols] -> q[rows, cols], scale[rows, ceil(cols / 32)]. */
 int scape_layer_pack8(const void *x, int64_t ldx, int dtype, int64_t rows, int64_t cols,

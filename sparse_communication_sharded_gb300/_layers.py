@@ -12,6 +12,7 @@ ACTIVATIONS = {None: 0, "relu": 1, "gelu": 2, "silu": 3}
 PROTOS = {
     "scape_layer_last_error": (ctypes.c_char_p, []),
     "scape_layer_status": (_i32, [_vp, _vp]),
+    "scape_layer_probe_wait": (_i32, [_i64, _vp]),
     "scape_layer_pack8": (_i32, [_vp, _i64, _i32, _i64, _i64, _vp, _i64, _vp, _vp]),
     "scape_layer_unpack8": (_i32, [_vp, _i64, _vp, _i64, _i64, _i32, _vp, _i64, _i32, _vp]),
     "scape_layer_act_grad": (_i32, [_vp, _i64, _vp, _i64, _vp, _i64, _i64, _i32, _vp, _i64, _i32,

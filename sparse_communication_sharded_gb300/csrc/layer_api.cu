@@ -12,10 +12,11 @@ namespace scapek {
 namespace layer {
 namespace {
 
-__device__ unsigned int g_status;  // set by a kernel that gave up a wait
+__device__ unsigned int g_status;  // waits that kernels gave up
 
 constexpr int kMaxDevices = RaisedLimits::kDevices;
 std::atomic<unsigned int*> g_status_word[kMaxDevices];
+LastSeen g_status_seen[kMaxDevices];
 
 thread_local char g_error[256];
 
@@ -75,6 +76,17 @@ __global__ __launch_bounds__(256) void align_rows_kernel(const __grid_constant__
         *reinterpret_cast<uint4*>(m.dst + (row + 8 * i) * m.ldd + c) =
             make_uint4(v[i].w[0], v[i].w[1], v[i].w[2], v[i].w[3]);
   }
+}
+
+// A wait that runs out: nothing arrives at the barrier.
+__global__ void probe_wait_kernel(uint64_t limit_ns, unsigned int* count) {
+  start();
+  __shared__ __align__(8) uint64_t bar;
+  __shared__ volatile int gave_up;
+  if (threadIdx.x != 0) return;
+  mbar_init(smem_addr(&bar), 1);
+  gave_up = 0;
+  limited_wait(smem_addr(&bar), 0, limit_ns, &gave_up, count);
 }
 
 int64_t round8(int64_t n) { return (n + 7) / 8 * 8; }
@@ -225,15 +237,27 @@ extern "C" const char* scape_layer_last_error(void) { return g_error; }
 
 extern "C" int scape_layer_status(int* host_status, void* stream) {
   if (!host_status) return fail(SCAPE_EINVAL, "host_status is NULL");
+  *host_status = 0;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   unsigned int* word = nullptr;
   unsigned int v = 0;
+  int dev = 0;
   cudaError_t e = gemm_status_word(&word);
+  if (e == cudaSuccess) e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaMemcpyAsync(&v, word, sizeof v, cudaMemcpyDeviceToHost, st);
-  if (e == cudaSuccess) e = cudaMemsetAsync(word, 0, sizeof v, st);
   if (e == cudaSuccess) e = cudaStreamSynchronize(st);
-  *host_status = (int)v;
+  if (e == cudaSuccess) *host_status = g_status_seen[dev].news(v);
   return cuda_result(e, "scape_layer_status");
+}
+
+extern "C" int scape_layer_probe_wait(int64_t limit_ns, void* stream) {
+  if (limit_ns < 1 || limit_ns > (int64_t)kWaitLimitNs)
+    return fail(SCAPE_EINVAL, "limit_ns must be from 1 to two seconds");
+  unsigned int* word = nullptr;
+  cudaError_t e = gemm_status_word(&word);
+  if (e == cudaSuccess)
+    e = launch_kernel(probe_wait_kernel, dim3(1), 32, 0, 0, static_cast<cudaStream_t>(stream), (uint64_t)limit_ns, word);
+  return cuda_result(e, "scape_layer_probe_wait");
 }
 
 extern "C" int scape_layer_pack8(const void* x, int64_t ldx, int dtype, int64_t rows, int64_t cols,

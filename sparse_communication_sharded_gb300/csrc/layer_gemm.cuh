@@ -86,7 +86,7 @@ cudaError_t skinny_weight_grad(const SkinnyWeightGrad& a, cudaStream_t st);
 int64_t gemm_clusters(int blocks);
 cudaError_t gemm_probe_clusters(int blocks, int* n);
 
-// Where kernels record that they gave up a wait (one word a device).
+// Where kernels count the waits that they gave up (one word a device, never cleared).
 cudaError_t gemm_status_word(unsigned int** word);
 
 // 2-D tensor map of box_rows x box_cols boxes, their rows (64 or 128 bytes)
@@ -128,6 +128,23 @@ __device__ __forceinline__ uint64_t now_ns() {
   uint64_t t;
   asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
   return t;
+}
+// Every wait ends: after the limit the block records it (here and in the device's
+// count) and all its roles stop, as they look at gave_up while they wait.
+__device__ __forceinline__ bool limited_wait(uint32_t bar, uint32_t parity, uint64_t limit_ns,
+                                             volatile int* gave_up, unsigned int* count) {
+  if (mbar_try(bar, parity)) return true;
+  const uint64_t t0 = now_ns();
+  for (;;) {
+    for (int i = 0; i < 16; ++i)
+      if (mbar_try(bar, parity)) return true;
+    if (*gave_up) return false;
+    if (now_ns() - t0 > limit_ns) {
+      *gave_up = 1;
+      atomicAdd(count, 1u);
+      return false;
+    }
+  }
 }
 // PAIR: the copy signals a barrier of the pair's first block (bar is that one's
 // address in the cluster).
@@ -755,21 +772,8 @@ __global__ __launch_bounds__(Tile<KIND, BN, MODE, FULL>::kThreads, 1) void gemm_
   const uint32_t tmem = tmem_base;
   wait_for_earlier();  // all of the above is this kernel's own
 
-  // Every wait ends: after the limit the kernel records it and all its roles
-  // stop (they look at gave_up while they wait).
   auto wait = [&](uint32_t bar, uint32_t parity, uint64_t limit = kWaitLimitNs) -> bool {
-    if (mbar_try(bar, parity)) return true;
-    const uint64_t t0 = now_ns();
-    for (;;) {
-      for (int i = 0; i < 16; ++i)
-        if (mbar_try(bar, parity)) return true;
-      if (gave_up) return false;
-      if (now_ns() - t0 > limit) {
-        gave_up = 1;
-        atomicExch(s.status, 1u);
-        return false;
-      }
-    }
+    return limited_wait(bar, parity, limit, &gave_up, s.status);
   };
 
   const int bn = PAIR ? s.bn : BN;

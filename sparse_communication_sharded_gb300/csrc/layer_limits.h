@@ -61,5 +61,25 @@ class RaisedLimits {
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 constexpr uint64_t product_wait_ns(int64_t stages) { return kWaitLimitNs + (uint64_t)stages * 5000u; }
 
+// A device's count of waits given up only grows; who asks for news is told what was
+// added since anyone last asked.  Nothing is cleared on the device, so no report falls
+// between a read and a clear.
+class LastSeen {
+ public:
+  // How many were added since the last call, for a count read as v.  Of two callers
+  // the later read may arrive first; the other then has nothing new.
+  int news(unsigned v) {
+    unsigned seen = seen_.load(std::memory_order_relaxed);
+    for (;;) {
+      const int more = (int)(v - seen);
+      if (more <= 0) return 0;
+      if (seen_.compare_exchange_weak(seen, v, std::memory_order_relaxed)) return more;
+    }
+  }
+
+ private:
+  std::atomic<unsigned> seen_{0};
+};
+
 }  // namespace layer
 }  // namespace scapek

@@ -415,8 +415,12 @@ PyObject* do_linear_backward_weight(Args a) {
 
 // () -> int
 PyObject* do_status(Args) {
-  int v = 0;
-  library(scape_layer_status(&v, c10::cuda::getCurrentCUDAStream().stream()));
+  int v = 0, rc = 0;
+  void* st = c10::cuda::getCurrentCUDAStream().stream();
+  // the stream may have to wait for a host function that needs the interpreter
+  Py_BEGIN_ALLOW_THREADS rc = scape_layer_status(&v, st);
+  Py_END_ALLOW_THREADS
+  library(rc);
   return PyLong_FromLong(v);
 }
 

@@ -149,7 +149,8 @@ def linear_backward_weight(dy, x, activation=None, dweight=None, dbias=None, gra
 
 
 def status() -> int:
-    """Nonzero if a matrix-product kernel on the current device gave up a wait
-    since the last call (its output is then incomplete).  Synchronises the
-    current stream."""
+    """How many waits inside matrix-product kernels on the current device were given
+    up since the last call (0: none): the output of a product that gave up is
+    incomplete, and its call returned without an error.  Synchronises the current
+    stream and answers for the work on it; ask before gradients are used."""
     return _lib().status()

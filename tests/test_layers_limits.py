@@ -1,6 +1,7 @@
 """What the host keeps about kernels between calls (csrc/layer_limits.h, compiled
 here): the record of what CUDA was told they may use, with two host threads in it
-at once and a fake for CUDA's call, and the limits of their waits."""
+at once and a fake for CUDA's call, the limits of their waits, and which waits given
+up have been reported."""
 import os
 import subprocess
 
@@ -81,7 +82,30 @@ int main(int argc, char** argv) {
   static int many[80];
   int full = 0;
   for (int& k : many) full += limits.raise(2, &k, 1, -1, [](int) { return 0; }) == -1;
-  return full == 80 - scapek::layer::RaisedLimits::kKernels ? 0 : 6;
+  if (full != 80 - scapek::layer::RaisedLimits::kKernels) return 6;
+
+  // Waits given up: each is told once, whatever is added while it is asked for.
+  scapek::layer::LastSeen seen;
+  if (seen.news(0) != 0 || seen.news(2) != 2 || seen.news(2) != 0) return 7;
+  // two readers, of whom the one with the older value comes last
+  if (seen.news(5) != 3 || seen.news(4) != 0 || seen.news(5) != 0) return 8;
+  // the count passes 32 bits
+  scapek::layer::LastSeen far;
+  if (far.news(0x7FFFFFFFu) <= 0 || far.news(0xFFFFFFFEu) <= 0 || far.news(3) != 5) return 9;
+  std::atomic<unsigned> count{0};
+  std::atomic<bool> stop{false};
+  std::atomic<long> told_of{0};
+  scapek::layer::LastSeen both;
+  std::thread readers[2];
+  for (std::thread& r : readers)
+    r = std::thread([&] {
+      while (!stop) told_of += both.news(count.load());
+    });
+  for (int i = 0; i < 200000; ++i) ++count;
+  stop = true;
+  for (std::thread& r : readers) r.join();
+  told_of += both.news(count.load());
+  return told_of == 200000 ? 0 : 10;
 }
 """
 
@@ -100,3 +124,13 @@ def program(tmp_path_factory):
 def test_two_threads_raise_one_kernel(program, first, second, early):
     r = subprocess.run([program, str(first), str(second), str(early)], capture_output=True, text=True, timeout=30)
     assert r.returncode == 0, r.stdout
+
+
+def test_probe_refusals():
+    from sparse_communication_sharded_gb300 import _scape as C
+    from sparse_communication_sharded_gb300 import build as B
+    B.build()
+    lib = C.load()
+    for ns in (0, -5, 2 * 10 ** 9 + 1):
+        assert lib.scape_layer_probe_wait(ns, None) == C.SCAPE_EINVAL
+        assert "limit_ns" in lib.scape_layer_last_error().decode()
