@@ -26,6 +26,9 @@ int fail(int code, const char* what) {
 }
 int cuda_result(cudaError_t e, const char* what) {
   if (e == cudaSuccess) return SCAPE_OK;
+  // told here: CUDA's own record of it would fail the next scape_* call, whose
+  // launches are checked by that record
+  (void)cudaGetLastError();
   std::snprintf(g_error, sizeof g_error, "%s: %s", what, cudaGetErrorString(e));
   return SCAPE_ECUDA;
 }
