@@ -101,6 +101,9 @@ def train(workers=4, steps=30, hidden=256, blocks=3, tokens=512, out=64, sparsit
             err = y.float() - torch.tanh(x.float() @ teacher)
             total = total + err.square().mean() / workers
             model.backward(p, (err * (2.0 / err.numel())).bfloat16(), kept, model.views(grads[w]))
+        # a product that gave up a wait has left gradients that nobody may use
+        if L.status():
+            raise RuntimeError("a matrix product did not finish: gradients of this step are incomplete")
         opt.step(grads)
         opt.refresh_mask()
         losses.append(float(total))

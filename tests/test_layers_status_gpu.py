@@ -36,3 +36,24 @@ def test_report_is_not_lost_to_another_stream(cuda_device):
         told += L.status()  # of this stream's work, and what else has been counted
     side.synchronize()
     assert told + L.status() == 8
+
+
+def test_example_does_not_use_incomplete_gradients(cuda_device, monkeypatch):
+    """A wait given up in a step's products ends training before the optimizer reads them."""
+    from tests.test_layers_train_gpu import example
+    steps = []
+    monkeypatch.setattr(example.Scape, "step", lambda self, grads: steps.append(1))
+    monkeypatch.setattr(example.Scape, "refresh_mask", lambda self: None)
+    backward = example.Blocks.backward
+
+    def backward_that_gives_up(*a):
+        r = backward(*a)
+        if len(steps) == 2:
+            probe(1000)
+        return r
+
+    monkeypatch.setattr(example.Blocks, "backward", backward_that_gives_up)
+    L.status()
+    with pytest.raises(RuntimeError, match="incomplete"):
+        example.train(workers=2, steps=5, hidden=64, blocks=1, tokens=32, out=8)
+    assert len(steps) == 2
