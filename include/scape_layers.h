@@ -21,7 +21,9 @@
  *     Calls can be captured into a CUDA graph.
  *   - Matrices are row-major with unit column stride and a row stride (ld*,
  *     in elements, at least the number of columns).  Any alignment and any
- *     stride is accepted; outputs must not overlap inputs unless said.
+ *     stride is accepted.  Outputs that share memory with an input or with each
+ *     other are refused, but where one "may be" an input: the same address and
+ *     stride then.  (Slices of a wider buffer may lie between each other.)
  *     Rows or columns of zero length are valid and do nothing (a weight
  *     gradient of no rows is zero).
  *   - dtype arguments are scape_dtype (SCAPE_F32, SCAPE_BF16).  Sums, norms and

@@ -4,9 +4,11 @@
 #include <atomic>
 #include <cmath>
 #include <cstdio>
+#include <initializer_list>
 
 #include "layer_gemm.cuh"
 #include "layer_limits.h"
+#include "layer_overlap.h"
 
 namespace scapek {
 namespace layer {
@@ -155,6 +157,31 @@ int check_matrix(const void* p, int64_t ld, int64_t cols, int dtype, const char*
   return SCAPE_OK;
 }
 
+size_t elem_size(int dtype) { return dtype == SCAPE_BF16 ? 2 : 4; }
+Span matrix_span(const void* p, int64_t ld, int64_t rows, int64_t cols, size_t elem) {
+  return Span(p, ld * (int64_t)elem, cols * (int64_t)elem, rows);
+}
+Span vector_span(const void* p, int64_t n, size_t elem) { return Span(p, n * (int64_t)elem, n * (int64_t)elem, 1); }
+Span scale_span(const void* p, int64_t rows, int64_t cols) { return vector_span(p, rows * ceil_div(cols, kBlock), 1); }
+
+// An input, and whether the call's first output may take its place.
+struct Input {
+  Span s;
+  bool may_be_first = false;
+};
+// No output shares memory with an input or another output, but where the header
+// says that one may be the other.
+int check_apart(std::initializer_list<Span> outs, std::initializer_list<Input> ins) {
+  for (const Span* o = outs.begin(); o != outs.end(); ++o) {
+    for (const Input& i : ins)
+      if (overlap(*o, i.s) && !(i.may_be_first && o == outs.begin() && o->same(i.s)))
+        return fail(SCAPE_EINVAL, "an output overlaps an input");
+    for (const Span* p = outs.begin(); p != o; ++p)
+      if (overlap(*o, *p)) return fail(SCAPE_EINVAL, "two outputs overlap");
+  }
+  return SCAPE_OK;
+}
+
 }  // namespace
 
 cudaError_t gemm_status_word(unsigned int** word) {
@@ -270,6 +297,9 @@ extern "C" int scape_layer_pack8(const void* x, int64_t ldx, int dtype, int64_t 
   if (rows == 0 || cols == 0) return SCAPE_OK;
   int rc = check_matrix(x, ldx, cols, dtype, "x is NULL or misaligned");
   if (!rc) rc = check_packed(q, ldq, scale, cols);
+  if (!rc)
+    rc = check_apart({matrix_span(q, ldq, rows, cols, 1), scale_span(scale, rows, cols)},
+                     {{matrix_span(x, ldx, rows, cols, elem_size(dtype))}});
   if (rc) return rc;
   return cuda_result(launch_pack8(x, ldx, dtype, rows, cols, q, ldq, scale,
                                   static_cast<cudaStream_t>(stream)),
@@ -285,6 +315,9 @@ extern "C" int scape_layer_unpack8(const uint8_t* q, int64_t ldq, const uint8_t*
   if (rows == 0 || cols == 0) return SCAPE_OK;
   int rc = check_packed(q, ldq, scale, cols);
   if (!rc) rc = check_matrix(y, ldy, cols, dtype, "y is NULL or misaligned");
+  if (!rc)
+    rc = check_apart({matrix_span(y, ldy, rows, cols, elem_size(dtype))},
+                     {{matrix_span(q, ldq, rows, cols, 1)}, {scale_span(scale, rows, cols)}});
   if (rc) return rc;
   return cuda_result(launch_unpack8(q, ldq, scale, rows, cols, activation, y, ldy, dtype,
                                     static_cast<cudaStream_t>(stream)),
@@ -302,6 +335,11 @@ extern "C" int scape_layer_act_grad(const void* dy, int64_t lddy, const uint8_t*
   int rc = check_matrix(dy, lddy, cols, dtype, "dy is NULL or misaligned");
   if (!rc) rc = check_packed(q, ldq, scale, cols);
   if (!rc) rc = check_matrix(dz, lddz, cols, dtype, "dz is NULL or misaligned");
+  if (!rc)
+    rc = check_apart({matrix_span(dz, lddz, rows, cols, elem_size(dtype))},
+                     {{matrix_span(dy, lddy, rows, cols, elem_size(dtype)), true},
+                      {matrix_span(q, ldq, rows, cols, 1)},
+                      {scale_span(scale, rows, cols)}});
   if (rc) return rc;
   return cuda_result(launch_act_grad(dy, lddy, q, ldq, scale, rows, cols, activation, dz, lddz,
                                      dtype, static_cast<cudaStream_t>(stream)),
@@ -324,6 +362,14 @@ extern "C" int scape_layer_add_rmsnorm(const void* x, int64_t ldx, const void* r
   if (!rc && !elem_ok(weight, weight_dtype)) rc = fail(SCAPE_EINVAL, "weight is NULL or misaligned");
   if (!rc && rstd && !aligned(rstd, 4)) rc = fail(SCAPE_EINVAL, "rstd is misaligned");
   if (!rc && (q || scale)) rc = check_packed(q, ldq, scale, cols);
+  if (!rc) {
+    const size_t e = elem_size(dtype);
+    rc = check_apart({matrix_span(h, ldh, rows, cols, e), matrix_span(y, ldy, rows, cols, e), vector_span(rstd, rows, 4),
+                      matrix_span(q, ldq, rows, cols, 1), scale_span(scale, rows, cols)},
+                     {{matrix_span(x, ldx, rows, cols, e), true},
+                      {matrix_span(residual, ldres, rows, cols, e), true},
+                      {vector_span(weight, cols, elem_size(weight_dtype))}});
+  }
   if (rc) return rc;
   NormFwd a;
   a.x = x, a.res = residual, a.w = weight;
@@ -368,6 +414,16 @@ extern "C" int scape_layer_add_rmsnorm_bwd(const void* dy, int64_t lddy, const v
   size_t need = 0;
   if (!rc && dweight) rc = scape_layer_add_rmsnorm_bwd_workspace(rows, cols, &need);
   if (!rc) rc = check_workspace(workspace, ws_bytes, need);
+  if (!rc) {
+    const size_t e = elem_size(dtype);
+    rc = check_apart({matrix_span(dx, lddx, rows, cols, e), vector_span(dweight, cols, elem_size(dweight_dtype)),
+                      vector_span(workspace, need, 1)},
+                     {{matrix_span(dy, lddy, rows, cols, e), true},
+                      {matrix_span(h, ldh, rows, cols, e)},
+                      {vector_span(weight, cols, elem_size(weight_dtype))},
+                      {vector_span(rstd, rows, 4)},
+                      {matrix_span(dh, lddh, rows, cols, e), true}});
+  }
   if (rc) return rc;
   NormBwd a;
   a.dy = dy, a.h = h, a.w = weight, a.dh = dh;
@@ -407,6 +463,13 @@ extern "C" int scape_layer_linear(const void* x, int64_t ldx, const void* weight
   size_t need = 0;
   if (!rc) rc = scape_layer_linear_workspace(x, ldx, weight, ldw, rows, k, n, &need);
   if (!rc) rc = check_workspace(workspace, ws_bytes, need);
+  if (!rc)
+    rc = check_apart({matrix_span(y, ldy, rows, n, 2), matrix_span(q, ldq, rows, n, 1), scale_span(scale, rows, n),
+                      vector_span(workspace, need, 1)},
+                     {{matrix_span(x, ldx, rows, k, 2)},
+                      {matrix_span(weight, ldw, n, k, 2)},
+                      {vector_span(bias, n, 2)},
+                      {matrix_span(residual, ldres, rows, n, 2), true}});
   if (rc) return rc;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   GemmCall c = {};
@@ -455,6 +518,14 @@ extern "C" int scape_layer_linear_bwd_input(const void* dy, int64_t lddy, const 
   size_t need = 0;
   if (!rc) rc = scape_layer_linear_bwd_input_workspace(dy, lddy, weight, ldw, rows, k, n, &need);
   if (!rc) rc = check_workspace(workspace, ws_bytes, need);
+  if (!rc) {
+    const int64_t pre = activation != SCAPE_ACT_NONE ? rows : 0;
+    rc = check_apart({matrix_span(dx, lddx, rows, k, 2), vector_span(workspace, need, 1)},
+                     {{matrix_span(dy, lddy, rows, n, 2)},
+                      {matrix_span(weight, ldw, n, k, 2)},
+                      {matrix_span(q, ldq, pre, k, 1)},
+                      {scale_span(scale, pre, k)}});
+  }
   if (rc) return rc;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   GemmCall c = {};
@@ -525,6 +596,12 @@ extern "C" int scape_layer_linear_bwd_weight(const void* dy, int64_t lddy, const
   size_t need = 0;
   if (!rc) rc = scape_layer_linear_bwd_weight_workspace(dy, lddy, x, ldx, rows, k, n, &need);
   if (!rc) rc = check_workspace(workspace, ws_bytes, need);
+  if (!rc)
+    rc = check_apart({matrix_span(dweight, lddw, n, k, ge), vector_span(dbias, n, ge), vector_span(workspace, need, 1)},
+                     {{matrix_span(dy, lddy, rows, n, 2)},
+                      {matrix_span(x, ldx, rows, k, 2)},
+                      {matrix_span(q, ldq, rows, k, 1)},
+                      {scale_span(q ? scale : nullptr, rows, k)}});
   if (rc) return rc;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   cudaError_t e = cudaSuccess;

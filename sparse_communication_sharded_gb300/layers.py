@@ -9,8 +9,9 @@ and the current stream, on which all work is enqueued.
 A tensor of any number of dimensions is taken as rows of its last one: its
 last dimension has unit stride and the others collapse to one row stride
 (slices of a wider buffer are fine).  Outputs are new contiguous tensors
-unless given.  ValueError: an argument's type, shape, layout or device;
-ScapeError: what the library refuses.
+unless given, and given ones share no memory with what the call reads unless
+said.  ValueError: an argument's type, shape, layout or device; ScapeError:
+what the library refuses.
 """
 from __future__ import annotations
 
