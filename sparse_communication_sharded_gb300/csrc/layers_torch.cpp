@@ -9,6 +9,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
+#include <ATen/core/grad_mode.h>
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -58,9 +59,21 @@ std::string names(int types) {
   return s;
 }
 
+// A tensor argument.  These operators record nothing for autograd: where it would
+// look for a graph, a result without one would train less than the caller thinks.
 const Tensor& tensor(PyObject* o, const char* name) {
   if (!THPVariable_Check(o)) throw ValueError(std::string(name) + " must be a tensor");
-  return THPVariable_Unpack(o);
+  const Tensor& t = THPVariable_Unpack(o);
+  if (t.requires_grad() && at::GradMode::is_enabled())
+    throw ValueError(std::string(name) +
+                     " requires grad, and layer operators are not recorded by autograd: call them "
+                     "under torch.no_grad() (or in an autograd.Function), or detach it");
+  return t;
+}
+// A tensor that the call has written in place, for autograd's check that saved
+// values are as they were.
+void written(const Tensor& t) {
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
 }
 
 // A tensor seen as the rows of its last dimension.
@@ -165,6 +178,12 @@ Tensor bytes(size_t n, const Tensor& ref) {
 struct Out {
   Tensor t;
   Rows r;
+  bool is_given = false;
+  // the call has filled it
+  PyObject* done() {
+    if (is_given) written(t);
+    return THPVariable_Wrap(std::move(t));
+  }
 };
 Out output(PyObject* o, at::IntArrayRef lead, int64_t cols, at::ScalarType type, const Tensor& ref,
            const char* name) {
@@ -175,6 +194,7 @@ Out output(PyObject* o, at::IntArrayRef lead, int64_t cols, at::ScalarType type,
     out.r.ld = cols;
   } else {
     out.t = tensor(o, name);
+    out.is_given = true;
     if (out.t.scalar_type() != type) throw ValueError(std::string(name) + " has the wrong type");
     out.r = like(out.t, kBf16 | kF32, lead, cols, ref, name);
   }
@@ -237,7 +257,7 @@ PyObject* do_unpack8(Args a) {
   Out out = output(a[3], lead_of(q), p.q.cols, type, q, "out");
   library(scape_layer_unpack8(static_cast<uint8_t*>(p.q.p), p.q.ld, p.scale, p.q.rows, p.q.cols,
                               integer(a[2]), out.r.p, out.r.ld, dtype_of(out.t), stream_of(q)));
-  return wrap(out.t);
+  return out.done();
 }
 
 // (dy, packed, activation, out) -> dz
@@ -249,7 +269,7 @@ PyObject* do_activation_grad(Args a) {
   Out out = output(a[3], lead_of(dy), r.cols, dy.scalar_type(), dy, "out");
   library(scape_layer_act_grad(r.p, r.ld, static_cast<uint8_t*>(p.q.p), p.q.ld, p.scale, r.rows,
                                r.cols, integer(a[2]), out.r.p, out.r.ld, dtype_of(dy), stream_of(dy)));
-  return wrap(out.t);
+  return out.done();
 }
 
 // (x, weight, residual, eps, pack) -> (y, h, rstd, q, scale), h None without a residual
@@ -308,7 +328,8 @@ PyObject* do_add_rmsnorm_backward(Args a) {
   library(scape_layer_add_rmsnorm_bwd(r.p, r.ld, h.p, h.ld, wp, dtype_of(w), rstd.data_ptr<float>(),
                                       dh.p, dh.ld, r.rows, r.cols, dtype_of(dy), out.r.p, out.r.ld,
                                       dw, dwt, n ? ws.data_ptr() : nullptr, n, stream_of(dy)));
-  return wrap(out.t);
+  if (dw) written(tensor(a[5], "dweight"));
+  return out.done();
 }
 
 Rows weight_of(const Tensor& w, const Tensor& ref) {
@@ -340,8 +361,8 @@ PyObject* do_linear(Args a) {
   library(scape_layer_linear(r.p, r.ld, w.p, w.ld, bias, res.p, res.ld, r.rows, r.cols, n,
                              integer(a[4]), out.r.p, out.r.ld, p.qp, n, p.sp,
                              bytes_needed ? ws.data_ptr() : nullptr, bytes_needed, stream_of(x)));
-  if (!keep) return wrap(out.t);
-  return tuple({wrap(out.t), wrap(p.q), wrap(p.scale)});
+  if (!keep) return out.done();
+  return tuple({out.done(), wrap(p.q), wrap(p.scale)});
 }
 
 // (dy, weight, packed or None, activation, out) -> dx
@@ -363,7 +384,7 @@ PyObject* do_linear_backward_input(Args a) {
   library(scape_layer_linear_bwd_input(r.p, r.ld, w.p, w.ld, static_cast<uint8_t*>(p.q.p), p.q.ld,
                                        p.scale, integer(a[3]), r.rows, k, r.cols, out.r.p, out.r.ld,
                                        n ? ws.data_ptr() : nullptr, n, stream_of(dy)));
-  return wrap(out.t);
+  return out.done();
 }
 
 // (dy, x or packed, activation, dweight or None, dbias or None, new one is float32) -> dweight
@@ -375,7 +396,7 @@ PyObject* do_linear_backward_weight(Args a) {
   Packed p = {{nullptr, 0, 0, 0}, nullptr};
   int64_t k;
   if (THPVariable_Check(a[1])) {
-    const Tensor& t = THPVariable_Unpack(a[1]);
+    const Tensor& t = tensor(a[1], "x");
     k = t.dim() ? t.size(-1) : 0;
     x = like(t, kBf16, lead, k, dy, "x");
     p.q.ld = k;
@@ -410,6 +431,8 @@ PyObject* do_linear_backward_weight(Args a) {
                                         p.scale, integer(a[2]), r.rows, k, n, wr.p, wr.ld, db,
                                         dtype_of(dw), need ? ws.data_ptr() : nullptr, need,
                                         stream_of(dy)));
+  if (given(a[3])) written(dw);
+  if (db) written(tensor(a[4], "dbias"));
   return wrap(dw);
 }
 

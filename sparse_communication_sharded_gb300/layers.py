@@ -12,6 +12,11 @@ last dimension has unit stride and the others collapse to one row stride
 unless given, and given ones share no memory with what the call reads unless
 said.  ValueError: an argument's type, shape, layout or device; ScapeError:
 what the library refuses.
+
+Nothing is recorded for autograd: the gradients are operators of their own
+(*_backward).  A tensor that requires grad is refused while autograd records
+(ValueError); under torch.no_grad() or in an autograd.Function it is taken.
+Tensors written in place (out, dweight, dbias) count as modified.
 """
 from __future__ import annotations
 
