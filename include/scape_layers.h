@@ -36,8 +36,13 @@
  * 448), x ~ q 2^(code - 127): code is the smallest value >= 1 for which the
  * block's largest finite magnitude is at most 448 2^(code - 127); q is rounded
  * to nearest even.  Infinities and NaN become NaN and do not affect the rest of
- * their block.  A power-of-two scale makes every q 2^(code - 127) exact in
- * bfloat16.  Scales are uint8, ceil(cols / 32) contiguous bytes a row.
+ * their block.  Scales are uint8, ceil(cols / 32) contiguous bytes a row; codes
+ * written are 1 to 247, and 0 and 255 are not read as powers of two.
+ * A power-of-two scale makes every q 2^(code - 127) exact in bfloat16 and float32
+ * but for the ends of their range.  At code 247 a magnitude of 248 2^120 (3.3e38) on
+ * rounds to q = 256, which stands for 2^128 and is read as infinity; at codes 1 and
+ * 2 the least values, odd multiples of 2^-135 and 2^-134, are read in bfloat16 as
+ * the nearest multiple of 2^-133, its smallest step.
  */
 #ifndef SCAPE_LAYERS_H
 #define SCAPE_LAYERS_H

@@ -92,7 +92,9 @@ def pack8(x: torch.Tensor) -> Packed8:
 
 def unpack8(p: Packed8, dtype=torch.bfloat16, activation=None, out=None) -> torch.Tensor:
     """The values of p, through an activation (None, "relu", "gelu" in its tanh
-    form, or "silu").  Without one the result is exact in either dtype."""
+    form, or "silu").  Without one the result is exact in either dtype, up to
+    3.3e38 (a magnitude packed from above that is read as infinity) and, in
+    bfloat16, down to its smallest step 2^-133."""
     if dtype is not torch.bfloat16 and dtype is not torch.float32:
         raise ValueError("dtype must be torch.float32 or torch.bfloat16")
     return _lib().unpack8(p, dtype is torch.bfloat16, _activation(activation), out)
