@@ -543,14 +543,23 @@ extern "C" int scape_layer_linear_bwd_input(const void* dy, int64_t lddy, const 
   return cuda_result(e, "scape_layer_linear_bwd_input");
 }
 
-// Whether the bias sums go into the launch that unpacks the input: both read
-// memory, and neither fills the GPU to its end (8192 x 4096 against 1024 columns
-// of dy: 69.3 us with the product, in a launch of their own 72.2; 4096 x 1280
-// against 3584: 36.1, 41.1; 64 x 256 against 256: 6.4, 8.2).  Where the sums are
-// the longer part, a launch of their own has more of them in flight (65536 x 256
-// against 1024: 105 us, 98 so; 32768 x 64 against 512: 35.1, 31.1).
+// Whether the bias sums go into the launch that unpacks the input.  That spares a
+// launch (us with them there / in one of their own; dy n wide, the input k):
+//   64 x 256, n 256   6.4 / 8.0      4096 x 1280, n 3584   36.1 / 41.1
+//   2048 x 1024, n 4096   20.4 / 25.8     8192 x 4096, n 4096   189 / 194
+// But a block of the sums takes an eighth of the rows, however little else there is
+// to do, and of the blocks beside the unpacking fewer are in flight.  Where the bytes
+// of a row, 3 k + 2 n, are few that is the longer part, the more so the more rows:
+//   rows            12000        16384        24576        65536        131072
+//   k 64, n 64    17.2 / 17.4  20.5 / 19.9  25.9 / 24.6     -          98 / 89
+//   k 256, n 256  19.7 / 20.1  22.8 / 23.6  29.4 / 29.7  64.3 / 58.8   134 / 115
+//   k 64, n 1024  20.4 / 21.2  23.5 / 23.9  33.0 / 30.0  77.6 / 70.0   141 / 123
+//   k 256, n 1024 24.6 / 26.1  31.1 / 31.2  42.5 / 42.0  107 / 98      195 / 182
+// while rows of 3200 bytes and more hide it at any length:
+//   k 1024, n 64  24.4 / 27.5  29.8 / 33.5  40.8 / 45.7     -          205 / 214
+//   k 256, n 2048 33.8 / 35.9  44.4 / 48.5  64.2 / 68.9     -          316 / 345
 static bool sums_beside(const void* dy, int64_t lddy, int64_t rows, int64_t k, int64_t n) {
-  return rows16(dy, lddy, 2) && (rows <= 16384 || k >= n);
+  return rows16(dy, lddy, 2) && (rows <= 12288 || 3 * k + 2 * n >= 3200);
 }
 
 extern "C" int scape_layer_linear_bwd_weight_workspace(const void* dy, int64_t lddy, const void* x,
