@@ -1,5 +1,6 @@
-// layer_skinny.cu -- the linear layer and its gradients for a few rows, where the matrix is read (or the gradient written) once and
-// nothing else is in the way: bound by memory and, at these sizes, by latency.
+// layer_skinny.cu -- the linear layer and its gradients for a few rows, where the
+// matrix is read (or the gradient written) once and nothing else is in the way:
+// bound by memory and, at these sizes, by latency.
 //
 // The tensor cores would multiply a tile of 128 rows for them and cost a launch's
 // set-up (tensor maps, barriers, tensor memory); here a thread multiplies what it
@@ -360,57 +361,69 @@ int cuts(int64_t clusters, int64_t contraction, int64_t least) {
   while (s < 8 && clusters * s * 2 <= 2 * sm_count() && contraction / (s * 2) >= least) s *= 2;
   return s;
 }
-#define SCAPE_ROWS_SWITCH(rows, vec, MOST, CALL)        \
-  if (vec) {                                            \
-    constexpr int VEC = 8;                              \
-    if (rows == 1) { constexpr int R = 1; CALL; }       \
-    else if (rows <= 4) { constexpr int R = 4; CALL; }  \
-    else { constexpr int R = MOST; CALL; }              \
-  } else {                                              \
-    constexpr int VEC = 1;                              \
-    if (rows == 1) { constexpr int R = 1; CALL; }       \
-    else if (rows <= 4) { constexpr int R = 4; CALL; }  \
-    else { constexpr int R = MOST; CALL; }              \
+// CALL with the rows' bound R (1 or 4) and columns a thread as constants.
+#define SCAPE_ROWS_SWITCH(rows, vec, CALL)             \
+  if (vec) {                                           \
+    constexpr int VEC = 8;                             \
+    if (rows == 1) { constexpr int R = 1; CALL; }      \
+    else { constexpr int R = 4; CALL; }                \
+  } else {                                             \
+    constexpr int VEC = 1;                             \
+    if (rows == 1) { constexpr int R = 1; CALL; }      \
+    else { constexpr int R = 4; CALL; }                \
   }
+
+template <int R, int VEC>
+cudaError_t run_forward(const GemmCall& c, int64_t clusters, int s, cudaStream_t st) {
+  return launch_kernel(skinny_forward_kernel<R, VEC>, (unsigned)(clusters * s), kThreads, 0, s, st, c.a.p, c.a.ld,
+                       c.b.p, c.b.ld, (int)c.m, c.k, c.n, c.e);
+}
+template <int R, int VEC>
+cudaError_t run_input_grad(const GemmCall& c, int64_t clusters, int s, cudaStream_t st) {
+  return launch_kernel(skinny_input_grad_kernel<R, VEC>, (unsigned)(clusters * s), kThreads, 0, s, st, c.a.p, c.a.ld,
+                       c.b.p, c.b.ld, (int)c.m, c.n, c.k, c.e);
+}
+template <int R, int VEC, typename T>
+cudaError_t run_weight_grad(const SkinnyWeightGrad& a, cudaStream_t st) {
+  const bool x16 = rows16(a.x, a.ldx, 2), q8 = rows8(a.q, a.ldq);
+  const unsigned grid = (unsigned)(ceil_div(a.k, 256) * ceil_div(a.n, kWarps * kPerWarp));
+  return launch_kernel(skinny_weight_grad_kernel<R, VEC, T>, grid, kThreads, 0, 0, st, a.dy, a.lddy, a.x, a.ldx, a.q,
+                       a.ldq, a.scale, x16, q8, a.act, (int)a.rows, a.k, a.n, static_cast<T*>(a.dw), a.lddw,
+                       static_cast<T*>(a.db));
+}
+template <typename T>
+cudaError_t weight_grad_of(const SkinnyWeightGrad& a, cudaStream_t st) {
+  const bool vec = rows16(a.dw, a.lddw, sizeof(T));
+  if (a.rows > 4) return vec ? run_weight_grad<kSkinnyWeightRows, 8, T>(a, st) : run_weight_grad<kSkinnyWeightRows, 1, T>(a, st);
+  cudaError_t e = cudaSuccess;
+  SCAPE_ROWS_SWITCH(a.rows, vec, e = (run_weight_grad<R, VEC, T>(a, st)));
+  return e;
+}
+static_assert(kSkinnyRows == 4, "the rows' bounds that the kernels are made for");
 
 }  // namespace
 
+// The weight's rows alone decide how it is read: x comes value by value into shared
+// memory, dy too (one row at an odd address through 4096 x 4096: 7.5 us, and 28.6
+// when its alignment counted).
 cudaError_t skinny_forward(const GemmCall& c, cudaStream_t st) {
-  const bool vec = rows16(c.a.p, c.a.ld, 2) && rows16(c.b.p, c.b.ld, 2);
-  const int rows = (int)c.m;
+  const bool vec = rows16(c.b.p, c.b.ld, 2);
   const int64_t clusters = ceil_div(c.n, kCols);
   const int s = cuts(clusters, c.k, 512);
   cudaError_t e = cudaSuccess;
-  SCAPE_ROWS_SWITCH(rows, vec, kSkinnyRows, e = (launch_kernel(skinny_forward_kernel<R, VEC>, (unsigned)(clusters * s), kThreads, 0, s, st, c.a.p, c.a.ld,
-                                           c.b.p, c.b.ld, rows, c.k, c.n, c.e)));
+  SCAPE_ROWS_SWITCH(c.m, vec, e = (run_forward<R, VEC>(c, clusters, s, st)));
   return e;
 }
 cudaError_t skinny_input_grad(const GemmCall& c, cudaStream_t st) {
   const bool vec = rows16(c.b.p, c.b.ld, 2);
-  const int rows = (int)c.m;
   const int64_t clusters = ceil_div(c.n, kGradCols);
   const int s = cuts(clusters, c.k, 128);
   cudaError_t e = cudaSuccess;
-  SCAPE_ROWS_SWITCH(rows, vec, kSkinnyRows, e = (launch_kernel(skinny_input_grad_kernel<R, VEC>, (unsigned)(clusters * s), kThreads, 0, s, st, c.a.p,
-                                           c.a.ld, c.b.p, c.b.ld, rows, c.n, c.k, c.e)));
+  SCAPE_ROWS_SWITCH(c.m, vec, e = (run_input_grad<R, VEC>(c, clusters, s, st)));
   return e;
 }
 cudaError_t skinny_weight_grad(const SkinnyWeightGrad& a, cudaStream_t st) {
-  const size_t ge = a.out_f32 ? 4 : 2;
-  const bool vec = rows16(a.dw, a.lddw, ge), x16 = rows16(a.x, a.ldx, 2), q8 = rows8(a.q, a.ldq);
-  const int rows = (int)a.rows;
-  const unsigned grid = (unsigned)(ceil_div(a.k, 256) * ceil_div(a.n, kWarps * kPerWarp));
-  cudaError_t e = cudaSuccess;
-  if (a.out_f32) {
-    SCAPE_ROWS_SWITCH(rows, vec, kSkinnyWeightRows, e = (launch_kernel(skinny_weight_grad_kernel<R, VEC, float>, grid, kThreads, 0, 0, st,
-                                     a.dy, a.lddy, a.x, a.ldx, a.q, a.ldq, a.scale, x16, q8, a.act, rows, a.k, a.n,
-                                     static_cast<float*>(a.dw), a.lddw, static_cast<float*>(a.db))));
-  } else {
-    SCAPE_ROWS_SWITCH(rows, vec, kSkinnyWeightRows, e = (launch_kernel(skinny_weight_grad_kernel<R, VEC, bf16>, grid, kThreads, 0, 0, st,
-                                     a.dy, a.lddy, a.x, a.ldx, a.q, a.ldq, a.scale, x16, q8, a.act, rows, a.k, a.n,
-                                     static_cast<bf16*>(a.dw), a.lddw, static_cast<bf16*>(a.db))));
-  }
-  return e;
+  return a.out_f32 ? weight_grad_of<float>(a, st) : weight_grad_of<bf16>(a, st);
 }
 
 }  // namespace layer
