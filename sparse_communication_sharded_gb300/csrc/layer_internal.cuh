@@ -486,23 +486,28 @@ struct Slope : Activation<ACT> {
 // bfloat16 result shows it, a 32-bit one does.  So e's roundings and its
 // constants' low parts are carried along as d, and 2^e corrected by 1 + d ln 2.
 template <int ACT>
+__device__ __forceinline__ float exp_exact(float z) {
+  constexpr double k0 = ACT == SCAPE_ACT_GELU ? kGeluK0 : -kLog2e;
+  float t = high(k0), t_low = low(k0);
+  if constexpr (ACT == SCAPE_ACT_GELU) {
+    // the product's error and the sum's (either term may be the larger: Knuth, The
+    // Art of Computer Programming 2, 4.2.2), not contracted into one rounding
+    const float z2 = z * z, a = __fmul_rn(z2, high(kGeluK1));
+    t = __fadd_rn(a, high(k0));
+    const float b = __fsub_rn(t, a);
+    const float sum_low = __fadd_rn(__fsub_rn(a, __fsub_rn(t, b)), __fsub_rn(high(k0), b));
+    t_low = fmaf(z2, low(kGeluK1), low(k0)) + (fmaf(z2, high(kGeluK1), -a) + sum_low);
+  }
+  const float e = z * t;
+  const float d = fmaf(z, t_low, fmaf(z, t, -e));
+  const float x = exp2_fast(e);
+  // where e or z^2 has overflowed d says nothing, and 2^e is 0 or infinite
+  return x > 1e-37f && x < 1e37f ? fmaf(x, d * 0.69314718f, x) : x;
+}
+template <int ACT>
 __device__ __forceinline__ float act_exact(float z) {
   if constexpr (ACT == SCAPE_ACT_RELU) return above_zero(z);
-  if constexpr (ACT == SCAPE_ACT_GELU || ACT == SCAPE_ACT_SILU) {
-    constexpr double k0 = ACT == SCAPE_ACT_GELU ? kGeluK0 : -kLog2e;
-    float t = high(k0), t_low = low(k0);
-    if constexpr (ACT == SCAPE_ACT_GELU) {
-      const float z2 = z * z;
-      t = fmaf(z2, high(kGeluK1), high(k0));
-      t_low = fmaf(z2, low(kGeluK1), low(k0) + fmaf(z2, high(kGeluK1), high(k0) - t));
-    }
-    const float e = z * t;
-    const float d = fmaf(z, t_low, fmaf(z, t, -e));
-    float x = exp2_fast(e);
-    // where e or z^2 has overflowed d says nothing, and 2^e is 0 or infinite
-    if (x > 1e-37f && x < 1e37f) x = fmaf(x, d * 0.69314718f, x);
-    return z * reciprocal_fast(1.0f + x);
-  }
+  if constexpr (ACT == SCAPE_ACT_GELU || ACT == SCAPE_ACT_SILU) return z * reciprocal_fast(1.0f + exp_exact<ACT>(z));
   return z;
 }
 
