@@ -192,21 +192,35 @@ __global__ __launch_bounds__(kThreads) void act_grad_kernel(
   }
 #pragma unroll
   for (int i = 0; i < U; ++i) {
-    const Slope<ACT> f(scale_value(p[i].code));
     float g[VEC];
     to_floats(raw[i], g);
-    if constexpr (VEC == 1) {
-      uint64_t lo, hi;
-      e4m3_pairs(p[i].w[0], lo, hi);
-      float other;
-      unpair(mul2(f.slope(lo), pair(g[0], 0.0f)), g[0], other);
-    } else {
+    if constexpr (sizeof(T) == 4 && Slope<ACT>::kLogistic) {
+      const float scale = scale_value(p[i].code);
 #pragma unroll
-      for (int j = 0; j < VEC / 4; ++j) {
+      for (int j = 0; j < (VEC < 4 ? 1 : VEC / 4); ++j) {
         uint64_t lo, hi;
         e4m3_pairs(p[i].w[j], lo, hi);
-        unpair(mul2(f.slope(lo), pair(g[4 * j], g[4 * j + 1])), g[4 * j], g[4 * j + 1]);
-        unpair(mul2(f.slope(hi), pair(g[4 * j + 2], g[4 * j + 3])), g[4 * j + 2], g[4 * j + 3]);
+        float q[4];
+        unpair(lo, q[0], q[1]);
+        unpair(hi, q[2], q[3]);
+#pragma unroll
+        for (int l = 0; l < (VEC < 4 ? VEC : 4); ++l) g[4 * j + l] *= slope_exact<ACT>(q[l] * scale);
+      }
+    } else {
+      const Slope<ACT> f(scale_value(p[i].code));
+      if constexpr (VEC == 1) {
+        uint64_t lo, hi;
+        e4m3_pairs(p[i].w[0], lo, hi);
+        float other;
+        unpair(mul2(f.slope(lo), pair(g[0], 0.0f)), g[0], other);
+      } else {
+#pragma unroll
+        for (int j = 0; j < VEC / 4; ++j) {
+          uint64_t lo, hi;
+          e4m3_pairs(p[i].w[j], lo, hi);
+          unpair(mul2(f.slope(lo), pair(g[4 * j], g[4 * j + 1])), g[4 * j], g[4 * j + 1]);
+          unpair(mul2(f.slope(hi), pair(g[4 * j + 2], g[4 * j + 3])), g[4 * j + 2], g[4 * j + 3]);
+        }
       }
     }
     store_part<VEC>(dz + un[i].row * lddz + un[i].col, un[i].n, g);

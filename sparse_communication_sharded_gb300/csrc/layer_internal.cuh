@@ -510,6 +510,17 @@ __device__ __forceinline__ float act_exact(float z) {
   if constexpr (ACT == SCAPE_ACT_GELU || ACT == SCAPE_ACT_SILU) return z * reciprocal_fast(1.0f + exp_exact<ACT>(z));
   return z;
 }
+// p + z a'(z) p (1 - p), whose 1 - p is 2^e p: a difference would have no digits
+// where p is near 1.  Past |z| = 1024 the second term is 0 (limited there, it does
+// not overflow); 2^e is limited where p is 0.
+template <int ACT>
+__device__ __forceinline__ float slope_exact(float z) {
+  static_assert(ACT == SCAPE_ACT_GELU || ACT == SCAPE_ACT_SILU, "the others' slopes need no arithmetic");
+  const float x = exp_exact<ACT>(z), p = reciprocal_fast(1.0f + x);
+  const float l = fminf(fmaxf(z, -1024.0f), 1024.0f);
+  const float g = ACT == SCAPE_ACT_GELU ? l * fmaf(l * l, high(3.0 * kGelu2C * kGeluA), high(kGelu2C)) : l;
+  return fmaf(g * p, fminf(x, 1e37f) * p, p);
+}
 
 // CALL with ACT a constant, for an activation known at run time.
 #define SCAPE_ACT_SWITCH(act, CALL)                              \
