@@ -168,12 +168,13 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, i
 __device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 __device__ __forceinline__ void tma_store(const CUtensorMap* map, int x, int y, uint32_t src) {
   asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
                    map),
                "r"(x), "r"(y), "r"(src)
                : "memory");
-  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+  bulk_commit();
 }
 // At most N of this thread's stores still read shared memory.
 template <int N>
@@ -611,8 +612,10 @@ __device__ __forceinline__ void store_box_rows(uint32_t box, int lane, char* out
 
 // A warp's 32 x 32 values, one row a lane, through shared memory: 64-byte rows
 // whose 16-byte quarters are swizzled as the output's tensor map has them, so
-// neither side meets a bank twice.  Aligned outputs leave as one bulk copy
-// (which cuts what is past the matrix), others row by row.
+// neither side meets a bank twice.  Aligned outputs leave as one bulk copy, which
+// cuts what is past the matrix, but of a row in whole pieces of 16 bytes: a last box
+// that ends inside one goes row by row, as outputs of any alignment do, or the copy
+// would write past the row's end into whatever lies beside the output.
 __device__ __forceinline__ void store_box(const float (&v)[32], uint32_t box, int lane,
                                           const CUtensorMap* map, int64_t row0, int c0, int rows,
                                           int left, const Epilogue& e) {
@@ -623,12 +626,14 @@ __device__ __forceinline__ void store_box(const float (&v)[32], uint32_t box, in
                  "r"(bf16_pair(v[8 * j], v[8 * j + 1])), "r"(bf16_pair(v[8 * j + 2], v[8 * j + 3])),
                  "r"(bf16_pair(v[8 * j + 4], v[8 * j + 5])), "r"(bf16_pair(v[8 * j + 6], v[8 * j + 7]))
                  : "memory");
-  if (e.out_vec) {
+  if (e.out_vec && (left >= 32 || left % 8 == 0)) {
     fence_for_bulk();
     __syncwarp();
     if (lane == 0) tma_store(map, c0, (int)row0, box);
   } else {
     __syncwarp();
+    // one group a store, so that groups count boxes
+    if (e.out_vec && lane == 0) bulk_commit();
     char* out = static_cast<char*>(e.out) + (row0 * e.ldo + c0) * 2;
     if (e.out_align == 8)
       store_box_rows<8>(box, lane, out, e.ldo * 2, rows, left);
