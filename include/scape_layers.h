@@ -167,6 +167,26 @@ int scape_layer_linear_bwd_weight(const void *dy, int64_t lddy, const void *x, i
                                   void *dweight, int64_t lddw, void *dbias, int grad_dtype,
                                   void *workspace, size_t ws_bytes, void *stream);
 
+/*
+ * Which kernels the current device runs for a product of these sizes (an answer for
+ * profiling and tests; nothing is launched).  kernel: one of scape_linear_kernel;
+ * columns: of a tile (0: no tiles); cluster: blocks that share a tile's
+ * contraction (0: one each).  keeps_8bit: the forward product also stores z in 8 bits.
+ */
+enum scape_linear_product {
+    SCAPE_LINEAR_FORWARD = 0,
+    SCAPE_LINEAR_INPUT_GRAD = 1,
+    SCAPE_LINEAR_WEIGHT_GRAD = 2
+};
+enum scape_linear_kernel {
+    SCAPE_PLAN_FEW_ROWS = 0,       /* without tensor cores */
+    SCAPE_PLAN_SPLIT = 1,          /* tiles of 128 rows */
+    SCAPE_PLAN_PAIRS = 2,          /* tiles of 256 rows by pairs of blocks */
+    SCAPE_PLAN_PAIRS_AND_SPLIT = 3 /* whole rounds of those, the tiles left over split */
+};
+int scape_layer_linear_plan(int product, int64_t rows, int64_t k, int64_t n, int keeps_8bit,
+                            int *kernel, int *columns, int *cluster);
+
 #ifdef __cplusplus
 }
 #endif

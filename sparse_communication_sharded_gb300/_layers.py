@@ -33,4 +33,5 @@ PROTOS = {
                                                        _vp]),
     "scape_layer_linear_bwd_weight": (_i32, [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _i32, _i64,
                                              _i64, _i64, _vp, _i64, _vp, _i32, _vp, _sz, _vp]),
+    "scape_layer_linear_plan": (_i32, [_i32, _i64, _i64, _i64, _i32, _vp, _vp, _vp]),
 }

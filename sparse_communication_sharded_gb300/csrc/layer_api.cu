@@ -218,6 +218,57 @@ int64_t gemm_clusters(int blocks) {
   return n < 0 ? 0 : n;
 }
 
+// Pairs do the most work a byte read and keep the tensor cores
+// busy through the epilogue; they take whole tiles, so their time goes by the
+// number of tiles the busiest pair gets times a tile's.  A stage of a tile takes
+// 2 clocks a column on the tensor cores, or 18 a kilobyte that comes into the SM
+// (measured: 590 clocks for 32 KB, whatever the width), whichever is more.  The
+// width with the least time is taken, or whole rounds of pairs with a second
+// launch for the tiles left over, or one round of wider tiles (4096 x 1280,
+// contraction 3584: 80 tiles for 76 pairs, 42 us in two rounds, 34.5 with 4 left
+// over, 26.1 as 64 of 320 columns; contraction 1280: 23.0 left over, 13.3 wide;
+// 5120 x 1024, 4096: 37.4, 31.8).  Pairs want at least 3/4 of the SMs at
+// work.  Below that, narrow tiles, each cut over a cluster as far as there are
+// SMs and at least four stages of the contraction for every block.
+GemmPlan gemm_plan(int kind, int64_t m, int64_t n, int64_t k, bool packs) {
+  const int64_t sms = sm_count(), pairs = sms / 2;
+  const int64_t tp = ceil_div(m, 2 * kBM), ksteps = ceil_div(k, kBK);
+  int best = 0, best_split = 0;
+  int64_t least = 0;
+  for (int bn = 256; bn >= 128; bn -= 32) {
+    const int64_t tiles = tp * ceil_div(n, bn);
+    const int64_t kb = 16 + (kind == kGemmForward ? bn / 16 : ceil_div(bn, 128) * 8);
+    const int64_t tile = ksteps * std::max<int64_t>(2 * bn, 18 * kb) + kTileCost;
+    const int64_t cost = ceil_div(tiles, pairs) * tile;
+    if (tiles * 4 >= pairs * 3 && (best == 0 || cost < least)) best = bn, best_split = 0, least = cost;
+    // whole rounds of pairs, and the tiles left over as 128 x 128 ones cut over
+    // clusters, all at one time
+    const int64_t rest = tiles % pairs;
+    if (bn % 128 != 0 || tiles < pairs || rest == 0) continue;
+    const int64_t small = rest * 2 * (bn / 128);
+    int split = 1;
+    while (split < 8 && small <= gemm_clusters(split * 2) && ksteps / (split * 2) >= 4) split *= 2;
+    const int64_t both_cost = tiles / pairs * tile + ceil_div(ksteps, split) * kSmallStage + kSmallLaunch;
+    if (small <= gemm_clusters(split) && both_cost < least) best = bn, best_split = split, least = both_cost;
+  }
+  // One round of tiles of 320 or 384 columns, where that is less.  They are read
+  // out after their products, not beside them, so further rounds would wait, and
+  // a short contraction is better off with two rounds of narrow ones (forward,
+  // 4096 x 1280: 9.9 against 8.9 us at 512).
+  for (int bn = 384; bn > 256; bn -= 64) {
+    const int64_t tiles = tp * ceil_div(n, bn);
+    const int64_t cost = ksteps * std::max<int64_t>(2 * bn, 18 * 40) + kTileCost + (packs ? kWidePackCost : kWideCost);
+    if (tiles <= pairs && tiles * 4 >= pairs * 3 && best && cost < least) best = bn, best_split = 0, least = cost;
+  }
+  if (best) return {best_split ? kPlanPairsAndRest : kPlanPairs, best, best_split};
+  const int64_t tm = ceil_div(m, kBM);
+  const int bn = tm * ceil_div(n, 64) <= sms ? 64 : 128;
+  const int64_t tiles = tm * ceil_div(n, bn);
+  int split = 1;
+  while (split < 8 && tiles <= gemm_clusters(split * 2) && ksteps / (split * 2) >= 4) split *= 2;
+  return {kPlanSplit, bn, split};
+}
+
 cudaError_t allow_smem(const void* kernel, int bytes) {
   static RaisedLimits limits;
   int dev = 0;
@@ -541,6 +592,25 @@ extern "C" int scape_layer_linear_bwd_input(const void* dy, int64_t lddy, const 
   c.e.out_align = row_alignment(dx, lddx * 2);
   if (e == cudaSuccess) e = skinny ? skinny_input_grad(c, st) : gemm_input_grad(c, st);
   return cuda_result(e, "scape_layer_linear_bwd_input");
+}
+
+extern "C" int scape_layer_linear_plan(int product, int64_t rows, int64_t k, int64_t n, int keeps_8bit, int* kernel,
+                                       int* columns, int* cluster) {
+  if (product < SCAPE_LINEAR_FORWARD || product > SCAPE_LINEAR_WEIGHT_GRAD) return fail(SCAPE_EINVAL, "unknown product");
+  if (!kernel || !columns || !cluster) return fail(SCAPE_EINVAL, "kernel, columns and cluster must be given");
+  if (!size_ok(rows) || !size_ok(k) || !size_ok(n) || !rows || !k || !n) return fail(SCAPE_EINVAL, "a size is out of range");
+  *columns = *cluster = 0;
+  if (rows <= (product == SCAPE_LINEAR_WEIGHT_GRAD ? kSkinnyWeightRows : kSkinnyRows)) {
+    *kernel = SCAPE_PLAN_FEW_ROWS;
+    return SCAPE_OK;
+  }
+  const GemmPlan p = product == SCAPE_LINEAR_FORWARD      ? gemm_plan(kGemmForward, rows, n, k, keeps_8bit != 0)
+                     : product == SCAPE_LINEAR_INPUT_GRAD ? gemm_plan(kGemmInputGrad, rows, k, n, false)
+                                                          : gemm_plan(kGemmWeightGrad, n, k, rows, false);
+  *kernel = p.how == kPlanSplit ? SCAPE_PLAN_SPLIT : p.how == kPlanPairs ? SCAPE_PLAN_PAIRS : SCAPE_PLAN_PAIRS_AND_SPLIT;
+  *columns = p.columns;
+  *cluster = p.cluster;
+  return SCAPE_OK;
 }
 
 // Whether the bias sums go into the launch that unpacks the input.  That spares a

@@ -56,6 +56,17 @@ struct GemmCall {
   int64_t m, n, k;
   Epilogue e;
 };
+// How a product is cut: tiles of 128 rows, each cut over a cluster of `cluster`
+// blocks; tiles of 256 rows by pairs of blocks; or whole rounds of those, and the
+// tiles left over in a split launch of 128 x 128 ones.
+enum GemmHow { kPlanSplit, kPlanPairs, kPlanPairsAndRest };
+struct GemmPlan {
+  GemmHow how;
+  int columns;  // of a tile
+  int cluster;  // blocks that share a split tile
+};
+GemmPlan gemm_plan(int kind, int64_t m, int64_t n, int64_t k, bool packs);
+
 cudaError_t gemm_forward(const GemmCall& c, cudaStream_t st);
 cudaError_t gemm_input_grad(const GemmCall& c, cudaStream_t st);
 cudaError_t gemm_weight_grad(const GemmCall& c, cudaStream_t st);
@@ -1116,65 +1127,24 @@ cudaError_t gemm_pairs(const GemmCall& c, int bn, cudaStream_t st, TileRange ran
   return gemm_launch<KIND, 256, kModePair, false>(c, bn, 2, st, range);
 }
 
-// Tile and mode.  Pairs do the most work a byte read and keep the tensor cores
-// busy through the epilogue; they take whole tiles, so their time goes by the
-// number of tiles the busiest pair gets times a tile's.  A stage of a tile takes
-// 2 clocks a column on the tensor cores, or 18 a kilobyte that comes into the SM
-// (measured: 590 clocks for 32 KB, whatever the width), whichever is more.  The
-// width with the least time is taken, or whole rounds of pairs with a second
-// launch for the tiles left over, or one round of wider tiles (4096 x 1280,
-// contraction 3584: 80 tiles for 76 pairs, 42 us in two rounds, 34.5 with 4 left
-// over, 26.1 as 64 of 320 columns; contraction 1280: 23.0 left over, 13.3 wide;
-// 5120 x 1024, 4096: 37.4, 31.8).  Pairs want at least 3/4 of the SMs at
-// work.  Below that, narrow tiles, each cut over a cluster as far as there are
-// SMs and at least four stages of the contraction for every block.
 template <int KIND>
 cudaError_t gemm_run(const GemmCall& c, cudaStream_t st) {
-  const int64_t sms = sm_count(), pairs = sms / 2;
-  const int64_t tp = ceil_div(c.m, 2 * kBM), ksteps = ceil_div(c.k, kBK);
-  int best = 0, best_split = 0;
-  int64_t least = 0;
-  for (int bn = 256; bn >= 128; bn -= 32) {
-    const int64_t tiles = tp * ceil_div(c.n, bn);
-    const int64_t kb = 16 + (KIND == kGemmForward ? bn / 16 : ceil_div(bn, 128) * 8);
-    const int64_t tile = ksteps * std::max<int64_t>(2 * bn, 18 * kb) + kTileCost;
-    const int64_t cost = ceil_div(tiles, pairs) * tile;
-    if (tiles * 4 >= pairs * 3 && (best == 0 || cost < least)) best = bn, best_split = 0, least = cost;
-    // whole rounds of pairs, and the tiles left over as 128 x 128 ones cut over
-    // clusters, all at one time
-    const int64_t rest = tiles % pairs;
-    if (bn % 128 != 0 || tiles < pairs || rest == 0) continue;
-    const int64_t small = rest * 2 * (bn / 128);
-    int split = 1;
-    while (split < 8 && small <= gemm_clusters(split * 2) && ksteps / (split * 2) >= 4) split *= 2;
-    const int64_t both_cost = tiles / pairs * tile + ceil_div(ksteps, split) * kSmallStage + kSmallLaunch;
-    if (small <= gemm_clusters(split) && both_cost < least) best = bn, best_split = split, least = both_cost;
+  const GemmPlan plan = gemm_plan(KIND, c.m, c.n, c.k, c.e.q != nullptr);
+  switch (plan.how) {
+    case kPlanPairs: return gemm_pairs<KIND>(c, plan.columns, st, {});
+    case kPlanPairsAndRest: {
+      const int64_t pairs = sm_count() / 2;
+      const int64_t whole = ceil_div(c.m, 2 * kBM) * ceil_div(c.n, plan.columns) / pairs * pairs;
+      TileRange first, rest;
+      first.count = rest.base = whole;
+      rest.of_bn = plan.columns;
+      const cudaError_t e = gemm_pairs<KIND>(c, plan.columns, st, first);
+      return e != cudaSuccess ? e : gemm_launch<KIND, 128, kModeSplit, true>(c, 128, plan.cluster, st, rest);
+    }
+    default:
+      return plan.columns == 64 ? gemm_launch<KIND, 64, kModeSplit, true>(c, 64, plan.cluster, st)
+                                : gemm_launch<KIND, 128, kModeSplit, true>(c, 128, plan.cluster, st);
   }
-  // One round of tiles of 320 or 384 columns, where that is less.  They are read
-  // out after their products, not beside them, so further rounds would wait, and
-  // a short contraction is better off with two rounds of narrow ones (forward,
-  // 4096 x 1280: 9.9 against 8.9 us at 512).
-  for (int bn = 384; bn > 256; bn -= 64) {
-    const int64_t tiles = tp * ceil_div(c.n, bn);
-    const int64_t cost = ksteps * std::max<int64_t>(2 * bn, 18 * 40) + kTileCost + (c.e.q ? kWidePackCost : kWideCost);
-    if (tiles <= pairs && tiles * 4 >= pairs * 3 && best && cost < least) best = bn, best_split = 0, least = cost;
-  }
-  if (best && best_split) {
-    const int64_t whole = tp * ceil_div(c.n, best) / pairs * pairs;
-    TileRange first, rest;
-    first.count = rest.base = whole;
-    rest.of_bn = best;
-    const cudaError_t e = gemm_pairs<KIND>(c, best, st, first);
-    return e != cudaSuccess ? e : gemm_launch<KIND, 128, kModeSplit, true>(c, 128, best_split, st, rest);
-  }
-  if (best) return gemm_pairs<KIND>(c, best, st, {});
-  const int64_t tm = ceil_div(c.m, kBM);
-  const int bn = tm * ceil_div(c.n, 64) <= sms ? 64 : 128;
-  const int64_t tiles = tm * ceil_div(c.n, bn);
-  int split = 1;
-  while (split < 8 && tiles <= gemm_clusters(split * 2) && ksteps / (split * 2) >= 4) split *= 2;
-  return bn == 64 ? gemm_launch<KIND, 64, kModeSplit, true>(c, 64, split, st)
-                  : gemm_launch<KIND, 128, kModeSplit, true>(c, 128, split, st);
 }
 
 #endif  // __CUDACC__

@@ -134,3 +134,17 @@ def test_probe_refusals():
     for ns in (0, -5, 2 * 10 ** 9 + 1):
         assert lib.scape_layer_probe_wait(ns, None) == C.SCAPE_EINVAL
         assert "limit_ns" in lib.scape_layer_last_error().decode()
+
+
+def test_plan_refusals():
+    import ctypes
+
+    from sparse_communication_sharded_gb300 import _scape as C
+    from sparse_communication_sharded_gb300 import build as B
+    B.build()
+    lib = C.load()
+    a, b, c = (ctypes.byref(ctypes.c_int()) for _ in range(3))
+    assert lib.scape_layer_linear_plan(3, 8, 8, 8, 0, a, b, c) == C.SCAPE_EINVAL
+    assert lib.scape_layer_linear_plan(0, 8, 0, 8, 0, a, b, c) == C.SCAPE_EINVAL
+    assert lib.scape_layer_linear_plan(0, 8, 8, 8, 0, None, b, c) == C.SCAPE_EINVAL
+    assert lib.scape_layer_linear_plan(0, 4, 8, 8, 0, a, b, c) == C.SCAPE_OK  # no tiles
