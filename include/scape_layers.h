@@ -27,7 +27,12 @@
  *     Rows or columns of zero length are valid and do nothing (a weight
  *     gradient of no rows is zero).
  *   - dtype arguments are scape_dtype (SCAPE_F32, SCAPE_BF16).  Sums, norms and
- *     products are held in 32 bits and rounded once, when they are stored.
+ *     products are held in 32 bits and rounded once, when they are stored.  The
+ *     32-bit sums of a product (more than a few rows) are the tensor cores', which
+ *     cut what does not fit instead of rounding it: sums come out too near 0, by
+ *     1e-6 of themselves for a contraction of 1024 and 2e-5 for 65536 (normally
+ *     distributed operands; a chain of rounded 32-bit sums: 3e-7 and 6e-7, to
+ *     either side).  Results of an activation or its slope below 2^-110 may be 0.
  *   - Results do not depend on timing: equal calls give equal bits.
  *
  * 8-bit format.  Each row is cut into blocks of 32 consecutive columns (the

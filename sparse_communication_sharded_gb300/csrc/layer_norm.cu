@@ -625,10 +625,9 @@ cudaError_t launch_colsum(const ColumnSums& a, cudaStream_t st) {
   return launch_kernel(rows16(a.m, a.ld, 2) ? colsum_kernel<false> : colsum_kernel<true>,
                        (unsigned)(ceil_div(a.cols, kSumCols) * blocks), kColsumThreads, 0, blocks, st, a);
 }
-// In clusters of one block where there is little to add up: they start sooner.
 cudaError_t launch_sum_partials(const float* partial, int64_t parts, int64_t cols, void* out,
                                 int out_bf16, cudaStream_t st) {
-  const int blocks = parts <= 128 ? 1 : kPartBlocks;
+  const int blocks = parts <= 128 ? 1 : kPartBlocks;  // as in sum_cluster()
   return launch_kernel(sum_partials_kernel, (unsigned)(ceil_div(cols, 32) * blocks), 32 * kPartWarps, 0, blocks,
                        st, partial, parts, cols, out, out_bf16);
 }

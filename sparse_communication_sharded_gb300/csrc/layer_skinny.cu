@@ -311,6 +311,9 @@ __global__ __launch_bounds__(kThreads) void skinny_weight_grad_kernel(
     }
   }
   if (act != SCAPE_ACT_NONE) {
+    // rounded to bfloat16: the forward product took it so, and the tensor cores'
+    // form of this product, for more rows, has to (its error in the gradient, 2^-9 of
+    // a term at most and as often up as down, is below the result's own rounding)
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       SCAPE_ACT_SWITCH(act, act_values<ACT>(a[r]));
