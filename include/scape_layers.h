@@ -3,7 +3,9 @@
  *
  * A sharded optimizer step reads W workers' gradients; these operators produce
  * them on the same GPU: the residual RMS norm, activation checkpoints in
- * 8 bits, and the linear layer with its gradients.  What the backward pass
+ * 8 bits, and the linear layer with its gradients; at the two ends of a language
+ * model the embedding and the log probabilities of tokens, with theirs; and before
+ * the step the gradients' norm and clipping.  What the backward pass
  * keeps of a layer is 8 bits a value, because the workers' residuals
  * (scape_bind()) take most of the device's memory; weight gradients are written
  * where the caller wants them, e.g. into the flat vector scape_step() reads.
@@ -191,6 +193,104 @@ enum scape_linear_kernel {
 };
 int scape_layer_linear_plan(int product, int64_t rows, int64_t k, int64_t n, int keeps_8bit,
                             int *kernel, int *columns, int *cluster);
+
+/* ---------------------------------------------------------------- tokens
+ * Tokens (and targets) are int32 or int64 (token_bytes 4 or 8).  One below 0 stands
+ * for none; one that is not below vocab is never used as an index, and what is
+ * computed for it is NaN.
+ */
+
+/*
+ * y[i] = scale * weight[tokens[i]], zeros where the token is none.  weight[vocab, cols]
+ * is of weight_dtype, y[count, cols] of dtype.  vocab >= 1.
+ */
+int scape_layer_embedding(const void *tokens, int token_bytes, int64_t count, const void *weight,
+                          int64_t ldw, int weight_dtype, int64_t vocab, int64_t cols, float scale,
+                          void *y, int64_t ldy, int dtype, void *stream);
+
+/*
+ * dweight[v] = scale * sum of dy[i] over the i with tokens[i] = v, in an order fixed
+ * by the tokens alone.  accumulate 0: rows without a token become zeros; else the
+ * sum is added to dweight (in 32 bits, rounded once) and rows without a token are
+ * left alone, for a table that is also the output layer's weight.  Tokens that are
+ * none or out of range contribute nothing.
+ */
+int scape_layer_embedding_bwd_workspace(int64_t count, int64_t vocab, int64_t cols, size_t *bytes);
+int scape_layer_embedding_bwd(const void *dy, int64_t lddy, int dtype, const void *tokens,
+                              int token_bytes, int64_t count, int64_t vocab, int64_t cols,
+                              float scale, int accumulate, void *dweight, int64_t lddw,
+                              int dweight_dtype, void *workspace, size_t ws_bytes, void *stream);
+
+/*
+ * Of logits x[rows, vocab] (dtype), a row at a time:
+ *   lse = log sum_j exp x_j;  logprob = x_target - lse (0 where the target is none);
+ *   entropy = -sum_j p_j log p_j with p_j = exp(x_j - lse);
+ *   the `top` (0 to SCAPE_TOP_MAX, at most vocab) largest logits in falling order,
+ *   of equal ones the lowest column first: their columns and log probabilities.
+ * A logit of -infinity has p = 0 and adds nothing; in a row of nothing else lse is
+ * -infinity, the entropy 0 and every log probability -infinity.  NaN or +infinity in
+ * a row makes its results NaN (NaN is last among the alternatives, whose columns
+ * are still distinct).  entropy, top_logprob and top_token [rows, top] may be NULL
+ * (the last two together).
+ */
+#define SCAPE_TOP_MAX 32
+int scape_layer_token_logprobs(const void *logits, int64_t ldx, int dtype, const void *targets,
+                               int token_bytes, int64_t rows, int64_t vocab, int top,
+                               float *logprob, float *lse, float *entropy, float *top_logprob,
+                               int64_t *top_token, void *stream);
+
+/*
+ * dlogits_j = dlogprob (1[j = target] - p_j) - dentropy p_j (log p_j + entropy), from
+ * what the forward call gave.  dentropy NULL: its term is left out (entropy is then
+ * not read); a row whose target is none is then zeros, whatever its logits.  dlogits
+ * may be logits.
+ */
+int scape_layer_token_logprobs_bwd(const void *logits, int64_t ldx, int dtype, const void *targets,
+                                   int token_bytes, int64_t rows, int64_t vocab, const float *lse,
+                                   const float *dlogprob, const float *entropy,
+                                   const float *dentropy, void *dlogits, int64_t lddx,
+                                   void *stream);
+
+/*
+ * A row's loss and its gradient in one pass over the logits:
+ *   loss = -w logprob;  dlogits_j = w (p_j - 1[j = target]),
+ * w = weight[row], or weight_all for every row where weight is NULL.  Both are 0 where
+ * the target is none, whatever the logits.  dlogits may be logits.
+ */
+int scape_layer_token_loss_workspace(const void *logits, int64_t ldx, int dtype, int64_t rows,
+                                     int64_t vocab, const void *dlogits, int64_t lddx,
+                                     size_t *bytes);
+int scape_layer_token_loss(const void *logits, int64_t ldx, int dtype, const void *targets,
+                           int token_bytes, int64_t rows, int64_t vocab, const float *weight,
+                           float weight_all, float *loss, void *dlogits, int64_t lddx,
+                           void *workspace, size_t ws_bytes, void *stream);
+
+/* ---------------------------------------------------------------- gradients
+ * n tensors of host_numel[i] contiguous elements of host_dtype[i].  The host arrays
+ * are read during the call only.
+ */
+
+/*
+ * norm = sqrt(sum over all tensors of the elements' squares), one float32.  The sum
+ * is held in 64 bits above short 32-bit ones, and squares outside float32's range are
+ * scaled, so it neither overflows nor loses small gradients (a norm past float32's
+ * largest is infinity).  NaN or an infinity among the elements makes it NaN or infinite.
+ */
+int scape_layer_grad_norm_workspace(int n, const int64_t *host_numel, size_t *bytes);
+int scape_layer_grad_norm(int n, const void *const *host_grads, const int64_t *host_numel,
+                          const int *host_dtype, float *norm, void *workspace, size_t ws_bytes,
+                          void *stream);
+
+/*
+ * The norm, and out[i] = grads[i] * min(1, max_norm / (norm + eps)), each of
+ * host_out_dtype[i].  host_out NULL: in place; out[i] may be grads[i] (same type).
+ * max_norm >= 0, eps >= 0.  The factor is used as it comes out: NaN where the norm is
+ * NaN, 0 where it is infinite.
+ */
+int scape_layer_clip_grads(int n, const void *const *host_grads, const int64_t *host_numel,
+                           const int *host_dtype, void *const *host_out,
+                           const int *host_out_dtype, float max_norm, float eps, float *norm,
+                           void *workspace, size_t ws_bytes, void *stream);
 
 #ifdef __cplusplus
 }

@@ -33,5 +33,21 @@ PROTOS = {
                                                        _vp]),
     "scape_layer_linear_bwd_weight": (_i32, [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _i32, _i64,
                                              _i64, _i64, _vp, _i64, _vp, _i32, _vp, _sz, _vp]),
+    "scape_layer_embedding": (_i32, [_vp, _i32, _i64, _vp, _i64, _i32, _i64, _i64, _f32, _vp, _i64,
+                                     _i32, _vp]),
+    "scape_layer_embedding_bwd_workspace": (_i32, [_i64, _i64, _i64, _vp]),
+    "scape_layer_embedding_bwd": (_i32, [_vp, _i64, _i32, _vp, _i32, _i64, _i64, _i64, _f32, _i32,
+                                         _vp, _i64, _i32, _vp, _sz, _vp]),
+    "scape_layer_token_logprobs": (_i32, [_vp, _i64, _i32, _vp, _i32, _i64, _i64, _i32, _vp, _vp,
+                                          _vp, _vp, _vp, _vp]),
+    "scape_layer_token_logprobs_bwd": (_i32, [_vp, _i64, _i32, _vp, _i32, _i64, _i64, _vp, _vp, _vp,
+                                              _vp, _vp, _i64, _vp]),
+    "scape_layer_token_loss_workspace": (_i32, [_vp, _i64, _i32, _i64, _i64, _vp, _i64, _vp]),
+    "scape_layer_token_loss": (_i32, [_vp, _i64, _i32, _vp, _i32, _i64, _i64, _vp, _f32, _vp, _vp,
+                                      _i64, _vp, _sz, _vp]),
+    "scape_layer_grad_norm_workspace": (_i32, [_i32, _vp, _vp]),
+    "scape_layer_grad_norm": (_i32, [_i32, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "scape_layer_clip_grads": (_i32, [_i32, _vp, _vp, _vp, _vp, _vp, _f32, _f32, _vp, _vp, _sz,
+                                      _vp]),
     "scape_layer_linear_plan": (_i32, [_i32, _i64, _i64, _i64, _i32, _vp, _vp, _vp]),
 }

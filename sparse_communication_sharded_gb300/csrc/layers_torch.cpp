@@ -17,6 +17,7 @@
 
 #include <exception>
 #include <string>
+#include <vector>
 
 #include "scape_layers.h"
 
@@ -436,6 +437,245 @@ PyObject* do_linear_backward_weight(Args a) {
   return wrap(dw);
 }
 
+// ------------------------------------------------------------------ tokens
+// Tokens or targets: contiguous, int64 or int32.
+struct Ids {
+  const void* p;
+  int bytes;
+};
+Ids ids_of(const Tensor& t, at::IntArrayRef shape, const Tensor& ref, const char* name) {
+  on_device(t, ref, name);
+  if (t.scalar_type() != at::kLong && t.scalar_type() != at::kInt)
+    throw ValueError(std::string(name) + " must be of type int64 or int32");
+  if (t.sizes() != shape) throw ValueError(std::string(name) + " has another shape than the call's other tensors say");
+  if (!t.is_contiguous()) throw ValueError(std::string(name) + " must be contiguous");
+  return {t.data_ptr(), t.scalar_type() == at::kLong ? 8 : 4};
+}
+// One float32 a row.
+float* floats_of(const Tensor& t, at::IntArrayRef shape, const Tensor& ref, const char* name) {
+  on_device(t, ref, name);
+  if (t.scalar_type() != at::kFloat || t.sizes() != shape || !t.is_contiguous())
+    throw ValueError(std::string(name) + " must be contiguous float32, one a row");
+  return t.data_ptr<float>();
+}
+Tensor row_floats(at::IntArrayRef lead, const Tensor& ref) {
+  return at::detail::empty_cuda(lead, at::kFloat, ref.device(), std::nullopt);
+}
+double number(PyObject* o) {
+  const double v = PyFloat_AsDouble(o);
+  if (v == -1.0 && PyErr_Occurred()) {
+    PyErr_Clear();
+    throw ValueError("scale, weight, max_norm and eps must be numbers");
+  }
+  return v;
+}
+bool truth(PyObject* o) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) {
+    PyErr_Clear();
+    throw ValueError("entropy and accumulate must be true or false");
+  }
+  return v != 0;
+}
+
+Rows table_of(const Tensor& t, const char* name) {
+  if (t.dim() != 2) throw ValueError(std::string(name) + " must be a matrix");
+  if (t.size(0) == 0) throw ValueError(std::string(name) + " has no rows");
+  return rows_of(t, kBf16 | kF32, name);
+}
+
+// (tokens, weight, scale, 0 or 1: bfloat16 or 2: float32, out) -> y
+PyObject* do_embedding(Args a) {
+  const Tensor& tokens = tensor(a[0], "tokens");
+  const Tensor& w = tensor(a[1], "weight");
+  const Rows t = table_of(w, "weight");
+  const Ids ids = ids_of(tokens, tokens.sizes(), w, "tokens");
+  const double scale = number(a[2]);
+  const int kind = integer(a[3]);
+  c10::cuda::CUDAGuard guard(w.device());
+  at::ScalarType type = kind == 0 ? w.scalar_type() : kind == 1 ? at::kBFloat16 : at::kFloat;
+  if (kind == 0 && given(a[4])) {
+    const Tensor& o = tensor(a[4], "out");
+    if (type_of(o) & (kBf16 | kF32)) type = o.scalar_type();
+  }
+  Out out = output(a[4], tokens.sizes(), t.cols, type, w, "out");
+  library(scape_layer_embedding(ids.p, ids.bytes, tokens.numel(), t.p, t.ld, dtype_of(w), t.rows, t.cols,
+                                (float)scale, out.r.p, out.r.ld, dtype_of(out.t), stream_of(w)));
+  return out.done();
+}
+
+// (dy, tokens, dweight, scale, accumulate) -> dweight
+PyObject* do_embedding_backward(Args a) {
+  const Tensor& dy = tensor(a[0], "dy");
+  const Rows r = rows_of(dy, kBf16 | kF32, "dy");
+  const Ids ids = ids_of(tensor(a[1], "tokens"), lead_of(dy), dy, "tokens");
+  const Tensor& dw = tensor(a[2], "dweight");
+  on_device(dw, dy, "dweight");
+  const Rows w = table_of(dw, "dweight");
+  if (w.cols != r.cols) throw ValueError("dweight and dy differ in their columns");
+  const double scale = number(a[3]);
+  const bool accumulate = truth(a[4]);
+  c10::cuda::CUDAGuard guard(dy.device());
+  size_t n = 0;
+  library(scape_layer_embedding_bwd_workspace(r.rows, w.rows, r.cols, &n));
+  Tensor ws;
+  if (n) ws = bytes(n, dy);
+  library(scape_layer_embedding_bwd(r.p, r.ld, dtype_of(dy), ids.p, ids.bytes, r.rows, w.rows, r.cols, (float)scale,
+                                    accumulate, w.p, w.ld, dtype_of(dw), n ? ws.data_ptr() : nullptr, n,
+                                    stream_of(dy)));
+  written(dw);
+  return wrap(dw);
+}
+
+// (logits, targets, entropy, top) -> (logprob, lse, entropy, top_logprob, top_token)
+PyObject* do_token_logprobs(Args a) {
+  const Tensor& x = tensor(a[0], "logits");
+  const Rows r = rows_of(x, kBf16 | kF32, "logits");
+  const auto lead = lead_of(x);
+  const Ids ids = ids_of(tensor(a[1], "targets"), lead, x, "targets");
+  const bool entropy = truth(a[2]);
+  const long top = PyLong_AsLong(a[3]);
+  if (top == -1 && PyErr_Occurred()) return nullptr;
+  if (top < 0 || top > SCAPE_TOP_MAX || top > r.cols)
+    throw ValueError("top must be 0 to 32, and at most the logits' columns");
+  c10::cuda::CUDAGuard guard(x.device());
+  Tensor lp = row_floats(lead, x), lse = row_floats(lead, x), ent, tops, token;
+  if (entropy) ent = row_floats(lead, x);
+  if (top) {
+    tops = empty(lead, top, at::kFloat, x);
+    token = empty(lead, top, at::kLong, x);
+  }
+  library(scape_layer_token_logprobs(r.p, r.ld, dtype_of(x), ids.p, ids.bytes, r.rows, r.cols, (int)top,
+                                     lp.data_ptr<float>(), lse.data_ptr<float>(),
+                                     entropy ? ent.data_ptr<float>() : nullptr, top ? tops.data_ptr<float>() : nullptr,
+                                     top ? token.data_ptr<int64_t>() : nullptr, stream_of(x)));
+  return tuple({wrap(lp), wrap(lse), entropy ? wrap(ent) : none(), top ? wrap(tops) : none(),
+                top ? wrap(token) : none()});
+}
+
+// (logits, targets, lse, dlogprob, entropy or None, dentropy or None, out) -> dlogits
+PyObject* do_token_logprobs_backward(Args a) {
+  const Tensor& x = tensor(a[0], "logits");
+  const Rows r = rows_of(x, kBf16 | kF32, "logits");
+  const auto lead = lead_of(x);
+  const Ids ids = ids_of(tensor(a[1], "targets"), lead, x, "targets");
+  const float* lse = floats_of(tensor(a[2], "lse"), lead, x, "lse");
+  const float* dlp = floats_of(tensor(a[3], "dlogprob"), lead, x, "dlogprob");
+  const float* ent = given(a[4]) ? floats_of(tensor(a[4], "entropy"), lead, x, "entropy") : nullptr;
+  const float* dent = given(a[5]) ? floats_of(tensor(a[5], "dentropy"), lead, x, "dentropy") : nullptr;
+  c10::cuda::CUDAGuard guard(x.device());
+  Out out = output(a[6], lead, r.cols, x.scalar_type(), x, "out");
+  library(scape_layer_token_logprobs_bwd(r.p, r.ld, dtype_of(x), ids.p, ids.bytes, r.rows, r.cols, lse, dlp, ent, dent,
+                                         out.r.p, out.r.ld, stream_of(x)));
+  return out.done();
+}
+
+// (logits, targets, weight or None, weight of every row, out) -> (loss, dlogits)
+PyObject* do_token_loss(Args a) {
+  const Tensor& x = tensor(a[0], "logits");
+  const Rows r = rows_of(x, kBf16 | kF32, "logits");
+  const auto lead = lead_of(x);
+  const Ids ids = ids_of(tensor(a[1], "targets"), lead, x, "targets");
+  const float* w = given(a[2]) ? floats_of(tensor(a[2], "weight"), lead, x, "weight") : nullptr;
+  const double all = number(a[3]);
+  c10::cuda::CUDAGuard guard(x.device());
+  Out out = output(a[4], lead, r.cols, x.scalar_type(), x, "out");
+  Tensor loss = row_floats(lead, x), ws;
+  size_t n = 0;
+  library(scape_layer_token_loss_workspace(r.p, r.ld, dtype_of(x), r.rows, r.cols, out.r.p, out.r.ld, &n));
+  if (n) ws = bytes(n, x);
+  library(scape_layer_token_loss(r.p, r.ld, dtype_of(x), ids.p, ids.bytes, r.rows, r.cols, w, (float)all,
+                                 loss.data_ptr<float>(), out.r.p, out.r.ld, n ? ws.data_ptr() : nullptr, n,
+                                 stream_of(x)));
+  return tuple({wrap(loss), out.done()});
+}
+
+// ------------------------------------------------------------------ gradients
+struct Set {
+  std::vector<Tensor> t;
+  std::vector<const void*> p;
+  std::vector<int64_t> numel;
+  std::vector<int> dtype;
+};
+Set set_of(PyObject* o, const char* name) {
+  Set s;
+  if (THPVariable_Check(o)) throw ValueError(std::string(name) + " must be a list or tuple of tensors");
+  PyObject* seq = PySequence_Fast(o, "");
+  if (!seq) {
+    PyErr_Clear();
+    throw ValueError(std::string(name) + " must be a list or tuple of tensors");
+  }
+  const Py_ssize_t n = PySequence_Fast_GET_SIZE(seq);
+  try {
+    s.t.reserve(n), s.p.reserve(n), s.numel.reserve(n), s.dtype.reserve(n);
+    for (Py_ssize_t i = 0; i < n; ++i) {
+      const Tensor& t = tensor(PySequence_Fast_GET_ITEM(seq, i), name);
+      if (!t.is_cuda()) throw ValueError(std::string(name) + " must be CUDA tensors");
+      if (!(type_of(t) & (kBf16 | kF32)))
+        throw ValueError(std::string(name) + " must be of type" + names(kBf16 | kF32));
+      if (i && t.device() != s.t[0].device()) throw ValueError(std::string(name) + " are on several devices");
+      if (!t.is_non_overlapping_and_dense())
+        throw ValueError(std::string(name) + " holds a tensor whose elements do not lie together");
+      s.t.push_back(t);
+      s.p.push_back(t.data_ptr());
+      s.numel.push_back(t.numel());
+      s.dtype.push_back(dtype_of(t));
+    }
+  } catch (...) {
+    Py_DECREF(seq);
+    throw;
+  }
+  Py_DECREF(seq);
+  if (n == 0) throw ValueError(std::string(name) + " has no tensor");
+  if (n > 0x7FFFFFFF) throw ValueError(std::string(name) + " has too many tensors");
+  return s;
+}
+Tensor norm_space(const Set& s, Tensor* ws, size_t* n) {
+  library(scape_layer_grad_norm_workspace((int)s.t.size(), s.numel.data(), n));
+  if (*n) *ws = bytes(*n, s.t[0]);
+  return at::detail::empty_cuda({}, at::kFloat, s.t[0].device(), std::nullopt);
+}
+
+// (grads) -> norm
+PyObject* do_grad_norm(Args a) {
+  const Set s = set_of(a[0], "grads");
+  c10::cuda::CUDAGuard guard(s.t[0].device());
+  Tensor ws;
+  size_t n = 0;
+  Tensor norm = norm_space(s, &ws, &n);
+  library(scape_layer_grad_norm((int)s.t.size(), s.p.data(), s.numel.data(), s.dtype.data(), norm.data_ptr<float>(),
+                                n ? ws.data_ptr() : nullptr, n, stream_of(s.t[0])));
+  return wrap(norm);
+}
+
+// (grads, max_norm, eps, out or None) -> norm
+PyObject* do_clip_grad_norm(Args a) {
+  const Set s = set_of(a[0], "grads");
+  const double max_norm = number(a[1]), eps = number(a[2]);
+  Set o;
+  if (given(a[3])) {
+    o = set_of(a[3], "out");
+    if (o.t.size() != s.t.size()) throw ValueError("out has another number of tensors than grads");
+    for (size_t i = 0; i < s.t.size(); ++i) {
+      on_device(o.t[i], s.t[0], "out");
+      if (o.t[i].sizes() != s.t[i].sizes()) throw ValueError("a tensor of out has another shape than grads'");
+      if (o.t[i].strides() != s.t[i].strides() && !(o.t[i].is_contiguous() && s.t[i].is_contiguous()))
+        throw ValueError("a tensor of out has its dimensions in another order than grads'");
+    }
+  }
+  c10::cuda::CUDAGuard guard(s.t[0].device());
+  Tensor ws;
+  size_t n = 0;
+  Tensor norm = norm_space(s, &ws, &n);
+  const Set& into = given(a[3]) ? o : s;
+  library(scape_layer_clip_grads((int)s.t.size(), s.p.data(), s.numel.data(), s.dtype.data(),
+                                 const_cast<void* const*>(into.p.data()), into.dtype.data(), (float)max_norm,
+                                 (float)eps, norm.data_ptr<float>(), n ? ws.data_ptr() : nullptr, n,
+                                 stream_of(s.t[0])));
+  for (const Tensor& t : into.t) written(t);
+  return wrap(norm);
+}
+
 // () -> int
 PyObject* do_status(Args) {
   int v = 0, rc = 0;
@@ -496,6 +736,13 @@ PyMethodDef kMethods[] = {ENTRY(pack8, 1),
                           ENTRY(linear, 7),
                           ENTRY(linear_backward_input, 5),
                           ENTRY(linear_backward_weight, 6),
+                          ENTRY(embedding, 5),
+                          ENTRY(embedding_backward, 5),
+                          ENTRY(token_logprobs, 4),
+                          ENTRY(token_logprobs_backward, 7),
+                          ENTRY(token_loss, 5),
+                          ENTRY(grad_norm, 1),
+                          ENTRY(clip_grad_norm, 4),
                           ENTRY(status, 0),
                           {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_layers_torch", nullptr, -1, kMethods,

@@ -2,7 +2,9 @@
 
 The gradients that Scape.step() reads are made with these on the same GPU:
 the residual RMS norm, activation checkpoints in 8 bits, and the linear layer
-with bias, activation and residual in its epilogue, each with its gradient.
+with bias, activation and residual in its epilogue, each with its gradient; the
+embedding and the log probabilities of tokens (or a loss) at a language model's
+ends, with theirs; and the gradients' norm and clipping before the step.
 Every computation is a kernel of libscape.so; PyTorch provides device memory
 and the current stream, on which all work is enqueued.
 
@@ -154,6 +156,87 @@ def linear_backward_weight(dy, x, activation=None, dweight=None, dbias=None, gra
             raise ValueError("dweight is not of grad_dtype")
     return _lib().linear_backward_weight(dy, x, _activation(activation), dweight, dbias,
                                          grad_dtype is torch.float32)
+
+
+# ------------------------------------------------------------------ tokens
+def embedding(tokens, weight, scale=1.0, dtype=None, out=None) -> torch.Tensor:
+    """scale * weight[tokens], a row of zeros for a token below 0 (none).  tokens:
+    contiguous int64 or int32; weight [vocabulary, columns] and the result float32 or
+    bfloat16 each (the result weight's unless dtype or out says otherwise).  A token
+    outside the vocabulary gives a row of NaN."""
+    if dtype is not None and dtype is not torch.bfloat16 and dtype is not torch.float32:
+        raise ValueError("dtype must be torch.float32 or torch.bfloat16")
+    kind = 0 if dtype is None else 1 if dtype is torch.bfloat16 else 2
+    return _lib().embedding(tokens, weight, scale, kind, out)
+
+
+def embedding_backward(dy, tokens, dweight, scale=1.0, accumulate=False) -> torch.Tensor:
+    """The gradient of embedding's weight, written into dweight [vocabulary, columns]
+    (a view of a flat gradient, say), which is returned: scale times the sum of dy's
+    rows of each token, zeros where there are none.  accumulate: added to what
+    dweight holds, for a table that is the output layer's weight as well.  Sums
+    are in 32 bits and in the same order in every call; tokens below 0 or outside
+    the vocabulary add nothing."""
+    return _lib().embedding_backward(dy, tokens, dweight, scale, accumulate)
+
+
+class TokenLogprobs(NamedTuple):
+    """Each of the rows' leading shape, float32: the targets' log probabilities, the
+    logits' log-sum-exp, the entropies (None unless asked for); the `top` largest
+    logits' log probabilities and columns (int64), in falling order, in one more
+    dimension (None unless asked for)."""
+    logprob: torch.Tensor
+    lse: torch.Tensor
+    entropy: torch.Tensor | None
+    top_logprob: torch.Tensor | None
+    top_token: torch.Tensor | None
+
+
+def token_logprobs(logits, targets, entropy=False, top=0) -> TokenLogprobs:
+    """Log probabilities of the targets (contiguous int64 or int32, of the logits'
+    leading shape) under softmax(logits), logits float32 or bfloat16.  A target below
+    0 stands for none and gives 0; one outside the vocabulary gives NaN.  top: 0 to
+    32; of equal logits the lower column comes first.  A logit of -infinity has
+    probability 0; in a row of nothing else every log probability is -infinity and
+    the entropy 0."""
+    return TokenLogprobs(*_lib().token_logprobs(logits, targets, entropy, top))
+
+
+def token_logprobs_backward(logits, targets, lse, dlogprob, entropy=None, dentropy=None,
+                            out=None) -> torch.Tensor:
+    """The gradient of the logits, from that of the log probabilities and, if given,
+    that of the entropies (with the entropies themselves).  lse, dlogprob, entropy and
+    dentropy: contiguous float32, one a row.  out may be logits."""
+    if dentropy is not None and entropy is None:
+        raise ValueError("dentropy needs the entropies that token_logprobs gave")
+    return _lib().token_logprobs_backward(logits, targets, lse, dlogprob, entropy, dentropy, out)
+
+
+def token_loss(logits, targets, weight, out=None):
+    """(loss, dlogits): each row's -weight * log probability of its target, and the
+    gradient of their sum, with the logits read once.  weight: a number, or
+    contiguous float32, one a row; 1 / the number of targets makes the sum a mean.  A
+    row whose target is below 0 (none) has neither, whatever its logits.  out
+    (the gradient) may be logits."""
+    if isinstance(weight, torch.Tensor):
+        return _lib().token_loss(logits, targets, weight, 0.0, out)
+    return _lib().token_loss(logits, targets, None, float(weight), out)
+
+
+# ------------------------------------------------------------------ gradients
+def grad_norm(grads) -> torch.Tensor:
+    """sqrt of the sum of all elements' squares over a list of float32 or bfloat16
+    tensors on one device, as a float32 scalar there.  A tensor's elements lie
+    together in memory, in any order of its dimensions."""
+    return _lib().grad_norm(grads)
+
+
+def clip_grad_norm(grads, max_norm, out=None, eps=1e-6) -> torch.Tensor:
+    """Multiplies every tensor by min(1, max_norm / (norm + eps)) and returns the norm
+    from before, without waiting for it.  In place, or into the tensors of `out`, of
+    the same shapes and strides and of either type: float32 sums over
+    several batches go into a worker's flat bfloat16 gradient so."""
+    return _lib().clip_grad_norm(grads, max_norm, eps, out)
 
 
 def status() -> int:
