@@ -104,35 +104,42 @@ __global__ __launch_bounds__(kFwdThreads) void embed_fwd_kernel(const __grid_con
 // for another block.  All blocks reading all tokens is 152 x 8 bytes a token out of
 // L2, as much as a row of dy is out of memory; several passes of a radix sort would
 // each be a launch.
-constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32, kSortUnroll = 8;
+constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32, kSortUnroll = 16;
 constexpr int kSortRows = 352;  // 44 KB of counts
 
 template <typename I>
 __global__ __launch_bounds__(kSortThreads) void sort_tokens_kernel(const I* __restrict__ tokens, int64_t count,
                                                                    int64_t vocab, int rows, int2* entries,
                                                                    int* starts) {
-  start();
   extern __shared__ int counts[];  // [kSortWarps][rows]
-  __shared__ int below_of[kSortWarps], sums[kSortWarps];
+  __shared__ int below_of[kSortWarps], sums[kSortWarps], first[kSortRows];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t lo = (int64_t)blockIdx.x * rows;
   const int mine = (int)min((int64_t)rows, vocab - lo);
   for (int i = threadIdx.x; i < kSortWarps * rows; i += kSortThreads) counts[i] = 0;
+  start();
   __syncthreads();
-  const int64_t share = ((count + kSortThreads - 1) / kSortThreads) * 32;
+  const int64_t share = (count + kSortThreads - 1) / kSortThreads * 32;
   const int64_t begin = min(count, warp * share), end = min(count, begin + share);
   int* own = counts + warp * rows;
-  int below = 0;
-  for (int64_t i = begin; i < end; i += 32 * kSortUnroll) {
+  int d[kSortUnroll];  // places of 32 x kSortUnroll tokens among this block's, or -1
+  auto read = [&](int64_t i, int& below) {
     I t[kSortUnroll];
 #pragma unroll
     for (int u = 0; u < kSortUnroll; ++u) t[u] = i + u * 32 + lane < end ? tokens[i + u * 32 + lane] : (I)-1;
 #pragma unroll
     for (int u = 0; u < kSortUnroll; ++u) {
-      const int64_t d = (int64_t)t[u] - lo;
-      if (t[u] >= 0 && d < 0) ++below;
-      if (d >= 0 && d < mine) atomicAdd(&own[d], 1);
+      const int64_t at = (int64_t)t[u] - lo;
+      below += t[u] >= 0 && at < 0;
+      d[u] = at >= 0 && at < mine ? (int)at : -1;
     }
+  };
+  int below = 0;
+  for (int64_t i = begin; i < end; i += 32 * kSortUnroll) {
+    read(i, below);
+#pragma unroll
+    for (int u = 0; u < kSortUnroll; ++u)
+      if (d[u] >= 0) atomicAdd(&own[d[u]], 1);
   }
   below = __reduce_add_sync(0xFFFFFFFFu, below);
   if (lane == 0) below_of[warp] = below;
@@ -155,37 +162,24 @@ __global__ __launch_bounds__(kSortThreads) void sort_tokens_kernel(const I* __re
   }
   if (lane == 31) sums[warp] = scan;
   __syncthreads();
-  int base = scan - total, all = 0, before = 0;
-  for (int w = 0; w < kSortWarps; ++w) {
-    if (w < warp) base += sums[w];
-    all += sums[w];
-    before += below_of[w];
-  }
-  base += before;
+  const int before = __reduce_add_sync(0xFFFFFFFFu, below_of[lane]);
+  const int base = before + scan - total + __reduce_add_sync(0xFFFFFFFFu, lane < warp ? sums[lane] : 0);
+  if ((int)threadIdx.x < rows) first[threadIdx.x] = base;
   if ((int)threadIdx.x < mine) starts[lo + threadIdx.x] = base;
-  if (lo + mine == vocab && threadIdx.x == 0) starts[vocab] = before + all;
-  if ((int)threadIdx.x < rows) {
-#pragma unroll 8
-    for (int w = 0; w < kSortWarps; ++w) counts[w * rows + threadIdx.x] += base;
-  }
+  if (lo + mine == vocab && (int)threadIdx.x == mine - 1) starts[vocab] = base + total;
   __syncthreads();
   for (int64_t i = begin; i < end; i += 32 * kSortUnroll) {
-    I t[kSortUnroll];
-#pragma unroll
-    for (int u = 0; u < kSortUnroll; ++u) t[u] = i + u * 32 + lane < end ? tokens[i + u * 32 + lane] : (I)-1;
+    if (end - begin > 32 * kSortUnroll) read(i, below);  // else they are still there
 #pragma unroll
     for (int u = 0; u < kSortUnroll; ++u) {
-      const int64_t d = (int64_t)t[u] - lo;
-      const bool in = d >= 0 && d < mine;
-      if (!__any_sync(0xFFFFFFFFu, in)) continue;
-      const int key = in ? (int)d : -1;
-      const uint32_t same = __match_any_sync(0xFFFFFFFFu, key);
+      if (!__any_sync(0xFFFFFFFFu, d[u] >= 0)) continue;
+      const uint32_t same = __match_any_sync(0xFFFFFFFFu, d[u]);
       const int rank = __popc(same & ((1u << lane) - 1));
-      const int at = in ? own[key] : 0;
+      const int at = d[u] >= 0 ? own[d[u]] + rank : 0;
       __syncwarp();
-      if (in) {
-        entries[at + rank] = make_int2((int)(i + u * 32 + lane), (int)t[u]);
-        if ((same >> lane) == 1u) own[key] = at + rank + 1;
+      if (d[u] >= 0) {
+        entries[first[d[u]] + at] = make_int2((int)(i + u * 32 + lane), (int)(lo + d[u]));
+        if ((same >> lane) == 1u) own[d[u]] = at + 1;
       }
       __syncwarp();
     }
@@ -225,47 +219,68 @@ __device__ __forceinline__ void zero_row(T* p, int cols, int lane) {
   if (lane < tail) p[cols - tail + lane] = (T)0.0f;
 }
 
-// The first tiles * chunks blocks add up a tile's columns, the others write zeros.
+// The first blocks write zeros, the others each add up some columns of a tile's
+// entries: those of the tokens that start in it, and, of a token with more than
+// kLong entries, the tile's own part, which goes to `partial` for the join.  So a
+// common word's entries are spread over blocks and few tokens need a join.
+constexpr int kLong = 2 * kEmbedTile;
+
 template <typename TD, typename TG, bool ANY>
-__global__ __launch_bounds__(kTileThreads) void embed_sum_kernel(const __grid_constant__ EmbedBwd a, int tiles,
+__global__ __launch_bounds__(kTileThreads) void embed_sum_kernel(const __grid_constant__ EmbedBwd a, int fill,
                                                                  int chunks, bool dw16) {
   start();
   constexpr int VEC = 16 / (int)sizeof(TD);
   extern __shared__ __align__(16) uint4 staged[];  // [kEmbedTile][threads]
-  __shared__ int position[kEmbedTile + 2], token[kEmbedTile + 2];
+  __shared__ int position[kEmbedTile + kLong], token[kEmbedTile + kLong];
+  __shared__ int ends[4];  // where the first and the last entry's tokens start and end
   TG* dw = static_cast<TG*>(a.dw);
-  if ((int64_t)blockIdx.x >= (int64_t)tiles * chunks) {
+  if ((int)blockIdx.x < fill) {
     const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-    const int64_t v0 = (((int64_t)blockIdx.x - (int64_t)tiles * chunks) * warps + (threadIdx.x >> 5)) * 32;
+    const int64_t v0 = ((int64_t)blockIdx.x * warps + (threadIdx.x >> 5)) * 32;
     if (v0 >= a.vocab) return;
     const bool none = v0 + lane < a.vocab && a.starts[v0 + lane] == a.starts[v0 + lane + 1];
     for (uint32_t left = __ballot_sync(0xFFFFFFFFu, none); left; left &= left - 1)
       zero_row(dw + (v0 + __ffs(left) - 1) * a.lddw, a.cols, lane);
     return;
   }
-  const int tile = blockIdx.x / chunks, chunk = blockIdx.x % chunks;
+  const int tile = ((int)blockIdx.x - fill) / chunks, chunk = ((int)blockIdx.x - fill) % chunks;
   const int valid = a.starts[a.vocab], i0 = tile * kEmbedTile;
-  const int n = min(kEmbedTile, valid - i0);
-  if (n <= 0) {
+  const int i1 = min(i0 + kEmbedTile, valid);
+  if (i0 >= valid) {
     if (chunk == 0 && threadIdx.x == 0) a.crossing[tile] = -1;
     return;
   }
-  if (threadIdx.x < kEmbedTile + 2) {
-    const int i = i0 - 1 + (int)threadIdx.x;
-    const int2 e = i >= 0 && i < valid ? a.entries[i] : make_int2(0, -1);
-    position[threadIdx.x] = e.x;
-    token[threadIdx.x] = e.y;
+  for (int i = threadIdx.x; i < kEmbedTile + kLong; i += blockDim.x) {
+    const int2 e = i0 + i < valid ? a.entries[i0 + i] : make_int2(0, -1);
+    position[i] = e.x;
+    token[i] = e.y;
+  }
+  if (threadIdx.x < 4) {
+    const int64_t v = a.entries[threadIdx.x < 2 ? i0 : i1 - 1].y;
+    ends[threadIdx.x] = a.starts[v + (threadIdx.x & 1)];
   }
   __syncthreads();
+  // entries of a short token go with the tile where it starts
+  const bool first_before = ends[0] < i0, first_long = ends[1] - ends[0] > kLong;
+  const bool last_long = ends[3] - ends[2] > kLong;
+  const int begin = first_before && !first_long ? min(ends[1], i1) : i0;
+  const int end = last_long || ends[2] < i0 ? i1 : ends[3];
+  if (chunk == 0 && threadIdx.x == 0) a.crossing[tile] = last_long && ends[2] >= i0 ? token[i1 - 1 - i0] : -1;
   const int c0 = (chunk * (int)blockDim.x + (int)threadIdx.x) * VEC;
   const int mine = a.cols - c0;
+  if (mine <= 0) return;
   const TD* dy = static_cast<const TD*>(a.dy);
   const TD* hi = dy + (a.tokens.count - 1) * a.lddy + a.cols;
-  if (mine > 0) {
+  float acc[VEC];
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) acc[i] = 0.0f;
+  for (int at = begin; at < end; at += kEmbedTile) {
+    const int n = min(kEmbedTile, end - at);
     if constexpr (ANY) {
 #pragma unroll 8
       for (int l = 0; l < n; ++l) {
-        const Raw<TD, VEC> r = load_any<VEC>(dy + (int64_t)position[l + 1] * a.lddy + c0, min(mine, VEC), dy, hi);
+        const Raw<TD, VEC> r =
+            load_any<VEC>(dy + (int64_t)position[at - i0 + l] * a.lddy + c0, min(mine, VEC), dy, hi);
         staged[l * blockDim.x + threadIdx.x] = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
       }
     } else {
@@ -273,15 +288,11 @@ __global__ __launch_bounds__(kTileThreads) void embed_sum_kernel(const __grid_co
       for (int l = 0; l < n; ++l) {
         const uint32_t to = (uint32_t)__cvta_generic_to_shared(&staged[l * blockDim.x + threadIdx.x]);
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to),
-                     "l"(dy + (int64_t)position[l + 1] * a.lddy + c0), "r"(bytes)
+                     "l"(dy + (int64_t)position[at - i0 + l] * a.lddy + c0), "r"(bytes)
                      : "memory");
       }
       asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
     }
-    float acc[VEC];
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) acc[i] = 0.0f;
-    bool whole = token[1] != token[0];  // the sum so far began in this tile
     for (int l = 0; l < n; ++l) {
       const uint4 u = staged[l * blockDim.x + threadIdx.x];
       Raw<TD, VEC> r;
@@ -290,35 +301,33 @@ __global__ __launch_bounds__(kTileThreads) void embed_sum_kernel(const __grid_co
       to_floats(r, f);
 #pragma unroll
       for (int i = 0; i < VEC; ++i) acc[i] += f[i];
-      const bool goes_on = token[l + 2] == token[l + 1];
-      if (goes_on && l + 1 < n) continue;
-      if (whole && !goes_on) {
-        TG* p = dw + (int64_t)token[l + 1] * a.lddw + c0;
+      const int i = at + l, v = token[i - i0];
+      if (i + 1 < end && token[i + 1 - i0] == v) continue;
+      // a long token's sum is whole where it starts and ends in this tile's entries only
+      const bool from_first = i < ends[1];
+      const bool part = (from_first && first_long) || (i + 1 == end && last_long);
+      if (!part) {
+        TG* p = dw + (int64_t)v * a.lddw + c0;
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          acc[i] *= a.scale;
-          if (a.accumulate && i < mine) acc[i] += (float)p[i];
+        for (int k = 0; k < VEC; ++k) {
+          acc[k] *= a.scale;
+          if (a.accumulate && k < mine) acc[k] += (float)p[k];
         }
         put<TG, VEC>(p, mine, dw16, acc);
       } else {
-        float* p = a.partial + ((int64_t)tile * 2 + (whole ? 1 : 0)) * a.partial_pitch + c0;
+        // first the sum of what started before the tile, second of what starts in it
+        float* p = a.partial + ((int64_t)tile * 2 + (from_first && first_before ? 0 : 1)) * a.partial_pitch + c0;
         put<float, VEC>(p, VEC, true, acc);
       }
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) acc[i] = 0.0f;
-      whole = true;
+      for (int k = 0; k < VEC; ++k) acc[k] = 0.0f;
     }
-  }
-  if (chunk == 0 && threadIdx.x == 0) {
-    // what the tile's last entry belongs to, if it starts here and goes on
-    const bool goes_on = token[n + 1] == token[n];
-    a.crossing[tile] = goes_on && a.starts[token[n]] >= i0 ? token[n] : -1;
   }
 }
 
 // ------------------------------------------------------------------ joining
-// Item (tile, 128 columns): the sum of the token that starts in the tile and goes
-// on.  A block first looks at all its items' tiles.
+// Item (tile, 128 columns): the sum of the long token that starts in the tile.  A
+// block first looks at all its items' tiles.
 constexpr int kJoinThreads = 256, kJoinCols = 128;
 
 template <typename TG>
@@ -326,19 +335,25 @@ __global__ __launch_bounds__(kJoinThreads) void embed_join_kernel(const __grid_c
                                                                   int chunks, bool dw8) {
   start();
   __shared__ float4 part[kJoinThreads / 32][32];
-  __shared__ int found[kJoinThreads];
+  __shared__ int found[kJoinThreads], found_tile[kJoinThreads], found_chunk[kJoinThreads];
+  __shared__ int finds;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t items = (int64_t)tiles * chunks;
   TG* dw = static_cast<TG*>(a.dw);
   for (int64_t base = blockIdx.x; base < items; base += (int64_t)gridDim.x * kJoinThreads) {
-    const int64_t my = base + (int64_t)threadIdx.x * gridDim.x;
-    found[threadIdx.x] = my < items ? a.crossing[my / chunks] : -1;
+    if (threadIdx.x == 0) finds = 0;
     __syncthreads();
-    for (int k = 0; k < kJoinThreads; ++k) {
-      const int v = found[k];
-      if (v < 0) continue;
-      const int64_t item = base + (int64_t)k * gridDim.x;
-      const int tile = (int)(item / chunks), c0 = (int)(item % chunks) * kJoinCols + lane * 4;
+    const int64_t my = base + (int64_t)threadIdx.x * gridDim.x;
+    if (my < items) {
+      const int tile = (int)(my / chunks), v = a.crossing[tile];
+      if (v >= 0) {
+        const int at = atomicAdd(&finds, 1);  // their order changes nothing
+        found[at] = v, found_tile[at] = tile, found_chunk[at] = (int)(my % chunks);
+      }
+    }
+    __syncthreads();
+    for (int k = 0; k < finds; ++k) {
+      const int v = found[k], tile = found_tile[k], c0 = found_chunk[k] * kJoinCols + lane * 4;
       const int last = (a.starts[v + 1] - 1) / kEmbedTile;
       float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       if (c0 < a.cols) {
@@ -369,7 +384,6 @@ __global__ __launch_bounds__(kJoinThreads) void embed_join_kernel(const __grid_c
       }
       __syncthreads();
     }
-    __syncthreads();
   }
 }
 
@@ -411,7 +425,7 @@ cudaError_t run_embedding_bwd(const EmbedBwd& a, cudaStream_t st) {
   const bool dw16 = aligned(a.dw, std::min<size_t>(16, VEC * sizeof(TG))) &&
                     (a.lddw * sizeof(TG)) % std::min<size_t>(16, VEC * sizeof(TG)) == 0;
   e = launch_kernel(any ? embed_sum_kernel<TD, TG, true> : embed_sum_kernel<TD, TG, false>,
-                    (unsigned)(tiles * chunks + fill), threads, smem, 0, st, a, (int)tiles, (int)chunks, dw16);
+                    (unsigned)(tiles * chunks + fill), threads, smem, 0, st, a, (int)fill, (int)chunks, dw16);
   if (e != cudaSuccess) return e;
   const int64_t join = ceil_div(a.cols, kJoinCols);
   const bool dw8 = aligned(a.dw, 4 * sizeof(TG)) && (a.lddw * sizeof(TG)) % (4 * sizeof(TG)) == 0;

@@ -2,10 +2,18 @@
 // of rows of logits, their gradient, and a loss that takes its gradient along.
 //
 // With m a row's largest logit and d = x - m: S = sum exp d, lse = m + ln S,
-// entropy = ln S - (sum exp(d) d) / S.  A thread keeps m, S and the entropy's sum of
-// its own pieces (16 bytes at the row's 16-byte boundaries) while it reads them, once;
-// a larger m scales S by exp(m - m'), and the threads' sums are joined the same way.
+// entropy = ln S - (sum exp(d) d) / S, for any m near the row's largest.  A thread
+// keeps m, S and the entropy's sum of its own pieces (16 bytes at the row's 16-byte
+// boundaries) while it reads them, once.  Its m is the largest of its first values:
+// later ones may be above it, and only where some add 1024 to S (or are no numbers)
+// is m raised, which scales S by exp(m - m'); the threads' sums are joined the same
+// way.  (Exponents up to 10 keep their digits; the largest of every few values is an
+// instruction a value.)
 // Exponents are of base 2: a = d log2 e.
+//
+// Memory bounds these kernels only if the instructions stay few: a value's share of
+// the copy rate is 10 of an SM's lane-instructions in bfloat16, an exponential alone
+// is 8 of them where its unit does 16 a clock.
 #include <algorithm>
 #include <type_traits>
 
@@ -40,7 +48,9 @@ struct RowPieces {
   }
   __device__ int column(int v) const { return v * kPer - phase; }
   __device__ bool whole(int v) const { return column(v) >= 0 && column(v) + kPer <= cols; }
-  __device__ uint4 load_whole(int v) const { return *reinterpret_cast<const uint4*>(x + column(v)); }
+  // Whole pieces among [v0, v1): all but the row's first and last, if they are not.
+  __device__ int first_whole(int v0) const { return v0 == 0 && phase > 0 ? 1 : v0; }
+  __device__ int end_whole(int v1) const { return v1 == pieces && column(v1) > cols ? v1 - 1 : v1; }
   // Columns outside the row are -infinity.
   __device__ uint4 load_part(int v) const {
     uint32_t w[4];
@@ -59,13 +69,7 @@ struct RowPieces {
       }
     return make_uint4(w[0], w[1], w[2], w[3]);
   }
-  __device__ uint4 load(int v) const { return whole(v) ? load_whole(v) : load_part(v); }
 };
-template <typename T>
-__device__ __forceinline__ uint4 minus_infinity() {
-  const uint32_t w = sizeof(T) == 2 ? 0xFF80FF80u : 0xFF800000u;
-  return make_uint4(w, w, w, w);
-}
 // A piece's values as pairs of floats.
 template <typename T>
 __device__ __forceinline__ void piece_pairs(const uint4& u, uint64_t (&p)[8 / sizeof(T)]) {
@@ -78,18 +82,25 @@ __device__ __forceinline__ void piece_pairs(const uint4& u, uint64_t (&p)[8 / si
     p[1] = pair(__uint_as_float(w[2]), __uint_as_float(w[3]));
   }
 }
-// The largest of a piece's values that are not NaN (-infinity if all are).
-template <typename T>
-__device__ __forceinline__ float piece_top(const uint4& u) {
+// The largest of some pieces' values that are not NaN (if any is not).
+template <typename T, int U>
+__device__ __forceinline__ float pieces_top(const uint4 (&u)[U]) {
   if constexpr (sizeof(T) == 2) {
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-    __nv_bfloat162 t[4];
+    __nv_bfloat162 m = __float2bfloat162_rn(-INFINITY);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) t[i] = *reinterpret_cast<const __nv_bfloat162*>(&w[i]);
-    const __nv_bfloat162 m = __hmax2(__hmax2(t[0], t[1]), __hmax2(t[2], t[3]));
+    for (int i = 0; i < U; ++i) {
+      const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) m = __hmax2(m, *reinterpret_cast<const __nv_bfloat162*>(&w[k]));
+    }
     return fmaxf(__low2float(m), __high2float(m));
   } else {
-    return fmaxf(fmaxf(__uint_as_float(u.x), __uint_as_float(u.y)), fmaxf(__uint_as_float(u.z), __uint_as_float(u.w)));
+    float m = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < U; ++i)
+      m = fmaxf(m, fmaxf(fmaxf(__uint_as_float(u[i].x), __uint_as_float(u[i].y)),
+                         fmaxf(__uint_as_float(u[i].z), __uint_as_float(u[i].w))));
+    return m;
   }
 }
 
@@ -105,15 +116,10 @@ struct Sums {
     s *= f;
     m = top;
   }
-  // A few pieces' values.
   template <typename T, int U>
-  __device__ __forceinline__ void add(const uint4 (&u)[U]) {
-    float top = piece_top<T>(u[0]);
-#pragma unroll
-    for (int i = 1; i < U; ++i) top = fmaxf(top, piece_top<T>(u[i]));
-    if (top > m) raise(top);
+  __device__ __forceinline__ void sum(const uint4 (&u)[U], float& s_out, float& a_out) const {
     const uint64_t minus = pair(-m, -m), log2e = pair(kLog2eF, kLog2eF);
-    uint64_t s2 = pair(s, 0.0f), a2 = pair(a, 0.0f);
+    uint64_t s2[2] = {pair(s, 0.0f), pair(0.0f, 0.0f)}, a2[2] = {pair(a, 0.0f), pair(0.0f, 0.0f)};
 #pragma unroll
     for (int i = 0; i < U; ++i) {
       uint64_t p[8 / sizeof(T)];
@@ -124,18 +130,34 @@ struct Sums {
         float x, y;
         unpair(e, x, y);
         const uint64_t f = pair(exp2_fast(x), exp2_fast(y));
-        s2 = add2(s2, f);
+        s2[k % 2] = add2(s2[k % 2], f);
         // where 2^e is 0 its product with an infinite e would be NaN
-        if (ENT) a2 = fma2(f, pair(fmaxf(x, -1e4f), fmaxf(y, -1e4f)), a2);
+        if (ENT) a2[k % 2] = fma2(f, pair(fmaxf(x, -1e4f), fmaxf(y, -1e4f)), a2[k % 2]);
       }
     }
     float x, y;
-    unpair(s2, x, y);
-    s = x + y;
+    unpair(add2(s2[0], s2[1]), x, y);
+    s_out = x + y;
     if (ENT) {
-      unpair(a2, x, y);
-      a = x + y;
+      unpair(add2(a2[0], a2[1]), x, y);
+      a_out = x + y;
     }
+  }
+  // A few pieces' values.
+  template <typename T, int U>
+  __device__ __forceinline__ void add(const uint4 (&u)[U]) {
+    if (m == kLowest) {
+      const float top = pieces_top<T, U>(u);
+      if (top > m) raise(top);
+    }
+    float s1, a1 = 0.0f;
+    for (bool raised = false;; raised = true) {
+      sum<T, U>(u, s1, a1);
+      if (s1 - s < 1024.0f || raised) break;
+      const float top = pieces_top<T, U>(u);
+      if (top > m) raise(top);
+    }
+    s = s1, a = a1;
   }
   // Of the warp, the same bits in every lane.
   __device__ __forceinline__ void over_warp() {
@@ -169,6 +191,10 @@ __device__ __forceinline__ Sums<ENT> join_parts(const Part* part, int n) {
     if (ENT) r.a += p.a;
   }
   return r;
+}
+// Where the rank-th block's pieces start; a cluster has a power of two of blocks.
+__device__ __forceinline__ int share_of(int pieces, uint32_t rank, uint32_t ranks) {
+  return (int)(((uint64_t)pieces * rank) >> (31 - __clz(ranks)));
 }
 // Stores to rank's copy of a place in shared memory.
 __device__ __forceinline__ uint32_t place_in(const void* p, uint32_t rank) {
@@ -207,11 +233,12 @@ __device__ __forceinline__ uint64_t max_over_warp(uint64_t k) {
   }
   return k;
 }
+// A piece's values inside the row, with their columns.
 template <typename T, typename F>
-__device__ __forceinline__ void for_values(const RowPieces<T>& row, int v, F&& f) {
+__device__ __forceinline__ void for_values(const RowPieces<T>& row, int v, const uint4& u, F&& f) {
   constexpr int kPer = RowPieces<T>::kPer;
   uint64_t p[8 / sizeof(T)];
-  piece_pairs<T>(row.load(v), p);
+  piece_pairs<T>(u, p);
   const int c = row.column(v);
 #pragma unroll
   for (int k = 0; k < kPer / 2; ++k) {
@@ -222,29 +249,27 @@ __device__ __forceinline__ void for_values(const RowPieces<T>& row, int v, F&& f
   }
 }
 
-constexpr int kThreads = 256, kUnroll = 4, kMaxCluster = 8;
+constexpr int kMaxThreads = 1024, kMaxCluster = 8;
 constexpr int kCandidates = 512;  // keys that pass the bound, before they are ranked
 
 struct TopScratch {
   float group[32];
   uint64_t keys[kCandidates];
   uint64_t best[SCAPE_TOP_MAX];
-  uint64_t of_warp[kThreads / 32];
+  uint64_t of_warp[kMaxThreads / 32];
   int count;
+  uint64_t all[2][kMaxCluster * SCAPE_TOP_MAX];  // the cluster's, in its first block; rows in turn
 };
-struct TopShared {
-  TopScratch scratch;
-  uint64_t all[kMaxCluster * SCAPE_TOP_MAX];
-};
-// The `top` largest keys of this block's pieces [v0, v1) into t.best (0 where there are
-// fewer), from each thread's largest value.  The threads form 32 groups; the top-th
-// of the groups' largest values is a bound that at least `top` values reach and, with
-// values spread over the groups, few more, so only threads whose own largest reaches
-// it read their pieces again (from the caches) and collect what does.  Where that
-// is too many (equal values) or too few (NaN, -infinity), the keys are found one
-// after the other, each the largest below the last.
-template <typename T>
-__device__ void find_top(const RowPieces<T>& row, int v0, int v1, int top, float largest, TopScratch& t) {
+// The `top` largest keys of this block's values into t.best, in falling order (0 where
+// there are fewer), from each thread's largest value.  The threads form 32 groups; the
+// top-th of the groups' largest values is a bound that at least `top` values reach
+// and, with values spread over the groups, few more, so only threads whose own largest
+// reaches it look through their values again (own_values(f) calls f(value, column)
+// for each) and collect what does.  Where that is too many (equal values) or too few
+// (NaN, -infinity), the keys are found one after the other, each the largest below
+// the last.
+template <typename V>
+__device__ __forceinline__ void find_top(V&& own_values, int top, float largest, TopScratch& t) {
   const int lane = threadIdx.x & 31, threads = blockDim.x, lanes = threads / 32;
   float g = largest;
   for (int o = 1; o < lanes; o <<= 1) g = fmaxf(g, __shfl_xor_sync(kAll, g, o));
@@ -259,13 +284,12 @@ __device__ void find_top(const RowPieces<T>& row, int v0, int v1, int top, float
   }
   const float bound = __shfl_sync(kAll, g, __ffs(__ballot_sync(kAll, rank == top - 1)) - 1);
   if (largest >= bound) {
-    for (int v = v0 + threadIdx.x; v < v1; v += threads)
-      for_values(row, v, [&](float x, int c) {
-        if (x >= bound) {
-          const int at = atomicAdd(&t.count, 1);
-          if (at < kCandidates) t.keys[at] = key_of(x, c);
-        }
-      });
+    own_values([&](float x, int c) {
+      if (x >= bound) {
+        const int at = atomicAdd(&t.count, 1);  // their order changes nothing: keys differ
+        if (at < kCandidates) t.keys[at] = key_of(x, c);
+      }
+    });
   }
   if (threadIdx.x < SCAPE_TOP_MAX) t.best[threadIdx.x] = 0;
   __syncthreads();
@@ -281,11 +305,10 @@ __device__ void find_top(const RowPieces<T>& row, int v0, int v1, int top, float
     uint64_t last = ~0ull;
     for (int j = 0; j < top; ++j) {
       uint64_t k = 0;
-      for (int v = v0 + threadIdx.x; v < v1; v += threads)
-        for_values(row, v, [&](float x, int c) {
-          const uint64_t q = key_of(x, c);
-          if (q < last && q > k) k = q;
-        });
+      own_values([&](float x, int c) {
+        const uint64_t q = key_of(x, c);
+        if (q < last && q > k) k = q;
+      });
       k = max_over_warp(k);
       if (lane == 0) t.of_warp[threadIdx.x >> 5] = k;
       __syncthreads();
@@ -299,69 +322,335 @@ __device__ void find_top(const RowPieces<T>& row, int v0, int v1, int top, float
   __syncthreads();
 }
 
+// ------------------------------------------------------------------ results of a row
+// x - lse from the row's sums; -infinity where nothing is left.
+template <bool ENT>
+__device__ __forceinline__ float log_probability(float x, const Sums<ENT>& all, float ln_s) {
+  return x == -INFINITY && all.s == 0.0f ? x : (x - all.m) - ln_s;
+}
+// Of the n keys of a cluster's blocks, the largest.
+template <bool ENT>
+__device__ __forceinline__ void write_top(const Logprobs& a, int64_t row, const uint64_t* keys, int n,
+                                          const Sums<ENT>& all, float ln_s) {
+  for (int i = threadIdx.x; i < n; i += blockDim.x) {
+    const uint64_t k = keys[i];
+    int r = i;
+    if (n > a.top) {
+      r = 0;
+      for (int j = 0; j < n; ++j) r += keys[j] > k;
+    }
+    if (r >= a.top || k == 0) continue;
+    a.top_token[row * a.top + r] = (int64_t)(0xFFFFFFFFu - (uint32_t)k);
+    a.top_logprob[row * a.top + r] = log_probability(logit_of(k), all, ln_s);
+  }
+}
+
+// A row's pieces [v0, v1) of a block, of which [w0, w1) are whole.
+template <typename T>
+struct Share {
+  RowPieces<T> row;
+  int v0, v1, w0, w1;
+  __device__ Share(const T* x, int64_t vocab, uint32_t rank, uint32_t ranks) : row(x, (int)vocab) {
+    v0 = share_of(row.pieces, rank, ranks);
+    v1 = share_of(row.pieces, rank + 1, ranks);
+    w0 = row.first_whole(v0);
+    w1 = max(w0, row.end_whole(v1));
+  }
+  __device__ bool part_before() const { return v0 < w0 && v0 < v1; }
+  __device__ bool part_after() const { return w1 < v1; }
+  __device__ const uint4* whole_pieces() const { return reinterpret_cast<const uint4*>(row.x - row.phase) + w0; }
+};
+
 // ------------------------------------------------------------------ forward
-// A cluster of blocks (one, where there are rows enough) takes a row.
+// Blocks of up to 256 threads, several an SM, go through rows, every thread with a ring
+// of its own pieces in shared memory that runs ahead across rows: while a row's sums
+// are joined the next one's pieces arrive.  A cluster of blocks shares a row where
+// there are few.
+//
+// 8192 x 32000 in bfloat16 with entropy: pieces read into registers 105 us, four blocks
+// an SM; rows held whole, one block of 1024 threads an SM, 181.
+constexpr int kThreads = 256, kUnroll = 4, kAhead = 3;
+constexpr int kBlocks = 4, kBlocksTop = 3;  // an SM
+
 template <typename T, bool ENT, bool TOP>
-__global__ __launch_bounds__(kThreads, 4) void logprobs_kernel(const __grid_constant__ Logprobs a) {
+__global__ __launch_bounds__(kThreads, TOP ? kBlocksTop : kBlocks) void logprobs_kernel(const __grid_constant__ Logprobs a,
+                                                                         int64_t rows, int batches) {
   cluster_begin();
   start();
-  __shared__ Part of_warp[kThreads / 32], of_block[kMaxCluster];
-  __shared__ std::conditional_t<TOP, TopShared, int> shared;
+  extern __shared__ __align__(16) uint4 ring[];  // [kAhead][kUnroll][threads]
+  __shared__ Part of_warp[2][kThreads / 32], of_block[2][kMaxCluster];
+  __shared__ std::conditional_t<TOP, TopScratch, int> scratch;
   const uint32_t rank = block_rank(), ranks = cluster_blocks();
-  const int64_t row = blockIdx.x / ranks;
-  const T* x = static_cast<const T*>(a.x) + row * a.ldx;
-  const RowPieces<T> pieces(x, (int)a.vocab);
-  const int v0 = (int)((int64_t)pieces.pieces * rank / ranks), v1 = (int)((int64_t)pieces.pieces * (rank + 1) / ranks);
-  const int64_t target = load_target(a.targets, row);
-  const bool in = target >= 0 && target < a.vocab;
-  float chosen = 0.0f;
-  if (threadIdx.x == 0 && rank == 0 && in) chosen = load_logit(x + target);
-  Sums<ENT> own;
-  for (int v = v0 + threadIdx.x; v < v1; v += kUnroll * blockDim.x) {
-    uint4 u[kUnroll];
+  const int lane = threadIdx.x & 31, threads = blockDim.x, warps = threads / 32;
+  const int64_t step = gridDim.x / ranks;
+  auto share = [&](int64_t row) { return Share<T>(static_cast<const T*>(a.x) + row * a.ldx, a.vocab, rank, ranks); };
+  // what the ring is to be given next
+  int64_t row_ahead = blockIdx.x / ranks;
+  int batch_ahead = 0, left_ahead = 0;
+  const uint4* from = nullptr;
+  auto begin_row = [&]() {
+    if (row_ahead >= rows) return;
+    const Share<T> r = share(row_ahead);
+    from = r.whole_pieces() + threadIdx.x;
+    left_ahead = r.w1 - r.w0 - (int)threadIdx.x;
+  };
+  begin_row();
+  const uint32_t own_ring = (uint32_t)__cvta_generic_to_shared(ring + threadIdx.x);
+  auto copy = [&](int stage) {
+    if (row_ahead < rows) {
 #pragma unroll
-    for (int i = 0; i < kUnroll; ++i) {
-      const int w = v + i * blockDim.x;
-      u[i] = w < v1 ? pieces.load(w) : minus_infinity<T>();
+      for (int i = 0; i < kUnroll; ++i)
+        if (left_ahead > i * threads)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(own_ring + (stage * kUnroll + i) * threads * 16),
+                       "l"(from + i * threads)
+                       : "memory");
+      from += kUnroll * threads;
+      left_ahead -= kUnroll * threads;
+      if (++batch_ahead == batches) {
+        batch_ahead = 0;
+        row_ahead += step;
+        begin_row();
+      }
     }
-    own.template add<T, kUnroll>(u);
-  }
-  const float largest = own.m;
-  own.over_warp();
-  if ((threadIdx.x & 31) == 0) {
-    of_warp[threadIdx.x >> 5] = {own.m, own.s, own.a};
-  }
-  __syncthreads();
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll
+  for (int s = 0; s < kAhead; ++s) copy(s);
   cluster_ready();
-  if constexpr (TOP) {
-    find_top(pieces, v0, v1, a.top, largest, shared.scratch);
-    if ((int)threadIdx.x < a.top) send(&shared.all[rank * a.top + threadIdx.x], 0, shared.scratch.best[threadIdx.x]);
-  }
-  if (threadIdx.x == 0) send(&of_block[rank], 0, join_parts<ENT>(of_warp, blockDim.x / 32));
-  cluster_done();
-  if (rank != 0) return;
-  const Sums<ENT> all = join_parts<ENT>(of_block, (int)ranks);
-  const float ln_s = logf(all.s), lse = all.m + ln_s;
-  if (threadIdx.x == 0) {
-    float lp = in ? (chosen - all.m) - ln_s : target < 0 ? 0.0f : __uint_as_float(0x7FC00000u);
-    if (in && chosen == -INFINITY && all.s == 0.0f) lp = -INFINITY;
-    if (a.loss && target >= 0) lp *= -(a.weight ? a.weight[row] : a.weight_all);
-    if (a.logprob) a.logprob[row] = lp;
-    if (a.lse) a.lse[row] = lse;
-    if (ENT) a.entropy[row] = all.s == 0.0f ? 0.0f : ln_s - all.a * kLn2F / all.s;
-  }
-  if constexpr (TOP) {
-    const uint64_t* tops = shared.all;
-    const int n = (int)ranks * a.top;
-    for (int i = threadIdx.x; i < n; i += blockDim.x) {
-      const uint64_t k = tops[i];
-      int r = 0;
-      for (int j = 0; j < n; ++j) r += tops[j] > k;
-      if (r >= a.top || k == 0) continue;
-      const float v = logit_of(k);
-      a.top_token[row * a.top + r] = (int64_t)(0xFFFFFFFFu - (uint32_t)k);
-      a.top_logprob[row * a.top + r] = v == -INFINITY && all.s == 0.0f ? v : (v - all.m) - ln_s;
+  int stage = 0, flip = 0;
+  for (int64_t row = blockIdx.x / ranks; row < rows; row += step) {
+    const Share<T> r = share(row);
+    const int64_t target = load_target(a.targets, row);
+    const bool in = target >= 0 && target < a.vocab;
+    float chosen = 0.0f;
+    if (threadIdx.x == 0 && rank == 0 && in) chosen = (float)r.row.x[target];
+    Sums<ENT> own;
+    float largest = kLowest;
+    auto take = [&](auto& u) {
+      constexpr int U = sizeof(u) / sizeof(uint4);
+      own.template add<T, U>(u);
+      if (TOP) largest = fmaxf(largest, pieces_top<T, U>(u));
+    };
+    int left = r.w1 - r.w0 - (int)threadIdx.x;
+    for (int b = 0; b < batches; ++b) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+      const uint4* p = ring + stage * kUnroll * threads + threadIdx.x;
+      if (left > (kUnroll - 1) * threads) {
+        uint4 u[kUnroll];
+#pragma unroll
+        for (int i = 0; i < kUnroll; ++i) u[i] = p[i * threads];
+        take(u);
+      } else {
+        for (int l = left; l > 0; l -= threads, p += threads) {
+          const uint4 u[1] = {*p};
+          take(u);
+        }
+      }
+      left -= kUnroll * threads;
+      copy(stage);
+      if (++stage == kAhead) stage = 0;
     }
+    if (threadIdx.x == 0) {
+      for (int i = 0; i < 2; ++i) {
+        if (!(i ? r.part_after() : r.part_before())) continue;
+        const uint4 u[1] = {r.row.load_part(i ? r.w1 : r.v0)};
+        take(u);
+      }
+    }
+    own.over_warp();
+    if (lane == 0) of_warp[flip][threadIdx.x >> 5] = {own.m, own.s, own.a};
+    __syncthreads();
+    if constexpr (TOP) {
+      find_top(
+          [&](auto&& f) {
+            // out of the caches
+            const uint4* q = r.whole_pieces();
+            for (int v = r.w0 + (int)threadIdx.x; v < r.w1; v += threads) for_values(r.row, v, q[v - r.w0], f);
+            if (threadIdx.x == 0) {
+              if (r.part_before()) for_values(r.row, r.v0, r.row.load_part(r.v0), f);
+              if (r.part_after()) for_values(r.row, r.w1, r.row.load_part(r.w1), f);
+            }
+          },
+          a.top, largest, scratch);
+    }
+    if (ranks > 1) {
+      if constexpr (TOP) {
+        if ((int)threadIdx.x < a.top)
+          send(&scratch.all[flip][rank * a.top + threadIdx.x], 0, scratch.best[threadIdx.x]);
+      }
+      if (threadIdx.x == 0) send(&of_block[flip][rank], 0, join_parts<ENT>(of_warp[flip], warps));
+      cluster_done();
+    }
+    if (rank == 0 && (TOP || threadIdx.x == 0)) {
+      const Sums<ENT> all = ranks > 1 ? join_parts<ENT>(of_block[flip], (int)ranks) : join_parts<ENT>(of_warp[flip], warps);
+      const float ln_s = logf(all.s);
+      if (threadIdx.x == 0) {
+        float lp = in ? log_probability(chosen, all, ln_s) : target < 0 ? 0.0f : __uint_as_float(0x7FC00000u);
+        if (a.loss && target >= 0) lp *= -(a.weight ? a.weight[row] : a.weight_all);
+        a.logprob[row] = lp;
+        if (a.lse) a.lse[row] = all.m + ln_s;
+        if (ENT) a.entropy[row] = all.s == 0.0f ? 0.0f : ln_s - all.a * kLn2F / all.s;
+      }
+      if constexpr (TOP) write_top(a, row, ranks > 1 ? scratch.all[flip] : scratch.best, (int)ranks * a.top, all, ln_s);
+    }
+    // what a block sends for the row after next it sends after the next cluster_done(),
+    // and the first block has read this row's by then
+    flip ^= 1;
+  }
+}
+
+// ------------------------------------------------------------------ rows held on chip
+// A block, or a cluster of them each with a part of the row, copies `stages` rows
+// ahead into shared memory, every thread its own pieces to places of its own, which
+// it alone reads: for the sums, and again for the gradient, so that logits are read
+// once.  The first thread has the pieces that are part of a row at its ends.
+//
+// With two stages the next row is on its way while one is worked on, whatever the
+// barriers between its sums and its gradient: 276 us for 8192 x 50304, against 384
+// for the sums and the gradient in a kernel each.
+constexpr int kHeldUnroll = 2;
+
+template <typename T>
+__global__ __launch_bounds__(kMaxThreads) void token_loss_kernel(const __grid_constant__ Logprobs a, int64_t rows,
+                                                                int stages, int stage_pieces) {
+  cluster_begin();
+  start();
+  constexpr int kPer = RowPieces<T>::kPer;
+  extern __shared__ __align__(16) uint4 held_rows[];  // [stages][stage_pieces]
+  __shared__ Part of_warp[2][kMaxThreads / 32], of_block[2][kMaxCluster];
+  __shared__ uint4 ends[2];  // the first thread's
+  const uint32_t rank = block_rank(), ranks = cluster_blocks();
+  const int lane = threadIdx.x & 31, threads = blockDim.x, warps = threads / 32;
+  const int64_t step = gridDim.x / ranks;
+  auto share = [&](int64_t row) { return Share<T>(static_cast<const T*>(a.x) + row * a.ldx, a.vocab, rank, ranks); };
+  auto copy = [&](int64_t row, int stage) {
+    if (row < rows) {
+      const Share<T> r = share(row);
+      uint32_t to = (uint32_t)__cvta_generic_to_shared(held_rows + stage * stage_pieces + threadIdx.x);
+      const uint4* from = r.whole_pieces() + threadIdx.x;
+      for (int left = r.w1 - r.w0 - (int)threadIdx.x; left > 0; left -= threads, to += threads * 16, from += threads)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  auto read_ends = [&](int64_t row) {
+    if (row >= rows || threadIdx.x != 0) return;
+    const Share<T> r = share(row);
+    if (r.part_before()) ends[0] = r.row.load_part(r.v0);
+    if (r.part_after()) ends[1] = r.row.load_part(r.w1);
+  };
+  const int64_t first = blockIdx.x / ranks;
+  for (int s = 0; s < stages; ++s) copy(first + s * step, s);
+  read_ends(first);
+  cluster_ready();
+  int stage = 0, flip = 0;
+  for (int64_t row = first; row < rows; row += step) {
+    const Share<T> r = share(row);
+    const int64_t target = load_target(a.targets, row);
+    float w = a.weight ? a.weight[row] : a.weight_all;
+    if (stages == 2)
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+    else
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+    const uint4* mine = held_rows + stage * stage_pieces + threadIdx.x;  // every threads-th
+    const int n = r.w1 - r.w0 - (int)threadIdx.x;  // pieces from this thread's first one on
+    Sums<false> own;
+    {
+      const uint4* p = mine;
+      int left = n;
+      for (; left > (kHeldUnroll - 1) * threads; left -= kHeldUnroll * threads, p += kHeldUnroll * threads) {
+        uint4 u[kHeldUnroll];
+#pragma unroll
+        for (int i = 0; i < kHeldUnroll; ++i) u[i] = p[i * threads];
+        own.template add<T, kHeldUnroll>(u);
+      }
+      for (; left > 0; left -= threads, p += threads) {
+        const uint4 u[1] = {*p};
+        own.template add<T, 1>(u);
+      }
+      if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) {
+          const uint4 u[1] = {ends[i]};
+          if (i ? r.part_after() : r.part_before()) own.template add<T, 1>(u);
+        }
+      }
+    }
+    own.over_warp();
+    if (lane == 0) of_warp[flip][threadIdx.x >> 5] = {own.m, own.s, 0.0f};
+    __syncthreads();
+    const Part p = of_warp[flip][lane < warps ? lane : 0];
+    own.m = p.m, own.s = lane < warps ? p.s : 0.0f;
+    own.over_warp();
+    if (ranks > 1) {
+      if (threadIdx.x < ranks) send(&of_block[flip][rank], threadIdx.x, own);
+      cluster_done();
+      own = join_parts<false>(of_block[flip], (int)ranks);
+    }
+    flip ^= 1;
+    const bool none = target < 0, in = !none && target < a.vocab;
+    w = none ? 0.0f : in ? w : __uint_as_float(0x7FC00000u);
+    const float scale = own.s == 0.0f ? 0.0f * w : w / own.s;
+    T* dx = static_cast<T*>(a.dx) + row * a.lddx;
+    const uint64_t minus = pair(-own.m, -own.m), log2e = pair(kLog2eF, kLog2eF), scale2 = pair(scale, scale);
+    auto gradient = [&](const uint4& u, float (&f)[kPer]) {
+      uint64_t q[kPer / 2];
+      piece_pairs<T>(u, q);
+#pragma unroll
+      for (int k = 0; k < kPer / 2; ++k) {
+        float x, y;
+        unpair(mul2(add2(q[k], minus), log2e), x, y);
+        unpair(mul2(pair(exp2_fast(x), exp2_fast(y)), scale2), f[2 * k], f[2 * k + 1]);
+      }
+    };
+    T* o = dx + r.row.column(r.w0 + threadIdx.x);
+    const uint4* p2 = mine;
+    for (int left = n; left > 0; left -= threads, p2 += threads, o += threads * kPer) {
+      float f[kPer];
+      if (none) {
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) f[k] = 0.0f;
+      } else {
+        gradient(*p2, f);
+      }
+      if constexpr (sizeof(T) == 2)
+        store_vec<8>(o, f);
+      else
+        *reinterpret_cast<float4*>(o) = make_float4(f[0], f[1], f[2], f[3]);
+    }
+    if (threadIdx.x == 0) {
+      for (int i = 0; i < 2; ++i) {
+        if (!(i ? r.part_after() : r.part_before())) continue;
+        float f[kPer];
+        gradient(ends[i], f);
+        const int c = r.row.column(i ? r.w1 : r.v0);
+#pragma unroll
+        for (int k = 0; k < kPer; ++k)
+          if (c + k >= 0 && c + k < r.row.cols) dx[c + k] = none ? (T)0.0f : (T)f[k];
+      }
+    }
+    // the target, by the thread that has its piece (and has stored its gradient)
+    if (in) {
+      const uint32_t at = (uint32_t)target + (uint32_t)r.row.phase;
+      const int v = (int)(at / kPer), k = (int)(at % kPer);
+      const bool whole = v >= r.w0 && v < r.w1;
+      if (v >= r.v0 && v < r.v1 && (int)threadIdx.x == (whole ? (v - r.w0) & (threads - 1) : 0)) {
+        const uint4 u = whole ? mine[(v - r.w0) & -threads] : ends[v < r.w0 ? 0 : 1];
+        const uint32_t words[4] = {u.x, u.y, u.z, u.w};
+        float x = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+          if (i == k) x = __uint_as_float(sizeof(T) == 2 ? (i % 2 ? words[i / 2] & 0xFFFF0000u : words[i / 2] << 16)
+                                                         : words[i * (int)sizeof(T) / 4]);
+        const float d = log_probability(x, own, logf(own.s));
+        dx[target] = (T)(w * expm1f(d));  // p - 1 without the difference
+        a.logprob[row] = -w * d;
+      }
+    } else if (rank == 0 && threadIdx.x == 0) {
+      a.logprob[row] = w;  // 0 or NaN
+    }
+    copy(row + stages * step, stage);
+    read_ends(row + step);
+    if (++stage == stages) stage = 0;
   }
 }
 
@@ -370,6 +659,7 @@ __global__ __launch_bounds__(kThreads, 4) void logprobs_kernel(const __grid_cons
 // masked whole with the type's lowest value: lse is that value, and exp(x - lse)
 // would be 1 everywhere), so the row's sums are formed again.
 constexpr float kFarLse = 4096.0f;
+constexpr int kBwdUnroll = 4;
 
 // Such a row, by one block, which alone reads and writes it.
 template <typename T, bool ENT>
@@ -393,7 +683,7 @@ __device__ __noinline__ void far_row(const T* x, T* dx, int cols, int64_t target
   }
 }
 
-// A block takes kUnroll pieces a thread of one row, on the output's boundaries.
+// A block takes kBwdUnroll pieces a thread of one row, on the output's boundaries.
 template <typename T, bool ENT>
 __global__ __launch_bounds__(kThreads) void logprobs_bwd_kernel(const __grid_constant__ LogprobsBwd a, int chunks,
                                                                 int64_t rows) {
@@ -416,11 +706,11 @@ __global__ __launch_bounds__(kThreads) void logprobs_bwd_kernel(const __grid_con
     if (chunk == 0) far_row<T, ENT>(x, dx, (int)a.vocab, target, g, dh, h);
     return;
   }
-  const int first = chunk * (kUnroll * (int)blockDim.x) + (int)threadIdx.x;
+  const int first = chunk * (kBwdUnroll * (int)blockDim.x) + (int)threadIdx.x;
   const uint64_t minus = pair(-lse, -lse), log2e = pair(kLog2eF, kLog2eF);
-  Raw<T, kPer> u[kUnroll];
+  Raw<T, kPer> u[kBwdUnroll];
 #pragma unroll
-  for (int i = 0; i < kUnroll; ++i) {
+  for (int i = 0; i < kBwdUnroll; ++i) {
     const int v = first + i * blockDim.x, c = out.column(v);
     if (none || v >= out.pieces) {
 #pragma unroll
@@ -444,7 +734,7 @@ __global__ __launch_bounds__(kThreads) void logprobs_bwd_kernel(const __grid_con
     }
   }
 #pragma unroll
-  for (int i = 0; i < kUnroll; ++i) {
+  for (int i = 0; i < kBwdUnroll; ++i) {
     const int v = first + i * blockDim.x;
     if (v >= out.pieces) continue;
     const int c = out.column(v);
@@ -495,33 +785,71 @@ __global__ __launch_bounds__(kThreads) void logprobs_bwd_kernel(const __grid_con
 }
 
 // ------------------------------------------------------------------ launches
+// How rows are held: blocks a row, rows ahead, threads.  cluster 0: not at all.
+struct HeldPlan {
+  int cluster, stages, threads, stage_pieces;
+  int64_t groups;
+};
+constexpr int64_t kHeldBytes = 220 * 1024;  // beside what is static
+
+HeldPlan held_plan(int64_t rows, int64_t vocab, int elem) {
+  const int64_t per = 16 / elem, pieces = ceil_div(vocab + per - 1, per);
+  HeldPlan p = {};
+  for (int cluster = 1; cluster <= kMaxCluster; cluster *= 2) {
+    const int64_t part = ceil_div(pieces, cluster);
+    // few rows are spread over the SMs
+    if (cluster < kMaxCluster && rows * cluster * 2 <= sm_count() && part >= 2 * 512) continue;
+    const int threads = part >= 2048 ? 1024 : part >= 512 ? 512 : part >= 128 ? 128 : 32;
+    const int64_t stage = part * 16;
+    const int stages = 2 * stage <= kHeldBytes ? 2 : cluster == kMaxCluster && stage <= kHeldBytes ? 1 : 0;
+    if (!stages) continue;
+    p.cluster = cluster, p.stages = stages, p.threads = threads, p.stage_pieces = (int)part;
+    const int64_t fit = std::min<int64_t>(227 * 1024 / (stages * stage + 2048), 1024 / threads);
+    p.groups = std::min<int64_t>(rows, std::max<int64_t>(1, sm_count() * std::max<int64_t>(fit, 1) / cluster));
+    break;
+  }
+  return p;
+}
+// Pieces of the logits are pieces of the gradient.
+bool same_places(const void* x, int64_t ldx, const void* dx, int64_t lddx, int elem) {
+  return (reinterpret_cast<uintptr_t>(x) - reinterpret_cast<uintptr_t>(dx)) % 16 == 0 && (ldx - lddx) * elem % 16 == 0;
+}
+
 int threads_for(int64_t pieces) {
   int t = kThreads;
   while (t > 32 && pieces * 2 <= t) t /= 2;
   return t;
 }
-
+template <typename T, bool ENT, bool TOP>
+cudaError_t run_rows(const Logprobs& a, cudaStream_t st) {
+  const int64_t rows = a.targets.count, pieces = ceil_div(a.vocab + RowPieces<T>::kPer - 1, RowPieces<T>::kPer);
+  int cluster = 1;
+  while (cluster < kMaxCluster && rows * cluster * 2 <= sm_count() && pieces >= (int64_t)cluster * 2 * kThreads)
+    cluster *= 2;
+  const int64_t part = ceil_div(pieces, cluster);
+  const int threads = threads_for(ceil_div(part, kUnroll));
+  const int batches = (int)ceil_div(part, threads * kUnroll);
+  const int64_t per_sm = std::min((TOP ? kBlocksTop : kBlocks) * kThreads / threads, 32);
+  const int64_t groups = std::min<int64_t>(rows, sm_count() * per_sm / cluster);
+  auto* const kernel = logprobs_kernel<T, ENT, TOP>;
+  const int smem = kAhead * kUnroll * threads * 16;
+  if (smem > 32 * 1024) {  // with the static part, what a kernel may have unasked is 48 KB
+    const cudaError_t e = allow_smem((const void*)kernel, smem);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_kernel(kernel, (unsigned)(groups * cluster), threads, smem, cluster, st, a, rows, batches);
+}
 template <typename T>
 cudaError_t run_logprobs(const Logprobs& a, cudaStream_t st) {
-  const int64_t pieces = ceil_div(a.vocab + RowPieces<T>::kPer - 1, RowPieces<T>::kPer);
-  int cluster = 1;
-  while (cluster < kMaxCluster && a.targets.count * cluster * 2 <= sm_count() &&
-         pieces >= (int64_t)cluster * 2 * kThreads)
-    cluster *= 2;
-  const int threads = threads_for(ceil_div(pieces, cluster));
-  const int64_t grid = a.targets.count * cluster;
-  if (grid > 0x7FFFFFFF) return cudaErrorInvalidValue;
-  void (*kernel)(Logprobs) =
-      a.top ? (a.entropy ? logprobs_kernel<T, true, true> : logprobs_kernel<T, false, true>)
-            : (a.entropy ? logprobs_kernel<T, true, false> : logprobs_kernel<T, false, false>);
-  return launch_kernel(kernel, (unsigned)grid, threads, 0, cluster, st, a);
+  if (a.top) return a.entropy ? run_rows<T, true, true>(a, st) : run_rows<T, false, true>(a, st);
+  return a.entropy ? run_rows<T, true, false>(a, st) : run_rows<T, false, false>(a, st);
 }
 
 template <typename T>
 cudaError_t run_logprobs_bwd(const LogprobsBwd& a, cudaStream_t st) {
   const int64_t pieces = ceil_div(a.vocab + RowPieces<T>::kPer - 1, RowPieces<T>::kPer);
-  const int threads = threads_for(ceil_div(pieces, kUnroll));
-  const int64_t chunks = ceil_div(pieces, threads * kUnroll), grid = a.targets.count * chunks;
+  const int threads = threads_for(ceil_div(pieces, kBwdUnroll));
+  const int64_t chunks = ceil_div(pieces, threads * kBwdUnroll), grid = a.targets.count * chunks;
   if (grid > 0x7FFFFFFF) return cudaErrorInvalidValue;
   return launch_kernel(a.dentropy ? logprobs_bwd_kernel<T, true> : logprobs_bwd_kernel<T, false>, (unsigned)grid,
                        threads, 0, 0, st, a, (int)chunks, a.targets.count);
@@ -531,7 +859,19 @@ template <typename T>
 cudaError_t run_token_loss(const TokenLoss& a, cudaStream_t st) {
   Logprobs f = {};
   f.x = a.x, f.ldx = a.ldx, f.targets = a.targets, f.vocab = a.vocab;
-  f.logprob = a.loss, f.lse = a.lse, f.loss = true, f.weight = a.weight, f.weight_all = a.weight_all;
+  f.logprob = a.loss, f.loss = true, f.weight = a.weight, f.weight_all = a.weight_all;
+  if (same_places(a.x, a.ldx, a.dx, a.lddx, sizeof(T))) {
+    const HeldPlan p = held_plan(a.targets.count, a.vocab, sizeof(T));
+    if (p.cluster) {
+      f.dx = a.dx, f.lddx = a.lddx;
+      const int smem = p.stages * p.stage_pieces * 16;
+      const cudaError_t e = allow_smem((const void*)token_loss_kernel<T>, smem);
+      if (e != cudaSuccess) return e;
+      return launch_kernel(token_loss_kernel<T>, (unsigned)(p.groups * p.cluster), p.threads, smem, p.cluster, st, f,
+                           a.targets.count, p.stages, p.stage_pieces);
+    }
+  }
+  f.lse = a.lse;
   const cudaError_t e = run_logprobs<T>(f, st);
   if (e != cudaSuccess) return e;
   LogprobsBwd b = {};
@@ -549,7 +889,10 @@ cudaError_t launch_logprobs(const Logprobs& a, int dtype, cudaStream_t st) {
 cudaError_t launch_logprobs_bwd(const LogprobsBwd& a, int dtype, cudaStream_t st) {
   return dtype == SCAPE_BF16 ? run_logprobs_bwd<bf16>(a, st) : run_logprobs_bwd<float>(a, st);
 }
-bool loss_on_chip(const void*, int64_t, int, int64_t, int64_t, const void*, int64_t) { return false; }
+bool loss_on_chip(const void* x, int64_t ldx, int dtype, int64_t rows, int64_t vocab, const void* dx, int64_t lddx) {
+  const int elem = dtype == SCAPE_BF16 ? 2 : 4;
+  return held_plan(rows, vocab, elem).cluster && same_places(x, ldx, dx, lddx, elem);
+}
 cudaError_t launch_token_loss(const TokenLoss& a, int dtype, cudaStream_t st) {
   return dtype == SCAPE_BF16 ? run_token_loss<bf16>(a, st) : run_token_loss<float>(a, st);
 }

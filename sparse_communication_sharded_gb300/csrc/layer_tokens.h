@@ -53,10 +53,13 @@ struct Logprobs {
   int top;
   float *logprob, *lse, *entropy, *top_logprob;
   int64_t* top_token;
-  // a loss: logprob receives -w times it, w = weight[row] or weight_all
+  // a loss: logprob receives -w times it, w = weight[row] or weight_all, and dx (in the
+  // logits' places modulo 16 bytes), where it is given, the gradient
   bool loss;
   const float* weight;
   float weight_all;
+  void* dx;
+  int64_t lddx;
 };
 cudaError_t launch_logprobs(const Logprobs& a, int dtype, cudaStream_t st);
 

@@ -6,12 +6,15 @@ U(t): half a step of type t relative to the value.  E = 2^-24, a rounding in 32 
 An exponential 2^a in hardware is off by 2^-22 of itself, and a's roundings (the
 difference from the row's largest, its product with log2 e and that constant's own)
 by 3 E |d| more.  A thread adds up no more than vocab / 64 + 64 terms in a row, sums
-over lanes and blocks included."""
+over lanes and blocks included.  Differences may be taken from a number below the row's
+largest by ln 1024 at most (a larger term of a sum makes the kernel raise it): B = 7
+more in the size of every difference and of the logarithm of their exponentials' sum."""
 import math
 
 import torch
 
 E = 2.0 ** -24
+B = 7.0
 
 
 def U(dtype):
@@ -67,34 +70,34 @@ class Rows:
         self.entropy = torch.where(self.empty, 0.0, self.ln_s - self.pd.sum(1))
         # relative error of S
         self.chain = (self.vocab / 64 + 64) * E
-        self.ds = self.chain + 2.0 ** -22 + 3 * E * self.pd.abs().sum(1)
+        self.ds = self.chain + 2.0 ** -22 + 3 * E * (self.pd.abs().sum(1) + B)
         self.at = (torch.arange(rows, device=x.device), self.t.clamp(0, self.vocab - 1))
 
     def logprob(self):
         v = self.logp[self.at]
         v = torch.where(self.none, 0.0, torch.where(self.bad, math.nan, v))
-        tol = self.ds + 2 * E * (self.d[self.at].abs() + self.ln_s + v.abs())
+        tol = self.ds + 2 * E * (self.d[self.at].abs() + self.ln_s + 2 * B + v.abs())
         return v, torch.where(torch.isfinite(tol), tol, 0.0)
 
     def lse_and_tol(self):
-        return self.lse, torch.where(self.empty, 0.0, self.ds + 2 * E * (self.ln_s + self.lse.abs()))
+        return self.lse, torch.where(self.empty, 0.0, self.ds + 2 * E * (self.ln_s + B + self.lse.abs()))
 
     def entropy_and_tol(self):
-        a = torch.where(self.p > 0, self.p * self.d.abs() * (self.chain + 2.0 ** -22 + 4 * E * self.d.abs()), 0.0).sum(1)
+        a = torch.where(self.p > 0, self.p * (self.d.abs() + B) * (self.chain + 2.0 ** -22 + 4 * E * (self.d.abs() + B)), 0.0).sum(1)
         mean = self.pd.sum(1).abs()
-        return self.entropy, self.ds * (1 + mean) + a + 4 * E * (self.ln_s + mean)
+        return self.entropy, self.ds * (1 + mean + B) + a + 4 * E * (self.ln_s + mean + 2 * B)
 
     def top_k(self, k):
         """Columns and logits in falling order, equal ones by column."""
         value, place = torch.sort(self.x, dim=1, descending=True, stable=True)
         v = (value[:, :k] - self.top[:, None]) - self.ln_s[:, None]
-        tol = self.ds[:, None] + 2 * E * (self.d.gather(1, place[:, :k]).abs() + self.ln_s[:, None] + v.abs())
+        tol = self.ds[:, None] + 2 * E * (self.d.gather(1, place[:, :k]).abs() + self.ln_s[:, None] + 2 * B + v.abs())
         return place[:, :k], v, torch.where(torch.isfinite(tol), tol, 0.0)
 
     def gradient(self, dlogprob, dtype, entropy=None, dentropy=None, own_lse=None):
         """own_lse: the float32 log-sum-exp that the call is given (else its own sums)."""
         logp, p = self.logp, self.p
-        off = self.ds[:, None] + 3 * E * self.d.abs()
+        off = self.ds[:, None] + 3 * E * (self.d.abs() + B)
         if own_lse is not None:
             # (a number of 4096 or more has too few digits left: own sums then)
             far = (own_lse.abs() > 4096) & ~self.empty

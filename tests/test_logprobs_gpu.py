@@ -55,7 +55,7 @@ def near(got, want, tol, what=""):
 
 
 SIZES = [(1, 1), (3, 2), (5, 7), (2, 32), (9, 33), (4, 255), (300, 257), (7, 1000), (1, 32000), (40, 8191), (2, 50301),
-         (200, 4100), (1, 262147)]
+         (200, 4100), (1, 262147), (2, 1000003)]
 KINDS = ["normal", "peaked", "masked", "lowest", "equal", "rising", "large", "empty"]
 
 
