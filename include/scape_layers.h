@@ -234,6 +234,7 @@ int scape_layer_embedding_bwd(const void *dy, int64_t lddy, int dtype, const voi
  * (the last two together).
  */
 #define SCAPE_TOP_MAX 32
+#define SCAPE_TOP_VOCAB_MAX 4194304 /* columns, where alternatives are asked for */
 int scape_layer_token_logprobs(const void *logits, int64_t ldx, int dtype, const void *targets,
                                int token_bytes, int64_t rows, int64_t vocab, int top,
                                float *logprob, float *lse, float *entropy, float *top_logprob,

@@ -251,30 +251,34 @@ __device__ __forceinline__ void for_values(const RowPieces<T>& row, int v, const
 
 constexpr int kMaxThreads = 1024, kMaxCluster = 8;
 constexpr int kCandidates = 512;  // keys that pass the bound, before they are ranked
+constexpr int kMarks = 512;       // batches that hold some
 
 struct TopScratch {
   float group[32];
   uint64_t keys[kCandidates];
   uint64_t best[SCAPE_TOP_MAX];
-  uint64_t of_warp[kMaxThreads / 32];
-  int count;
-  uint64_t all[2][kMaxCluster * SCAPE_TOP_MAX];  // the cluster's, in its first block; rows in turn
+  uint64_t of_warp[32];
+  int marks[kMarks];
+  int count, marked;
+  uint64_t all[kMaxCluster * SCAPE_TOP_MAX];  // the cluster's, in its first block
 };
 // The `top` largest keys of this block's values into t.best, in falling order (0 where
 // there are fewer), from each thread's largest value.  The threads form 32 groups; the
 // top-th of the groups' largest values is a bound that at least `top` values reach
-// and, with values spread over the groups, few more, so only threads whose own largest
-// reaches it look through their values again (own_values(f) calls f(value, column)
-// for each) and collect what does.  Where that is too many (equal values) or too few
-// (NaN, -infinity), the keys are found one after the other, each the largest below
-// the last.
-template <typename V>
-__device__ __forceinline__ void find_top(V&& own_values, int top, float largest, TopScratch& t) {
+// and, with values spread over the groups, few more.  mark(bound, f) calls f(batch) for
+// the thread's batches of pieces that hold a value that reaches it; these are shared
+// out among all threads, a piece each: look(batch, piece, f) calls f(value, column).
+// Where too many values pass (equal ones) or too few (NaN, -infinity), the keys are
+// found one after the other, each the largest below the last: every(f) calls f for
+// all of the thread's values.
+template <typename M, typename L, typename V>
+__device__ __forceinline__ void find_top(M&& mark, L&& look, V&& every, int pieces, int top, float largest,
+                                         TopScratch& t) {
   const int lane = threadIdx.x & 31, threads = blockDim.x, lanes = threads / 32;
   float g = largest;
   for (int o = 1; o < lanes; o <<= 1) g = fmaxf(g, __shfl_xor_sync(kAll, g, o));
   if (threadIdx.x % lanes == 0) t.group[threadIdx.x / lanes] = g;
-  if (threadIdx.x == 0) t.count = 0;
+  if (threadIdx.x == 0) t.count = t.marked = 0;
   __syncthreads();
   g = t.group[lane];
   int rank = 0;
@@ -283,18 +287,26 @@ __device__ __forceinline__ void find_top(V&& own_values, int top, float largest,
     rank += o > g || (o == g && i < lane);
   }
   const float bound = __shfl_sync(kAll, g, __ffs(__ballot_sync(kAll, rank == top - 1)) - 1);
-  if (largest >= bound) {
-    own_values([&](float x, int c) {
-      if (x >= bound) {
-        const int at = atomicAdd(&t.count, 1);  // their order changes nothing: keys differ
-        if (at < kCandidates) t.keys[at] = key_of(x, c);
-      }
+  // the order of marks and keys changes nothing: keys differ and are ranked
+  if (largest >= bound)
+    mark(bound, [&](int batch) {
+      const int at = atomicAdd(&t.marked, 1);
+      if (at < kMarks) t.marks[at] = batch;
     });
-  }
+  __syncthreads();
+  const int marked = t.marked;
+  if (marked <= kMarks)
+    for (int i = threadIdx.x; i < marked * pieces; i += threads)
+      look(t.marks[i / pieces], i % pieces, [&](float x, int c) {
+        if (x >= bound) {
+          const int at = atomicAdd(&t.count, 1);
+          if (at < kCandidates) t.keys[at] = key_of(x, c);
+        }
+      });
   if (threadIdx.x < SCAPE_TOP_MAX) t.best[threadIdx.x] = 0;
   __syncthreads();
   const int n = t.count;
-  if (n >= top && n <= kCandidates) {
+  if (marked <= kMarks && n >= top && n <= kCandidates) {
     for (int i = threadIdx.x; i < n; i += threads) {
       const uint64_t k = t.keys[i];
       int r = 0;
@@ -305,7 +317,7 @@ __device__ __forceinline__ void find_top(V&& own_values, int top, float largest,
     uint64_t last = ~0ull;
     for (int j = 0; j < top; ++j) {
       uint64_t k = 0;
-      own_values([&](float x, int c) {
+      every([&](float x, int c) {
         const uint64_t q = key_of(x, c);
         if (q < last && q > k) k = q;
       });
@@ -362,295 +374,269 @@ struct Share {
 };
 
 // ------------------------------------------------------------------ forward
-// Blocks of up to 256 threads, several an SM, go through rows, every thread with a ring
-// of its own pieces in shared memory that runs ahead across rows: while a row's sums
-// are joined the next one's pieces arrive.  A cluster of blocks shares a row where
-// there are few.
-//
-// 8192 x 32000 in bfloat16 with entropy: pieces read into registers 105 us, four blocks
-// an SM; rows held whole, one block of 1024 threads an SM, 181.
-constexpr int kThreads = 256, kUnroll = 4, kAhead = 3;
-constexpr int kBlocks = 4, kBlocksTop = 3;  // an SM
+// A block, or a cluster of them each with a part of the row, takes one row; every
+// thread has a ring of its own pieces in shared memory, kAhead batches deep, and waits
+// for nothing but its own copies until the threads' sums are joined.  Seven blocks of
+// 128 threads an SM, so that others read meanwhile (8192 x 32000 in bfloat16 with
+// entropy: 84 us, 92% of the copy rate; blocks that go from row to row 88, four of 256
+// threads 103, pieces read into registers 105).  Six with alternatives, whose search
+// takes more registers (4096 x 32000 with five: 64 us, three of 256 threads 88, without
+// alternatives 44).
+constexpr int kTeam = 128, kUnroll = 4, kAhead = 3;
+constexpr int kBlocks = 7, kBlocksTop = 6;  // an SM
 
 template <typename T, bool ENT, bool TOP>
-__global__ __launch_bounds__(kThreads, TOP ? kBlocksTop : kBlocks) void logprobs_kernel(const __grid_constant__ Logprobs a,
-                                                                         int64_t rows, int batches) {
+__global__ __launch_bounds__(kTeam, TOP ? kBlocksTop : kBlocks) void logprobs_kernel(
+    const __grid_constant__ Logprobs a, int batches) {
   cluster_begin();
   start();
   extern __shared__ __align__(16) uint4 ring[];  // [kAhead][kUnroll][threads]
-  __shared__ Part of_warp[2][kThreads / 32], of_block[2][kMaxCluster];
+  // and, for the alternatives, each batch's largest value: the thread's own, every
+  // threads-th
+  float* const tops = reinterpret_cast<float*>(ring + kAhead * kUnroll * blockDim.x) + threadIdx.x;
+  __shared__ Part of_warp[kTeam / 32], of_block[kMaxCluster];
   __shared__ std::conditional_t<TOP, TopScratch, int> scratch;
   const uint32_t rank = block_rank(), ranks = cluster_blocks();
   const int lane = threadIdx.x & 31, threads = blockDim.x, warps = threads / 32;
-  const int64_t step = gridDim.x / ranks;
-  auto share = [&](int64_t row) { return Share<T>(static_cast<const T*>(a.x) + row * a.ldx, a.vocab, rank, ranks); };
-  // what the ring is to be given next
-  int64_t row_ahead = blockIdx.x / ranks;
-  int batch_ahead = 0, left_ahead = 0;
-  const uint4* from = nullptr;
-  auto begin_row = [&]() {
-    if (row_ahead >= rows) return;
-    const Share<T> r = share(row_ahead);
-    from = r.whole_pieces() + threadIdx.x;
-    left_ahead = r.w1 - r.w0 - (int)threadIdx.x;
-  };
-  begin_row();
+  const int64_t row = blockIdx.x / ranks;
+  const Share<T> r(static_cast<const T*>(a.x) + row * a.ldx, a.vocab, rank, ranks);
+  const uint4* const whole = r.whole_pieces();
+  const int n = r.w1 - r.w0;
   const uint32_t own_ring = (uint32_t)__cvta_generic_to_shared(ring + threadIdx.x);
+  int ahead = (int)threadIdx.x;  // the piece that the ring is to be given next
   auto copy = [&](int stage) {
-    if (row_ahead < rows) {
 #pragma unroll
-      for (int i = 0; i < kUnroll; ++i)
-        if (left_ahead > i * threads)
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(own_ring + (stage * kUnroll + i) * threads * 16),
-                       "l"(from + i * threads)
-                       : "memory");
-      from += kUnroll * threads;
-      left_ahead -= kUnroll * threads;
-      if (++batch_ahead == batches) {
-        batch_ahead = 0;
-        row_ahead += step;
-        begin_row();
-      }
-    }
+    for (int i = 0; i < kUnroll; ++i)
+      if (ahead + i * threads < n)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(own_ring + (stage * kUnroll + i) * threads * 16),
+                     "l"(whole + ahead + i * threads)
+                     : "memory");
+    ahead += kUnroll * threads;
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
 #pragma unroll
   for (int s = 0; s < kAhead; ++s) copy(s);
-  cluster_ready();
-  int stage = 0, flip = 0;
-  for (int64_t row = blockIdx.x / ranks; row < rows; row += step) {
-    const Share<T> r = share(row);
-    const int64_t target = load_target(a.targets, row);
-    const bool in = target >= 0 && target < a.vocab;
-    float chosen = 0.0f;
-    if (threadIdx.x == 0 && rank == 0 && in) chosen = (float)r.row.x[target];
-    Sums<ENT> own;
-    float largest = kLowest;
-    auto take = [&](auto& u) {
-      constexpr int U = sizeof(u) / sizeof(uint4);
-      own.template add<T, U>(u);
-      if (TOP) largest = fmaxf(largest, pieces_top<T, U>(u));
-    };
-    int left = r.w1 - r.w0 - (int)threadIdx.x;
-    for (int b = 0; b < batches; ++b) {
-      asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
-      const uint4* p = ring + stage * kUnroll * threads + threadIdx.x;
-      if (left > (kUnroll - 1) * threads) {
-        uint4 u[kUnroll];
+  const int64_t target = load_target(a.targets, row);
+  const bool in = target >= 0 && target < a.vocab;
+  float chosen = 0.0f;
+  if (threadIdx.x == 0 && rank == 0 && in) chosen = (float)r.row.x[target];
+  Sums<ENT> own;
+  float largest = kLowest, batch_top;
+  auto take = [&](auto& u) {
+    constexpr int U = sizeof(u) / sizeof(uint4);
+    own.template add<T, U>(u);
+    if (TOP) batch_top = fmaxf(batch_top, pieces_top<T, U>(u));
+  };
+  int stage = 0, left = n - (int)threadIdx.x;
+  for (int b = 0; b < batches; ++b) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+    const uint4* p = ring + stage * kUnroll * threads + threadIdx.x;
+    batch_top = kLowest;
+    if (left > (kUnroll - 1) * threads) {
+      uint4 u[kUnroll];
 #pragma unroll
-        for (int i = 0; i < kUnroll; ++i) u[i] = p[i * threads];
-        take(u);
-      } else {
-        for (int l = left; l > 0; l -= threads, p += threads) {
-          const uint4 u[1] = {*p};
-          take(u);
-        }
-      }
-      left -= kUnroll * threads;
-      copy(stage);
-      if (++stage == kAhead) stage = 0;
-    }
-    if (threadIdx.x == 0) {
-      for (int i = 0; i < 2; ++i) {
-        if (!(i ? r.part_after() : r.part_before())) continue;
-        const uint4 u[1] = {r.row.load_part(i ? r.w1 : r.v0)};
+      for (int i = 0; i < kUnroll; ++i) u[i] = p[i * threads];
+      take(u);
+    } else {
+      for (int l = left; l > 0; l -= threads, p += threads) {
+        const uint4 u[1] = {*p};
         take(u);
       }
     }
-    own.over_warp();
-    if (lane == 0) of_warp[flip][threadIdx.x >> 5] = {own.m, own.s, own.a};
-    __syncthreads();
-    if constexpr (TOP) {
-      find_top(
-          [&](auto&& f) {
-            // out of the caches
-            const uint4* q = r.whole_pieces();
-            for (int v = r.w0 + (int)threadIdx.x; v < r.w1; v += threads) for_values(r.row, v, q[v - r.w0], f);
-            if (threadIdx.x == 0) {
-              if (r.part_before()) for_values(r.row, r.v0, r.row.load_part(r.v0), f);
-              if (r.part_after()) for_values(r.row, r.w1, r.row.load_part(r.w1), f);
-            }
-          },
-          a.top, largest, scratch);
-    }
-    if (ranks > 1) {
-      if constexpr (TOP) {
-        if ((int)threadIdx.x < a.top)
-          send(&scratch.all[flip][rank * a.top + threadIdx.x], 0, scratch.best[threadIdx.x]);
-      }
-      if (threadIdx.x == 0) send(&of_block[flip][rank], 0, join_parts<ENT>(of_warp[flip], warps));
-      cluster_done();
-    }
-    if (rank == 0 && (TOP || threadIdx.x == 0)) {
-      const Sums<ENT> all = ranks > 1 ? join_parts<ENT>(of_block[flip], (int)ranks) : join_parts<ENT>(of_warp[flip], warps);
-      const float ln_s = logf(all.s);
-      if (threadIdx.x == 0) {
-        float lp = in ? log_probability(chosen, all, ln_s) : target < 0 ? 0.0f : __uint_as_float(0x7FC00000u);
-        if (a.loss && target >= 0) lp *= -(a.weight ? a.weight[row] : a.weight_all);
-        a.logprob[row] = lp;
-        if (a.lse) a.lse[row] = all.m + ln_s;
-        if (ENT) a.entropy[row] = all.s == 0.0f ? 0.0f : ln_s - all.a * kLn2F / all.s;
-      }
-      if constexpr (TOP) write_top(a, row, ranks > 1 ? scratch.all[flip] : scratch.best, (int)ranks * a.top, all, ln_s);
-    }
-    // what a block sends for the row after next it sends after the next cluster_done(),
-    // and the first block has read this row's by then
-    flip ^= 1;
+    if (TOP) tops[b * threads] = batch_top, largest = fmaxf(largest, batch_top);
+    left -= kUnroll * threads;
+    copy(stage);
+    if (++stage == kAhead) stage = 0;
   }
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      if (!(i ? r.part_after() : r.part_before())) continue;
+      const uint4 u[1] = {r.row.load_part(i ? r.w1 : r.v0)};
+      take(u);
+      if (TOP) largest = fmaxf(largest, batch_top);
+    }
+  }
+  own.over_warp();
+  if (lane == 0) of_warp[threadIdx.x >> 5] = {own.m, own.s, own.a};
+  __syncthreads();
+  cluster_ready();
+  if constexpr (TOP) {
+    find_top(
+        [&](float bound, auto&& f) {
+          for (int b = 0; b < batches; ++b)
+            if (tops[b * threads] >= bound) f(b * threads + (int)threadIdx.x);
+          if (threadIdx.x == 0 && (r.part_before() || r.part_after())) f(-1);
+        },
+        [&](int batch, int piece, auto&& f) {  // out of the caches
+          if (batch < 0) {
+            if (piece == 0 && r.part_before()) for_values(r.row, r.v0, r.row.load_part(r.v0), f);
+            if (piece == 1 && r.part_after()) for_values(r.row, r.w1, r.row.load_part(r.w1), f);
+            return;
+          }
+          const int v = batch / threads * (kUnroll * threads) + batch % threads + piece * threads;
+          if (v < n) for_values(r.row, r.w0 + v, whole[v], f);
+        },
+        [&](auto&& f) {
+          for (int v = (int)threadIdx.x; v < n; v += threads) for_values(r.row, r.w0 + v, whole[v], f);
+          if (threadIdx.x != 0) return;
+          if (r.part_before()) for_values(r.row, r.v0, r.row.load_part(r.v0), f);
+          if (r.part_after()) for_values(r.row, r.w1, r.row.load_part(r.w1), f);
+        },
+        kUnroll, a.top, largest, scratch);
+  }
+  if (ranks > 1) {
+    if constexpr (TOP) {
+      if ((int)threadIdx.x < a.top) send(&scratch.all[rank * a.top + threadIdx.x], 0, scratch.best[threadIdx.x]);
+    }
+    if (threadIdx.x == 0) send(&of_block[rank], 0, join_parts<ENT>(of_warp, warps));
+    cluster_done();
+  }
+  if (rank != 0 || (!TOP && threadIdx.x != 0)) return;
+  const Sums<ENT> all = ranks > 1 ? join_parts<ENT>(of_block, (int)ranks) : join_parts<ENT>(of_warp, warps);
+  const float ln_s = logf(all.s);
+  if (threadIdx.x == 0) {
+    float lp = in ? log_probability(chosen, all, ln_s) : target < 0 ? 0.0f : __uint_as_float(0x7FC00000u);
+    if (a.loss && target >= 0) lp *= -(a.weight ? a.weight[row] : a.weight_all);
+    a.logprob[row] = lp;
+    if (a.lse) a.lse[row] = all.m + ln_s;
+    if (ENT) a.entropy[row] = all.s == 0.0f ? 0.0f : ln_s - all.a * kLn2F / all.s;
+  }
+  if constexpr (TOP) write_top(a, row, ranks > 1 ? scratch.all : scratch.best, (int)ranks * a.top, all, ln_s);
 }
 
-// ------------------------------------------------------------------ rows held on chip
-// A block, or a cluster of them each with a part of the row, copies `stages` rows
-// ahead into shared memory, every thread its own pieces to places of its own, which
-// it alone reads: for the sums, and again for the gradient, so that logits are read
-// once.  The first thread has the pieces that are part of a row at its ends.
-//
-// With two stages the next row is on its way while one is worked on, whatever the
-// barriers between its sums and its gradient: 276 us for 8192 x 50304, against 384
-// for the sums and the gradient in a kernel each.
-constexpr int kHeldUnroll = 2;
-
+// ------------------------------------------------------------------ loss
+// The row stays in shared memory between its sums and its gradient, so logits are
+// read once.  A block, or a cluster of them each with a part of the row, takes one
+// row; every thread copies its own pieces to places of its own, which it alone reads.
+// Two or more blocks an SM and no more than a row's life for each: while some wait
+// for their row or their barrier others compute or store, and none waits for the
+// slowest.  (8192 x 50304 in bfloat16: 238 us, what a copy of as many bytes takes; as
+// many blocks as fit, going from row to row, 255; one block an SM with the next row on
+// its way 277; sums and gradient in a kernel each 384.)
 template <typename T>
-__global__ __launch_bounds__(kMaxThreads) void token_loss_kernel(const __grid_constant__ Logprobs a, int64_t rows,
-                                                                int stages, int stage_pieces) {
+__global__ __launch_bounds__(kMaxThreads) void token_loss_kernel(const __grid_constant__ Logprobs a) {
   cluster_begin();
   start();
-  constexpr int kPer = RowPieces<T>::kPer;
-  extern __shared__ __align__(16) uint4 held_rows[];  // [stages][stage_pieces]
-  __shared__ Part of_warp[2][kMaxThreads / 32], of_block[2][kMaxCluster];
-  __shared__ uint4 ends[2];  // the first thread's
+  constexpr int kPer = RowPieces<T>::kPer, kHeldUnroll = 2;
+  extern __shared__ __align__(16) uint4 held[];  // the block's pieces
+  __shared__ Part of_warp[kMaxThreads / 32], of_block[kMaxCluster];
   const uint32_t rank = block_rank(), ranks = cluster_blocks();
   const int lane = threadIdx.x & 31, threads = blockDim.x, warps = threads / 32;
-  const int64_t step = gridDim.x / ranks;
-  auto share = [&](int64_t row) { return Share<T>(static_cast<const T*>(a.x) + row * a.ldx, a.vocab, rank, ranks); };
-  auto copy = [&](int64_t row, int stage) {
-    if (row < rows) {
-      const Share<T> r = share(row);
-      uint32_t to = (uint32_t)__cvta_generic_to_shared(held_rows + stage * stage_pieces + threadIdx.x);
-      const uint4* from = r.whole_pieces() + threadIdx.x;
-      for (int left = r.w1 - r.w0 - (int)threadIdx.x; left > 0; left -= threads, to += threads * 16, from += threads)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
-    }
+  const int64_t row = blockIdx.x / ranks;
+  const Share<T> r(static_cast<const T*>(a.x) + row * a.ldx, a.vocab, rank, ranks);
+  const int n = r.w1 - r.w0 - (int)threadIdx.x;  // pieces from this thread's first one on
+  uint4* const mine = held + threadIdx.x;        // every threads-th
+  {
+    uint32_t to = (uint32_t)__cvta_generic_to_shared(mine);
+    const uint4* from = r.whole_pieces() + threadIdx.x;
+    for (int left = n; left > 0; left -= threads, to += threads * 16, from += threads)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
     asm volatile("cp.async.commit_group;" ::: "memory");
-  };
-  auto read_ends = [&](int64_t row) {
-    if (row >= rows || threadIdx.x != 0) return;
-    const Share<T> r = share(row);
+  }
+  // the pieces that are part of a row at its ends are the first thread's
+  __shared__ uint4 ends[2];
+  if (threadIdx.x == 0) {
     if (r.part_before()) ends[0] = r.row.load_part(r.v0);
     if (r.part_after()) ends[1] = r.row.load_part(r.w1);
-  };
-  const int64_t first = blockIdx.x / ranks;
-  for (int s = 0; s < stages; ++s) copy(first + s * step, s);
-  read_ends(first);
+  }
+  const int64_t target = load_target(a.targets, row);
+  float w = a.weight ? a.weight[row] : a.weight_all;
   cluster_ready();
-  int stage = 0, flip = 0;
-  for (int64_t row = first; row < rows; row += step) {
-    const Share<T> r = share(row);
-    const int64_t target = load_target(a.targets, row);
-    float w = a.weight ? a.weight[row] : a.weight_all;
-    if (stages == 2)
-      asm volatile("cp.async.wait_group 1;" ::: "memory");
-    else
-      asm volatile("cp.async.wait_group 0;" ::: "memory");
-    const uint4* mine = held_rows + stage * stage_pieces + threadIdx.x;  // every threads-th
-    const int n = r.w1 - r.w0 - (int)threadIdx.x;  // pieces from this thread's first one on
-    Sums<false> own;
-    {
-      const uint4* p = mine;
-      int left = n;
-      for (; left > (kHeldUnroll - 1) * threads; left -= kHeldUnroll * threads, p += kHeldUnroll * threads) {
-        uint4 u[kHeldUnroll];
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  Sums<false> own;
+  {
+    const uint4* p = mine;
+    int left = n;
+    for (; left > (kHeldUnroll - 1) * threads; left -= kHeldUnroll * threads, p += kHeldUnroll * threads) {
+      uint4 u[kHeldUnroll];
 #pragma unroll
-        for (int i = 0; i < kHeldUnroll; ++i) u[i] = p[i * threads];
-        own.template add<T, kHeldUnroll>(u);
-      }
-      for (; left > 0; left -= threads, p += threads) {
-        const uint4 u[1] = {*p};
-        own.template add<T, 1>(u);
-      }
-      if (threadIdx.x == 0) {
-        for (int i = 0; i < 2; ++i) {
-          const uint4 u[1] = {ends[i]};
-          if (i ? r.part_after() : r.part_before()) own.template add<T, 1>(u);
-        }
-      }
+      for (int i = 0; i < kHeldUnroll; ++i) u[i] = p[i * threads];
+      own.template add<T, kHeldUnroll>(u);
     }
-    own.over_warp();
-    if (lane == 0) of_warp[flip][threadIdx.x >> 5] = {own.m, own.s, 0.0f};
-    __syncthreads();
-    const Part p = of_warp[flip][lane < warps ? lane : 0];
-    own.m = p.m, own.s = lane < warps ? p.s : 0.0f;
-    own.over_warp();
-    if (ranks > 1) {
-      if (threadIdx.x < ranks) send(&of_block[flip][rank], threadIdx.x, own);
-      cluster_done();
-      own = join_parts<false>(of_block[flip], (int)ranks);
-    }
-    flip ^= 1;
-    const bool none = target < 0, in = !none && target < a.vocab;
-    w = none ? 0.0f : in ? w : __uint_as_float(0x7FC00000u);
-    const float scale = own.s == 0.0f ? 0.0f * w : w / own.s;
-    T* dx = static_cast<T*>(a.dx) + row * a.lddx;
-    const uint64_t minus = pair(-own.m, -own.m), log2e = pair(kLog2eF, kLog2eF), scale2 = pair(scale, scale);
-    auto gradient = [&](const uint4& u, float (&f)[kPer]) {
-      uint64_t q[kPer / 2];
-      piece_pairs<T>(u, q);
-#pragma unroll
-      for (int k = 0; k < kPer / 2; ++k) {
-        float x, y;
-        unpair(mul2(add2(q[k], minus), log2e), x, y);
-        unpair(mul2(pair(exp2_fast(x), exp2_fast(y)), scale2), f[2 * k], f[2 * k + 1]);
-      }
-    };
-    T* o = dx + r.row.column(r.w0 + threadIdx.x);
-    const uint4* p2 = mine;
-    for (int left = n; left > 0; left -= threads, p2 += threads, o += threads * kPer) {
-      float f[kPer];
-      if (none) {
-#pragma unroll
-        for (int k = 0; k < kPer; ++k) f[k] = 0.0f;
-      } else {
-        gradient(*p2, f);
-      }
-      if constexpr (sizeof(T) == 2)
-        store_vec<8>(o, f);
-      else
-        *reinterpret_cast<float4*>(o) = make_float4(f[0], f[1], f[2], f[3]);
+    for (; left > 0; left -= threads, p += threads) {
+      const uint4 u[1] = {*p};
+      own.template add<T, 1>(u);
     }
     if (threadIdx.x == 0) {
       for (int i = 0; i < 2; ++i) {
-        if (!(i ? r.part_after() : r.part_before())) continue;
-        float f[kPer];
-        gradient(ends[i], f);
-        const int c = r.row.column(i ? r.w1 : r.v0);
-#pragma unroll
-        for (int k = 0; k < kPer; ++k)
-          if (c + k >= 0 && c + k < r.row.cols) dx[c + k] = none ? (T)0.0f : (T)f[k];
+        const uint4 u[1] = {ends[i]};
+        if (i ? r.part_after() : r.part_before()) own.template add<T, 1>(u);
       }
     }
-    // the target, by the thread that has its piece (and has stored its gradient)
-    if (in) {
-      const uint32_t at = (uint32_t)target + (uint32_t)r.row.phase;
-      const int v = (int)(at / kPer), k = (int)(at % kPer);
-      const bool whole = v >= r.w0 && v < r.w1;
-      if (v >= r.v0 && v < r.v1 && (int)threadIdx.x == (whole ? (v - r.w0) & (threads - 1) : 0)) {
-        const uint4 u = whole ? mine[(v - r.w0) & -threads] : ends[v < r.w0 ? 0 : 1];
-        const uint32_t words[4] = {u.x, u.y, u.z, u.w};
-        float x = 0.0f;
+  }
+  own.over_warp();
+  if (warps > 1) {
+    if (lane == 0) of_warp[threadIdx.x >> 5] = {own.m, own.s, 0.0f};
+    __syncthreads();
+    const Part p = of_warp[lane < warps ? lane : 0];
+    own.m = p.m, own.s = lane < warps ? p.s : 0.0f;
+    own.over_warp();
+  }
+  if (ranks > 1) {
+    if (threadIdx.x < ranks) send(&of_block[rank], threadIdx.x, own);
+    cluster_done();
+    own = join_parts<false>(of_block, (int)ranks);
+  }
+  const bool none = target < 0, in = !none && target < a.vocab;
+  w = none ? 0.0f : in ? w : __uint_as_float(0x7FC00000u);
+  const float scale = own.s == 0.0f ? 0.0f * w : w / own.s;
+  T* dx = static_cast<T*>(a.dx) + row * a.lddx;
+  const uint64_t minus = pair(-own.m, -own.m), log2e = pair(kLog2eF, kLog2eF), scale2 = pair(scale, scale);
+  auto gradient = [&](const uint4& u, float (&f)[kPer]) {
+    uint64_t q[kPer / 2];
+    piece_pairs<T>(u, q);
 #pragma unroll
-        for (int i = 0; i < kPer; ++i)
-          if (i == k) x = __uint_as_float(sizeof(T) == 2 ? (i % 2 ? words[i / 2] & 0xFFFF0000u : words[i / 2] << 16)
-                                                         : words[i * (int)sizeof(T) / 4]);
-        const float d = log_probability(x, own, logf(own.s));
-        dx[target] = (T)(w * expm1f(d));  // p - 1 without the difference
-        a.logprob[row] = -w * d;
-      }
-    } else if (rank == 0 && threadIdx.x == 0) {
-      a.logprob[row] = w;  // 0 or NaN
+    for (int k = 0; k < kPer / 2; ++k) {
+      float x, y;
+      unpair(mul2(add2(q[k], minus), log2e), x, y);
+      unpair(mul2(pair(exp2_fast(x), exp2_fast(y)), scale2), f[2 * k], f[2 * k + 1]);
     }
-    copy(row + stages * step, stage);
-    read_ends(row + step);
-    if (++stage == stages) stage = 0;
+  };
+  T* o = dx + r.row.column(r.w0 + threadIdx.x);
+  const uint4* p = mine;
+  for (int left = n; left > 0; left -= threads, p += threads, o += threads * kPer) {
+    float f[kPer];
+    if (none) {
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) f[k] = 0.0f;
+    } else {
+      gradient(*p, f);
+    }
+    if constexpr (sizeof(T) == 2)
+      store_vec<8>(o, f);
+    else
+      *reinterpret_cast<float4*>(o) = make_float4(f[0], f[1], f[2], f[3]);
+  }
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      if (!(i ? r.part_after() : r.part_before())) continue;
+      float f[kPer];
+      gradient(ends[i], f);
+      const int c = r.row.column(i ? r.w1 : r.v0);
+#pragma unroll
+      for (int k = 0; k < kPer; ++k)
+        if (c + k >= 0 && c + k < r.row.cols) dx[c + k] = none ? (T)0.0f : (T)f[k];
+    }
+  }
+  // the target, by the thread that has its piece (and has stored its gradient)
+  if (in) {
+    const uint32_t at = (uint32_t)target + (uint32_t)r.row.phase;
+    const int v = (int)(at / kPer), k = (int)(at % kPer);
+    const bool whole = v >= r.w0 && v < r.w1;
+    if (v >= r.v0 && v < r.v1 && (int)threadIdx.x == (whole ? (v - r.w0) & (threads - 1) : 0)) {
+      const uint4 u = whole ? mine[(v - r.w0) & -threads] : ends[v < r.w0 ? 0 : 1];
+      const uint32_t words[4] = {u.x, u.y, u.z, u.w};
+      float x = 0.0f;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        if (i == k) x = __uint_as_float(sizeof(T) == 2 ? (i % 2 ? words[i / 2] & 0xFFFF0000u : words[i / 2] << 16)
+                                                       : words[i * (int)sizeof(T) / 4]);
+      const float d = log_probability(x, own, logf(own.s));
+      dx[target] = (T)(w * expm1f(d));  // p - 1 without the difference
+      a.logprob[row] = -w * d;
+    }
+  } else if (rank == 0 && threadIdx.x == 0) {
+    a.logprob[row] = w;  // 0 or NaN
   }
 }
 
@@ -659,12 +645,12 @@ __global__ __launch_bounds__(kMaxThreads) void token_loss_kernel(const __grid_co
 // masked whole with the type's lowest value: lse is that value, and exp(x - lse)
 // would be 1 everywhere), so the row's sums are formed again.
 constexpr float kFarLse = 4096.0f;
-constexpr int kBwdUnroll = 4;
+constexpr int kBwdThreads = 256, kBwdUnroll = 4;
 
 // Such a row, by one block, which alone reads and writes it.
 template <typename T, bool ENT>
 __device__ __noinline__ void far_row(const T* x, T* dx, int cols, int64_t target, float g, float dh, float h) {
-  __shared__ Part part[kThreads / 32];
+  __shared__ Part part[kBwdThreads / 32];
   float top = kLowest, s = 0.0f;
   for (int c = threadIdx.x; c < cols; c += blockDim.x) top = fmaxf(top, (float)x[c]);
   for (int c = threadIdx.x; c < cols; c += blockDim.x) s += exp2_fast(((float)x[c] - top) * kLog2eF);
@@ -685,7 +671,7 @@ __device__ __noinline__ void far_row(const T* x, T* dx, int cols, int64_t target
 
 // A block takes kBwdUnroll pieces a thread of one row, on the output's boundaries.
 template <typename T, bool ENT>
-__global__ __launch_bounds__(kThreads) void logprobs_bwd_kernel(const __grid_constant__ LogprobsBwd a, int chunks,
+__global__ __launch_bounds__(kBwdThreads) void logprobs_bwd_kernel(const __grid_constant__ LogprobsBwd a, int chunks,
                                                                 int64_t rows) {
   start();
   constexpr int kPer = RowPieces<T>::kPer;
@@ -785,59 +771,64 @@ __global__ __launch_bounds__(kThreads) void logprobs_bwd_kernel(const __grid_con
 }
 
 // ------------------------------------------------------------------ launches
-// How rows are held: blocks a row, rows ahead, threads.  cluster 0: not at all.
+// How rows are held: blocks a row, threads and pieces a block.  cluster 0: not at all.
 struct HeldPlan {
-  int cluster, stages, threads, stage_pieces;
-  int64_t groups;
+  int cluster, threads, pieces;
 };
-constexpr int64_t kHeldBytes = 220 * 1024;  // beside what is static
+constexpr int64_t kSmBytes = 227 * 1024, kTopBytes = 211 * 1024;
 
 HeldPlan held_plan(int64_t rows, int64_t vocab, int elem) {
   const int64_t per = 16 / elem, pieces = ceil_div(vocab + per - 1, per);
-  HeldPlan p = {};
   for (int cluster = 1; cluster <= kMaxCluster; cluster *= 2) {
-    const int64_t part = ceil_div(pieces, cluster);
-    // few rows are spread over the SMs
-    if (cluster < kMaxCluster && rows * cluster * 2 <= sm_count() && part >= 2 * 512) continue;
-    const int threads = part >= 2048 ? 1024 : part >= 512 ? 512 : part >= 128 ? 128 : 32;
-    const int64_t stage = part * 16;
-    const int stages = 2 * stage <= kHeldBytes ? 2 : cluster == kMaxCluster && stage <= kHeldBytes ? 1 : 0;
-    if (!stages) continue;
-    p.cluster = cluster, p.stages = stages, p.threads = threads, p.stage_pieces = (int)part;
-    const int64_t fit = std::min<int64_t>(227 * 1024 / (stages * stage + 2048), 1024 / threads);
-    p.groups = std::min<int64_t>(rows, std::max<int64_t>(1, sm_count() * std::max<int64_t>(fit, 1) / cluster));
-    break;
+    const int64_t part = ceil_div(pieces, cluster), fit = kSmBytes / (part * 16 + 2048);
+    // few rows are spread over the SMs; two blocks or more an SM
+    if (cluster < kMaxCluster && ((rows * cluster * 2 <= sm_count() && part >= 2 * 512) || fit < 2)) continue;
+    if (fit < 1) break;
+    const int most = fit == 1 ? 1024 : fit == 2 ? 512 : fit == 3 ? 256 : 128;
+    int threads = 32;
+    while (threads < most && part >= 4 * threads) threads *= 2;
+    return {cluster, threads, (int)part};
   }
-  return p;
+  return {};
 }
 // Pieces of the logits are pieces of the gradient.
 bool same_places(const void* x, int64_t ldx, const void* dx, int64_t lddx, int elem) {
   return (reinterpret_cast<uintptr_t>(x) - reinterpret_cast<uintptr_t>(dx)) % 16 == 0 && (ldx - lddx) * elem % 16 == 0;
 }
 
-int threads_for(int64_t pieces) {
-  int t = kThreads;
+int threads_for(int64_t pieces, int most) {
+  int t = most;
   while (t > 32 && pieces * 2 <= t) t /= 2;
   return t;
 }
 template <typename T, bool ENT, bool TOP>
 cudaError_t run_rows(const Logprobs& a, cudaStream_t st) {
   const int64_t rows = a.targets.count, pieces = ceil_div(a.vocab + RowPieces<T>::kPer - 1, RowPieces<T>::kPer);
-  int cluster = 1;
-  while (cluster < kMaxCluster && rows * cluster * 2 <= sm_count() && pieces >= (int64_t)cluster * 2 * kThreads)
-    cluster *= 2;
-  const int64_t part = ceil_div(pieces, cluster);
-  const int threads = threads_for(ceil_div(part, kUnroll));
-  const int batches = (int)ceil_div(part, threads * kUnroll);
-  const int64_t per_sm = std::min((TOP ? kBlocksTop : kBlocks) * kThreads / threads, 32);
-  const int64_t groups = std::min<int64_t>(rows, sm_count() * per_sm / cluster);
+  // As many blocks a row as make the least of the rounds of blocks times a block's
+  // batches, of which joining the sums is worth two and looking for alternatives four
+  // more.
+  int cluster = 0, threads = 0, smem = 0;
+  int64_t batches = 0, least = 0;
+  for (int c = 1; c <= kMaxCluster; c *= 2) {
+    const int64_t part = ceil_div(pieces, c);
+    const int t = threads_for(ceil_div(part, kUnroll), kTeam);
+    const int64_t n = ceil_div(part, t * kUnroll);
+    const int64_t bytes = (int64_t)kAhead * kUnroll * t * 16 + (TOP ? n * t * 4 : 0);
+    if (bytes > kTopBytes) continue;
+    const int64_t per_sm = std::min<int64_t>(std::min((TOP ? kBlocksTop : kBlocks) * kTeam / t, 32),
+                                             kSmBytes / (bytes + (TOP ? 12800 : 2048)));
+    const int64_t cost = ceil_div(rows * c, sm_count() * per_sm) * (n + (TOP ? 6 : 2));
+    if (cluster && cost >= least) continue;
+    cluster = c, threads = t, batches = n, smem = (int)bytes, least = cost;
+  }
+  if (!cluster || rows * cluster > 0x7FFFFFFF) return cudaErrorInvalidValue;
   auto* const kernel = logprobs_kernel<T, ENT, TOP>;
-  const int smem = kAhead * kUnroll * threads * 16;
   if (smem > 32 * 1024) {  // with the static part, what a kernel may have unasked is 48 KB
     const cudaError_t e = allow_smem((const void*)kernel, smem);
     if (e != cudaSuccess) return e;
   }
-  return launch_kernel(kernel, (unsigned)(groups * cluster), threads, smem, cluster, st, a, rows, batches);
+  return launch_kernel(kernel, (unsigned)(rows * cluster), threads, smem, cluster > 1 ? cluster : 0, st, a,
+                       (int)batches);
 }
 template <typename T>
 cudaError_t run_logprobs(const Logprobs& a, cudaStream_t st) {
@@ -848,7 +839,7 @@ cudaError_t run_logprobs(const Logprobs& a, cudaStream_t st) {
 template <typename T>
 cudaError_t run_logprobs_bwd(const LogprobsBwd& a, cudaStream_t st) {
   const int64_t pieces = ceil_div(a.vocab + RowPieces<T>::kPer - 1, RowPieces<T>::kPer);
-  const int threads = threads_for(ceil_div(pieces, kBwdUnroll));
+  const int threads = threads_for(ceil_div(pieces, kBwdUnroll), kBwdThreads);
   const int64_t chunks = ceil_div(pieces, threads * kBwdUnroll), grid = a.targets.count * chunks;
   if (grid > 0x7FFFFFFF) return cudaErrorInvalidValue;
   return launch_kernel(a.dentropy ? logprobs_bwd_kernel<T, true> : logprobs_bwd_kernel<T, false>, (unsigned)grid,
@@ -864,11 +855,14 @@ cudaError_t run_token_loss(const TokenLoss& a, cudaStream_t st) {
     const HeldPlan p = held_plan(a.targets.count, a.vocab, sizeof(T));
     if (p.cluster) {
       f.dx = a.dx, f.lddx = a.lddx;
-      const int smem = p.stages * p.stage_pieces * 16;
-      const cudaError_t e = allow_smem((const void*)token_loss_kernel<T>, smem);
-      if (e != cudaSuccess) return e;
-      return launch_kernel(token_loss_kernel<T>, (unsigned)(p.groups * p.cluster), p.threads, smem, p.cluster, st, f,
-                           a.targets.count, p.stages, p.stage_pieces);
+      const int smem = p.pieces * 16;
+      if (smem > 32 * 1024) {  // with the static part, what a kernel may have unasked is 48 KB
+        const cudaError_t e = allow_smem((const void*)token_loss_kernel<T>, smem);
+        if (e != cudaSuccess) return e;
+      }
+      const int64_t grid = a.targets.count * p.cluster;
+      if (grid > 0x7FFFFFFF) return cudaErrorInvalidValue;
+      return launch_kernel(token_loss_kernel<T>, (unsigned)grid, p.threads, smem, p.cluster > 1 ? p.cluster : 0, st, f);
     }
   }
   f.lse = a.lse;

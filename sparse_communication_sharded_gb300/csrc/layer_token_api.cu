@@ -126,6 +126,7 @@ extern "C" int scape_layer_token_logprobs(const void* logits, int64_t ldx, int d
   if (!size_ok(rows) || !size_ok(vocab)) return fail(SCAPE_EINVAL, "rows or vocab out of range");
   if (vocab == 0) return fail(SCAPE_EINVAL, "vocab must be at least 1");
   if (top < 0 || top > SCAPE_TOP_MAX || top > vocab) return fail(SCAPE_EINVAL, "top must be 0 to 32, and at most vocab");
+  if (top && vocab > SCAPE_TOP_VOCAB_MAX) return fail(SCAPE_EINVAL, "vocab is too large for alternatives");
   if (rows == 0) return SCAPE_OK;
   int rc = check_logits(logits, ldx, dtype, targets, token_bytes, vocab);
   if (!rc) rc = check_floats(logprob, "logprob is NULL or misaligned");

@@ -93,6 +93,7 @@ def test_logprobs(lib):
     refused(lib, f(top=33), "top")
     refused(lib, f(top=-1), "top")
     refused(lib, f(vocab=4, top=5), "top")
+    refused(lib, f(vocab=(1 << 22) + 1, ldx=(1 << 22) + 1, top=1), "too large")
     refused(lib, f(lp=None), "logprob")
     refused(lib, f(lse=4 * A + 2), "lse")
     refused(lib, f(ent=5), "entropy")
