@@ -53,29 +53,34 @@ __global__ __launch_bounds__(kFwdThreads) void embed_fwd_kernel(const __grid_con
     if (piece >= pieces) piece -= pieces, ++r;
   }
   Raw<TW, 8> v[kFwdUnroll];
+  AnyLoad<TW, 8> any[kFwdUnroll];
+  const TW* from[kFwdUnroll];
 #pragma unroll
   for (int u = 0; u < kFwdUnroll; ++u) {
     if (ANY) c[u] -= phase_of(static_cast<const TY*>(a.y) + row[u] * a.ldy) % kPer;
     const bool in = token[u] >= 0 && token[u] < a.vocab;
-    const TW* p = w + (in ? token[u] : 0) * a.ldw + c[u];
-    if constexpr (ANY) {
-      if (in && c[u] >= 0) {
-        v[u] = load_any<8>(p, max(0, min(8, a.cols - c[u])), w, hi);
-      } else {
+    from[u] = w + (in ? token[u] : 0) * a.ldw + c[u];
+    if constexpr (ANY)
+      any[u].begin(from[u], in && c[u] >= 0 ? a.cols - c[u] : 0, w, hi);
+    else
+      v[u] = load_raw<8>(from[u], in ? a.cols - c[u] : 0);
+  }
+  if constexpr (ANY) {
+#pragma unroll
+    for (int u = 0; u < kFwdUnroll; ++u) {
+      const bool in = token[u] >= 0 && token[u] < a.vocab;
+      v[u] = any[u].end(from[u], in && c[u] >= 0 ? a.cols - c[u] : 0);
+      if (in && c[u] < 0) {
         // a row's first elements, at the end of the piece
 #pragma unroll
-        for (int i = 0; i < Raw<TW, 8>::kWords; ++i) v[u].w[i] = 0;
-#pragma unroll
         for (int i = 0; i < 8; ++i)
-          if (in && c[u] + i >= 0 && c[u] + i < a.cols) {
+          if (c[u] + i >= 0 && c[u] + i < a.cols) {
             if constexpr (sizeof(TW) == 2)
-              v[u].w[i / 2] |= (uint32_t) reinterpret_cast<const uint16_t*>(p)[i] << (16 * (i % 2));
+              v[u].w[i / 2] |= (uint32_t) reinterpret_cast<const uint16_t*>(from[u])[i] << (16 * (i % 2));
             else
-              v[u].w[i] = reinterpret_cast<const uint32_t*>(p)[i];
+              v[u].w[i] = reinterpret_cast<const uint32_t*>(from[u])[i];
           }
       }
-    } else {
-      v[u] = load_raw<8>(p, in ? a.cols - c[u] : 0);
     }
   }
 #pragma unroll
@@ -103,16 +108,20 @@ __global__ __launch_bounds__(kFwdThreads) void embed_fwd_kernel(const __grid_con
 // its first: that gives every one of its entries a place of its own, without waiting
 // for another block.  All blocks reading all tokens is 152 x 8 bytes a token out of
 // L2, as much as a row of dy is out of memory; several passes of a radix sort would
-// each be a launch.
+// each be a launch.  What a warp finds it keeps, in order, up to kSortKept; only a warp
+// that finds more (a very common token) reads its share again.
 constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32, kSortUnroll = 16;
-constexpr int kSortRows = 352;  // 44 KB of counts
+constexpr int kSortRows = 352, kSortKept = 64;  // 44 KB of counts, 16 KB
+static_assert(kSortRows <= kSortThreads && kSortWarps <= 32, "a thread for each token, a lane for each warp");
 
 template <typename I>
 __global__ __launch_bounds__(kSortThreads) void sort_tokens_kernel(const I* __restrict__ tokens, int64_t count,
-                                                                   int64_t vocab, int rows, int2* entries,
+                                                                   int64_t vocab, int rows, int4* entries,
                                                                    int* starts) {
-  extern __shared__ int counts[];  // [kSortWarps][rows]
-  __shared__ int below_of[kSortWarps], sums[kSortWarps], first[kSortRows];
+  extern __shared__ __align__(8) int counts[];  // [kSortWarps][rows], rows even
+  int2* const kept_of = reinterpret_cast<int2*>(counts + kSortWarps * rows);  // [kSortWarps][kSortKept]
+  __shared__ int below_of[kSortWarps], sums[kSortWarps];
+  __shared__ int2 range[kSortRows];  // of a token's entries
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t lo = (int64_t)blockIdx.x * rows;
   const int mine = (int)min((int64_t)rows, vocab - lo);
@@ -122,24 +131,27 @@ __global__ __launch_bounds__(kSortThreads) void sort_tokens_kernel(const I* __re
   const int64_t share = (count + kSortThreads - 1) / kSortThreads * 32;
   const int64_t begin = min(count, warp * share), end = min(count, begin + share);
   int* own = counts + warp * rows;
-  int d[kSortUnroll];  // places of 32 x kSortUnroll tokens among this block's, or -1
-  auto read = [&](int64_t i, int& below) {
+  int2* kept = kept_of + warp * kSortKept;
+  int below = 0, found = 0;
+  for (int64_t i = begin; i < end; i += 32 * kSortUnroll) {
     I t[kSortUnroll];
 #pragma unroll
     for (int u = 0; u < kSortUnroll; ++u) t[u] = i + u * 32 + lane < end ? tokens[i + u * 32 + lane] : (I)-1;
 #pragma unroll
     for (int u = 0; u < kSortUnroll; ++u) {
-      const int64_t at = (int64_t)t[u] - lo;
-      below += t[u] >= 0 && at < 0;
-      d[u] = at >= 0 && at < mine ? (int)at : -1;
+      const bool valid = t[u] >= 0 && (int64_t)t[u] < vocab;
+      const int d = (int)((uint32_t)t[u] - (uint32_t)lo);
+      below += valid && d < 0;
+      const bool in = valid && (uint32_t)d < (uint32_t)mine;
+      const uint32_t all = __ballot_sync(0xFFFFFFFFu, in);
+      if (!all) continue;
+      if (in) {
+        atomicAdd(&own[d], 1);
+        const int at = found + __popc(all & ((1u << lane) - 1));
+        if (at < kSortKept) kept[at] = make_int2((int)(i + u * 32 + lane), d);
+      }
+      found += __popc(all);
     }
-  };
-  int below = 0;
-  for (int64_t i = begin; i < end; i += 32 * kSortUnroll) {
-    read(i, below);
-#pragma unroll
-    for (int u = 0; u < kSortUnroll; ++u)
-      if (d[u] >= 0) atomicAdd(&own[d[u]], 1);
   }
   below = __reduce_add_sync(0xFFFFFFFFu, below);
   if (lane == 0) below_of[warp] = below;
@@ -162,27 +174,36 @@ __global__ __launch_bounds__(kSortThreads) void sort_tokens_kernel(const I* __re
   }
   if (lane == 31) sums[warp] = scan;
   __syncthreads();
-  const int before = __reduce_add_sync(0xFFFFFFFFu, below_of[lane]);
+  const int before = __reduce_add_sync(0xFFFFFFFFu, lane < kSortWarps ? below_of[lane] : 0);
   const int base = before + scan - total + __reduce_add_sync(0xFFFFFFFFu, lane < warp ? sums[lane] : 0);
-  if ((int)threadIdx.x < rows) first[threadIdx.x] = base;
+  if ((int)threadIdx.x < rows) range[threadIdx.x] = make_int2(base, base + total);
   if ((int)threadIdx.x < mine) starts[lo + threadIdx.x] = base;
   if (lo + mine == vocab && (int)threadIdx.x == mine - 1) starts[vocab] = base + total;
   __syncthreads();
-  for (int64_t i = begin; i < end; i += 32 * kSortUnroll) {
-    if (end - begin > 32 * kSortUnroll) read(i, below);  // else they are still there
-#pragma unroll
-    for (int u = 0; u < kSortUnroll; ++u) {
-      if (!__any_sync(0xFFFFFFFFu, d[u] >= 0)) continue;
-      const uint32_t same = __match_any_sync(0xFFFFFFFFu, d[u]);
-      const int rank = __popc(same & ((1u << lane) - 1));
-      const int at = d[u] >= 0 ? own[d[u]] + rank : 0;
-      __syncwarp();
-      if (d[u] >= 0) {
-        entries[first[d[u]] + at] = make_int2((int)(i + u * 32 + lane), (int)(lo + d[u]));
-        if ((same >> lane) == 1u) own[d[u]] = at + 1;
-      }
-      __syncwarp();
+  // 32 positions' entries, in their order; d: the place of its token, or -1
+  auto place = [&](int position, int d) {
+    const uint32_t same = __match_any_sync(0xFFFFFFFFu, d);
+    const int rank = __popc(same & ((1u << lane) - 1));
+    const int at = d >= 0 ? own[d] + rank : 0;
+    __syncwarp();
+    if (d >= 0) {
+      const int2 r = range[d];
+      entries[r.x + at] = make_int4(position, (int)(lo + d), r.x, r.y);
+      if ((same >> lane) == 1u) own[d] = at + 1;
     }
+    __syncwarp();
+  };
+  if (found <= kSortKept) {
+    for (int k = 0; k < found; k += 32) {
+      const int2 e = k + lane < found ? kept[k + lane] : make_int2(0, -1);
+      place(e.x, e.y);
+    }
+    return;
+  }
+  for (int64_t i = begin; i < end; i += 32) {
+    const int64_t t = i + lane < end ? (int64_t)tokens[i + lane] : -1;
+    const bool in = t >= lo && t < lo + mine;
+    if (__any_sync(0xFFFFFFFFu, in)) place((int)(i + lane), in ? (int)(t - lo) : -1);
   }
 }
 
@@ -219,94 +240,132 @@ __device__ __forceinline__ void zero_row(T* p, int cols, int lane) {
   if (lane < tail) p[cols - tail + lane] = (T)0.0f;
 }
 
-// The first blocks write zeros, the others each add up some columns of a tile's
-// entries: those of the tokens that start in it, and, of a token with more than
-// kLong entries, the tile's own part, which goes to `partial` for the join.  So a
-// common word's entries are spread over blocks and few tokens need a join.
-constexpr int kLong = 2 * kEmbedTile;
+// Blocks write rows of zeros, or add up some columns of a tile's entries: those of the tokens that start in it.  A token with more than kLong entries
+// is cut into parts of kPart tiles, from the one where it starts on, each summed by the
+// block of its first tile and left in `partial` for the join: so a common word is
+// spread over blocks, and few tokens need a join.
+constexpr int kLong = 2 * kEmbedTile, kPart = 4, kStage = 8;
+// entries that a tile's block may go through: a part of a long token, or the tile's and
+// those of a short token from its last one on
+constexpr int kWindow = (kPart > 3 ? kPart : 3) * kEmbedTile;
+static_assert(kWindow == 64, "a bit for each, in words of 32");
 
 template <typename TD, typename TG, bool ANY>
 __global__ __launch_bounds__(kTileThreads) void embed_sum_kernel(const __grid_constant__ EmbedBwd a, int fill,
-                                                                 int chunks, bool dw16) {
+                                                                 int chunks, bool dw16, uint32_t sms) {
   start();
   constexpr int VEC = 16 / (int)sizeof(TD);
-  extern __shared__ __align__(16) uint4 staged[];  // [kEmbedTile][threads]
-  __shared__ int position[kEmbedTile + kLong], token[kEmbedTile + kLong];
-  __shared__ int ends[4];  // where the first and the last entry's tokens start and end
+  extern __shared__ __align__(16) uint4 staged[];  // [2][kStage][threads]
+  __shared__ int position[kWindow], token[kWindow];
+  __shared__ int2 ends[2];  // where the tile's first and last entry's tokens start and end
   TG* dw = static_cast<TG*>(a.dw);
-  if ((int)blockIdx.x < fill) {
-    const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-    const int64_t v0 = ((int64_t)blockIdx.x * warps + (threadIdx.x >> 5)) * 32;
-    if (v0 >= a.vocab) return;
-    const bool none = v0 + lane < a.vocab && a.starts[v0 + lane] == a.starts[v0 + lane + 1];
-    for (uint32_t left = __ballot_sync(0xFFFFFFFFu, none); left; left &= left - 1)
-      zero_row(dw + (v0 + __ffs(left) - 1) * a.lddw, a.cols, lane);
+  // tiles and rows of zeros in turn, as long as there are both: the ones wait for
+  // loads, the others use what bandwidth is left.  (Blocks go round the SMs, of which
+  // there is an even number: every round begins with the other kind.)
+  const int sums = (int)gridDim.x - fill, both = 2 * min(sums, fill);
+  const bool is_sum = (int)blockIdx.x < both ? (blockIdx.x + blockIdx.x / sms) % 2 == 0 : sums > fill;
+  const int job = (int)blockIdx.x < both ? blockIdx.x / 2 : (int)blockIdx.x - both / 2;
+  if (!is_sum) {
+    // a row a warp: few stores each and many in flight
+    const int64_t v = (int64_t)job * (blockDim.x >> 5) + (threadIdx.x >> 5);
+    if (v < a.vocab && a.starts[v] == a.starts[v + 1]) zero_row(dw + v * a.lddw, a.cols, threadIdx.x & 31);
     return;
   }
-  const int tile = ((int)blockIdx.x - fill) / chunks, chunk = ((int)blockIdx.x - fill) % chunks;
-  const int valid = a.starts[a.vocab], i0 = tile * kEmbedTile;
-  const int i1 = min(i0 + kEmbedTile, valid);
-  if (i0 >= valid) {
+  const int tile = job / chunks, chunk = job % chunks;
+  const int i0 = tile * kEmbedTile;
+  const int valid = a.starts[a.vocab], last = min(valid - 1, i0 + kEmbedTile - 1) - i0;
+  for (int i = threadIdx.x; i < kWindow; i += blockDim.x) {
+    // (there are count entries, of which the first `valid` mean something)
+    int4 e = i0 + i < a.tokens.count ? a.entries[i0 + i] : make_int4(0, -1, 0, 0);
+    if (i0 + i >= valid) e.y = -1;
+    position[i] = e.x;
+    token[i] = e.y;
+    if (i == 0) ends[0] = make_int2(e.z, e.w);
+    if (i == last) ends[1] = make_int2(e.z, e.w);
+  }
+  if (last < 0) {
     if (chunk == 0 && threadIdx.x == 0) a.crossing[tile] = -1;
     return;
   }
-  for (int i = threadIdx.x; i < kEmbedTile + kLong; i += blockDim.x) {
-    const int2 e = i0 + i < valid ? a.entries[i0 + i] : make_int2(0, -1);
-    position[i] = e.x;
-    token[i] = e.y;
-  }
-  if (threadIdx.x < 4) {
-    const int64_t v = a.entries[threadIdx.x < 2 ? i0 : i1 - 1].y;
-    ends[threadIdx.x] = a.starts[v + (threadIdx.x & 1)];
-  }
   __syncthreads();
-  // entries of a short token go with the tile where it starts
-  const bool first_before = ends[0] < i0, first_long = ends[1] - ends[0] > kLong;
-  const bool last_long = ends[3] - ends[2] > kLong;
-  const int begin = first_before && !first_long ? min(ends[1], i1) : i0;
-  const int end = last_long || ends[2] < i0 ? i1 : ends[3];
-  if (chunk == 0 && threadIdx.x == 0) a.crossing[tile] = last_long && ends[2] >= i0 ? token[i1 - 1 - i0] : -1;
+  const int i1 = i0 + last + 1;
+  const int2 head = ends[0], tail = ends[1];
+  const bool head_long = head.y - head.x > kLong, tail_long = tail.y - tail.x > kLong;
+  // the first token: its part from here on, or nothing if it is another block's
+  const bool head_here = head.x >= i0 || (head_long && (tile - head.x / kEmbedTile) % kPart == 0);
+  const int begin = head_here ? i0 : min(head.y, i1);
+  int end = tail.x >= i0 || begin < i1 ? min(tail.y, tail_long ? i0 + kPart * kEmbedTile : tail.y) : begin;
+  if (tail.x < i0 && !head_here) end = begin;  // all of the tile is that token's
+  if (chunk == 0 && threadIdx.x == 0) a.crossing[tile] = tail_long && tail.x >= i0 ? token[last] : -1;
+  // bit i: entry i0 + i is its token's last here
+  uint64_t lasts = 0;
+#pragma unroll
+  for (int h = 0; h < kWindow; h += 32) {
+    const int i = h + ((int)threadIdx.x & 31);
+    lasts |= (uint64_t)__ballot_sync(0xFFFFFFFFu, i + 1 >= kWindow || token[i] != token[i + 1]) << h;
+  }
+  lasts |= 1ull << ((end - 1 - i0) & 63);
   const int c0 = (chunk * (int)blockDim.x + (int)threadIdx.x) * VEC;
   const int mine = a.cols - c0;
   if (mine <= 0) return;
   const TD* dy = static_cast<const TD*>(a.dy);
   const TD* hi = dy + (a.tokens.count - 1) * a.lddy + a.cols;
-  float acc[VEC];
+  uint64_t sum[VEC / 2];  // pairs
 #pragma unroll
-  for (int i = 0; i < VEC; ++i) acc[i] = 0.0f;
-  for (int at = begin; at < end; at += kEmbedTile) {
-    const int n = min(kEmbedTile, end - at);
+  for (int i = 0; i < VEC / 2; ++i) sum[i] = 0;
+  // kStage entries' rows are on their way while as many are added up
+  auto stage = [&](int at, int half) {
+    uint4* to = staged + half * kStage * blockDim.x + threadIdx.x;
+    const int n = min(kStage, end - at);
     if constexpr (ANY) {
-#pragma unroll 8
-      for (int l = 0; l < n; ++l) {
-        const Raw<TD, VEC> r =
-            load_any<VEC>(dy + (int64_t)position[at - i0 + l] * a.lddy + c0, min(mine, VEC), dy, hi);
-        staged[l * blockDim.x + threadIdx.x] = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
-      }
+      const int want = min(mine, VEC);
+      if (n <= 0) return;
+      AnyLoad<TD, VEC> any[kStage];
+#pragma unroll
+      for (int k = 0; k < kStage; ++k)
+        if (k < n) any[k].begin(dy + (int64_t)position[at - i0 + k] * a.lddy + c0, want, dy, hi);
+#pragma unroll
+      for (int k = 0; k < kStage; ++k)
+        if (k < n) {
+          const Raw<TD, VEC> r = any[k].end(dy + (int64_t)position[at - i0 + k] * a.lddy + c0, want);
+          to[k * blockDim.x] = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
+        }
     } else {
       const int bytes = min(mine, VEC) * (int)sizeof(TD);
-      for (int l = 0; l < n; ++l) {
-        const uint32_t to = (uint32_t)__cvta_generic_to_shared(&staged[l * blockDim.x + threadIdx.x]);
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to),
+      for (int l = 0; l < n; ++l)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                         (uint32_t)__cvta_generic_to_shared(to + l * blockDim.x)),
                      "l"(dy + (int64_t)position[at - i0 + l] * a.lddy + c0), "r"(bytes)
                      : "memory");
-      }
-      asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
+      asm volatile("cp.async.commit_group;" ::: "memory");
     }
+  };
+  stage(begin, 0);
+  int half = 0;
+  for (int at = begin; at < end; at += kStage, half ^= 1) {
+    const int n = min(kStage, end - at);
+    stage(at + kStage, half ^ 1);
+    if (!ANY) asm volatile("cp.async.wait_group 1;" ::: "memory");
+    const uint4* from = staged + half * kStage * blockDim.x + threadIdx.x;
     for (int l = 0; l < n; ++l) {
-      const uint4 u = staged[l * blockDim.x + threadIdx.x];
+      const uint4 u = from[l * blockDim.x];
       Raw<TD, VEC> r;
       r.w[0] = u.x, r.w[1] = u.y, r.w[2] = u.z, r.w[3] = u.w;
       float f[VEC];
       to_floats(r, f);
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) acc[i] += f[i];
-      const int i = at + l, v = token[i - i0];
-      if (i + 1 < end && token[i + 1 - i0] == v) continue;
-      // a long token's sum is whole where it starts and ends in this tile's entries only
-      const bool from_first = i < ends[1];
-      const bool part = (from_first && first_long) || (i + 1 == end && last_long);
-      if (!part) {
+      for (int i = 0; i < VEC / 2; ++i) sum[i] = add2(sum[i], pair(f[2 * i], f[2 * i + 1]));
+      const int i = at + l;
+      if (!(lasts >> (i - i0) & 1)) continue;
+      const int v = token[i - i0];
+      float acc[VEC];
+#pragma unroll
+      for (int k = 0; k < VEC / 2; ++k) {
+        unpair(sum[k], acc[2 * k], acc[2 * k + 1]);
+        sum[k] = 0;
+      }
+      const bool of_head = i < head.y;
+      if (of_head ? !head_long : i < tail.x || !tail_long) {
         TG* p = dw + (int64_t)v * a.lddw + c0;
 #pragma unroll
         for (int k = 0; k < VEC; ++k) {
@@ -316,28 +375,26 @@ __global__ __launch_bounds__(kTileThreads) void embed_sum_kernel(const __grid_co
         put<TG, VEC>(p, mine, dw16, acc);
       } else {
         // first the sum of what started before the tile, second of what starts in it
-        float* p = a.partial + ((int64_t)tile * 2 + (from_first && first_before ? 0 : 1)) * a.partial_pitch + c0;
+        float* p = a.partial + ((int64_t)tile * 2 + (of_head && head.x < i0 ? 0 : 1)) * a.partial_pitch + c0;
         put<float, VEC>(p, VEC, true, acc);
       }
-#pragma unroll
-      for (int k = 0; k < VEC; ++k) acc[k] = 0.0f;
     }
   }
 }
 
 // ------------------------------------------------------------------ joining
-// Item (tile, 128 columns): the sum of the long token that starts in the tile.  A
-// block first looks at all its items' tiles.
+// Item (tile, 128 columns): the sum of the long token that starts in the tile, by a
+// warp, which goes through its parts in order.  A block first looks at all its items'
+// tiles.
 constexpr int kJoinThreads = 256, kJoinCols = 128;
 
 template <typename TG>
 __global__ __launch_bounds__(kJoinThreads) void embed_join_kernel(const __grid_constant__ EmbedBwd a, int tiles,
-                                                                  int chunks, bool dw8) {
+                                                                  int chunks) {
   start();
-  __shared__ float4 part[kJoinThreads / 32][32];
   __shared__ int found[kJoinThreads], found_tile[kJoinThreads], found_chunk[kJoinThreads];
   __shared__ int finds;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31;
   const int64_t items = (int64_t)tiles * chunks;
   TG* dw = static_cast<TG*>(a.dw);
   for (int64_t base = blockIdx.x; base < items; base += (int64_t)gridDim.x * kJoinThreads) {
@@ -352,38 +409,26 @@ __global__ __launch_bounds__(kJoinThreads) void embed_join_kernel(const __grid_c
       }
     }
     __syncthreads();
-    for (int k = 0; k < finds; ++k) {
+    for (int k = threadIdx.x >> 5; k < finds; k += kJoinThreads / 32) {
       const int v = found[k], tile = found_tile[k], c0 = found_chunk[k] * kJoinCols + lane * 4;
+      if (c0 >= a.cols) continue;
       const int last = (a.starts[v + 1] - 1) / kEmbedTile;
-      float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      if (c0 < a.cols) {
-#pragma unroll 4
-        for (int t = tile + warp; t <= last; t += kJoinThreads / 32) {
-          // its part of the tile where it starts is the tile's second sum
-          const float4 p = *reinterpret_cast<const float4*>(
-              a.partial + ((int64_t)t * 2 + (t == tile ? 1 : 0)) * a.partial_pitch + c0);
-          s.x += p.x, s.y += p.y, s.z += p.z, s.w += p.w;
-        }
+      // its part of the tile where it starts is the tile's second sum, others the first
+      const float* p = a.partial + ((int64_t)tile * 2 + 1) * a.partial_pitch + c0;
+      float4 s = *reinterpret_cast<const float4*>(p);
+      p += (2 * kPart - 1) * a.partial_pitch;
+#pragma unroll 8
+      for (int t = tile + kPart; t <= last; t += kPart, p += 2 * kPart * a.partial_pitch) {
+        const float4 q = *reinterpret_cast<const float4*>(p);
+        s.x += q.x, s.y += q.y, s.z += q.z, s.w += q.w;
       }
-      part[warp][lane] = s;
-      __syncthreads();
-      if (warp == 0 && c0 < a.cols) {
-        float f[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      const float f[4] = {s.x, s.y, s.z, s.w};
+      TG* out = dw + (int64_t)v * a.lddw + c0;
 #pragma unroll
-        for (int w = 0; w < kJoinThreads / 32; ++w) {
-          const float4 p = part[w][lane];
-          f[0] += p.x, f[1] += p.y, f[2] += p.z, f[3] += p.w;
-        }
-        TG* p = dw + (int64_t)v * a.lddw + c0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          f[i] *= a.scale;
-          if (a.accumulate && c0 + i < a.cols) f[i] += (float)p[i];
-        }
-        put<TG, 4>(p, a.cols - c0, dw8, f);
-      }
-      __syncthreads();
+      for (int i = 0; i < 4; ++i)
+        if (c0 + i < a.cols) out[i] = (TG)(f[i] * a.scale + (a.accumulate ? (float)out[i] : 0.0f));
     }
+    __syncthreads();
   }
 }
 
@@ -401,15 +446,18 @@ cudaError_t run_embedding(const EmbedFwd& a, cudaStream_t st) {
 
 template <typename TD, typename TG>
 cudaError_t run_embedding_bwd(const EmbedBwd& a, cudaStream_t st) {
-  const int rows = (int)std::min<int64_t>(kSortRows, ceil_div(a.vocab, sm_count()));
+  const int rows = (int)std::min<int64_t>(kSortRows, ceil_div(ceil_div(a.vocab, sm_count()), 2) * 2);
   const unsigned sorters = (unsigned)ceil_div(a.vocab, rows);
-  const size_t counts = (size_t)kSortWarps * rows * 4;
-  cudaError_t e =
-      a.tokens.bytes == 8
-          ? launch_kernel(sort_tokens_kernel<int64_t>, sorters, kSortThreads, counts, 0, st,
-                          static_cast<const int64_t*>(a.tokens.p), a.tokens.count, a.vocab, rows, a.entries, a.starts)
-          : launch_kernel(sort_tokens_kernel<int32_t>, sorters, kSortThreads, counts, 0, st,
-                          static_cast<const int32_t*>(a.tokens.p), a.tokens.count, a.vocab, rows, a.entries, a.starts);
+  const int bytes = kSortWarps * (rows * 4 + kSortKept * 8);
+  auto sort = [&](auto* kernel, auto* tokens) {
+    cudaError_t e = cudaSuccess;
+    if (bytes > 44 * 1024) e = allow_smem((const void*)kernel, bytes);
+    if (e != cudaSuccess) return e;
+    return launch_kernel(kernel, sorters, kSortThreads, (size_t)bytes, 0, st, tokens, a.tokens.count, a.vocab, rows,
+                         a.entries, a.starts);
+  };
+  cudaError_t e = a.tokens.bytes == 8 ? sort(sort_tokens_kernel<int64_t>, static_cast<const int64_t*>(a.tokens.p))
+                                      : sort(sort_tokens_kernel<int32_t>, static_cast<const int32_t*>(a.tokens.p));
   if (e != cudaSuccess) return e;
   constexpr int VEC = 16 / (int)sizeof(TD);
   const int64_t vecs = ceil_div(a.cols, VEC), tiles = ceil_div(a.tokens.count, kEmbedTile);
@@ -417,20 +465,21 @@ cudaError_t run_embedding_bwd(const EmbedBwd& a, cudaStream_t st) {
   const int64_t parts = ceil_div(vecs, kTileThreads);
   const int threads = (int)(ceil_div(ceil_div(vecs, parts), 32) * 32);
   const int64_t chunks = ceil_div(vecs, threads);
-  const int64_t fill = a.accumulate ? 0 : ceil_div(a.vocab, 32 * (threads / 32));
+  const int64_t fill = a.accumulate ? 0 : ceil_div(a.vocab, threads / 32);
   if (tiles * chunks + fill > 0x7FFFFFFF) return cudaErrorInvalidValue;
-  const size_t smem = (size_t)kEmbedTile * threads * 16;
+  const size_t smem = (size_t)2 * kStage * threads * 16;
   const bool any = !rows16(a.dy, a.lddy, sizeof(TD));
   // whether VEC of the output's elements can be stored together
   const bool dw16 = aligned(a.dw, std::min<size_t>(16, VEC * sizeof(TG))) &&
                     (a.lddw * sizeof(TG)) % std::min<size_t>(16, VEC * sizeof(TG)) == 0;
   e = launch_kernel(any ? embed_sum_kernel<TD, TG, true> : embed_sum_kernel<TD, TG, false>,
-                    (unsigned)(tiles * chunks + fill), threads, smem, 0, st, a, (int)fill, (int)chunks, dw16);
+                    (unsigned)(tiles * chunks + fill), threads, smem, 0, st, a, (int)fill, (int)chunks, dw16,
+                    (uint32_t)(sm_count() / 2 * 2));
   if (e != cudaSuccess) return e;
+  if (a.tokens.count <= kLong) return e;  // no token has so many
   const int64_t join = ceil_div(a.cols, kJoinCols);
-  const bool dw8 = aligned(a.dw, 4 * sizeof(TG)) && (a.lddw * sizeof(TG)) % (4 * sizeof(TG)) == 0;
-  return launch_kernel(embed_join_kernel<TG>, (unsigned)std::min<int64_t>(tiles * join, (int64_t)sm_count() * 4),
-                       kJoinThreads, 0, 0, st, a, (int)tiles, (int)join, dw8);
+  return launch_kernel(embed_join_kernel<TG>, (unsigned)std::min<int64_t>(tiles * join, (int64_t)sm_count() * 2),
+                       kJoinThreads, 0, 0, st, a, (int)tiles, (int)join);
 }
 
 }  // namespace

@@ -191,49 +191,54 @@ __global__ __launch_bounds__(kThreads) void norm_kernel(const double* partial, i
 }
 
 // ------------------------------------------------------------------ clipping
-// Pieces of 8 elements on the output's boundaries.
-template <typename TI, typename TO>
-__device__ __forceinline__ void chunk_scale(const TI* p, TO* o, int64_t numel, int64_t chunk, float factor) {
-  constexpr int kPerOut = 16 / (int)sizeof(TO);
-  const int phase = phase_of(o) % kPerOut;
-  Raw<TI, 8> r[kUnroll];
+// Pieces of 8 elements on the output's boundaries, U of a thread's kUnroll at a time.
+// ANY: they are on no boundary of the input.
+template <bool ANY, int U, typename TI, typename TO>
+__device__ __forceinline__ void chunk_scale_as(const TI* p, TO* o, int64_t numel, int64_t chunk, float factor) {
+  const int phase = phase_of(o) % (16 / (int)sizeof(TO));
+#pragma unroll 1
+  for (int u0 = 0; u0 < kUnroll; u0 += U) {
+    const int64_t first = (chunk * kChunk + u0 * kThreads + threadIdx.x) * 8 - phase;
+    Raw<TI, 8> r[U];
+    AnyLoad<TI, 8> any[U];
 #pragma unroll
-  for (int u = 0; u < kUnroll; ++u) {
-    const int64_t c = (chunk * kChunk + u * kThreads + threadIdx.x) * 8 - phase;
-    if (c >= 0) {
-      r[u] = load_any<8>(p + c, (int)max((int64_t)0, min((int64_t)8, numel - c)), p, p + numel);
-    } else {
-#pragma unroll
-      for (int k = 0; k < Raw<TI, 8>::kWords; ++k) r[u].w[k] = 0;
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (c + k >= 0 && c + k < numel) {
-          if constexpr (sizeof(TI) == 2)
-            r[u].w[k / 2] |= (uint32_t) reinterpret_cast<const uint16_t*>(p)[c + k] << (16 * (k % 2));
-          else
-            r[u].w[k] = reinterpret_cast<const uint32_t*>(p)[c + k];
-        }
+    for (int u = 0; u < U; ++u) {
+      const int64_t c = first + u * kThreads * 8;
+      const int n = c >= 0 ? (int)max((int64_t)0, min((int64_t)8, numel - c)) : 0;
+      if constexpr (ANY)
+        any[u].begin(p + c, n, p, p + numel);
+      else
+        r[u] = load_raw<8>(p + c, n);
     }
-  }
 #pragma unroll
-  for (int u = 0; u < kUnroll; ++u) {
-    const int64_t c = (chunk * kChunk + u * kThreads + threadIdx.x) * 8 - phase;
-    float f[8];
-    to_floats(r[u], f);
+    for (int u = 0; u < U; ++u) {
+      const int64_t c = first + u * kThreads * 8;
+      const int n = c >= 0 ? (int)max((int64_t)0, min((int64_t)8, numel - c)) : 0;
+      if constexpr (ANY) r[u] = any[u].end(p + c, n);
+      float f[8];
+      to_floats(r[u], f);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) f[k] *= factor;
-    if (c >= 0) {
-      store_part<8>(o + c, (int)max((int64_t)0, min((int64_t)8, numel - c)), f);
-    } else {
+      for (int k = 0; k < 8; ++k) f[k] *= factor;
+      store_part<8>(o + c, n, f);
+      if (c < 0) {
+        // a tensor's first elements, at the end of the piece
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (c + k >= 0 && c + k < numel) o[c + k] = (TO)f[k];
+        for (int k = 0; k < 8; ++k)
+          if (c + k >= 0 && c + k < numel) o[c + k] = (TO)((float)p[c + k] * factor);
+      }
     }
   }
 }
+template <typename TI, typename TO>
+__device__ __forceinline__ void chunk_scale(const TI* p, TO* o, int64_t numel, int64_t chunk, float factor) {
+  if ((phase_of(p) - phase_of(o) % (16 / (int)sizeof(TO))) % (16 / (int)sizeof(TI)) == 0)
+    chunk_scale_as<false, kUnroll>(p, o, numel, chunk, factor);
+  else
+    chunk_scale_as<true, 2>(p, o, numel, chunk, factor);
+}
 
 template <int N>
-__global__ __launch_bounds__(kThreads) void clip_kernel(const __grid_constant__ Table<N> t, const double* partial,
+__global__ __launch_bounds__(kThreads, 3) void clip_kernel(const __grid_constant__ Table<N> t, const double* partial,
                                                         int parts, float max_norm, float eps, float* norm) {
   start();
   __shared__ double red[kThreads / 32];

@@ -124,6 +124,59 @@ __device__ __forceinline__ Raw<T, VEC> load_any(const T* p, int n, const T* lo, 
   }
   return r;
 }
+// The same in two steps, so that a thread's loads are in flight together: the
+// branches of load_any() keep one waiting for the other.  begin() loads the aligned
+// words that hold VEC elements (one word more than they are), end() puts the elements
+// together; where those words do not lie in the matrix entirely, or fewer than VEC
+// elements are wanted, end() reads element by element.
+template <typename T, int VEC>
+struct AnyLoad {
+  static constexpr int kPer = 16 / sizeof(T), kPieces = VEC / kPer;
+  uint4 w[kPieces + 1];
+  uint32_t off;
+  bool fast;
+  __device__ __forceinline__ void begin(const T* p, int n, const T* lo, const T* hi) {
+    off = (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15u);
+    const char* a = reinterpret_cast<const char*>(p) - off;
+    fast = n >= VEC && (off == 0 || (a >= reinterpret_cast<const char*>(lo) &&
+                                     a + 16 * (kPieces + 1) <= reinterpret_cast<const char*>(hi)));
+#pragma unroll
+    for (int i = 0; i <= kPieces; ++i)
+      if (fast && (i < kPieces || off)) w[i] = reinterpret_cast<const uint4*>(a)[i];
+  }
+  __device__ __forceinline__ Raw<T, VEC> end(const T* p, int n) const {
+    Raw<T, VEC> r;
+    if (fast) {
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i) {
+        uint32_t v[8] = {w[i].x, w[i].y, w[i].z, w[i].w, w[i + 1].x, w[i + 1].y, w[i + 1].z, w[i + 1].w};
+        if (off & 8) {
+#pragma unroll
+          for (int j = 0; j < 6; ++j) v[j] = v[j + 2];
+        }
+        if (off & 4) {
+#pragma unroll
+          for (int j = 0; j < 5; ++j) v[j] = v[j + 1];
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          r.w[4 * i + j] = sizeof(T) == 4 ? v[j] : __funnelshift_r(v[j], v[j + 1], (off & 2) * 8);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < Raw<T, VEC>::kWords; ++j) r.w[j] = 0;
+#pragma unroll
+      for (int j = 0; j < VEC; ++j)
+        if (j < n) {
+          if constexpr (sizeof(T) == 2)
+            r.w[j / 2] |= (uint32_t) reinterpret_cast<const uint16_t*>(p)[j] << (16 * (j % 2));
+          else
+            r.w[j] = reinterpret_cast<const uint32_t*>(p)[j];
+        }
+    }
+    return r;
+  }
+};
 template <typename T, int VEC>
 __device__ __forceinline__ void to_floats(const Raw<T, VEC>& r, float (&v)[VEC]) {
 #pragma unroll

@@ -694,38 +694,31 @@ __global__ __launch_bounds__(kBwdThreads) void logprobs_bwd_kernel(const __grid_
   }
   const int first = chunk * (kBwdUnroll * (int)blockDim.x) + (int)threadIdx.x;
   const uint64_t minus = pair(-lse, -lse), log2e = pair(kLog2eF, kLog2eF);
-  Raw<T, kPer> u[kBwdUnroll];
+  AnyLoad<T, kPer> any[kBwdUnroll];
 #pragma unroll
   for (int i = 0; i < kBwdUnroll; ++i) {
     const int v = first + i * blockDim.x, c = out.column(v);
-    if (none || v >= out.pieces) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) u[i].w[k] = 0;
-    } else if (out.whole(v)) {
-      u[i] = load_any<kPer>(x + c, kPer, lo, hi);
-    } else {
-      const RowPieces<T> in(x, (int)a.vocab);
-      // this piece's columns of the input, whose own boundaries may be others
-      uint32_t w[4] = {0, 0, 0, 0};
-#pragma unroll
-      for (int k = 0; k < kPer; ++k)
-        if (c + k >= 0 && c + k < in.cols) {
-          if constexpr (sizeof(T) == 2)
-            w[k / 2] |= (uint32_t) reinterpret_cast<const uint16_t*>(x)[c + k] << (16 * (k % 2));
-          else
-            w[k] = reinterpret_cast<const uint32_t*>(x)[c + k];
-        }
-#pragma unroll
-      for (int k = 0; k < 4; ++k) u[i].w[k] = w[k];
-    }
+    any[i].begin(x + c, !none && v < out.pieces && out.whole(v) ? kPer : 0, lo, hi);
   }
 #pragma unroll
   for (int i = 0; i < kBwdUnroll; ++i) {
     const int v = first + i * blockDim.x;
     if (v >= out.pieces) continue;
     const int c = out.column(v);
+    Raw<T, kPer> u = any[i].end(x + c, !none && out.whole(v) ? kPer : 0);
+    if (!none && !out.whole(v)) {
+      // columns at a row's ends
+#pragma unroll
+      for (int k = 0; k < kPer; ++k)
+        if (c + k >= 0 && c + k < out.cols) {
+          if constexpr (sizeof(T) == 2)
+            u.w[k / 2] |= (uint32_t) reinterpret_cast<const uint16_t*>(x)[c + k] << (16 * (k % 2));
+          else
+            u.w[k] = reinterpret_cast<const uint32_t*>(x)[c + k];
+        }
+    }
     float f[kPer];
-    to_floats(u[i], f);
+    to_floats(u, f);
     if (none) {
 #pragma unroll
       for (int k = 0; k < kPer; ++k) f[k] = 0.0f;

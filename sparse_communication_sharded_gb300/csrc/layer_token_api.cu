@@ -28,7 +28,7 @@ EmbedSpace embed_space(int64_t count, int64_t vocab, int64_t cols) {
   EmbedSpace s;
   const int64_t tiles = ceil_div(count, kEmbedTile);
   s.entries = 0;
-  s.starts = round256((size_t)count * 8);
+  s.starts = round256((size_t)count * sizeof(int4));
   s.crossing = s.starts + round256((size_t)(vocab + 1) * 4);
   s.partial = s.crossing + round256((size_t)tiles * 4);
   s.bytes = s.partial + round256((size_t)tiles * 2 * embed_partial_pitch(cols) * 4);
@@ -102,7 +102,7 @@ extern "C" int scape_layer_embedding_bwd(const void* dy, int64_t lddy, int dtype
   a.dy = dy, a.lddy = lddy, a.tokens = {tokens, token_bytes, count};
   a.vocab = vocab, a.cols = (int)cols, a.scale = scale, a.accumulate = accumulate != 0;
   a.dw = dweight, a.lddw = lddw;
-  a.entries = reinterpret_cast<int2*>(ws + s.entries);
+  a.entries = reinterpret_cast<int4*>(ws + s.entries);
   a.starts = reinterpret_cast<int*>(ws + s.starts);
   a.crossing = reinterpret_cast<int*>(ws + s.crossing);
   a.partial = reinterpret_cast<float*>(ws + s.partial);

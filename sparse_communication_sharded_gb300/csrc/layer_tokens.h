@@ -35,7 +35,8 @@ struct EmbedBwd {
   void* dw;
   int64_t lddw;
   // workspace
-  int2* entries;   // (position, token) of the tokens in range, by token, then position
+  int4* entries;   // of the tokens in range, by token, then position: position, token, and
+                   // where the token's entries start and end
   int* starts;     // [vocab + 1]: where a token's entries start
   int* crossing;   // a tile of entries: the token whose entries start in it and go on past it, or -1
   float* partial;  // [tiles][2][partial_pitch]: sums of entries whose token goes on in another tile
