@@ -200,10 +200,16 @@ __global__ __launch_bounds__(kSortThreads) void sort_tokens_kernel(const I* __re
     }
     return;
   }
-  for (int64_t i = begin; i < end; i += 32) {
-    const int64_t t = i + lane < end ? (int64_t)tokens[i + lane] : -1;
-    const bool in = t >= lo && t < lo + mine;
-    if (__any_sync(0xFFFFFFFFu, in)) place((int)(i + lane), in ? (int)(t - lo) : -1);
+  constexpr int kAgain = 8;
+  for (int64_t i = begin; i < end; i += 32 * kAgain) {
+    I t[kAgain];
+#pragma unroll
+    for (int u = 0; u < kAgain; ++u) t[u] = i + u * 32 + lane < end ? tokens[i + u * 32 + lane] : (I)-1;
+#pragma unroll
+    for (int u = 0; u < kAgain; ++u) {
+      const bool in = (int64_t)t[u] >= lo && (int64_t)t[u] < lo + mine;
+      if (__any_sync(0xFFFFFFFFu, in)) place((int)(i + u * 32 + lane), in ? (int)((int64_t)t[u] - lo) : -1);
+    }
   }
 }
 
@@ -383,20 +389,39 @@ __global__ __launch_bounds__(kTileThreads) void embed_sum_kernel(const __grid_co
 }
 
 // ------------------------------------------------------------------ joining
-// Item (tile, 128 columns): the sum of the long token that starts in the tile, by a
-// warp, which goes through its parts in order.  A block first looks at all its items'
-// tiles.
-constexpr int kJoinThreads = 256, kJoinCols = 128;
+// Item (tile, 128 columns): the sum of the long token that starts in the tile, its
+// parts in order by a warp, or, where they are many, a share of them by each of the
+// block's warps, and these in order.  A block first looks at all its items' tiles.
+constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32, kJoinCols = 128, kJoinAlone = 12;
 
 template <typename TG>
 __global__ __launch_bounds__(kJoinThreads) void embed_join_kernel(const __grid_constant__ EmbedBwd a, int tiles,
                                                                   int chunks) {
   start();
-  __shared__ int found[kJoinThreads], found_tile[kJoinThreads], found_chunk[kJoinThreads];
+  __shared__ int4 found[kJoinThreads];  // tile, its token, the token's last tile, columns
+  __shared__ float4 share[kJoinWarps][32];
   __shared__ int finds;
-  const int lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t items = (int64_t)tiles * chunks;
-  TG* dw = static_cast<TG*>(a.dw);
+  // parts first, first + step, ... of an item; part 0 is the tile's second sum, others
+  // are their tiles' first
+  auto sum_parts = [&](const int4& e, int c0, int parts, int first, int step) {
+    float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+    for (int k = first; k < parts; k += step) {
+      const float4 q = *reinterpret_cast<const float4*>(
+          a.partial + ((int64_t)(e.x + k * kPart) * 2 + (k == 0 ? 1 : 0)) * a.partial_pitch + c0);
+      s.x += q.x, s.y += q.y, s.z += q.z, s.w += q.w;
+    }
+    return s;
+  };
+  auto write = [&](const int4& e, int c0, const float4& s) {
+    const float f[4] = {s.x, s.y, s.z, s.w};
+    TG* out = static_cast<TG*>(a.dw) + (int64_t)e.y * a.lddw + c0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (c0 + i < a.cols) out[i] = (TG)(f[i] * a.scale + (a.accumulate ? (float)out[i] : 0.0f));
+  };
   for (int64_t base = blockIdx.x; base < items; base += (int64_t)gridDim.x * kJoinThreads) {
     if (threadIdx.x == 0) finds = 0;
     __syncthreads();
@@ -404,29 +429,33 @@ __global__ __launch_bounds__(kJoinThreads) void embed_join_kernel(const __grid_c
     if (my < items) {
       const int tile = (int)(my / chunks), v = a.crossing[tile];
       if (v >= 0) {
-        const int at = atomicAdd(&finds, 1);  // their order changes nothing
-        found[at] = v, found_tile[at] = tile, found_chunk[at] = (int)(my % chunks);
+        const int last = (a.starts[v + 1] - 1) / kEmbedTile;
+        // their order changes nothing
+        found[atomicAdd(&finds, 1)] = make_int4(tile, v, last, (int)(my % chunks) * kJoinCols);
       }
     }
     __syncthreads();
-    for (int k = threadIdx.x >> 5; k < finds; k += kJoinThreads / 32) {
-      const int v = found[k], tile = found_tile[k], c0 = found_chunk[k] * kJoinCols + lane * 4;
-      if (c0 >= a.cols) continue;
-      const int last = (a.starts[v + 1] - 1) / kEmbedTile;
-      // its part of the tile where it starts is the tile's second sum, others the first
-      const float* p = a.partial + ((int64_t)tile * 2 + 1) * a.partial_pitch + c0;
-      float4 s = *reinterpret_cast<const float4*>(p);
-      p += (2 * kPart - 1) * a.partial_pitch;
-#pragma unroll 8
-      for (int t = tile + kPart; t <= last; t += kPart, p += 2 * kPart * a.partial_pitch) {
-        const float4 q = *reinterpret_cast<const float4*>(p);
-        s.x += q.x, s.y += q.y, s.z += q.z, s.w += q.w;
-      }
-      const float f[4] = {s.x, s.y, s.z, s.w};
-      TG* out = dw + (int64_t)v * a.lddw + c0;
+    for (int k = warp; k < finds; k += kJoinWarps) {
+      const int4 e = found[k];
+      const int parts = (e.z - e.x) / kPart + 1, c0 = e.w + lane * 4;
+      if (parts <= kJoinAlone && c0 < a.cols) write(e, c0, sum_parts(e, c0, parts, 0, 1));
+    }
+    for (int k = 0; k < finds; ++k) {
+      const int4 e = found[k];
+      const int parts = (e.z - e.x) / kPart + 1, c0 = e.w + lane * 4;
+      if (parts <= kJoinAlone) continue;
+      share[warp][lane] = c0 < a.cols ? sum_parts(e, c0, parts, warp, kJoinWarps) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      __syncthreads();
+      if (warp == 0 && c0 < a.cols) {
+        float4 s = share[0][lane];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (c0 + i < a.cols) out[i] = (TG)(f[i] * a.scale + (a.accumulate ? (float)out[i] : 0.0f));
+        for (int w = 1; w < kJoinWarps; ++w) {
+          const float4 q = share[w][lane];
+          s.x += q.x, s.y += q.y, s.z += q.z, s.w += q.w;
+        }
+        write(e, c0, s);
+      }
+      __syncthreads();
     }
     __syncthreads();
   }

@@ -194,7 +194,7 @@ __global__ __launch_bounds__(kThreads) void norm_kernel(const double* partial, i
 // Pieces of 8 elements on the output's boundaries, U of a thread's kUnroll at a time.
 // ANY: they are on no boundary of the input.
 template <bool ANY, int U, typename TI, typename TO>
-__device__ __forceinline__ void chunk_scale_as(const TI* p, TO* o, int64_t numel, int64_t chunk, float factor) {
+__device__ __forceinline__ void chunk_scale(const TI* p, TO* o, int64_t numel, int64_t chunk, float factor) {
   const int phase = phase_of(o) % (16 / (int)sizeof(TO));
 #pragma unroll 1
   for (int u0 = 0; u0 < kUnroll; u0 += U) {
@@ -229,43 +229,44 @@ __device__ __forceinline__ void chunk_scale_as(const TI* p, TO* o, int64_t numel
     }
   }
 }
-template <typename TI, typename TO>
-__device__ __forceinline__ void chunk_scale(const TI* p, TO* o, int64_t numel, int64_t chunk, float factor) {
-  if ((phase_of(p) - phase_of(o) % (16 / (int)sizeof(TO))) % (16 / (int)sizeof(TI)) == 0)
-    chunk_scale_as<false, kUnroll>(p, o, numel, chunk, factor);
-  else
-    chunk_scale_as<true, 2>(p, o, numel, chunk, factor);
+// Whether pieces on the output's boundaries are on 16 bytes of the input.
+inline bool same_boundaries(const void* in, bool in_bf16, const void* out, bool out_bf16) {
+  const int out_elem = out_bf16 ? 2 : 4, in_elem = in_bf16 ? 2 : 4;
+  const int phase = (int)(reinterpret_cast<uintptr_t>(out) & 15u) / out_elem;
+  return (reinterpret_cast<uintptr_t>(in) - (uintptr_t)(phase * in_elem)) % 16 == 0;
 }
 
-template <int N>
-__global__ __launch_bounds__(kThreads, 3) void clip_kernel(const __grid_constant__ Table<N> t, const double* partial,
-                                                        int parts, float max_norm, float eps, float* norm) {
+// ANY: some tensor's pieces are on no boundaries of the input (a kernel of its own, as
+// its loads take twice the registers).
+template <int N, bool ANY>
+__global__ __launch_bounds__(kThreads, kBlocksPerSm) void clip_kernel(const __grid_constant__ Table<N> t, const double* partial,
+                                                        int parts, float max_norm, float eps, float* norm,
+                                                                 bool in_place) {
   start();
   __shared__ double red[kThreads / 32];
   const double n = norm_of(partial, parts, red);
   if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)n;
   const double q = (double)max_norm / (n + (double)eps);
   const float factor = q >= 1.0 ? 1.0f : (float)q;  // NaN stays
+  if (in_place && factor == 1.0f) return;  // one of itself is itself
   const int begin = (int)((int64_t)t.chunks * blockIdx.x / gridDim.x);
   const int end = (int)((int64_t)t.chunks * (blockIdx.x + 1) / gridDim.x);
   int i = tensor_of(t, begin);
   for (int c = begin; c < end; ++c) {
     while (i + 1 < t.n && t.first[i + 1] <= c) ++i;
     const int64_t m = t.numel[i], k = c - t.first[i];
-    // one of itself is itself
-    if (factor == 1.0f && t.in[i] == t.out[i]) continue;
     if (t.in_bf16[i]) {
       const bf16* p = static_cast<const bf16*>(t.in[i]);
       if (t.out_bf16[i])
-        chunk_scale(p, static_cast<bf16*>(t.out[i]), m, k, factor);
+        chunk_scale<ANY, ANY ? 1 : kUnroll>(p, static_cast<bf16*>(t.out[i]), m, k, factor);
       else
-        chunk_scale(p, static_cast<float*>(t.out[i]), m, k, factor);
+        chunk_scale<ANY, ANY ? 1 : kUnroll>(p, static_cast<float*>(t.out[i]), m, k, factor);
     } else {
       const float* p = static_cast<const float*>(t.in[i]);
       if (t.out_bf16[i])
-        chunk_scale(p, static_cast<bf16*>(t.out[i]), m, k, factor);
+        chunk_scale<ANY, ANY ? 1 : kUnroll>(p, static_cast<bf16*>(t.out[i]), m, k, factor);
       else
-        chunk_scale(p, static_cast<float*>(t.out[i]), m, k, factor);
+        chunk_scale<ANY, ANY ? 1 : kUnroll>(p, static_cast<float*>(t.out[i]), m, k, factor);
     }
   }
 }
@@ -317,8 +318,12 @@ cudaError_t run_grad_norm(const GradSet& a, cudaStream_t st) {
   if (!a.out) return launch_kernel(norm_kernel, 1u, kThreads, 0, 0, st, (const double*)a.partial, parts, a.norm);
   float* norm = a.norm;
   return in_tables<N>(a, true, [&](const Table<N>& t) {
-    const cudaError_t r = launch_kernel(clip_kernel<N>, (unsigned)grid_of(t.chunks), kThreads, 0, 0, st, t,
-                                        (const double*)a.partial, parts, a.max_norm, a.eps, norm);
+    bool same = true, in_place = true;
+    for (int i = 0; i < t.n; ++i) in_place &= t.in[i] == t.out[i];
+    for (int i = 0; i < t.n; ++i) same &= same_boundaries(t.in[i], t.in_bf16[i], t.out[i], t.out_bf16[i]);
+    const cudaError_t r = launch_kernel(same ? clip_kernel<N, false> : clip_kernel<N, true>, (unsigned)grid_of(t.chunks),
+                                        kThreads, 0, 0, st, t, (const double*)a.partial, parts, a.max_norm, a.eps, norm,
+                                        in_place);
     norm = nullptr;  // told once
     return r;
   });
