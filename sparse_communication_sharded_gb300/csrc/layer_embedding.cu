@@ -27,7 +27,9 @@ __device__ __forceinline__ int phase_of(const T* p) {
 }
 
 // ------------------------------------------------------------------ forward
-constexpr int kFwdThreads = 256, kFwdUnroll = 4;
+constexpr int kFwdThreads = 256;
+template <bool ANY>
+constexpr int kFwdUnroll = ANY ? 1 : 4;
 
 // Items are (row, piece of 8 columns).  ANY: rows of w or y are not on 16 bytes;
 // pieces then lie on y's boundaries, and the first of a row starts before it.
@@ -35,28 +37,28 @@ template <typename TW, typename TY, bool ANY>
 __global__ __launch_bounds__(kFwdThreads) void embed_fwd_kernel(const __grid_constant__ EmbedFwd a, int pieces,
                                                                 int64_t items) {
   start();
-  constexpr int kPer = 16 / (int)sizeof(TY);
+  constexpr int kPer = 16 / (int)sizeof(TY), U = kFwdUnroll<ANY>;
   const TW* w = static_cast<const TW*>(a.w);
   const TW* hi = w + (a.vocab - 1) * a.ldw + a.cols;
-  const int64_t first = (int64_t)blockIdx.x * (kFwdThreads * kFwdUnroll) + threadIdx.x;
-  int64_t row[kFwdUnroll], token[kFwdUnroll];
-  int c[kFwdUnroll];
+  const int64_t first = (int64_t)blockIdx.x * (kFwdThreads * U) + threadIdx.x;
+  int64_t row[U], token[U];
+  int c[U];
   int64_t r = items <= 0xFFFFFFFFll ? (int64_t)((uint32_t)first / (uint32_t)pieces) : first / pieces;
   int piece = (int)(first - r * pieces);
   const int step_rows = kFwdThreads / pieces, step_pieces = kFwdThreads % pieces;
 #pragma unroll
-  for (int u = 0; u < kFwdUnroll; ++u) {
+  for (int u = 0; u < U; ++u) {
     row[u] = r;
     token[u] = r < a.tokens.count ? load_token(a.tokens, r) : -1;
     c[u] = piece * 8;
     piece += step_pieces, r += step_rows;
     if (piece >= pieces) piece -= pieces, ++r;
   }
-  Raw<TW, 8> v[kFwdUnroll];
-  AnyLoad<TW, 8> any[kFwdUnroll];
-  const TW* from[kFwdUnroll];
+  Raw<TW, 8> v[U];
+  AnyLoad<TW, 8> any[U];
+  const TW* from[U];
 #pragma unroll
-  for (int u = 0; u < kFwdUnroll; ++u) {
+  for (int u = 0; u < U; ++u) {
     if (ANY) c[u] -= phase_of(static_cast<const TY*>(a.y) + row[u] * a.ldy) % kPer;
     const bool in = token[u] >= 0 && token[u] < a.vocab;
     from[u] = w + (in ? token[u] : 0) * a.ldw + c[u];
@@ -67,7 +69,7 @@ __global__ __launch_bounds__(kFwdThreads) void embed_fwd_kernel(const __grid_con
   }
   if constexpr (ANY) {
 #pragma unroll
-    for (int u = 0; u < kFwdUnroll; ++u) {
+    for (int u = 0; u < U; ++u) {
       const bool in = token[u] >= 0 && token[u] < a.vocab;
       v[u] = any[u].end(from[u], in && c[u] >= 0 ? a.cols - c[u] : 0);
       if (in && c[u] < 0) {
@@ -84,7 +86,7 @@ __global__ __launch_bounds__(kFwdThreads) void embed_fwd_kernel(const __grid_con
     }
   }
 #pragma unroll
-  for (int u = 0; u < kFwdUnroll; ++u) {
+  for (int u = 0; u < U; ++u) {
     if (row[u] >= a.tokens.count) continue;
     float f[8];
     to_floats(v[u], f);
@@ -467,7 +469,7 @@ cudaError_t run_embedding(const EmbedFwd& a, cudaStream_t st) {
   const bool vec = rows16(a.w, a.ldw, sizeof(TW)) && rows16(a.y, a.ldy, sizeof(TY));
   // pieces of a row, with room for one that starts before it
   const int pieces = (int)(vec ? ceil_div(a.cols, 8) : ceil_div((int64_t)a.cols + 16 / (int)sizeof(TY) - 1, 8));
-  const int64_t items = a.tokens.count * pieces, blocks = ceil_div(items, kFwdThreads * kFwdUnroll);
+  const int64_t items = a.tokens.count * pieces, blocks = ceil_div(items, kFwdThreads * (vec ? kFwdUnroll<false> : kFwdUnroll<true>));
   if (blocks > 0x7FFFFFFF) return cudaErrorInvalidValue;
   return launch_kernel(vec ? embed_fwd_kernel<TW, TY, false> : embed_fwd_kernel<TW, TY, true>, (unsigned)blocks,
                        kFwdThreads, 0, 0, st, a, pieces, items);
