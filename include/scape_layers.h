@@ -197,7 +197,7 @@ int scape_layer_linear_plan(int product, int64_t rows, int64_t k, int64_t n, int
 /* ---------------------------------------------------------------- tokens
  * Tokens (and targets) are int32 or int64 (token_bytes 4 or 8).  One below 0 stands
  * for none; one that is not below vocab is never used as an index, and what is
- * computed for it is NaN.
+ * computed for it is NaN.  A row has at most 2^30 columns.
  */
 
 /*

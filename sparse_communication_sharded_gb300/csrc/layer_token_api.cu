@@ -20,6 +20,10 @@ int check_floats(const float* p, const char* what) {
   return p && aligned(p, 4) ? (int)SCAPE_OK : fail(SCAPE_EINVAL, what);
 }
 
+// Columns of a row: column numbers, rounded up to a block's, stay in an int.
+constexpr int64_t kMaxCols = int64_t{1} << 30;
+bool cols_ok(int64_t n) { return n >= 0 && n <= kMaxCols; }
+
 // Where the parts of embedding_bwd's workspace lie.
 struct EmbedSpace {
   size_t entries, starts, crossing, partial, bytes;
@@ -48,7 +52,7 @@ extern "C" int scape_layer_embedding(const void* tokens, int token_bytes, int64_
                                      int64_t ldw, int weight_dtype, int64_t vocab, int64_t cols, float scale, void* y,
                                      int64_t ldy, int dtype, void* stream) {
   if (!dtype_ok(dtype) || !dtype_ok(weight_dtype)) return fail(SCAPE_EINVAL, "unknown dtype");
-  if (!size_ok(count) || !size_ok(vocab) || !size_ok(cols)) return fail(SCAPE_EINVAL, "a size is out of range");
+  if (!size_ok(count) || !size_ok(vocab) || !cols_ok(cols)) return fail(SCAPE_EINVAL, "a size is out of range");
   if (vocab == 0) return fail(SCAPE_EINVAL, "vocab must be at least 1");
   if (count == 0 || cols == 0) return SCAPE_OK;
   int rc = check_tokens(tokens, token_bytes, "tokens is NULL or misaligned");
@@ -66,7 +70,7 @@ extern "C" int scape_layer_embedding(const void* tokens, int token_bytes, int64_
 
 extern "C" int scape_layer_embedding_bwd_workspace(int64_t count, int64_t vocab, int64_t cols, size_t* bytes) {
   if (!bytes) return fail(SCAPE_EINVAL, "bytes is NULL");
-  if (!size_ok(count) || !size_ok(vocab) || !size_ok(cols)) return fail(SCAPE_EINVAL, "a size is out of range");
+  if (!size_ok(count) || !size_ok(vocab) || !cols_ok(cols)) return fail(SCAPE_EINVAL, "a size is out of range");
   *bytes = count && vocab && cols ? embed_space(count, vocab, cols).bytes : 0;
   return SCAPE_OK;
 }
@@ -78,7 +82,7 @@ extern "C" int scape_layer_embedding_bwd(const void* dy, int64_t lddy, int dtype
   const char* const who = "scape_layer_embedding_bwd";
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (!dtype_ok(dtype) || !dtype_ok(dweight_dtype)) return fail(SCAPE_EINVAL, "unknown dtype");
-  if (!size_ok(count) || !size_ok(vocab) || !size_ok(cols)) return fail(SCAPE_EINVAL, "a size is out of range");
+  if (!size_ok(count) || !size_ok(vocab) || !cols_ok(cols)) return fail(SCAPE_EINVAL, "a size is out of range");
   if (vocab == 0) return fail(SCAPE_EINVAL, "vocab must be at least 1");
   if (cols == 0) return SCAPE_OK;
   const size_t ge = elem_size(dweight_dtype);
@@ -123,7 +127,7 @@ extern "C" int scape_layer_token_logprobs(const void* logits, int64_t ldx, int d
                                           float* lse, float* entropy, float* top_logprob, int64_t* top_token,
                                           void* stream) {
   if (!dtype_ok(dtype)) return fail(SCAPE_EINVAL, "unknown dtype");
-  if (!size_ok(rows) || !size_ok(vocab)) return fail(SCAPE_EINVAL, "rows or vocab out of range");
+  if (!size_ok(rows) || !cols_ok(vocab)) return fail(SCAPE_EINVAL, "rows or vocab out of range");
   if (vocab == 0) return fail(SCAPE_EINVAL, "vocab must be at least 1");
   if (top < 0 || top > SCAPE_TOP_MAX || top > vocab) return fail(SCAPE_EINVAL, "top must be 0 to 32, and at most vocab");
   if (top && vocab > SCAPE_TOP_VOCAB_MAX) return fail(SCAPE_EINVAL, "vocab is too large for alternatives");
@@ -152,7 +156,7 @@ extern "C" int scape_layer_token_logprobs_bwd(const void* logits, int64_t ldx, i
                                               const float* dlogprob, const float* entropy, const float* dentropy,
                                               void* dlogits, int64_t lddx, void* stream) {
   if (!dtype_ok(dtype)) return fail(SCAPE_EINVAL, "unknown dtype");
-  if (!size_ok(rows) || !size_ok(vocab)) return fail(SCAPE_EINVAL, "rows or vocab out of range");
+  if (!size_ok(rows) || !cols_ok(vocab)) return fail(SCAPE_EINVAL, "rows or vocab out of range");
   if (vocab == 0) return fail(SCAPE_EINVAL, "vocab must be at least 1");
   if (rows == 0) return SCAPE_OK;
   int rc = check_logits(logits, ldx, dtype, targets, token_bytes, vocab);
@@ -183,7 +187,7 @@ extern "C" int scape_layer_token_loss_workspace(const void* logits, int64_t ldx,
                                                 int64_t vocab, const void* dlogits, int64_t lddx, size_t* bytes) {
   if (!bytes) return fail(SCAPE_EINVAL, "bytes is NULL");
   if (!dtype_ok(dtype)) return fail(SCAPE_EINVAL, "unknown dtype");
-  if (!size_ok(rows) || !size_ok(vocab)) return fail(SCAPE_EINVAL, "rows or vocab out of range");
+  if (!size_ok(rows) || !cols_ok(vocab)) return fail(SCAPE_EINVAL, "rows or vocab out of range");
   *bytes = rows && vocab && !loss_on_chip(logits, ldx, dtype, rows, vocab, dlogits, lddx) ? round256((size_t)rows * 4) : 0;
   return SCAPE_OK;
 }
@@ -193,7 +197,7 @@ extern "C" int scape_layer_token_loss(const void* logits, int64_t ldx, int dtype
                                       float weight_all, float* loss, void* dlogits, int64_t lddx, void* workspace,
                                       size_t ws_bytes, void* stream) {
   if (!dtype_ok(dtype)) return fail(SCAPE_EINVAL, "unknown dtype");
-  if (!size_ok(rows) || !size_ok(vocab)) return fail(SCAPE_EINVAL, "rows or vocab out of range");
+  if (!size_ok(rows) || !cols_ok(vocab)) return fail(SCAPE_EINVAL, "rows or vocab out of range");
   if (vocab == 0) return fail(SCAPE_EINVAL, "vocab must be at least 1");
   if (rows == 0) return SCAPE_OK;
   int rc = check_logits(logits, ldx, dtype, targets, token_bytes, vocab);

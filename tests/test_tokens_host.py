@@ -37,6 +37,7 @@ def test_embedding(lib):
     refused(lib, f(count=1 << 31), "range")
     refused(lib, f(vocab=0), "vocab")
     refused(lib, f(vocab=-5), "range")
+    refused(lib, f(cols=(1 << 30) + 1, ldw=1 << 31, ldy=1 << 31), "range")
     refused(lib, f(w=None), "weight")
     refused(lib, f(w=2 * A + 1), "weight")
     refused(lib, f(ldw=63), "stride")
@@ -89,6 +90,7 @@ def test_logprobs(lib):
     refused(lib, f(t=2 * A + 4), "targets")
     refused(lib, f(tb=16), "token_bytes")
     refused(lib, f(rows=-1), "range")
+    refused(lib, f(vocab=(1 << 30) + 1, ldx=1 << 31), "range")
     refused(lib, f(vocab=0), "vocab")
     refused(lib, f(top=33), "top")
     refused(lib, f(top=-1), "top")
