@@ -11,10 +11,9 @@
 // token (stable: integers only), cut into tiles of kEmbedTile that blocks add up in
 // 32 bits; a token with many positions leaves partial sums, joined in the tiles' order
 // by a last launch.  Most rows of a large table have no token, and writing their zeros
-// is most of the bytes: that goes on beside the sums, a row a warp (32 rows a warp:
-// 58 us instead of 26 for 32000 x 2048 from 1000 tokens).
+// is most of the bytes: that goes on beside the sums.
 //
-// 50304 x 1024 from 8192 tokens of a text, bfloat16: 29 us (sort 6, sums and zeros 20,
+// 50304 x 1024 from 8192 tokens of a text, bfloat16: 29 us (sort 6, sums and zeros 18,
 // join 6, under ncu), its bytes at the copy rate 17.6.  The three launches wait for
 // each other; each has a latency of 3 us or more.
 #include <algorithm>
@@ -241,7 +240,7 @@ __device__ __forceinline__ void put(T* p, int n, bool aligned, const float (&v)[
   }
 }
 
-constexpr int kTileThreads = 160;  // at most: 16 x 160 x 16 bytes stay below 48 KB
+constexpr int kTileThreads = 160;  // at most: 16 x 161 x 16 bytes stay below 48 KB
 
 // Zeros for one warp's row of any alignment.
 template <typename T>
@@ -271,11 +270,12 @@ static_assert(kWindow == 64, "a bit for each, in words of 32");
 
 template <typename TD, typename TG, bool ANY>
 __global__ __launch_bounds__(kTileThreads) void embed_sum_kernel(const __grid_constant__ EmbedBwd a, int fill,
-                                                                 int chunks, bool dw16, uint32_t sms) {
+                                                                 int fill_rows, int chunks, bool dw16, uint32_t sms) {
   start();
   constexpr int VEC = 16 / (int)sizeof(TD);
-  extern __shared__ __align__(16) uint4 staged[];  // [2][kStage][threads]
-  __shared__ int position[kWindow], token[kWindow];
+  extern __shared__ __align__(16) uint4 staged[];  // [2][kStage][pitch]
+  __shared__ uintptr_t address[kWindow];  // of the block's columns in an entry's row
+  __shared__ int token[kWindow];
   __shared__ int2 ends[2];  // where the tile's first and last entry's tokens start and end
   TG* dw = static_cast<TG*>(a.dw);
   // tiles and rows of zeros in turn, as long as there are both: the ones wait for
@@ -285,19 +285,23 @@ __global__ __launch_bounds__(kTileThreads) void embed_sum_kernel(const __grid_co
   const bool is_sum = (int)blockIdx.x < both ? (blockIdx.x + blockIdx.x / sms) % 2 == 0 : sums > fill;
   const int job = (int)blockIdx.x < both ? blockIdx.x / 2 : (int)blockIdx.x - both / 2;
   if (!is_sum) {
-    // a row a warp: few stores each and many in flight
-    const int64_t v = (int64_t)job * (blockDim.x >> 5) + (threadIdx.x >> 5);
-    if (v < a.vocab && a.starts[v] == a.starts[v + 1]) zero_row(dw + v * a.lddw, a.cols, threadIdx.x & 31);
+    const int lane = threadIdx.x & 31;
+    const int64_t v0 = ((int64_t)job * (blockDim.x >> 5) + (threadIdx.x >> 5)) * fill_rows;
+    const bool none = lane < fill_rows && v0 + lane < a.vocab && a.starts[v0 + lane] == a.starts[v0 + lane + 1];
+    for (uint32_t left = __ballot_sync(0xFFFFFFFFu, none); left; left &= left - 1)
+      zero_row(dw + (v0 + __ffs(left) - 1) * a.lddw, a.cols, lane);
     return;
   }
   const int tile = job / chunks, chunk = job % chunks;
   const int i0 = tile * kEmbedTile;
+  const int cs = chunk * (int)blockDim.x * VEC;
+  const TD* dy = static_cast<const TD*>(a.dy);
   const int valid = a.starts[a.vocab], last = min(valid - 1, i0 + kEmbedTile - 1) - i0;
   for (int i = threadIdx.x; i < kWindow; i += blockDim.x) {
     // (there are count entries, of which the first `valid` mean something)
     int4 e = i0 + i < a.tokens.count ? a.entries[i0 + i] : make_int4(0, -1, 0, 0);
     if (i0 + i >= valid) e.y = -1;
-    position[i] = e.x;
+    address[i] = reinterpret_cast<uintptr_t>(dy + (int64_t)e.x * a.lddy + cs);
     token[i] = e.y;
     if (i == 0) ends[0] = make_int2(e.z, e.w);
     if (i == last) ends[1] = make_int2(e.z, e.w);
@@ -324,52 +328,80 @@ __global__ __launch_bounds__(kTileThreads) void embed_sum_kernel(const __grid_co
     lasts |= (uint64_t)__ballot_sync(0xFFFFFFFFu, i + 1 >= kWindow || token[i] != token[i + 1]) << h;
   }
   lasts |= 1ull << ((end - 1 - i0) & 63);
-  const int c0 = (chunk * (int)blockDim.x + (int)threadIdx.x) * VEC;
+  const int c0 = cs + (int)threadIdx.x * VEC;
   const int mine = a.cols - c0;
-  if (mine <= 0) return;
-  const TD* dy = static_cast<const TD*>(a.dy);
-  const TD* hi = dy + (a.tokens.count - 1) * a.lddy + a.cols;
+  if (!ANY && mine <= 0) return;
   uint64_t sum[VEC / 2];  // pairs
 #pragma unroll
   for (int i = 0; i < VEC / 2; ++i) sum[i] = 0;
-  // kStage entries' rows are on their way while as many are added up
+  // kStage entries' rows are on their way while as many are added up, every thread's
+  // piece at a place of its own.  ANY: the rows are on no 16-byte boundaries; what the
+  // block's columns lie in is copied from the boundary before them on, a piece more
+  // than there are threads, and a thread's values are put together from two pieces.
+  const int pitch = (int)blockDim.x + (ANY ? 1 : 0);
+  const uint32_t width = min(a.cols - cs, (int)blockDim.x * VEC) * (uint32_t)sizeof(TD);
+  const uintptr_t lo = reinterpret_cast<uintptr_t>(dy);
+  const uintptr_t hi = reinterpret_cast<uintptr_t>(dy + (a.tokens.count - 1) * a.lddy + a.cols);
+  auto copy = [&](const uint4* to, uintptr_t from, int bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(to)),
+                 "l"(from), "r"(bytes)
+                 : "memory");
+  };
   auto stage = [&](int at, int half) {
-    uint4* to = staged + half * kStage * blockDim.x + threadIdx.x;
+    uint4* to = staged + half * kStage * pitch;
     const int n = min(kStage, end - at);
-    if constexpr (ANY) {
-      const int want = min(mine, VEC);
-      if (n <= 0) return;
-      AnyLoad<TD, VEC> any[kStage];
-#pragma unroll
-      for (int k = 0; k < kStage; ++k)
-        if (k < n) any[k].begin(dy + (int64_t)position[at - i0 + k] * a.lddy + c0, want, dy, hi);
-#pragma unroll
-      for (int k = 0; k < kStage; ++k)
-        if (k < n) {
-          const Raw<TD, VEC> r = any[k].end(dy + (int64_t)position[at - i0 + k] * a.lddy + c0, want);
-          to[k * blockDim.x] = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
+    for (int l = 0; l < n; ++l, to += pitch) {
+      const uintptr_t row = address[at - i0 + l];
+      if constexpr (!ANY) {
+        copy(to + threadIdx.x, row + threadIdx.x * 16, min(mine, VEC) * (int)sizeof(TD));
+      } else {
+        const uint32_t off = (uint32_t)row & 15u;
+        for (uint32_t j = threadIdx.x; j <= blockDim.x && j * 16 < off + width; j += blockDim.x) {
+          const uintptr_t from = row - off + j * 16;
+          if (from >= lo) {
+            copy(to + j, from, (int)min((uint64_t)16, (uint64_t)(hi - from)));
+          } else {
+            // the matrix starts inside this piece
+            for (int k = 0; k < VEC; ++k)
+              if (from + k * sizeof(TD) >= lo && from + k * sizeof(TD) < hi)
+                reinterpret_cast<TD*>(to + j)[k] = reinterpret_cast<const TD*>(from)[k];
+          }
         }
-    } else {
-      const int bytes = min(mine, VEC) * (int)sizeof(TD);
-      for (int l = 0; l < n; ++l)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
-                         (uint32_t)__cvta_generic_to_shared(to + l * blockDim.x)),
-                     "l"(dy + (int64_t)position[at - i0 + l] * a.lddy + c0), "r"(bytes)
-                     : "memory");
-      asm volatile("cp.async.commit_group;" ::: "memory");
+      }
     }
+    asm volatile("cp.async.commit_group;" ::: "memory");
   };
   stage(begin, 0);
   int half = 0;
   for (int at = begin; at < end; at += kStage, half ^= 1) {
     const int n = min(kStage, end - at);
+    if (ANY) __syncthreads();  // the other half has been read
     stage(at + kStage, half ^ 1);
-    if (!ANY) asm volatile("cp.async.wait_group 1;" ::: "memory");
-    const uint4* from = staged + half * kStage * blockDim.x + threadIdx.x;
-    for (int l = 0; l < n; ++l) {
-      const uint4 u = from[l * blockDim.x];
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+    if (ANY) __syncthreads();
+    const uint4* from = staged + half * kStage * pitch + threadIdx.x;
+    for (int l = 0; l < n; ++l, from += pitch) {
+      if (ANY && mine <= 0) break;
+      const uint4 u = *from;
       Raw<TD, VEC> r;
-      r.w[0] = u.x, r.w[1] = u.y, r.w[2] = u.z, r.w[3] = u.w;
+      if constexpr (ANY) {
+        const uint4 next = from[1];
+        const uint32_t off = (uint32_t)address[at + l - i0] & 15u;
+        uint32_t w[8] = {u.x, u.y, u.z, u.w, next.x, next.y, next.z, next.w};
+        if (off & 8) {
+#pragma unroll
+          for (int j = 0; j < 6; ++j) w[j] = w[j + 2];
+        }
+        if (off & 4) {
+#pragma unroll
+          for (int j = 0; j < 5; ++j) w[j] = w[j + 1];
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          r.w[j] = sizeof(TD) == 4 ? w[j] : __funnelshift_r(w[j], w[j + 1], (off & 2) * 8);
+      } else {
+        r.w[0] = u.x, r.w[1] = u.y, r.w[2] = u.z, r.w[3] = u.w;
+      }
       float f[VEC];
       to_floats(r, f);
 #pragma unroll
@@ -507,15 +539,20 @@ cudaError_t run_embedding_bwd(const EmbedBwd& a, cudaStream_t st) {
   const int64_t parts = ceil_div(vecs, kTileThreads);
   const int threads = (int)(ceil_div(ceil_div(vecs, parts), 32) * 32);
   const int64_t chunks = ceil_div(vecs, threads);
-  const int64_t fill = a.accumulate ? 0 : ceil_div(a.vocab, threads / 32);
+  // Rows of zeros a warp: enough to be worth a block's launch (77248 rows of 64 in
+  // bfloat16 for 592 tokens: one a warp 86 us, 16 a warp 17; 50304 of 1024 for 8192 spread
+  // evenly: one 28, two 25), and no more, as few warps have few stores in flight (32000 of 2048
+  // for 1000: one 26, 32 a warp 58).
+  const int fill_rows = (int)std::min<int64_t>(16, std::max<int64_t>(1, 4096 / ((int64_t)a.cols * (int)sizeof(TG))));
+  const int64_t fill = a.accumulate ? 0 : ceil_div(a.vocab, fill_rows * (threads / 32));
   if (tiles * chunks + fill > 0x7FFFFFFF) return cudaErrorInvalidValue;
-  const size_t smem = (size_t)2 * kStage * threads * 16;
   const bool any = !rows16(a.dy, a.lddy, sizeof(TD));
+  const size_t smem = (size_t)2 * kStage * (threads + (any ? 1 : 0)) * 16;
   // whether VEC of the output's elements can be stored together
   const bool dw16 = aligned(a.dw, std::min<size_t>(16, VEC * sizeof(TG))) &&
                     (a.lddw * sizeof(TG)) % std::min<size_t>(16, VEC * sizeof(TG)) == 0;
   e = launch_kernel(any ? embed_sum_kernel<TD, TG, true> : embed_sum_kernel<TD, TG, false>,
-                    (unsigned)(tiles * chunks + fill), threads, smem, 0, st, a, (int)fill, (int)chunks, dw16,
+                    (unsigned)(tiles * chunks + fill), threads, smem, 0, st, a, (int)fill, fill_rows, (int)chunks, dw16,
                     (uint32_t)(sm_count() / 2 * 2));
   if (e != cudaSuccess) return e;
   if (a.tokens.count <= kLong) return e;  // no token has so many

@@ -127,8 +127,9 @@ __device__ __forceinline__ Raw<T, VEC> load_any(const T* p, int n, const T* lo, 
 // The same in two steps, so that a thread's loads are in flight together: the
 // branches of load_any() keep one waiting for the other.  begin() loads the aligned
 // words that hold VEC elements (one word more than they are), end() puts the elements
-// together; where those words do not lie in the matrix entirely, or fewer than VEC
-// elements are wanted, end() reads element by element.
+// together; where those words do not lie in the matrix entirely, end() reads element
+// by element.  Of fewer than VEC elements (n, at a row's end) the others are what
+// follows in the matrix, or 0.
 template <typename T, int VEC>
 struct AnyLoad {
   static constexpr int kPer = 16 / sizeof(T), kPieces = VEC / kPer;
@@ -138,8 +139,8 @@ struct AnyLoad {
   __device__ __forceinline__ void begin(const T* p, int n, const T* lo, const T* hi) {
     off = (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15u);
     const char* a = reinterpret_cast<const char*>(p) - off;
-    fast = n >= VEC && (off == 0 || (a >= reinterpret_cast<const char*>(lo) &&
-                                     a + 16 * (kPieces + 1) <= reinterpret_cast<const char*>(hi)));
+    fast = n > 0 && a >= reinterpret_cast<const char*>(lo) &&
+           a + 16 * (kPieces + (off ? 1 : 0)) <= reinterpret_cast<const char*>(hi);
 #pragma unroll
     for (int i = 0; i <= kPieces; ++i)
       if (fast && (i < kPieces || off)) w[i] = reinterpret_cast<const uint4*>(a)[i];

@@ -645,7 +645,9 @@ __global__ __launch_bounds__(kMaxThreads) void token_loss_kernel(const __grid_co
 // masked whole with the type's lowest value: lse is that value, and exp(x - lse)
 // would be 1 everywhere), so the row's sums are formed again.
 constexpr float kFarLse = 4096.0f;
-constexpr int kBwdThreads = 256, kBwdUnroll = 4;
+constexpr int kBwdThreads = 256;
+template <bool ANY>
+constexpr int kBwdUnroll = ANY ? 2 : 4;
 
 // Such a row, by one block, which alone reads and writes it.
 template <typename T, bool ENT>
@@ -670,13 +672,13 @@ __device__ __noinline__ void far_row(const T* x, T* dx, int cols, int64_t target
 }
 
 // A block takes kBwdUnroll pieces a thread of one row, on the output's boundaries.
-// ANY: they are on no boundaries of the logits' rows (the loads' registers are twice as
-// many, 117 us instead of 81 for 4096 x 32000).
+// ANY: they are on no boundaries of the logits' rows, and a load is two (4096 x 32000
+// in bfloat16 without entropy: 81 us, ANY 98; with four pieces at a time 112).
 template <typename T, bool ENT, bool ANY>
 __global__ __launch_bounds__(kBwdThreads) void logprobs_bwd_kernel(const __grid_constant__ LogprobsBwd a, int chunks,
                                                                 int64_t rows) {
   start();
-  constexpr int kPer = RowPieces<T>::kPer;
+  constexpr int kPer = RowPieces<T>::kPer, U = kBwdUnroll<ANY>;
   const int64_t row = blockIdx.x / chunks;
   const int chunk = (int)(blockIdx.x % chunks);
   const T* x = static_cast<const T*>(a.x) + row * a.ldx;
@@ -694,12 +696,12 @@ __global__ __launch_bounds__(kBwdThreads) void logprobs_bwd_kernel(const __grid_
     if (chunk == 0) far_row<T, ENT>(x, dx, (int)a.vocab, target, g, dh, h);
     return;
   }
-  const int first = chunk * (kBwdUnroll * (int)blockDim.x) + (int)threadIdx.x;
+  const int first = chunk * (U * (int)blockDim.x) + (int)threadIdx.x;
   const uint64_t minus = pair(-lse, -lse), log2e = pair(kLog2eF, kLog2eF);
-  AnyLoad<T, kPer> any[kBwdUnroll];
-  uint4 plain[kBwdUnroll] = {};
+  AnyLoad<T, kPer> any[U];
+  uint4 plain[U] = {};
 #pragma unroll
-  for (int i = 0; i < kBwdUnroll; ++i) {
+  for (int i = 0; i < U; ++i) {
     const int v = first + i * blockDim.x, c = out.column(v);
     const int n = !none && v < out.pieces && out.whole(v) ? kPer : 0;
     if constexpr (ANY)
@@ -708,7 +710,7 @@ __global__ __launch_bounds__(kBwdThreads) void logprobs_bwd_kernel(const __grid_
       plain[i] = *reinterpret_cast<const uint4*>(x + c);
   }
 #pragma unroll
-  for (int i = 0; i < kBwdUnroll; ++i) {
+  for (int i = 0; i < U; ++i) {
     const int v = first + i * blockDim.x;
     if (v >= out.pieces) continue;
     const int c = out.column(v);
@@ -841,10 +843,11 @@ cudaError_t run_logprobs(const Logprobs& a, cudaStream_t st) {
 template <typename T>
 cudaError_t run_logprobs_bwd(const LogprobsBwd& a, cudaStream_t st) {
   const int64_t pieces = ceil_div(a.vocab + RowPieces<T>::kPer - 1, RowPieces<T>::kPer);
-  const int threads = threads_for(ceil_div(pieces, kBwdUnroll), kBwdThreads);
-  const int64_t chunks = ceil_div(pieces, threads * kBwdUnroll), grid = a.targets.count * chunks;
-  if (grid > 0x7FFFFFFF) return cudaErrorInvalidValue;
   const bool same = same_places(a.x, a.ldx, a.dx, a.lddx, sizeof(T));
+  const int unroll = same ? kBwdUnroll<false> : kBwdUnroll<true>;
+  const int threads = threads_for(ceil_div(pieces, unroll), kBwdThreads);
+  const int64_t chunks = ceil_div(pieces, threads * unroll), grid = a.targets.count * chunks;
+  if (grid > 0x7FFFFFFF) return cudaErrorInvalidValue;
   auto* const kernel = a.dentropy ? (same ? logprobs_bwd_kernel<T, true, false> : logprobs_bwd_kernel<T, true, true>)
                                   : (same ? logprobs_bwd_kernel<T, false, false> : logprobs_bwd_kernel<T, false, true>);
   return launch_kernel(kernel, (unsigned)grid, threads, 0, 0, st, a, (int)chunks, a.targets.count);
