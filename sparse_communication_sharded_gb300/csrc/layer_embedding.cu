@@ -10,12 +10,12 @@
 // in an order that changes, and in the output's type.  So the positions are sorted by
 // token (stable: integers only), cut into tiles of kEmbedTile that blocks add up in
 // 32 bits; a token with many positions leaves partial sums, joined in the tiles' order
-// by a last launch.  Most rows of a large table have no token, and writing their zeros
-// is most of the bytes: that goes on beside the sums.
+// by blocks that are done last.  Most rows of a large table have no token, and writing
+// their zeros is most of the bytes: that goes on beside the sums.
 //
-// 50304 x 1024 from 8192 tokens of a text, bfloat16: 29 us (sort 6, sums and zeros 18,
-// join 6, under ncu), its bytes at the copy rate 17.6.  The three launches wait for
-// each other; each has a latency of 3 us or more.
+// 50304 x 1024 from 8192 tokens of a text, bfloat16: 28.4 to 29.3 us (sort 8, sums and
+// zeros 22, each alone under ncu), its bytes at the copy rate 17.6.  The second launch
+// waits for the first, which writes nothing but the order.
 #include <algorithm>
 
 #include "layer_tokens.h"
@@ -126,7 +126,7 @@ static_assert(kSortRows <= kSortThreads && kSortWarps <= 32, "a thread for each 
 template <typename I>
 __global__ __launch_bounds__(kSortThreads) void sort_tokens_kernel(const I* __restrict__ tokens, int64_t count,
                                                                    int64_t vocab, int rows, int4* entries,
-                                                                   int* starts) {
+                                                                   int* starts, int* arrived, int64_t arrivals) {
   extern __shared__ __align__(8) int counts[];  // [kSortWarps][rows], rows even
   int2* const kept_of = reinterpret_cast<int2*>(counts + kSortWarps * rows);  // [kSortWarps][kSortKept]
   __shared__ int below_of[kSortWarps], sums[kSortWarps];
@@ -136,6 +136,8 @@ __global__ __launch_bounds__(kSortThreads) void sort_tokens_kernel(const I* __re
   const int mine = (int)min((int64_t)rows, vocab - lo);
   for (int i = threadIdx.x; i < kSortWarps * rows; i += kSortThreads) counts[i] = 0;
   start();
+  const int64_t all = (int64_t)gridDim.x * kSortThreads;
+  for (int64_t i = (int64_t)blockIdx.x * kSortThreads + threadIdx.x; i < arrivals; i += all) arrived[i] = 0;
   __syncthreads();
   const int64_t share = (count + kSortThreads - 1) / kSortThreads * 32;
   const int64_t begin = min(count, warp * share), end = min(count, begin + share);
@@ -256,17 +258,22 @@ __device__ __forceinline__ void zero_row(T* p, int cols, int lane) {
 }
 
 // Blocks write rows of zeros, or add up some columns of a tile's entries: those of the
-// tokens that start in it.  A token with more than kLong entries is cut into parts of
-// kPart tiles, from the one where it starts on, each summed by the block of its first
-// tile and left in `partial` for the join: so a common word is spread over blocks, and
-// few tokens need a join.  (Parts of 4 tiles: with 2 a padded batch's join is longer,
-// 32000 x 1280 from 16384 tokens 45 -> 48 us, with 8 the sum is, 38 -> 45 for 50304 x
-// 1024 from 8192.)
-constexpr int kLong = 2 * kEmbedTile, kPart = 4, kStage = 8;
-// entries that a tile's block may go through: a part of a long token, or the tile's and
-// those of a short token from its last one on
-constexpr int kWindow = (kPart > 3 ? kPart : 3) * kEmbedTile;
+// tokens that start in it.  A long token, one that reaches over more than kPart tiles,
+// is cut into parts of as many, from the tile where it starts on, each summed by the
+// block of its first tile and left in `partial`; of every few parts the block that is
+// done last (nobody waits) adds them up in their order, whichever it is.  So a common
+// word is spread over blocks.  (Parts of 4 tiles: with 2 a padded batch's common token
+// has more to join, 32000 x 1280 from 16384 tokens 45 -> 48 us, with 8 the sums take
+// longer, 38 -> 45 for 50304 x 1024 from 8192.  A launch of its own to join them was
+// 0.5 to 1.5 us slower for these and 5 for 50304 x 1024 in float32.  All of a token's
+// parts by one block: 32000 x 512 from 65536 tokens 51 us, by eights 42.2, by sixteens
+// 43.8; there a token of 9 to 16 parts needs one step less, 50304 x 1024 28.2 for 29.2.)
+constexpr int kPart = 4, kStage = 8;
+constexpr int kWindow = kPart * kEmbedTile;  // entries that a tile's block may go through
 static_assert(kWindow == 64, "a bit for each, in words of 32");
+constexpr int kGroup = 8, kLevels = kPart;  // of joining a long token's parts
+// Of a token's entries [x, y).
+__device__ __forceinline__ int parts_of(int2 e) { return ((e.y - 1) / kEmbedTile - e.x / kEmbedTile) / kPart + 1; }
 
 template <typename TD, typename TG, bool ANY>
 __global__ __launch_bounds__(kTileThreads) void embed_sum_kernel(const __grid_constant__ EmbedBwd a, int fill,
@@ -277,6 +284,7 @@ __global__ __launch_bounds__(kTileThreads) void embed_sum_kernel(const __grid_co
   __shared__ uintptr_t address[kWindow];  // of the block's columns in an entry's row
   __shared__ int token[kWindow];
   __shared__ int2 ends[2];  // where the tile's first and last entry's tokens start and end
+  __shared__ int is_last;
   TG* dw = static_cast<TG*>(a.dw);
   // tiles and rows of zeros in turn, as long as there are both: the ones wait for
   // loads, the others use what bandwidth is left.  (Blocks go round the SMs, of which
@@ -306,20 +314,17 @@ __global__ __launch_bounds__(kTileThreads) void embed_sum_kernel(const __grid_co
     if (i == 0) ends[0] = make_int2(e.z, e.w);
     if (i == last) ends[1] = make_int2(e.z, e.w);
   }
-  if (last < 0) {
-    if (chunk == 0 && threadIdx.x == 0) a.crossing[tile] = -1;
-    return;
-  }
+  if (last < 0) return;
   __syncthreads();
   const int i1 = i0 + last + 1;
   const int2 head = ends[0], tail = ends[1];
-  const bool head_long = head.y - head.x > kLong, tail_long = tail.y - tail.x > kLong;
+  const int head_parts = parts_of(head), tail_parts = parts_of(tail);
+  const bool head_long = head_parts > 1, tail_long = tail_parts > 1;
   // the first token: its part from here on, or nothing if it is another block's
   const bool head_here = head.x >= i0 || (head_long && (tile - head.x / kEmbedTile) % kPart == 0);
   const int begin = head_here ? i0 : min(head.y, i1);
-  int end = tail.x >= i0 || begin < i1 ? min(tail.y, tail_long ? i0 + kPart * kEmbedTile : tail.y) : begin;
+  int end = tail.x >= i0 || begin < i1 ? min(tail.y, i0 + kWindow) : begin;
   if (tail.x < i0 && !head_here) end = begin;  // all of the tile is that token's
-  if (chunk == 0 && threadIdx.x == 0) a.crossing[tile] = tail_long && tail.x >= i0 ? token[last] : -1;
   // bit i: entry i0 + i is its token's last here
   uint64_t lasts = 0;
 #pragma unroll
@@ -329,8 +334,17 @@ __global__ __launch_bounds__(kTileThreads) void embed_sum_kernel(const __grid_co
   }
   lasts |= 1ull << ((end - 1 - i0) & 63);
   const int c0 = cs + (int)threadIdx.x * VEC;
-  const int mine = a.cols - c0;
-  if (!ANY && mine <= 0) return;
+  const int mine = a.cols - c0;  // may be 0 or less
+  // a row's columns from their sum
+  auto write = [&](int v, float (&acc)[VEC]) {
+    TG* p = dw + (int64_t)v * a.lddw + c0;
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) {
+      acc[k] *= a.scale;
+      if (a.accumulate && k < mine) acc[k] += (float)p[k];
+    }
+    put<TG, VEC>(p, mine, dw16, acc);
+  };
   uint64_t sum[VEC / 2];  // pairs
 #pragma unroll
   for (int i = 0; i < VEC / 2; ++i) sum[i] = 0;
@@ -353,7 +367,7 @@ __global__ __launch_bounds__(kTileThreads) void embed_sum_kernel(const __grid_co
     for (int l = 0; l < n; ++l, to += pitch) {
       const uintptr_t row = address[at - i0 + l];
       if constexpr (!ANY) {
-        copy(to + threadIdx.x, row + threadIdx.x * 16, min(mine, VEC) * (int)sizeof(TD));
+        if (mine > 0) copy(to + threadIdx.x, row + threadIdx.x * 16, min(mine, VEC) * (int)sizeof(TD));
       } else {
         const uint32_t off = (uint32_t)row & 15u;
         for (uint32_t j = threadIdx.x; j <= blockDim.x && j * 16 < off + width; j += blockDim.x) {
@@ -381,7 +395,7 @@ __global__ __launch_bounds__(kTileThreads) void embed_sum_kernel(const __grid_co
     if (ANY) __syncthreads();
     const uint4* from = staged + half * kStage * pitch + threadIdx.x;
     for (int l = 0; l < n; ++l, from += pitch) {
-      if (ANY && mine <= 0) break;
+      if (mine <= 0) break;
       const uint4 u = *from;
       Raw<TD, VEC> r;
       if constexpr (ANY) {
@@ -417,13 +431,7 @@ __global__ __launch_bounds__(kTileThreads) void embed_sum_kernel(const __grid_co
       }
       const bool of_head = i < head.y;
       if (of_head ? !head_long : i < tail.x || !tail_long) {
-        TG* p = dw + (int64_t)v * a.lddw + c0;
-#pragma unroll
-        for (int k = 0; k < VEC; ++k) {
-          acc[k] *= a.scale;
-          if (a.accumulate && k < mine) acc[k] += (float)p[k];
-        }
-        put<TG, VEC>(p, mine, dw16, acc);
+        write(v, acc);
       } else {
         // first the sum of what started before the tile, second of what starts in it
         float* p = a.partial + ((int64_t)tile * 2 + (of_head && head.x < i0 ? 0 : 1)) * a.partial_pitch + c0;
@@ -431,79 +439,56 @@ __global__ __launch_bounds__(kTileThreads) void embed_sum_kernel(const __grid_co
       }
     }
   }
-}
-
-// ------------------------------------------------------------------ joining
-// Item (tile, 128 columns): the sum of the long token that starts in the tile, its
-// parts in order by a warp, or, where they are many, a share of them by each of the
-// block's warps, and these in order.  A block first looks at all its items' tiles.
-constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32, kJoinCols = 128, kJoinAlone = 12;
-
-template <typename TG>
-__global__ __launch_bounds__(kJoinThreads) void embed_join_kernel(const __grid_constant__ EmbedBwd a, int tiles,
-                                                                  int chunks) {
-  start();
-  __shared__ int4 found[kJoinThreads];  // tile, its token, the token's last tile, columns
-  __shared__ float4 share[kJoinWarps][32];
-  __shared__ int finds;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t items = (int64_t)tiles * chunks;
-  // parts first, first + step, ... of an item; part 0 is the tile's second sum, others
-  // are their tiles' first
-  auto sum_parts = [&](const int4& e, int c0, int parts, int first, int step) {
-    float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  // A long token of which a part is done.  Parts are joined by eights, the eighths' sums
+  // by eights again, and so on, each time by the block that comes last: its sum takes
+  // the place of the first.  A group of two or more counts in its first part's first
+  // tile, a level's at as many tiles further on: that part is not the token's last, so
+  // its kPart tiles are all there and no other token counts in them.
+  auto join = [&](int v, const int2& e, int units, int unit) {
+    const int t0 = e.x / kEmbedTile;
+    for (int level = 0, width = 1;; ++level, width *= kGroup) {
+      const int first = level < kLevels - 1 ? unit / kGroup * kGroup : 0;
+      const int count = level < kLevels - 1 ? min(kGroup, units - first) : units;
+      unit /= kGroup;
+      if (count == 1) {  // its sum stays where it is
+        units = (units + kGroup - 1) / kGroup;
+        continue;
+      }
+      __threadfence();
+      __syncthreads();
+      if (threadIdx.x == 0)
+        is_last = atomicAdd(&a.arrived[((int64_t)t0 + (int64_t)first * width * kPart + level) * chunks + chunk], 1) ==
+                  count - 1;
+      __syncthreads();
+      if (!is_last) return;
+      __threadfence();
+      float acc[VEC];
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) acc[i] = 0.0f;
+      auto place = [&](int k) {  // of the k-th unit's sum
+        return a.partial + (((int64_t)t0 + (int64_t)k * width * kPart) * 2 + (k == 0 ? 1 : 0)) * a.partial_pitch + c0;
+      };
+      if (mine > 0) {
 #pragma unroll 8
-    for (int k = first; k < parts; k += step) {
-      const float4 q = *reinterpret_cast<const float4*>(
-          a.partial + ((int64_t)(e.x + k * kPart) * 2 + (k == 0 ? 1 : 0)) * a.partial_pitch + c0);
-      s.x += q.x, s.y += q.y, s.z += q.z, s.w += q.w;
-    }
-    return s;
-  };
-  auto write = [&](const int4& e, int c0, const float4& s) {
-    const float f[4] = {s.x, s.y, s.z, s.w};
-    TG* out = static_cast<TG*>(a.dw) + (int64_t)e.y * a.lddw + c0;
+        for (int k = first; k < first + count; ++k) {
+          const float* p = place(k);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (c0 + i < a.cols) out[i] = (TG)(f[i] * a.scale + (a.accumulate ? (float)out[i] : 0.0f));
-  };
-  for (int64_t base = blockIdx.x; base < items; base += (int64_t)gridDim.x * kJoinThreads) {
-    if (threadIdx.x == 0) finds = 0;
-    __syncthreads();
-    const int64_t my = base + (int64_t)threadIdx.x * gridDim.x;
-    if (my < items) {
-      const int tile = (int)(my / chunks), v = a.crossing[tile];
-      if (v >= 0) {
-        const int last = (a.starts[v + 1] - 1) / kEmbedTile;
-        // their order changes nothing
-        found[atomicAdd(&finds, 1)] = make_int4(tile, v, last, (int)(my % chunks) * kJoinCols);
-      }
-    }
-    __syncthreads();
-    for (int k = warp; k < finds; k += kJoinWarps) {
-      const int4 e = found[k];
-      const int parts = (e.z - e.x) / kPart + 1, c0 = e.w + lane * 4;
-      if (parts <= kJoinAlone && c0 < a.cols) write(e, c0, sum_parts(e, c0, parts, 0, 1));
-    }
-    for (int k = 0; k < finds; ++k) {
-      const int4 e = found[k];
-      const int parts = (e.z - e.x) / kPart + 1, c0 = e.w + lane * 4;
-      if (parts <= kJoinAlone) continue;
-      share[warp][lane] = c0 < a.cols ? sum_parts(e, c0, parts, warp, kJoinWarps) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      __syncthreads();
-      if (warp == 0 && c0 < a.cols) {
-        float4 s = share[0][lane];
-#pragma unroll
-        for (int w = 1; w < kJoinWarps; ++w) {
-          const float4 q = share[w][lane];
-          s.x += q.x, s.y += q.y, s.z += q.z, s.w += q.w;
+          for (int i = 0; i < VEC; i += 4) {
+            const float4 q = __ldcg(reinterpret_cast<const float4*>(p + i));
+            acc[i] += q.x, acc[i + 1] += q.y, acc[i + 2] += q.z, acc[i + 3] += q.w;
+          }
         }
-        write(e, c0, s);
+        if (count == units)
+          write(v, acc);
+        else
+          put<float, VEC>(place(first), VEC, true, acc);
       }
-      __syncthreads();
+      if (count == units) return;
+      units = (units + kGroup - 1) / kGroup;
     }
-    __syncthreads();
-  }
+  };
+  if (head_long && head_here) join(token[0], head, head_parts, (tile - head.x / kEmbedTile) / kPart);
+  if (tail_long && tail.x >= i0 && tail.x > head.x) join(token[last], tail, tail_parts, 0);
 }
 
 // ------------------------------------------------------------------ launches
@@ -520,6 +505,12 @@ cudaError_t run_embedding(const EmbedFwd& a, cudaStream_t st) {
 
 template <typename TD, typename TG>
 cudaError_t run_embedding_bwd(const EmbedBwd& a, cudaStream_t st) {
+  constexpr int VEC = 16 / (int)sizeof(TD);
+  const int64_t vecs = ceil_div(a.cols, VEC), tiles = ceil_div(a.tokens.count, kEmbedTile);
+  // equal chunks of at most kTileThreads pieces
+  const int64_t parts = ceil_div(vecs, kTileThreads);
+  const int threads = (int)(ceil_div(ceil_div(vecs, parts), 32) * 32);
+  const int64_t chunks = ceil_div(vecs, threads);
   const int rows = (int)std::min<int64_t>(kSortRows, ceil_div(ceil_div(a.vocab, sm_count()), 2) * 2);
   const unsigned sorters = (unsigned)ceil_div(a.vocab, rows);
   const int bytes = kSortWarps * (rows * 4 + kSortKept * 8);
@@ -528,17 +519,11 @@ cudaError_t run_embedding_bwd(const EmbedBwd& a, cudaStream_t st) {
     if (bytes > 44 * 1024) e = allow_smem((const void*)kernel, bytes);
     if (e != cudaSuccess) return e;
     return launch_kernel(kernel, sorters, kSortThreads, (size_t)bytes, 0, st, tokens, a.tokens.count, a.vocab, rows,
-                         a.entries, a.starts);
+                         a.entries, a.starts, a.arrived, tiles * chunks);
   };
   cudaError_t e = a.tokens.bytes == 8 ? sort(sort_tokens_kernel<int64_t>, static_cast<const int64_t*>(a.tokens.p))
                                       : sort(sort_tokens_kernel<int32_t>, static_cast<const int32_t*>(a.tokens.p));
   if (e != cudaSuccess) return e;
-  constexpr int VEC = 16 / (int)sizeof(TD);
-  const int64_t vecs = ceil_div(a.cols, VEC), tiles = ceil_div(a.tokens.count, kEmbedTile);
-  // equal chunks of at most kTileThreads pieces
-  const int64_t parts = ceil_div(vecs, kTileThreads);
-  const int threads = (int)(ceil_div(ceil_div(vecs, parts), 32) * 32);
-  const int64_t chunks = ceil_div(vecs, threads);
   // Rows of zeros a warp: enough to be worth a block's launch (77248 rows of 64 in
   // bfloat16 for 592 tokens: one a warp 86 us, 16 a warp 17; 50304 of 1024 for 8192 spread
   // evenly: one 28, two 25), and no more, as few warps have few stores in flight (32000 of 2048
@@ -551,19 +536,16 @@ cudaError_t run_embedding_bwd(const EmbedBwd& a, cudaStream_t st) {
   // whether VEC of the output's elements can be stored together
   const bool dw16 = aligned(a.dw, std::min<size_t>(16, VEC * sizeof(TG))) &&
                     (a.lddw * sizeof(TG)) % std::min<size_t>(16, VEC * sizeof(TG)) == 0;
-  e = launch_kernel(any ? embed_sum_kernel<TD, TG, true> : embed_sum_kernel<TD, TG, false>,
-                    (unsigned)(tiles * chunks + fill), threads, smem, 0, st, a, (int)fill, fill_rows, (int)chunks, dw16,
-                    (uint32_t)(sm_count() / 2 * 2));
-  if (e != cudaSuccess) return e;
-  if (a.tokens.count <= kLong) return e;  // no token has so many
-  const int64_t join = ceil_div(a.cols, kJoinCols);
-  return launch_kernel(embed_join_kernel<TG>, (unsigned)std::min<int64_t>(tiles * join, (int64_t)sm_count() * 2),
-                       kJoinThreads, 0, 0, st, a, (int)tiles, (int)join);
+  return launch_kernel(any ? embed_sum_kernel<TD, TG, true> : embed_sum_kernel<TD, TG, false>,
+                       (unsigned)(tiles * chunks + fill), threads, smem, 0, st, a, (int)fill, fill_rows, (int)chunks,
+                       dw16, (uint32_t)(sm_count() / 2 * 2));
 }
 
 }  // namespace
 
 int64_t embed_partial_pitch(int64_t cols) { return ceil_div(cols, 8) * 8; }
+// of pieces of 4 elements (float32 gradients; of 8, half as many)
+int64_t embed_chunks_most(int64_t cols) { return ceil_div(ceil_div(cols, 4), kTileThreads); }
 
 cudaError_t launch_embedding(const EmbedFwd& a, int w_dtype, int dtype, cudaStream_t st) {
   if (w_dtype == SCAPE_BF16)

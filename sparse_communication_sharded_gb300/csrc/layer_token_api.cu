@@ -26,15 +26,15 @@ bool cols_ok(int64_t n) { return n >= 0 && n <= kMaxCols; }
 
 // Where the parts of embedding_bwd's workspace lie.
 struct EmbedSpace {
-  size_t entries, starts, crossing, partial, bytes;
+  size_t entries, starts, arrived, partial, bytes;
 };
 EmbedSpace embed_space(int64_t count, int64_t vocab, int64_t cols) {
   EmbedSpace s;
   const int64_t tiles = ceil_div(count, kEmbedTile);
   s.entries = 0;
   s.starts = round256((size_t)count * sizeof(int4));
-  s.crossing = s.starts + round256((size_t)(vocab + 1) * 4);
-  s.partial = s.crossing + round256((size_t)tiles * 4);
+  s.arrived = s.starts + round256((size_t)(vocab + 1) * 4);
+  s.partial = s.arrived + round256((size_t)tiles * embed_chunks_most(cols) * 4);
   s.bytes = s.partial + round256((size_t)tiles * 2 * embed_partial_pitch(cols) * 4);
   return s;
 }
@@ -108,7 +108,7 @@ extern "C" int scape_layer_embedding_bwd(const void* dy, int64_t lddy, int dtype
   a.dw = dweight, a.lddw = lddw;
   a.entries = reinterpret_cast<int4*>(ws + s.entries);
   a.starts = reinterpret_cast<int*>(ws + s.starts);
-  a.crossing = reinterpret_cast<int*>(ws + s.crossing);
+  a.arrived = reinterpret_cast<int*>(ws + s.arrived);
   a.partial = reinterpret_cast<float*>(ws + s.partial);
   a.partial_pitch = embed_partial_pitch(cols);
   return cuda_result(launch_embedding_bwd(a, dtype, dweight_dtype, st), who);

@@ -38,12 +38,14 @@ struct EmbedBwd {
   int4* entries;   // of the tokens in range, by token, then position: position, token, and
                    // where the token's entries start and end
   int* starts;     // [vocab + 1]: where a token's entries start
-  int* crossing;   // a tile of entries: the token whose entries start in it and go on past it, or -1
-  float* partial;  // [tiles][2][partial_pitch]: sums of entries whose token goes on in another tile
+  int* arrived;    // [tiles][embed_chunks_most()] at most: parts done of the long token that starts
+                   // in a tile, for a block's columns
+  float* partial;  // [tiles][2][partial_pitch]: sums of long tokens' parts
   int64_t partial_pitch;
 };
 constexpr int kEmbedTile = 16;
 int64_t embed_partial_pitch(int64_t cols);
+int64_t embed_chunks_most(int64_t cols);
 cudaError_t launch_embedding_bwd(const EmbedBwd& a, int dtype, int dw_dtype, cudaStream_t st);
 
 struct Logprobs {

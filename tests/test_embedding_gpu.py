@@ -128,6 +128,27 @@ def test_gradient_anywhere(cuda_device, cols, gap, offset, dtype, grad):
     assert bool((flat == 7).all())
 
 
+@pytest.mark.parametrize("lengths", [(65, 64, 66, 80, 81, 96, 1), (512, 513, 528, 529, 577, 576, 16),
+                                     (4097, 4095, 33, 4161, 4672), (32769, 17, 33344, 32704), (300001, 64, 65)])
+@pytest.mark.parametrize("cols", [8, 13, 2056])
+@pytest.mark.parametrize("before", [0, 7])
+def test_gradient_of_common_tokens(cuda_device, lengths, cols, before):
+    """Tokens with many positions side by side: whole values below 2^24 in all, so the sums
+    are exact in any order and each position counts once."""
+    lengths = ((before,) if before else ()) + lengths
+    if cols > 100:
+        lengths = tuple(n % 40000 for n in lengths)
+    t = torch.repeat_interleave(torch.arange(len(lengths)), torch.tensor(lengths)).cuda()
+    g = torch.Generator(device="cuda").manual_seed(cols)
+    order = torch.randperm(t.numel(), device="cuda", generator=g)
+    dy = torch.randint(-8, 9, (t.numel(), cols), device="cuda", generator=g)
+    dy[:, 0] = 1  # counts
+    want = torch.zeros(len(lengths), cols, dtype=torch.float64, device="cuda").index_add_(0, t, dy.double())
+    for at in (torch.arange(t.numel(), device="cuda"), order):
+        dw = L.embedding_backward(dy[at].bfloat16(), t[at], torch.empty(len(lengths), cols, device="cuda"))
+        assert torch.equal(dw.double(), want)
+
+
 def test_gradient_is_the_lookups(cuda_device):
     """By differences: the lookup is linear, so (y(w + h) - y(w - h)) . dy = 2 h . dw."""
     w, h = rand(1, 30, 24, dtype=F32), rand(2, 30, 24, dtype=F32)
