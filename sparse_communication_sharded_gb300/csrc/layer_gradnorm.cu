@@ -244,9 +244,10 @@ inline bool same_boundaries(const void* in, bool in_bf16, const void* out, bool 
 // ANY: some tensor's pieces are on no boundaries of the input (a kernel of its own, as
 // its loads take twice the registers).
 template <int N, bool ANY>
-__global__ __launch_bounds__(kThreads, kBlocksPerSm) void clip_kernel(const __grid_constant__ Table<N> t, const double* partial,
-                                                        int parts, float max_norm, float eps, float* norm,
-                                                                 bool in_place) {
+__global__ __launch_bounds__(kThreads, kBlocksPerSm) void clip_kernel(const __grid_constant__ Table<N> t,
+                                                                      const double* partial, int parts,
+                                                                      float max_norm, float eps, float* norm,
+                                                                      bool in_place) {
   start();
   __shared__ double red[kThreads / 32];
   const double n = norm_of(partial, parts, red);
@@ -326,9 +327,9 @@ cudaError_t run_grad_norm(const GradSet& a, cudaStream_t st) {
     bool same = true, in_place = true;
     for (int i = 0; i < t.n; ++i) in_place &= t.in[i] == t.out[i];
     for (int i = 0; i < t.n; ++i) same &= same_boundaries(t.in[i], t.in_bf16[i], t.out[i], t.out_bf16[i]);
-    const cudaError_t r = launch_kernel(same ? clip_kernel<N, false> : clip_kernel<N, true>, (unsigned)grid_of(t.chunks),
-                                        kThreads, 0, 0, st, t, (const double*)a.partial, parts, a.max_norm, a.eps, norm,
-                                        in_place);
+    auto* const kernel = same ? clip_kernel<N, false> : clip_kernel<N, true>;
+    const cudaError_t r = launch_kernel(kernel, (unsigned)grid_of(t.chunks), kThreads, 0, 0, st, t,
+                                        (const double*)a.partial, parts, a.max_norm, a.eps, norm, in_place);
     norm = nullptr;  // told once
     return r;
   });

@@ -676,7 +676,7 @@ __device__ __noinline__ void far_row(const T* x, T* dx, int cols, int64_t target
 // in bfloat16 without entropy: 81 us, ANY 98; with four pieces at a time 112).
 template <typename T, bool ENT, bool ANY>
 __global__ __launch_bounds__(kBwdThreads) void logprobs_bwd_kernel(const __grid_constant__ LogprobsBwd a, int chunks,
-                                                                int64_t rows) {
+                                                                   int64_t rows) {
   start();
   constexpr int kPer = RowPieces<T>::kPer, U = kBwdUnroll<ANY>;
   const int64_t row = blockIdx.x / chunks;

@@ -188,7 +188,8 @@ extern "C" int scape_layer_token_loss_workspace(const void* logits, int64_t ldx,
   if (!bytes) return fail(SCAPE_EINVAL, "bytes is NULL");
   if (!dtype_ok(dtype)) return fail(SCAPE_EINVAL, "unknown dtype");
   if (!size_ok(rows) || !cols_ok(vocab)) return fail(SCAPE_EINVAL, "rows or vocab out of range");
-  *bytes = rows && vocab && !loss_on_chip(logits, ldx, dtype, rows, vocab, dlogits, lddx) ? round256((size_t)rows * 4) : 0;
+  const bool none = !rows || !vocab || loss_on_chip(logits, ldx, dtype, rows, vocab, dlogits, lddx);
+  *bytes = none ? 0 : round256((size_t)rows * 4);
   return SCAPE_OK;
 }
 
@@ -316,7 +317,9 @@ extern "C" int scape_layer_clip_grads(int n, const void* const* host_grads, cons
   // in place: the tensors themselves
   a.out = host_out ? host_out : const_cast<void* const*>(host_grads);
   a.out_dtype = host_out ? host_out_dtype : host_dtype;
-  if (!rc && host_out) rc = check_set(n, const_cast<const void* const*>(host_out), host_numel, host_out_dtype, "an output is NULL or misaligned");
+  if (!rc && host_out)
+    rc = check_set(n, const_cast<const void* const*>(host_out), host_numel, host_out_dtype,
+                   "an output is NULL or misaligned");
   if (rc) return rc;
   return run_set(a, workspace, ws_bytes, static_cast<cudaStream_t>(stream), "scape_layer_clip_grads");
 }

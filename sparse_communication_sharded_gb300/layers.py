@@ -196,9 +196,9 @@ def token_logprobs(logits, targets, entropy=False, top=0) -> TokenLogprobs:
     """Log probabilities of the targets (contiguous int64 or int32, of the logits'
     leading shape) under softmax(logits), logits float32 or bfloat16.  A target below
     0 stands for none and gives 0; one outside the vocabulary gives NaN.  top: 0 to
-    32 (of up to 4194304 columns); of equal logits the lower column comes first.  A logit of -infinity has
-    probability 0; in a row of nothing else every log probability is -infinity and
-    the entropy 0."""
+    32 (of up to 4194304 columns); of equal logits the lower column comes first.  A
+    logit of -infinity has probability 0; in a row of nothing else every log
+    probability is -infinity and the entropy 0."""
     return TokenLogprobs(*_lib().token_logprobs(logits, targets, entropy, top))
 
 
