@@ -340,6 +340,16 @@ template <bool ENT>
 __device__ __forceinline__ float log_probability(float x, const Sums<ENT>& all, float ln_s) {
   return x == -INFINITY && all.s == 0.0f ? x : (x - all.m) - ln_s;
 }
+// By one thread; chosen: the target's logit, if there is one.
+template <bool ENT>
+__device__ __forceinline__ void write_row(const Logprobs& a, int64_t row, int64_t target, float chosen,
+                                          const Sums<ENT>& all, float ln_s) {
+  float lp = target < 0 ? 0.0f : target < a.vocab ? log_probability(chosen, all, ln_s) : __uint_as_float(0x7FC00000u);
+  if (a.loss && target >= 0) lp *= -(a.weight ? a.weight[row] : a.weight_all);
+  a.logprob[row] = lp;
+  if (a.lse) a.lse[row] = all.m + ln_s;
+  if (ENT) a.entropy[row] = all.s == 0.0f ? 0.0f : ln_s - all.a * kLn2F / all.s;
+}
 // Of the n keys of a cluster's blocks, the largest.
 template <bool ENT>
 __device__ __forceinline__ void write_top(const Logprobs& a, int64_t row, const uint64_t* keys, int n,
@@ -494,17 +504,39 @@ __global__ __launch_bounds__(kTeam, TOP ? kBlocksTop : kBlocks) void logprobs_ke
   if (rank != 0 || (!TOP && threadIdx.x != 0)) return;
   const Sums<ENT> all = ranks > 1 ? join_parts<ENT>(of_block, (int)ranks) : join_parts<ENT>(of_warp, warps);
   const float ln_s = logf(all.s);
-  if (threadIdx.x == 0) {
-    float lp = in ? log_probability(chosen, all, ln_s) : target < 0 ? 0.0f : __uint_as_float(0x7FC00000u);
-    if (a.loss && target >= 0) lp *= -(a.weight ? a.weight[row] : a.weight_all);
-    a.logprob[row] = lp;
-    if (a.lse) a.lse[row] = all.m + ln_s;
-    if (ENT) a.entropy[row] = all.s == 0.0f ? 0.0f : ln_s - all.a * kLn2F / all.s;
-  }
+  if (threadIdx.x == 0) write_row(a, row, target, chosen, all, ln_s);
   if constexpr (TOP) write_top(a, row, ranks > 1 ? scratch.all : scratch.best, (int)ranks * a.top, all, ln_s);
 }
 
 // ------------------------------------------------------------------ loss
+// What a row's gradient is of its exponentials: w / S, w 0 without a target and NaN with
+// one that is none of the columns.
+__device__ __forceinline__ float loss_weight(const Logprobs& a, int64_t target, float w) {
+  return target < 0 ? 0.0f : target < a.vocab ? w : __uint_as_float(0x7FC00000u);
+}
+__device__ __forceinline__ float loss_scale(const Sums<false>& all, float w) {
+  return all.s == 0.0f ? 0.0f * w : w / all.s;
+}
+template <typename T, int N>
+__device__ __forceinline__ void loss_gradient(const uint4& u, float m, float scale, float (&f)[N]) {
+  const uint64_t minus = pair(-m, -m), log2e = pair(kLog2eF, kLog2eF), scale2 = pair(scale, scale);
+  uint64_t q[N / 2];
+  piece_pairs<T>(u, q);
+#pragma unroll
+  for (int k = 0; k < N / 2; ++k) {
+    float x, y;
+    unpair(mul2(add2(q[k], minus), log2e), x, y);
+    unpair(mul2(pair(exp2_fast(x), exp2_fast(y)), scale2), f[2 * k], f[2 * k + 1]);
+  }
+}
+template <typename T>
+__device__ __forceinline__ void store_piece(T* o, const float (&f)[16 / sizeof(T)]) {
+  if constexpr (sizeof(T) == 2)
+    store_vec<8>(o, f);
+  else
+    *reinterpret_cast<float4*>(o) = make_float4(f[0], f[1], f[2], f[3]);
+}
+
 // The row stays in shared memory between its sums and its gradient, so logits are
 // read once.  A block, or a cluster of them each with a part of the row, takes one
 // row; every thread copies its own pieces to places of its own, which it alone reads.
@@ -578,20 +610,9 @@ __global__ __launch_bounds__(kMaxThreads) void token_loss_kernel(const __grid_co
     own = join_parts<false>(of_block, (int)ranks);
   }
   const bool none = target < 0, in = !none && target < a.vocab;
-  w = none ? 0.0f : in ? w : __uint_as_float(0x7FC00000u);
-  const float scale = own.s == 0.0f ? 0.0f * w : w / own.s;
+  w = loss_weight(a, target, w);
+  const float scale = loss_scale(own, w);
   T* dx = static_cast<T*>(a.dx) + row * a.lddx;
-  const uint64_t minus = pair(-own.m, -own.m), log2e = pair(kLog2eF, kLog2eF), scale2 = pair(scale, scale);
-  auto gradient = [&](const uint4& u, float (&f)[kPer]) {
-    uint64_t q[kPer / 2];
-    piece_pairs<T>(u, q);
-#pragma unroll
-    for (int k = 0; k < kPer / 2; ++k) {
-      float x, y;
-      unpair(mul2(add2(q[k], minus), log2e), x, y);
-      unpair(mul2(pair(exp2_fast(x), exp2_fast(y)), scale2), f[2 * k], f[2 * k + 1]);
-    }
-  };
   T* o = dx + r.row.column(r.w0 + threadIdx.x);
   const uint4* p = mine;
   for (int left = n; left > 0; left -= threads, p += threads, o += threads * kPer) {
@@ -600,18 +621,15 @@ __global__ __launch_bounds__(kMaxThreads) void token_loss_kernel(const __grid_co
 #pragma unroll
       for (int k = 0; k < kPer; ++k) f[k] = 0.0f;
     } else {
-      gradient(*p, f);
+      loss_gradient<T>(*p, own.m, scale, f);
     }
-    if constexpr (sizeof(T) == 2)
-      store_vec<8>(o, f);
-    else
-      *reinterpret_cast<float4*>(o) = make_float4(f[0], f[1], f[2], f[3]);
+    store_piece(o, f);
   }
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       if (!(i ? r.part_after() : r.part_before())) continue;
       float f[kPer];
-      gradient(ends[i], f);
+      loss_gradient<T>(ends[i], own.m, scale, f);
       const int c = r.row.column(i ? r.w1 : r.v0);
 #pragma unroll
       for (int k = 0; k < kPer; ++k)
@@ -637,6 +655,92 @@ __global__ __launch_bounds__(kMaxThreads) void token_loss_kernel(const __grid_co
     }
   } else if (rank == 0 && threadIdx.x == 0) {
     a.logprob[row] = w;  // 0 or NaN
+  }
+}
+
+// ------------------------------------------------------------------ short rows
+// A warp takes a row, each lane kShortUnroll of its pieces in registers, with the next
+// row's on their way; with LOSS its gradient goes out from there.
+constexpr int kShortWarps = 4, kShortUnroll = 4, kShortBlocks = 6;
+constexpr int kShortPieces = 32 * kShortUnroll;
+
+template <typename T, bool ENT, bool LOSS>
+__global__ __launch_bounds__(kShortWarps * 32, kShortBlocks) void short_rows_kernel(
+    const __grid_constant__ Logprobs a) {
+  start();
+  constexpr int kPer = RowPieces<T>::kPer, U = kShortUnroll;
+  const int lane = threadIdx.x & 31;
+  const int64_t step = (int64_t)gridDim.x * kShortWarps;
+  uint4 next[U];
+  int64_t next_target = 0;
+  float next_w = 0.0f;
+  auto load = [&](int64_t row) {
+    if (row >= a.targets.count) return;
+    const RowPieces<T> r(static_cast<const T*>(a.x) + row * a.ldx, (int)a.vocab);
+    next_target = load_target(a.targets, row);
+    if (LOSS) next_w = a.weight ? a.weight[row] : a.weight_all;
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int v = lane + i * 32;
+      constexpr uint32_t none = sizeof(T) == 2 ? 0xFF80FF80u : 0xFF800000u;  // -infinity
+      next[i] = make_uint4(none, none, none, none);
+      if (r.whole(v)) next[i] = *reinterpret_cast<const uint4*>(r.x + r.column(v));
+    }
+    if (r.phase == 0 && r.cols % kPer == 0) return;
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int v = lane + i * 32;
+      if (v < r.pieces && !r.whole(v)) next[i] = r.load_part(v);
+    }
+  };
+  int64_t row = (int64_t)blockIdx.x * kShortWarps + (threadIdx.x >> 5);
+  load(row);
+  for (; row < a.targets.count; row += step) {
+    uint4 u[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) u[i] = next[i];
+    const int64_t target = next_target;
+    const float weight = next_w;
+    load(row + step);
+    const T* x = static_cast<const T*>(a.x) + row * a.ldx;
+    const bool in = target >= 0 && target < a.vocab;
+    const float chosen = in ? (float)x[target] : 0.0f;
+    Sums<ENT> own;
+    own.template add<T, U>(u);
+    own.over_warp();
+    const float ln_s = logf(own.s);
+    if constexpr (!LOSS) {
+      if (lane == 0) write_row(a, row, target, chosen, own, ln_s);
+    } else {
+      const float w = loss_weight(a, target, weight), scale = loss_scale(own, w);
+      T* dx = static_cast<T*>(a.dx) + row * a.lddx;
+      const RowPieces<T> r(dx, (int)a.vocab);
+      __syncwarp();  // all have the target's logit, which may be in the gradient's place
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        const int v = lane + i * 32, c = r.column(v);
+        if (v >= r.pieces) continue;
+        float f[kPer];
+        loss_gradient<T>(u[i], own.m, scale, f);
+        if (target < 0) {
+#pragma unroll
+          for (int k = 0; k < kPer; ++k) f[k] = 0.0f;
+        }
+        if (r.whole(v)) {
+          store_piece(dx + c, f);
+        } else {
+#pragma unroll
+          for (int k = 0; k < kPer; ++k)
+            if (c + k >= 0 && c + k < r.cols) dx[c + k] = (T)f[k];
+        }
+      }
+      __syncwarp();  // the target's, over what its piece had
+      if (lane == 0) {
+        const float d = log_probability(chosen, own, ln_s);
+        if (in) dx[target] = (T)(w * expm1f(d));
+        a.logprob[row] = in ? -w * d : w;  // 0 or NaN
+      }
+    }
   }
 }
 
@@ -762,10 +866,7 @@ __global__ __launch_bounds__(kBwdThreads) void logprobs_bwd_kernel(const __grid_
     }
     T* p = dx + c;
     if (out.whole(v)) {
-      if constexpr (sizeof(T) == 2)
-        store_vec<8>(p, f);
-      else
-        *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+      store_piece(p, f);
     } else {
 #pragma unroll
       for (int k = 0; k < kPer; ++k)
@@ -834,8 +935,19 @@ cudaError_t run_rows(const Logprobs& a, cudaStream_t st) {
   return launch_kernel(kernel, (unsigned)(rows * cluster), threads, smem, cluster > 1 ? cluster : 0, st, a,
                        (int)batches);
 }
+// Whether a warp holds a row, wherever it starts.
+template <typename T>
+bool is_short(int64_t vocab) {
+  return ceil_div(vocab + RowPieces<T>::kPer - 1, RowPieces<T>::kPer) <= kShortPieces;
+}
+template <typename T, bool ENT, bool LOSS>
+cudaError_t run_short(const Logprobs& a, cudaStream_t st) {
+  const int64_t grid = std::min<int64_t>(ceil_div(a.targets.count, kShortWarps), (int64_t)sm_count() * kShortBlocks);
+  return launch_kernel(short_rows_kernel<T, ENT, LOSS>, (unsigned)grid, kShortWarps * 32, 0, 0, st, a);
+}
 template <typename T>
 cudaError_t run_logprobs(const Logprobs& a, cudaStream_t st) {
+  if (!a.top && is_short<T>(a.vocab)) return a.entropy ? run_short<T, true, false>(a, st) : run_short<T, false, false>(a, st);
   if (a.top) return a.entropy ? run_rows<T, true, true>(a, st) : run_rows<T, false, true>(a, st);
   return a.entropy ? run_rows<T, true, false>(a, st) : run_rows<T, false, false>(a, st);
 }
@@ -862,6 +974,7 @@ cudaError_t run_token_loss(const TokenLoss& a, cudaStream_t st) {
     const HeldPlan p = held_plan(a.targets.count, a.vocab, sizeof(T));
     if (p.cluster) {
       f.dx = a.dx, f.lddx = a.lddx;
+      if (is_short<T>(a.vocab)) return run_short<T, false, true>(f, st);
       const int smem = p.pieces * 16;
       if (smem > 32 * 1024) {  // with the static part, what a kernel may have unasked is 48 KB
         const cudaError_t e = allow_smem((const void*)token_loss_kernel<T>, smem);
