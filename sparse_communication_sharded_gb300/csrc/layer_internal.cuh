@@ -602,11 +602,11 @@ __device__ __forceinline__ void start() {
   wait_for_earlier();
 }
 template <typename... P, typename... A>
-cudaError_t launch_kernel(void (*kernel)(P...), dim3 grid, int threads, size_t smem, int cluster,
+cudaError_t launch_kernel(void (*kernel)(P...), dim3 grid, dim3 threads, size_t smem, int cluster,
                           cudaStream_t st, const A&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
-  cfg.blockDim = dim3((unsigned)threads);
+  cfg.blockDim = threads;
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute at[2];

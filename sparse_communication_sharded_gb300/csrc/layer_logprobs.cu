@@ -659,16 +659,20 @@ __global__ __launch_bounds__(kMaxThreads) void token_loss_kernel(const __grid_co
 }
 
 // ------------------------------------------------------------------ short rows
-// A warp takes a row, each lane kShortUnroll of its pieces in registers, with the next
-// row's on their way; with LOSS its gradient goes out from there.
-constexpr int kShortWarps = 4, kShortUnroll = 4, kShortBlocks = 6;
-constexpr int kShortPieces = 32 * kShortUnroll;
+// A warp takes a row, each lane U of its pieces in registers, with the next row's on
+// their way; with LOSS its gradient goes out from there.  What bounds it is a row's own
+// work, the joining of 32 lanes' sums and what lane 0 does with them.  16384 rows in
+// bfloat16, log probabilities and loss: of 256 columns 7.7 and 10.3 us, of 1000 9.4 and
+// 15.3 (a block a row 19 and 20.7), of 2000, where U is 8 and four blocks fit, 13.8 and
+// 25.5 (24.8 and 34.5).  Longer rows have no room in registers.
+constexpr int kShortWarps = 4;
+constexpr int short_blocks(int u) { return u <= 4 ? 6 : 4; }  // an SM
 
-template <typename T, bool ENT, bool LOSS>
-__global__ __launch_bounds__(kShortWarps * 32, kShortBlocks) void short_rows_kernel(
+template <typename T, bool ENT, bool LOSS, int U>
+__global__ __launch_bounds__(kShortWarps * 32, short_blocks(U)) void short_rows_kernel(
     const __grid_constant__ Logprobs a) {
   start();
-  constexpr int kPer = RowPieces<T>::kPer, U = kShortUnroll;
+  constexpr int kPer = RowPieces<T>::kPer;
   const int lane = threadIdx.x & 31;
   const int64_t step = (int64_t)gridDim.x * kShortWarps;
   uint4 next[U];
@@ -749,11 +753,11 @@ __global__ __launch_bounds__(kShortWarps * 32, kShortBlocks) void short_rows_ker
 // masked whole with the type's lowest value: lse is that value, and exp(x - lse)
 // would be 1 everywhere), so the row's sums are formed again.
 constexpr float kFarLse = 4096.0f;
-constexpr int kBwdThreads = 256;
+constexpr int kBwdThreads = 256, kBwdRows = 8;
 template <bool ANY>
 constexpr int kBwdUnroll = ANY ? 2 : 4;
 
-// Such a row, by one block, which alone reads and writes it.
+// Such a row, by the threads of one threadIdx.y, which alone read and write it.
 template <typename T, bool ENT>
 __device__ __noinline__ void far_row(const T* x, T* dx, int cols, int64_t target, float g, float dh, float h) {
   __shared__ Part part[kBwdThreads / 32];
@@ -763,9 +767,11 @@ __device__ __noinline__ void far_row(const T* x, T* dx, int cols, int64_t target
   Sums<false> own;
   own.m = top, own.s = s;
   own.over_warp();
-  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = {own.m, own.s, 0.0f};
-  __syncthreads();
-  own = join_parts<false>(part, blockDim.x / 32);
+  if (blockDim.x > 32) {  // the block's only row
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = {own.m, own.s, 0.0f};
+    __syncthreads();
+    own = join_parts<false>(part, blockDim.x / 32);
+  }
   const float ln_s = logf(own.s);
   for (int c = threadIdx.x; c < cols; c += blockDim.x) {
     const float d = ((float)x[c] - own.m) - ln_s, p = exp2_fast(d * kLog2eF);
@@ -776,15 +782,18 @@ __device__ __noinline__ void far_row(const T* x, T* dx, int cols, int64_t target
 }
 
 // A block takes kBwdUnroll pieces a thread of one row, on the output's boundaries.
+// MANY: a warp's are a row, and a block takes kBwdRows of them (16384 x 256 in bfloat16:
+// 7.6 us, a block a row 17).
 // ANY: they are on no boundaries of the logits' rows, and a load is two (4096 x 32000
 // in bfloat16 without entropy: 81 us, ANY 98; with four pieces at a time 112).
-template <typename T, bool ENT, bool ANY>
+template <typename T, bool ENT, bool ANY, bool MANY>
 __global__ __launch_bounds__(kBwdThreads) void logprobs_bwd_kernel(const __grid_constant__ LogprobsBwd a, int chunks,
                                                                    int64_t rows) {
   start();
   constexpr int kPer = RowPieces<T>::kPer, U = kBwdUnroll<ANY>;
-  const int64_t row = blockIdx.x / chunks;
-  const int chunk = (int)(blockIdx.x % chunks);
+  const int64_t row = MANY ? (int64_t)blockIdx.x * kBwdRows + threadIdx.y : blockIdx.x / chunks;
+  if (MANY && row >= rows) return;
+  const int chunk = MANY ? 0 : (int)(blockIdx.x % chunks);
   const T* x = static_cast<const T*>(a.x) + row * a.ldx;
   T* dx = static_cast<T*>(a.dx) + row * a.lddx;
   const T *lo = static_cast<const T*>(a.x), *hi = lo + (rows - 1) * a.ldx + a.vocab;
@@ -935,19 +944,23 @@ cudaError_t run_rows(const Logprobs& a, cudaStream_t st) {
   return launch_kernel(kernel, (unsigned)(rows * cluster), threads, smem, cluster > 1 ? cluster : 0, st, a,
                        (int)batches);
 }
-// Whether a warp holds a row, wherever it starts.
+// Pieces a lane of a warp that holds a row, wherever it starts; 0: too many.
 template <typename T>
-bool is_short(int64_t vocab) {
-  return ceil_div(vocab + RowPieces<T>::kPer - 1, RowPieces<T>::kPer) <= kShortPieces;
+int short_unroll(int64_t vocab) {
+  const int64_t pieces = ceil_div(vocab + RowPieces<T>::kPer - 1, RowPieces<T>::kPer);
+  return pieces <= 32 * 4 ? 4 : pieces <= 32 * 8 ? 8 : 0;
 }
 template <typename T, bool ENT, bool LOSS>
-cudaError_t run_short(const Logprobs& a, cudaStream_t st) {
-  const int64_t grid = std::min<int64_t>(ceil_div(a.targets.count, kShortWarps), (int64_t)sm_count() * kShortBlocks);
-  return launch_kernel(short_rows_kernel<T, ENT, LOSS>, (unsigned)grid, kShortWarps * 32, 0, 0, st, a);
+cudaError_t run_short(const Logprobs& a, int unroll, cudaStream_t st) {
+  const int64_t blocks = ceil_div(a.targets.count, kShortWarps);
+  const unsigned grid = (unsigned)std::min<int64_t>(blocks, (int64_t)sm_count() * short_blocks(unroll));
+  auto* const kernel = unroll == 4 ? short_rows_kernel<T, ENT, LOSS, 4> : short_rows_kernel<T, ENT, LOSS, 8>;
+  return launch_kernel(kernel, grid, kShortWarps * 32, 0, 0, st, a);
 }
 template <typename T>
 cudaError_t run_logprobs(const Logprobs& a, cudaStream_t st) {
-  if (!a.top && is_short<T>(a.vocab)) return a.entropy ? run_short<T, true, false>(a, st) : run_short<T, false, false>(a, st);
+  const int unroll = a.top ? 0 : short_unroll<T>(a.vocab);
+  if (unroll) return a.entropy ? run_short<T, true, false>(a, unroll, st) : run_short<T, false, false>(a, unroll, st);
   if (a.top) return a.entropy ? run_rows<T, true, true>(a, st) : run_rows<T, false, true>(a, st);
   return a.entropy ? run_rows<T, true, false>(a, st) : run_rows<T, false, false>(a, st);
 }
@@ -958,11 +971,20 @@ cudaError_t run_logprobs_bwd(const LogprobsBwd& a, cudaStream_t st) {
   const bool same = same_places(a.x, a.ldx, a.dx, a.lddx, sizeof(T));
   const int unroll = same ? kBwdUnroll<false> : kBwdUnroll<true>;
   const int threads = threads_for(ceil_div(pieces, unroll), kBwdThreads);
-  const int64_t chunks = ceil_div(pieces, threads * unroll), grid = a.targets.count * chunks;
+  const bool many = threads == 32;
+  const int64_t chunks = ceil_div(pieces, threads * unroll);
+  const int64_t grid = many ? ceil_div(a.targets.count, kBwdRows) : a.targets.count * chunks;
   if (grid > 0x7FFFFFFF) return cudaErrorInvalidValue;
-  auto* const kernel = a.dentropy ? (same ? logprobs_bwd_kernel<T, true, false> : logprobs_bwd_kernel<T, true, true>)
-                                  : (same ? logprobs_bwd_kernel<T, false, false> : logprobs_bwd_kernel<T, false, true>);
-  return launch_kernel(kernel, (unsigned)grid, threads, 0, 0, st, a, (int)chunks, a.targets.count);
+  auto run = [&](auto kernel) {
+    return launch_kernel(kernel, (unsigned)grid, dim3((unsigned)threads, many ? kBwdRows : 1), 0, 0, st, a,
+                         (int)chunks, a.targets.count);
+  };
+  auto of = [&](auto ent, auto any) {
+    constexpr bool E = decltype(ent)::value, A = decltype(any)::value;
+    return many ? run(logprobs_bwd_kernel<T, E, A, true>) : run(logprobs_bwd_kernel<T, E, A, false>);
+  };
+  if (a.dentropy) return same ? of(std::true_type(), std::false_type()) : of(std::true_type(), std::true_type());
+  return same ? of(std::false_type(), std::false_type()) : of(std::false_type(), std::true_type());
 }
 
 template <typename T>
@@ -974,7 +996,8 @@ cudaError_t run_token_loss(const TokenLoss& a, cudaStream_t st) {
     const HeldPlan p = held_plan(a.targets.count, a.vocab, sizeof(T));
     if (p.cluster) {
       f.dx = a.dx, f.lddx = a.lddx;
-      if (is_short<T>(a.vocab)) return run_short<T, false, true>(f, st);
+      const int unroll = short_unroll<T>(a.vocab);
+      if (unroll) return run_short<T, false, true>(f, unroll, st);
       const int smem = p.pieces * 16;
       if (smem > 32 * 1024) {  // with the static part, what a kernel may have unasked is 48 KB
         const cudaError_t e = allow_smem((const void*)token_loss_kernel<T>, smem);

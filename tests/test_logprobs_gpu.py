@@ -4,6 +4,7 @@ import math
 
 import pytest
 import torch
+import torch.nn.functional as F
 
 from sparse_communication_sharded_gb300 import ScapeError
 from sparse_communication_sharded_gb300 import layers as L
@@ -153,6 +154,39 @@ def test_anywhere(cuda_device, vocab, gap, offset, dtype):
     L.token_loss(x, t, w, out=x)
     near(x, *o.gradient(-w, dtype))
     assert bool((buf[:, :offset] == INF).all()) and bool((buf[:, offset + vocab:] == INF).all())
+
+
+@pytest.mark.parametrize("vocab", [1, 8, 257, 500, 513, 1017, 1024, 1025, 2041, 2049])
+@pytest.mark.parametrize("gap", [0, 3])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_many_short_rows(cuda_device, vocab, gap, dtype):
+    """More rows than a grid has warps, with all kinds of them side by side."""
+    kinds = [logits_of(vocab + i, 719, vocab, dtype, gap, kind) for i, kind in enumerate(KINDS)]
+    rows = 719 * len(kinds)
+    buffer = torch.stack([F.pad(k, (0, gap), value=7.0) for k in kinds], 1).reshape(rows, vocab + gap)
+    x = buffer[:, :vocab]
+    t = targets_of(vocab, rows, vocab)
+    g = torch.Generator(device="cuda").manual_seed(vocab)
+    w = torch.rand(rows, device="cuda", generator=g) + 0.1
+    dent = torch.randn(rows, device="cuda", generator=g)
+    o = R.Rows(x, t)
+    r, plain = L.token_logprobs(x, t, entropy=True), L.token_logprobs(x, t)
+    near(r.logprob, *o.logprob(), "logprob")
+    near(r.lse, *o.lse_and_tol(), "lse")
+    near(r.entropy, *o.entropy_and_tol(), "entropy")
+    near(plain.logprob, *o.logprob(), "logprob alone")
+    near(plain.lse, *o.lse_and_tol(), "lse alone")
+    near(L.token_logprobs_backward(x, t, r.lse, w), *o.gradient(w, dtype, own_lse=r.lse), "dlogits")
+    got = L.token_logprobs_backward(x, t, r.lse, w, entropy=r.entropy, dentropy=dent)
+    near(got, *o.gradient(w, dtype, r.entropy, dent, own_lse=r.lse), "with entropy")
+    want, tol = o.logprob()
+    to = torch.full_like(buffer, 7.0)[:, :vocab]
+    for out in (to, x):
+        loss, dx = L.token_loss(x, t, w, out=out)
+        assert dx is out
+        near(loss, -want * w, tol * w + want.abs() * w * 2.0 ** -23, "loss")
+        near(dx, *o.gradient(-w, dtype), "gradient")
+    assert bool((buffer[:, vocab:] == 7).all())
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
