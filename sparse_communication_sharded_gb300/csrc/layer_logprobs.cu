@@ -597,13 +597,11 @@ __global__ __launch_bounds__(kMaxThreads) void token_loss_kernel(const __grid_co
     }
   }
   own.over_warp();
-  if (warps > 1) {
-    if (lane == 0) of_warp[threadIdx.x >> 5] = {own.m, own.s, 0.0f};
-    __syncthreads();
-    const Part p = of_warp[lane < warps ? lane : 0];
-    own.m = p.m, own.s = lane < warps ? p.s : 0.0f;
-    own.over_warp();
-  }
+  if (lane == 0) of_warp[threadIdx.x >> 5] = {own.m, own.s, 0.0f};
+  __syncthreads();
+  const Part p0 = of_warp[lane < warps ? lane : 0];
+  own.m = p0.m, own.s = lane < warps ? p0.s : 0.0f;
+  own.over_warp();
   if (ranks > 1) {
     if (threadIdx.x < ranks) send(&of_block[rank], threadIdx.x, own);
     cluster_done();
@@ -908,10 +906,7 @@ HeldPlan held_plan(int64_t rows, int64_t vocab, int elem) {
     // few rows are spread over the SMs; two blocks or more an SM
     if (cluster < kMaxCluster && ((rows * cluster * 2 <= sm_count() && part >= 2 * 512) || fit < 2)) continue;
     if (fit < 1) break;
-    const int most = fit == 1 ? 1024 : fit == 2 ? 512 : fit == 3 ? 256 : 128;
-    int threads = 32;
-    while (threads < most && part >= 4 * threads) threads *= 2;
-    return {cluster, threads, (int)part};
+    return {cluster, fit == 1 ? 1024 : fit == 2 ? 512 : fit == 3 ? 256 : 128, (int)part};
   }
   return {};
 }

@@ -458,6 +458,14 @@ float* floats_of(const Tensor& t, at::IntArrayRef shape, const Tensor& ref, cons
     throw ValueError(std::string(name) + " must be contiguous float32, one a row");
   return t.data_ptr<float>();
 }
+// A contiguous part of an allocation, from its at-th element on.  (An allocation is a
+// microsecond, and several a quarter of what a call for one row takes.)
+Tensor part_of(const Tensor& all, int64_t at, at::IntArrayRef sizes) {
+  Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(all.storage()), all.key_set(), all.dtype());
+  t.unsafeGetTensorImpl()->set_sizes_contiguous(sizes);
+  t.unsafeGetTensorImpl()->set_storage_offset(at);
+  return t;
+}
 Tensor row_floats(at::IntArrayRef lead, const Tensor& ref) {
   return at::detail::empty_cuda(lead, at::kFloat, ref.device(), std::nullopt);
 }
@@ -539,10 +547,14 @@ PyObject* do_token_logprobs(Args a) {
   if (top < 0 || top > SCAPE_TOP_MAX || top > r.cols)
     throw ValueError("top must be 0 to 32, and at most the logits' columns");
   c10::cuda::CUDAGuard guard(x.device());
-  Tensor lp = row_floats(lead, x), lse = row_floats(lead, x), ent, tops, token;
-  if (entropy) ent = row_floats(lead, x);
+  const int64_t each = (r.rows + 127) / 128 * 128;
+  const Tensor all = row_floats({each * (entropy ? 3 : 2) + r.rows * top}, x);
+  Tensor lp = part_of(all, 0, lead), lse = part_of(all, each, lead), ent, tops, token;
+  if (entropy) ent = part_of(all, 2 * each, lead);
   if (top) {
-    tops = empty(lead, top, at::kFloat, x);
+    c10::SmallVector<int64_t, 8> sizes(lead.begin(), lead.end());
+    sizes.push_back(top);
+    tops = part_of(all, each * (entropy ? 3 : 2), sizes);
     token = empty(lead, top, at::kLong, x);
   }
   library(scape_layer_token_logprobs(r.p, r.ld, dtype_of(x), ids.p, ids.bytes, r.rows, r.cols, (int)top,

@@ -184,7 +184,7 @@ class TokenLogprobs(NamedTuple):
     """Each of the rows' leading shape, float32: the targets' log probabilities, the
     logits' log-sum-exp, the entropies (None unless asked for); the `top` largest
     logits' log probabilities and columns (int64), in falling order, in one more
-    dimension (None unless asked for)."""
+    dimension (None unless asked for).  The float32 ones are parts of one allocation."""
     logprob: torch.Tensor
     lse: torch.Tensor
     entropy: torch.Tensor | None
