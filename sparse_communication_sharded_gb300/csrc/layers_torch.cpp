@@ -642,22 +642,27 @@ Set set_of(PyObject* o, const char* name) {
   if (n > 0x7FFFFFFF) throw ValueError(std::string(name) + " has too many tensors");
   return s;
 }
-Tensor norm_space(const Set& s, Tensor* ws, size_t* n) {
-  library(scape_layer_grad_norm_workspace((int)s.t.size(), s.numel.data(), n));
-  if (*n) *ws = bytes(*n, s.t[0]);
-  return at::detail::empty_cuda({}, at::kFloat, s.t[0].device(), std::nullopt);
-}
+// The norm, and behind it in the same allocation (of a few KB) the workspace.
+struct NormSpace {
+  Tensor norm;
+  void* ws = nullptr;
+  size_t n = 0;
+  explicit NormSpace(const Set& s) {
+    library(scape_layer_grad_norm_workspace((int)s.t.size(), s.numel.data(), &n));
+    const Tensor all = row_floats({64 + (int64_t)(n / 4)}, s.t[0]);
+    norm = part_of(all, 0, {});
+    if (n) ws = all.data_ptr<float>() + 64;
+  }
+};
 
 // (grads) -> norm
 PyObject* do_grad_norm(Args a) {
   const Set s = set_of(a[0], "grads");
   c10::cuda::CUDAGuard guard(s.t[0].device());
-  Tensor ws;
-  size_t n = 0;
-  Tensor norm = norm_space(s, &ws, &n);
-  library(scape_layer_grad_norm((int)s.t.size(), s.p.data(), s.numel.data(), s.dtype.data(), norm.data_ptr<float>(),
-                                n ? ws.data_ptr() : nullptr, n, stream_of(s.t[0])));
-  return wrap(norm);
+  const NormSpace to(s);
+  library(scape_layer_grad_norm((int)s.t.size(), s.p.data(), s.numel.data(), s.dtype.data(), to.norm.data_ptr<float>(),
+                                to.ws, to.n, stream_of(s.t[0])));
+  return wrap(to.norm);
 }
 
 // (grads, max_norm, eps, out or None) -> norm
@@ -676,16 +681,13 @@ PyObject* do_clip_grad_norm(Args a) {
     }
   }
   c10::cuda::CUDAGuard guard(s.t[0].device());
-  Tensor ws;
-  size_t n = 0;
-  Tensor norm = norm_space(s, &ws, &n);
+  const NormSpace to(s);
   const Set& into = given(a[3]) ? o : s;
   library(scape_layer_clip_grads((int)s.t.size(), s.p.data(), s.numel.data(), s.dtype.data(),
                                  const_cast<void* const*>(into.p.data()), into.dtype.data(), (float)max_norm,
-                                 (float)eps, norm.data_ptr<float>(), n ? ws.data_ptr() : nullptr, n,
-                                 stream_of(s.t[0])));
+                                 (float)eps, to.norm.data_ptr<float>(), to.ws, to.n, stream_of(s.t[0])));
   for (const Tensor& t : into.t) written(t);
-  return wrap(norm);
+  return wrap(to.norm);
 }
 
 // () -> int
