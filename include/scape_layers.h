@@ -239,6 +239,14 @@ int scape_layer_token_logprobs(const void *logits, int64_t ldx, int dtype, const
                                int token_bytes, int64_t rows, int64_t vocab, int top,
                                float *logprob, float *lse, float *entropy, float *top_logprob,
                                int64_t *top_token, void *stream);
+/*
+ * The same with the log-sum-exp in two numbers, lse + lse_rest [rows]: lse_rest is what
+ * lse's rounding to 32 bits leaves (0 where lse is not finite).  NULL: not wanted.
+ */
+int scape_layer_token_logprobs_rest(const void *logits, int64_t ldx, int dtype, const void *targets,
+                                    int token_bytes, int64_t rows, int64_t vocab, int top,
+                                    float *logprob, float *lse, float *lse_rest, float *entropy,
+                                    float *top_logprob, int64_t *top_token, void *stream);
 
 /*
  * dlogits_j = dlogprob (1[j = target] - p_j) - dentropy p_j (log p_j + entropy), from
@@ -251,6 +259,18 @@ int scape_layer_token_logprobs_bwd(const void *logits, int64_t ldx, int dtype, c
                                    const float *dlogprob, const float *entropy,
                                    const float *dentropy, void *dlogits, int64_t lddx,
                                    void *stream);
+/*
+ * The same from a log-sum-exp of two numbers.  From lse alone p_j = exp(x_j - lse) is off
+ * by lse's rounding, 2^-24 |lse| of itself, and 1 - p_target, where it is that small, is
+ * lost (from |lse| = 4096 on the sums of a row are formed again, and it is slower).  With
+ * lse_rest it is the softmax's wherever the logits lie.  NULL: lse alone.
+ */
+int scape_layer_token_logprobs_rest_bwd(const void *logits, int64_t ldx, int dtype,
+                                        const void *targets, int token_bytes, int64_t rows,
+                                        int64_t vocab, const float *lse, const float *lse_rest,
+                                        const float *dlogprob, const float *entropy,
+                                        const float *dentropy, void *dlogits, int64_t lddx,
+                                        void *stream);
 
 /*
  * A row's loss and its gradient in one pass over the logits:

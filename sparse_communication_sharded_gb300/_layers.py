@@ -42,6 +42,10 @@ PROTOS = {
                                           _vp, _vp, _vp, _vp]),
     "scape_layer_token_logprobs_bwd": (_i32, [_vp, _i64, _i32, _vp, _i32, _i64, _i64, _vp, _vp, _vp,
                                               _vp, _vp, _i64, _vp]),
+    "scape_layer_token_logprobs_rest": (_i32, [_vp, _i64, _i32, _vp, _i32, _i64, _i64, _i32, _vp,
+                                               _vp, _vp, _vp, _vp, _vp, _vp]),
+    "scape_layer_token_logprobs_rest_bwd": (_i32, [_vp, _i64, _i32, _vp, _i32, _i64, _i64, _vp, _vp,
+                                                   _vp, _vp, _vp, _vp, _i64, _vp]),
     "scape_layer_token_loss_workspace": (_i32, [_vp, _i64, _i32, _i64, _i64, _vp, _i64, _vp]),
     "scape_layer_token_loss": (_i32, [_vp, _i64, _i32, _vp, _i32, _i64, _i64, _vp, _f32, _vp, _vp,
                                       _i64, _vp, _sz, _vp]),

@@ -340,6 +340,11 @@ template <bool ENT>
 __device__ __forceinline__ float log_probability(float x, const Sums<ENT>& all, float ln_s) {
   return x == -INFINITY && all.s == 0.0f ? x : (x - all.m) - ln_s;
 }
+// What lse = m + ln S has lost in its rounding: the sum's error is a number in 32 bits.
+__device__ __forceinline__ float rest_of(float m, float ln_s, float lse) {
+  const float b = lse - m;
+  return fabsf(lse) < INFINITY ? (m - (lse - b)) + (ln_s - b) : 0.0f;
+}
 // By one thread; chosen: the target's logit, if there is one.
 template <bool ENT>
 __device__ __forceinline__ void write_row(const Logprobs& a, int64_t row, int64_t target, float chosen,
@@ -347,7 +352,9 @@ __device__ __forceinline__ void write_row(const Logprobs& a, int64_t row, int64_
   float lp = target < 0 ? 0.0f : target < a.vocab ? log_probability(chosen, all, ln_s) : __uint_as_float(0x7FC00000u);
   if (a.loss && target >= 0) lp *= -(a.weight ? a.weight[row] : a.weight_all);
   a.logprob[row] = lp;
-  if (a.lse) a.lse[row] = all.m + ln_s;
+  const float lse = all.m + ln_s;
+  if (a.lse) a.lse[row] = lse;
+  if (a.rest) a.rest[row] = rest_of(all.m, ln_s, lse);
   if (ENT) a.entropy[row] = all.s == 0.0f ? 0.0f : ln_s - all.a * kLn2F / all.s;
 }
 // Of the n keys of a cluster's blocks, the largest.
@@ -747,9 +754,10 @@ __global__ __launch_bounds__(kShortWarps * 32, short_blocks(U)) void short_rows_
 }
 
 // ------------------------------------------------------------------ gradient
-// Past this a float32 lse has lost what ln S adds to the row's largest logit (a row
-// masked whole with the type's lowest value: lse is that value, and exp(x - lse)
-// would be 1 everywhere), so the row's sums are formed again.
+// p = exp((x - lse) - rest).  Without the rest p is off by what lse's rounding is, 2^-24
+// |lse| of itself: 2^-12 here, where lse tells ln S to 2^-12, and in a row masked whole
+// with the type's lowest value it says nothing of ln S (lse is that value, and exp(x -
+// lse) would be 1 everywhere).  So past this the row's sums are formed again.
 constexpr float kFarLse = 4096.0f;
 constexpr int kBwdThreads = 256, kBwdRows = 8;
 template <bool ANY>
@@ -780,11 +788,12 @@ __device__ __noinline__ void far_row(const T* x, T* dx, int cols, int64_t target
 }
 
 // A block takes kBwdUnroll pieces a thread of one row, on the output's boundaries.
+// REST: lse comes in two numbers.
 // MANY: a warp's are a row, and a block takes kBwdRows of them (16384 x 256 in bfloat16:
 // 7.6 us, a block a row 17).
 // ANY: they are on no boundaries of the logits' rows, and a load is two (4096 x 32000
 // in bfloat16 without entropy: 81 us, ANY 98; with four pieces at a time 112).
-template <typename T, bool ENT, bool ANY, bool MANY>
+template <typename T, bool ENT, bool ANY, bool MANY, bool REST>
 __global__ __launch_bounds__(kBwdThreads) void logprobs_bwd_kernel(const __grid_constant__ LogprobsBwd a, int chunks,
                                                                    int64_t rows) {
   start();
@@ -800,14 +809,25 @@ __global__ __launch_bounds__(kBwdThreads) void logprobs_bwd_kernel(const __grid_
   float g = a.dlogprob ? a.dlogprob[row] : a.dlogprob_all;
   if (a.negate) g = -g;
   g = target < 0 ? 0.0f : target < a.vocab ? g : __uint_as_float(0x7FC00000u);
-  const float lse0 = a.lse[row], lse = lse0 == -INFINITY ? 0.0f : lse0;
+  const float lse0 = a.lse[row], rest0 = REST ? a.rest[row] : 0.0f;  // (one load does not wait for the other)
+  const float lse = lse0 == -INFINITY ? 0.0f : lse0, rest = lse0 == -INFINITY ? 0.0f : rest0;
   const float dh = ENT ? a.dentropy[row] : 0.0f, h = ENT ? a.entropy[row] : 0.0f;
   const bool none = !ENT && target < 0;
-  if (fabsf(lse) > kFarLse && !none) {
+  if (!REST && fabsf(lse) > kFarLse && !none) {
     if (chunk == 0) far_row<T, ENT>(x, dx, (int)a.vocab, target, g, dh, h);
     return;
   }
   const int first = chunk * (U * (int)blockDim.x) + (int)threadIdx.x;
+  // p is exp(x - lse) times the rest's exponential, which goes to the row's factors.
+  // (Before the loads or after them: 8192 x 50304 in bfloat16 at other places, the loss,
+  // 454 us or 427, 2000 x 50304 in float32 212 or 227.)
+  float g_all = g, dh_all = dh, h_all = h;
+  auto join_rest = [&] {
+    if (!REST) return;
+    const float e = exp2_fast(-rest * kLog2eF);
+    g_all *= e, dh_all *= e, h_all -= rest;
+  };
+  if (sizeof(T) == 4) join_rest();
   const uint64_t minus = pair(-lse, -lse), log2e = pair(kLog2eF, kLog2eF);
   AnyLoad<T, kPer> any[U];
   uint4 plain[U] = {};
@@ -820,6 +840,7 @@ __global__ __launch_bounds__(kBwdThreads) void logprobs_bwd_kernel(const __grid_
     else if (n)
       plain[i] = *reinterpret_cast<const uint4*>(x + c);
   }
+  if (sizeof(T) == 2) join_rest();
 #pragma unroll
   for (int i = 0; i < U; ++i) {
     const int v = first + i * blockDim.x;
@@ -853,17 +874,20 @@ __global__ __launch_bounds__(kBwdThreads) void logprobs_bwd_kernel(const __grid_
         p = exp2_fast(p), q = exp2_fast(q);
         if (ENT) {
           unpair(d, dp, dq);
-          f[k] = -p * fmaf(dh, fmaxf(dp, -1e4f) + h, g);
-          f[k + 1] = -q * fmaf(dh, fmaxf(dq, -1e4f) + h, g);
+          f[k] = -p * fmaf(dh_all, fmaxf(dp, -1e4f) + h_all, g_all);
+          f[k + 1] = -q * fmaf(dh_all, fmaxf(dq, -1e4f) + h_all, g_all);
         } else {
-          f[k] = -p * g;
-          f[k + 1] = -q * g;
+          f[k] = -p * g_all;
+          f[k + 1] = -q * g_all;
         }
       }
       const int64_t at = target - c;
       if (at >= 0 && at < kPer) {
-        // 1 - p without the difference, which has no digits where p is near 1
-        const float d = load_logit(x + target) - lse, p = exp2_fast(d * kLog2eF);
+        // 1 - p without the difference, which has no digits where p is near 1 (nor has d
+        // there, if the rest of lse is not given)
+        float d = load_logit(x + target) - lse;
+        if (REST) d -= rest;
+        const float p = exp2_fast(d * kLog2eF);
         float e = -g * expm1f(d);
         if (ENT) e -= p * dh * (fmaxf(d, -1e4f) + h);
 #pragma unroll
@@ -974,12 +998,15 @@ cudaError_t run_logprobs_bwd(const LogprobsBwd& a, cudaStream_t st) {
     return launch_kernel(kernel, (unsigned)grid, dim3((unsigned)threads, many ? kBwdRows : 1), 0, 0, st, a,
                          (int)chunks, a.targets.count);
   };
-  auto of = [&](auto ent, auto any) {
-    constexpr bool E = decltype(ent)::value, A = decltype(any)::value;
-    return many ? run(logprobs_bwd_kernel<T, E, A, true>) : run(logprobs_bwd_kernel<T, E, A, false>);
+  auto of = [&](auto ent, auto any, auto rest) {
+    constexpr bool E = decltype(ent)::value, A = decltype(any)::value, R = decltype(rest)::value;
+    return many ? run(logprobs_bwd_kernel<T, E, A, true, R>) : run(logprobs_bwd_kernel<T, E, A, false, R>);
   };
-  if (a.dentropy) return same ? of(std::true_type(), std::false_type()) : of(std::true_type(), std::true_type());
-  return same ? of(std::false_type(), std::false_type()) : of(std::false_type(), std::true_type());
+  auto with = [&](auto ent, auto any) {
+    return a.rest ? of(ent, any, std::true_type()) : of(ent, any, std::false_type());
+  };
+  if (a.dentropy) return same ? with(std::true_type(), std::false_type()) : with(std::true_type(), std::true_type());
+  return same ? with(std::false_type(), std::false_type()) : with(std::false_type(), std::true_type());
 }
 
 template <typename T>
@@ -1003,12 +1030,12 @@ cudaError_t run_token_loss(const TokenLoss& a, cudaStream_t st) {
       return launch_kernel(token_loss_kernel<T>, (unsigned)grid, p.threads, smem, p.cluster > 1 ? p.cluster : 0, st, f);
     }
   }
-  f.lse = a.lse;
+  f.lse = a.lse, f.rest = a.rest;
   const cudaError_t e = run_logprobs<T>(f, st);
   if (e != cudaSuccess) return e;
   LogprobsBwd b = {};
   b.x = a.x, b.ldx = a.ldx, b.targets = a.targets, b.vocab = a.vocab;
-  b.lse = a.lse, b.dlogprob = a.weight, b.dlogprob_all = a.weight_all, b.negate = true;
+  b.lse = a.lse, b.rest = a.rest, b.dlogprob = a.weight, b.dlogprob_all = a.weight_all, b.negate = true;
   b.dx = a.dx, b.lddx = a.lddx;
   return run_logprobs_bwd<T>(b, st);
 }

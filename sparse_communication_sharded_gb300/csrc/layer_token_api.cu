@@ -126,6 +126,14 @@ extern "C" int scape_layer_token_logprobs(const void* logits, int64_t ldx, int d
                                           int token_bytes, int64_t rows, int64_t vocab, int top, float* logprob,
                                           float* lse, float* entropy, float* top_logprob, int64_t* top_token,
                                           void* stream) {
+  return scape_layer_token_logprobs_rest(logits, ldx, dtype, targets, token_bytes, rows, vocab, top, logprob, lse,
+                                         nullptr, entropy, top_logprob, top_token, stream);
+}
+
+extern "C" int scape_layer_token_logprobs_rest(const void* logits, int64_t ldx, int dtype, const void* targets,
+                                               int token_bytes, int64_t rows, int64_t vocab, int top, float* logprob,
+                                               float* lse, float* lse_rest, float* entropy, float* top_logprob,
+                                               int64_t* top_token, void* stream) {
   if (!dtype_ok(dtype)) return fail(SCAPE_EINVAL, "unknown dtype");
   if (!size_ok(rows) || !cols_ok(vocab)) return fail(SCAPE_EINVAL, "rows or vocab out of range");
   if (vocab == 0) return fail(SCAPE_EINVAL, "vocab must be at least 1");
@@ -135,19 +143,20 @@ extern "C" int scape_layer_token_logprobs(const void* logits, int64_t ldx, int d
   int rc = check_logits(logits, ldx, dtype, targets, token_bytes, vocab);
   if (!rc) rc = check_floats(logprob, "logprob is NULL or misaligned");
   if (!rc) rc = check_floats(lse, "lse is NULL or misaligned");
+  if (!rc && lse_rest) rc = check_floats(lse_rest, "lse_rest is misaligned");
   if (!rc && entropy) rc = check_floats(entropy, "entropy is misaligned");
   if (!rc && top) rc = check_floats(top_logprob, "top_logprob is NULL or misaligned");
   if (!rc && top && (!top_token || !aligned(top_token, 8))) rc = fail(SCAPE_EINVAL, "top_token is NULL or misaligned");
   if (!rc)
-    rc = check_apart({vector_span(logprob, rows, 4), vector_span(lse, rows, 4), vector_span(entropy, rows, 4),
-                      vector_span(top ? top_logprob : nullptr, rows * top, 4),
+    rc = check_apart({vector_span(logprob, rows, 4), vector_span(lse, rows, 4), vector_span(lse_rest, rows, 4),
+                      vector_span(entropy, rows, 4), vector_span(top ? top_logprob : nullptr, rows * top, 4),
                       vector_span(top ? top_token : nullptr, rows * top, 8)},
                      {{matrix_span(logits, ldx, rows, vocab, elem_size(dtype))},
                       {vector_span(targets, rows, token_bytes)}});
   if (rc) return rc;
   Logprobs a = {};
   a.x = logits, a.ldx = ldx, a.targets = {targets, token_bytes, rows}, a.vocab = vocab, a.top = top;
-  a.logprob = logprob, a.lse = lse, a.entropy = entropy, a.top_logprob = top_logprob, a.top_token = top_token;
+  a.logprob = logprob, a.lse = lse, a.rest = lse_rest, a.entropy = entropy, a.top_logprob = top_logprob, a.top_token = top_token;
   return cuda_result(launch_logprobs(a, dtype, static_cast<cudaStream_t>(stream)), "scape_layer_token_logprobs");
 }
 
@@ -155,12 +164,21 @@ extern "C" int scape_layer_token_logprobs_bwd(const void* logits, int64_t ldx, i
                                               int token_bytes, int64_t rows, int64_t vocab, const float* lse,
                                               const float* dlogprob, const float* entropy, const float* dentropy,
                                               void* dlogits, int64_t lddx, void* stream) {
+  return scape_layer_token_logprobs_rest_bwd(logits, ldx, dtype, targets, token_bytes, rows, vocab, lse, nullptr,
+                                             dlogprob, entropy, dentropy, dlogits, lddx, stream);
+}
+
+extern "C" int scape_layer_token_logprobs_rest_bwd(const void* logits, int64_t ldx, int dtype, const void* targets,
+                                                   int token_bytes, int64_t rows, int64_t vocab, const float* lse,
+                                                   const float* lse_rest, const float* dlogprob, const float* entropy,
+                                                   const float* dentropy, void* dlogits, int64_t lddx, void* stream) {
   if (!dtype_ok(dtype)) return fail(SCAPE_EINVAL, "unknown dtype");
   if (!size_ok(rows) || !cols_ok(vocab)) return fail(SCAPE_EINVAL, "rows or vocab out of range");
   if (vocab == 0) return fail(SCAPE_EINVAL, "vocab must be at least 1");
   if (rows == 0) return SCAPE_OK;
   int rc = check_logits(logits, ldx, dtype, targets, token_bytes, vocab);
   if (!rc) rc = check_floats(lse, "lse is NULL or misaligned");
+  if (!rc && lse_rest) rc = check_floats(lse_rest, "lse_rest is misaligned");
   if (!rc) rc = check_floats(dlogprob, "dlogprob is NULL or misaligned");
   if (!rc && dentropy) rc = check_floats(dentropy, "dentropy is misaligned");
   if (!rc && dentropy) rc = check_floats(entropy, "entropy is NULL or misaligned");
@@ -171,13 +189,14 @@ extern "C" int scape_layer_token_logprobs_bwd(const void* logits, int64_t ldx, i
                      {{matrix_span(logits, ldx, rows, vocab, e), true},
                       {vector_span(targets, rows, token_bytes)},
                       {vector_span(lse, rows, 4)},
+                      {vector_span(lse_rest, rows, 4)},
                       {vector_span(dlogprob, rows, 4)},
                       {vector_span(dentropy ? entropy : nullptr, rows, 4)},
                       {vector_span(dentropy, rows, 4)}});
   if (rc) return rc;
   LogprobsBwd a = {};
   a.x = logits, a.ldx = ldx, a.targets = {targets, token_bytes, rows}, a.vocab = vocab;
-  a.lse = lse, a.dlogprob = dlogprob, a.entropy = entropy, a.dentropy = dentropy;
+  a.lse = lse, a.rest = lse_rest, a.dlogprob = dlogprob, a.entropy = entropy, a.dentropy = dentropy;
   a.dx = dlogits, a.lddx = lddx;
   return cuda_result(launch_logprobs_bwd(a, dtype, static_cast<cudaStream_t>(stream)),
                      "scape_layer_token_logprobs_bwd");
@@ -189,7 +208,7 @@ extern "C" int scape_layer_token_loss_workspace(const void* logits, int64_t ldx,
   if (!dtype_ok(dtype)) return fail(SCAPE_EINVAL, "unknown dtype");
   if (!size_ok(rows) || !cols_ok(vocab)) return fail(SCAPE_EINVAL, "rows or vocab out of range");
   const bool none = !rows || !vocab || loss_on_chip(logits, ldx, dtype, rows, vocab, dlogits, lddx);
-  *bytes = none ? 0 : round256((size_t)rows * 4);
+  *bytes = none ? 0 : round256((size_t)rows * 8);  // lse in two numbers
   return SCAPE_OK;
 }
 
@@ -219,7 +238,7 @@ extern "C" int scape_layer_token_loss(const void* logits, int64_t ldx, int dtype
   TokenLoss a = {};
   a.x = logits, a.ldx = ldx, a.targets = {targets, token_bytes, rows}, a.vocab = vocab;
   a.weight = weight, a.weight_all = weight_all, a.loss = loss, a.dx = dlogits, a.lddx = lddx;
-  a.lse = static_cast<float*>(workspace);
+  a.lse = static_cast<float*>(workspace), a.rest = need ? a.lse + rows : nullptr;
   return cuda_result(launch_token_loss(a, dtype, static_cast<cudaStream_t>(stream)), "scape_layer_token_loss");
 }
 

@@ -56,6 +56,7 @@ struct Logprobs {
   int top;
   float *logprob, *lse, *entropy, *top_logprob;
   int64_t* top_token;
+  float* rest;  // what lse's rounding leaves of it, or NULL
   // a loss: logprob receives -w times it, w = weight[row] or weight_all, and dx (in the
   // logits' places modulo 16 bytes), where it is given, the gradient
   bool loss;
@@ -72,6 +73,7 @@ struct LogprobsBwd {
   Tokens targets;
   int64_t vocab;
   const float *lse, *dlogprob, *entropy, *dentropy;
+  const float* rest;   // of lse, or NULL
   float dlogprob_all;  // for every row where dlogprob is NULL
   bool negate;         // of dlogprob (a loss's weights)
   void* dx;
@@ -89,7 +91,7 @@ struct TokenLoss {
   float* loss;
   void* dx;
   int64_t lddx;
-  float* lse;  // workspace, where the row does not stay on chip
+  float *lse, *rest;  // workspace, where the row does not stay on chip
 };
 // Whether token_loss keeps a row of these on chip between its two passes.
 bool loss_on_chip(const void* x, int64_t ldx, int dtype, int64_t rows, int64_t vocab, const void* dx, int64_t lddx);

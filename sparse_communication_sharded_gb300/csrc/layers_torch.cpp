@@ -481,7 +481,7 @@ bool truth(PyObject* o) {
   const int v = PyObject_IsTrue(o);
   if (v < 0) {
     PyErr_Clear();
-    throw ValueError("entropy and accumulate must be true or false");
+    throw ValueError("entropy, lse_rest and accumulate must be true or false");
   }
   return v != 0;
 }
@@ -535,7 +535,7 @@ PyObject* do_embedding_backward(Args a) {
   return wrap(dw);
 }
 
-// (logits, targets, entropy, top) -> (logprob, lse, entropy, top_logprob, top_token)
+// (logits, targets, entropy, top, with lse_rest) -> (logprob, lse, entropy, top_logprob, top_token[, lse_rest])
 PyObject* do_token_logprobs(Args a) {
   const Tensor& x = tensor(a[0], "logits");
   const Rows r = rows_of(x, kBf16 | kF32, "logits");
@@ -546,26 +546,32 @@ PyObject* do_token_logprobs(Args a) {
   if (top == -1 && PyErr_Occurred()) return nullptr;
   if (top < 0 || top > SCAPE_TOP_MAX || top > r.cols)
     throw ValueError("top must be 0 to 32, and at most the logits' columns");
+  const bool with_rest = truth(a[4]);
   c10::cuda::CUDAGuard guard(x.device());
-  const int64_t each = (r.rows + 127) / 128 * 128;
-  const Tensor all = row_floats({each * (entropy ? 3 : 2) + r.rows * top}, x);
-  Tensor lp = part_of(all, 0, lead), lse = part_of(all, each, lead), ent, tops, token;
-  if (entropy) ent = part_of(all, 2 * each, lead);
+  const int64_t each = (r.rows + 127) / 128 * 128, at_ent = 2 * each, at_rest = at_ent + (entropy ? each : 0),
+                at_tops = at_rest + (with_rest ? each : 0);
+  const Tensor all = row_floats({at_tops + r.rows * top}, x);
+  Tensor lp = part_of(all, 0, lead), lse = part_of(all, each, lead), rest, ent, tops, token;
+  if (entropy) ent = part_of(all, at_ent, lead);
+  if (with_rest) rest = part_of(all, at_rest, lead);
   if (top) {
     c10::SmallVector<int64_t, 8> sizes(lead.begin(), lead.end());
     sizes.push_back(top);
-    tops = part_of(all, each * (entropy ? 3 : 2), sizes);
+    tops = part_of(all, at_tops, sizes);
     token = empty(lead, top, at::kLong, x);
   }
-  library(scape_layer_token_logprobs(r.p, r.ld, dtype_of(x), ids.p, ids.bytes, r.rows, r.cols, (int)top,
-                                     lp.data_ptr<float>(), lse.data_ptr<float>(),
-                                     entropy ? ent.data_ptr<float>() : nullptr, top ? tops.data_ptr<float>() : nullptr,
-                                     top ? token.data_ptr<int64_t>() : nullptr, stream_of(x)));
-  return tuple({wrap(lp), wrap(lse), entropy ? wrap(ent) : none(), top ? wrap(tops) : none(),
-                top ? wrap(token) : none()});
+  library(scape_layer_token_logprobs_rest(
+      r.p, r.ld, dtype_of(x), ids.p, ids.bytes, r.rows, r.cols, (int)top, lp.data_ptr<float>(), lse.data_ptr<float>(),
+      with_rest ? rest.data_ptr<float>() : nullptr, entropy ? ent.data_ptr<float>() : nullptr, top ? tops.data_ptr<float>() : nullptr,
+      top ? token.data_ptr<int64_t>() : nullptr, stream_of(x)));
+  PyObject* const e = entropy ? wrap(ent) : none();
+  PyObject* const l = top ? wrap(tops) : none();
+  PyObject* const k = top ? wrap(token) : none();
+  if (with_rest) return tuple({wrap(lp), wrap(lse), e, l, k, wrap(rest)});
+  return tuple({wrap(lp), wrap(lse), e, l, k});
 }
 
-// (logits, targets, lse, dlogprob, entropy or None, dentropy or None, out) -> dlogits
+// (logits, targets, lse, dlogprob, entropy or None, dentropy or None, out, lse_rest or None) -> dlogits
 PyObject* do_token_logprobs_backward(Args a) {
   const Tensor& x = tensor(a[0], "logits");
   const Rows r = rows_of(x, kBf16 | kF32, "logits");
@@ -575,10 +581,11 @@ PyObject* do_token_logprobs_backward(Args a) {
   const float* dlp = floats_of(tensor(a[3], "dlogprob"), lead, x, "dlogprob");
   const float* ent = given(a[4]) ? floats_of(tensor(a[4], "entropy"), lead, x, "entropy") : nullptr;
   const float* dent = given(a[5]) ? floats_of(tensor(a[5], "dentropy"), lead, x, "dentropy") : nullptr;
+  const float* rest = given(a[7]) ? floats_of(tensor(a[7], "lse_rest"), lead, x, "lse_rest") : nullptr;
   c10::cuda::CUDAGuard guard(x.device());
   Out out = output(a[6], lead, r.cols, x.scalar_type(), x, "out");
-  library(scape_layer_token_logprobs_bwd(r.p, r.ld, dtype_of(x), ids.p, ids.bytes, r.rows, r.cols, lse, dlp, ent, dent,
-                                         out.r.p, out.r.ld, stream_of(x)));
+  library(scape_layer_token_logprobs_rest_bwd(r.p, r.ld, dtype_of(x), ids.p, ids.bytes, r.rows, r.cols, lse, rest, dlp,
+                                              ent, dent, out.r.p, out.r.ld, stream_of(x)));
   return out.done();
 }
 
@@ -752,8 +759,8 @@ PyMethodDef kMethods[] = {ENTRY(pack8, 1),
                           ENTRY(linear_backward_weight, 6),
                           ENTRY(embedding, 5),
                           ENTRY(embedding_backward, 5),
-                          ENTRY(token_logprobs, 4),
-                          ENTRY(token_logprobs_backward, 7),
+                          ENTRY(token_logprobs, 5),
+                          ENTRY(token_logprobs_backward, 8),
                           ENTRY(token_loss, 5),
                           ENTRY(grad_norm, 1),
                           ENTRY(clip_grad_norm, 4),

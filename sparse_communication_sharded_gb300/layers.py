@@ -180,11 +180,7 @@ def embedding_backward(dy, tokens, dweight, scale=1.0, accumulate=False) -> torc
     return _lib().embedding_backward(dy, tokens, dweight, scale, accumulate)
 
 
-class TokenLogprobs(NamedTuple):
-    """Each of the rows' leading shape, float32: the targets' log probabilities, the
-    logits' log-sum-exp, the entropies (None unless asked for); the `top` largest
-    logits' log probabilities and columns (int64), in falling order, in one more
-    dimension (None unless asked for).  The float32 ones are parts of one allocation."""
+class _TokenLogprobs(NamedTuple):
     logprob: torch.Tensor
     lse: torch.Tensor
     entropy: torch.Tensor | None
@@ -192,24 +188,41 @@ class TokenLogprobs(NamedTuple):
     top_token: torch.Tensor | None
 
 
-def token_logprobs(logits, targets, entropy=False, top=0) -> TokenLogprobs:
+class TokenLogprobs(_TokenLogprobs):
+    """Each of the rows' leading shape, float32: the targets' log probabilities, the
+    logits' log-sum-exp, the entropies (None unless asked for); the `top` largest
+    logits' log probabilities and columns (int64), in falling order, in one more
+    dimension (None unless asked for).  Beside these five, lse_rest: what lse's rounding
+    leaves of the log-sum-exp, for token_logprobs_backward (None unless asked for).  The
+    float32 ones are parts of one allocation."""
+    lse_rest: torch.Tensor | None = None
+
+
+def token_logprobs(logits, targets, entropy=False, top=0, lse_rest=False) -> TokenLogprobs:
     """Log probabilities of the targets (contiguous int64 or int32, of the logits'
     leading shape) under softmax(logits), logits float32 or bfloat16.  A target below
     0 stands for none and gives 0; one outside the vocabulary gives NaN.  top: 0 to
     32 (of up to 4194304 columns); of equal logits the lower column comes first.  A
     logit of -infinity has probability 0; in a row of nothing else every log
     probability is -infinity and the entropy 0."""
-    return TokenLogprobs(*_lib().token_logprobs(logits, targets, entropy, top))
+    values = _lib().token_logprobs(logits, targets, entropy, top, lse_rest)
+    if not lse_rest:
+        return TokenLogprobs(*values)
+    r = TokenLogprobs(*values[:5])
+    r.lse_rest = values[5]
+    return r
 
 
 def token_logprobs_backward(logits, targets, lse, dlogprob, entropy=None, dentropy=None,
-                            out=None) -> torch.Tensor:
+                            out=None, lse_rest=None) -> torch.Tensor:
     """The gradient of the logits, from that of the log probabilities and, if given,
-    that of the entropies (with the entropies themselves).  lse, dlogprob, entropy and
-    dentropy: contiguous float32, one a row.  out may be logits."""
+    that of the entropies (with the entropies themselves).  lse, lse_rest, dlogprob,
+    entropy and dentropy: contiguous float32, one a row.  out may be logits.  lse_rest
+    is what token_logprobs gives if asked: without it probabilities are off by lse's rounding, 2^-24
+    |lse| of themselves, and a target with nearly all of it has no gradient left."""
     if dentropy is not None and entropy is None:
         raise ValueError("dentropy needs the entropies that token_logprobs gave")
-    return _lib().token_logprobs_backward(logits, targets, lse, dlogprob, entropy, dentropy, out)
+    return _lib().token_logprobs_backward(logits, targets, lse, dlogprob, entropy, dentropy, out, lse_rest)
 
 
 def token_loss(logits, targets, weight, out=None):
