@@ -119,12 +119,14 @@ __global__ __launch_bounds__(kFwdThreads) void embed_fwd_kernel(const __grid_con
 // L2, as much as a row of dy is out of memory; several passes of a radix sort would
 // each be a launch.  What a warp finds it keeps, in order, up to kSortKept; only a warp
 // that finds more (a very common token) reads its share again.
+// (tokens is no __restrict__ pointer: the grid may start while an earlier kernel still
+// writes them, so they are no data that stays as it is from start to end.)
 constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32, kSortUnroll = 16;
 constexpr int kSortRows = 352, kSortKept = 256;  // 44 KB of counts, 64 KB
 static_assert(kSortRows <= kSortThreads && kSortWarps <= 32, "a thread for each token, a lane for each warp");
 
 template <typename I>
-__global__ __launch_bounds__(kSortThreads) void sort_tokens_kernel(const I* __restrict__ tokens, int64_t count,
+__global__ __launch_bounds__(kSortThreads) void sort_tokens_kernel(const I* tokens, int64_t count,
                                                                    int64_t vocab, int rows, int4* entries,
                                                                    int* starts, int* arrived, int64_t arrivals) {
   extern __shared__ __align__(8) int counts[];  // [kSortWarps][rows], rows even
