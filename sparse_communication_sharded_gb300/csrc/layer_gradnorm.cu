@@ -337,10 +337,14 @@ cudaError_t run_grad_norm(const GradSet& a, cudaStream_t st) {
 
 }  // namespace
 
+// Blocks of all launches: a table is full with kLong tensors, or once it has more than
+// 2^30 chunks and the next tensor's no longer fit (kShort tables: one is enough).
 int64_t grad_norm_partials(int n, const int64_t* numel) {
-  int64_t chunks = 0;
-  for (int i = 0; i < n; ++i) chunks += numel[i] > 0 ? chunks_of(numel[i], 4) : 0;
-  return std::min<int64_t>(chunks, (ceil_div(n, kShort) + 1) * (int64_t)sm_count() * kBlocksPerSm);
+  int64_t chunks = 0, some = 0;
+  for (int i = 0; i < n; ++i)
+    if (numel[i] > 0) chunks += chunks_of(numel[i], 4), ++some;
+  const int64_t tables = ceil_div(some, kLong) + (chunks >> 30);
+  return std::min<int64_t>(chunks, tables * sm_count() * kBlocksPerSm);
 }
 cudaError_t launch_grad_norm(const GradSet& a, cudaStream_t st) {
   int64_t some = 0;
