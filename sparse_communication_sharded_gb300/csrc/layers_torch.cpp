@@ -649,16 +649,25 @@ Set set_of(PyObject* o, const char* name) {
   if (n > 0x7FFFFFFF) throw ValueError(std::string(name) + " has too many tensors");
   return s;
 }
-// The norm, and behind it in the same allocation (of a few KB) the workspace.
+// The norm and the workspace.  A kept norm keeps its allocation, so the workspace has
+// one of its own, unless both fit in kTogether: two allocations take no less, as each is
+// 512 bytes at least, and the second is a microsecond of the 6 that a small set takes.
 struct NormSpace {
-  Tensor norm;
+  static constexpr int64_t kTogether = 1024, kNormFloats = 64;
+  Tensor norm, own;
   void* ws = nullptr;
   size_t n = 0;
   explicit NormSpace(const Set& s) {
     library(scape_layer_grad_norm_workspace((int)s.t.size(), s.numel.data(), &n));
-    const Tensor all = row_floats({64 + (int64_t)(n / 4)}, s.t[0]);
-    norm = part_of(all, 0, {});
-    if (n) ws = all.data_ptr<float>() + 64;
+    if (kNormFloats * 4 + (int64_t)n <= kTogether) {
+      const Tensor all = row_floats({kNormFloats + (int64_t)(n / 4)}, s.t[0]);
+      norm = part_of(all, 0, {});
+      if (n) ws = all.data_ptr<float>() + kNormFloats;
+    } else {
+      norm = row_floats({}, s.t[0]);
+      own = bytes(n, s.t[0]);
+      ws = own.data_ptr();
+    }
   }
 };
 
