@@ -57,3 +57,50 @@ def test_norm(cuda_device, tensors, numel):
     for a, b in zip(t, into):
         # the factor by the norm's error, its rounding, and the product's
         assert bool(((b.double() - a.double() / 2).abs() <= a.double().abs() * (tol + 2 * R.E)).all())
+
+
+@pytest.mark.parametrize("count,vocab,cols", [(1, 1, 1), (17, 5, 1), (33, 9, 8200), (579, 3, 700), (1000, 50, 1283),
+                                              (5000, 7, 2600), (16 * 4 * 9 + 1, 1, 641), (8191, 999, 64)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("gap", [0, 3])
+def test_embedding_gradient(cuda_device, count, vocab, cols, dtype, gap):
+    """Whole numbers' sums, which are exact; tokens that repeat over many tiles."""
+    lib = C.load()
+    g = torch.Generator(device="cuda").manual_seed(count)
+    dy = torch.randint(-3, 4, (count, cols + gap), device="cuda", generator=g).to(dtype)[:, :cols]
+    t = torch.randint(-1, vocab, (count,), device="cuda", generator=g)
+    t[count // 3:2 * count // 3] = vocab // 2
+    need = ctypes.c_size_t()
+    assert lib.scape_layer_embedding_bwd_workspace(count, vocab, cols, ctypes.byref(need)) == C.SCAPE_OK
+    dw, ws = torch.full((vocab, cols), 5.0, device="cuda"), Space(need.value)
+    want = torch.zeros(vocab + 1, cols, device="cuda", dtype=torch.float64)
+    want.index_add_(0, torch.where(t < 0, vocab, t), dy.double())
+    for accumulate in (0, 1):
+        run(lib.scape_layer_embedding_bwd(dy.data_ptr(), cols + gap, DT[dtype], t.data_ptr(), 8, count, vocab, cols, 1.0,
+                                          accumulate, dw.data_ptr(), cols, C.SCAPE_F32, ws.p, ws.n,
+                                          torch.cuda.current_stream().cuda_stream))
+        ws.check()
+        assert torch.equal(dw.double(), want[:vocab] * (1 + accumulate))
+
+
+@pytest.mark.parametrize("rows,vocab", [(1, 40), (32, 2000), (64, 33), (33, 5001), (256, 1000)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_loss_elsewhere(cuda_device, rows, vocab, dtype):
+    lib = C.load()
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    x = torch.randn(rows, vocab, device="cuda", generator=g).to(dtype)
+    t = torch.randint(-1, vocab, (rows,), device="cuda", generator=g)
+    out = torch.empty(rows, vocab + 1, device="cuda", dtype=dtype)[:, 1:]
+    args = (x.data_ptr(), vocab, DT[dtype])
+    need = ctypes.c_size_t()
+    assert lib.scape_layer_token_loss_workspace(*args, rows, vocab, out.data_ptr(), vocab + 1, ctypes.byref(need)) == C.SCAPE_OK
+    assert need.value >= 8 * rows  # lse in two numbers
+    loss, ws = torch.empty(rows, device="cuda"), Space(need.value)
+    run(lib.scape_layer_token_loss(*args, t.data_ptr(), 8, rows, vocab, None, 0.5, loss.data_ptr(), out.data_ptr(), vocab + 1,
+                                   ws.p, ws.n, torch.cuda.current_stream().cuda_stream))
+    ws.check()
+    o = R.Rows(x, t)
+    want, tol = o.gradient(torch.full((rows,), -0.5, device="cuda"), dtype)
+    assert bool(((out.double() - want).abs() <= tol).all())
+    lp, tol = o.logprob()
+    assert bool(((loss.double() + 0.5 * lp).abs() <= 0.5 * tol + lp.abs() * R.E).all())
