@@ -305,8 +305,9 @@ int scape_layer_grad_norm(int n, const void *const *host_grads, const int64_t *h
 /*
  * The norm, and out[i] = grads[i] * min(1, max_norm / (norm + eps)), each of
  * host_out_dtype[i].  host_out NULL: in place; out[i] may be grads[i] (same type).
- * max_norm >= 0, eps >= 0.  The factor is used as it comes out: NaN where the norm is
- * NaN, 0 where it is infinite.
+ * max_norm >= 0, eps >= 0.  The factor is used as it comes out of the norm in 64 bits:
+ * NaN where an element is, 0 where one is infinite, and NaN for 0 / 0 (max_norm, the
+ * norm and eps all 0) or infinity / infinity.
  */
 int scape_layer_clip_grads(int n, const void *const *host_grads, const int64_t *host_numel,
                            const int *host_dtype, void *const *host_out,

@@ -2,9 +2,9 @@
 //
 // Forward: y[i] = scale w[token i].  Bound by memory; a thread takes four pieces of 8
 // columns so that their loads are in flight together (16384 x 1280 in bfloat16: 11.6
-// us, 106% of the copy rate, as rows come twice).  Where rows are on no 16-byte
-// boundary one piece, whose aligned words are three loads (16381 x 1283 from float32:
-// 22.7 us, with four pieces and their registers 38).
+// us, 106% of the copy rate, where rows that come twice are in L2, 13.9 where none is).
+// Where rows are on no 16-byte boundary one piece, whose aligned words are three loads
+// (16381 x 1283 from float32: 20 us, with four pieces and their registers 38).
 //
 // Gradient: dw[v] = scale * sum of the dy rows of token v.  Atomics on dw would add
 // in an order that changes, and in the output's type.  So the positions are sorted by
@@ -13,9 +13,10 @@
 // by blocks that are done last.  Most rows of a large table have no token, and writing
 // their zeros is most of the bytes: that goes on beside the sums.
 //
-// 50304 x 1024 from 8192 tokens of a text, bfloat16: 28.4 to 29.3 us (sort 8, sums and
-// zeros 22, each alone under ncu), its bytes at the copy rate 17.6.  The second launch
-// waits for the first, which writes nothing but the order.
+// 50304 x 1024 from 8192 tokens of a text, bfloat16: 27.9 to 29.3 us (sort 8, sums and
+// zeros 22, each alone under ncu), its bytes at the copy rate 17.6; added to what is
+// there, without zeros, 23.5.  The second launch waits for the first, which writes
+// nothing but the order.
 #include <algorithm>
 
 #include "layer_tokens.h"
@@ -116,8 +117,10 @@ __global__ __launch_bounds__(kFwdThreads) void embed_fwd_kernel(const __grid_con
 // each of its own occurs in each warp's share of them and how many tokens are below
 // its first: that gives every one of its entries a place of its own, without waiting
 // for another block.  All blocks reading all tokens is 152 x 8 bytes a token out of
-// L2, as much as a row of dy is out of memory; several passes of a radix sort would
-// each be a launch.  What a warp finds it keeps, in order, up to kSortKept; only a warp
+// L2 for tables of up to 152 x kSortRows = 53504 rows, as much as a row of dy is out of
+// memory; past that a block more for every kSortRows rows, and it is vocab / 44 bytes a
+// token (alone, from 65536 tokens: 50304 rows 17 us, 131072 35, 262144 50; from 8192 8
+// and 22).  Several passes of a radix sort would each be a launch.  What a warp finds it keeps, in order, up to kSortKept; only a warp
 // that finds more (a very common token) reads its share again.
 // (tokens is no __restrict__ pointer: the grid may start while an earlier kernel still
 // writes them, so they are no data that stays as it is from start to end.)

@@ -397,10 +397,10 @@ struct Share {
 // thread has a ring of its own pieces in shared memory, kAhead batches deep, and waits
 // for nothing but its own copies until the threads' sums are joined.  Seven blocks of
 // 128 threads an SM, so that others read meanwhile (8192 x 32000 in bfloat16 with
-// entropy: 84 us, 92% of the copy rate; blocks that go from row to row 88, four of 256
+// entropy: 82 us, 94% of the copy rate; blocks that go from row to row 88, four of 256
 // threads 103, pieces read into registers 105).  Six with alternatives, whose search
-// takes more registers (4096 x 32000 with five: 64 us, three of 256 threads 88, without
-// alternatives 44).
+// takes more registers (4096 x 32000 with five: 63 us, three of 256 threads 88, without
+// alternatives 42).
 constexpr int kTeam = 128, kUnroll = 4, kAhead = 3;
 constexpr int kBlocks = 7, kBlocksTop = 6;  // an SM
 
@@ -551,7 +551,7 @@ __device__ __forceinline__ void store_piece(T* o, const float (&f)[16 / sizeof(T
 // row; every thread copies its own pieces to places of its own, which it alone reads.
 // Two or more blocks an SM and no more than a row's life for each: while some wait
 // for their row or their barrier others compute or store, and none waits for the
-// slowest.  (8192 x 50304 in bfloat16: 238 us, what a copy of as many bytes takes; as
+// slowest.  (8192 x 50304 in bfloat16: 234 us, what a copy of as many bytes takes; as
 // many blocks as fit, going from row to row, 255; one block an SM with the next row on
 // its way 277; sums and gradient in a kernel each 384.)
 template <typename T>
@@ -669,9 +669,9 @@ __global__ __launch_bounds__(kMaxThreads) void token_loss_kernel(const __grid_co
 // A warp takes a row, each lane U of its pieces in registers, with the next row's on
 // their way; with LOSS its gradient goes out from there.  What bounds it is a row's own
 // work, the joining of 32 lanes' sums and what lane 0 does with them.  16384 rows in
-// bfloat16, log probabilities and loss: of 256 columns 7.7 and 10.3 us, of 1000 9.4 and
-// 15.3 (a block a row 19 and 20.7), of 2000, where U is 8 and four blocks fit, 13.8 and
-// 25.5 (24.8 and 34.5).  Longer rows have no room in registers.
+// bfloat16, log probabilities and loss: of 256 columns 7.9 and 10.8 us, of 1000 9.2 and
+// 15.6 (a block a row 19 and 20.7), of 2000, where U is 8 and four blocks fit, 13.5 and
+// 25.6 (24.8 and 34.5).  Longer rows have no room in registers.
 constexpr int kShortWarps = 4;
 constexpr int short_blocks(int u) { return u <= 4 ? 6 : 4; }  // an SM
 
@@ -790,11 +790,13 @@ __device__ __noinline__ void far_row(const T* x, T* dx, int cols, int64_t target
 }
 
 // A block takes kBwdUnroll pieces a thread of one row, on the output's boundaries.
-// REST: lse comes in two numbers.
+// REST: lse comes in two numbers, and no row has to be looked at before its loads are on
+// their way (4096 x 32000 with the entropy: 78 us, without REST 85; without the entropy
+// 81 and 82, at other places 96 and 99).
 // MANY: a warp's are a row, and a block takes kBwdRows of them (16384 x 256 in bfloat16:
-// 7.6 us, a block a row 17).
+// 7.5 us, a block a row 17).
 // ANY: they are on no boundaries of the logits' rows, and a load is two (4096 x 32000
-// in bfloat16 without entropy: 81 us, ANY 98; with four pieces at a time 112).
+// in bfloat16 without entropy: 82 us, ANY 99; with four pieces at a time 112).
 template <typename T, bool ENT, bool ANY, bool MANY, bool REST>
 __global__ __launch_bounds__(kBwdThreads) void logprobs_bwd_kernel(const __grid_constant__ LogprobsBwd a, int chunks,
                                                                    int64_t rows) {
