@@ -9,7 +9,7 @@
 // is m raised, which scales S by exp(m - m'); the threads' sums are joined the same
 // way.  (Exponents up to 10 keep their digits; the largest of every few values is an
 // instruction a value.)  The m of a row is one of its values, at most ln 1024 below its
-// largest, so where it is not the largest the others' probability is 1e-3 or more and
+// largest, so where it is not the largest the others' probability is 1/1025 or more and
 // the difference of two numbers that the entropy is stays above 0 by 1e4 roundings.
 // Exponents are of base 2: a = d log2 e.
 //

@@ -156,7 +156,8 @@ extern "C" int scape_layer_token_logprobs_rest(const void* logits, int64_t ldx, 
   if (rc) return rc;
   Logprobs a = {};
   a.x = logits, a.ldx = ldx, a.targets = {targets, token_bytes, rows}, a.vocab = vocab, a.top = top;
-  a.logprob = logprob, a.lse = lse, a.rest = lse_rest, a.entropy = entropy, a.top_logprob = top_logprob, a.top_token = top_token;
+  a.logprob = logprob, a.lse = lse, a.rest = lse_rest, a.entropy = entropy;
+  a.top_logprob = top_logprob, a.top_token = top_token;
   return cuda_result(launch_logprobs(a, dtype, static_cast<cudaStream_t>(stream)), "scape_layer_token_logprobs");
 }
 

@@ -562,8 +562,8 @@ PyObject* do_token_logprobs(Args a) {
   }
   library(scape_layer_token_logprobs_rest(
       r.p, r.ld, dtype_of(x), ids.p, ids.bytes, r.rows, r.cols, (int)top, lp.data_ptr<float>(), lse.data_ptr<float>(),
-      with_rest ? rest.data_ptr<float>() : nullptr, entropy ? ent.data_ptr<float>() : nullptr, top ? tops.data_ptr<float>() : nullptr,
-      top ? token.data_ptr<int64_t>() : nullptr, stream_of(x)));
+      with_rest ? rest.data_ptr<float>() : nullptr, entropy ? ent.data_ptr<float>() : nullptr,
+      top ? tops.data_ptr<float>() : nullptr, top ? token.data_ptr<int64_t>() : nullptr, stream_of(x)));
   PyObject* const e = entropy ? wrap(ent) : none();
   PyObject* const l = top ? wrap(tops) : none();
   PyObject* const k = top ? wrap(token) : none();
