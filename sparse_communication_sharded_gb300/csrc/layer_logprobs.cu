@@ -790,13 +790,13 @@ __device__ __noinline__ void far_row(const T* x, T* dx, int cols, int64_t target
 }
 
 // A block takes kBwdUnroll pieces a thread of one row, on the output's boundaries.
-// REST: lse comes in two numbers, and no row has to be looked at before its loads are on
-// their way (4096 x 32000 with the entropy: 78 us, without REST 85; without the entropy
-// 81 and 82, at other places 96 and 99).
+// REST: lse comes in two numbers, and a row's loads need not wait for lse to tell whether
+// it is far (4096 x 32000 in bfloat16 with the entropy: 78 us, without REST 85; without
+// the entropy 82 and 79, at other places 97 and 100).
 // MANY: a warp's are a row, and a block takes kBwdRows of them (16384 x 256 in bfloat16:
 // 7.5 us, a block a row 17).
 // ANY: they are on no boundaries of the logits' rows, and a load is two (4096 x 32000
-// in bfloat16 without entropy: 82 us, ANY 99; with four pieces at a time 112).
+// in bfloat16 without entropy: 79 us, ANY 100; with four pieces at a time 112).
 template <typename T, bool ENT, bool ANY, bool MANY, bool REST>
 __global__ __launch_bounds__(kBwdThreads) void logprobs_bwd_kernel(const __grid_constant__ LogprobsBwd a, int chunks,
                                                                    int64_t rows) {
@@ -813,6 +813,9 @@ __global__ __launch_bounds__(kBwdThreads) void logprobs_bwd_kernel(const __grid_
   float g = a.dlogprob ? a.dlogprob[row] : a.dlogprob_all;
   if (a.negate) g = -g;
   g = target < 0 ? 0.0f : target < a.vocab ? g : __uint_as_float(0x7FC00000u);
+  // The target's column, or one that no piece has: pieces reach over both ends of a row
+  // (from column 1 - kPer on), and a target that is none or too large may be a number there.
+  const int64_t chosen = target >= 0 && target < a.vocab ? target : -kPer;
   const float lse0 = a.lse[row], rest0 = REST ? a.rest[row] : 0.0f;  // (one load does not wait for the other)
   const float lse = lse0 == -INFINITY ? 0.0f : lse0, rest = lse0 == -INFINITY ? 0.0f : rest0;
   const float dh = ENT ? a.dentropy[row] : 0.0f, h = ENT ? a.entropy[row] : 0.0f;
@@ -824,7 +827,7 @@ __global__ __launch_bounds__(kBwdThreads) void logprobs_bwd_kernel(const __grid_
   const int first = chunk * (U * (int)blockDim.x) + (int)threadIdx.x;
   // p is exp(x - lse) times the rest's exponential, which goes to the row's factors.
   // (Before the loads or after them: 8192 x 50304 in bfloat16 at other places, the loss,
-  // 454 us or 427, 2000 x 50304 in float32 212 or 227.)
+  // 454 us or 429, 2000 x 50304 in float32 211 or 227.)
   float g_all = g, dh_all = dh, h_all = h;
   auto join_rest = [&] {
     if (!REST) return;
@@ -885,11 +888,11 @@ __global__ __launch_bounds__(kBwdThreads) void logprobs_bwd_kernel(const __grid_
           f[k + 1] = -q * g_all;
         }
       }
-      const int64_t at = target - c;
+      const int64_t at = chosen - c;
       if (at >= 0 && at < kPer) {
         // 1 - p without the difference, which has no digits where p is near 1 (nor has d
         // there, if the rest of lse is not given)
-        float d = load_logit(x + target) - lse;
+        float d = load_logit(x + chosen) - lse;
         if (REST) d -= rest;
         const float p = exp2_fast(d * kLog2eF);
         float e = -g * expm1f(d);
